@@ -15,6 +15,7 @@ ATTN_ERR_UNSUPPORTED = 2
 ATTN_ERR_CUDA = 3
 ATTN_ERR_TIMEOUT = 4
 ATTN_ERR_DEVICE_INPUT = 5
+ATTN_CACHE_I8, ATTN_CACHE_E4M3 = 0, 1
 ATTN_FLAG_OUT_F32 = 1
 ATTN_FLAG_DETERMINISTIC = 2
 
@@ -71,6 +72,16 @@ def load() -> ctypes.CDLL:
         lib.attn_bwd_cross_workspace_bytes.restype = ctypes.c_size_t
         lib.attn_bwd_cross.argtypes = [vp] * 10 + [ctypes.c_size_t] + [i] * 7 + [f, i, u, vp]
         lib.attn_bwd_cross.restype = i
+        lib.attn_kvcache8_append.argtypes = [vp] * 8 + [i] * 8 + [vp]
+        lib.attn_kvcache8_append.restype = i
+        lib.attn_fwd_kvcache8_workspace_bytes.argtypes = [i] * 6
+        lib.attn_fwd_kvcache8_workspace_bytes.restype = ctypes.c_size_t
+        lib.attn_fwd_kvcache8.argtypes = [vp] * 9 + [ctypes.c_size_t] + [i] * 8 + [f, i, i, u, vp]
+        lib.attn_fwd_kvcache8.restype = i
+        lib.attn_kvcache_weights.argtypes = [vp] * 6 + [i] * 7 + [f, i, vp]
+        lib.attn_kvcache_weights.restype = i
+        lib.attn_kvcache_evict.argtypes = [vp] * 9 + [i] * 8 + [vp]
+        lib.attn_kvcache_evict.restype = i
         lib.attn_get_device_status.argtypes = [vp]
         lib.attn_get_device_status.restype = i
         lib.attn_status_string.argtypes = [i]
@@ -111,6 +122,35 @@ def attn_fwd_kvcache(q, k_cache, v_cache, cache_seqlens, o, lse, workspace, work
                      causal, scale, num_splits, dtype, flags, stream) -> int:
     return load().attn_fwd_kvcache(q, k_cache, v_cache, cache_seqlens, o, lse, workspace, workspace_bytes, B, Hq, Hkv,
                                    Nq, Nk, d, int(causal), float(scale), int(num_splits), dtype, flags, stream)
+
+
+def attn_kvcache8_append(k8, v8, k_scale, v_scale, k_new, v_new, cache_seqlens, new_seqlens, B, Hkv, Nn, Nk, d, block,
+                         dtype, cache_dtype, stream) -> int:
+    return load().attn_kvcache8_append(k8, v8, k_scale, v_scale, k_new, v_new, cache_seqlens, new_seqlens, B, Hkv, Nn,
+                                       Nk, d, block, dtype, cache_dtype, stream)
+
+
+def attn_fwd_kvcache8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d) -> int:
+    return load().attn_fwd_kvcache8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d)
+
+
+def attn_fwd_kvcache8(q, k8, v8, k_scale, v_scale, cache_seqlens, o, lse, workspace, workspace_bytes, B, Hq, Hkv, Nq,
+                      Nk, d, block, causal, scale, dtype, cache_dtype, flags, stream) -> int:
+    return load().attn_fwd_kvcache8(q, k8, v8, k_scale, v_scale, cache_seqlens, o, lse, workspace, workspace_bytes, B,
+                                    Hq, Hkv, Nq, Nk, d, block, int(causal), float(scale), dtype, cache_dtype, flags,
+                                    stream)
+
+
+def attn_kvcache_weights(q, k_cache, lse, cache_seqlens, weights_in, weights_out, B, Hq, Hkv, Nq, Nk, d, causal, scale,
+                         dtype, stream) -> int:
+    return load().attn_kvcache_weights(q, k_cache, lse, cache_seqlens, weights_in, weights_out, B, Hq, Hkv, Nq, Nk, d,
+                                       int(causal), float(scale), dtype, stream)
+
+
+def attn_kvcache_evict(k_cache, v_cache, weights, cache_seqlens, k_out, v_out, weights_out, index, out_seqlens, B, Hkv,
+                       Nk, capacity, d, keep, recent, dtype, stream) -> int:
+    return load().attn_kvcache_evict(k_cache, v_cache, weights, cache_seqlens, k_out, v_out, weights_out, index,
+                                     out_seqlens, B, Hkv, Nk, capacity, d, keep, recent, dtype, stream)
 
 
 def attn_bwd_cross_workspace_bytes(B, Hq, Nq, Nk, d, dtype, flags) -> int:

@@ -9,6 +9,9 @@ every step of the computation runs in libattn_gb300.so's kernels.
   causal defaults to False; window_size, softcap, alibi_slopes and return_attn_probs are
   rejected; dropout is not provided).
 - ``fwd``, ``bwd``, ``fwd_varlen``: explicit calls that also return the LSE / take workspaces.
+- ``kvcache8_append``, ``fwd_kvcache8``: a KV cache held in 8 bits with a scale per block of
+  tokens and head, and attention over it; ``kvcache_weights``, ``kvcache_evict``: the attention
+  weight that each cached key has received, and eviction by it.
 """
 from __future__ import annotations
 
@@ -18,6 +21,7 @@ import torch
 
 from . import _lib
 
+_DT8 = {torch.int8: _lib.ATTN_CACHE_I8, torch.float8_e4m3fn: _lib.ATTN_CACHE_E4M3}
 _DT = {torch.float32: _lib.ATTN_F32, torch.float16: _lib.ATTN_F16, torch.bfloat16: _lib.ATTN_BF16}
 
 
@@ -216,6 +220,166 @@ def fwd_kvcache(q, k_cache, v_cache, cache_seqlens=None, causal: bool = False, s
                                _lib.ATTN_FLAG_OUT_F32 if out_f32 else 0, _stream())
     _lib._check(st, "attn_fwd_kvcache")
     return o, lse
+
+
+def _cache_args(first, name: str, tensors, optional=()):
+    """Checks of the cache calls: (tensor, name, dtype) each, contiguous and on the first one's
+    GPU.  Returns that device."""
+    for t, n, dtype in tensors + tuple(x for x in optional if x[0] is not None):
+        _require(t, n, dtype)
+        if t.device != first.device:
+            raise ValueError(f"{n} must be on {name}'s device")
+    return first.device
+
+
+def _lens_ptr(t, name: str, B: int):
+    if t is None:
+        return None
+    if t.shape != (B,):
+        raise ValueError(f"{name} must be int32 [B]")
+    return t.data_ptr()
+
+
+def _check_cache8(k8, v8, k_scale, v_scale, block: int):
+    if k8.dtype not in _DT8:
+        raise TypeError(f"unsupported cache dtype {k8.dtype}: int8 or float8_e4m3fn")
+    if block not in (16, 32, 64, 128):
+        raise ValueError("block must be 16, 32, 64 or 128")
+    if k8.dim() != 4 or k8.shape != v8.shape:
+        raise ValueError("k8 and v8 must be [B,Hkv,Nk,d]")
+    B, Hkv, Nk, _ = k8.shape
+    if k_scale.shape != (B, Hkv, -(-Nk // block)) or v_scale.shape != k_scale.shape:
+        raise ValueError("k_scale and v_scale must be [B,Hkv,ceil(Nk/block)]")
+
+
+def kvcache8_append(k8, v8, k_scale, v_scale, k_new, v_new, cache_seqlens=None, new_seqlens=None, block: int = 64):
+    """Writes tokens into an 8-bit cache, in place.  k8, v8 [B,Hkv,Nk,d] int8 or float8_e4m3fn;
+    k_scale, v_scale float32 [B,Hkv,ceil(Nk/block)]; k_new, v_new [B,Hkv,Nn,d].  Batch b's tokens
+    go behind its first cache_seqlens[b] (int32 [B] on the device; None: an empty cache), the
+    first new_seqlens[b] of them (None: Nn); the caller advances the lengths.  block: tokens per
+    scale, 16, 32, 64 or 128."""
+    _require(k8, "k8")
+    _require(k_new, "k_new")
+    dev = _cache_args(k8, "k8", ((v8, "v8", k8.dtype), (k_scale, "k_scale", torch.float32),
+                                 (v_scale, "v_scale", torch.float32), (k_new, "k_new", None), (v_new, "v_new", k_new.dtype)),
+                      ((cache_seqlens, "cache_seqlens", torch.int32), (new_seqlens, "new_seqlens", torch.int32)))
+    _check_cache8(k8, v8, k_scale, v_scale, block)
+    B, Hkv, Nk, d = k8.shape
+    if k_new.dim() != 4 or k_new.shape != v_new.shape or k_new.shape[:2] != (B, Hkv) or k_new.shape[3] != d:
+        raise ValueError("k_new and v_new must be [B,Hkv,Nn,d]")
+    with torch.cuda.device(dev):
+        st = _lib.attn_kvcache8_append(k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                       k_new.data_ptr(), v_new.data_ptr(), _lens_ptr(cache_seqlens, "cache_seqlens", B),
+                                       _lens_ptr(new_seqlens, "new_seqlens", B), B, Hkv, k_new.shape[2], Nk, d, block,
+                                       _dtype_code(k_new), _DT8[k8.dtype], _stream())
+    _lib._check(st, "attn_kvcache8_append")
+
+
+def kvcache8_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Nk: int, d: int) -> int:
+    """Bytes of the device workspace fwd_kvcache8 needs for these sizes."""
+    return _lib.attn_fwd_kvcache8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d)
+
+
+def fwd_kvcache8(q, k8, v8, k_scale, v_scale, cache_seqlens=None, causal: bool = False, scale=None, block: int = 64,
+                 out_f32: bool = False, with_lse: bool = True, workspace=None):
+    """fwd_kvcache over an 8-bit cache.  q [B,Hq,Nq,d] float16 or bfloat16; k8, v8, k_scale,
+    v_scale and block as kvcache8_append writes them; cache_seqlens int32 [B] on the device (None:
+    Nk tokens each).  Returns (o [B,Hq,Nq,d], lse [B,Hq,Nq] or None)."""
+    _require(q, "q")
+    _require(k8, "k8")
+    dev = _cache_args(q, "q", ((k8, "k8", None), (v8, "v8", k8.dtype), (k_scale, "k_scale", torch.float32),
+                               (v_scale, "v_scale", torch.float32)),
+                      ((cache_seqlens, "cache_seqlens", torch.int32), (workspace, "workspace", None)))
+    _check_cache8(k8, v8, k_scale, v_scale, block)
+    B, Hkv, Nk, d = k8.shape
+    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != d:
+        raise ValueError("q must be [B,Hq,Nq,d], with the cache's batch and head_dim")
+    Hq, Nq = q.shape[1], q.shape[2]
+    o = torch.empty(q.shape, dtype=torch.float32 if out_f32 else q.dtype, device=dev)
+    lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev) if with_lse else None
+    if workspace is None:
+        need = _lib.attn_fwd_kvcache8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        st = _lib.attn_fwd_kvcache8(q.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                    _lens_ptr(cache_seqlens, "cache_seqlens", B), o.data_ptr(),
+                                    lse.data_ptr() if with_lse else None, workspace.data_ptr(),
+                                    workspace.numel() * workspace.element_size(), B, Hq, Hkv, Nq, Nk, d, block, causal,
+                                    _scale_arg(scale), _dtype_code(q), _DT8[k8.dtype],
+                                    _lib.ATTN_FLAG_OUT_F32 if out_f32 else 0, _stream())
+    _lib._check(st, "attn_fwd_kvcache8")
+    return o, lse
+
+
+def kvcache_weights(q, k_cache, lse, cache_seqlens=None, causal: bool = False, scale=None, weights=None, out=None):
+    """The attention weight that each cached key receives from these queries, added up over them
+    and over the query heads of its kv head.  q [B,Hq,Nq,d], k_cache [B,Hkv,Nk,d], cache_seqlens,
+    causal and scale as given to fwd_kvcache (or fwd), and lse [B,Hq,Nq] as it returned it.
+    weights float32 [B,Hkv,Nk]: what earlier queries added up to (None: zeros).  out: where to
+    write (may be weights).  Returns float32 [B,Hkv,Nk]."""
+    _require(q, "q")
+    dev = _cache_args(q, "q", ((k_cache, "k_cache", q.dtype), (lse, "lse", torch.float32)),
+                      ((cache_seqlens, "cache_seqlens", torch.int32), (weights, "weights", torch.float32),
+                       (out, "out", torch.float32)))
+    if q.dim() != 4 or k_cache.dim() != 4:
+        raise ValueError("q must be [B,Hq,Nq,d] and k_cache [B,Hkv,Nk,d]")
+    B, Hq, Nq, d = q.shape
+    _, Hkv, Nk, dk = k_cache.shape
+    if k_cache.shape[0] != B or dk != d:
+        raise ValueError("q and the cache disagree on batch or head_dim")
+    if lse.shape != (B, Hq, Nq):
+        raise ValueError("lse must be [B,Hq,Nq]")
+    for t, n in ((weights, "weights"), (out, "out")):
+        if t is not None and t.shape != (B, Hkv, Nk):
+            raise ValueError(f"{n} must be [B,Hkv,Nk]")
+    if out is None:
+        out = torch.empty((B, Hkv, Nk), dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        st = _lib.attn_kvcache_weights(q.data_ptr(), k_cache.data_ptr(), lse.data_ptr(),
+                                       _lens_ptr(cache_seqlens, "cache_seqlens", B),
+                                       weights.data_ptr() if weights is not None else None, out.data_ptr(), B, Hq, Hkv,
+                                       Nq, Nk, d, causal, _scale_arg(scale), _dtype_code(q), _stream())
+    _lib._check(st, "attn_kvcache_weights")
+    return out
+
+
+def kvcache_evict(k_cache, v_cache, weights, keep: int, recent: int, cache_seqlens=None, out=None):
+    """Cuts caches down to their last `recent` keys and, of the others, the `keep` of the largest
+    weights (per batch and kv head; equal weights: the lowest positions), in the order of their
+    positions.  k_cache, v_cache [B,Hkv,Nk,d]; weights float32 [B,Hkv,Nk]; cache_seqlens int32 [B]
+    on the device (None: Nk each).  out: (k_out, v_out) [B,Hkv,capacity,d] to write into, capacity
+    >= keep + recent; rows past the kept ones are left as they are (None: new caches of capacity
+    keep + recent, zeros past the kept ones).  Returns (k_out, v_out, weights
+    [B,Hkv,capacity], index int32 [B,Hkv,keep+recent] with -1 past the kept keys, lengths int32
+    [B])."""
+    _require(k_cache, "k_cache")
+    dev = _cache_args(k_cache, "k_cache", ((v_cache, "v_cache", k_cache.dtype), (weights, "weights", torch.float32)),
+                      ((cache_seqlens, "cache_seqlens", torch.int32),))
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or weights.shape != k_cache.shape[:3]:
+        raise ValueError("k_cache and v_cache must be [B,Hkv,Nk,d] and weights [B,Hkv,Nk]")
+    B, Hkv, Nk, d = k_cache.shape
+    keep, recent = int(keep), int(recent)
+    if keep < 0 or recent < 0 or keep + recent < 1:
+        raise ValueError("keep and recent must not be negative, nor both zero")
+    if out is None:
+        out = tuple(torch.zeros((B, Hkv, keep + recent, d), dtype=k_cache.dtype, device=dev) for _ in range(2))
+    k_out, v_out = out
+    _cache_args(k_cache, "k_cache", ((k_out, "k_out", k_cache.dtype), (v_out, "v_out", k_cache.dtype)))
+    if k_out.dim() != 4 or k_out.shape != v_out.shape or k_out.shape[:2] != (B, Hkv) or k_out.shape[3] != d:
+        raise ValueError("k_out and v_out must be [B,Hkv,capacity,d]")
+    cap = k_out.shape[2]
+    if cap < keep + recent:
+        raise ValueError("the capacity of k_out and v_out must be at least keep + recent")
+    w_out = torch.empty((B, Hkv, cap), dtype=torch.float32, device=dev)
+    index = torch.empty((B, Hkv, keep + recent), dtype=torch.int32, device=dev)
+    lens = torch.empty((B,), dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        st = _lib.attn_kvcache_evict(k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(),
+                                     _lens_ptr(cache_seqlens, "cache_seqlens", B), k_out.data_ptr(), v_out.data_ptr(),
+                                     w_out.data_ptr(), index.data_ptr(), lens.data_ptr(), B, Hkv, Nk, cap, d, keep,
+                                     recent, _dtype_code(k_cache), _stream())
+    _lib._check(st, "attn_kvcache_evict")
+    return k_out, v_out, w_out, index, lens
 
 
 class _AttnFn(torch.autograd.Function):

@@ -613,6 +613,170 @@ attn_status_t attn_fwd_kvcache(const void* q, const void* k_cache, const void* v
   return from_cuda(attn::launch_kv_combine(p, dtype, causal != 0, s));
 }
 
+namespace {
+
+// Sizes shared by the calls on [B, Hkv, Nk, d] caches; the grids and row counts are 32-bit.
+attn_status_t check_cache(int B, int Hkv, int Nk, int d) {
+  if (B < 0 || Hkv <= 0 || Nk < 0 || d <= 0) return ATTN_ERR_INVALID_ARG;
+  if (d % 16 != 0 || d > 128) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * Hkv > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+bool block_ok(int block) { return block == 16 || block == 32 || block == 64 || block == 128; }
+
+bool cache_dtype_ok(attn_cache_dtype_t c) { return c == ATTN_CACHE_I8 || c == ATTN_CACHE_E4M3; }
+
+bool dtype_ok(attn_dtype_t dt) { return dt == ATTN_F32 || dt == ATTN_F16 || dt == ATTN_BF16; }
+
+bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + bn && y < x + an;
+}
+
+}  // namespace
+
+attn_status_t attn_kvcache8_append(void* k8, void* v8, float* k_scale, float* v_scale, const void* k_new,
+                                   const void* v_new, const int32_t* cache_seqlens, const int32_t* new_seqlens, int B,
+                                   int Hkv, int Nn, int Nk, int d, int block, attn_dtype_t dtype,
+                                   attn_cache_dtype_t cache_dtype, void* stream) {
+  attn_status_t st = check_cache(B, Hkv, Nk, d);
+  if (st != ATTN_OK) return st;
+  if (!dtype_ok(dtype) || !cache_dtype_ok(cache_dtype) || !block_ok(block) || Nn < 0) return ATTN_ERR_INVALID_ARG;
+  if (B == 0 || Nn == 0) return ATTN_OK;
+  if (Nn > Nk) return ATTN_ERR_INVALID_ARG;
+  if (!all_aligned16({k8, v8, k_new, v_new}) || !k_scale || !v_scale || !aligned(k_scale, 4) || !aligned(v_scale, 4) ||
+      !aligned(cache_seqlens, 4) || !aligned(new_seqlens, 4))
+    return ATTN_ERR_INVALID_ARG;
+  attn::AppendParams p{};
+  p.x8[0] = static_cast<uint8_t*>(k8); p.x8[1] = static_cast<uint8_t*>(v8);
+  p.scale[0] = k_scale; p.scale[1] = v_scale;
+  p.x_new[0] = k_new; p.x_new[1] = v_new;
+  p.cache_seqlens = cache_seqlens;
+  p.new_seqlens = new_seqlens;
+  p.B = B; p.Hkv = Hkv; p.Nn = Nn; p.Nk = Nk; p.d = d; p.block = block;
+  p.n_blocks = static_cast<int>((static_cast<long long>(Nk) + block - 1) / block);
+  // tokens L .. L + Nn - 1 touch the most blocks when L is the last token of one
+  p.blocks_per_head = static_cast<int>(std::min<long long>((static_cast<long long>(Nn) + block - 2) / block + 1, p.n_blocks));
+  if (static_cast<long long>(B) * Hkv * 2 * p.blocks_per_head > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  if (!(p.status = status_word())) return ATTN_ERR_CUDA;
+  return from_cuda(attn::launch_cache8_append(p, dtype, cache_dtype, static_cast<cudaStream_t>(stream)));
+}
+
+size_t attn_fwd_kvcache8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Nq <= 0 || Nk < 0 || d <= 0) return 0;
+  return 256;
+}
+
+attn_status_t attn_fwd_kvcache8(const void* q, const void* k8, const void* v8, const float* k_scale,
+                                const float* v_scale, const int32_t* cache_seqlens, void* o, float* lse,
+                                void* workspace, size_t workspace_bytes, int B, int Hq, int Hkv, int Nq, int Nk, int d,
+                                int block, int causal, float scale, attn_dtype_t dtype, attn_cache_dtype_t cache_dtype,
+                                unsigned flags, void* stream) {
+  attn_status_t st = check_common(d, scale, dtype);
+  if (st != ATTN_OK) return st;
+  if (B < 0 || Nq < 0 || Nk < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+  if (flags & ~ATTN_FLAG_OUT_F32) return ATTN_ERR_INVALID_ARG;
+  if (!cache_dtype_ok(cache_dtype) || !block_ok(block)) return ATTN_ERR_INVALID_ARG;
+  if (dtype == ATTN_F32) return ATTN_ERR_UNSUPPORTED;
+  if (B == 0 || Nq == 0) return ATTN_OK;
+  // an empty cache (Nk == 0) is never read: its pointers may be null
+  if (!all_aligned16({q, o}) || (Nk > 0 && (!k8 || !v8 || !k_scale || !v_scale)) || !aligned(k8, 16) || !aligned(v8, 16) ||
+      !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(lse, 4) || !aligned(cache_seqlens, 4))
+    return ATTN_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < attn_fwd_kvcache8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d))
+    return ATTN_ERR_INVALID_ARG;
+  const long long R = static_cast<long long>(Hq / Hkv) * Nq;
+  if (R > 0x7fffffffLL || static_cast<long long>(B) * Hkv * R > 0x7fffffffLL || static_cast<long long>(B) * Hq > 0x7fffffffLL)
+    return ATTN_ERR_UNSUPPORTED;
+  attn::Cache8Params p{};
+  p.q = q;
+  p.k8 = static_cast<const uint8_t*>(k8);
+  p.v8 = static_cast<const uint8_t*>(v8);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.cache_seqlens = cache_seqlens;
+  p.o = o;
+  p.lse = lse;
+  p.wait_ns = wait_limit_ns();
+  if (!(p.status = status_word())) return ATTN_ERR_CUDA;
+  p.B = B; p.Hkv = Hkv; p.Nq = Nq; p.Nk = Nk; p.R = static_cast<int>(R); p.d = d;
+  p.block_shift = block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7;
+  p.n_blocks = static_cast<int>((static_cast<long long>(Nk) + block - 1) / block);
+  p.causal = causal != 0;
+  p.scale_log2 = resolve_scale(scale, d) * kLog2e;
+  p.out_f32 = (flags & ATTN_FLAG_OUT_F32) ? 1 : 0;
+  return from_cuda(attn::launch_cache8_fwd(p, dtype, cache_dtype, static_cast<cudaStream_t>(stream)));
+}
+
+attn_status_t attn_kvcache_weights(const void* q, const void* k_cache, const float* lse, const int32_t* cache_seqlens,
+                                   const float* weights_in, float* weights_out, int B, int Hq, int Hkv, int Nq, int Nk,
+                                   int d, int causal, float scale, attn_dtype_t dtype, void* stream) {
+  attn_status_t st = check_common(d, scale, dtype);
+  if (st != ATTN_OK) return st;
+  if (B < 0 || Nq < 0 || Nk < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+  if (B == 0 || Nk == 0) return ATTN_OK;
+  if (!weights_out || !aligned(weights_out, 4) || !aligned(weights_in, 4) || !aligned(cache_seqlens, 4))
+    return ATTN_ERR_INVALID_ARG;
+  const long long R = static_cast<long long>(Hq / Hkv) * Nq, bh = static_cast<long long>(B) * Hkv;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (Nq == 0) {  // no query adds anything
+    const size_t bytes = static_cast<size_t>(bh) * Nk * sizeof(float);
+    if (!weights_in) return from_cuda(cudaMemsetAsync(weights_out, 0, bytes, s));
+    return weights_in == weights_out ? ATTN_OK
+                                     : from_cuda(cudaMemcpyAsync(weights_out, weights_in, bytes, cudaMemcpyDeviceToDevice, s));
+  }
+  if (!all_aligned16({q, k_cache}) || !lse || !aligned(lse, 4)) return ATTN_ERR_INVALID_ARG;
+  if (R > 0x7fffffffLL || bh * R > 0x7fffffffLL || static_cast<long long>(B) * Hq > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  if (bh * ((static_cast<long long>(Nk) + 63) / 64) > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  attn::WeightParams p{};
+  p.q = q;
+  p.k = k_cache;
+  p.lse = lse;
+  p.cache_seqlens = cache_seqlens;
+  p.w_in = weights_in;
+  p.w_out = weights_out;
+  p.wait_ns = wait_limit_ns();
+  if (!(p.status = status_word())) return ATTN_ERR_CUDA;
+  p.B = B; p.Hkv = Hkv; p.Nq = Nq; p.Nk = Nk; p.R = static_cast<int>(R); p.d = d;
+  p.causal = causal != 0;
+  p.scale_log2 = resolve_scale(scale, d) * kLog2e;
+  return from_cuda(attn::launch_cache_weights(p, dtype, s));
+}
+
+attn_status_t attn_kvcache_evict(const void* k_cache, const void* v_cache, const float* weights,
+                                 const int32_t* cache_seqlens, void* k_out, void* v_out, float* weights_out,
+                                 int32_t* index, int32_t* out_seqlens, int B, int Hkv, int Nk, int capacity, int d,
+                                 int keep, int recent, attn_dtype_t dtype, void* stream) {
+  attn_status_t st = check_cache(B, Hkv, Nk, d);
+  if (st != ATTN_OK) return st;
+  if (!dtype_ok(dtype) || keep < 0 || recent < 0) return ATTN_ERR_INVALID_ARG;
+  const long long M = static_cast<long long>(keep) + recent;
+  if (M < 1 || capacity < M) return ATTN_ERR_INVALID_ARG;
+  if (B == 0) return ATTN_OK;
+  const long long bh = static_cast<long long>(B) * Hkv;
+  if ((Nk > 0 && (!k_cache || !v_cache || !weights)) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(weights, 4) ||
+      !all_aligned16({k_out, v_out}) || !weights_out || !aligned(weights_out, 4) || !index || !aligned(index, 4) ||
+      !out_seqlens || !aligned(out_seqlens, 4) || !aligned(cache_seqlens, 4))
+    return ATTN_ERR_INVALID_ARG;
+  const size_t es = dtype == ATTN_F32 ? 4 : 2, row = static_cast<size_t>(d) * es;
+  const size_t in_bytes = static_cast<size_t>(bh) * Nk * row, out_bytes = static_cast<size_t>(bh) * capacity * row;
+  const size_t w_bytes = static_cast<size_t>(bh) * Nk * 4, wo_bytes = static_cast<size_t>(bh) * capacity * 4;
+  for (const void* out : {static_cast<const void*>(k_out), static_cast<const void*>(v_out)})
+    if (overlap(out, out_bytes, k_cache, in_bytes) || overlap(out, out_bytes, v_cache, in_bytes)) return ATTN_ERR_INVALID_ARG;
+  if (overlap(k_out, out_bytes, v_out, out_bytes) || overlap(weights_out, wo_bytes, weights, w_bytes)) return ATTN_ERR_INVALID_ARG;
+  attn::EvictParams p{};
+  p.k = k_cache; p.v = v_cache; p.w = weights;
+  p.cache_seqlens = cache_seqlens;
+  p.k_out = k_out; p.v_out = v_out; p.w_out = weights_out;
+  p.index = index;
+  p.out_seqlens = out_seqlens;
+  if (!(p.status = status_word())) return ATTN_ERR_CUDA;
+  p.B = B; p.Hkv = Hkv; p.Nk = Nk; p.cap = capacity; p.keep = keep; p.recent = recent; p.M = static_cast<int>(M);
+  p.row_bytes = static_cast<int>(row);
+  return from_cuda(attn::launch_cache_evict(p, static_cast<cudaStream_t>(stream)));
+}
+
 attn_status_t attn_get_device_status(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return ATTN_ERR_CUDA;
   unsigned* w = status_word();
@@ -638,6 +802,6 @@ const char* attn_status_string(attn_status_t status) {
   return "unknown status";
 }
 
-int attn_version(void) { return 100; }
+int attn_version(void) { return 101; }
 
 }  // extern "C"

@@ -138,4 +138,65 @@ cudaError_t launch_bwd_tc(const BwdMaps& maps, const BwdParams& p, attn_dtype_t 
                           cudaStream_t stream);  // varlen when p.cu_seqlens is set
 cudaError_t launch_bwd_f32(const BwdParams& p, bool causal, cudaStream_t stream);
 
+// ---------------------------------------------------------------- KV caches in 8 bits, eviction
+struct AppendParams {
+  uint8_t* x8[2];          // k8, v8
+  float* scale[2];         // [B,Hkv,n_blocks]
+  const void* x_new[2];    // [B,Hkv,Nn,d]
+  const int32_t* cache_seqlens;  // nullable: 0 each
+  const int32_t* new_seqlens;    // nullable: Nn each
+  unsigned* status;
+  int B, Hkv, Nn, Nk, d, block, n_blocks;
+  int blocks_per_head;     // the most blocks that Nn tokens touch: CTAs per (batch, kv head)
+};
+cudaError_t launch_cache8_append(const AppendParams& p, attn_dtype_t dtype, attn_cache_dtype_t cache, cudaStream_t stream);
+
+// Attention over an 8-bit cache: rows r = g * Nq + i of a (batch, kv head) as in FwdParams.
+struct Cache8Params {
+  const void* q;           // [B*Hkv, R, d]
+  const uint8_t* k8;       // [B*Hkv, Nk, d]
+  const uint8_t* v8;
+  const float* k_scale;    // [B*Hkv, n_blocks]
+  const float* v_scale;
+  const int32_t* cache_seqlens;  // nullable: Nk each
+  void* o;                 // [B*Hkv, R, d]
+  float* lse;              // [B*Hkv, R]; nullable
+  unsigned* status;
+  unsigned long long wait_ns;
+  int B, Hkv, Nq, Nk, R, d, block_shift, n_blocks, causal;
+  float scale_log2;
+  int out_f32;
+};
+cudaError_t launch_cache8_fwd(const Cache8Params& p, attn_dtype_t dtype, attn_cache_dtype_t cache, cudaStream_t stream);
+
+struct WeightParams {
+  const void* q;           // [B*Hkv, R, d]
+  const void* k;           // [B*Hkv, Nk, d]
+  const float* lse;        // [B*Hkv, R]
+  const int32_t* cache_seqlens;  // nullable: Nk each
+  const float* w_in;       // [B*Hkv, Nk]; nullable
+  float* w_out;
+  unsigned* status;
+  unsigned long long wait_ns;
+  int B, Hkv, Nq, Nk, R, d, causal;
+  float scale_log2;
+};
+cudaError_t launch_cache_weights(const WeightParams& p, attn_dtype_t dtype, cudaStream_t stream);
+
+struct EvictParams {
+  const void* k;           // [B*Hkv, Nk, d]
+  const void* v;
+  const float* w;          // [B*Hkv, Nk]
+  const int32_t* cache_seqlens;  // nullable: Nk each
+  void* k_out;             // [B*Hkv, cap, d]
+  void* v_out;
+  float* w_out;            // [B*Hkv, cap]
+  int32_t* index;          // [B*Hkv, M]
+  int32_t* out_seqlens;    // [B]
+  unsigned* status;
+  int B, Hkv, Nk, cap, keep, recent, M;
+  int row_bytes;           // d * sizeof(dtype), a multiple of 16
+};
+cudaError_t launch_cache_evict(const EvictParams& p, cudaStream_t stream);
+
 }  // namespace attn

@@ -58,7 +58,8 @@ typedef enum {
   ATTN_ERR_CUDA = 3,         /* a CUDA runtime/driver call failed (launch, tensor map, ...) */
   ATTN_ERR_TIMEOUT = 4,      /* device: a pipeline wait exceeded its time limit; CTA stopped */
   ATTN_ERR_DEVICE_INPUT = 5  /* device: cu_seqlens not non-decreasing from 0, a sequence
-                                longer than max_seqlen, or a cache length outside [0, Nk] */
+                                longer than max_seqlen, a cache length outside [0, Nk], or
+                                tokens appended past the end of a cache */
 } attn_status_t;
 
 #define ATTN_FLAG_OUT_F32 1u
@@ -226,6 +227,94 @@ attn_status_t attn_fwd_kvcache(const void* q, const void* k_cache, const void* v
                                void* o, float* lse, void* workspace, size_t workspace_bytes, int B, int Hq, int Hkv,
                                int Nq, int Nk, int d, int causal, float scale, int num_splits, attn_dtype_t dtype,
                                unsigned flags, void* stream);
+
+/*
+ * A KV cache held in 8 bits.  Serving keeps the cache of every sequence on the device and reads
+ * it once per token (the FlashAttention-T review, FAQ 4 and practical advice 2: blocked KV-cache
+ * computation, the decode phase), so its bytes bound the time; these calls hold them in 8 bits.
+ *   k8, v8           [B, Hkv, Nk, d] codes of cache_dtype: int8 (codes -127 .. 127) or e4m3
+ *   k_scale, v_scale [B, Hkv, ceil(Nk / block)] float32: one scale per head and block of `block`
+ *                    consecutive tokens; token j stands for code * scale[j / block]
+ *   block            16, 32, 64 or 128
+ */
+typedef enum { ATTN_CACHE_I8 = 0, ATTN_CACHE_E4M3 = 1 } attn_cache_dtype_t;
+
+/*
+ * Writes new tokens into an 8-bit cache, in place.  Batch b's tokens go to positions
+ * L .. L + n - 1, L = cache_seqlens[b] and n = new_seqlens[b]; the lengths themselves are not
+ * changed.  For each block that receives tokens, of keys and of values alike and in float32
+ * throughout (every operation rounded to nearest):
+ *   s     = max |x| over its new tokens times 1/127 (int8) or 1/448 (e4m3); below 2^-126: 0
+ *   s     = the larger of s and the block's present scale when it already holds tokens (< L)
+ *   code  = round to nearest even (x * (1/s)), within the type's range; 0 when s is 0
+ * and when the scale of a block that holds tokens grew, their codes are recoded,
+ * round(code * (s_old * (1/s))).  Writing the same tokens at the same place again changes
+ * nothing.  An infinity or NaN among a block's tokens makes its scale that and the block reads back
+ * as infinities and NaN.  Blocks and tokens outside L .. L + n - 1 are left as they are, but for
+ * that recoding; the scale of a block without tokens is never read.
+ *   k_new, v_new   [B, Hkv, Nn, d] (dtype: float32, float16 or bfloat16)
+ *   cache_seqlens  DEVICE int32 [B], or NULL: empty caches (L = 0)
+ *   new_seqlens    DEVICE int32 [B], 0 <= new_seqlens[b] <= Nn, or NULL: Nn each
+ * A batch with a length out of its range, or L + n > Nk, is left untouched and
+ * attn_get_device_status() returns ATTN_ERR_DEVICE_INPUT.
+ */
+attn_status_t attn_kvcache8_append(void* k8, void* v8, float* k_scale, float* v_scale, const void* k_new,
+                                   const void* v_new, const int32_t* cache_seqlens, const int32_t* new_seqlens, int B,
+                                   int Hkv, int Nn, int Nk, int d, int block, attn_dtype_t dtype,
+                                   attn_cache_dtype_t cache_dtype, void* stream);
+
+/*
+ * attn_fwd_kvcache over an 8-bit cache: O = softmax(scale * Q K^T, masked) V with the keys and
+ * values that the codes and scales stand for.  Shapes, masks, rows without keys, flags and
+ * argument rules are those of attn_fwd_kvcache; dtype (of q and o) is ATTN_F16 or ATTN_BF16
+ * (ATTN_F32: ATTN_ERR_UNSUPPORTED).  The split over key ranges is chosen from the sizes.
+ *   workspace  DEVICE, at least attn_fwd_kvcache8_workspace_bytes(...) bytes, 256-byte aligned;
+ *              contents on entry are ignored, on exit undefined.  Calls that may run at the same
+ *              time need one each.
+ */
+size_t attn_fwd_kvcache8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d);
+attn_status_t attn_fwd_kvcache8(const void* q, const void* k8, const void* v8, const float* k_scale,
+                                const float* v_scale, const int32_t* cache_seqlens, void* o, float* lse,
+                                void* workspace, size_t workspace_bytes, int B, int Hq, int Hkv, int Nq, int Nk, int d,
+                                int block, int causal, float scale, attn_dtype_t dtype, attn_cache_dtype_t cache_dtype,
+                                unsigned flags, void* stream);
+
+/*
+ * The attention weight that each cached key receives, added up over the queries and over the
+ * query heads of its kv head -- the sums by which attn_kvcache_evict chooses:
+ *   weights_out[b, h, j] = weights_in[b, h, j] + sum over heads g of h and queries i that see key j
+ *                          of exp(scale * Q_gi . K_j - lse_gi)
+ *   q, k_cache, cache_seqlens, causal, scale, dtype: as given to attn_fwd_kvcache (or, with
+ *                Nq == Nk and no lengths, to attn_fwd)
+ *   lse          its float32 LSE [B, Hq, Nq]; a row with LSE -inf (no key) adds nothing
+ *   weights_in   [B, Hkv, Nk] float32, or NULL: zeros
+ *   weights_out  [B, Hkv, Nk] float32; may be weights_in.  Keys past a cache's length get
+ *                weights_in (0 when it is NULL)
+ * The sums are float32, in an order fixed by the sizes: results are bitwise reproducible.
+ */
+attn_status_t attn_kvcache_weights(const void* q, const void* k_cache, const float* lse, const int32_t* cache_seqlens,
+                                   const float* weights_in, float* weights_out, int B, int Hq, int Hkv, int Nq, int Nk,
+                                   int d, int causal, float scale, attn_dtype_t dtype, void* stream);
+
+/*
+ * Cuts caches down to the keys that matter: of a (batch, kv head)'s L keys the last `recent` stay,
+ * and of the others the `keep` with the largest weights (equal weights: the lowest positions; a
+ * NaN counts as larger than every number).  With L <= keep + recent all stay.  The kept keys are
+ * copied, in the order of their positions, to the front of another cache.
+ *   k_cache, v_cache, weights   [B, Hkv, Nk, d] (dtype), [B, Hkv, Nk] float32
+ *   cache_seqlens  DEVICE int32 [B], or NULL: Nk keys for every batch
+ *   k_out, v_out   [B, Hkv, capacity, d], capacity >= keep + recent; they must not overlap the
+ *                  inputs.  Rows past the kept ones are left as they are
+ *   weights_out    [B, Hkv, capacity] float32: the kept keys' weights, then zeros
+ *   index          int32 [B, Hkv, keep + recent]: the kept keys' positions, then -1
+ *   out_seqlens    int32 [B]: min(L, keep + recent)
+ * keep, recent >= 0 and keep + recent >= 1.  A cache_seqlens entry outside [0, Nk] counts as 0
+ * and attn_get_device_status() returns ATTN_ERR_DEVICE_INPUT.
+ */
+attn_status_t attn_kvcache_evict(const void* k_cache, const void* v_cache, const float* weights,
+                                 const int32_t* cache_seqlens, void* k_out, void* v_out, float* weights_out,
+                                 int32_t* index, int32_t* out_seqlens, int B, int Hkv, int Nk, int capacity, int d,
+                                 int keep, int recent, attn_dtype_t dtype, void* stream);
 
 /*
  * attn_bwd_noalloc -- the backward (same arguments, layouts and results as attn_bwd) for callers

@@ -1,0 +1,319 @@
+"""GPU tests of the 8-bit KV cache: codes and scales bit by bit against the definition in single
+float32 operations, attention against 64 bits with bounds from the roundings that the kernels
+make, and what a serving program does with them (graphs, streams, ragged and padded batches)."""
+import numpy as np
+import pytest
+import torch
+
+from exact_attention_50_gb300 import _lib, build
+from exact_attention_50_gb300 import attention as A
+from tests import cache_plain as P
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def dev():
+    assert torch.cuda.is_available(), "the gpu tests need a CUDA device"
+    build.build()
+    _lib.load()
+    return torch.device("cuda:0")
+
+
+def rows(seed, shape, dev, dtype=torch.float32):
+    """Keys or values with columns and tokens of different magnitude."""
+    g = torch.Generator(dev).manual_seed(seed)
+    x = torch.randn(shape, generator=g, device=dev)
+    x *= torch.exp(0.5 * torch.randn(shape[:2] + (1, shape[3]), generator=g, device=dev))
+    x *= torch.exp(0.5 * torch.randn(shape[:3] + (1,), generator=g, device=dev))
+    return x.to(dtype)
+
+
+def status_ok():
+    torch.cuda.synchronize()
+    assert A.get_device_status() == _lib.ATTN_OK
+
+
+# ------------------------------------------------------------------------------------- append
+def values(x8):
+    return x8.float().cpu().numpy()
+
+
+@pytest.mark.parametrize("cache", ["i8", "e4m3"])
+@pytest.mark.parametrize("dtype,d,block", [("bf16", 128, 64), ("f16", 64, 32), ("f32", 80, 16), ("bf16", 16, 128), ("f32", 128, 128)])
+def test_append_matches_the_definition_bit_by_bit(dev, cache, dtype, d, block):
+    """Ragged lengths around the blocks' edges, one batch that appends nothing, one that fills its
+    cache; everything outside the touched blocks, and the scales of untouched ones, stays."""
+    Nk, Nn = 301, 150
+    lens, new = [0, 1, block - 1, block, block + 5, 151, 301, 70], [150, 1, 2, block, 77, 150, 0, 0]
+    B, H = len(lens), 3
+    k8, v8 = ((torch.randint(-120, 120, (B, H, Nk, d), device=dev).to(torch.int8) if cache == "i8"
+               else torch.randn(B, H, Nk, d, device=dev).mul(60).to(torch.float8_e4m3fn)) for _ in range(2))
+    nb = -(-Nk // block)
+    ks, vs = (torch.rand(B, H, nb, device=dev) * (0.02 if cache == "i8" else 0.005) for _ in range(2))
+    kn, vn = (rows(i, (B, H, Nn, d), dev, DT[dtype]) for i in (1, 2))
+    kn[4, 1] *= 0.001   # a block's present scale stays
+    vn[3] = 0           # a block of zeros: scale 0
+    vn[1] *= 1e-38 if dtype == "f32" else 1  # scales below the smallest normal number
+    want = []
+    for x8, s, x in ((k8, ks, kn), (v8, vs, vn)):
+        c, sc, xn = values(x8), s.cpu().numpy().copy(), x.float().cpu().numpy()
+        for b in range(B):
+            for h in range(H):
+                P.append(c[b, h], sc[b, h], xn[b, h], lens[b], new[b], block, cache)
+        want.append((c, sc))
+    cl, nl = (torch.tensor(x, dtype=torch.int32, device=dev) for x in (lens, new))
+    for _ in range(2):  # the second time changes nothing
+        A.kvcache8_append(k8, v8, ks, vs, kn, vn, cl, nl, block=block)
+        status_ok()
+        for x8, s, (c, sc) in ((k8, ks, want[0]), (v8, vs, want[1])):
+            assert np.array_equal(s.cpu().numpy(), sc)
+            assert np.array_equal(values(x8), c)
+
+
+def test_append_defaults_empty_cache_and_whole_lengths(dev):
+    kn, vn = (rows(i, (2, 2, 40, 64), dev, torch.bfloat16) for i in (3, 4))
+    k8, v8 = (torch.zeros(2, 2, 64, 64, dtype=torch.int8, device=dev) for _ in range(2))
+    ks, vs = (torch.full((2, 2, 1), float("nan"), device=dev) for _ in range(2))  # never read
+    A.kvcache8_append(k8, v8, ks, vs, kn, vn)
+    status_ok()
+    c, s = P.quantise(torch.nn.functional.pad(kn.float(), (0, 0, 0, 24)), 64, "i8")
+    assert float((ks - s).abs().max() / s.max()) < 2.0 ** -22
+    assert float((k8.float() - c.float()).abs().max()) <= 1
+
+
+def test_append_keeps_infinities_and_nan_visible(dev):
+    k8, v8 = (torch.zeros(1, 1, 128, 16, dtype=torch.int8, device=dev) for _ in range(2))
+    ks, vs = (torch.zeros(1, 1, 2, device=dev) for _ in range(2))
+    kn = torch.ones(1, 1, 3, 16, device=dev)
+    vn = kn.clone()
+    kn[0, 0, 1, 3], vn[0, 0, 2, 0] = float("nan"), float("-inf")
+    A.kvcache8_append(k8, v8, ks, vs, kn, vn, torch.tensor([63], dtype=torch.int32, device=dev))
+    status_ok()
+    assert float(ks[0, 0, 0]) == pytest.approx(1 / 127) and bool(torch.isnan(ks[0, 0, 1])) and bool(torch.isinf(vs[0, 0, 1]))
+    # a block that holds a NaN keeps it
+    A.kvcache8_append(k8, v8, ks, vs, torch.ones_like(kn), vn, torch.tensor([66], dtype=torch.int32, device=dev))
+    status_ok()
+    assert bool(torch.isnan(ks[0, 0, 1]))
+
+
+@pytest.mark.parametrize("lens,new", [([100, 10], [4, 1]), ([-1, 10], [1, 1]), ([5, 10], [-1, 1]), ([5, 10], [5, 1]),
+                                      ([2 ** 31 - 1, 10], [4, 1])])
+def test_append_reports_bad_lengths_and_leaves_the_batch(dev, lens, new):
+    k8, v8 = (torch.full((2, 2, 103, 32), 7, dtype=torch.int8, device=dev) for _ in range(2))
+    ks, vs = (torch.full((2, 2, 4), 0.5, device=dev) for _ in range(2))
+    x = torch.full((2, 2, 4, 32), 200.0, device=dev)
+    cl, nl = (torch.tensor(t, dtype=torch.int32, device=dev) for t in (lens, new))
+    A.kvcache8_append(k8, v8, ks, vs, x, x, cl, nl, block=32)
+    torch.cuda.synchronize()
+    assert A.get_device_status() == _lib.ATTN_ERR_DEVICE_INPUT and A.get_device_status() == _lib.ATTN_OK
+    assert bool((k8[0] == 7).all()) and bool((v8[0] == 7).all()) and bool((ks[0] == 0.5).all())
+    assert bool((k8[1, :, 10] == 127).all()) and bool((k8[1, :, 11:] == 7).all())
+
+
+# ------------------------------------------------------------------------------------- attend
+def check_attend(o32, o, lse, q, k8, v8, ks, vs, block, lens, causal, scale=None):
+    """o32: with out_f32.  Bounds: the weights, and where the kernel keeps 16-bit copies of the values
+    those, are each rounded once to the output's type: 2 u P|V| (u half a step); the scores' float32
+    sums give E twice (numerator and denominator), the exponential 2^-18; a weight below the 16-bit
+    range is off by at most 2^-24 of the largest value; the stored output adds u |o|."""
+    u = P.HALF[q.dtype]
+    kd, vd = P.dequantise(k8, ks, block), P.dequantise(v8, vs, block)
+    ro, rl, A_, E = P.attend(q, kd, vd, lens, causal, scale)
+    top = torch.zeros(q.shape[0], 1, 1, 1, dtype=torch.float64, device=q.device)
+    for b in range(q.shape[0]):
+        L = k8.shape[2] if lens is None else int(lens[b])
+        if L:
+            top[b] = vd[b, :, :L].abs().max() * L * 2.0 ** -24
+    bound = A_ * (2 * u + 2 * E[..., None] + 2.0 ** -18) + top
+    assert bool(torch.isfinite(o32).all())
+    assert bool(((o32.double() - ro).abs() <= bound).all()), float(((o32.double() - ro).abs() - bound).max())
+    assert bool(((o.double() - ro).abs() <= bound + u * (ro.abs() + bound) + 2.0 ** -24).all())
+    empty = torch.isneginf(rl)
+    assert torch.equal(torch.isneginf(lse), empty)
+    assert bool((o32[empty] == 0).all())
+    err = (lse.double() - rl).abs().masked_fill(empty, 0)
+    assert bool((err <= E + 2.0 ** -18 + rl.abs().masked_fill(empty, 0) * 2.0 ** -22).all()), float(err.max())
+
+
+def run_attend(dev, B, Hq, Hkv, Nq, Nk, d, block, dtype, cache, lens, causal, seed, poison=True, scale=None):
+    q = torch.randn(B, Hq, Nq, d, generator=torch.Generator(dev).manual_seed(seed), device=dev).to(DT[dtype])
+    k8, ks = P.quantise(rows(seed + 1, (B, Hkv, Nk, d), dev), block, cache)
+    v8, vs = P.quantise(rows(seed + 2, (B, Hkv, Nk, d), dev), block, cache)
+    cl = None if lens is None else torch.tensor(lens, dtype=torch.int32, device=dev)
+    if poison and lens is not None:  # what lies behind a length may hold anything
+        for b, L in enumerate(lens):
+            for x8 in (k8, v8):
+                x8.view(torch.uint8)[b, :, L:] = 0x7f  # 127, or e4m3's NaN
+            first = -(-L // block)
+            ks[b, :, first:], vs[b, :, first:] = float("nan"), float("inf")
+    o32, lse = A.fwd_kvcache8(q, k8, v8, ks, vs, cl, causal, scale, block, out_f32=True)
+    o, lse2 = A.fwd_kvcache8(q, k8, v8, ks, vs, cl, causal, scale, block)
+    status_ok()
+    assert torch.equal(lse, lse2)
+    check_attend(o32, o, lse, q, k8, v8, ks, vs, block, lens, causal, scale)
+    return q, k8, v8, ks, vs, cl, o
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype,cache,d,block", [("bf16", "i8", 128, 64), ("f16", "e4m3", 64, 32), ("bf16", "e4m3", 128, 128),
+                                                 ("f16", "i8", 80, 16), ("bf16", "i8", 16, 64), ("f16", "i8", 48, 128)])
+@pytest.mark.parametrize("Hq,Hkv,Nq", [(8, 2, 1), (4, 4, 1), (8, 1, 2), (6, 2, 5), (16, 2, 5), (4, 1, 37), (8, 2, 130)])
+def test_attend_ragged(dev, causal, dtype, cache, d, block, Hq, Hkv, Nq):
+    """Row counts of 1 to 520 per kv head; caches that are empty, of one token, shorter than the
+    queries, ending inside a block or a tile, and full."""
+    run_attend(dev, 7, Hq, Hkv, Nq, 700, d, block, dtype, cache, [700, 333, 64, 3, 1, 0, 513], causal, seed=Nq)
+
+
+@pytest.mark.parametrize("Nk", [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 1025, 5000])
+@pytest.mark.parametrize("Hq,Hkv,Nq", [(4, 1, 1), (2, 2, 9), (32, 1, 8)])
+def test_attend_lengths(dev, Nk, Hq, Hkv, Nq):
+    run_attend(dev, 2, Hq, Hkv, Nq, Nk, 128, 64, "bf16", "i8", None, True, seed=Nk)
+    run_attend(dev, 2, Hq, Hkv, Nq, Nk, 64, 16, "f16", "e4m3", [Nk, Nk // 2], True, seed=Nk)
+
+
+@pytest.mark.parametrize("cache", ["i8", "e4m3"])
+@pytest.mark.parametrize("Nq,Nk", [(300, 300), (1000, 2500), (129, 4100), (700, 130)])
+def test_attend_prefill(dev, cache, Nq, Nk):
+    run_attend(dev, 2, 4, 2, Nq, Nk, 128, 64, "bf16", cache, [Nk, max(1, Nk - 77)], True, seed=5)
+    run_attend(dev, 1, 4, 4, Nq, Nk, 64, 16, "f16", cache, None, False, seed=6)
+
+
+def test_attend_many_short_sequences(dev):
+    lens = [(37 * b) % 130 for b in range(120)]
+    run_attend(dev, 120, 8, 4, 1, 130, 128, 64, "bf16", "i8", lens, True, seed=7)
+
+
+def test_attend_scales_of_very_different_size(dev):
+    """Blocks whose value scales lie many powers of two apart, the weights concentrated on the
+    small ones and on the large ones; a block of zeros; rows of large and of tiny queries."""
+    B, H, Nk, d, block = 2, 2, 512, 64, 16
+    for dtype in ("bf16", "f16"):
+        q = torch.randn(B, H, 3, d, device=dev)
+        q[:, :, 1] *= 20.0
+        q[:, :, 2] *= 1e-4
+        q = q.to(DT[dtype])
+        k8, ks = P.quantise(rows(11, (B, H, Nk, d), dev), block, "i8")
+        v8, vs = P.quantise(rows(12, (B, H, Nk, d), dev), block, "i8")
+        vs *= torch.exp2(torch.arange(vs.shape[2], device=dev) % 14 - 13.0)
+        vs[:, :, 5] = 0
+        ks[:, :, 9] = 0
+        o32, lse = A.fwd_kvcache8(q, k8, v8, ks, vs, None, False, None, block, out_f32=True)
+        o, _ = A.fwd_kvcache8(q, k8, v8, ks, vs, None, False, None, block)
+        status_ok()
+        check_attend(o32, o, lse, q, k8, v8, ks, vs, block, None, False)
+
+
+def test_attend_scale_argument_and_without_lse(dev):
+    q, k8, v8, ks, vs, cl, o = run_attend(dev, 2, 4, 2, 3, 200, 64, 64, "bf16", "i8", [200, 90], True, 8, scale=0.3)
+    o2, none = A.fwd_kvcache8(q, k8, v8, ks, vs, cl, True, 0.3, 64, with_lse=False)
+    assert none is None and torch.equal(o, o2)
+
+
+def test_attend_empty_cache_and_no_queries(dev):
+    q = torch.randn(2, 4, 3, 64, device=dev).bfloat16()
+    k8, s = torch.zeros(2, 2, 0, 64, dtype=torch.int8, device=dev), torch.zeros(2, 2, 0, device=dev)
+    o, lse = A.fwd_kvcache8(q, k8, k8, s, s)
+    assert torch.count_nonzero(o).item() == 0 and bool(torch.isneginf(lse).all())
+    o, lse = A.fwd_kvcache8(q[:, :, :0].contiguous(), k8, k8, s, s)
+    assert o.shape == (2, 4, 0, 64) and lse.shape == (2, 4, 0)
+    status_ok()
+
+
+@pytest.mark.parametrize("Nq", [1, 200])
+def test_attend_reports_bad_lengths(dev, Nq):
+    q = torch.randn(2, 4, Nq, 64, device=dev).bfloat16()
+    k8 = torch.ones(2, 2, 300, 64, dtype=torch.int8, device=dev)
+    s = torch.ones(2, 2, 5, device=dev)
+    for bad in (301, -1):
+        o, lse = A.fwd_kvcache8(q, k8, k8, s, s, torch.tensor([100, bad], dtype=torch.int32, device=dev))
+        torch.cuda.synchronize()
+        assert A.get_device_status() == _lib.ATTN_ERR_DEVICE_INPUT and A.get_device_status() == _lib.ATTN_OK
+        assert bool(torch.isneginf(lse[1]).all()) and bool((o[1] == 0).all()) and bool((o[0] == 1).all())
+
+
+def test_attend_in_graphs_and_on_other_streams(dev):
+    """Captured once and replayed with other lengths and other codes; two streams at a time, each
+    call with its own workspace; a caller's workspace."""
+    B, Hq, Hkv, Nk, d = 3, 8, 2, 2000, 128
+    q = torch.randn(B, Hq, 1, d, device=dev).bfloat16()
+    k8, ks = P.quantise(rows(21, (B, Hkv, Nk, d), dev), 64, "i8")
+    v8, vs = P.quantise(rows(22, (B, Hkv, Nk, d), dev), 64, "i8")
+    cl = torch.tensor([2000, 700, 1], dtype=torch.int32, device=dev)
+    ws = torch.empty(A.kvcache8_workspace_bytes(B, Hq, Hkv, 1, Nk, d), dtype=torch.uint8, device=dev)
+    A.fwd_kvcache8(q, k8, v8, ks, vs, cl, True, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = A.fwd_kvcache8(q, k8, v8, ks, vs, cl, True, workspace=ws)
+    for lens in ([2000, 700, 1], [5, 1999, 0], [64, 65, 1500]):
+        cl.copy_(torch.tensor(lens, dtype=torch.int32))
+        v8.neg_()
+        ws.fill_(255)  # what it holds does not matter
+        graph.replay()
+        want, wl = A.fwd_kvcache8(q, k8, v8, ks, vs, cl, True)
+        torch.cuda.synchronize()
+        assert torch.equal(o, want) and torch.equal(lse, wl)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    torch.cuda.synchronize()
+    for i in range(6):
+        with torch.cuda.stream(streams[i % 2]):
+            outs.append(A.fwd_kvcache8(q, k8, v8, ks, vs, cl, True)[0])
+    torch.cuda.synchronize()
+    for x in outs:
+        assert torch.equal(x, want)
+    status_ok()
+
+
+def test_attend_refusals_of_the_python_layer(dev):
+    q = torch.randn(2, 4, 1, 64, device=dev).bfloat16()
+    k8 = torch.ones(2, 2, 128, 64, dtype=torch.int8, device=dev)
+    s = torch.ones(2, 2, 2, device=dev)
+    cl = torch.tensor([1, 2], dtype=torch.int32, device=dev)
+    ok = lambda **kw: A.fwd_kvcache8(**{**dict(q=q, k8=k8, v8=k8, k_scale=s, v_scale=s, cache_seqlens=cl), **kw})
+    ok()
+    for kw in (dict(q=q[:1]), dict(q=q[:, :3].contiguous()), dict(k8=k8[..., :32]), dict(v8=k8[:, :1].contiguous()), dict(block=48),
+               dict(block=32), dict(k_scale=s[:, :, :1].contiguous()), dict(cache_seqlens=cl[:1]), dict(cache_seqlens=cl.cpu()),
+               dict(scale=-1.0), dict(q=q.transpose(1, 2)), dict(workspace=torch.empty(8, dtype=torch.uint8, device=dev))):
+        with pytest.raises((ValueError, _lib.AttnError)):
+            ok(**kw)
+    for kw in (dict(k8=k8.float()), dict(v8=k8.to(torch.float8_e4m3fn)), dict(k_scale=s.half()), dict(cache_seqlens=cl.long())):
+        with pytest.raises(TypeError):
+            ok(**kw)
+    with pytest.raises(_lib.AttnError):
+        ok(q=q.float())
+    x = torch.ones(2, 2, 3, 64, device=dev)
+    for kw in (dict(k_new=x[:, :1].contiguous()), dict(k_new=torch.ones(2, 2, 129, 64, device=dev), v_new=torch.ones(2, 2, 129, 64, device=dev)),
+               dict(new_seqlens=cl[:1])):
+        with pytest.raises((ValueError, _lib.AttnError)):
+            A.kvcache8_append(**{**dict(k8=k8, v8=k8.clone(), k_scale=s, v_scale=s.clone(), k_new=x, v_new=x), **kw})
+    status_ok()
+
+
+def test_offsets_past_32_bits(dev):
+    """A cache of more than 2^32 bytes per tensor: the last sequence's codes are found and written."""
+    B, Nk, d = 3, 2 ** 23 * 3 // 2 + 100, 128  # 12.6 M tokens: 1.6 GB of codes each, the last from 3.2 GB on
+    Hkv = 3                                    # 14.5 GB per tensor
+    k8, v8 = (torch.zeros(B, Hkv, Nk, d, dtype=torch.int8, device=dev) for _ in range(2))
+    ks, vs = (torch.zeros(B, Hkv, -(-Nk // 128), device=dev) for _ in range(2))
+    L = [5, 40, Nk - 3]
+    x, y = (rows(i, (B, Hkv, 3, d), dev, torch.bfloat16) for i in (31, 32))
+    A.kvcache8_append(k8, v8, ks, vs, x, y, torch.tensor(L, dtype=torch.int32, device=dev), block=128)
+    q = torch.randn(B, Hkv, 1, d, device=dev).bfloat16()
+    cl = torch.tensor([8, 43, Nk], dtype=torch.int32, device=dev)
+    o, lse = A.fwd_kvcache8(q, k8, v8, ks, vs, cl, False, 4.0, 128, out_f32=True)
+    status_ok()
+    # every earlier key is zero: scores 0, weight exp(0), values 0
+    back = lambda x8, s, b, h: x8[b, h, L[b]:L[b] + 3].double() * torch.stack([s[b, h, (L[b] + i) // 128] for i in range(3)]).double()[:, None]
+    for b in range(B):
+        for h in range(Hkv):
+            kk, vv = back(k8, ks, b, h), back(v8, vs, b, h)
+            assert float((kk - x[b, h].double()).abs().max()) <= float(x[b, h].abs().max()) / 250
+            s = 4.0 * (kk @ q[b, h, 0].double())
+            m = s.max().clamp(min=0)
+            z = torch.exp(s - m).sum() + L[b] * torch.exp(-m)
+            want = (torch.exp(s - m) / z) @ vv
+            assert float((o[b, h, 0].double() - want).abs().max()) <= 2.0 ** -6 * float(vv.abs().max())
+            assert abs(float(lse[b, h, 0]) - float(m + torch.log(z))) <= 1e-4 * max(1.0, float(m))
