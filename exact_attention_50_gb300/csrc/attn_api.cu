@@ -629,6 +629,26 @@ bool cache_dtype_ok(attn_cache_dtype_t c) { return c == ATTN_CACHE_I8 || c == AT
 
 bool dtype_ok(attn_dtype_t dt) { return dt == ATTN_F32 || dt == ATTN_F16 || dt == ATTN_BF16; }
 
+// The 8-bit codes [heads, Nk, d]: boxes of one tile's tokens, 64 or 128 columns, swizzled over a row's
+// 16-byte chunks; tokens past Nk and columns past d load as zeros.
+bool make_cache8_map(CUtensorMap* map, const void* base, int heads, int Nk, int d) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const uint64_t dims[3] = {static_cast<uint64_t>(d), static_cast<uint64_t>(Nk), static_cast<uint64_t>(heads)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(d), static_cast<uint64_t>(Nk) * d};
+  const uint32_t box[3] = {d <= 64 ? 64u : 128u, attn::kCache8Keys, 1};
+  const uint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, d <= 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// CTAs of the few-rows kernel: two per SM of a 152-SM GPU, no more than there are tiles.
+int cache8_ctas(int B, int Hkv, int Nk) {
+  const long long tiles = static_cast<long long>(B) * Hkv * ((static_cast<long long>(Nk) + attn::kCache8Keys - 1) / attn::kCache8Keys);
+  return static_cast<int>(std::max(1LL, std::min(tiles, 2LL * 152)));
+}
+
 bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + bn && y < x + an;
@@ -665,7 +685,10 @@ attn_status_t attn_kvcache8_append(void* k8, void* v8, float* k_scale, float* v_
 
 size_t attn_fwd_kvcache8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Nq <= 0 || Nk < 0 || d <= 0) return 0;
-  return 256;
+  const size_t R = static_cast<size_t>(Hq / Hkv) * Nq;
+  if (R > static_cast<size_t>(attn::kCache8Rows)) return 256;
+  const size_t rows = 2 * static_cast<size_t>(cache8_ctas(B, Hkv, Nk)) * R;
+  return round256(rows * d * sizeof(float)) + round256(rows * sizeof(float));
 }
 
 attn_status_t attn_fwd_kvcache8(const void* q, const void* k8, const void* v8, const float* k_scale,
@@ -706,7 +729,15 @@ attn_status_t attn_fwd_kvcache8(const void* q, const void* k8, const void* v8, c
   p.causal = causal != 0;
   p.scale_log2 = resolve_scale(scale, d) * kLog2e;
   p.out_f32 = (flags & ATTN_FLAG_OUT_F32) ? 1 : 0;
-  return from_cuda(attn::launch_cache8_fwd(p, dtype, cache_dtype, static_cast<cudaStream_t>(stream)));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (Nk == 0) return from_cuda(attn::launch_cache8_none(p, s));
+  if (R > attn::kCache8Rows) return from_cuda(attn::launch_cache8_wide(p, dtype, cache_dtype, s));
+  p.ctas = cache8_ctas(B, Hkv, Nk);
+  p.o_part = static_cast<float*>(workspace);
+  p.lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + round256(2 * static_cast<size_t>(p.ctas) * R * d * sizeof(float)));
+  CUtensorMap mk, mv;
+  if (!make_cache8_map(&mk, k8, B * Hkv, Nk, d) || !make_cache8_map(&mv, v8, B * Hkv, Nk, d)) return ATTN_ERR_CUDA;
+  return from_cuda(attn::launch_cache8_fwd(mk, mv, p, dtype, cache_dtype, s));
 }
 
 attn_status_t attn_kvcache_weights(const void* q, const void* k_cache, const float* lse, const int32_t* cache_seqlens,

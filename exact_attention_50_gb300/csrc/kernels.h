@@ -166,8 +166,17 @@ struct Cache8Params {
   int B, Hkv, Nq, Nk, R, d, block_shift, n_blocks, causal;
   float scale_log2;
   int out_f32;
+  // few rows (R <= kCache8Rows): the tiles of all caches are dealt to `ctas` CTAs in equal runs; a
+  // run's part of a (batch, kv head) pair that it does not hold whole goes here, two slots a run
+  int ctas;
+  float* o_part;           // [2 * ctas, R, d], normalised
+  float* lse_part;         // [2 * ctas, R], log2
 };
-cudaError_t launch_cache8_fwd(const Cache8Params& p, attn_dtype_t dtype, attn_cache_dtype_t cache, cudaStream_t stream);
+constexpr int kCache8Rows = 64, kCache8Keys = 48;
+cudaError_t launch_cache8_fwd(const CUtensorMap& k, const CUtensorMap& v, const Cache8Params& p, attn_dtype_t dtype,
+                              attn_cache_dtype_t cache, cudaStream_t stream);
+cudaError_t launch_cache8_wide(const Cache8Params& p, attn_dtype_t dtype, attn_cache_dtype_t cache, cudaStream_t stream);
+cudaError_t launch_cache8_none(const Cache8Params& p, cudaStream_t stream);
 
 struct WeightParams {
   const void* q;           // [B*Hkv, R, d]

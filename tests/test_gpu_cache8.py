@@ -185,6 +185,15 @@ def test_attend_many_short_sequences(dev):
     run_attend(dev, 120, 8, 4, 1, 130, 128, 64, "bf16", "i8", lens, True, seed=7)
 
 
+@pytest.mark.parametrize("cache,d", [("i8", 128), ("e4m3", 64)])
+@pytest.mark.parametrize("Hq,Nq", [(8, 1), (32, 1), (32, 5), (32, 10)])
+def test_attend_long_runs_behind_short_sequences(dev, cache, d, Hq, Nq):
+    """Many tiles per CTA, long sequences next to sequences of one tile: a CTA's warps take very
+    unequal numbers of them, and the ring turns many times."""
+    lens = [9000, 1, 1, 40, 12321, 2, 3, 1, 1, 5, 8000]
+    run_attend(dev, len(lens), Hq, 8, Nq, 12321, d, 64, "bf16", cache, lens, True, seed=Nq)
+
+
 def test_attend_scales_of_very_different_size(dev):
     """Blocks whose value scales lie many powers of two apart, the weights concentrated on the
     small ones and on the large ones; a block of zeros; rows of large and of tiny queries."""
