@@ -15,12 +15,14 @@ every step of the computation runs in libattn_gb300.so's kernels.
 """
 from __future__ import annotations
 
+import contextlib
 import math
 
 import torch
 
 from . import _lib
 
+_SAME = contextlib.nullcontext()  # the current device is the tensors'
 _DT8 = {torch.int8: _lib.ATTN_CACHE_I8, torch.float8_e4m3fn: _lib.ATTN_CACHE_E4M3}
 _DT = {torch.float32: _lib.ATTN_F32, torch.float16: _lib.ATTN_F16, torch.bfloat16: _lib.ATTN_BF16}
 
@@ -223,13 +225,19 @@ def fwd_kvcache(q, k_cache, v_cache, cache_seqlens=None, causal: bool = False, s
 
 
 def _cache_args(first, name: str, tensors, optional=()):
-    """Checks of the cache calls: (tensor, name, dtype) each, contiguous and on the first one's
-    GPU.  Returns that device."""
+    """Checks of the cache calls: (tensor, name, dtype or None) each, contiguous and on the first
+    one's GPU."""
+    dev = first.device
     for t, n, dtype in tensors + tuple(x for x in optional if x[0] is not None):
         _require(t, n, dtype)
-        if t.device != first.device:
+        if t.device != dev:
             raise ValueError(f"{n} must be on {name}'s device")
-    return first.device
+
+
+def _device_stream(t: torch.Tensor):
+    """(context to call in, current stream) of the tensor's device."""
+    dev = t.get_device()
+    return (_SAME if dev == torch.cuda.current_device() else torch.cuda.device(dev)), torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _lens_ptr(t, name: str, B: int):
@@ -245,11 +253,13 @@ def _check_cache8(k8, v8, k_scale, v_scale, block: int):
         raise TypeError(f"unsupported cache dtype {k8.dtype}: int8 or float8_e4m3fn")
     if block not in (16, 32, 64, 128):
         raise ValueError("block must be 16, 32, 64 or 128")
-    if k8.dim() != 4 or k8.shape != v8.shape:
+    shape = k8.shape
+    if len(shape) != 4 or shape != v8.shape:
         raise ValueError("k8 and v8 must be [B,Hkv,Nk,d]")
-    B, Hkv, Nk, _ = k8.shape
+    B, Hkv, Nk, d = shape
     if k_scale.shape != (B, Hkv, -(-Nk // block)) or v_scale.shape != k_scale.shape:
         raise ValueError("k_scale and v_scale must be [B,Hkv,ceil(Nk/block)]")
+    return B, Hkv, Nk, d
 
 
 def kvcache8_append(k8, v8, k_scale, v_scale, k_new, v_new, cache_seqlens=None, new_seqlens=None, block: int = 64):
@@ -260,18 +270,18 @@ def kvcache8_append(k8, v8, k_scale, v_scale, k_new, v_new, cache_seqlens=None, 
     scale, 16, 32, 64 or 128."""
     _require(k8, "k8")
     _require(k_new, "k_new")
-    dev = _cache_args(k8, "k8", ((v8, "v8", k8.dtype), (k_scale, "k_scale", torch.float32),
-                                 (v_scale, "v_scale", torch.float32), (k_new, "k_new", None), (v_new, "v_new", k_new.dtype)),
-                      ((cache_seqlens, "cache_seqlens", torch.int32), (new_seqlens, "new_seqlens", torch.int32)))
-    _check_cache8(k8, v8, k_scale, v_scale, block)
-    B, Hkv, Nk, d = k8.shape
+    _cache_args(k8, "k8", ((v8, "v8", k8.dtype), (k_scale, "k_scale", torch.float32),
+                           (v_scale, "v_scale", torch.float32), (k_new, "k_new", None), (v_new, "v_new", k_new.dtype)),
+                ((cache_seqlens, "cache_seqlens", torch.int32), (new_seqlens, "new_seqlens", torch.int32)))
+    B, Hkv, Nk, d = _check_cache8(k8, v8, k_scale, v_scale, block)
     if k_new.dim() != 4 or k_new.shape != v_new.shape or k_new.shape[:2] != (B, Hkv) or k_new.shape[3] != d:
         raise ValueError("k_new and v_new must be [B,Hkv,Nn,d]")
-    with torch.cuda.device(dev):
+    ctx, stream = _device_stream(k8)
+    with ctx:
         st = _lib.attn_kvcache8_append(k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                        k_new.data_ptr(), v_new.data_ptr(), _lens_ptr(cache_seqlens, "cache_seqlens", B),
                                        _lens_ptr(new_seqlens, "new_seqlens", B), B, Hkv, k_new.shape[2], Nk, d, block,
-                                       _dtype_code(k_new), _DT8[k8.dtype], _stream())
+                                       _dtype_code(k_new), _DT8[k8.dtype], stream)
     _lib._check(st, "attn_kvcache8_append")
 
 
@@ -287,26 +297,27 @@ def fwd_kvcache8(q, k8, v8, k_scale, v_scale, cache_seqlens=None, causal: bool =
     Nk tokens each).  Returns (o [B,Hq,Nq,d], lse [B,Hq,Nq] or None)."""
     _require(q, "q")
     _require(k8, "k8")
-    dev = _cache_args(q, "q", ((k8, "k8", None), (v8, "v8", k8.dtype), (k_scale, "k_scale", torch.float32),
-                               (v_scale, "v_scale", torch.float32)),
-                      ((cache_seqlens, "cache_seqlens", torch.int32), (workspace, "workspace", None)))
-    _check_cache8(k8, v8, k_scale, v_scale, block)
-    B, Hkv, Nk, d = k8.shape
+    _cache_args(q, "q", ((k8, "k8", None), (v8, "v8", k8.dtype), (k_scale, "k_scale", torch.float32),
+                         (v_scale, "v_scale", torch.float32)),
+                ((cache_seqlens, "cache_seqlens", torch.int32), (workspace, "workspace", None)))
+    B, Hkv, Nk, d = _check_cache8(k8, v8, k_scale, v_scale, block)
     if q.dim() != 4 or q.shape[0] != B or q.shape[3] != d:
         raise ValueError("q must be [B,Hq,Nq,d], with the cache's batch and head_dim")
-    Hq, Nq = q.shape[1], q.shape[2]
+    _, Hq, Nq, _ = q.shape
+    dev = q.device
     o = torch.empty(q.shape, dtype=torch.float32 if out_f32 else q.dtype, device=dev)
     lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev) if with_lse else None
     if workspace is None:
         need = _lib.attn_fwd_kvcache8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d)
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
+    ctx, stream = _device_stream(q)
+    with ctx:
         st = _lib.attn_fwd_kvcache8(q.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                     _lens_ptr(cache_seqlens, "cache_seqlens", B), o.data_ptr(),
                                     lse.data_ptr() if with_lse else None, workspace.data_ptr(),
                                     workspace.numel() * workspace.element_size(), B, Hq, Hkv, Nq, Nk, d, block, causal,
                                     _scale_arg(scale), _dtype_code(q), _DT8[k8.dtype],
-                                    _lib.ATTN_FLAG_OUT_F32 if out_f32 else 0, _stream())
+                                    _lib.ATTN_FLAG_OUT_F32 if out_f32 else 0, stream)
     _lib._check(st, "attn_fwd_kvcache8")
     return o, lse
 
@@ -318,9 +329,9 @@ def kvcache_weights(q, k_cache, lse, cache_seqlens=None, causal: bool = False, s
     weights float32 [B,Hkv,Nk]: what earlier queries added up to (None: zeros).  out: where to
     write (may be weights).  Returns float32 [B,Hkv,Nk]."""
     _require(q, "q")
-    dev = _cache_args(q, "q", ((k_cache, "k_cache", q.dtype), (lse, "lse", torch.float32)),
-                      ((cache_seqlens, "cache_seqlens", torch.int32), (weights, "weights", torch.float32),
-                       (out, "out", torch.float32)))
+    _cache_args(q, "q", ((k_cache, "k_cache", q.dtype), (lse, "lse", torch.float32)),
+                ((cache_seqlens, "cache_seqlens", torch.int32), (weights, "weights", torch.float32),
+                 (out, "out", torch.float32)))
     if q.dim() != 4 or k_cache.dim() != 4:
         raise ValueError("q must be [B,Hq,Nq,d] and k_cache [B,Hkv,Nk,d]")
     B, Hq, Nq, d = q.shape
@@ -333,12 +344,13 @@ def kvcache_weights(q, k_cache, lse, cache_seqlens=None, causal: bool = False, s
         if t is not None and t.shape != (B, Hkv, Nk):
             raise ValueError(f"{n} must be [B,Hkv,Nk]")
     if out is None:
-        out = torch.empty((B, Hkv, Nk), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
+        out = torch.empty((B, Hkv, Nk), dtype=torch.float32, device=q.device)
+    ctx, stream = _device_stream(q)
+    with ctx:
         st = _lib.attn_kvcache_weights(q.data_ptr(), k_cache.data_ptr(), lse.data_ptr(),
                                        _lens_ptr(cache_seqlens, "cache_seqlens", B),
                                        weights.data_ptr() if weights is not None else None, out.data_ptr(), B, Hq, Hkv,
-                                       Nq, Nk, d, causal, _scale_arg(scale), _dtype_code(q), _stream())
+                                       Nq, Nk, d, causal, _scale_arg(scale), _dtype_code(q), stream)
     _lib._check(st, "attn_kvcache_weights")
     return out
 
@@ -353,8 +365,9 @@ def kvcache_evict(k_cache, v_cache, weights, keep: int, recent: int, cache_seqle
     [B,Hkv,capacity], index int32 [B,Hkv,keep+recent] with -1 past the kept keys, lengths int32
     [B])."""
     _require(k_cache, "k_cache")
-    dev = _cache_args(k_cache, "k_cache", ((v_cache, "v_cache", k_cache.dtype), (weights, "weights", torch.float32)),
-                      ((cache_seqlens, "cache_seqlens", torch.int32),))
+    _cache_args(k_cache, "k_cache", ((v_cache, "v_cache", k_cache.dtype), (weights, "weights", torch.float32)),
+                ((cache_seqlens, "cache_seqlens", torch.int32),))
+    dev = k_cache.device
     if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or weights.shape != k_cache.shape[:3]:
         raise ValueError("k_cache and v_cache must be [B,Hkv,Nk,d] and weights [B,Hkv,Nk]")
     B, Hkv, Nk, d = k_cache.shape
@@ -373,11 +386,12 @@ def kvcache_evict(k_cache, v_cache, weights, keep: int, recent: int, cache_seqle
     w_out = torch.empty((B, Hkv, cap), dtype=torch.float32, device=dev)
     index = torch.empty((B, Hkv, keep + recent), dtype=torch.int32, device=dev)
     lens = torch.empty((B,), dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
+    ctx, stream = _device_stream(k_cache)
+    with ctx:
         st = _lib.attn_kvcache_evict(k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(),
                                      _lens_ptr(cache_seqlens, "cache_seqlens", B), k_out.data_ptr(), v_out.data_ptr(),
                                      w_out.data_ptr(), index.data_ptr(), lens.data_ptr(), B, Hkv, Nk, cap, d, keep,
-                                     recent, _dtype_code(k_cache), _stream())
+                                     recent, _dtype_code(k_cache), stream)
     _lib._check(st, "attn_kvcache_evict")
     return k_out, v_out, w_out, index, lens
 

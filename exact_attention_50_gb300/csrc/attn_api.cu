@@ -631,22 +631,31 @@ bool dtype_ok(attn_dtype_t dt) { return dt == ATTN_F32 || dt == ATTN_F16 || dt =
 
 // The 8-bit codes [heads, Nk, d]: boxes of one tile's tokens, 64 or 128 columns, swizzled over a row's
 // 16-byte chunks; tokens past Nk and columns past d load as zeros.
-bool make_cache8_map(CUtensorMap* map, const void* base, int heads, int Nk, int d) {
+bool make_cache8_map(CUtensorMap* map, const void* base, int heads, int Nk, int d, int keys) {
   auto fn = encode_fn();
   if (!fn) return false;
   const uint64_t dims[3] = {static_cast<uint64_t>(d), static_cast<uint64_t>(Nk), static_cast<uint64_t>(heads)};
   const uint64_t strides[2] = {static_cast<uint64_t>(d), static_cast<uint64_t>(Nk) * d};
-  const uint32_t box[3] = {d <= 64 ? 64u : 128u, attn::kCache8Keys, 1};
+  const uint32_t box[3] = {d <= 64 ? 64u : 128u, static_cast<uint32_t>(keys), 1};
   const uint32_t estr[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, d <= 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// CTAs of the few-rows kernel: two per SM of a 152-SM GPU, no more than there are tiles.
-int cache8_ctas(int B, int Hkv, int Nk) {
-  const long long tiles = static_cast<long long>(B) * Hkv * ((static_cast<long long>(Nk) + attn::kCache8Keys - 1) / attn::kCache8Keys);
-  return static_cast<int>(std::max(1LL, std::min(tiles, 2LL * 152)));
+// The few-rows kernel's CTAs -- as many as a 152-SM GPU holds, no more than there are tiles for -- and
+// its workspace: the parts' outputs and LSEs, and per (batch, kv head) its runs.
+struct Cache8Plan {
+  int ctas;
+  size_t o_bytes, lse_bytes, parts_bytes;
+};
+Cache8Plan cache8_plan(int B, int Hkv, int R, int Nk, int d) {
+  const int nb = attn::cache8_row_blocks(R), keys = attn::cache8_keys(nb), workers = 4 / attn::cache8_run_warps(R);
+  const long long tiles = static_cast<long long>(B) * Hkv * ((static_cast<long long>(Nk) + keys - 1) / keys);
+  const long long ctas = std::max(1LL, std::min((tiles + workers - 1) / workers, attn::cache8_ctas_per_sm(nb) * 152LL));
+  const size_t rows = 2 * static_cast<size_t>(ctas) * workers * R;
+  return {static_cast<int>(ctas), round256(rows * d * sizeof(float)), round256(rows * sizeof(float)),
+          round256(static_cast<size_t>(B) * Hkv * sizeof(int2))};
 }
 
 bool overlap(const void* a, size_t an, const void* b, size_t bn) {
@@ -687,8 +696,8 @@ size_t attn_fwd_kvcache8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk,
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Nq <= 0 || Nk < 0 || d <= 0) return 0;
   const size_t R = static_cast<size_t>(Hq / Hkv) * Nq;
   if (R > static_cast<size_t>(attn::kCache8Rows)) return 256;
-  const size_t rows = 2 * static_cast<size_t>(cache8_ctas(B, Hkv, Nk)) * R;
-  return round256(rows * d * sizeof(float)) + round256(rows * sizeof(float));
+  const Cache8Plan plan = cache8_plan(B, Hkv, static_cast<int>(R), Nk, d);
+  return plan.o_bytes + plan.lse_bytes + plan.parts_bytes;
 }
 
 attn_status_t attn_fwd_kvcache8(const void* q, const void* k8, const void* v8, const float* k_scale,
@@ -709,9 +718,8 @@ attn_status_t attn_fwd_kvcache8(const void* q, const void* k8, const void* v8, c
     return ATTN_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < attn_fwd_kvcache8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d))
     return ATTN_ERR_INVALID_ARG;
-  const long long R = static_cast<long long>(Hq / Hkv) * Nq;
-  if (R > 0x7fffffffLL || static_cast<long long>(B) * Hkv * R > 0x7fffffffLL || static_cast<long long>(B) * Hq > 0x7fffffffLL)
-    return ATTN_ERR_UNSUPPORTED;
+  const long long R = static_cast<long long>(Hq / Hkv) * Nq, bh = static_cast<long long>(B) * Hkv;
+  if (R > 0x7fffffffLL || bh * R > 0x7fffffffLL || static_cast<long long>(B) * Hq > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
   attn::Cache8Params p{};
   p.q = q;
   p.k8 = static_cast<const uint8_t*>(k8);
@@ -732,11 +740,18 @@ attn_status_t attn_fwd_kvcache8(const void* q, const void* k8, const void* v8, c
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (Nk == 0) return from_cuda(attn::launch_cache8_none(p, s));
   if (R > attn::kCache8Rows) return from_cuda(attn::launch_cache8_wide(p, dtype, cache_dtype, s));
-  p.ctas = cache8_ctas(B, Hkv, Nk);
-  p.o_part = static_cast<float*>(workspace);
-  p.lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + round256(2 * static_cast<size_t>(p.ctas) * R * d * sizeof(float)));
+  p.tile_keys = attn::cache8_keys(attn::cache8_row_blocks(p.R));
+  // tiles are numbered in 32 bits (two terabytes of codes)
+  if (bh * ((static_cast<long long>(Nk) + p.tile_keys - 1) / p.tile_keys) > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  const Cache8Plan plan = cache8_plan(B, Hkv, p.R, Nk, d);
+  char* const ws = static_cast<char*>(workspace);
+  p.ctas = plan.ctas;
+  p.runs = plan.ctas * (4 / attn::cache8_run_warps(p.R));
+  p.o_part = reinterpret_cast<float*>(ws);
+  p.lse_part = reinterpret_cast<float*>(ws + plan.o_bytes);
+  p.parts = reinterpret_cast<int2*>(ws + plan.o_bytes + plan.lse_bytes);
   CUtensorMap mk, mv;
-  if (!make_cache8_map(&mk, k8, B * Hkv, Nk, d) || !make_cache8_map(&mv, v8, B * Hkv, Nk, d)) return ATTN_ERR_CUDA;
+  if (!make_cache8_map(&mk, k8, B * Hkv, Nk, d, p.tile_keys) || !make_cache8_map(&mv, v8, B * Hkv, Nk, d, p.tile_keys)) return ATTN_ERR_CUDA;
   return from_cuda(attn::launch_cache8_fwd(mk, mv, p, dtype, cache_dtype, s));
 }
 

@@ -1,5 +1,6 @@
 // cache8.cuh -- the 8-bit cache codes shared by the kernels that write and read them.
 #pragma once
+#include <atomic>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include "kernels.h"
@@ -48,6 +49,38 @@ __device__ __forceinline__ int cache_len(const int32_t* lens, int b, int Nk, uns
     return 0;
   }
   return L;
+}
+
+// Programmatic dependent launch: the first kernel lets the next one's CTAs start as soon as there is
+// room; those wait, before they read its results, until all of it has completed.
+__device__ __forceinline__ void dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, int threads, cudaStream_t stream, Args... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, Params(args)...);
+}
+
+// Runs `set_up` at the first call on each device (its result is not kept when it fails).
+template <typename F>
+cudaError_t once_per_device(std::atomic<unsigned long long>& ready, F set_up) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (bit && (ready.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = set_up();
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 }  // namespace attn

@@ -5,61 +5,63 @@
 // keys.  With code c and block scales ks, vs:
 //   s_j = scale ks_j (q . ck_j), masked;  l = sum_j exp(s_j - m);  o = sum_j exp(s_j - m) vs_j cv_j / l.
 //
-// Work: the caches are cut into tiles of 48 keys, and all tiles of all (batch, kv head) pairs, one
-// after the other, are dealt to the CTAs (two per SM) in equal runs, whatever the sequences'
-// lengths.  A run may begin and end inside a sequence: such parts go to the workspace, normalised
-// with their log-sum-exp, and a second kernel merges them; a sequence that lies within one run
-// is finished by its CTA.
+// Work: the caches are cut into tiles of 32 keys (48 for more than 8 rows), and all tiles of all
+// (batch, kv head) pairs, one after the other, are dealt in equal runs to the workers, whatever the
+// sequences' lengths.  A worker is one warp per block of rows, four warps a CTA, as many CTAs as
+// fit.  A run may begin and end inside a pair: such parts go to the workspace, normalised with
+// their log-sum-exp, and a second kernel merges them; a pair that lies within one run is
+// finished by its worker.  (Warps of a CTA that shared a run and joined their sums in shared memory
+// for every pair took 55 us for 256 sequences of 100 to 200 keys, now REPL_SHORT.)
 //
-// A CTA is one producer warp and four consumer warps.  The producer keeps a ring of tiles full
-// with TMA tile loads (K and V, swizzled, 12 KB a tile for d = 128) and 4-byte asynchronous
-// copies of the scales.  A tile belongs to one consumer warp per 16 rows, which converts codes to
-// fp16 in registers (exact: int8 by placing the byte in the mantissa of 1024 + u and subtracting,
-// e4m3 by the conversion instruction) and multiplies with mma.sync.m16n8k16, fp32 sums. A tcgen05
-// product would have to take the converted tiles through shared memory again, 5 times the
-// traffic of the codes, to fill 4 of its 128 rows.  The contraction index is permuted so that a
-// thread's B fragments are whole 16-byte chunks: columns 32 t .. 32 t + 31 of a key for Q K^T
-// (t = lane % 4), columns 16 g .. 16 g + 15 of four keys for P V (g = lane / 4); the swizzle
-// makes both conflict-free.
+// A worker keeps its own ring of tiles full: when a tile's codes are in registers its first warp
+// starts the copies of the tile that follows in that stage -- TMA tile loads of K and V, swizzled,
+// and 4-byte asynchronous copies of the scales -- so there is no producer warp and, with one
+// row block, no barrier but the copies' own.  Codes become fp16 in registers and are multiplied
+// with mma.sync.m16n8k16, fp32 sums, keys (or columns of V) as the 16 rows and query rows as the 8
+// columns: S^T = K Q^T, O^T = V^T P^T.  A tcgen05 product would have to take the converted tiles
+// through shared memory again, 5 times the traffic of the codes, and has at least 64 rows of
+// which the few queries of a decode fill 4.
+//
+// The contraction index is permuted so that a thread's fragments are whole 16-byte chunks: columns
+// 32 t .. 32 t + 31 of a key for K Q^T (t = lane % 4), columns 16 g .. 16 g + 15 of four keys for
+// V^T P^T (g = lane / 4); the swizzle makes both conflict-free.  P^T goes from the layout of S^T to
+// that of an operand by an 8 x 8 transposition between the lanes (movmatrix).
+//
+// Conversion: K's int8 codes as fp16 subnormals, (code + 128) 2^-24, exact, two instructions a pair;
+// the sum starts at -128 2^-24 sum(q).  V's by placing code + 128 in the mantissa of 1024 + u and
+// subtracting 1152: there the offset would be far larger than the sums.  e4m3 by the conversion
+// instruction.
 //
 // Rounding: q in bf16 becomes fp16 after a multiplication by a power of two per row (largest
 // element in [2^14, 2^15)), exact but for elements below 2^-28 of that.  P is rounded to fp16
 // (half a step 2^-11) after its multiplication by vs / (the largest vs so far): a block whose
 // scale is below 2^-14 of that has absolute errors of 2^-25 times the largest value instead.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 #include "cache8.cuh"
 
 namespace attn {
 namespace {
 
-constexpr int kKeys = kCache8Keys;  // keys of a tile: 48
-constexpr int kGroups = kKeys / 16; // 16 keys share a scale
-constexpr int kConsumers = 4;   // consumer warps of a CTA
-constexpr int kThreads = 2 * kConsumers * 32;  // a warpgroup of consumers, one that holds the producer
-// Registers: launched at 128 a thread (two CTAs fill the SM's file), then split by setmaxnreg; a
-// consumer holds 64 sums of O, 32 of S and 32 registers of Q.
-constexpr uint32_t kLaunchRegs = 128, kRegsConsumer = 216, kRegsProducer = 40;
-static_assert(kRegsConsumer + kRegsProducer == 2 * kLaunchRegs, "register split must match the launch");
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr float kLazy = 8.0f;   // log2 units by which a tile's maximum may exceed the running one
 
-template <int DP>
+// NB: blocks of 8 query rows per warp, 1 or 2.
+template <int DP, int NB>
 struct Layout {
+  static constexpr int kKeys = cache8_keys(NB);
+  static constexpr int kGroups = kKeys / 16;                  // 16 keys share a scale
+  static constexpr int kCtas = cache8_ctas_per_sm(NB);
   static constexpr int kTile = kKeys * DP;                    // bytes of codes
-  // A multiple of the consumer warps: tile n of the run goes to stage n % kStages and to the warps
-  // with tg == n % TG, so a stage has the same readers in every turn and none of them can
-  // run ahead of its phase. Two stages a warp (d = 128) with 48 keys; 64 would leave room for one.
-  static constexpr int kStages = DP == 128 ? 8 : 16;
-  static_assert(kStages % kConsumers == 0, "a stage belongs to one consumer");
+  static constexpr int kStages = DP == 128 ? 2 : 4;           // per warp
   static constexpr int kOffV = kTile;                         // within a stage: K, V
   static constexpr int kStage = 2 * kTile;
-  static constexpr int kOffMerge = kStages * kStage;          // two warps' O: [DP / 8][32] float4
-  static constexpr int kMerge = 16 * DP * 4;
-  static constexpr int kOffStat = kOffMerge + 2 * kMerge;     // two warps' (m, l) of 16 rows
-  static constexpr int kOffScale = kOffStat + 2 * 16 * 8;     // per stage: (ks, vs) of each group
-  static constexpr int kOffBar = kOffScale + kStages * 32;    // full[], empty[], merge
-  static constexpr int kOffMisc = kOffBar + (2 * kStages + 1) * 8;  // pad, abort flag, wait limit
+  static constexpr int kOffScale = kWarps * kStages * kStage; // per stage: (ks, vs) of each group
+  static constexpr int kOffBar = kOffScale + kWarps * kStages * 32;  // full[], empty[]
+  static constexpr int kOffMisc = kOffBar + 2 * kWarps * kStages * 8;  // pad, abort flag, wait limit
   static constexpr int kBytes = kOffMisc + 16;
+  static_assert((kBytes + 1024) * kCtas <= 228 * 1024, "shared memory of an SM");
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -79,6 +81,24 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Four codes of K as two pairs of fp16, less the offset and in units of kUnitK.
+template <typename Code>
+constexpr float kUnitK = 1.f;
+template <>
+constexpr float kUnitK<CodeI8> = 16777216.f;  // 2^24
+__device__ __forceinline__ void k_to_half(CodeI8, uint32_t w, uint32_t& lo, uint32_t& hi) {
+  w ^= 0x80808080u;
+  lo = __byte_perm(w, 0u, 0x4140);
+  hi = __byte_perm(w, 0u, 0x4342);
+}
+__device__ __forceinline__ void k_to_half(CodeE4m3 c, uint32_t w, uint32_t& lo, uint32_t& hi);
+
 // Four codes as two pairs of fp16.
 __device__ __forceinline__ void to_half(CodeI8, uint32_t w, uint32_t& lo, uint32_t& hi) {
   w ^= 0x80808080u;  // code + 128, 0 .. 255
@@ -94,6 +114,8 @@ __device__ __forceinline__ void to_half(CodeE4m3, uint32_t w, uint32_t& lo, uint
       : "=r"(lo), "=r"(hi)
       : "r"(w));
 }
+
+__device__ __forceinline__ void k_to_half(CodeE4m3 c, uint32_t w, uint32_t& lo, uint32_t& hi) { to_half(c, w, lo, hi); }
 
 __device__ __forceinline__ uint32_t pack_half(float a, float b) {
   const __half2 v = __floats2half2_rn(a, b);
@@ -117,62 +139,31 @@ __device__ __forceinline__ uint32_t pack2(const __nv_bfloat16*, float a, float b
 
 // Batch b's tiles per kv head.
 __device__ __forceinline__ int tiles_of(const Cache8Params& p, int b) {
-  return (cache_len(p.cache_seqlens, b, p.Nk, nullptr, false) + kKeys - 1) / kKeys;
+  return (cache_len(p.cache_seqlens, b, p.Nk, nullptr, false) + p.tile_keys - 1) / p.tile_keys;
 }
 
-// All tiles of all (batch, kv head) pairs; every lane of a warp calls it and gets the sum.
-__device__ __forceinline__ long long total_tiles(const Cache8Params& p) {
-  if (!p.cache_seqlens) return static_cast<long long>(p.B) * p.Hkv * ((p.Nk + kKeys - 1) / kKeys);
-  long long sum = 0;
-  for (int b = threadIdx.x & 31; b < p.B; b += 32) sum += tiles_of(p, b);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return sum * p.Hkv;
-}
+// The runs: all tiles of all (batch, kv head) pairs in one numbering, the first total % runs runs one
+// tile longer than the others; runs without a tile come last.
+struct Deal {
+  int total, base, rest;
+  __device__ __forceinline__ void set(int tiles, int runs) {
+    total = tiles;
+    base = tiles / runs;
+    rest = tiles % runs;
+  }
+  __device__ __forceinline__ int start(int run) const { return run * base + min(run, rest); }
+  __device__ __forceinline__ int holder(int tile) const {  // the run that holds a tile
+    const int longer = rest * (base + 1);
+    return tile < longer ? tile / (base + 1) : rest + (tile - longer) / base;
+  }
+};
 
-// Walks the parts of (batch, kv head) pairs that tiles [t, end) of the common numbering cover.
+// Walks the parts of (batch, kv head) pairs that tiles [t, end) cover.
 struct Walk {
-  long long t, end;    // the next tile and the end
-  int b, h, nt;        // the pair that holds tile t, its tiles
-  int j;               // tile t's number within the pair
-  // Whole warps call start: the batch that holds tile t is found by a scan over the lengths.
-  __device__ __forceinline__ void start(const Cache8Params& p, long long first, long long last) {
-    t = first;
-    end = last;
-    b = h = nt = j = 0;
-    if (t >= end) return;
-    const int lane = threadIdx.x & 31;
-    long long off = 0;  // tiles before the 32 batches at b0
-    for (int b0 = 0;; b0 += 32) {
-      const int mine = b0 + lane < p.B ? tiles_of(p, b0 + lane) : 0;
-      long long x = static_cast<long long>(mine) * p.Hkv;
-      const long long own = x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, off + x > t);
-      if (hit) {
-        const int src = __ffs(hit) - 1;
-        const long long before = off + __shfl_sync(0xffffffffu, x - own, src);
-        nt = __shfl_sync(0xffffffffu, mine, src);
-        b = b0 + src;
-        h = static_cast<int>((t - before) / nt);
-        j = static_cast<int>((t - before) % nt);
-        return;
-      }
-      off += __shfl_sync(0xffffffffu, x, 31);
-      if (b0 + 32 >= p.B) {  // not reached: t is below the total
-        end = t;
-        return;
-      }
-    }
-  }
-  __device__ __forceinline__ int part() const {  // tiles of this pair within the run
-    const long long rest = end - t;
-    return rest < nt - j ? static_cast<int>(rest) : nt - j;
-  }
+  int t, end;    // the next tile and the end
+  int b, h, nt;  // the pair that holds tile t, its tiles
+  int j;         // tile t's number within the pair
+  __device__ __forceinline__ int part() const { return min(end - t, nt - j); }  // tiles of this pair within the run
   __device__ __forceinline__ void next(const Cache8Params& p) {
     t += part();
     j = 0;
@@ -188,174 +179,225 @@ struct Walk {
   }
 };
 
-__device__ __forceinline__ long long run_start(long long total, int c, int ctas) { return total * c / ctas; }
-// The CTA whose run holds tile t.
-__device__ __forceinline__ int run_of(long long total, long long t, int ctas) {
-  return static_cast<int>(((t + 1) * ctas + total - 1) / total) - 1;
+// The deal, and the walk of one run; whole warps call it. The lengths are read by 32 lanes at a
+// time: once for up to 32 batches, twice for more.
+__device__ __forceinline__ void deal_and_find(const Cache8Params& p, int runs, int run, Deal& deal, Walk& w) {
+  const int lane = threadIdx.x & 31;
+  auto scan = [&](int b0, int& mine) {  // inclusive sum of the tiles of batches b0 .. b0 + lane
+    mine = b0 + lane < p.B ? tiles_of(p, b0 + lane) : 0;
+    int x = mine * p.Hkv;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    return x;
+  };
+  int mine, x = scan(0, mine);
+  int total = __shfl_sync(0xffffffffu, x, 31);
+  for (int b0 = 32; b0 < p.B; b0 += 32) {
+    int m2;
+    total += __shfl_sync(0xffffffffu, scan(b0, m2), 31);
+  }
+  deal.set(total, runs);
+  w.t = deal.start(run);
+  w.end = deal.start(run + 1);
+  w.b = w.h = w.nt = w.j = 0;
+  if (w.t >= w.end) return;
+  int off = 0;  // tiles before the 32 batches at b0
+  for (int b0 = 0;;) {
+    const unsigned hit = __ballot_sync(0xffffffffu, off + x > w.t);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      const int before = off + __shfl_sync(0xffffffffu, x - mine * p.Hkv, src);
+      w.nt = __shfl_sync(0xffffffffu, mine, src);
+      w.b = b0 + src;
+      w.h = (w.t - before) / w.nt;
+      w.j = (w.t - before) % w.nt;
+      return;
+    }
+    off += __shfl_sync(0xffffffffu, x, 31);
+    b0 += 32;
+    if (b0 >= p.B) {  // not reached: tile t is below the total
+      w.end = w.t;
+      return;
+    }
+    x = scan(b0, mine);
+  }
 }
 
-template <typename T, typename Code, int DP>
-__global__ void __launch_bounds__(kThreads, 2)
+template <typename T, typename Code, int DP, int NB>
+__global__ void __launch_bounds__(kThreads, (Layout<DP, NB>::kCtas))
     cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Cache8Params p) {
-  using L = Layout<DP>;
-  constexpr int kSteps = DP / 16;  // contraction steps of Q K^T
-  constexpr int kCols = DP / 8;    // 8-column blocks of O
+  using L = Layout<DP, NB>;
+  constexpr int kKeys = L::kKeys, kGroups = L::kGroups;
+  constexpr int kSteps = DP / 16;  // contraction steps of K Q^T
+  constexpr int kCols = DP / 16;   // 16-column blocks of V
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {  // the swizzle needs aligned tiles
     if (threadIdx.x == 0) raise_status(p.status, ATTN_ERR_CUDA);
     return;
   }
-  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
-  uint64_t* const empty = full + L::kStages;
-  uint64_t* const merge = empty + L::kStages;
-  float* const s_scale = reinterpret_cast<float*>(smem + L::kOffScale);
   const uint32_t abort_flag = smem_u32(smem + L::kOffMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // warps by row block and by tile: RBW row blocks of 16 (a power of two), TG tiles at a time
-  const int RB = (p.R + 15) / 16;
-  const int RBW = RB <= 1 ? 1 : RB <= 2 ? 2 : 4, TG = kConsumers / RBW;
+  // a worker: RB warps, one per 8 NB rows, in RBW (a power of two) places
+  const int RB = (p.R + 8 * NB - 1) / (8 * NB);
+  const int RBW = RB <= 1 ? 1 : RB <= 2 ? 2 : 4;
+  const int rb = warp % RBW, first_warp = warp - rb;
+  const uint32_t stages = L::kStages * RBW;  // of the worker's ring
+  uint8_t* const ring = smem + first_warp * L::kStages * L::kStage;
+  float* const s_scale = reinterpret_cast<float*>(smem + L::kOffScale) + first_warp * L::kStages * 8;
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + L::kOffBar) + first_warp * L::kStages;
+  uint64_t* const empty = full + kWarps * L::kStages;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < L::kStages; ++i) {
-      mbar_init(full + i, 1 + 2 * kGroups);  // the tile's bytes, and its scales
-      mbar_init(empty + i, RB);
+    uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+    for (int i = 0; i < kWarps * L::kStages; ++i) {
+      mbar_init(bars + i, 1 + 2 * kGroups);  // the tile's bytes, and its scales
+      mbar_init(bars + kWarps * L::kStages + i, RB);
     }
-    mbar_init(merge, kConsumers);
     abort_set(abort_flag, 0);
     wait_limit_set(abort_flag, p.wait_ns);
     mbar_init_fence();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
   }
   __syncthreads();
-  const long long total = total_tiles(p);
+  dependents_launch();
+  const int per_cta = kWarps / RBW;
+  const int run = blockIdx.x * per_cta + warp / RBW;
+  Deal deal;
   Walk w;
-  w.start(p, run_start(total, blockIdx.x, gridDim.x), run_start(total, blockIdx.x + 1, gridDim.x));
+  deal_and_find(p, p.runs, run, deal, w);
 
-  if (warp >= kConsumers) {
-    regs_dec<kRegsProducer>();
-    if (warp > kConsumers) return;
-    // ================================================================ producer
-    uint32_t n = 0;  // tiles issued
-    bool ok = true;
-    if (lane == 0) {
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
+  // ---- the copies of the run's next tile, into the stage of its number
+  Walk ahead = w;
+  uint32_t issued = 0;
+  bool ok = true;
+  auto issue = [&]() {
+    if (ahead.t >= ahead.end) return;
+    const uint32_t st = issued % stages;
+    if (RB > 1 && issued >= stages && !mbar_wait_warp(empty + st, ((issued / stages) - 1) & 1, abort_flag, p.status)) {
+      ok = false;
+      return;
     }
-    for (; ok && w.t < w.end; w.next(p)) {
-      const int len = cache_len(p.cache_seqlens, w.b, p.Nk, nullptr, false);
-      const int bh = w.b * p.Hkv + w.h;
-      const int part = w.part();
-      for (int i = 0; i < part; ++i, ++n) {
-        const uint32_t st = n % L::kStages;
-        if (n >= L::kStages && !mbar_wait_warp(empty + st, ((n / L::kStages) - 1) & 1, abort_flag, p.status)) { ok = false; break; }
-        const int key0 = (w.j + i) * kKeys;
-        if (lane == 0) {
-          mbar_expect_tx(full + st, L::kStage);
-          tma_load_3d(smem + st * L::kStage, &tmK, full + st, 0, key0, bh);
-          tma_load_3d(smem + st * L::kStage + L::kOffV, &tmV, full + st, 0, key0, bh);
-        }
-        if (lane < 2 * kGroups) {
-          // the scale of 16 keys; of none that the cache holds: 0, the scale there is not read
-          const int key = key0 + (lane >> 1) * 16;
-          float* dst = s_scale + st * 8 + lane;
-          if (key < len) {
-            const float* src = ((lane & 1) == 0 ? p.k_scale : p.v_scale) + static_cast<size_t>(bh) * p.n_blocks + (key >> p.block_shift);
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full + st)) : "memory");
-          } else {
-            *dst = 0.f;
-            mbar_arrive(full + st);
-          }
-        }
+    const int bh = ahead.b * p.Hkv + ahead.h, key0 = ahead.j * kKeys;
+    if (lane == 0) {
+      mbar_expect_tx(full + st, L::kStage);
+      tma_load_3d(ring + st * L::kStage, &tmK, full + st, 0, key0, bh);
+      tma_load_3d(ring + st * L::kStage + L::kOffV, &tmV, full + st, 0, key0, bh);
+    }
+    if (lane < 2 * kGroups) {
+      // the scale of 16 keys; of none that the cache holds: 0, the scale there is not read
+      const int key = key0 + (lane >> 1) * 16;
+      float* dst = s_scale + st * 8 + lane;
+      if (key < cache_len(p.cache_seqlens, ahead.b, p.Nk, nullptr, false)) {
+        const float* src = ((lane & 1) == 0 ? p.k_scale : p.v_scale) + static_cast<size_t>(bh) * p.n_blocks + (key >> p.block_shift);
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full + st)) : "memory");
+      } else {
+        *dst = 0.f;
+        mbar_arrive(full + st);
       }
     }
-    if (!ok || abort_read(abort_flag))  // let the copies land before the shared memory goes away
-      for (uint32_t i = n > L::kStages ? n - L::kStages : 0; i < n; ++i) mbar_drain(full + i % L::kStages, (i / L::kStages) & 1);
-    return;
-  }
+    __syncwarp();
+    ++issued;
+    if (ahead.j + 1 < ahead.nt) {
+      ++ahead.t;
+      ++ahead.j;
+    } else {
+      ahead.next(p);  // the pair's last tile: its part is this one
+    }
+  };
+  if (rb == 0)
+    for (uint32_t i = 0; i < stages; ++i) issue();
 
-  regs_inc<kRegsConsumer>();
-  // ================================================================ consumers
   const int g = lane >> 2, t = lane & 3;
-  const int rb = warp % RBW, tg = warp / RBW;
   const bool works = rb < RB;
-  const uint32_t tiles = smem_u32(smem);
-  const int r0 = rb * 16 + g, r1 = r0 + 8;  // this thread's rows
-  const int i0 = r0 % p.Nq, i1 = r1 % p.Nq;
-  uint32_t n = 0;       // tiles of the run passed
-  uint32_t merges = 0;  // phases of the merge barrier
-  bool ok = true;       // after a failed wait: no more waits or sums, but the same barriers
-  for (; w.t < w.end; w.next(p)) {
+  const uint32_t tiles = smem_u32(ring);
+  const int row0 = rb * 8 * NB;  // this warp's rows; as columns of S^T and O^T this thread has rows 8 b + 2 t + e of them
+  uint32_t n = 0;                // tiles of the run passed
+  for (; works && ok && w.t < w.end; w.next(p)) {
     const int len = cache_len(p.cache_seqlens, w.b, p.Nk, nullptr, false);
     const size_t bh = static_cast<size_t>(w.b) * p.Hkv + w.h;
     const int part = w.part();
-    const int active = min(TG, part);  // warps (of a row block) with a tile: those with place < active
-    const int place = (tg - static_cast<int>(n % TG) + TG) % TG;  // this warp's first tile of the part
-    // ---- Q as A fragments: step s holds columns (DP / 4) t + 4 s .. + 3
-    uint32_t qa[kSteps][4];
-    float f0 = 0.f, f1 = 0.f;  // scale log2(e) over the row's power of two
-    if (works && place < active) {
+    // ---- Q as B fragments: step s holds columns (DP / 4) t + 4 s .. + 3 of row g
+    uint32_t qb[NB][kSteps][2];
+    float f[NB][2], start[NB][2];  // per row: scale log2(e) over its power of two; where its sums start
+    int last[NB][2];               // the last key the row sees
+    {
       const T* q = static_cast<const T*>(p.q) + bh * p.R * p.d;
-      float mx[2] = {0.f, 0.f};
-      uint2 raw[2][kSteps];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = e ? r1 : r0;
+      for (int b = 0; b < NB; ++b) {
+        const int r = row0 + 8 * b + g;
+        uint2 raw[kSteps];
+        uint32_t mx = 0;  // an ordered maximum of magnitudes that keeps infinity and NaN
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
           const int c = (DP / 4) * t + 4 * s;
-          raw[e][s] = r < p.R && c < p.d ? *reinterpret_cast<const uint2*>(q + static_cast<size_t>(r) * p.d + c) : make_uint2(0, 0);
-          float a, b, c2, d2;
-          unpack2(q, raw[e][s].x, a, b);
-          unpack2(q, raw[e][s].y, c2, d2);
-          // an ordered maximum of magnitudes that keeps infinity and NaN
-          const uint32_t hi = max(max(__float_as_uint(a) & 0x7fffffffu, __float_as_uint(b) & 0x7fffffffu),
-                                  max(__float_as_uint(c2) & 0x7fffffffu, __float_as_uint(d2) & 0x7fffffffu));
-          mx[e] = __uint_as_float(max(__float_as_uint(mx[e]), hi));
-        }
-        uint32_t u = __float_as_uint(mx[e]);
-        u = max(u, __shfl_xor_sync(0xffffffffu, u, 1));
-        u = max(u, __shfl_xor_sync(0xffffffffu, u, 2));
-        mx[e] = __uint_as_float(u);
-      }
-      float up[2], down[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        int k = 0;  // q 2^k has its largest element in [2^14, 2^15)
-        const uint32_t u = __float_as_uint(mx[e]);
-        if (sizeof(T) == 2 && !std::is_same<T, __half>::value && u != 0 && u < 0x7f800000u)
-          k = min(100, 14 + 127 - static_cast<int>(u >> 23));
-        up[e] = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
-        down[e] = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-      }
-      f0 = p.scale_log2 * down[0];
-      f1 = p.scale_log2 * down[1];
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (std::is_same<T, __half>::value) {
-            qa[s][e] = raw[e][s].x;
-            qa[s][2 + e] = raw[e][s].y;
-          } else {
-            float a, b;
-            unpack2(q, raw[e][s].x, a, b);
-            qa[s][e] = pack_half(a * up[e], b * up[e]);
-            unpack2(q, raw[e][s].y, a, b);
-            qa[s][2 + e] = pack_half(a * up[e], b * up[e]);
+          raw[s] = r < p.R && c < p.d ? *reinterpret_cast<const uint2*>(q + static_cast<size_t>(r) * p.d + c) : make_uint2(0, 0);
+          if (!std::is_same<T, __half>::value) {
+            const uint32_t x = raw[s].x & 0x7fff7fffu, y = raw[s].y & 0x7fff7fffu;
+            mx = max(max(mx, max(x << 16, x & 0xffff0000u)), max(y << 16, y & 0xffff0000u));
           }
         }
-    }
-    const int last0 = p.causal ? min(len - p.Nq + i0, len - 1) : len - 1;  // the last key each row sees
-    const int last1 = p.causal ? min(len - p.Nq + i1, len - 1) : len - 1;
-    float o[kCols][4];
+        float up = 1.f, down = 1.f;
+        if (!std::is_same<T, __half>::value) {
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          int k = 0;  // q 2^k has its largest element in [2^14, 2^15)
+          if (mx != 0 && mx < 0x7f800000u) k = min(100, 14 + 127 - static_cast<int>(mx >> 23));
+          up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+          down = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+        }
+        float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+        for (int s = 0; s < kSteps; ++s) {
+          float a, c, a2, c2;
+          if (std::is_same<T, __half>::value) {
+            qb[b][s][0] = raw[s].x;
+            qb[b][s][1] = raw[s].y;
+          } else {
+            unpack2(q, raw[s].x, a, c);
+            qb[b][s][0] = pack_half(a * up, c * up);
+            unpack2(q, raw[s].y, a, c);
+            qb[b][s][1] = pack_half(a * up, c * up);
+          }
+          if (std::is_same<Code, CodeI8>::value) {
+            unpack2(static_cast<const __half*>(nullptr), qb[b][s][0], a, c);
+            unpack2(static_cast<const __half*>(nullptr), qb[b][s][1], a2, c2);
+            sum += (a + c) + (a2 + c2);
+          }
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          f[b][e] = __shfl_sync(0xffffffffu, down, 4 * (2 * t + e)) * p.scale_log2 * kUnitK<Code>;
+          start[b][e] = __shfl_sync(0xffffffffu, sum, 4 * (2 * t + e)) * (-128.f / 16777216.f);
+          if (std::is_same<Code, CodeE4m3>::value) start[b][e] = 0.f;
+          const int i = (row0 + 8 * b + 2 * t + e) % p.Nq;
+          last[b][e] = p.causal ? min(len - p.Nq + i, len - 1) : len - 1;
+        }
+      }
+    }
+    float o[kCols][NB][4];
+#pragma unroll
+    for (int i = 0; i < kCols; ++i)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) o[i][b][0] = o[i][b][1] = o[i][b][2] = o[i][b][3] = 0.f;
+    float m[NB][2], l[NB][2];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      m[b][0] = m[b][1] = -INFINITY;
+      l[b][0] = l[b][1] = 0.f;
+    }
     float vref = 0.f;  // the largest value scale so far: o is in units of it
-    if (works) {
-      for (int x = place; x < part; x += TG) {
-        const uint32_t at = n + x, st = at % L::kStages;
-        if (ok) ok = mbar_wait_warp(full + st, (at / L::kStages) & 1, abort_flag, p.status);
-        if (!ok) break;
+    {
+      for (int x = 0; x < part; ++x, ++n) {
+        const uint32_t st = n % stages;
+        // several warps read a tile: the one before has been read by all of them before its stage is filled again
+        if (RB > 1 && rb == 0 && n > 0) issue();
+        if (!ok || !mbar_wait_warp(full + st, (n / stages) & 1, abort_flag, p.status)) { ok = false; break; }
         const uint32_t kt = tiles + st * L::kStage, vt = kt + L::kOffV;
         float kg[kGroups], vg[kGroups];
 #pragma unroll
@@ -364,98 +406,120 @@ __global__ void __launch_bounds__(kThreads, 2)
           kg[i] = kv.x;
           vg[i] = kv.y;
         }
-        // ---- S = Q K^T: six blocks of 8 keys, three at a time
-        float s[2 * kGroups][4];
+        // ---- S^T = K Q^T: blocks of 16 keys, side by side
+        float s[kGroups][NB][4];
 #pragma unroll
-        for (int i = 0; i < 2 * kGroups; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+        for (int i = 0; i < kGroups; ++i)
 #pragma unroll
-        for (int i = 0; i < 2 * kGroups; i += 3) {
-          constexpr int kChunks = DP / 64;  // 16-byte chunks of a thread
+          for (int b = 0; b < NB; ++b) {
+            s[i][b][0] = s[i][b][2] = start[b][0];
+            s[i][b][1] = s[i][b][3] = start[b][1];
+          }
+        constexpr int kChunks = DP / 64;  // 16-byte chunks of a thread
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            uint4 kw[3];
+        for (int c = 0; c < kChunks; ++c) {
+          uint4 kw[kGroups][2];
 #pragma unroll
-            for (int e = 0; e < 3; ++e) {
-              const int row = (i + e) * 8 + g;
+          for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int row = i * 16 + e * 8 + g;
               const int chunk = kChunks * t + c;
               const int sw = DP == 128 ? (chunk ^ (row & 7)) : (chunk ^ ((row >> 1) & 3));
-              kw[e] = lds128(kt + row * DP + sw * 16);
+              kw[i][e] = lds128(kt + row * DP + sw * 16);
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < 4; ++k)
 #pragma unroll
-              for (int e = 0; e < 3; ++e) {
-                const uint32_t word = k == 0 ? kw[e].x : k == 1 ? kw[e].y : k == 2 ? kw[e].z : kw[e].w;
-                uint32_t b0, b1;
-                to_half(Code{}, word, b0, b1);
-                mma16816(s[i + e], qa[c * 4 + k], b0, b1);
+            for (int i = 0; i < kGroups; ++i) {
+              uint32_t a[4];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t word = k == 0 ? kw[i][e].x : k == 1 ? kw[i][e].y : k == 2 ? kw[i][e].z : kw[i][e].w;
+                k_to_half(Code{}, word, a[e], a[2 + e]);
               }
-          }
+#pragma unroll
+              for (int b = 0; b < NB; ++b) mma16816(s[i][b], a, qb[b][c * 4 + k][0], qb[b][c * 4 + k][1]);
+            }
         }
         // ---- scale, mask, running maximum
-        const int key0 = (w.j + x) * kKeys + 2 * t;
-        float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 2 * kGroups; ++i) {
-          const float a = f0 * kg[i >> 1], b = f1 * kg[i >> 1];
-          s[i][0] *= a; s[i][1] *= a; s[i][2] *= b; s[i][3] *= b;
-        }
-        if (key0 - 2 * t + kKeys - 1 > min(last0, last1)) {
-#pragma unroll
-          for (int i = 0; i < 2 * kGroups; ++i) {
-            const int key = key0 + i * 8;
-            if (key > last0) s[i][0] = -INFINITY;
-            if (key + 1 > last0) s[i][1] = -INFINITY;
-            if (key > last1) s[i][2] = -INFINITY;
-            if (key + 1 > last1) s[i][3] = -INFINITY;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 2 * kGroups; ++i) {
-          mx0 = max3f(mx0, s[i][0], s[i][1]);
-          mx1 = max3f(mx1, s[i][2], s[i][3]);
-        }
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+        const int key0 = (w.j + x) * kKeys;
         const float v_old = vref;
-        vref = fmaxf(fmaxf(fmaxf(vg[0], vg[1]), vg[2]), vref);
-        const bool move0 = mx0 > m0 + kLazy || (m0 == -INFINITY && mx0 != -INFINITY);
-        const bool move1 = mx1 > m1 + kLazy || (m1 == -INFINITY && mx1 != -INFINITY);
-        if (__any_sync(0xffffffffu, move0 || move1 || vref != v_old)) {
-          const float back = v_old == vref ? 1.f : v_old / vref;
-          const float a0 = !move0 ? 1.f : m0 == -INFINITY ? 0.f : ex2_approx(m0 - mx0);
-          const float a1 = !move1 ? 1.f : m1 == -INFINITY ? 0.f : ex2_approx(m1 - mx1);
-          if (move0) m0 = mx0;
-          if (move1) m1 = mx1;
-          l0 *= a0;
-          l1 *= a1;
-          const float c0 = a0 * back, c1 = a1 * back;
 #pragma unroll
-          for (int i = 0; i < kCols; ++i) {
-            o[i][0] *= c0; o[i][1] *= c0; o[i][2] *= c1; o[i][3] *= c1;
+        for (int i = 0; i < kGroups; ++i) vref = fmaxf(vref, vg[i]);
+        bool move = vref != v_old;
+        float mx[NB][2];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+#pragma unroll
+          for (int i = 0; i < kGroups; ++i) {
+            const float f0 = f[b][0] * kg[i], f1 = f[b][1] * kg[i];
+            s[i][b][0] *= f0; s[i][b][1] *= f1; s[i][b][2] *= f0; s[i][b][3] *= f1;
+          }
+          if (__any_sync(0xffffffffu, key0 + kKeys - 1 > min(last[b][0], last[b][1]))) {
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) {
+              const int key = key0 + i * 16 + g;
+              if (key > last[b][0]) s[i][b][0] = -INFINITY;
+              if (key > last[b][1]) s[i][b][1] = -INFINITY;
+              if (key + 8 > last[b][0]) s[i][b][2] = -INFINITY;
+              if (key + 8 > last[b][1]) s[i][b][3] = -INFINITY;
+            }
+          }
+          mx[b][0] = mx[b][1] = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < kGroups; ++i) {
+            mx[b][0] = max3f(mx[b][0], s[i][b][0], s[i][b][2]);
+            mx[b][1] = max3f(mx[b][1], s[i][b][1], s[i][b][3]);
+          }
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) {
+            mx[b][0] = fmaxf(mx[b][0], __shfl_xor_sync(0xffffffffu, mx[b][0], d));
+            mx[b][1] = fmaxf(mx[b][1], __shfl_xor_sync(0xffffffffu, mx[b][1], d));
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) move |= mx[b][e] > m[b][e] + kLazy || (m[b][e] == -INFINITY && mx[b][e] != -INFINITY);
+        }
+        if (__any_sync(0xffffffffu, move)) {
+          const float back = v_old == vref ? 1.f : v_old / vref;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            float c[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float top = fmaxf(m[b][e], mx[b][e]);
+              const float a = m[b][e] == top ? 1.f : m[b][e] == -INFINITY ? 0.f : ex2_approx(m[b][e] - top);
+              m[b][e] = top;
+              l[b][e] *= a;
+              c[e] = a * back;
+            }
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) {
+              o[i][b][0] *= c[0]; o[i][b][1] *= c[1]; o[i][b][2] *= c[0]; o[i][b][3] *= c[1];
+            }
           }
         }
-        const float n0 = m0 == -INFINITY ? 0.f : -m0, n1 = m1 == -INFINITY ? 0.f : -m1;
-        // ---- P = exp2(S - m), its sum, and P vs / vref as fp16 A fragments
         float ratio[kGroups];
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) ratio[i] = vref == 0.f ? 0.f : vg[i] / vref;
-        uint32_t pa[kGroups][4];
+        // ---- P = exp2(S - m), its sum, and P vs / vref as fp16 B fragments
+        uint32_t pb[kGroups][NB][2];
 #pragma unroll
-        for (int i = 0; i < 2 * kGroups; ++i) {
-          const float rv = ratio[i >> 1];
-          const float e0 = ex2_approx(s[i][0] + n0), e1 = ex2_approx(s[i][1] + n0);
-          const float e2 = ex2_approx(s[i][2] + n1), e3 = ex2_approx(s[i][3] + n1);
-          l0 += e0 + e1;
-          l1 += e2 + e3;
-          pa[i >> 1][(i & 1) * 2] = pack_half(e0 * rv, e1 * rv);
-          pa[i >> 1][(i & 1) * 2 + 1] = pack_half(e2 * rv, e3 * rv);
+        for (int b = 0; b < NB; ++b) {
+          const float n0 = m[b][0] == -INFINITY ? 0.f : m[b][0], n1 = m[b][1] == -INFINITY ? 0.f : m[b][1];
+#pragma unroll
+          for (int i = 0; i < kGroups; ++i) {
+            const float e0 = ex2_approx(s[i][b][0] - n0), e1 = ex2_approx(s[i][b][1] - n1);
+            const float e2 = ex2_approx(s[i][b][2] - n0), e3 = ex2_approx(s[i][b][3] - n1);
+            l[b][0] += e0 + e2;
+            l[b][1] += e1 + e3;
+            pb[i][b][0] = transpose8x8(pack_half(e0 * ratio[i], e1 * ratio[i]));
+            pb[i][b][1] = transpose8x8(pack_half(e2 * ratio[i], e3 * ratio[i]));
+          }
         }
         // a code behind the cache's end may be e4m3's NaN, which a weight of zero does not cancel
-        const int over = std::is_same<Code, CodeE4m3>::value ? len - (w.j + x) * kKeys : kKeys;
-        // ---- O += P V: per 16 keys, this thread's columns (DP / 8) g .. of keys 2t, 2t+1, 2t+8, 2t+9
+        const int over = std::is_same<Code, CodeE4m3>::value ? len - key0 : kKeys;
+        // ---- O^T += V^T P^T: per 16 keys, this thread's columns (DP / 8) g .. of keys 2t, 2t+1, 2t+8, 2t+9
 #pragma unroll
         for (int j = 0; j < kGroups; ++j) {
           uint32_t vw[4][DP / 32];
@@ -474,199 +538,171 @@ __global__ void __launch_bounds__(kThreads, 2)
               for (int k = 0; k < DP / 32; ++k) vw[e][k] = 0;
             }
           }
-#pragma unroll
-          for (int k = 0; k < DP / 32; ++k) {
-            uint32_t x0[4], x1[4];  // pairs of keys (0, 1) and (2, 3) at four columns
-            to_half(Code{}, __byte_perm(vw[0][k], vw[1][k], 0x5140), x0[0], x0[1]);
-            to_half(Code{}, __byte_perm(vw[0][k], vw[1][k], 0x7362), x0[2], x0[3]);
-            to_half(Code{}, __byte_perm(vw[2][k], vw[3][k], 0x5140), x1[0], x1[1]);
-            to_half(Code{}, __byte_perm(vw[2][k], vw[3][k], 0x7362), x1[2], x1[3]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) mma16816(o[k * 4 + c], pa[j], x0[c], x1[c]);
+          if (j == kGroups - 1) {  // the tile is in registers: the next one into its stage
+            __syncwarp();
+            if (RB > 1 && lane == 0) mbar_arrive(empty + st);
+            if (RB == 1) issue();
           }
+#pragma unroll
+          for (int k = 0; k < DP / 32; ++k)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {  // columns 4 k + 2 c and + 1 of the chunk
+              uint32_t a[4];
+              to_half(Code{}, __byte_perm(vw[0][k], vw[1][k], c ? 0x7362 : 0x5140), a[0], a[1]);
+              to_half(Code{}, __byte_perm(vw[2][k], vw[3][k], c ? 0x7362 : 0x5140), a[2], a[3]);
+#pragma unroll
+              for (int b = 0; b < NB; ++b) mma16816(o[2 * k + c][b], a, pb[j][b][0], pb[j][b][1]);
+            }
         }
-        mbar_arrive_warp(empty + st);
       }
     }
-    n += part;
-    // ---- this warp's part: sums over the four threads of a row, o in units of one
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    if (!ok) break;
+    // ---- this warp's part: sums over the eight lanes that share a row, o in units of one
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) {
-      o[i][0] *= vref; o[i][1] *= vref; o[i][2] *= vref; o[i][3] *= vref;
-    }
-    // ---- joined over the warps of a row block: the upper half hands its part to the lower
-    float4* const mo = reinterpret_cast<float4*>(smem + L::kOffMerge);
-    float2* const ms = reinterpret_cast<float2*>(smem + L::kOffStat);
-    for (int half = TG / 2; half >= 1; half >>= 1) {
-      if (active <= half) continue;  // the upper half had no tile
-      const bool gives = place >= half && place < 2 * half;
-      const int slot = (gives ? place - half : place) * RBW + rb;
-      if (gives) {
+    for (int b = 0; b < NB; ++b) {
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) mo[(slot * kCols + i) * 32 + lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
-        if (t == 0) {
-          ms[slot * 16 + g] = make_float2(m0, l0);
-          ms[slot * 16 + 8 + g] = make_float2(m1, l1);
-        }
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], d);
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) {
+        o[i][b][0] *= vref; o[i][b][1] *= vref; o[i][b][2] *= vref; o[i][b][3] *= vref;
       }
-      mbar_arrive_warp(merge);
-      if (ok) ok = mbar_wait_warp(merge, merges & 1, abort_flag, p.status);
-      ++merges;
-      if (place < half) {
-        const float2 y0 = ms[slot * 16 + g], y1 = ms[slot * 16 + 8 + g];
-        const float M0 = fmaxf(m0, y0.x), M1 = fmaxf(m1, y1.x);
-        const float a0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - M0), b0 = y0.x == -INFINITY ? 0.f : ex2_approx(y0.x - M0);
-        const float a1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - M1), b1 = y1.x == -INFINITY ? 0.f : ex2_approx(y1.x - M1);
-#pragma unroll
-        for (int i = 0; i < kCols; ++i) {
-          const float4 y = mo[(slot * kCols + i) * 32 + lane];
-          o[i][0] = o[i][0] * a0 + y.x * b0;
-          o[i][1] = o[i][1] * a0 + y.y * b0;
-          o[i][2] = o[i][2] * a1 + y.z * b1;
-          o[i][3] = o[i][3] * a1 + y.w * b1;
-        }
-        l0 = l0 * a0 + y0.y * b0;
-        l1 = l1 * a1 + y1.y * b1;
-        m0 = M0;
-        m1 = M1;
-      }
-      mbar_arrive_warp(merge);
-      if (ok) ok = mbar_wait_warp(merge, merges & 1, abort_flag, p.status);
-      ++merges;
     }
     // ---- the pair's output, or this run's part of it
-    if (works && place == 0) {
+    {
       const bool whole = part == w.nt;
       // a run's first part may begin inside a pair (slot 0), another one ends inside it (slot 1)
-      const size_t slot = static_cast<size_t>(blockIdx.x) * 2 + (w.j > 0 ? 0 : 1);
+      const size_t slot = static_cast<size_t>(run) * 2 + (w.j > 0 ? 0 : 1);
+      // for the merge: the pair's first run and its number of runs
+      if (w.j == 0 && rb == 0 && lane == 0)
+        p.parts[bh] = make_int2(run, whole ? 0 : deal.holder(w.t + w.nt - 1) - run + 1);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = e ? r1 : r0;
-        if (r >= p.R) continue;
-        const float l = e ? l1 : l0, m = e ? m1 : m0;
-        const float il = l == 0.f ? 0.f : 1.f / l;
-        const float lse2 = l == 0.f ? -INFINITY : m + __log2f(l);
-        const size_t row = whole ? bh * p.R + r : slot * p.R + r;
-        if (t == 0) {
-          if (!whole) p.lse_part[row] = lse2;
-          else if (p.lse) p.lse[row] = lse2 * 0.69314718055994531f;
-        }
-        // columns (DP / 4) t + i (element 2e of block i) and + DP / 8 (element 2e + 1)
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int c = 0; c < DP / 4; c += 8) {
-          const int col = (DP / 4) * t + c;
-          if (col >= p.d) continue;
-          float y[8];
+        for (int e = 0; e < 2; ++e) {
+          const int r = row0 + 8 * b + 2 * t + e;
+          if (r >= p.R) continue;
+          const float il = l[b][e] == 0.f ? 0.f : 1.f / l[b][e];
+          const float lse2 = l[b][e] == 0.f ? -INFINITY : m[b][e] + __log2f(l[b][e]);
+          const size_t row = whole ? bh * p.R + r : slot * p.R + r;
+          if (g == 0) {
+            if (!whole) p.lse_part[row] = lse2;
+            else if (p.lse) p.lse[row] = lse2 * 0.69314718055994531f;
+          }
+          // columns (DP / 8) g + i: element 2 (i % 2) + e of block i / 2
 #pragma unroll
-          for (int k = 0; k < 8; ++k) y[k] = o[(c + k) % kCols][2 * e + (c + k) / kCols] * il;
-          if (!whole || p.out_f32) {
-            float4* dst = reinterpret_cast<float4*>((whole ? static_cast<float*>(p.o) : p.o_part) + row * p.d + col);
-            dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-            dst[1] = make_float4(y[4], y[5], y[6], y[7]);
-          } else {
-            const T* tag = nullptr;
-            *reinterpret_cast<uint4*>(static_cast<T*>(p.o) + row * p.d + col) =
-                make_uint4(pack2(tag, y[0], y[1]), pack2(tag, y[2], y[3]), pack2(tag, y[4], y[5]), pack2(tag, y[6], y[7]));
+          for (int c = 0; c < DP / 8; c += 8) {
+            const int col = (DP / 8) * g + c;
+            if (col >= p.d) continue;
+            float y[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = o[(c + k) / 2][b][2 * (k & 1) + e] * il;
+            if (!whole || p.out_f32) {
+              float4* dst = reinterpret_cast<float4*>((whole ? static_cast<float*>(p.o) : p.o_part) + row * p.d + col);
+              dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+              dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+            } else {
+              const T* tag = nullptr;
+              *reinterpret_cast<uint4*>(static_cast<T*>(p.o) + row * p.d + col) =
+                  make_uint4(pack2(tag, y[0], y[1]), pack2(tag, y[2], y[3]), pack2(tag, y[4], y[5]), pack2(tag, y[6], y[7]));
+            }
           }
         }
-      }
     }
   }
-  // ---- batches without a key: O = 0, LSE = -inf, dealt to the CTAs
+  if (rb == 0 && (!ok || abort_read(abort_flag)))  // let the copies land before the shared memory goes away
+    for (uint32_t i = issued > stages ? issued - stages : 0; i < issued; ++i) mbar_drain(full + i % stages, (i / stages) & 1);
+  // ---- batches without a key: O = 0, LSE = -inf, nothing to merge; dealt to the CTAs
   if (p.cache_seqlens) {
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
       if (cache_len(p.cache_seqlens, b, p.Nk, p.status, threadIdx.x == 0) > 0) continue;
       const size_t rows = static_cast<size_t>(p.Hkv) * p.R;
       uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.o) + b * rows * p.d * (p.out_f32 ? 4 : 2));
       const size_t n16 = rows * p.d * (p.out_f32 ? 4 : 2) / 16;
-      for (size_t i = threadIdx.x; i < n16; i += kConsumers * 32) dst[i] = make_uint4(0, 0, 0, 0);
+      for (size_t i = threadIdx.x; i < n16; i += kThreads) dst[i] = make_uint4(0, 0, 0, 0);
       if (p.lse)
-        for (size_t i = threadIdx.x; i < rows; i += kConsumers * 32) p.lse[b * rows + i] = -INFINITY;
+        for (size_t i = threadIdx.x; i < rows; i += kThreads) p.lse[b * rows + i] = -INFINITY;
+      for (int i = threadIdx.x; i < p.Hkv; i += kThreads) p.parts[static_cast<size_t>(b) * p.Hkv + i] = make_int2(0, 0);
     }
   }
 }
 
-// Merges the parts of the pairs that lie in several runs.  CTA (c, r): if run c + 1 is the first to
-// begin inside a pair, that pair's row r; four warps take every fourth part each.
-template <typename OutT>
-__global__ void __launch_bounds__(128) cache8_merge_kernel(const Cache8Params p, int ctas) {
-  __shared__ float4 s_o[4][32];
-  __shared__ float2 s_ml[4];
+// Merges the parts of the pairs that several runs share.  A row is one warp's (W = 1) or a CTA's
+// eight warps' (W = 8), each taking every W-th part, eight at a time.
+template <typename OutT, int W>
+__global__ void __launch_bounds__(256) cache8_merge_kernel(const Cache8Params p) {
+  __shared__ float4 s_o[8][32];
+  __shared__ float2 s_ml[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long total = total_tiles(p);
-  const int c = blockIdx.x;
-  const long long cut = run_start(total, c + 1, ctas);
-  if (cut >= total || cut == 0) return;
-  Walk w;
-  w.start(p, cut, total);
-  if (w.j == 0) return;  // the cut lies between two pairs
-  const long long first = cut - w.j;
-  const int c0 = run_of(total, first, ctas), c1 = run_of(total, first + w.nt - 1, ctas);
-  // one of the cuts inside the pair works: the first (an empty run's cut comes again with the next)
-  if (c > 0 && run_start(total, c, ctas) > first) return;
-  for (int r = blockIdx.y; r < p.R; r += gridDim.y) {
-    float m = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = c0 + warp; k0 <= c1; k0 += 16) {
-      float e[4];
-      float4 x[4];
+  const long long row = W == 8 ? blockIdx.x : static_cast<long long>(blockIdx.x) * 8 + warp;
+  dependency_wait();
+  if (row >= static_cast<long long>(p.B) * p.Hkv * p.R) return;
+  const int bh = static_cast<int>(row / p.R), r = static_cast<int>(row % p.R);
+  const int2 parts = p.parts[bh];
+  // none, or (left by a run that ended with an error status) anything
+  if (parts.y <= 0 || parts.x < 0 || parts.x >= p.runs || parts.y > p.runs - parts.x) return;
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = W == 8 ? warp : 0; k0 < parts.y; k0 += 8 * W) {
+    float e[8];
+    float4 x[8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int k = k0 + 4 * u;
-        // run k's part of this pair begins at its start, or where the pair begins
-        const bool in = k <= c1 && run_start(total, k, ctas) < run_start(total, k + 1, ctas);
-        const size_t row = (static_cast<size_t>(k) * 2 + (run_start(total, k, ctas) > first ? 0 : 1)) * p.R + r;
-        e[u] = in ? p.lse_part[row] : -INFINITY;
-        x[u] = in && lane * 4 < p.d ? *reinterpret_cast<const float4*>(p.o_part + row * p.d + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (e[u] == -INFINITY) continue;
-        const float M = fmaxf(m, e[u]);
-        const float a = m == -INFINITY ? 0.f : ex2_approx(m - M), b = ex2_approx(e[u] - M);
-        acc.x = acc.x * a + x[u].x * b;
-        acc.y = acc.y * a + x[u].y * b;
-        acc.z = acc.z * a + x[u].z * b;
-        acc.w = acc.w * a + x[u].w * b;
-        l = l * a + b;
-        m = M;
-      }
+    for (int u = 0; u < 8; ++u) {
+      const int k = k0 + u * W;
+      const bool in = k < parts.y;
+      // the first run's part ends inside the pair, the others' begin there
+      const size_t at = (static_cast<size_t>(parts.x + k) * 2 + (k == 0 ? 1 : 0)) * p.R + r;
+      e[u] = in ? p.lse_part[at] : -INFINITY;
+      x[u] = in && lane * 4 < p.d ? *reinterpret_cast<const float4*>(p.o_part + at * p.d + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) top = fmaxf(top, e[u]);
+    const float a = m == top ? 1.f : ex2_approx(m - top);  // m = -inf: 0
+    acc.x *= a; acc.y *= a; acc.z *= a; acc.w *= a;
+    l *= a;
+    m = top;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      // a NaN part stays; an empty one (no key that the row sees) has no weight
+      const float b = e[u] == -INFINITY ? 0.f : ex2_approx(e[u] - top);
+      acc.x += x[u].x * b;
+      acc.y += x[u].y * b;
+      acc.z += x[u].z * b;
+      acc.w += x[u].w * b;
+      l += b;
+    }
+  }
+  if (W == 8) {
     s_o[warp][lane] = acc;
     if (lane == 0) s_ml[warp] = make_float2(m, l);
     __syncthreads();
-    if (warp == 0) {
-      float M = -INFINITY;
+    if (warp != 0) return;
+    m = -INFINITY;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) M = fmaxf(M, s_ml[u].x);
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-      float sum = 0.f;
+    for (int u = 0; u < 8; ++u) m = fmaxf(m, s_ml[u].x);
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    l = 0.f;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float b = s_ml[u].x == -INFINITY ? 0.f : ex2_approx(s_ml[u].x - M);
-        const float4 x = s_o[u][lane];
-        y.x += x.x * b; y.y += x.y * b; y.z += x.z * b; y.w += x.w * b;
-        sum += s_ml[u].y * b;
-      }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const size_t row = (static_cast<size_t>(w.b) * p.Hkv + w.h) * p.R + r;
-      if (lane * 4 < p.d) {
-        if constexpr (std::is_same<OutT, float>::value) {
-          *reinterpret_cast<float4*>(static_cast<float*>(p.o) + row * p.d + lane * 4) = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
-        } else {
-          const OutT* tag = nullptr;
-          *reinterpret_cast<uint2*>(static_cast<OutT*>(p.o) + row * p.d + lane * 4) =
-              make_uint2(pack2(tag, y.x * inv, y.y * inv), pack2(tag, y.z * inv, y.w * inv));
-        }
-      }
-      if (lane == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (M + __log2f(sum)) * 0.69314718055994531f;
+    for (int u = 0; u < 8; ++u) {
+      const float b = s_ml[u].x == -INFINITY ? 0.f : ex2_approx(s_ml[u].x - m);
+      const float4 x = s_o[u][lane];
+      acc.x += x.x * b; acc.y += x.y * b; acc.z += x.z * b; acc.w += x.w * b;
+      l += s_ml[u].y * b;
     }
-    __syncthreads();
   }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  if (lane * 4 < p.d) {
+    if constexpr (std::is_same<OutT, float>::value) {
+      *reinterpret_cast<float4*>(static_cast<float*>(p.o) + row * p.d + lane * 4) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    } else {
+      const OutT* tag = nullptr;
+      *reinterpret_cast<uint2*>(static_cast<OutT*>(p.o) + row * p.d + lane * 4) =
+          make_uint2(pack2(tag, acc.x * inv, acc.y * inv), pack2(tag, acc.z * inv, acc.w * inv));
+    }
+  }
+  if (lane == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
 }
 
 // A cache of capacity 0: O = 0, LSE = -inf for every row.
@@ -679,29 +715,39 @@ __global__ void __launch_bounds__(256) cache8_none_kernel(const Cache8Params p) 
   if (first < static_cast<size_t>(p.B)) cache_len(p.cache_seqlens, static_cast<int>(first), p.Nk, p.status, true);
 }
 
-template <typename T, typename Code, int DP>
+template <typename T, typename Code, int DP, int NB>
 cudaError_t run(const CUtensorMap& k, const CUtensorMap& v, const Cache8Params& p, cudaStream_t stream) {
-  auto kern = cache8_kernel<T, Code, DP>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DP>::kBytes);
+  using L = Layout<DP, NB>;
+  auto kern = cache8_kernel<T, Code, DP, NB>;
+  static std::atomic<unsigned long long> ready{0};  // devices on which the kernel is set up
+  cudaError_t e = once_per_device(ready, [&] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  });
   if (e != cudaSuccess) return e;
-  cudaFuncAttributes fa;  // the register split assumes the launch's allocation; never launch otherwise
-  e = cudaFuncGetAttributes(&fa, kern);
-  if (e != cudaSuccess) return e;
-  if (fa.numRegs != static_cast<int>(kLaunchRegs)) return cudaErrorInvalidConfiguration;
-  kern<<<p.ctas, kThreads, Layout<DP>::kBytes, stream>>>(k, v, p);
+  kern<<<p.ctas, kThreads, L::kBytes, stream>>>(k, v, p);
   e = cudaGetLastError();
-  if (e != cudaSuccess || p.ctas == 1) return e;
-  const dim3 grid(p.ctas - 1, std::min(p.R, 64));
-  if (p.out_f32) cache8_merge_kernel<float><<<grid, 128, 0, stream>>>(p, p.ctas);
-  else cache8_merge_kernel<T><<<grid, 128, 0, stream>>>(p, p.ctas);
-  return cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // launched while the first kernel runs (it takes its SMs' room as that ends), waits for it inside.
+  // Rows by the thousand have few parts each; few rows have many
+  const long long rows = static_cast<long long>(p.B) * p.Hkv * p.R;
+  if (rows >= 4096) {
+    const dim3 grid(static_cast<unsigned>((rows + 7) / 8));
+    return p.out_f32 ? launch_dependent(cache8_merge_kernel<float, 1>, grid, 256, stream, p) : launch_dependent(cache8_merge_kernel<T, 1>, grid, 256, stream, p);
+  }
+  const dim3 grid(static_cast<unsigned>(rows));
+  return p.out_f32 ? launch_dependent(cache8_merge_kernel<float, 8>, grid, 256, stream, p) : launch_dependent(cache8_merge_kernel<T, 8>, grid, 256, stream, p);
+}
+
+template <typename T, typename Code>
+cudaError_t run_c(const CUtensorMap& k, const CUtensorMap& v, const Cache8Params& p, cudaStream_t stream) {
+  const bool few = cache8_row_blocks(p.R) == 1;
+  if (p.d <= 64) return few ? run<T, Code, 64, 1>(k, v, p, stream) : run<T, Code, 64, 2>(k, v, p, stream);
+  return few ? run<T, Code, 128, 1>(k, v, p, stream) : run<T, Code, 128, 2>(k, v, p, stream);
 }
 
 template <typename T>
 cudaError_t run_t(const CUtensorMap& k, const CUtensorMap& v, const Cache8Params& p, attn_cache_dtype_t cache, cudaStream_t stream) {
-  if (p.d <= 64)
-    return cache == ATTN_CACHE_I8 ? run<T, CodeI8, 64>(k, v, p, stream) : run<T, CodeE4m3, 64>(k, v, p, stream);
-  return cache == ATTN_CACHE_I8 ? run<T, CodeI8, 128>(k, v, p, stream) : run<T, CodeE4m3, 128>(k, v, p, stream);
+  return cache == ATTN_CACHE_I8 ? run_c<T, CodeI8>(k, v, p, stream) : run_c<T, CodeE4m3>(k, v, p, stream);
 }
 
 }  // namespace

@@ -166,13 +166,21 @@ struct Cache8Params {
   int B, Hkv, Nq, Nk, R, d, block_shift, n_blocks, causal;
   float scale_log2;
   int out_f32;
-  // few rows (R <= kCache8Rows): the tiles of all caches are dealt to `ctas` CTAs in equal runs; a
-  // run's part of a (batch, kv head) pair that it does not hold whole goes here, two slots a run
-  int ctas;
-  float* o_part;           // [2 * ctas, R, d], normalised
-  float* lse_part;         // [2 * ctas, R], log2
+  // few rows (R <= kCache8Rows): the tiles of all caches are dealt in equal runs to the workers of
+  // `ctas` CTAs; a run's part of a (batch, kv head) pair that it does not hold whole goes here, two
+  // slots a run
+  int ctas, runs, tile_keys;
+  float* o_part;           // [2 * runs, R, d], normalised
+  float* lse_part;         // [2 * runs, R], log2
+  int2* parts;             // [B * Hkv]: the first run of a pair that several share and their number, else (., 0)
 };
-constexpr int kCache8Rows = 64, kCache8Keys = 48;
+constexpr int kCache8Rows = 64;
+// For R rows: blocks of 8 rows per warp, the warps that share a run, and the keys of a tile and CTAs (of
+// four warps) per SM that go with the former.
+constexpr int cache8_row_blocks(int R) { return R <= 8 ? 1 : 2; }
+constexpr int cache8_run_warps(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : 4; }
+constexpr int cache8_keys(int row_blocks) { return row_blocks == 1 ? 32 : 48; }
+constexpr int cache8_ctas_per_sm(int row_blocks) { return row_blocks == 1 ? 3 : 2; }
 cudaError_t launch_cache8_fwd(const CUtensorMap& k, const CUtensorMap& v, const Cache8Params& p, attn_dtype_t dtype,
                               attn_cache_dtype_t cache, cudaStream_t stream);
 cudaError_t launch_cache8_wide(const Cache8Params& p, attn_dtype_t dtype, attn_cache_dtype_t cache, cudaStream_t stream);
