@@ -658,6 +658,69 @@ Cache8Plan cache8_plan(int B, int Hkv, int R, int Nk, int d) {
           round256(static_cast<size_t>(B) * Hkv * sizeof(int2))};
 }
 
+// Many rows: the key ranges, one as soon as the row blocks fill the GPU twice (a second pass over the
+// fp32 parts costs more than the last wave's idle SMs), and the workspace: the expanded K and V,
+// then the ranges' parts.
+struct Kv8Plan {
+  KvSplit split;
+  size_t cache_bytes, o_bytes, lse_bytes;  // cache_bytes: K or V
+};
+Kv8Plan kv8_plan(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
+  const long long R = static_cast<long long>(Hq / Hkv) * Nq, bh = static_cast<long long>(B) * Hkv;
+  Kv8Plan plan{};
+  plan.split = kv_split(B, Hq, Hkv, Nq, Nk, bh * ((R + attn::kBM - 1) / attn::kBM) >= 2 * 152 ? 1 : 0);
+  plan.cache_bytes = round256(static_cast<size_t>(bh) * Nk * d * 2);
+  if (plan.split.n_splits > 1) {
+    plan.o_bytes = round256(static_cast<size_t>(plan.split.n_splits) * bh * R * d * sizeof(float));
+    plan.lse_bytes = round256(static_cast<size_t>(plan.split.n_splits) * bh * R * sizeof(float));
+  }
+  return plan;
+}
+
+// The forward over many rows and an 8-bit cache; p describes the call.
+attn_status_t fwd_kv8(const attn::Cache8Params& c, void* workspace, int Hq, attn_dtype_t dtype, attn_cache_dtype_t cache_dtype,
+                      cudaStream_t s) {
+  const Kv8Plan plan = kv8_plan(c.B, Hq, c.Hkv, c.Nq, c.Nk, c.d);
+  const int bh = c.B * c.Hkv;
+  const long long n_rb = (static_cast<long long>(c.R) + attn::kBM - 1) / attn::kBM;
+  if (n_rb * bh * plan.split.n_splits > 0x7fffffffLL || (static_cast<long long>(c.Nk) + 127) / 128 * bh > 0x7fffffffLL)
+    return ATTN_ERR_UNSUPPORTED;
+  char* const ws = static_cast<char*>(workspace);
+  void* const k16 = ws;
+  void* const v16 = ws + plan.cache_bytes;
+  FwdParams p{};
+  p.o = c.o;
+  p.lse = c.lse;
+  p.status = c.status;
+  p.wait_ns = c.wait_ns;
+  p.B = c.B; p.Hq = Hq; p.Hkv = c.Hkv; p.N = c.Nk; p.d = c.d; p.G = Hq / c.Hkv;
+  p.Nq = c.Nq; p.Nk = c.Nk; p.R = c.R;
+  p.cache_seqlens = c.cache_seqlens;
+  p.n_splits = plan.split.n_splits;
+  p.tiles_per_split = plan.split.tiles_per_split;
+  p.o_part = reinterpret_cast<float*>(ws + 2 * plan.cache_bytes);
+  p.lse_part = reinterpret_cast<float*>(ws + 2 * plan.cache_bytes + plan.o_bytes);
+  p.n_qtiles = static_cast<int>(n_rb);
+  p.scale_log2 = c.scale_log2;
+  p.out_f32 = c.out_f32;
+  p.k_scale = c.k_scale;
+  p.n_blocks = c.n_blocks;
+  p.block_shift = c.block_shift;
+  FwdMaps maps;
+  if (!make_dense_map(&maps.q, c.q, dtype, bh, c.R, c.d) || !make_dense_map(&maps.k, k16, dtype, bh, c.Nk, c.d) ||
+      !make_dense_map(&maps.v, v16, dtype, bh, c.Nk, c.d))
+    return ATTN_ERR_CUDA;
+  const bool final16 = p.n_splits == 1 && !p.out_f32;  // tile stores of 16-bit outputs
+  if (!final16)
+    maps.o = maps.q;
+  else if (!make_dense_map(&maps.o, c.o, dtype, bh, c.R, c.d))
+    return ATTN_ERR_CUDA;
+  if (attn::launch_cache8_expand(c, k16, v16, dtype, cache_dtype, s) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (attn::launch_fwd_kv8(maps, p, dtype, c.causal != 0, s) != cudaSuccess) return ATTN_ERR_CUDA;
+  return from_cuda(p.n_splits > 1 ? attn::launch_kv_combine(p, dtype, c.causal != 0, s)
+                                  : attn::launch_kv8_unseen(p, !p.out_f32, c.causal != 0, s));
+}
+
 bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + bn && y < x + an;
@@ -695,7 +758,10 @@ attn_status_t attn_kvcache8_append(void* k8, void* v8, float* k_scale, float* v_
 size_t attn_fwd_kvcache8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Nq <= 0 || Nk < 0 || d <= 0) return 0;
   const size_t R = static_cast<size_t>(Hq / Hkv) * Nq;
-  if (R > static_cast<size_t>(attn::kCache8Rows)) return 256;
+  if (R > static_cast<size_t>(attn::kCache8Rows)) {
+    const Kv8Plan plan = kv8_plan(B, Hq, Hkv, Nq, Nk, d);
+    return std::max<size_t>(256, 2 * plan.cache_bytes + plan.o_bytes + plan.lse_bytes);
+  }
   const Cache8Plan plan = cache8_plan(B, Hkv, static_cast<int>(R), Nk, d);
   return plan.o_bytes + plan.lse_bytes + plan.parts_bytes;
 }
@@ -739,7 +805,7 @@ attn_status_t attn_fwd_kvcache8(const void* q, const void* k8, const void* v8, c
   p.out_f32 = (flags & ATTN_FLAG_OUT_F32) ? 1 : 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (Nk == 0) return from_cuda(attn::launch_cache8_none(p, s));
-  if (R > attn::kCache8Rows) return from_cuda(attn::launch_cache8_wide(p, dtype, cache_dtype, s));
+  if (R > attn::kCache8Rows) return fwd_kv8(p, workspace, Hq, dtype, cache_dtype, s);
   p.tile_keys = attn::cache8_keys(attn::cache8_row_blocks(p.R));
   // tiles are numbered in 32 bits (two terabytes of codes)
   if (bh * ((static_cast<long long>(Nk) + p.tile_keys - 1) / p.tile_keys) > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;

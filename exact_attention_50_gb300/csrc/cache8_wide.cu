@@ -1,97 +1,103 @@
-// cache8_wide.cu -- attention of many query rows over an 8-bit KV cache.
+// cache8_wide.cu -- many query rows over an 8-bit KV cache (chunks of a prompt): the cache is expanded
+// to 16 bits once, in the caller's workspace, and the tcgen05 forward runs on that.
 //
-// CUDA-core kernel: a CTA of 128 threads owns one query row of a (batch, kv head) and walks the
-// keys in tiles of 128, a thread per key for the scores, an online softmax over the tile, a thread
-// per column for P V.  The key scale multiplies the score, the value scale the weight.
+// With R rows per kv head the forward reads every key R / 128 times, so expanding inside it would
+// repeat the conversion as often, on the warps whose exponentials bound it; once costs 5 bytes of
+// traffic per code.  K is expanded to bare codes, exact in either 16-bit type, and its scales
+// multiply the scores in fp32.  V is expanded to values, code * scale, rounded once (half a step 2^-8
+// bf16, 2^-11 fp16): its scale differs from key to key inside the P V sum.
+#include <algorithm>
+#include <type_traits>
 #include "cache8.cuh"
 
 namespace attn {
 namespace {
 
-template <typename T>
-__device__ __forceinline__ float to_f(T x);
-template <>
-__device__ __forceinline__ float to_f<__half>(__half x) { return __half2float(x); }
-template <>
-__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void from_f(__half* p, float x) { *p = __float2half_rn(x); }
-__device__ __forceinline__ void from_f(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ uint32_t pair(const __half*, float a, float b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pair(const __nv_bfloat16*, float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 
 template <typename T, typename Code>
-__global__ void __launch_bounds__(128) simple_kernel(const Cache8Params p) {
-  __shared__ float s_q[128], s_p[128], s_red[4];
-  const int bh = blockIdx.x / p.R, r = blockIdx.x % p.R, b = bh / p.Hkv, tid = threadIdx.x;
-  const int L = cache_len(p.cache_seqlens, b, p.Nk, p.status, tid == 0 && r == 0 && bh % p.Hkv == 0);
-  const int last = p.causal ? min(L - p.Nq + r % p.Nq, L - 1) : L - 1;
-  const size_t row = static_cast<size_t>(bh) * p.R + r;
-  if (tid < p.d) s_q[tid] = to_f<T>(static_cast<const T*>(p.q)[row * p.d + tid]);
-  __syncthreads();
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  for (int j0 = 0; j0 <= last; j0 += 128) {
-    const int j = j0 + tid;
-    float s = -INFINITY, vs = 0.f;
-    if (j <= last) {
-      const size_t at = static_cast<size_t>(bh) * p.n_blocks + (j >> p.block_shift);
-      const uint32_t* k = reinterpret_cast<const uint32_t*>(p.k8 + (static_cast<size_t>(bh) * p.Nk + j) * p.d);
-      float dot = 0.f;
-      for (int c = 0; c < p.d / 4; ++c) {
-        float x[4];
-        Code::decode4(k[c], x);
+__device__ __forceinline__ void expand16(const uint4 w, float scale, uint4* dst) {
+  const T* tag = nullptr;
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  uint32_t out[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dot = fmaf(x[i], s_q[4 * c + i], dot);
-      }
-      s = dot * p.k_scale[at] * p.scale_log2;
-      vs = p.v_scale[at];
-    }
-    float mx = s;
-#pragma unroll
-    for (int i = 16; i > 0; i >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
-    if ((tid & 31) == 0) s_red[tid >> 5] = mx;
-    __syncthreads();
-    const float mn = fmaxf(m, fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3])));
-    const float e = j <= last ? exp2f(s - mn) : 0.f;
-    s_p[tid] = e == 0.f ? 0.f : e * vs;
-    float sum = e;
-#pragma unroll
-    for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
-    __syncthreads();
-    if ((tid & 31) == 0) s_red[tid >> 5] = sum;
-    __syncthreads();
-    const float alpha = m == -INFINITY ? 0.f : exp2f(m - mn);
-    l = l * alpha + (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
-    m = mn;
-    o *= alpha;
-    const int n = min(128, last + 1 - j0);
-    if (tid < p.d) {
-      const uint8_t* v = p.v8 + (static_cast<size_t>(bh) * p.Nk + j0) * p.d + (tid & ~3);
-      for (int i = 0; i < n; ++i) {
-        float x[4];
-        Code::decode4(*reinterpret_cast<const uint32_t*>(v + static_cast<size_t>(i) * p.d), x);
-        o = fmaf(s_p[i], x[tid & 3], o);
-      }
-    }
-    __syncthreads();
+  for (int i = 0; i < 4; ++i) {
+    float x[4];
+    Code::decode4(in[i], x);
+    out[2 * i] = pair(tag, x[0] * scale, x[1] * scale);
+    out[2 * i + 1] = pair(tag, x[2] * scale, x[3] * scale);
   }
-  o = l > 0.f ? o / l : (l == 0.f ? 0.f : l);
-  if (tid < p.d) {
-    if (p.out_f32) static_cast<float*>(p.o)[row * p.d + tid] = o;
-    else from_f(static_cast<T*>(p.o) + row * p.d + tid, o);
+  dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+  dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+}
+
+// A CTA expands 128 tokens of one (batch, kv head): 16 codes of K and of V per thread and step.
+template <typename T, typename Code>
+__global__ void __launch_bounds__(256) expand_kernel(const Cache8Params p, T* k16, T* v16, int tiles) {
+  const int bh = blockIdx.x / tiles, j0 = (blockIdx.x % tiles) * 128;
+  const int L = cache_len(p.cache_seqlens, bh / p.Hkv, p.Nk, nullptr, false);
+  if (j0 >= L) return;
+  const int chunks = p.d / 16, n = min(128, p.Nk - j0) * chunks;
+  const size_t base = (static_cast<size_t>(bh) * p.Nk + j0) * p.d;
+  const uint4* k = reinterpret_cast<const uint4*>(p.k8 + base);
+  const uint4* v = reinterpret_cast<const uint4*>(p.v8 + base);
+  uint4* ko = reinterpret_cast<uint4*>(k16 + base);
+  uint4* vo = reinterpret_cast<uint4*>(v16 + base);
+  for (int i = threadIdx.x; i < n; i += 256) {
+    const int j = j0 + i / chunks;
+    if (j < L) {
+      const float vs = p.v_scale[static_cast<size_t>(bh) * p.n_blocks + (j >> p.block_shift)];
+      const uint4 a = k[i], b = v[i];
+      expand16<T, Code>(a, 1.f, ko + 2 * i);
+      expand16<T, Code>(b, vs, vo + 2 * i);
+    } else {  // the tile's rest: a weight of zero times what lies there has to be zero
+      const uint4 z = make_uint4(0, 0, 0, 0);
+      ko[2 * i] = ko[2 * i + 1] = vo[2 * i] = vo[2 * i + 1] = z;
+    }
   }
-  if (tid == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+// One key range: rows of a 128-row block that sees no key have no work item; O = 0, LSE = -inf.
+__global__ void __launch_bounds__(256) unseen_kernel(const FwdParams p, int es, bool causal) {
+  const int bh = blockIdx.x / p.n_qtiles, rb = blockIdx.x % p.n_qtiles;
+  const int L = cache_len(p.cache_seqlens, bh / p.Hkv, p.Nk, nullptr, false);
+  if (kv_needed_keys(L, p.Nq, p.R, rb, causal) > 0) return;
+  const int rows = min(128, p.R - rb * 128);
+  const size_t row = static_cast<size_t>(bh) * p.R + rb * 128;
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.o) + row * p.d * es);
+  for (int i = threadIdx.x; i < rows * p.d * es / 16; i += 256) dst[i] = make_uint4(0, 0, 0, 0);
+  if (p.lse)
+    for (int i = threadIdx.x; i < rows; i += 256) p.lse[row + i] = -INFINITY;
 }
 
 template <typename T>
-cudaError_t run(const Cache8Params& p, attn_cache_dtype_t cache, cudaStream_t stream) {
-  const int grid = p.B * p.Hkv * p.R;
-  if (cache == ATTN_CACHE_I8) simple_kernel<T, CodeI8><<<grid, 128, 0, stream>>>(p);
-  else simple_kernel<T, CodeE4m3><<<grid, 128, 0, stream>>>(p);
+cudaError_t expand(const Cache8Params& p, void* k16, void* v16, attn_cache_dtype_t cache, cudaStream_t stream) {
+  const int tiles = (p.Nk + 127) / 128;
+  const int grid = p.B * p.Hkv * tiles;
+  if (cache == ATTN_CACHE_I8)
+    expand_kernel<T, CodeI8><<<grid, 256, 0, stream>>>(p, static_cast<T*>(k16), static_cast<T*>(v16), tiles);
+  else
+    expand_kernel<T, CodeE4m3><<<grid, 256, 0, stream>>>(p, static_cast<T*>(k16), static_cast<T*>(v16), tiles);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_cache8_wide(const Cache8Params& p, attn_dtype_t dtype, attn_cache_dtype_t cache, cudaStream_t stream) {
-  return dtype == ATTN_F16 ? run<__half>(p, cache, stream) : run<__nv_bfloat16>(p, cache, stream);
+cudaError_t launch_cache8_expand(const Cache8Params& p, void* k16, void* v16, attn_dtype_t dtype, attn_cache_dtype_t cache,
+                                 cudaStream_t stream) {
+  return dtype == ATTN_F16 ? expand<__half>(p, k16, v16, cache, stream) : expand<__nv_bfloat16>(p, k16, v16, cache, stream);
+}
+
+cudaError_t launch_kv8_unseen(const FwdParams& p, bool out16, bool causal, cudaStream_t stream) {
+  unseen_kernel<<<p.B * p.Hkv * p.n_qtiles, 256, 0, stream>>>(p, out16 ? 2 : 4, causal);
+  return cudaGetLastError();
 }
 
 }  // namespace attn

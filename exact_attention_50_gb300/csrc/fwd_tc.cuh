@@ -7,7 +7,9 @@
 //   scale); O_i = sum_j P_ij V_j / l_i; LSE_i = m_i + ln l_i.
 // In the KV-cache mode a row is query i = row % Nq of the G query heads of a kv head, its keys
 // are those of one range of the cache, masked past the cache length L and, when causal, past
-// L - Nq + i; it writes fp32 partials that a combine kernel merges.
+// L - Nq + i; it writes fp32 partials that a combine kernel merges.  The 8-bit cache mode is that
+// mode on bare key codes in 16 bits, with the codes' scales applied to the scores, and with one key
+// range it writes final outputs.
 // The tiling follows the attention-operator article (m.xxqk.cn/news/636956) section 2.2: Q/K/V
 // tiles staged on chip, the max-subtracted softmax kept in registers and only O written back.
 // The online max/sum update follows the FlashAttention-T review, best practice 4; scale and
@@ -83,6 +85,7 @@ struct FwdLayout {
   // has run, stages the item's output tile for the tile stores.  (1 Q + 3 V measured the same.)
   // The KV-cache mode stores no output tiles and streams K and V from HBM: one Q slot and a
   // third V stage (more bytes in flight) serve it better.
+  // The 8-bit cache mode, for many rows, has the dense layout.
   static constexpr bool kKv = MODE == kModeKv;
   static constexpr int kStagesQ = (DP == 128 && kKv) ? 1 : 2;
   static constexpr int kStagesK = DP == 128 ? 3 : 4;
@@ -133,7 +136,7 @@ __device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int idx) {
   FwdItem it;
   it.j0 = 0;
   it.split = 0;
-  if constexpr (MODE == kModeKv) {
+  if constexpr (MODE == kModeKv || MODE == kModeKv8) {
     // later row blocks first (under the causal mask they see the most keys), then the key
     // range (first ranges first: they are full, the last ones short or empty), then (batch,
     // kv head).  A CTA takes one item per round of gridDim.x items, so it gets a mix of
@@ -253,16 +256,19 @@ __global__ void __launch_bounds__(512, 1)
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                   const FwdParams p, int n_items) {
   constexpr bool VARLEN = MODE == kModeVarlen;
-  constexpr bool KV = MODE == kModeKv;
+  constexpr bool KV8 = MODE == kModeKv8;
+  constexpr bool KV = MODE == kModeKv || KV8;
+  // an 8-bit cache in one range: the items' outputs are final, written as a dense item's are
+  const bool kv_final = KV8 && p.n_splits == 1;
   // 16-bit output of a dense item, or of a varlen item whose 128 rows all lie in its
   // sequence: the epilogue warps stage the item's O tile in the item's Q slot (free once its
   // last S has run) and their thread 0 writes it with tile stores, then frees the slot.
   // Otherwise (a varlen tile that ends past its sequence must not write into the next one; fp32
   // output or KV-cache partials) the epilogue warps store their rows themselves and the last S
   // frees the Q slot.  Every role decides per item with the same function.
-  const bool tile_out = (MODE == kModeDense || MODE == kModeVarlen) && !p.out_f32;
+  const bool tile_out = (MODE == kModeDense || MODE == kModeVarlen || kv_final) && !p.out_f32;
   auto tile_item = [&](const FwdItem& it) -> bool {
-    return tile_out && (MODE == kModeDense || (it.qt + 1) * kBM <= it.seq_len);
+    return tile_out && (MODE != kModeVarlen || (it.qt + 1) * kBM <= it.seq_len);
   };
   using L = FwdLayout<DP, MODE>;
   constexpr int SQ = L::kStagesQ, SK = L::kStagesK, SV = L::kStagesV;
@@ -580,8 +586,8 @@ __global__ void __launch_bounds__(512, 1)
         row_off = kv_row * p.d;
       else
         row_off = ((static_cast<size_t>(it.b) * p.Hq + it.h) * p.N + q_row) * p.d;
-      const bool o_f32 = KV || p.out_f32;
-      void* const o_base = KV ? static_cast<void*>(p.o_part) : p.o;
+      const bool o_f32 = (KV && !kv_final) || p.out_f32;
+      void* const o_base = (KV && !kv_final) ? static_cast<void*>(p.o_part) : p.o;
       const bool tile = tile_item(it);
       uint8_t* srow = sQ + (ic % SQ) * L::kTileBytes + row * 128;
 #pragma unroll 1
@@ -656,7 +662,7 @@ __global__ void __launch_bounds__(512, 1)
               if constexpr (VARLEN)  // map {d, T, H} over the [T, H, d] output
                 tma_store_3d(&tmO, src, c * 64, it.seq_start + it.qt * kBM, it.h);
               else
-                tma_store_3d(&tmO, src, c * 64, it.qt * kBM, it.b * p.Hq + it.h);
+                tma_store_3d(&tmO, src, c * 64, it.qt * kBM, it.b * (KV ? p.Hkv : p.Hq) + it.h);
             }
             bulk_commit();
             bulk_wait_read<0>();
@@ -665,10 +671,10 @@ __global__ void __launch_bounds__(512, 1)
         }
         if (warp == 12) ok = __all_sync(0xffffffffu, ok);  // the warp leaves the loop together
       }
-      if (valid && (KV || p.lse)) {
+      if (valid && ((KV && !kv_final) || p.lse)) {
         const float lse = (mr + __log2f(l_all)) * 0.69314718055994531f;
         if constexpr (KV)
-          p.lse_part[kv_row] = lse;
+          (kv_final ? p.lse : p.lse_part)[kv_row] = lse;
         else if constexpr (VARLEN)
           p.lse[static_cast<size_t>(it.h) * p.total_tokens + it.seq_start + q_row] = lse;
         else
@@ -684,7 +690,6 @@ __global__ void __launch_bounds__(512, 1)
     const int row = threadIdx.x & 127;        // TMEM lane
     const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t tOg = tl + L::kColO + grp * DP;  // this group's accumulator O_g
-    const float sl2 = p.scale_log2;
     uint32_t kv = 0, ic = 0;
     bool ok = true;
     for (int k = 0; ok && k * static_cast<int>(gridDim.x) < n_items; ++k) {
@@ -704,6 +709,16 @@ __global__ void __launch_bounds__(512, 1)
       for (int j = 0; j < it.n_kv; ++j) {
         const uint32_t t = kv + j;
         const int b = t & 1;
+        // 8-bit cache: the K operand holds the bare codes; their scales (one per 16 to 128 keys) are
+        // fetched before the wait and multiply the scores.  Past the cache's end none is read.
+        float ks[4];
+        if constexpr (KV8) {
+          const int k0 = (it.j0 + j) * kBN + grp * 64;
+          const float* sc = p.k_scale + (static_cast<size_t>(it.b) * p.Hkv + it.h) * p.n_blocks;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            ks[i] = (i == 0 || p.block_shift < 6) && k0 + 16 * i < it.seq_len ? __ldg(sc + ((k0 + 16 * i) >> p.block_shift)) : 0.f;
+        }
         if (!mbar_wait_warp(s_full + b, (t >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
         tc_fence_after();
         const uint32_t tS = tl + b * 128 + grp * 64;  // this group's 64 columns of S buffer b
@@ -719,6 +734,16 @@ __global__ void __launch_bounds__(512, 1)
           for (int i = 0; i < 32; ++i) {
             s[i] = __uint_as_float(r0[i]);
             s[32 + i] = __uint_as_float(r1[i]);
+          }
+        }
+        float sl2 = p.scale_log2;
+        if constexpr (KV8) {
+          if (p.block_shift >= 6 && ks[0] > 0.f) {  // one scale for the group's 64 keys
+            sl2 *= ks[0];
+          } else {
+            if (p.block_shift >= 6) ks[1] = ks[2] = ks[3] = ks[0];
+#pragma unroll
+            for (int c = 0; c < 64; ++c) s[c] *= ks[c / 16];
           }
         }
         // keys key0 + c with c > lim are masked (past the diagonal, or past the sequence)
@@ -875,7 +900,7 @@ cudaError_t launch_fwd_tc_t(const FwdMaps& maps, const FwdParams& p, cudaStream_
   if (e != cudaSuccess) return e;
   if (fa.numRegs != static_cast<int>(L::kLaunchRegs)) return cudaErrorInvalidConfiguration;
   const long heads = MODE == kModeVarlen ? static_cast<long>(p.Hq) * p.nseq
-                     : MODE == kModeKv   ? static_cast<long>(p.B) * p.Hkv * p.n_splits
+                     : (MODE == kModeKv || MODE == kModeKv8) ? static_cast<long>(p.B) * p.Hkv * p.n_splits
                                          : static_cast<long>(p.B) * p.Hq;
   const long items = heads * p.n_qtiles;
   if (items > 0x7fffffffL) return cudaErrorInvalidValue;
@@ -904,6 +929,13 @@ cudaError_t launch_fwd_tc_dtype(const FwdMaps& maps, const FwdParams& p, bool ca
                                 cudaStream_t stream) {
   return p.d <= 64 ? launch_fwd_tc_dp<T, 64>(maps, p, causal, mode, stream)
                    : launch_fwd_tc_dp<T, 128>(maps, p, causal, mode, stream);
+}
+
+template <typename T>
+cudaError_t launch_fwd_kv8_dtype(const FwdMaps& maps, const FwdParams& p, bool causal, cudaStream_t stream) {
+  if (p.d <= 64)
+    return causal ? launch_fwd_tc_t<T, 64, true, kModeKv8>(maps, p, stream) : launch_fwd_tc_t<T, 64, false, kModeKv8>(maps, p, stream);
+  return causal ? launch_fwd_tc_t<T, 128, true, kModeKv8>(maps, p, stream) : launch_fwd_tc_t<T, 128, false, kModeKv8>(maps, p, stream);
 }
 
 }  // namespace attn
