@@ -18,7 +18,8 @@ LIB_PATH = os.path.join(PKG, "libattn_gb300.so")
 
 SOURCES = ["attn_api.cu", "fwd_tc_bf16.cu", "fwd_tc_f16.cu", "bwd_tc_bf16.cu", "bwd_tc_f16.cu", "kv_combine.cu",
            "simt_f32.cu", "bwd_aux.cu", "attn_noalloc.cu", "fwd_short.cu", "cache8_append.cu", "cache8_fwd.cu",
-           "cache8_wide.cu", "fwd_kv8_bf16.cu", "fwd_kv8_f16.cu", "cache_weights.cu", "cache_evict.cu"]
+           "cache8_wide.cu", "fwd_kv8_bf16.cu", "fwd_kv8_f16.cu", "cache_weights.cu",
+           "cache_weights_tc.cu", "cache_evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 

@@ -853,7 +853,15 @@ attn_status_t attn_kvcache_weights(const void* q, const void* k_cache, const flo
   p.B = B; p.Hkv = Hkv; p.Nq = Nq; p.Nk = Nk; p.R = static_cast<int>(R); p.d = d;
   p.causal = causal != 0;
   p.scale_log2 = resolve_scale(scale, d) * kLog2e;
-  return from_cuda(attn::launch_cache_weights(p, dtype, s));
+  if (dtype == ATTN_F32) return from_cuda(attn::launch_cache_weights_f32(p, s));
+  const int q_rows = R >= 128 ? 128 : static_cast<int>((R + 31) / 32 * 32);
+  const uint64_t dims[3] = {static_cast<uint64_t>(d), static_cast<uint64_t>(R), static_cast<uint64_t>(bh)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(d) * 2, static_cast<uint64_t>(R) * d * 2};
+  const uint32_t box[3] = {64, static_cast<uint32_t>(q_rows), 1};
+  CUtensorMap mq, mk;
+  if (!make_map(&mq, q, dtype, 3, dims, strides, box) || !make_dense_map(&mk, k_cache, dtype, static_cast<int>(bh), Nk, d))
+    return ATTN_ERR_CUDA;
+  return from_cuda(attn::launch_cache_weights_tc(mq, mk, p, q_rows, dtype, s));
 }
 
 attn_status_t attn_kvcache_evict(const void* k_cache, const void* v_cache, const float* weights,

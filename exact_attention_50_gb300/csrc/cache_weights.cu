@@ -1,4 +1,5 @@
-// cache_weights.cu -- the attention weight that each cached key receives, added up over queries:
+// cache_weights.cu -- the attention weight that each cached key receives, added up over queries, for
+// float32 (fp16 and bf16 run on the tensor cores, cache_weights_tc.cu):
 //   w_out[j] = w_in[j] + sum_r exp(scale Q_r . K_j - LSE_r) over the rows r = (head, query) of the
 //   key's kv head that see it.
 //
@@ -14,25 +15,14 @@ namespace {
 
 constexpr int kTile = 64, kPad = kTile + 4;
 
-template <typename T>
-__device__ __forceinline__ float to_f(T x);
-template <>
-__device__ __forceinline__ float to_f<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_f<__half>(__half x) { return __half2float(x); }
-template <>
-__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
-
-template <typename T>
-__device__ __forceinline__ void stage(float* dst, const T* src, int rows, int d) {
+__device__ __forceinline__ void stage(float* dst, const float* src, int rows, int d) {
   for (int i = threadIdx.x; i < kTile * d; i += 256) {
     const int r = i / d, c = i % d;
-    dst[c * kPad + r] = r < rows ? to_f<T>(src[static_cast<size_t>(r) * d + c]) : 0.f;
+    dst[c * kPad + r] = r < rows ? src[static_cast<size_t>(r) * d + c] : 0.f;
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) weights_simt_kernel(const WeightParams p, int key_tiles) {
+__global__ void __launch_bounds__(256) weights_f32_kernel(const WeightParams p, int key_tiles) {
   extern __shared__ __align__(16) float smem[];
   float* sK = smem;
   float* sQ = smem + p.d * kPad;
@@ -44,13 +34,13 @@ __global__ void __launch_bounds__(256) weights_simt_kernel(const WeightParams p,
   const int tk = tid & 15, tr = tid >> 4;  // keys 4 tk .. + 3, rows 4 tr .. + 3
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   if (key0 < L) {
-    stage<T>(sK, static_cast<const T*>(p.k) + (static_cast<size_t>(bh) * p.Nk + key0) * p.d, min(kTile, L - key0), p.d);
+    stage(sK, static_cast<const float*>(p.k) + (static_cast<size_t>(bh) * p.Nk + key0) * p.d, min(kTile, L - key0), p.d);
     for (int r0 = 0; r0 < p.R; r0 += kTile) {
       // under the causal mask a tile of rows within one head may end before this key
       const int r1 = min(r0 + kTile, p.R) - 1;
       if (p.causal && r0 / p.Nq == r1 / p.Nq && L - p.Nq + r1 % p.Nq < key0) continue;
       __syncthreads();
-      stage<T>(sQ, static_cast<const T*>(p.q) + (static_cast<size_t>(bh) * p.R + r0) * p.d, min(kTile, p.R - r0), p.d);
+      stage(sQ, static_cast<const float*>(p.q) + (static_cast<size_t>(bh) * p.R + r0) * p.d, min(kTile, p.R - r0), p.d);
       if (tid < kTile) {
         const int r = r0 + tid;
         s_nl[tid] = r < p.R ? -p.lse[static_cast<size_t>(bh) * p.R + r] * 1.4426950408889634f : -INFINITY;
@@ -91,23 +81,18 @@ __global__ void __launch_bounds__(256) weights_simt_kernel(const WeightParams p,
   }
 }
 
-template <typename T>
-cudaError_t run_simt(const WeightParams& p, cudaStream_t stream) {
-  const int key_tiles = (p.Nk + kTile - 1) / kTile;
-  const int bytes = std::max(2 * p.d, p.d + 16) * kPad * 4;
-  auto kern = weights_simt_kernel<T>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * 128 * kPad * 4);
-  if (e != cudaSuccess) return e;
-  kern<<<p.B * p.Hkv * key_tiles, 256, bytes, stream>>>(p, key_tiles);
-  return cudaGetLastError();
-}
-
 }  // namespace
 
-cudaError_t launch_cache_weights(const WeightParams& p, attn_dtype_t dtype, cudaStream_t stream) {
-  if (dtype == ATTN_F32) return run_simt<float>(p, stream);
-  if (dtype == ATTN_F16) return run_simt<__half>(p, stream);
-  return run_simt<__nv_bfloat16>(p, stream);
+cudaError_t launch_cache_weights_f32(const WeightParams& p, cudaStream_t stream) {
+  const int key_tiles = (p.Nk + kTile - 1) / kTile;
+  const int bytes = std::max(2 * p.d, p.d + 16) * kPad * 4;
+  static std::atomic<unsigned long long> ready{0};
+  cudaError_t e = once_per_device(ready, [&] {
+    return cudaFuncSetAttribute(weights_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * 128 * kPad * 4);
+  });
+  if (e != cudaSuccess) return e;
+  weights_f32_kernel<<<p.B * p.Hkv * key_tiles, 256, bytes, stream>>>(p, key_tiles);
+  return cudaGetLastError();
 }
 
 }  // namespace attn

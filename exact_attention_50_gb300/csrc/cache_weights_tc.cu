@@ -1,0 +1,349 @@
+// cache_weights_tc.cu -- accumulated attention weights for fp16 / bf16 on the tensor cores:
+//   w_out[j] = w_in[j] + sum_r exp(scale Q_r . K_j - LSE_r)
+// over the rows r = (head, query) of the key's kv head that see it.
+//
+// S^T = K Q^T: a key is a TMEM lane, so its sum over the rows is one thread's sum over columns -- no
+// reduction between threads, no atomics, an order fixed by the sizes.  A work item is 256 keys of
+// one (batch, kv head): two 128-key tiles that stay in shared memory while the rows' Q tiles
+// (128 rows; fewer when there are fewer) stream past both, which halves Q's traffic out of L2, the
+// bound of a 128-key item (32 KB of Q per 128 x 128 x 128 product).  With few rows (decode) every
+// item has one Q tile and K streams from HBM.  Items are numbered by key tile, those that the
+// most queries see first, and dealt to the CTAs in snake order.
+//
+// 352 threads: warps 0-3 and 4-7 sum the first and second 128 keys (tcgen05.ld, one paired FMA and
+// two ex2 per pair of scores), warp 8 issues the TMA loads, warp 9 the MMAs, warp 10 prepares the rows'
+// -LSE log2(e) and last visible keys.  TMEM: two S^T buffers of 128 columns per key tile.
+#include <algorithm>
+#include <atomic>
+#include "cache8.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kThreads = 352;
+constexpr int kMaxStages = 12;  // of either ring
+constexpr int kNl = 4;          // stages of row terms
+
+// Shared memory: the K ring (128-key tiles), the Q ring, then the fixed part.
+struct Smem {
+  static constexpr int kNlOff = 0;                                 // [kNl][128] float
+  static constexpr int kLimOff = kNlOff + kNl * 512;               // [kNl][128] int
+  static constexpr int kMinOff = kLimOff + kNl * 512;              // [kNl] int: the least of them
+  static constexpr int kBarOff = kMinOff + kNl * 4;                // k_full, k_empty, q_full, q_empty [12]; nl_full, nl_empty [4]; s_full, s_free [2][2]; drain
+  static constexpr int kMiscOff = kBarOff + (4 * kMaxStages + 2 * kNl + 8 + 1) * 8;  // tmem base, abort flag, wait limit
+  static constexpr int kBytes = kMiscOff + 16;
+};
+
+struct Item {
+  int bh, key0, L;
+};
+
+__device__ __forceinline__ int snake(int k) {
+  const int G = gridDim.x, c = blockIdx.x;
+  return k * G + ((k & 1) ? G - 1 - c : c);
+}
+
+__device__ __forceinline__ Item item_of(const WeightParams& p, int idx) {
+  const int bhs = p.B * p.Hkv;
+  Item it;
+  it.bh = idx % bhs;
+  it.key0 = idx / bhs * 256;
+  it.L = cache_len(p.cache_seqlens, it.bh / p.Hkv, p.Nk, nullptr, false);
+  return it;
+}
+
+// Does any row of Q tile rb see a key of the item?
+__device__ __forceinline__ bool tile_seen(const WeightParams& p, const Item& it, int rb) {
+  return kv_needed_keys(it.L, p.Nq, p.R, rb, p.causal != 0) > it.key0;
+}
+
+template <bool BF16, int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    weights_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, const WeightParams p,
+                      int n_items, int qn, int k_stages, int q_stages) {
+  constexpr int kChunks = DP / 64;
+  constexpr int kTileK = 128 * DP * 2;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {  // the swizzle needs aligned tiles
+    if (threadIdx.x == 0) raise_status(p.status, ATTN_ERR_CUDA);
+    return;
+  }
+  const int q_bytes = qn * DP * 2;
+  uint8_t* const sK = smem;
+  uint8_t* const sQ = smem + k_stages * kTileK;
+  uint8_t* const fixed = sQ + q_stages * q_bytes;
+  float* const s_nl = reinterpret_cast<float*>(fixed + Smem::kNlOff);
+  int* const s_lim = reinterpret_cast<int*>(fixed + Smem::kLimOff);
+  int* const s_min = reinterpret_cast<int*>(fixed + Smem::kMinOff);
+  uint64_t* const k_full = reinterpret_cast<uint64_t*>(fixed + Smem::kBarOff);
+  uint64_t* const k_empty = k_full + kMaxStages;
+  uint64_t* const q_full = k_empty + kMaxStages;
+  uint64_t* const q_empty = q_full + kMaxStages;
+  uint64_t* const nl_full = q_empty + kMaxStages;
+  uint64_t* const nl_empty = nl_full + kNl;
+  uint64_t* const s_full = nl_empty + kNl;  // [key tile][buffer]
+  uint64_t* const s_free = s_full + 4;
+  uint64_t* const drain = s_free + 4;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(fixed + Smem::kMiscOff);
+  const uint32_t abort_flag = smem_u32(fixed + Smem::kMiscOff + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kMaxStages; ++i) {
+      mbar_init(k_full + i, 1);
+      mbar_init(k_empty + i, 1);
+      mbar_init(q_full + i, 1);
+      mbar_init(q_empty + i, 1);
+    }
+    for (int i = 0; i < kNl; ++i) {
+      mbar_init(nl_full + i, 1);
+      mbar_init(nl_empty + i, 8);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(s_free + i, 4);
+    }
+    mbar_init(drain, 1);
+    abort_set(abort_flag, 0);
+    wait_limit_set(abort_flag, p.wait_ns);
+    mbar_init_fence();
+  }
+  if (warp == 8) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int n_rb = (p.R + 127) / 128;
+  const int G = gridDim.x;
+
+  if (warp == 8) {
+    // ================================================================ TMA producer
+    if (lane == 0) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      uint32_t nk = 0, nq = 0;  // tiles issued
+      bool ok = true;
+      for (int k = 0; ok && k * G < n_items; ++k) {
+        const int idx = snake(k);
+        if (idx >= n_items) continue;
+        const Item it = item_of(p, idx);
+        if (it.key0 >= it.L) continue;
+        bool first = true;
+        for (int rb = 0; ok && rb < n_rb; ++rb) {
+          if (!tile_seen(p, it, rb)) continue;
+          if (first) {  // the item's key tiles, if any row sees it
+            first = false;
+            for (int h = 0; h < 2 && it.key0 + 128 * h < it.L; ++h, ++nk) {
+              const uint32_t st = nk % k_stages;
+              if (nk >= static_cast<uint32_t>(k_stages) && !mbar_wait(k_empty + st, ((nk / k_stages) - 1) & 1, abort_flag, p.status)) { ok = false; break; }
+              mbar_expect_tx(k_full + st, kTileK);
+              for (int c = 0; c < kChunks; ++c)
+                tma_load_3d(sK + st * kTileK + c * 128 * 128, &tmK, k_full + st, c * 64, it.key0 + 128 * h, it.bh);
+            }
+            if (!ok) break;
+          }
+          const uint32_t st = nq % q_stages;
+          if (nq >= static_cast<uint32_t>(q_stages) && !mbar_wait(q_empty + st, ((nq / q_stages) - 1) & 1, abort_flag, p.status)) { ok = false; break; }
+          mbar_expect_tx(q_full + st, q_bytes);
+          for (int c = 0; c < kChunks; ++c) tma_load_3d(sQ + st * q_bytes + c * qn * 128, &tmQ, q_full + st, c * 64, rb * 128, it.bh);
+          ++nq;
+        }
+      }
+      if (!ok || abort_read(abort_flag)) {  // let the copies land before the shared memory goes away
+        for (uint32_t i = nk > static_cast<uint32_t>(k_stages) ? nk - k_stages : 0; i < nk; ++i) mbar_drain(k_full + i % k_stages, (i / k_stages) & 1);
+        for (uint32_t i = nq > static_cast<uint32_t>(q_stages) ? nq - q_stages : 0; i < nq; ++i) mbar_drain(q_full + i % q_stages, (i / q_stages) & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ================================================================ MMA issuer
+    if (lane == 0) {
+      const uint32_t id = idesc_f16(BF16, false, false, 128, qn);
+      const uint64_t dK = smem_desc_sw128(smem_u32(sK), 16, 1024), dQ = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+      uint32_t nk = 0, nq = 0, ns[2] = {0, 0};
+      bool ok = true;
+      for (int k = 0; ok && k * G < n_items; ++k) {
+        const int idx = snake(k);
+        if (idx >= n_items) continue;
+        const Item it = item_of(p, idx);
+        if (it.key0 >= it.L) continue;
+        const int halves = it.key0 + 128 < it.L ? 2 : 1;
+        bool first = true;
+        for (int rb = 0; ok && rb < n_rb; ++rb) {
+          if (!tile_seen(p, it, rb)) continue;
+          const uint32_t qs = nq % q_stages;
+          if (!mbar_wait(q_full + qs, (nq / q_stages) & 1, abort_flag, p.status)) { ok = false; break; }
+          for (int h = 0; h < halves; ++h) {
+            const uint32_t ks = (nk + h) % k_stages, b = ns[h] & 1;
+            if ((first && !mbar_wait(k_full + ks, ((nk + h) / k_stages) & 1, abort_flag, p.status)) ||
+                (ns[h] >= 2 && !mbar_wait(s_free + 2 * h + b, ((ns[h] >> 1) - 1) & 1, abort_flag, p.status))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t kx = dK + ((ks * kTileK) >> 4), qx = dQ + ((qs * q_bytes) >> 4);
+#pragma unroll
+            for (int s = 0; s < DP / 16; ++s)
+              mma_ss(tmem + h * 256 + b * 128, kx + (((s >> 2) * 128 * 128 + (s & 3) * 32) >> 4),
+                     qx + (((s >> 2) * qn * 128 + (s & 3) * 32) >> 4), id, s > 0 ? 1u : 0u);
+            mma_commit(s_full + 2 * h + b);
+            ++ns[h];
+          }
+          if (!ok) break;
+          mma_commit(q_empty + qs);
+          ++nq;
+          first = false;
+        }
+        if (ok && !first) {
+          for (int h = 0; h < halves; ++h) mma_commit(k_empty + (nk + h) % k_stages);
+          nk += halves;
+        }
+      }
+      if (!ok) {
+        mma_commit(drain);  // every MMA issued completes before this arrives
+        mbar_drain(drain, 0);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ================================================================ row terms
+    uint32_t n = 0;
+    bool ok = true;
+    for (int k = 0; ok && k * G < n_items; ++k) {
+      const int idx = snake(k);
+      if (idx >= n_items) continue;
+      const Item it = item_of(p, idx);
+      if (it.key0 >= it.L) continue;
+      const float* lse = p.lse + static_cast<size_t>(it.bh) * p.R;
+      for (int rb = 0; rb < n_rb; ++rb) {
+        if (!tile_seen(p, it, rb)) continue;
+        const uint32_t st = n % kNl;
+        float nl[4];
+        int lim[4], least = 0x7fffffff;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = rb * 128 + u * 32 + lane;
+          const float x = r < p.R ? lse[r] : -INFINITY;
+          nl[u] = x == -INFINITY ? -INFINITY : -x * 1.4426950408889634f;  // a row without a key adds nothing
+          lim[u] = r < p.R ? (p.causal ? min(it.L - p.Nq + r % p.Nq, it.L - 1) : it.L - 1) : 0x7fffffff;
+          least = min(least, lim[u]);
+        }
+        least = __reduce_min_sync(0xffffffffu, least);
+        if (n >= kNl && !mbar_wait_warp(nl_empty + st, ((n / kNl) - 1) & 1, abort_flag, p.status)) { ok = false; break; }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          s_nl[st * 128 + u * 32 + lane] = nl[u];
+          s_lim[st * 128 + u * 32 + lane] = lim[u];
+        }
+        if (lane == 0) s_min[st] = least;
+        mbar_arrive_warp(nl_full + st);
+        ++n;
+      }
+    }
+  } else {
+    // ================================================================ sums
+    const int h = warp >> 2;  // key tile of the item
+    const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + h * 256;
+    const uint64_t scl = f2_pack(p.scale_log2, p.scale_log2);
+    uint32_t n = 0, ns = 0;
+    bool ok = true;
+    for (int k = 0; ok && k * G < n_items; ++k) {
+      const int idx = snake(k);
+      if (idx >= n_items) continue;
+      const Item it = item_of(p, idx);
+      if (it.key0 == 0 && it.bh % p.Hkv == 0 && threadIdx.x == 0) cache_len(p.cache_seqlens, it.bh / p.Hkv, p.Nk, p.status, true);
+      const int key = it.key0 + h * 128 + (threadIdx.x & 127);
+      const bool works = it.key0 + h * 128 < it.L;
+      const size_t at = static_cast<size_t>(it.bh) * p.Nk + key;
+      const float before = p.w_in && key < p.Nk ? p.w_in[at] : 0.f;
+      float sum = 0.f;
+      if (it.key0 < it.L) {
+        for (int rb = 0; rb < n_rb; ++rb) {
+          if (!tile_seen(p, it, rb)) continue;
+          const uint32_t st = n % kNl;
+          if (!mbar_wait_warp(nl_full + st, (n / kNl) & 1, abort_flag, p.status)) { ok = false; break; }
+          if (works) {
+            const uint32_t b = ns & 1;
+            if (!mbar_wait_warp(s_full + 2 * h + b, (ns >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
+            ++ns;
+            tc_fence_after();
+            const float* nl = s_nl + st * 128;
+            const bool mask = s_min[st] < it.key0 + h * 128 + 127;  // some row of the tile sees not all these keys
+            uint64_t acc0 = 0, acc1 = 0;  // pairs of zeros
+#pragma unroll 1
+            for (int c0 = 0; c0 < qn; c0 += 32) {
+              uint32_t r[32];
+              tmem_ld32(tl + b * 128 + c0, r);
+              tmem_ld_wait();
+              tmem_reg_fence(r);
+              if (c0 + 32 >= qn) {
+                tc_fence_before();
+                mbar_arrive_warp(s_free + 2 * h + b);  // the buffer is in registers
+              }
+              if (!mask) {
+#pragma unroll
+                for (int c = 0; c < 32; c += 4) {
+                  const float4 t4 = *reinterpret_cast<const float4*>(nl + c0 + c);
+                  const float2 x = f2_unpack(f2_fma(f2_pack(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), scl, f2_pack(t4.x, t4.y)));
+                  const float2 y = f2_unpack(f2_fma(f2_pack(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])), scl, f2_pack(t4.z, t4.w)));
+                  acc0 = f2_add(acc0, f2_pack(ex2_approx(x.x), ex2_approx(x.y)));
+                  acc1 = f2_add(acc1, f2_pack(ex2_approx(y.x), ex2_approx(y.y)));
+                }
+              } else {
+                const int* lim = s_lim + st * 128 + c0;
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                  const float x = key > lim[c] ? -INFINITY : fmaf(__uint_as_float(r[c]), p.scale_log2, nl[c0 + c]);
+                  const float y = key > lim[c + 1] ? -INFINITY : fmaf(__uint_as_float(r[c + 1]), p.scale_log2, nl[c0 + c + 1]);
+                  acc0 = f2_add(acc0, f2_pack(ex2_approx(x), ex2_approx(y)));
+                }
+              }
+            }
+            const float2 a = f2_unpack(f2_add(acc0, acc1));
+            sum += a.x + a.y;  // tile by tile: a long sum of partial sums
+          }
+          mbar_arrive_warp(nl_empty + st);
+          ++n;
+        }
+        if (!ok) break;
+      }
+      if (key < p.Nk) p.w_out[at] = before + (key < it.L ? sum : 0.f);
+    }
+  }
+  // ---- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <bool BF16, int DP>
+cudaError_t run(const CUtensorMap& q, const CUtensorMap& k, const WeightParams& p, int qn, cudaStream_t stream) {
+  // 192 KB for the rings.  Few rows: K has most of it, Q four small stages.
+  constexpr int kTileK = 128 * DP * 2, kData = 192 * 1024;
+  const int q_bytes = qn * DP * 2;
+  const int q_stages = qn > 64 ? kData / 2 / kTileK : 4;
+  const int k_stages = std::min(kMaxStages, (kData - q_stages * q_bytes) / kTileK);
+  auto kern = weights_tc_kernel<BF16, DP>;
+  static std::atomic<unsigned long long> ready{0};
+  cudaError_t e = once_per_device(ready, [&] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kData + Smem::kBytes);
+  });
+  if (e != cudaSuccess) return e;
+  const long long items = static_cast<long long>(p.B) * p.Hkv * ((p.Nk + 255) / 256);
+  const int grid = static_cast<int>(std::min<long long>(items, 152));
+  kern<<<grid, kThreads, k_stages * kTileK + q_stages * q_bytes + Smem::kBytes, stream>>>(q, k, p, static_cast<int>(items), qn, k_stages, q_stages);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_weights_tc(const CUtensorMap& q, const CUtensorMap& k, const WeightParams& p, int q_rows, attn_dtype_t dtype,
+                                    cudaStream_t stream) {
+  if (dtype == ATTN_BF16)
+    return p.d <= 64 ? run<true, 64>(q, k, p, q_rows, stream) : run<true, 128>(q, k, p, q_rows, stream);
+  return p.d <= 64 ? run<false, 64>(q, k, p, q_rows, stream) : run<false, 128>(q, k, p, q_rows, stream);
+}
+
+}  // namespace attn

@@ -207,7 +207,11 @@ struct WeightParams {
   int B, Hkv, Nq, Nk, R, d, causal;
   float scale_log2;
 };
-cudaError_t launch_cache_weights(const WeightParams& p, attn_dtype_t dtype, cudaStream_t stream);
+cudaError_t launch_cache_weights_f32(const WeightParams& p, cudaStream_t stream);
+// fp16 / bf16: maps {d, R, B*Hkv} with boxes of q_rows rows (32, 64, 96 or 128: what R needs) and
+// {d, Nk, B*Hkv} with boxes of 128.
+cudaError_t launch_cache_weights_tc(const CUtensorMap& q, const CUtensorMap& k, const WeightParams& p, int q_rows, attn_dtype_t dtype,
+                                    cudaStream_t stream);
 
 struct EvictParams {
   const void* k;           // [B*Hkv, Nk, d]
