@@ -854,7 +854,9 @@ attn_status_t attn_kvcache_weights(const void* q, const void* k_cache, const flo
   p.causal = causal != 0;
   p.scale_log2 = resolve_scale(scale, d) * kLog2e;
   if (dtype == ATTN_F32) return from_cuda(attn::launch_cache_weights_f32(p, s));
-  const int q_rows = R >= 128 ? 128 : static_cast<int>((R + 31) / 32 * 32);
+  // Q tiles of up to 128 rows, in steps of 32, as even as R allows
+  const long long q_tiles = (R + 127) / 128;
+  const int q_rows = static_cast<int>(((R + q_tiles - 1) / q_tiles + 31) / 32 * 32);
   const uint64_t dims[3] = {static_cast<uint64_t>(d), static_cast<uint64_t>(R), static_cast<uint64_t>(bh)};
   const uint64_t strides[2] = {static_cast<uint64_t>(d) * 2, static_cast<uint64_t>(R) * d * 2};
   const uint32_t box[3] = {64, static_cast<uint32_t>(q_rows), 1};

@@ -3,16 +3,18 @@
 // over the rows r = (head, query) of the key's kv head that see it.
 //
 // S^T = K Q^T: a key is a TMEM lane, so its sum over the rows is one thread's sum over columns -- no
-// reduction between threads, no atomics, an order fixed by the sizes.  A work item is 256 keys of
+// reduction over threads, no atomics, an order fixed by the sizes.  A work item is 256 keys of
 // one (batch, kv head): two 128-key tiles that stay in shared memory while the rows' Q tiles
-// (128 rows; fewer when there are fewer) stream past both, which halves Q's traffic out of L2, the
-// bound of a 128-key item (32 KB of Q per 128 x 128 x 128 product).  With few rows (decode) every
-// item has one Q tile and K streams from HBM.  Items are numbered by key tile, those that the
-// most queries see first, and dealt to the CTAs in snake order.
+// (of up to 128 rows, as even as R allows) stream past both, which halves Q's traffic out of L2,
+// the bound of a 128-key item (32 KB of Q per 128 x 128 x 128 product).  With few rows (decode)
+// every item has one Q tile and K streams from HBM.  Items are numbered by key tile, those that
+// the most queries see first, and dealt to the CTAs in snake order.
 //
-// 352 threads: warps 0-3 and 4-7 sum the first and second 128 keys (tcgen05.ld, one paired FMA and
-// two ex2 per pair of scores), warp 8 issues the TMA loads, warp 9 the MMAs, warp 10 prepares the rows'
-// -LSE log2(e) and last visible keys.  TMEM: two S^T buffers of 128 columns per key tile.
+// 640 threads: sixteen warps of sums, four for each of the two key tiles and each of its two S^T
+// buffers (tcgen05.ld, one paired FMA and two ex2 per pair of scores; two warps per scheduler left
+// it idle half the time); then a warp for the TMA loads, one MMA issuer per key tile, on two
+// sub-partitions (one thread issues 16 of them in about 1700 cycles, more than they take), and one
+// that prepares the rows' -LSE log2(e) and last visible keys.  TMEM: 2 x 2 buffers of 128 columns.
 #include <algorithm>
 #include <atomic>
 #include "cache8.cuh"
@@ -20,17 +22,19 @@
 namespace attn {
 namespace {
 
-constexpr int kThreads = 352;
+constexpr int kThreads = 640;
 constexpr int kMaxStages = 12;  // of either ring
-constexpr int kNl = 4;          // stages of row terms
+constexpr int kNl = 4;          // stages of row terms; even: a stage is read by the groups of one buffer
 
 // Shared memory: the K ring (128-key tiles), the Q ring, then the fixed part.
 struct Smem {
-  static constexpr int kNlOff = 0;                                 // [kNl][128] float
-  static constexpr int kLimOff = kNlOff + kNl * 512;               // [kNl][128] int
-  static constexpr int kMinOff = kLimOff + kNl * 512;              // [kNl] int: the least of them
-  static constexpr int kBarOff = kMinOff + kNl * 4;                // k_full, k_empty, q_full, q_empty [12]; nl_full, nl_empty [4]; s_full, s_free [2][2]; drain
-  static constexpr int kMiscOff = kBarOff + (4 * kMaxStages + 2 * kNl + 8 + 1) * 8;  // tmem base, abort flag, wait limit
+  static constexpr int kNlOff = 0;                 // [kNl][128] float
+  static constexpr int kLimOff = kNlOff + kNl * 512;   // [kNl][128] int
+  static constexpr int kMinOff = kLimOff + kNl * 512;  // [kNl] int: the least of them
+  static constexpr int kSumOff = kMinOff + kNl * 4;    // [2][128] float: one buffer's sums for the other's warps
+  // k_full, k_empty, q_full, q_empty [12]; nl_full, nl_empty [4]; s_full, s_free [2][2]; sum_full, sum_free [2]; drain [2]
+  static constexpr int kBarOff = kSumOff + 2 * 512;
+  static constexpr int kMiscOff = kBarOff + (4 * kMaxStages + 2 * kNl + 8 + 4 + 2) * 8;  // tmem base, abort flag, wait limit
   static constexpr int kBytes = kMiscOff + 16;
 };
 
@@ -52,9 +56,15 @@ __device__ __forceinline__ Item item_of(const WeightParams& p, int idx) {
   return it;
 }
 
-// Does any row of Q tile rb see a key of the item?
-__device__ __forceinline__ bool tile_seen(const WeightParams& p, const Item& it, int rb) {
-  return kv_needed_keys(it.L, p.Nq, p.R, rb, p.causal != 0) > it.key0;
+// The first Q tile from rb on with a row that sees a key of the item (or a number past the last): under
+// the causal mask the rows of queries i >= key0 - (L - Nq) of each head.
+__device__ __forceinline__ int seen_tile(const WeightParams& p, const Item& it, int rb, int qn) {
+  const int least = it.key0 - (it.L - p.Nq);
+  if (!p.causal || least <= 0) return rb;
+  const int r0 = rb * qn;
+  if (r0 >= p.R) return rb;
+  const int head = r0 / p.Nq * p.Nq;
+  return r0 - head >= least ? rb : (head + least) / qn;
 }
 
 template <bool BF16, int DP>
@@ -83,7 +93,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* const nl_empty = nl_full + kNl;
   uint64_t* const s_full = nl_empty + kNl;  // [key tile][buffer]
   uint64_t* const s_free = s_full + 4;
-  uint64_t* const drain = s_free + 4;
+  uint64_t* const sum_full = s_free + 4;  // [key tile]
+  uint64_t* const sum_free = sum_full + 2;
+  uint64_t* const drain = sum_free + 2;
+  float* const s_sum = reinterpret_cast<float*>(fixed + Smem::kSumOff);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(fixed + Smem::kMiscOff);
   const uint32_t abort_flag = smem_u32(fixed + Smem::kMiscOff + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -92,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(k_full + i, 1);
       mbar_init(k_empty + i, 1);
       mbar_init(q_full + i, 1);
-      mbar_init(q_empty + i, 1);
+      mbar_init(q_empty + i, 2);  // both issuers
     }
     for (int i = 0; i < kNl; ++i) {
       mbar_init(nl_full + i, 1);
@@ -102,20 +115,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(s_full + i, 1);
       mbar_init(s_free + i, 4);
     }
-    mbar_init(drain, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(sum_full + i, 4);
+      mbar_init(sum_free + i, 4);
+      mbar_init(drain + i, 1);
+    }
     abort_set(abort_flag, 0);
     wait_limit_set(abort_flag, p.wait_ns);
     mbar_init_fence();
   }
-  if (warp == 8) tmem_alloc(tmem_slot, 512);
+  if (warp == 16) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int n_rb = (p.R + 127) / 128;
+  const int n_rb = (p.R + qn - 1) / qn;
   const int G = gridDim.x;
 
-  if (warp == 8) {
+  if (warp == 16) {
     // ================================================================ TMA producer
     if (lane == 0) {
       tma_prefetch_desc(&tmQ);
@@ -127,24 +144,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (idx >= n_items) continue;
         const Item it = item_of(p, idx);
         if (it.key0 >= it.L) continue;
-        bool first = true;
-        for (int rb = 0; ok && rb < n_rb; ++rb) {
-          if (!tile_seen(p, it, rb)) continue;
-          if (first) {  // the item's key tiles, if any row sees it
-            first = false;
-            for (int h = 0; h < 2 && it.key0 + 128 * h < it.L; ++h, ++nk) {
-              const uint32_t st = nk % k_stages;
-              if (nk >= static_cast<uint32_t>(k_stages) && !mbar_wait(k_empty + st, ((nk / k_stages) - 1) & 1, abort_flag, p.status)) { ok = false; break; }
-              mbar_expect_tx(k_full + st, kTileK);
-              for (int c = 0; c < kChunks; ++c)
-                tma_load_3d(sK + st * kTileK + c * 128 * 128, &tmK, k_full + st, c * 64, it.key0 + 128 * h, it.bh);
-            }
-            if (!ok) break;
-          }
+        int rb = seen_tile(p, it, 0, qn);
+        if (rb >= n_rb) continue;
+        for (int h = 0; ok && h < 2 && it.key0 + 128 * h < it.L; ++h) {
+          const uint32_t st = nk % k_stages;
+          if (nk >= static_cast<uint32_t>(k_stages) && !mbar_wait(k_empty + st, ((nk / k_stages) - 1) & 1, abort_flag, p.status)) { ok = false; break; }
+          mbar_expect_tx(k_full + st, kTileK);
+          for (int c = 0; c < kChunks; ++c)
+            tma_load_3d(sK + st * kTileK + c * 128 * 128, &tmK, k_full + st, c * 64, it.key0 + 128 * h, it.bh);
+          ++nk;
+        }
+        for (; ok && rb < n_rb; rb = seen_tile(p, it, rb + 1, qn)) {
           const uint32_t st = nq % q_stages;
           if (nq >= static_cast<uint32_t>(q_stages) && !mbar_wait(q_empty + st, ((nq / q_stages) - 1) & 1, abort_flag, p.status)) { ok = false; break; }
           mbar_expect_tx(q_full + st, q_bytes);
-          for (int c = 0; c < kChunks; ++c) tma_load_3d(sQ + st * q_bytes + c * qn * 128, &tmQ, q_full + st, c * 64, rb * 128, it.bh);
+          for (int c = 0; c < kChunks; ++c) tma_load_3d(sQ + st * q_bytes + c * qn * 128, &tmQ, q_full + st, c * 64, rb * qn, it.bh);
           ++nq;
         }
       }
@@ -154,57 +168,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 9) {
-    // ================================================================ MMA issuer
+  } else if (warp == 17 || warp == 18) {
+    // ================================================================ MMA issuers, one per key tile
     if (lane == 0) {
+      const int h = warp - 17;
       const uint32_t id = idesc_f16(BF16, false, false, 128, qn);
       const uint64_t dK = smem_desc_sw128(smem_u32(sK), 16, 1024), dQ = smem_desc_sw128(smem_u32(sQ), 16, 1024);
-      uint32_t nk = 0, nq = 0, ns[2] = {0, 0};
+      uint32_t nk = 0, nq = 0, ns[2] = {0, 0};  // K and Q tiles passed; tiles put into either buffer
       bool ok = true;
       for (int k = 0; ok && k * G < n_items; ++k) {
         const int idx = snake(k);
         if (idx >= n_items) continue;
         const Item it = item_of(p, idx);
         if (it.key0 >= it.L) continue;
+        int rb = seen_tile(p, it, 0, qn);
+        if (rb >= n_rb) continue;
         const int halves = it.key0 + 128 < it.L ? 2 : 1;
-        bool first = true;
-        for (int rb = 0; ok && rb < n_rb; ++rb) {
-          if (!tile_seen(p, it, rb)) continue;
-          const uint32_t qs = nq % q_stages;
+        const uint32_t ks = (nk + h) % k_stages;
+        if (h < halves && !mbar_wait(k_full + ks, ((nk + h) / k_stages) & 1, abort_flag, p.status)) { ok = false; break; }
+        for (; rb < n_rb; rb = seen_tile(p, it, rb + 1, qn), ++nq) {
+          const uint32_t qs = nq % q_stages, b = nq & 1;
           if (!mbar_wait(q_full + qs, (nq / q_stages) & 1, abort_flag, p.status)) { ok = false; break; }
-          for (int h = 0; h < halves; ++h) {
-            const uint32_t ks = (nk + h) % k_stages, b = ns[h] & 1;
-            if ((first && !mbar_wait(k_full + ks, ((nk + h) / k_stages) & 1, abort_flag, p.status)) ||
-                (ns[h] >= 2 && !mbar_wait(s_free + 2 * h + b, ((ns[h] >> 1) - 1) & 1, abort_flag, p.status))) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint64_t kx = dK + ((ks * kTileK) >> 4), qx = dQ + ((qs * q_bytes) >> 4);
-#pragma unroll
-            for (int s = 0; s < DP / 16; ++s)
-              mma_ss(tmem + h * 256 + b * 128, kx + (((s >> 2) * 128 * 128 + (s & 3) * 32) >> 4),
-                     qx + (((s >> 2) * qn * 128 + (s & 3) * 32) >> 4), id, s > 0 ? 1u : 0u);
-            mma_commit(s_full + 2 * h + b);
-            ++ns[h];
+          if (h >= halves) {  // no keys of this tile: its share of the Q stage is done
+            mbar_arrive(q_empty + qs);
+            continue;
           }
-          if (!ok) break;
+          if (ns[b] > 0 && !mbar_wait(s_free + 2 * h + b, (ns[b] - 1) & 1, abort_flag, p.status)) { ok = false; break; }
+          ++ns[b];
+          tc_fence_after();
+          const uint64_t kx = dK + ((ks * kTileK) >> 4), qx = dQ + ((qs * q_bytes) >> 4);
+#pragma unroll
+          for (int s = 0; s < DP / 16; ++s)
+            mma_ss(tmem + h * 256 + b * 128, kx + (((s >> 2) * 128 * 128 + (s & 3) * 32) >> 4),
+                   qx + (((s >> 2) * qn * 128 + (s & 3) * 32) >> 4), id, s > 0 ? 1u : 0u);
+          mma_commit(s_full + 2 * h + b);
           mma_commit(q_empty + qs);
-          ++nq;
-          first = false;
         }
-        if (ok && !first) {
-          for (int h = 0; h < halves; ++h) mma_commit(k_empty + (nk + h) % k_stages);
-          nk += halves;
-        }
+        if (!ok) break;
+        if (h < halves) mma_commit(k_empty + ks);
+        nk += halves;
       }
       if (!ok) {
-        mma_commit(drain);  // every MMA issued completes before this arrives
-        mbar_drain(drain, 0);
+        mma_commit(drain + h);  // every MMA issued completes before this arrives
+        mbar_drain(drain + h, 0);
       }
     }
     __syncwarp();
-  } else if (warp == 10) {
+  } else if (warp == 19) {
     // ================================================================ row terms
     uint32_t n = 0;
     bool ok = true;
@@ -214,17 +224,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Item it = item_of(p, idx);
       if (it.key0 >= it.L) continue;
       const float* lse = p.lse + static_cast<size_t>(it.bh) * p.R;
-      for (int rb = 0; rb < n_rb; ++rb) {
-        if (!tile_seen(p, it, rb)) continue;
+      for (int rb = seen_tile(p, it, 0, qn); rb < n_rb; rb = seen_tile(p, it, rb + 1, qn), ++n) {
         const uint32_t st = n % kNl;
         float nl[4];
         int lim[4], least = 0x7fffffff;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int r = rb * 128 + u * 32 + lane;
-          const float x = r < p.R ? lse[r] : -INFINITY;
+          const int c = u * 32 + lane, r = rb * qn + c;
+          const bool in = c < qn && r < p.R;
+          const float x = in ? lse[r] : -INFINITY;
           nl[u] = x == -INFINITY ? -INFINITY : -x * 1.4426950408889634f;  // a row without a key adds nothing
-          lim[u] = r < p.R ? (p.causal ? min(it.L - p.Nq + r % p.Nq, it.L - 1) : it.L - 1) : 0x7fffffff;
+          lim[u] = in ? (p.causal ? min(it.L - p.Nq + r % p.Nq, it.L - 1) : it.L - 1) : 0x7fffffff;
           least = min(least, lim[u]);
         }
         least = __reduce_min_sync(0xffffffffu, least);
@@ -236,34 +246,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) s_min[st] = least;
         mbar_arrive_warp(nl_full + st);
-        ++n;
       }
     }
   } else {
     // ================================================================ sums
-    const int h = warp >> 2;  // key tile of the item
-    const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + h * 256;
+    const int h = warp >> 3, b = (warp >> 2) & 1;  // key tile of the item, S^T buffer
+    const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + h * 256 + b * 128;
     const uint64_t scl = f2_pack(p.scale_log2, p.scale_log2);
-    uint32_t n = 0, ns = 0;
+    uint32_t n = 0, ns = 0, joins = 0;  // Q tiles passed, tiles summed, sums joined
     bool ok = true;
     for (int k = 0; ok && k * G < n_items; ++k) {
       const int idx = snake(k);
       if (idx >= n_items) continue;
       const Item it = item_of(p, idx);
-      if (it.key0 == 0 && it.bh % p.Hkv == 0 && threadIdx.x == 0) cache_len(p.cache_seqlens, it.bh / p.Hkv, p.Nk, p.status, true);
       const int key = it.key0 + h * 128 + (threadIdx.x & 127);
-      const bool works = it.key0 + h * 128 < it.L;
       const size_t at = static_cast<size_t>(it.bh) * p.Nk + key;
-      const float before = p.w_in && key < p.Nk ? p.w_in[at] : 0.f;
+      // the group of the item's first Q tile writes
+      const bool writes = static_cast<int>(n & 1) == b;
+      float before = 0.f;
+      if (writes && p.w_in && key < p.Nk) before = p.w_in[at];
+      if (it.key0 == 0 && it.bh % p.Hkv == 0 && threadIdx.x == 0) cache_len(p.cache_seqlens, it.bh / p.Hkv, p.Nk, p.status, true);
+      const bool works = it.key0 + h * 128 < it.L;
       float sum = 0.f;
+      int tiles = 0;
       if (it.key0 < it.L) {
-        for (int rb = 0; rb < n_rb; ++rb) {
-          if (!tile_seen(p, it, rb)) continue;
+        for (int rb = seen_tile(p, it, 0, qn); rb < n_rb; rb = seen_tile(p, it, rb + 1, qn), ++n) {
+          ++tiles;
+          if (static_cast<int>(n & 1) != b) continue;
           const uint32_t st = n % kNl;
           if (!mbar_wait_warp(nl_full + st, (n / kNl) & 1, abort_flag, p.status)) { ok = false; break; }
           if (works) {
-            const uint32_t b = ns & 1;
-            if (!mbar_wait_warp(s_full + 2 * h + b, (ns >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
+            if (!mbar_wait_warp(s_full + 2 * h + b, ns & 1, abort_flag, p.status)) { ok = false; break; }
             ++ns;
             tc_fence_after();
             const float* nl = s_nl + st * 128;
@@ -272,47 +285,62 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int c0 = 0; c0 < qn; c0 += 32) {
               uint32_t r[32];
-              tmem_ld32(tl + b * 128 + c0, r);
+              tmem_ld32(tl + c0, r);
               tmem_ld_wait();
               tmem_reg_fence(r);
               if (c0 + 32 >= qn) {
                 tc_fence_before();
                 mbar_arrive_warp(s_free + 2 * h + b);  // the buffer is in registers
               }
-              if (!mask) {
-#pragma unroll
-                for (int c = 0; c < 32; c += 4) {
-                  const float4 t4 = *reinterpret_cast<const float4*>(nl + c0 + c);
-                  const float2 x = f2_unpack(f2_fma(f2_pack(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), scl, f2_pack(t4.x, t4.y)));
-                  const float2 y = f2_unpack(f2_fma(f2_pack(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])), scl, f2_pack(t4.z, t4.w)));
-                  acc0 = f2_add(acc0, f2_pack(ex2_approx(x.x), ex2_approx(x.y)));
-                  acc1 = f2_add(acc1, f2_pack(ex2_approx(y.x), ex2_approx(y.y)));
-                }
-              } else {
+              if (mask) {
                 const int* lim = s_lim + st * 128 + c0;
 #pragma unroll
-                for (int c = 0; c < 32; c += 2) {
-                  const float x = key > lim[c] ? -INFINITY : fmaf(__uint_as_float(r[c]), p.scale_log2, nl[c0 + c]);
-                  const float y = key > lim[c + 1] ? -INFINITY : fmaf(__uint_as_float(r[c + 1]), p.scale_log2, nl[c0 + c + 1]);
-                  acc0 = f2_add(acc0, f2_pack(ex2_approx(x), ex2_approx(y)));
+                for (int c = 0; c < 32; c += 4) {  // a score of -inf adds nothing
+                  const int4 l4 = *reinterpret_cast<const int4*>(lim + c);
+                  if (key > l4.x) r[c] = 0xff800000u;
+                  if (key > l4.y) r[c + 1] = 0xff800000u;
+                  if (key > l4.z) r[c + 2] = 0xff800000u;
+                  if (key > l4.w) r[c + 3] = 0xff800000u;
                 }
+              }
+#pragma unroll
+              for (int c = 0; c < 32; c += 4) {
+                const float4 t4 = *reinterpret_cast<const float4*>(nl + c0 + c);
+                const float2 x = f2_unpack(f2_fma(f2_pack(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), scl, f2_pack(t4.x, t4.y)));
+                const float2 y = f2_unpack(f2_fma(f2_pack(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])), scl, f2_pack(t4.z, t4.w)));
+                acc0 = f2_add(acc0, f2_pack(ex2_approx(x.x), ex2_approx(x.y)));
+                acc1 = f2_add(acc1, f2_pack(ex2_approx(y.x), ex2_approx(y.y)));
               }
             }
             const float2 a = f2_unpack(f2_add(acc0, acc1));
             sum += a.x + a.y;  // tile by tile: a long sum of partial sums
           }
           mbar_arrive_warp(nl_empty + st);
-          ++n;
         }
         if (!ok) break;
       }
-      if (key < p.Nk) p.w_out[at] = before + (key < it.L ? sum : 0.f);
+      if (tiles > 1) {  // the other buffer's tiles
+        float* const other = s_sum + h * 128 + (threadIdx.x & 127);
+        if (!writes) {
+          if (joins > 0 && !mbar_wait_warp(sum_free + h, (joins - 1) & 1, abort_flag, p.status)) { ok = false; break; }
+          *other = sum;
+          mbar_arrive_warp(sum_full + h);
+        }
+        // both groups wait here, so that no warp can be a phase ahead when they change places
+        if (!mbar_wait_warp(sum_full + h, joins & 1, abort_flag, p.status)) { ok = false; break; }
+        if (writes) {
+          sum += *other;
+          mbar_arrive_warp(sum_free + h);
+        }
+        ++joins;
+      }
+      if (writes && key < p.Nk) p.w_out[at] = before + (key < it.L ? sum : 0.f);
     }
   }
   // ---- teardown
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 16) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
