@@ -10,19 +10,22 @@
 // every item has one Q tile and K streams from HBM.  Items are numbered by key tile, those that
 // the most queries see first, and dealt to the CTAs in snake order.
 //
-// 640 threads: sixteen warps of sums, four for each of the two key tiles and each of its two S^T
-// buffers (tcgen05.ld, one paired FMA and two ex2 per pair of scores; two warps per scheduler left
-// it idle half the time); then a warp for the TMA loads, one MMA issuer per key tile, on two
-// sub-partitions (one thread issues 16 of them in about 1700 cycles, more than they take), and one
-// that prepares the rows' -LSE log2(e) and last visible keys.  TMEM: 2 x 2 buffers of 128 columns.
+// 640 threads: sixteen warps that sum (tcgen05.ld, one paired FMA and two ex2 per pair of scores), four
+// for each key tile and each of its two S^T buffers of 128 columns, the buffers taken in turn;
+// then a warp for the TMA loads, one MMA issuer per key tile, on two sub-partitions (one thread
+// issues 16 of them in about 1700 cycles, more than they take), and one that prepares the rows'
+// -LSE log2(e) and last visible keys.  Measured on 2048-token prompts (B = 4, 32 over 8 heads,
+// d = 128): eight summing warps and one issuer 160 us without and 116 us with the causal mask, as
+// here 131 and 86; eight warps that take a whole tile into registers first 149 and 92; two groups
+// that halve every tile's columns 135 and 90; loads of 32 columns ahead of the sums 162 and 102.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 #include "cache8.cuh"
 
 namespace attn {
 namespace {
 
-constexpr int kThreads = 640;
 constexpr int kMaxStages = 12;  // of either ring
 constexpr int kNl = 4;          // stages of row terms; even: a stage is read by the groups of one buffer
 
@@ -67,8 +70,9 @@ __device__ __forceinline__ int seen_tile(const WeightParams& p, const Item& it, 
   return r0 - head >= least ? rb : (head + least) / qn;
 }
 
-template <bool BF16, int DP>
-__global__ void __launch_bounds__(kThreads, 1)
+// FEW: one Q tile per item, so the sets of summing warps take the items in turn and join no sums.
+template <bool BF16, int DP, bool FEW>
+__global__ void __launch_bounds__(640, 1)
     weights_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, const WeightParams p,
                       int n_items, int qn, int k_stages, int q_stages) {
   constexpr int kChunks = DP / 64;
@@ -99,6 +103,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* const s_sum = reinterpret_cast<float*>(fixed + Smem::kSumOff);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(fixed + Smem::kMiscOff);
   const uint32_t abort_flag = smem_u32(fixed + Smem::kMiscOff + 4);
+  constexpr int kSums = 16;  // summing warps
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
@@ -124,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     wait_limit_set(abort_flag, p.wait_ns);
     mbar_init_fence();
   }
-  if (warp == 16) tmem_alloc(tmem_slot, 512);
+  if (warp == kSums) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -132,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_rb = (p.R + qn - 1) / qn;
   const int G = gridDim.x;
 
-  if (warp == 16) {
+  if (warp == kSums) {
     // ================================================================ TMA producer
     if (lane == 0) {
       tma_prefetch_desc(&tmQ);
@@ -168,13 +173,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 17 || warp == 18) {
+  } else if (warp == kSums + 1 || warp == kSums + 2) {
     // ================================================================ MMA issuers, one per key tile
     if (lane == 0) {
-      const int h = warp - 17;
+      const int h = warp - kSums - 1;
       const uint32_t id = idesc_f16(BF16, false, false, 128, qn);
       const uint64_t dK = smem_desc_sw128(smem_u32(sK), 16, 1024), dQ = smem_desc_sw128(smem_u32(sQ), 16, 1024);
-      uint32_t nk = 0, nq = 0, ns[2] = {0, 0};  // K and Q tiles passed; tiles put into either buffer
+      uint32_t nk = 0, nq = 0, ns0 = 0, ns1 = 0;  // K and Q tiles passed; tiles put into either buffer
       bool ok = true;
       for (int k = 0; ok && k * G < n_items; ++k) {
         const int idx = snake(k);
@@ -193,8 +198,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(q_empty + qs);
             continue;
           }
-          if (ns[b] > 0 && !mbar_wait(s_free + 2 * h + b, (ns[b] - 1) & 1, abort_flag, p.status)) { ok = false; break; }
-          ++ns[b];
+          const uint32_t ns = b ? ns1 : ns0;
+          if (ns > 0 && !mbar_wait(s_free + 2 * h + b, (ns - 1) & 1, abort_flag, p.status)) { ok = false; break; }
+          ns0 += 1 - b;
+          ns1 += b;
           tc_fence_after();
           const uint64_t kx = dK + ((ks * kTileK) >> 4), qx = dQ + ((qs * q_bytes) >> 4);
 #pragma unroll
@@ -214,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 19) {
+  } else if (warp == kSums + 3) {
     // ================================================================ row terms
     uint32_t n = 0;
     bool ok = true;
@@ -250,8 +257,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ================================================================ sums
-    const int h = warp >> 3, b = (warp >> 2) & 1;  // key tile of the item, S^T buffer
-    const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + h * 256 + b * 128;
+    const int h = warp >> 3;             // key tile of the item
+    const uint32_t mine = (warp >> 2) & 1;       // FEW: the buffer of this set
+    const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + h * 256;
     const uint64_t scl = f2_pack(p.scale_log2, p.scale_log2);
     uint32_t n = 0, ns = 0, joins = 0;  // Q tiles passed, tiles summed, sums joined
     bool ok = true;
@@ -261,42 +269,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Item it = item_of(p, idx);
       const int key = it.key0 + h * 128 + (threadIdx.x & 127);
       const size_t at = static_cast<size_t>(it.bh) * p.Nk + key;
-      // the group of the item's first Q tile writes
-      const bool writes = static_cast<int>(n & 1) == b;
+      const bool writes = (n & 1) == mine;  // the set that has the item's first Q tile
+      int tiles = 0;
       float before = 0.f;
       if (writes && p.w_in && key < p.Nk) before = p.w_in[at];
       if (it.key0 == 0 && it.bh % p.Hkv == 0 && threadIdx.x == 0) cache_len(p.cache_seqlens, it.bh / p.Hkv, p.Nk, p.status, true);
       const bool works = it.key0 + h * 128 < it.L;
       float sum = 0.f;
-      int tiles = 0;
       if (it.key0 < it.L) {
         for (int rb = seen_tile(p, it, 0, qn); rb < n_rb; rb = seen_tile(p, it, rb + 1, qn), ++n) {
+          const uint32_t b = n & 1, st = n % kNl;
           ++tiles;
-          if (static_cast<int>(n & 1) != b) continue;
-          const uint32_t st = n % kNl;
+          if (b != mine) continue;
           if (!mbar_wait_warp(nl_full + st, (n / kNl) & 1, abort_flag, p.status)) { ok = false; break; }
           if (works) {
             if (!mbar_wait_warp(s_full + 2 * h + b, ns & 1, abort_flag, p.status)) { ok = false; break; }
             ++ns;
             tc_fence_after();
             const float* nl = s_nl + st * 128;
+            const int* lim = s_lim + st * 128;
             const bool mask = s_min[st] < it.key0 + h * 128 + 127;  // some row of the tile sees not all these keys
             uint64_t acc0 = 0, acc1 = 0;  // pairs of zeros
-#pragma unroll 1
-            for (int c0 = 0; c0 < qn; c0 += 32) {
-              uint32_t r[32];
-              tmem_ld32(tl + c0, r);
-              tmem_ld_wait();
-              tmem_reg_fence(r);
-              if (c0 + 32 >= qn) {
-                tc_fence_before();
-                mbar_arrive_warp(s_free + 2 * h + b);  // the buffer is in registers
-              }
+            auto add = [&](uint32_t (&r)[32], int c0) {
               if (mask) {
-                const int* lim = s_lim + st * 128 + c0;
 #pragma unroll
                 for (int c = 0; c < 32; c += 4) {  // a score of -inf adds nothing
-                  const int4 l4 = *reinterpret_cast<const int4*>(lim + c);
+                  const int4 l4 = *reinterpret_cast<const int4*>(lim + c0 + c);
                   if (key > l4.x) r[c] = 0xff800000u;
                   if (key > l4.y) r[c + 1] = 0xff800000u;
                   if (key > l4.z) r[c + 2] = 0xff800000u;
@@ -311,6 +309,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 acc0 = f2_add(acc0, f2_pack(ex2_approx(x.x), ex2_approx(x.y)));
                 acc1 = f2_add(acc1, f2_pack(ex2_approx(y.x), ex2_approx(y.y)));
               }
+            };
+#pragma unroll 1
+            for (int c0 = 0; c0 < qn; c0 += 32) {
+              uint32_t r[32];
+              tmem_ld32(tl + b * 128 + c0, r);
+              tmem_ld_wait();
+              tmem_reg_fence(r);
+              if (c0 + 32 >= qn) {
+                tc_fence_before();
+                mbar_arrive_warp(s_free + 2 * h + b);  // the buffer is in registers
+              }
+              add(r, c0);
             }
             const float2 a = f2_unpack(f2_add(acc0, acc1));
             sum += a.x + a.y;  // tile by tile: a long sum of partial sums
@@ -319,14 +329,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
       }
-      if (tiles > 1) {  // the other buffer's tiles
+      if (!FEW && tiles > 1) {  // the other buffer's tiles
         float* const other = s_sum + h * 128 + (threadIdx.x & 127);
         if (!writes) {
           if (joins > 0 && !mbar_wait_warp(sum_free + h, (joins - 1) & 1, abort_flag, p.status)) { ok = false; break; }
           *other = sum;
           mbar_arrive_warp(sum_full + h);
         }
-        // both groups wait here, so that no warp can be a phase ahead when they change places
+        // both sets wait here, so that no warp can be a phase ahead when they change places
         if (!mbar_wait_warp(sum_full + h, joins & 1, abort_flag, p.status)) { ok = false; break; }
         if (writes) {
           sum += *other;
@@ -340,20 +350,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- teardown
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == kSums) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
 }
 
-template <bool BF16, int DP>
+template <bool BF16, int DP, bool FEW>
 cudaError_t run(const CUtensorMap& q, const CUtensorMap& k, const WeightParams& p, int qn, cudaStream_t stream) {
   // 192 KB for the rings.  Few rows: K has most of it, Q four small stages.
   constexpr int kTileK = 128 * DP * 2, kData = 192 * 1024;
   const int q_bytes = qn * DP * 2;
   const int q_stages = qn > 64 ? kData / 2 / kTileK : 4;
   const int k_stages = std::min(kMaxStages, (kData - q_stages * q_bytes) / kTileK);
-  auto kern = weights_tc_kernel<BF16, DP>;
+  auto kern = weights_tc_kernel<BF16, DP, FEW>;
   static std::atomic<unsigned long long> ready{0};
   cudaError_t e = once_per_device(ready, [&] {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kData + Smem::kBytes);
@@ -361,7 +371,7 @@ cudaError_t run(const CUtensorMap& q, const CUtensorMap& k, const WeightParams& 
   if (e != cudaSuccess) return e;
   const long long items = static_cast<long long>(p.B) * p.Hkv * ((p.Nk + 255) / 256);
   const int grid = static_cast<int>(std::min<long long>(items, 152));
-  kern<<<grid, kThreads, k_stages * kTileK + q_stages * q_bytes + Smem::kBytes, stream>>>(q, k, p, static_cast<int>(items), qn, k_stages, q_stages);
+  kern<<<grid, 640, k_stages * kTileK + q_stages * q_bytes + Smem::kBytes, stream>>>(q, k, p, static_cast<int>(items), qn, k_stages, q_stages);
   return cudaGetLastError();
 }
 
@@ -369,9 +379,13 @@ cudaError_t run(const CUtensorMap& q, const CUtensorMap& k, const WeightParams& 
 
 cudaError_t launch_cache_weights_tc(const CUtensorMap& q, const CUtensorMap& k, const WeightParams& p, int q_rows, attn_dtype_t dtype,
                                     cudaStream_t stream) {
-  if (dtype == ATTN_BF16)
-    return p.d <= 64 ? run<true, 64>(q, k, p, q_rows, stream) : run<true, 128>(q, k, p, q_rows, stream);
-  return p.d <= 64 ? run<false, 64>(q, k, p, q_rows, stream) : run<false, 128>(q, k, p, q_rows, stream);
+  const bool few = p.R <= q_rows;
+  auto pick = [&](auto bf16) {
+    constexpr bool kB = decltype(bf16)::value;
+    if (p.d <= 64) return few ? run<kB, 64, true>(q, k, p, q_rows, stream) : run<kB, 64, false>(q, k, p, q_rows, stream);
+    return few ? run<kB, 128, true>(q, k, p, q_rows, stream) : run<kB, 128, false>(q, k, p, q_rows, stream);
+  };
+  return dtype == ATTN_BF16 ? pick(std::true_type{}) : pick(std::false_type{});
 }
 
 }  // namespace attn
