@@ -882,6 +882,7 @@ attn_status_t attn_kvcache_evict(const void* k_cache, const void* v_cache, const
       !out_seqlens || !aligned(out_seqlens, 4) || !aligned(cache_seqlens, 4))
     return ATTN_ERR_INVALID_ARG;
   const size_t es = dtype == ATTN_F32 ? 4 : 2, row = static_cast<size_t>(d) * es;
+  if (bh * ((M * static_cast<long long>(row / 16) + 1023) / 1024) > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;  // the copy's grid
   const size_t in_bytes = static_cast<size_t>(bh) * Nk * row, out_bytes = static_cast<size_t>(bh) * capacity * row;
   const size_t w_bytes = static_cast<size_t>(bh) * Nk * 4, wo_bytes = static_cast<size_t>(bh) * capacity * 4;
   for (const void* out : {static_cast<const void*>(k_out), static_cast<const void*>(v_out)})

@@ -2,7 +2,9 @@
 // scale s = max |x| / top (top = 127 or 448) and codes round(x / s).
 //
 // A CTA owns one touched block of one (batch, kv head) of keys or of values: it reads the block's
-// new tokens (16 bytes per load), reduces max |x|, and writes the codes. The
+// new tokens once into registers (16 bytes per load, up to eight in flight per thread), reduces
+// max |x|, and writes the codes.  (Reading them twice, the second time from L2, took 72 us for the
+// 317 MB of four prompts of 8k to 16k tokens; now REPL_APP.) The
 // block at the cache's end may hold tokens already: its scale only grows, and when it does the
 // codes there are recoded by the same CTA, so no other CTA ever touches them. Every operation
 // is one IEEE rounding (no contraction), so codes and scales are a function of the inputs alone.
@@ -11,37 +13,54 @@
 namespace attn {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kVecs = 8;  // vectors of eight elements that a thread holds
 
-// Eight consecutive elements as floats.
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __half* p, float (&x)[8]) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    x[2 * i] = f.x; x[2 * i + 1] = f.y;
+// Eight consecutive elements as they lie in memory, and as floats.
+template <typename T>
+struct Vec8;
+template <>
+struct Vec8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
   }
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
   }
-}
+};
+template <>
+struct Vec8<__half> {
+  uint4 v;
+  __device__ __forceinline__ void load(const __half* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      x[2 * i] = f.x; x[2 * i + 1] = f.y;
+    }
+  }
+};
+template <>
+struct Vec8<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
 
 // The bits of |x|: ordered like |x|, with infinity above every number and NaN above that.
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
-template <typename T, typename Code>
+template <typename T, typename Code, int kThreads>
 __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
   __shared__ uint32_t s_max[kThreads / 32];
   const int per_bh = 2 * p.blocks_per_head;
@@ -64,10 +83,19 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
   uint8_t* const head = p.x8[side] + static_cast<size_t>(bh) * p.Nk * p.d;
   float* const scale = p.scale[side] + static_cast<size_t>(bh) * p.n_blocks + blk;
   const int nvec = (t1 - t0) * p.d / 8;  // vectors of 8 elements: rows are contiguous on both sides
+  // all of the block's new tokens at once: block * d <= 8 * kVecs * kThreads
+  Vec8<T> raw[kVecs];
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) {
+    const int i = u * kThreads + threadIdx.x;
+    if (i < nvec) raw[u].load(src + static_cast<size_t>(i) * 8);
+  }
   uint32_t mx = 0;
-  for (int i = threadIdx.x; i < nvec; i += kThreads) {
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) {
+    if (u * kThreads + static_cast<int>(threadIdx.x) >= nvec) break;
     float x[8];
-    load8(src + static_cast<size_t>(i) * 8, x);
+    raw[u].get(x);
 #pragma unroll
     for (int e = 0; e < 8; ++e) mx = max(mx, abs_bits(x[e]));
   }
@@ -84,9 +112,12 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
   if (held && !(s_old <= s) && !(s != s)) s = s_old;  // larger, or NaN: it stays
   const float inv = s == 0.f ? 0.f : __frcp_rn(s);
   uint8_t* const dst = head + static_cast<size_t>(t0) * p.d;
-  for (int i = threadIdx.x; i < nvec; i += kThreads) {
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) {
+    const int i = u * kThreads + threadIdx.x;
+    if (i >= nvec) break;
     float x[8];
-    load8(src + static_cast<size_t>(i) * 8, x);
+    raw[u].get(x);
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(x[e], inv);
     reinterpret_cast<uint2*>(dst)[i] = make_uint2(Code::encode4(x[0], x[1], x[2], x[3]), Code::encode4(x[4], x[5], x[6], x[7]));
@@ -111,10 +142,14 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
 template <typename T>
 cudaError_t run(const AppendParams& p, attn_cache_dtype_t cache, cudaStream_t stream) {
   const int grid = p.B * p.Hkv * 2 * p.blocks_per_head;
-  if (cache == ATTN_CACHE_I8)
-    append_kernel<T, CodeI8><<<grid, kThreads, 0, stream>>>(p);
-  else
-    append_kernel<T, CodeE4m3><<<grid, kThreads, 0, stream>>>(p);
+  const bool small = p.block * p.d <= 8 * kVecs * 128;
+  if (cache == ATTN_CACHE_I8) {
+    if (small) append_kernel<T, CodeI8, 128><<<grid, 128, 0, stream>>>(p);
+    else append_kernel<T, CodeI8, 256><<<grid, 256, 0, stream>>>(p);
+  } else {
+    if (small) append_kernel<T, CodeE4m3, 128><<<grid, 128, 0, stream>>>(p);
+    else append_kernel<T, CodeE4m3, 256><<<grid, 256, 0, stream>>>(p);
+  }
   return cudaGetLastError();
 }
 
