@@ -15,14 +15,12 @@ every step of the computation runs in libattn_gb300.so's kernels.
 """
 from __future__ import annotations
 
-import contextlib
 import math
 
 import torch
 
 from . import _lib
 
-_SAME = contextlib.nullcontext()  # the current device is the tensors'
 _DT8 = {torch.int8: _lib.ATTN_CACHE_I8, torch.float8_e4m3fn: _lib.ATTN_CACHE_E4M3}
 _DT = {torch.float32: _lib.ATTN_F32, torch.float16: _lib.ATTN_F16, torch.bfloat16: _lib.ATTN_BF16}
 
@@ -224,20 +222,38 @@ def fwd_kvcache(q, k_cache, v_cache, cache_seqlens=None, causal: bool = False, s
     return o, lse
 
 
-def _cache_args(first, name: str, tensors, optional=()):
-    """Checks of the cache calls: (tensor, name, dtype or None) each, contiguous and on the first
-    one's GPU."""
-    dev = first.device
-    for t, n, dtype in tensors + tuple(x for x in optional if x[0] is not None):
-        _require(t, n, dtype)
-        if t.device != dev:
-            raise ValueError(f"{n} must be on {name}'s device")
+def _cache_args(name: str, *tensors) -> int:
+    """Checks of the cache calls: (tensor, name, dtype or None) each; contiguous tensors on one
+    GPU, that of the first, called `name`.  Returns the GPU's index."""
+    try:
+        dev = tensors[0][0].get_device()
+        if dev >= 0 and all(t.get_device() == dev and t.is_contiguous() and (dtype is None or t.dtype == dtype)
+                            for t, _, dtype in tensors if t is not None):
+            return dev
+    except AttributeError:
+        pass
+    for t, n, dtype in tensors:  # say what is wrong
+        if t is not None:
+            _require(t, n, dtype)
+            if t.device != tensors[0][0].device:
+                raise ValueError(f"{n} must be on {name}'s device")
+    raise TypeError("tensors on a CUDA device are wanted")
 
 
-def _device_stream(t: torch.Tensor):
-    """(context to call in, current stream) of the tensor's device."""
-    dev = t.get_device()
-    return (_SAME if dev == torch.cuda.current_device() else torch.cuda.device(dev)), torch._C._cuda_getCurrentRawStream(dev)
+def _on_device(dev: int, call, *args) -> int:
+    """call(*args, stream) with `dev` as the current device, on its current stream."""
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if dev == torch.cuda.current_device():
+        return call(*args, stream)
+    with torch.cuda.device(dev):
+        return call(*args, stream)
+
+
+def _tensor(t):
+    """A tensor that may not be missing."""
+    if t is None:
+        raise TypeError("a tensor is wanted where None was given")
+    return t
 
 
 def _lens_ptr(t, name: str, B: int):
@@ -270,18 +286,18 @@ def kvcache8_append(k8, v8, k_scale, v_scale, k_new, v_new, cache_seqlens=None, 
     scale, 16, 32, 64 or 128."""
     _require(k8, "k8")
     _require(k_new, "k_new")
-    _cache_args(k8, "k8", ((v8, "v8", k8.dtype), (k_scale, "k_scale", torch.float32),
-                           (v_scale, "v_scale", torch.float32), (k_new, "k_new", None), (v_new, "v_new", k_new.dtype)),
-                ((cache_seqlens, "cache_seqlens", torch.int32), (new_seqlens, "new_seqlens", torch.int32)))
+    dev = _cache_args("k8", (k8, "k8", None), (v8, "v8", k8.dtype), (_tensor(k_scale), "k_scale", torch.float32),
+                      (_tensor(v_scale), "v_scale", torch.float32), (k_new, "k_new", None),
+                      (_tensor(v_new), "v_new", k_new.dtype), (cache_seqlens, "cache_seqlens", torch.int32),
+                      (new_seqlens, "new_seqlens", torch.int32))
     B, Hkv, Nk, d = _check_cache8(k8, v8, k_scale, v_scale, block)
-    if k_new.dim() != 4 or k_new.shape != v_new.shape or k_new.shape[:2] != (B, Hkv) or k_new.shape[3] != d:
+    shape = k_new.shape
+    if len(shape) != 4 or shape != v_new.shape or shape[0] != B or shape[1] != Hkv or shape[3] != d:
         raise ValueError("k_new and v_new must be [B,Hkv,Nn,d]")
-    ctx, stream = _device_stream(k8)
-    with ctx:
-        st = _lib.attn_kvcache8_append(k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                                       k_new.data_ptr(), v_new.data_ptr(), _lens_ptr(cache_seqlens, "cache_seqlens", B),
-                                       _lens_ptr(new_seqlens, "new_seqlens", B), B, Hkv, k_new.shape[2], Nk, d, block,
-                                       _dtype_code(k_new), _DT8[k8.dtype], stream)
+    st = _on_device(dev, _lib.attn_kvcache8_append, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                    k_new.data_ptr(), v_new.data_ptr(), _lens_ptr(cache_seqlens, "cache_seqlens", B),
+                    _lens_ptr(new_seqlens, "new_seqlens", B), B, Hkv, shape[2], Nk, d, block, _dtype_code(k_new),
+                    _DT8[k8.dtype])
     _lib._check(st, "attn_kvcache8_append")
 
 
@@ -294,30 +310,30 @@ def fwd_kvcache8(q, k8, v8, k_scale, v_scale, cache_seqlens=None, causal: bool =
                  out_f32: bool = False, with_lse: bool = True, workspace=None):
     """fwd_kvcache over an 8-bit cache.  q [B,Hq,Nq,d] float16 or bfloat16; k8, v8, k_scale,
     v_scale and block as kvcache8_append writes them; cache_seqlens int32 [B] on the device (None:
-    Nk tokens each).  Returns (o [B,Hq,Nq,d], lse [B,Hq,Nq] or None)."""
+    Nk tokens each).  Calls that may run at the same time need a workspace each.  Returns
+    (o [B,Hq,Nq,d], lse [B,Hq,Nq] or None)."""
     _require(q, "q")
     _require(k8, "k8")
-    _cache_args(q, "q", ((k8, "k8", None), (v8, "v8", k8.dtype), (k_scale, "k_scale", torch.float32),
-                         (v_scale, "v_scale", torch.float32)),
-                ((cache_seqlens, "cache_seqlens", torch.int32), (workspace, "workspace", None)))
+    dev = _cache_args("q", (q, "q", None), (k8, "k8", None), (_tensor(v8), "v8", k8.dtype),
+                      (_tensor(k_scale), "k_scale", torch.float32), (_tensor(v_scale), "v_scale", torch.float32),
+                      (cache_seqlens, "cache_seqlens", torch.int32), (workspace, "workspace", None))
     B, Hkv, Nk, d = _check_cache8(k8, v8, k_scale, v_scale, block)
-    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != d:
-        raise ValueError("q must be [B,Hq,Nq,d], with the cache's batch and head_dim")
-    _, Hq, Nq, _ = q.shape
-    dev = q.device
-    o = torch.empty(q.shape, dtype=torch.float32 if out_f32 else q.dtype, device=dev)
-    lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev) if with_lse else None
+    if q.dim() != 4:
+        raise ValueError("q must be [B,Hq,Nq,d]")
+    Bq, Hq, Nq, dq = q.shape
+    if Bq != B or dq != d:
+        raise ValueError("q and the cache disagree on batch or head_dim")
+    device = q.device
+    o = torch.empty_like(q, dtype=torch.float32) if out_f32 else torch.empty_like(q)
+    lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=device) if with_lse else None
     if workspace is None:
         need = _lib.attn_fwd_kvcache8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-    ctx, stream = _device_stream(q)
-    with ctx:
-        st = _lib.attn_fwd_kvcache8(q.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                                    _lens_ptr(cache_seqlens, "cache_seqlens", B), o.data_ptr(),
-                                    lse.data_ptr() if with_lse else None, workspace.data_ptr(),
-                                    workspace.numel() * workspace.element_size(), B, Hq, Hkv, Nq, Nk, d, block, causal,
-                                    _scale_arg(scale), _dtype_code(q), _DT8[k8.dtype],
-                                    _lib.ATTN_FLAG_OUT_F32 if out_f32 else 0, stream)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+    st = _on_device(dev, _lib.attn_fwd_kvcache8, q.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(),
+                    v_scale.data_ptr(), _lens_ptr(cache_seqlens, "cache_seqlens", B), o.data_ptr(),
+                    lse.data_ptr() if with_lse else None, workspace.data_ptr(), workspace.nbytes, B, Hq, Hkv, Nq, Nk, d,
+                    block, causal, _scale_arg(scale), _dtype_code(q), _DT8[k8.dtype],
+                    _lib.ATTN_FLAG_OUT_F32 if out_f32 else 0)
     _lib._check(st, "attn_fwd_kvcache8")
     return o, lse
 
@@ -329,14 +345,14 @@ def kvcache_weights(q, k_cache, lse, cache_seqlens=None, causal: bool = False, s
     weights float32 [B,Hkv,Nk]: what earlier queries added up to (None: zeros).  out: where to
     write (may be weights).  Returns float32 [B,Hkv,Nk]."""
     _require(q, "q")
-    _cache_args(q, "q", ((k_cache, "k_cache", q.dtype), (lse, "lse", torch.float32)),
-                ((cache_seqlens, "cache_seqlens", torch.int32), (weights, "weights", torch.float32),
-                 (out, "out", torch.float32)))
+    dev = _cache_args("q", (q, "q", None), (_tensor(k_cache), "k_cache", q.dtype), (_tensor(lse), "lse", torch.float32),
+                      (cache_seqlens, "cache_seqlens", torch.int32), (weights, "weights", torch.float32),
+                      (out, "out", torch.float32))
     if q.dim() != 4 or k_cache.dim() != 4:
         raise ValueError("q must be [B,Hq,Nq,d] and k_cache [B,Hkv,Nk,d]")
     B, Hq, Nq, d = q.shape
-    _, Hkv, Nk, dk = k_cache.shape
-    if k_cache.shape[0] != B or dk != d:
+    Bk, Hkv, Nk, dk = k_cache.shape
+    if Bk != B or dk != d:
         raise ValueError("q and the cache disagree on batch or head_dim")
     if lse.shape != (B, Hq, Nq):
         raise ValueError("lse must be [B,Hq,Nq]")
@@ -345,12 +361,9 @@ def kvcache_weights(q, k_cache, lse, cache_seqlens=None, causal: bool = False, s
             raise ValueError(f"{n} must be [B,Hkv,Nk]")
     if out is None:
         out = torch.empty((B, Hkv, Nk), dtype=torch.float32, device=q.device)
-    ctx, stream = _device_stream(q)
-    with ctx:
-        st = _lib.attn_kvcache_weights(q.data_ptr(), k_cache.data_ptr(), lse.data_ptr(),
-                                       _lens_ptr(cache_seqlens, "cache_seqlens", B),
-                                       weights.data_ptr() if weights is not None else None, out.data_ptr(), B, Hq, Hkv,
-                                       Nq, Nk, d, causal, _scale_arg(scale), _dtype_code(q), stream)
+    st = _on_device(dev, _lib.attn_kvcache_weights, q.data_ptr(), k_cache.data_ptr(), lse.data_ptr(),
+                    _lens_ptr(cache_seqlens, "cache_seqlens", B), None if weights is None else weights.data_ptr(),
+                    out.data_ptr(), B, Hq, Hkv, Nq, Nk, d, causal, _scale_arg(scale), _dtype_code(q))
     _lib._check(st, "attn_kvcache_weights")
     return out
 
@@ -365,33 +378,32 @@ def kvcache_evict(k_cache, v_cache, weights, keep: int, recent: int, cache_seqle
     [B,Hkv,capacity], index int32 [B,Hkv,keep+recent] with -1 past the kept keys, lengths int32
     [B])."""
     _require(k_cache, "k_cache")
-    _cache_args(k_cache, "k_cache", ((v_cache, "v_cache", k_cache.dtype), (weights, "weights", torch.float32)),
-                ((cache_seqlens, "cache_seqlens", torch.int32),))
-    dev = k_cache.device
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or weights.shape != k_cache.shape[:3]:
-        raise ValueError("k_cache and v_cache must be [B,Hkv,Nk,d] and weights [B,Hkv,Nk]")
-    B, Hkv, Nk, d = k_cache.shape
     keep, recent = int(keep), int(recent)
     if keep < 0 or recent < 0 or keep + recent < 1:
         raise ValueError("keep and recent must not be negative, nor both zero")
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache and v_cache must be [B,Hkv,Nk,d]")
+    B, Hkv, Nk, d = k_cache.shape
+    device = k_cache.device
     if out is None:
-        out = tuple(torch.zeros((B, Hkv, keep + recent, d), dtype=k_cache.dtype, device=dev) for _ in range(2))
+        out = tuple(torch.zeros((B, Hkv, keep + recent, d), dtype=k_cache.dtype, device=device) for _ in range(2))
     k_out, v_out = out
-    _cache_args(k_cache, "k_cache", ((k_out, "k_out", k_cache.dtype), (v_out, "v_out", k_cache.dtype)))
+    dev = _cache_args("k_cache", (k_cache, "k_cache", None), (_tensor(v_cache), "v_cache", k_cache.dtype),
+                      (_tensor(weights), "weights", torch.float32), (_tensor(k_out), "k_out", k_cache.dtype),
+                      (_tensor(v_out), "v_out", k_cache.dtype), (cache_seqlens, "cache_seqlens", torch.int32))
+    if v_cache.shape != k_cache.shape or weights.shape != (B, Hkv, Nk):
+        raise ValueError("k_cache and v_cache must be [B,Hkv,Nk,d] and weights [B,Hkv,Nk]")
     if k_out.dim() != 4 or k_out.shape != v_out.shape or k_out.shape[:2] != (B, Hkv) or k_out.shape[3] != d:
         raise ValueError("k_out and v_out must be [B,Hkv,capacity,d]")
     cap = k_out.shape[2]
     if cap < keep + recent:
         raise ValueError("the capacity of k_out and v_out must be at least keep + recent")
-    w_out = torch.empty((B, Hkv, cap), dtype=torch.float32, device=dev)
-    index = torch.empty((B, Hkv, keep + recent), dtype=torch.int32, device=dev)
-    lens = torch.empty((B,), dtype=torch.int32, device=dev)
-    ctx, stream = _device_stream(k_cache)
-    with ctx:
-        st = _lib.attn_kvcache_evict(k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(),
-                                     _lens_ptr(cache_seqlens, "cache_seqlens", B), k_out.data_ptr(), v_out.data_ptr(),
-                                     w_out.data_ptr(), index.data_ptr(), lens.data_ptr(), B, Hkv, Nk, cap, d, keep,
-                                     recent, _dtype_code(k_cache), stream)
+    w_out = torch.empty((B, Hkv, cap), dtype=torch.float32, device=device)
+    index = torch.empty((B, Hkv, keep + recent), dtype=torch.int32, device=device)
+    lens = torch.empty((B,), dtype=torch.int32, device=device)
+    st = _on_device(dev, _lib.attn_kvcache_evict, k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(),
+                    _lens_ptr(cache_seqlens, "cache_seqlens", B), k_out.data_ptr(), v_out.data_ptr(), w_out.data_ptr(),
+                    index.data_ptr(), lens.data_ptr(), B, Hkv, Nk, cap, d, keep, recent, _dtype_code(k_cache))
     _lib._check(st, "attn_kvcache_evict")
     return k_out, v_out, w_out, index, lens
 
