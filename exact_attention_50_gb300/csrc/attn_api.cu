@@ -659,17 +659,18 @@ Cache8Plan cache8_plan(int B, int Hkv, int R, int Nk, int d) {
 }
 
 // Many rows: the key ranges, one as soon as the row blocks fill the GPU twice (a second pass over the
-// fp32 parts costs more than the last wave's idle SMs), and the workspace: the expanded K and V,
-// then the ranges' parts.
+// fp32 parts costs more than the last wave's idle SMs), and the workspace: the expanded K and V
+// and the units of V, then the ranges' parts.
 struct Kv8Plan {
   KvSplit split;
-  size_t cache_bytes, o_bytes, lse_bytes;  // cache_bytes: K or V
+  size_t cache_bytes, unit_bytes, o_bytes, lse_bytes;  // cache_bytes: K or V
 };
 Kv8Plan kv8_plan(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
   const long long R = static_cast<long long>(Hq / Hkv) * Nq, bh = static_cast<long long>(B) * Hkv;
   Kv8Plan plan{};
   plan.split = kv_split(B, Hq, Hkv, Nq, Nk, bh * ((R + attn::kBM - 1) / attn::kBM) >= 2 * 152 ? 1 : 0);
   plan.cache_bytes = round256(static_cast<size_t>(bh) * Nk * d * 2);
+  plan.unit_bytes = round256(static_cast<size_t>(bh) * sizeof(float));
   if (plan.split.n_splits > 1) {
     plan.o_bytes = round256(static_cast<size_t>(plan.split.n_splits) * bh * R * d * sizeof(float));
     plan.lse_bytes = round256(static_cast<size_t>(plan.split.n_splits) * bh * R * sizeof(float));
@@ -688,6 +689,8 @@ attn_status_t fwd_kv8(const attn::Cache8Params& c, void* workspace, int Hq, attn
   char* const ws = static_cast<char*>(workspace);
   void* const k16 = ws;
   void* const v16 = ws + plan.cache_bytes;
+  float* const v_unit = reinterpret_cast<float*>(ws + 2 * plan.cache_bytes);
+  char* const parts = ws + 2 * plan.cache_bytes + plan.unit_bytes;
   FwdParams p{};
   p.o = c.o;
   p.lse = c.lse;
@@ -698,24 +701,25 @@ attn_status_t fwd_kv8(const attn::Cache8Params& c, void* workspace, int Hq, attn
   p.cache_seqlens = c.cache_seqlens;
   p.n_splits = plan.split.n_splits;
   p.tiles_per_split = plan.split.tiles_per_split;
-  p.o_part = reinterpret_cast<float*>(ws + 2 * plan.cache_bytes);
-  p.lse_part = reinterpret_cast<float*>(ws + 2 * plan.cache_bytes + plan.o_bytes);
+  p.o_part = reinterpret_cast<float*>(parts);
+  p.lse_part = reinterpret_cast<float*>(parts + plan.o_bytes);
   p.n_qtiles = static_cast<int>(n_rb);
   p.scale_log2 = c.scale_log2;
   p.out_f32 = c.out_f32;
   p.k_scale = c.k_scale;
+  p.v_unit = v_unit;
   p.n_blocks = c.n_blocks;
   p.block_shift = c.block_shift;
   FwdMaps maps;
   if (!make_dense_map(&maps.q, c.q, dtype, bh, c.R, c.d) || !make_dense_map(&maps.k, k16, dtype, bh, c.Nk, c.d) ||
-      !make_dense_map(&maps.v, v16, dtype, bh, c.Nk, c.d))
+      !make_dense_map(&maps.v, v16, ATTN_F16, bh, c.Nk, c.d))
     return ATTN_ERR_CUDA;
   const bool final16 = p.n_splits == 1 && !p.out_f32;  // tile stores of 16-bit outputs
   if (!final16)
     maps.o = maps.q;
   else if (!make_dense_map(&maps.o, c.o, dtype, bh, c.R, c.d))
     return ATTN_ERR_CUDA;
-  if (attn::launch_cache8_expand(c, k16, v16, dtype, cache_dtype, s) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (attn::launch_cache8_expand(c, k16, v16, v_unit, dtype, cache_dtype, s) != cudaSuccess) return ATTN_ERR_CUDA;
   if (attn::launch_fwd_kv8(maps, p, dtype, c.causal != 0, s) != cudaSuccess) return ATTN_ERR_CUDA;
   return from_cuda(p.n_splits > 1 ? attn::launch_kv_combine(p, dtype, c.causal != 0, s)
                                   : attn::launch_kv8_unseen(p, !p.out_f32, c.causal != 0, s));
@@ -760,7 +764,7 @@ size_t attn_fwd_kvcache8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk,
   const size_t R = static_cast<size_t>(Hq / Hkv) * Nq;
   if (R > static_cast<size_t>(attn::kCache8Rows)) {
     const Kv8Plan plan = kv8_plan(B, Hq, Hkv, Nq, Nk, d);
-    return std::max<size_t>(256, 2 * plan.cache_bytes + plan.o_bytes + plan.lse_bytes);
+    return std::max<size_t>(256, 2 * plan.cache_bytes + plan.unit_bytes + plan.o_bytes + plan.lse_bytes);
   }
   const Cache8Plan plan = cache8_plan(B, Hkv, static_cast<int>(R), Nk, d);
   return plan.o_bytes + plan.lse_bytes + plan.parts_bytes;

@@ -4,8 +4,10 @@
 // With R rows per kv head the forward reads every key R / 128 times, so expanding inside it would
 // repeat the conversion as often, on the warps whose exponentials bound it; once costs 5 bytes of
 // traffic per code.  K is expanded to bare codes, exact in either 16-bit type, and its scales
-// multiply the scores in fp32.  V is expanded to values, code * scale, rounded once (half a step 2^-8
-// bf16, 2^-11 fp16): its scale differs from key to key inside the P V sum.
+// multiply the scores in fp32.  V is expanded to code * scale / unit in fp16, the unit the largest
+// scale of the head, rounded once (half a step 2^-11; absolute 2^-25 units where a scale is below
+// 2^-14 of it), and P, at most 2^8, is fp16 as well: with both in bf16 the outputs' error was 1.5
+// times that of their own rounding (2^-8), with either type it is now that alone.
 #include <algorithm>
 #include <type_traits>
 #include "cache8.cuh"
@@ -40,10 +42,22 @@ __device__ __forceinline__ void expand16(const uint4 w, float scale, uint4* dst)
 
 // A CTA expands 128 tokens of one (batch, kv head): 16 codes of K and of V per thread and step.
 template <typename T, typename Code>
-__global__ void __launch_bounds__(256) expand_kernel(const Cache8Params p, T* k16, T* v16, int tiles) {
+__global__ void __launch_bounds__(256) expand_kernel(const Cache8Params p, T* k16, __half* v16, float* v_unit, int tiles) {
+  __shared__ float s_max[8];
   const int bh = blockIdx.x / tiles, j0 = (blockIdx.x % tiles) * 128;
   const int L = cache_len(p.cache_seqlens, bh / p.Hkv, p.Nk, nullptr, false);
   if (j0 >= L) return;
+  // the unit: the largest scale of the blocks that hold tokens (a NaN shows in its own block's values)
+  const float* vs = p.v_scale + static_cast<size_t>(bh) * p.n_blocks;
+  float unit = 0.f;
+  for (int i = threadIdx.x; i <= (L - 1) >> p.block_shift; i += 256) unit = fmaxf(unit, vs[i]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) unit = fmaxf(unit, __shfl_xor_sync(0xffffffffu, unit, o));
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = unit;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) unit = fmaxf(unit, s_max[i]);
+  if (j0 == 0 && threadIdx.x == 0) v_unit[bh] = unit;
   const int chunks = p.d / 16, n = min(128, p.Nk - j0) * chunks;
   const size_t base = (static_cast<size_t>(bh) * p.Nk + j0) * p.d;
   const uint4* k = reinterpret_cast<const uint4*>(p.k8 + base);
@@ -53,10 +67,10 @@ __global__ void __launch_bounds__(256) expand_kernel(const Cache8Params p, T* k1
   for (int i = threadIdx.x; i < n; i += 256) {
     const int j = j0 + i / chunks;
     if (j < L) {
-      const float vs = p.v_scale[static_cast<size_t>(bh) * p.n_blocks + (j >> p.block_shift)];
+      const float r = unit == 0.f ? 0.f : vs[j >> p.block_shift] / unit;
       const uint4 a = k[i], b = v[i];
       expand16<T, Code>(a, 1.f, ko + 2 * i);
-      expand16<T, Code>(b, vs, vo + 2 * i);
+      expand16<__half, Code>(b, r, vo + 2 * i);
     } else {  // the tile's rest: a weight of zero times what lies there has to be zero
       const uint4 z = make_uint4(0, 0, 0, 0);
       ko[2 * i] = ko[2 * i + 1] = vo[2 * i] = vo[2 * i + 1] = z;
@@ -78,21 +92,21 @@ __global__ void __launch_bounds__(256) unseen_kernel(const FwdParams p, int es, 
 }
 
 template <typename T>
-cudaError_t expand(const Cache8Params& p, void* k16, void* v16, attn_cache_dtype_t cache, cudaStream_t stream) {
+cudaError_t expand(const Cache8Params& p, void* k16, void* v16, float* v_unit, attn_cache_dtype_t cache, cudaStream_t stream) {
   const int tiles = (p.Nk + 127) / 128;
   const int grid = p.B * p.Hkv * tiles;
   if (cache == ATTN_CACHE_I8)
-    expand_kernel<T, CodeI8><<<grid, 256, 0, stream>>>(p, static_cast<T*>(k16), static_cast<T*>(v16), tiles);
+    expand_kernel<T, CodeI8><<<grid, 256, 0, stream>>>(p, static_cast<T*>(k16), static_cast<__half*>(v16), v_unit, tiles);
   else
-    expand_kernel<T, CodeE4m3><<<grid, 256, 0, stream>>>(p, static_cast<T*>(k16), static_cast<T*>(v16), tiles);
+    expand_kernel<T, CodeE4m3><<<grid, 256, 0, stream>>>(p, static_cast<T*>(k16), static_cast<__half*>(v16), v_unit, tiles);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_cache8_expand(const Cache8Params& p, void* k16, void* v16, attn_dtype_t dtype, attn_cache_dtype_t cache,
-                                 cudaStream_t stream) {
-  return dtype == ATTN_F16 ? expand<__half>(p, k16, v16, cache, stream) : expand<__nv_bfloat16>(p, k16, v16, cache, stream);
+cudaError_t launch_cache8_expand(const Cache8Params& p, void* k16, void* v16, float* v_unit, attn_dtype_t dtype,
+                                 attn_cache_dtype_t cache, cudaStream_t stream) {
+  return dtype == ATTN_F16 ? expand<__half>(p, k16, v16, v_unit, cache, stream) : expand<__nv_bfloat16>(p, k16, v16, v_unit, cache, stream);
 }
 
 cudaError_t launch_kv8_unseen(const FwdParams& p, bool out16, bool causal, cudaStream_t stream) {

@@ -8,8 +8,8 @@
 // In the KV-cache mode a row is query i = row % Nq of the G query heads of a kv head, its keys
 // are those of one range of the cache, masked past the cache length L and, when causal, past
 // L - Nq + i; it writes fp32 partials that a combine kernel merges.  The 8-bit cache mode is that
-// mode on bare key codes in 16 bits, with the codes' scales applied to the scores, and with one key
-// range it writes final outputs.
+// mode on bare key codes in 16 bits, with the codes' scales applied to the scores, on values in fp16
+// in a unit of each kv head (so P is fp16 too), and with one key range it writes final outputs.
 // The tiling follows the attention-operator article (m.xxqk.cn/news/636956) section 2.2: Q/K/V
 // tiles staged on chip, the max-subtracted softmax kept in registers and only O written back.
 // The online max/sum update follows the FlashAttention-T review, best practice 4; scale and
@@ -46,6 +46,7 @@
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <type_traits>
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -260,6 +261,7 @@ __global__ void __launch_bounds__(512, 1)
   constexpr bool KV = MODE == kModeKv || KV8;
   // an 8-bit cache in one range: the items' outputs are final, written as a dense item's are
   const bool kv_final = KV8 && p.n_splits == 1;
+  using PElem = std::conditional_t<KV8, Elem<__half>, Elem<T>>;  // of P and V
   // 16-bit output of a dense item, or of a varlen item whose 128 rows all lie in its
   // sequence: the epilogue warps stage the item's O tile in the item's Q slot (free once its
   // last S has run) and their thread 0 writes it with tile stores, then frees the slot.
@@ -462,7 +464,7 @@ __global__ void __launch_bounds__(512, 1)
       if (lane == 0) {
         constexpr bool kB = Elem<T>::kBf16;
         constexpr uint32_t idS = idesc_f16(kB, false, false, 128, kBN);
-        constexpr uint32_t idO = idesc_f16(kB, false, true, 128, DP);
+        constexpr uint32_t idO = idesc_f16(PElem::kBf16, false, true, 128, DP);
         const uint64_t dQ = smem_desc_sw128(smem_u32(sQ), 16, 1024);
         const uint64_t dK = smem_desc_sw128(smem_u32(sK), 16, 1024);
         const uint64_t dV = smem_desc_sw128(smem_u32(sV), L::kChunkBytes, 1024);
@@ -571,7 +573,8 @@ __global__ void __launch_bounds__(512, 1)
       const float a0 = (s0.x == -INFINITY) ? 0.f : ex2_approx(s0.x - mr);
       const float a1 = (s1.x == -INFINITY) ? 0.f : ex2_approx(s1.x - mr);
       const float l_all = s0.y * a0 + s1.y * a1;
-      const float inv_l = (l_all > 0.f) ? 1.f / l_all : 0.f;
+      float inv_l = (l_all > 0.f) ? 1.f / l_all : 0.f;
+      if constexpr (KV8) inv_l *= p.v_unit[it.b * p.Hkv + it.h];
       const float c0 = a0 * inv_l, c1 = a1 * inv_l;  // weights of O_0 and O_1
       const uint32_t t_last = kv - 1;
       if (!mbar_wait_warp(pv_done + (t_last & 1), (t_last >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
@@ -828,7 +831,7 @@ __global__ void __launch_bounds__(512, 1)
               }
               acc[(c >> 1) & 3] = c < 8 ? e : f2_add(acc[(c >> 1) & 3], e);
               const float2 ef = f2_unpack(e);
-              pk[(c / 2) % (PK / 2)] = Elem<T>::pack(ef.x, ef.y);
+              pk[(c / 2) % (PK / 2)] = PElem::pack(ef.x, ef.y);
             }
           } else {
 #pragma unroll
@@ -837,7 +840,7 @@ __global__ void __launch_bounds__(512, 1)
               const float e0 = ex2_approx(xf.x), e1 = ex2_approx(xf.y);
               const uint64_t e = f2_pack(e0, e1);
               acc[(c >> 1) & 3] = c < 8 ? e : f2_add(acc[(c >> 1) & 3], e);
-              pk[(c / 2) % (PK / 2)] = Elem<T>::pack(e0, e1);
+              pk[(c / 2) % (PK / 2)] = PElem::pack(e0, e1);
             }
           }
           if constexpr (PH == 2) {

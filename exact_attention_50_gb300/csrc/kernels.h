@@ -32,8 +32,10 @@ struct FwdParams {
   int n_splits, tiles_per_split;
   float* o_part;           // [n_splits, B*Hkv*R, d]
   float* lse_part;         // [n_splits, B*Hkv*R] (natural log)
-  // KV cache in 8 bits (kModeKv8): the key codes' scales [B*Hkv, n_blocks], 2^block_shift keys each
+  // KV cache in 8 bits (kModeKv8): the key codes' scales [B*Hkv, n_blocks], 2^block_shift keys each,
+  // and the unit of each head's values [B*Hkv]
   const float* k_scale;
+  const float* v_unit;
   int n_blocks, block_shift;
 };
 
@@ -186,11 +188,12 @@ constexpr int cache8_keys(int row_blocks) { return row_blocks == 1 ? 32 : 48; }
 constexpr int cache8_ctas_per_sm(int row_blocks) { return row_blocks == 1 ? 3 : 2; }
 cudaError_t launch_cache8_fwd(const CUtensorMap& k, const CUtensorMap& v, const Cache8Params& p, attn_dtype_t dtype,
                               attn_cache_dtype_t cache, cudaStream_t stream);
-// Many rows: K's codes and V's values in 16 bits, [B*Hkv, Nk, d] each, for the tokens that the caches
-// hold and zeros behind them up to a tile's end; then the tcgen05 forward in kModeKv8 on those, and with
+// Many rows: K's codes in dtype and V's values in fp16, in units of the largest scale of their head
+// (v_unit [B*Hkv]), [B*Hkv, Nk, d] each, for the tokens that the caches hold and zeros behind them up to a
+// tile's end; then the tcgen05 forward in kModeKv8 on those, and with
 // one key range the rows of which it computed nothing.
-cudaError_t launch_cache8_expand(const Cache8Params& p, void* k16, void* v16, attn_dtype_t dtype, attn_cache_dtype_t cache,
-                                 cudaStream_t stream);
+cudaError_t launch_cache8_expand(const Cache8Params& p, void* k16, void* v16, float* v_unit, attn_dtype_t dtype,
+                                 attn_cache_dtype_t cache, cudaStream_t stream);
 cudaError_t launch_fwd_kv8(const FwdMaps& maps, const FwdParams& p, attn_dtype_t dtype, bool causal, cudaStream_t stream);
 cudaError_t launch_kv8_unseen(const FwdParams& p, bool out16, bool causal, cudaStream_t stream);
 cudaError_t launch_cache8_none(const Cache8Params& p, cudaStream_t stream);
