@@ -328,11 +328,12 @@ def fwd_kvcache8(q, k8, v8, k_scale, v_scale, cache_seqlens=None, causal: bool =
     lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=device) if with_lse else None
     if workspace is None:
         need = _lib.attn_fwd_kvcache8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
     st = _on_device(dev, _lib.attn_fwd_kvcache8, q.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(),
                     v_scale.data_ptr(), _lens_ptr(cache_seqlens, "cache_seqlens", B), o.data_ptr(),
-                    lse.data_ptr() if with_lse else None, workspace.data_ptr(), workspace.nbytes, B, Hq, Hkv, Nq, Nk, d,
-                    block, causal, _scale_arg(scale), _dtype_code(q), _DT8[k8.dtype],
+                    lse.data_ptr() if with_lse else None, None if workspace is None else workspace.data_ptr(),
+                    0 if workspace is None else workspace.nbytes, B, Hq, Hkv, Nq, Nk, d, block, causal,
+                    _scale_arg(scale), _dtype_code(q), _DT8[k8.dtype],
                     _lib.ATTN_FLAG_OUT_F32 if out_f32 else 0)
     _lib._check(st, "attn_fwd_kvcache8")
     return o, lse

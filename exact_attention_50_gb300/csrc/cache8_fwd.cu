@@ -11,7 +11,8 @@
 // fit.  A run may begin and end inside a pair: such parts go to the workspace, normalised with
 // their log-sum-exp, and a second kernel merges them; a pair that lies within one run is
 // finished by its worker.  (Warps of a CTA that shared a run and joined their sums in shared memory
-// for every pair took 55 us for 256 sequences of 100 to 200 keys, now REPL_SHORT.)
+// for every pair took 55 us for 256 sequences of 100 to 200 keys, now 31 us.)  Small problems take a
+// cluster of CTAs per pair instead.
 //
 // A worker keeps its own ring of tiles full: when a tile's codes are in registers its first warp
 // starts the copies of the tile that follows in that stage -- TMA tile loads of K and V, swizzled,
@@ -32,6 +33,11 @@
 // subtracting 1152: there the offset would be far larger than the sums.  e4m3 by the conversion
 // instruction.
 //
+// What it reaches (8 sequences of 16k to 32k keys, 32 over 8 heads, d = 128, int8): 76 us, 5.6 TB/s, 83% of
+// the copy rate; 73 us with one query row per head, so the conversions cost a little still; about 8 us
+// of it are the launches, the first tiles' latency and the merge.  With 16 rows (NB = 2) 87 us, with 32
+// (two warps per tile, the codes converted twice) 150 us, bound by instruction issue.
+//
 // Rounding: q in bf16 becomes fp16 after a multiplication by a power of two per row (largest
 // element in [2^14, 2^15)), exact but for elements below 2^-28 of that.  P is rounded to fp16
 // (half a step 2^-11) after its multiplication by vs / (the largest vs so far): a block whose
@@ -39,6 +45,7 @@
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
+#include <cooperative_groups.h>
 #include "cache8.cuh"
 
 namespace attn {
@@ -226,7 +233,9 @@ __device__ __forceinline__ void deal_and_find(const Cache8Params& p, int runs, i
   }
 }
 
-template <typename T, typename Code, int DP, int NB>
+// SPREAD: a cluster of CTAs per pair, whose workers take its tiles in turn and join their sums through
+// distributed shared memory; no workspace and no second kernel.
+template <typename T, typename Code, int DP, int NB, bool SPREAD>
 __global__ void __launch_bounds__(kThreads, (Layout<DP, NB>::kCtas))
     cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Cache8Params p) {
   using L = Layout<DP, NB>;
@@ -241,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, (Layout<DP, NB>::kCtas))
   const uint32_t abort_flag = smem_u32(smem + L::kOffMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // a worker: RB warps, one per 8 NB rows, in RBW (a power of two) places
-  const int RB = (p.R + 8 * NB - 1) / (8 * NB);
+  const int RB = SPREAD ? 1 : (p.R + 8 * NB - 1) / (8 * NB);
   const int RBW = RB <= 1 ? 1 : RB <= 2 ? 2 : 4;
   const int rb = warp % RBW, first_warp = warp - rb;
   const uint32_t stages = L::kStages * RBW;  // of the worker's ring
@@ -262,12 +271,24 @@ __global__ void __launch_bounds__(kThreads, (Layout<DP, NB>::kCtas))
     tma_prefetch_desc(&tmV);
   }
   __syncthreads();
-  dependents_launch();
+  if (!SPREAD) dependents_launch();
   const int per_cta = kWarps / RBW;
   const int run = blockIdx.x * per_cta + warp / RBW;
-  Deal deal;
+  const int stride = SPREAD ? p.cluster * kWarps : 1;  // from a worker's tile of a pair to its next
+  Deal deal{};
   Walk w;
-  deal_and_find(p, p.runs, run, deal, w);
+  if constexpr (SPREAD) {
+    const int bh = blockIdx.x / p.cluster;
+    w.b = bh / p.Hkv;
+    w.h = bh % p.Hkv;
+    w.j = run % stride;
+    const int len = cache_len(p.cache_seqlens, w.b, p.Nk, p.status, w.h == 0 && w.j == 0 && lane == 0);
+    w.nt = (len + kKeys - 1) / kKeys;
+    w.t = w.j;
+    w.end = w.nt;
+  } else {
+    deal_and_find(p, p.runs, run, deal, w);
+  }
 
   // ---- the copies of the run's next tile, into the stage of its number
   Walk ahead = w;
@@ -301,7 +322,9 @@ __global__ void __launch_bounds__(kThreads, (Layout<DP, NB>::kCtas))
     }
     __syncwarp();
     ++issued;
-    if (ahead.j + 1 < ahead.nt) {
+    if (SPREAD) {
+      ahead.t = ahead.j += stride;
+    } else if (ahead.j + 1 < ahead.nt) {
       ++ahead.t;
       ++ahead.j;
     } else {
@@ -316,10 +339,10 @@ __global__ void __launch_bounds__(kThreads, (Layout<DP, NB>::kCtas))
   const uint32_t tiles = smem_u32(ring);
   const int row0 = rb * 8 * NB;  // this warp's rows; as columns of S^T and O^T this thread has rows 8 b + 2 t + e of them
   uint32_t n = 0;                // tiles of the run passed
-  for (; works && ok && w.t < w.end; w.next(p)) {
+  for (; SPREAD || (works && ok && w.t < w.end); w.next(p)) {
     const int len = cache_len(p.cache_seqlens, w.b, p.Nk, nullptr, false);
     const size_t bh = static_cast<size_t>(w.b) * p.Hkv + w.h;
-    const int part = w.part();
+    const int part = SPREAD ? (max(w.nt - w.j, 0) + stride - 1) / stride : w.part();
     // ---- Q as B fragments: step s holds columns (DP / 4) t + 4 s .. + 3 of row g
     uint32_t qb[NB][kSteps][2];
     float f[NB][2], start[NB][2];  // per row: scale log2(e) over its power of two; where its sums start
@@ -443,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, (Layout<DP, NB>::kCtas))
             }
         }
         // ---- scale, mask, running maximum
-        const int key0 = (w.j + x) * kKeys;
+        const int key0 = (w.j + x * stride) * kKeys;
         const float v_old = vref;
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) vref = fmaxf(vref, vg[i]);
@@ -556,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, (Layout<DP, NB>::kCtas))
         }
       }
     }
-    if (!ok) break;
+    if (!SPREAD && !ok) break;
     // ---- this warp's part: sums over the eight lanes that share a row, o in units of one
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
@@ -568,6 +591,64 @@ __global__ void __launch_bounds__(kThreads, (Layout<DP, NB>::kCtas))
       for (int i = 0; i < kCols; ++i) {
         o[i][b][0] *= vref; o[i][b][1] *= vref; o[i][b][2] *= vref; o[i][b][3] *= vref;
       }
+    }
+    if constexpr (SPREAD) {
+      // ---- the workers' parts in their CTAs' shared memory (the ring, read to its end), then every
+      // thread of the cluster sums some outputs over them
+      const auto cluster = cooperative_groups::this_cluster();
+      const int rank = blockIdx.x % p.cluster, workers = min(stride, w.nt);  // those with a tile
+      constexpr int kRows = 8 * NB;
+      float* const part_o = reinterpret_cast<float*>(smem);                            // [kWarps][kRows][DP]
+      float2* const part_ml = reinterpret_cast<float2*>(smem + kWarps * kRows * DP * 4);  // [kWarps][kRows]
+      float2* const all_ml = part_ml + kWarps * kRows;                                 // [workers][kRows]
+      static_assert(kWarps * kRows * DP * 4 + 9 * kWarps * kRows * 8 <= L::kOffScale, "the parts lie in the ring");
+      if (!ok || abort_read(abort_flag))  // let the copies land before their stages are written
+        for (uint32_t i = issued > stages ? issued - stages : 0; i < issued; ++i) mbar_drain(full + i % stages, (i / stages) & 1);
+      __syncthreads();
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * b + 2 * t + e;
+          if (g == 0) part_ml[warp * kRows + r] = make_float2(m[b][e], l[b][e]);
+          float* dst = part_o + (warp * kRows + r) * DP + (DP / 8) * g;
+#pragma unroll
+          for (int c = 0; c < DP / 8; c += 4)
+            *reinterpret_cast<float4*>(dst + c) = make_float4(o[c / 2][b][e], o[c / 2][b][2 + e], o[c / 2 + 1][b][e], o[c / 2 + 1][b][2 + e]);
+        }
+      cluster.sync();
+      for (int i = threadIdx.x; i < workers * kRows; i += kThreads) {
+        const int k = i / kRows;
+        all_ml[i] = *cluster.map_shared_rank(part_ml + (k % kWarps) * kRows + i % kRows, k / kWarps);
+      }
+      __syncthreads();
+      const int half = p.d / 2;
+      for (int i = rank * kThreads + threadIdx.x; i < p.R * half; i += p.cluster * kThreads) {
+        const int r = i / half, c = i % half * 2;
+        float top = -INFINITY;
+        for (int k = 0; k < workers; ++k) top = fmaxf(top, all_ml[k * kRows + r].x);
+        float sum = 0.f, x = 0.f, y = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < workers; ++k) {
+          const float2 ml = all_ml[k * kRows + r];
+          const float2 v = *reinterpret_cast<const float2*>(cluster.map_shared_rank(part_o + ((k % kWarps) * kRows + r) * DP + c, k / kWarps));
+          const float a = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top);
+          sum += ml.y * a;
+          x += v.x * a;
+          y += v.y * a;
+        }
+        const float il = sum == 0.f ? 0.f : 1.f / sum;
+        const size_t row = bh * p.R + r;
+        if (p.out_f32) {
+          *reinterpret_cast<float2*>(static_cast<float*>(p.o) + row * p.d + c) = make_float2(x * il, y * il);
+        } else {
+          const T* tag = nullptr;
+          *reinterpret_cast<uint32_t*>(static_cast<T*>(p.o) + row * p.d + c) = pack2(tag, x * il, y * il);
+        }
+        if (c == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
+      }
+      cluster.sync();  // the others may still read this CTA's parts
+      return;
     }
     // ---- the pair's output, or this run's part of it
     {
@@ -715,15 +796,29 @@ __global__ void __launch_bounds__(256) cache8_none_kernel(const Cache8Params p) 
   if (first < static_cast<size_t>(p.B)) cache_len(p.cache_seqlens, static_cast<int>(first), p.Nk, p.status, true);
 }
 
-template <typename T, typename Code, int DP, int NB>
+template <typename T, typename Code, int DP, int NB, bool SPREAD>
 cudaError_t run(const CUtensorMap& k, const CUtensorMap& v, const Cache8Params& p, cudaStream_t stream) {
   using L = Layout<DP, NB>;
-  auto kern = cache8_kernel<T, Code, DP, NB>;
+  auto kern = cache8_kernel<T, Code, DP, NB, SPREAD>;
   static std::atomic<unsigned long long> ready{0};  // devices on which the kernel is set up
   cudaError_t e = once_per_device(ready, [&] {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   });
   if (e != cudaSuccess) return e;
+  if (SPREAD) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = p.cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(p.ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = L::kBytes;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, k, v, p);
+  }
   kern<<<p.ctas, kThreads, L::kBytes, stream>>>(k, v, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -738,11 +833,16 @@ cudaError_t run(const CUtensorMap& k, const CUtensorMap& v, const Cache8Params& 
   return p.out_f32 ? launch_dependent(cache8_merge_kernel<float, 8>, grid, 256, stream, p) : launch_dependent(cache8_merge_kernel<T, 8>, grid, 256, stream, p);
 }
 
+template <typename T, typename Code, int DP, int NB>
+cudaError_t run_s(const CUtensorMap& k, const CUtensorMap& v, const Cache8Params& p, cudaStream_t stream) {
+  return p.cluster ? run<T, Code, DP, NB, true>(k, v, p, stream) : run<T, Code, DP, NB, false>(k, v, p, stream);
+}
+
 template <typename T, typename Code>
 cudaError_t run_c(const CUtensorMap& k, const CUtensorMap& v, const Cache8Params& p, cudaStream_t stream) {
   const bool few = cache8_row_blocks(p.R) == 1;
-  if (p.d <= 64) return few ? run<T, Code, 64, 1>(k, v, p, stream) : run<T, Code, 64, 2>(k, v, p, stream);
-  return few ? run<T, Code, 128, 1>(k, v, p, stream) : run<T, Code, 128, 2>(k, v, p, stream);
+  if (p.d <= 64) return few ? run_s<T, Code, 64, 1>(k, v, p, stream) : run_s<T, Code, 64, 2>(k, v, p, stream);
+  return few ? run_s<T, Code, 128, 1>(k, v, p, stream) : run_s<T, Code, 128, 2>(k, v, p, stream);
 }
 
 template <typename T>

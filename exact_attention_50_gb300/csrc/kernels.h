@@ -175,6 +175,7 @@ struct Cache8Params {
   // `ctas` CTAs; a run's part of a (batch, kv head) pair that it does not hold whole goes here, two
   // slots a run
   int ctas, runs, tile_keys;
+  int cluster;             // 0, or the CTAs of a cluster that shares one pair's tiles; the parts are not used
   float* o_part;           // [2 * runs, R, d], normalised
   float* lse_part;         // [2 * runs, R], log2
   int2* parts;             // [B * Hkv]: the first run of a pair that several share and their number, else (., 0)

@@ -268,9 +268,9 @@ attn_status_t attn_kvcache8_append(void* k8, void* v8, float* k_scale, float* v_
  * values that the codes and scales stand for.  Shapes, masks, rows without keys, flags and
  * argument rules are those of attn_fwd_kvcache; dtype (of q and o) is ATTN_F16 or ATTN_BF16
  * (ATTN_F32: ATTN_ERR_UNSUPPORTED).  The split over key ranges is chosen from the sizes.
- *   workspace  DEVICE, at least attn_fwd_kvcache8_workspace_bytes(...) bytes, 256-byte aligned;
- *              contents on entry are ignored, on exit undefined.  Calls that may run at the same
- *              time need one each.
+ *   workspace  DEVICE, at least attn_fwd_kvcache8_workspace_bytes(...) bytes, 256-byte aligned
+ *              (0 bytes for small problems: it may then be NULL); contents on entry are ignored,
+ *              on exit undefined.  Calls that may run at the same time need one each.
  */
 size_t attn_fwd_kvcache8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d);
 attn_status_t attn_fwd_kvcache8(const void* q, const void* k8, const void* v8, const float* k_scale,

@@ -37,14 +37,17 @@ def test_append_refusals(lib):
 
 
 def test_attend_refusals_and_workspace(lib):
-    ws = _lib.attn_fwd_kvcache8_workspace_bytes(2, 4, 2, 3, 1000, 64)
+    ws = _lib.attn_fwd_kvcache8_workspace_bytes(2, 4, 2, 3, 100000, 64)
     assert ws >= 256 and ws % 256 == 0
+    assert _lib.attn_fwd_kvcache8_workspace_bytes(2, 4, 2, 3, 100, 64) == 0  # a cluster per head joins its parts on chip
+    # many rows: K and V in 16 bits, and what the key ranges leave
+    assert _lib.attn_fwd_kvcache8_workspace_bytes(2, 4, 2, 300, 1000, 64) >= 2 * 2 * 2 * 1000 * 64 * 2
     for bad in ((0, 4, 2, 3, 1000, 64), (2, 3, 2, 3, 1000, 64), (2, 4, 2, 0, 1000, 64), (2, 4, 2, 3, -1, 64), (2, 4, 2, 3, 9, 0)):
         assert _lib.attn_fwd_kvcache8_workspace_bytes(*bad) == 0
 
     def f(**kw):
         a = dict(q=4096, k8=4096, v8=4096, ks=4096, vs=4096, lens=None, o=4096, lse=None, ws=4096, wsb=ws, B=2, Hq=4, Hkv=2,
-                 Nq=3, Nk=1000, d=64, block=64, causal=1, scale=0.0, dtype=_lib.ATTN_BF16, cache=_lib.ATTN_CACHE_I8, flags=0)
+                 Nq=3, Nk=100000, d=64, block=64, causal=1, scale=0.0, dtype=_lib.ATTN_BF16, cache=_lib.ATTN_CACHE_I8, flags=0)
         a.update(kw)
         return _lib.attn_fwd_kvcache8(a["q"], a["k8"], a["v8"], a["ks"], a["vs"], a["lens"], a["o"], a["lse"], a["ws"],
                                       a["wsb"], a["B"], a["Hq"], a["Hkv"], a["Nq"], a["Nk"], a["d"], a["block"],

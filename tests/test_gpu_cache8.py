@@ -285,9 +285,17 @@ def test_attend_refusals_of_the_python_layer(dev):
     ok()
     for kw in (dict(q=q[:1]), dict(q=q[:, :3].contiguous()), dict(k8=k8[..., :32]), dict(v8=k8[:, :1].contiguous()), dict(block=48),
                dict(block=32), dict(k_scale=s[:, :, :1].contiguous()), dict(cache_seqlens=cl[:1]), dict(cache_seqlens=cl.cpu()),
-               dict(scale=-1.0), dict(q=q.transpose(1, 2)), dict(workspace=torch.empty(8, dtype=torch.uint8, device=dev))):
+               dict(scale=-1.0), dict(q=q.transpose(1, 2))):
         with pytest.raises((ValueError, _lib.AttnError)):
             ok(**kw)
+    big, sb = torch.ones(2, 2, 20000, 64, dtype=torch.int8, device=dev), torch.ones(2, 2, 313, device=dev)
+    need = A.kvcache8_workspace_bytes(2, 4, 2, 1, 20000, 64)
+    assert need > 0
+    for ws in (torch.empty(need - 1, dtype=torch.uint8, device=dev), torch.empty(need + 256, dtype=torch.uint8, device=dev)[128:]):
+        with pytest.raises(_lib.AttnError):
+            ok(k8=big, v8=big, k_scale=sb, v_scale=sb, workspace=ws)
+    assert A.kvcache8_workspace_bytes(2, 4, 2, 1, 128, 64) == 0  # small: none is used
+    ok(workspace=torch.empty(8, dtype=torch.uint8, device=dev))
     for kw in (dict(k8=k8.float()), dict(v8=k8.to(torch.float8_e4m3fn)), dict(k_scale=s.half()), dict(cache_seqlens=cl.long())):
         with pytest.raises(TypeError):
             ok(**kw)
