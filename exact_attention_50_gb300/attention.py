@@ -15,6 +15,7 @@ every step of the computation runs in libattn_gb300.so's kernels.
 """
 from __future__ import annotations
 
+import functools
 import math
 
 import torch
@@ -222,22 +223,34 @@ def fwd_kvcache(q, k_cache, v_cache, cache_seqlens=None, causal: bool = False, s
     return o, lse
 
 
-def _cache_args(name: str, *tensors) -> int:
-    """Checks of the cache calls: (tensor, name, dtype or None) each; contiguous tensors on one
-    GPU, that of the first, called `name`.  Returns the GPU's index."""
+def _cache_args(name: str, tensors, dtypes, names) -> int:
+    """Checks of the cache calls: contiguous tensors on one GPU, that of the first, called `name`; a
+    dtype or None for each.  Returns the GPU's index.  Optional tensors that are None are left out
+    by the caller."""
     try:
-        dev = tensors[0][0].get_device()
-        if dev >= 0 and all(t.get_device() == dev and t.is_contiguous() and (dtype is None or t.dtype == dtype)
-                            for t, _, dtype in tensors if t is not None):
+        dev = tensors[0].get_device()
+        ok = dev >= 0
+        for t, dtype in zip(tensors, dtypes):
+            if t.get_device() != dev or not t.is_contiguous() or (dtype is not None and t.dtype is not dtype):
+                ok = False
+                break
+        if ok:
             return dev
-    except AttributeError:
+    except AttributeError:  # not a tensor
         pass
-    for t, n, dtype in tensors:  # say what is wrong
-        if t is not None:
-            _require(t, n, dtype)
-            if t.device != tensors[0][0].device:
-                raise ValueError(f"{n} must be on {name}'s device")
+    for t, n, dtype in zip(tensors, names, dtypes):  # say what is wrong
+        _require(t, n, dtype)
+        if t.device != tensors[0].device:
+            raise ValueError(f"{n} must be on {name}'s device")
     raise TypeError("tensors on a CUDA device are wanted")
+
+
+def _optional(tensors, dtypes, names, *more):
+    """The argument lists with the optional (tensor, dtype, name) that are there behind them."""
+    for t, dtype, n in more:
+        if t is not None:
+            tensors, dtypes, names = tensors + (t,), dtypes + (dtype,), names + (n,)
+    return tensors, dtypes, names
 
 
 def _on_device(dev: int, call, *args) -> int:
@@ -247,13 +260,6 @@ def _on_device(dev: int, call, *args) -> int:
         return call(*args, stream)
     with torch.cuda.device(dev):
         return call(*args, stream)
-
-
-def _tensor(t):
-    """A tensor that may not be missing."""
-    if t is None:
-        raise TypeError("a tensor is wanted where None was given")
-    return t
 
 
 def _lens_ptr(t, name: str, B: int):
@@ -286,10 +292,11 @@ def kvcache8_append(k8, v8, k_scale, v_scale, k_new, v_new, cache_seqlens=None, 
     scale, 16, 32, 64 or 128."""
     _require(k8, "k8")
     _require(k_new, "k_new")
-    dev = _cache_args("k8", (k8, "k8", None), (v8, "v8", k8.dtype), (_tensor(k_scale), "k_scale", torch.float32),
-                      (_tensor(v_scale), "v_scale", torch.float32), (k_new, "k_new", None),
-                      (_tensor(v_new), "v_new", k_new.dtype), (cache_seqlens, "cache_seqlens", torch.int32),
-                      (new_seqlens, "new_seqlens", torch.int32))
+    dev = _cache_args("k8", *_optional((k8, v8, k_scale, v_scale, k_new, v_new),
+                                       (None, k8.dtype, torch.float32, torch.float32, None, k_new.dtype),
+                                       ("k8", "v8", "k_scale", "v_scale", "k_new", "v_new"),
+                                       (cache_seqlens, torch.int32, "cache_seqlens"),
+                                       (new_seqlens, torch.int32, "new_seqlens")))
     B, Hkv, Nk, d = _check_cache8(k8, v8, k_scale, v_scale, block)
     shape = k_new.shape
     if len(shape) != 4 or shape != v_new.shape or shape[0] != B or shape[1] != Hkv or shape[3] != d:
@@ -301,6 +308,7 @@ def kvcache8_append(k8, v8, k_scale, v_scale, k_new, v_new, cache_seqlens=None, 
     _lib._check(st, "attn_kvcache8_append")
 
 
+@functools.lru_cache(maxsize=1024)
 def kvcache8_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Nk: int, d: int) -> int:
     """Bytes of the device workspace fwd_kvcache8 needs for these sizes."""
     return _lib.attn_fwd_kvcache8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d)
@@ -314,20 +322,19 @@ def fwd_kvcache8(q, k8, v8, k_scale, v_scale, cache_seqlens=None, causal: bool =
     (o [B,Hq,Nq,d], lse [B,Hq,Nq] or None)."""
     _require(q, "q")
     _require(k8, "k8")
-    dev = _cache_args("q", (q, "q", None), (k8, "k8", None), (_tensor(v8), "v8", k8.dtype),
-                      (_tensor(k_scale), "k_scale", torch.float32), (_tensor(v_scale), "v_scale", torch.float32),
-                      (cache_seqlens, "cache_seqlens", torch.int32), (workspace, "workspace", None))
+    dev = _cache_args("q", *_optional((q, k8, v8, k_scale, v_scale), (None, None, k8.dtype, torch.float32, torch.float32),
+                                      ("q", "k8", "v8", "k_scale", "v_scale"), (cache_seqlens, torch.int32, "cache_seqlens"),
+                                      (workspace, None, "workspace")))
     B, Hkv, Nk, d = _check_cache8(k8, v8, k_scale, v_scale, block)
-    if q.dim() != 4:
-        raise ValueError("q must be [B,Hq,Nq,d]")
-    Bq, Hq, Nq, dq = q.shape
-    if Bq != B or dq != d:
-        raise ValueError("q and the cache disagree on batch or head_dim")
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != B or shape[3] != d:
+        raise ValueError("q must be [B,Hq,Nq,d], with the cache's batch and head_dim")
+    Hq, Nq = shape[1], shape[2]
     device = q.device
     o = torch.empty_like(q, dtype=torch.float32) if out_f32 else torch.empty_like(q)
     lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=device) if with_lse else None
     if workspace is None:
-        need = _lib.attn_fwd_kvcache8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d)
+        need = kvcache8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d)
         workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
     st = _on_device(dev, _lib.attn_fwd_kvcache8, q.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(),
                     v_scale.data_ptr(), _lens_ptr(cache_seqlens, "cache_seqlens", B), o.data_ptr(),
@@ -346,9 +353,9 @@ def kvcache_weights(q, k_cache, lse, cache_seqlens=None, causal: bool = False, s
     weights float32 [B,Hkv,Nk]: what earlier queries added up to (None: zeros).  out: where to
     write (may be weights).  Returns float32 [B,Hkv,Nk]."""
     _require(q, "q")
-    dev = _cache_args("q", (q, "q", None), (_tensor(k_cache), "k_cache", q.dtype), (_tensor(lse), "lse", torch.float32),
-                      (cache_seqlens, "cache_seqlens", torch.int32), (weights, "weights", torch.float32),
-                      (out, "out", torch.float32))
+    dev = _cache_args("q", *_optional((q, k_cache, lse), (None, q.dtype, torch.float32), ("q", "k_cache", "lse"),
+                                      (cache_seqlens, torch.int32, "cache_seqlens"), (weights, torch.float32, "weights"),
+                                      (out, torch.float32, "out")))
     if q.dim() != 4 or k_cache.dim() != 4:
         raise ValueError("q must be [B,Hq,Nq,d] and k_cache [B,Hkv,Nk,d]")
     B, Hq, Nq, d = q.shape
@@ -389,9 +396,10 @@ def kvcache_evict(k_cache, v_cache, weights, keep: int, recent: int, cache_seqle
     if out is None:
         out = tuple(torch.zeros((B, Hkv, keep + recent, d), dtype=k_cache.dtype, device=device) for _ in range(2))
     k_out, v_out = out
-    dev = _cache_args("k_cache", (k_cache, "k_cache", None), (_tensor(v_cache), "v_cache", k_cache.dtype),
-                      (_tensor(weights), "weights", torch.float32), (_tensor(k_out), "k_out", k_cache.dtype),
-                      (_tensor(v_out), "v_out", k_cache.dtype), (cache_seqlens, "cache_seqlens", torch.int32))
+    dt = k_cache.dtype
+    dev = _cache_args("k_cache", *_optional((k_cache, v_cache, weights, k_out, v_out), (dt, dt, torch.float32, dt, dt),
+                                            ("k_cache", "v_cache", "weights", "k_out", "v_out"),
+                                            (cache_seqlens, torch.int32, "cache_seqlens")))
     if v_cache.shape != k_cache.shape or weights.shape != (B, Hkv, Nk):
         raise ValueError("k_cache and v_cache must be [B,Hkv,Nk,d] and weights [B,Hkv,Nk]")
     if k_out.dim() != 4 or k_out.shape != v_out.shape or k_out.shape[:2] != (B, Hkv) or k_out.shape[3] != d:
