@@ -653,8 +653,9 @@ struct Cache8Plan {
   size_t o_bytes, lse_bytes, parts_bytes;
 };
 Cache8Plan cache8_plan(int B, int Hkv, int R, int Nk, int d) {
-  const int nb = attn::cache8_row_blocks(R), keys = attn::cache8_keys(nb), workers = 4 / attn::cache8_run_warps(R);
-  const long long pairs = static_cast<long long>(B) * Hkv, tiles = (static_cast<long long>(Nk) + keys - 1) / keys;
+  const long long pairs = static_cast<long long>(B) * Hkv;
+  const int nb = attn::cache8_row_blocks(R), keys = attn::cache8_keys(pairs, R, Nk, d), workers = 4 / attn::cache8_run_warps(R);
+  const long long tiles = (static_cast<long long>(Nk) + keys - 1) / keys;
   const long long room = attn::cache8_ctas_per_sm(nb) * 152LL;
   int cluster = 1;
   while (cluster < 8 && pairs * 2 * cluster <= room && tiles > 4 * cluster) cluster *= 2;
@@ -727,10 +728,10 @@ attn_status_t fwd_kv8(const attn::Cache8Params& c, void* workspace, int Hq, attn
     maps.o = maps.q;
   else if (!make_dense_map(&maps.o, c.o, dtype, bh, c.R, c.d))
     return ATTN_ERR_CUDA;
-  if (attn::launch_cache8_expand(c, k16, v16, v_unit, dtype, cache_dtype, s) != cudaSuccess) return ATTN_ERR_CUDA;
-  if (attn::launch_fwd_kv8(maps, p, dtype, c.causal != 0, s) != cudaSuccess) return ATTN_ERR_CUDA;
-  return from_cuda(p.n_splits > 1 ? attn::launch_kv_combine(p, dtype, c.causal != 0, s)
-                                  : attn::launch_kv8_unseen(p, !p.out_f32, c.causal != 0, s));
+  if (attn::launch_cache8_expand(c, k16, v16, v_unit, p.n_splits == 1, dtype, cache_dtype, s) != cudaSuccess) return ATTN_ERR_CUDA;
+  const cudaError_t e = attn::launch_fwd_kv8(maps, p, dtype, c.causal != 0, s);
+  if (e != cudaSuccess || p.n_splits == 1) return from_cuda(e);
+  return from_cuda(attn::launch_kv_combine(p, dtype, c.causal != 0, s));
 }
 
 bool overlap(const void* a, size_t an, const void* b, size_t bn) {
@@ -818,7 +819,7 @@ attn_status_t attn_fwd_kvcache8(const void* q, const void* k8, const void* v8, c
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (Nk == 0) return from_cuda(attn::launch_cache8_none(p, s));
   if (R > attn::kCache8Rows) return fwd_kv8(p, workspace, Hq, dtype, cache_dtype, s);
-  p.tile_keys = attn::cache8_keys(attn::cache8_row_blocks(p.R));
+  p.tile_keys = attn::cache8_keys(bh, p.R, Nk, d);
   // tiles are numbered in 32 bits (two terabytes of codes)
   if (bh * ((static_cast<long long>(Nk) + p.tile_keys - 1) / p.tile_keys) > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
   const Cache8Plan plan = cache8_plan(B, Hkv, p.R, Nk, d);

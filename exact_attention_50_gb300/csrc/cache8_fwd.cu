@@ -5,7 +5,7 @@
 // keys.  With code c and block scales ks, vs:
 //   s_j = scale ks_j (q . ck_j), masked;  l = sum_j exp(s_j - m);  o = sum_j exp(s_j - m) vs_j cv_j / l.
 //
-// Work: the caches are cut into tiles of 32 keys (48 for more than 8 rows), and all tiles of all
+// Work: the caches are cut into tiles of 32 keys (48 for more than 8 rows, 64 for many of 64 columns), and all tiles of all
 // (batch, kv head) pairs, one after the other, are dealt in equal runs to the workers, whatever the
 // sequences' lengths.  A worker is one warp per block of rows, four warps a CTA, as many CTAs as
 // fit.  A run may begin and end inside a pair: such parts go to the workspace, normalised with
@@ -55,13 +55,13 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr float kLazy = 8.0f;   // log2 units by which a tile's maximum may exceed the running one
 
 // NB: blocks of 8 query rows per warp, 1 or 2.
-template <int DP, int NB>
+template <int DP, int NB, int KEYS>
 struct Layout {
-  static constexpr int kKeys = cache8_keys(NB);
+  static constexpr int kKeys = KEYS;
   static constexpr int kGroups = kKeys / 16;                  // 16 keys share a scale
   static constexpr int kCtas = cache8_ctas_per_sm(NB);
   static constexpr int kTile = kKeys * DP;                    // bytes of codes
-  static constexpr int kStages = DP == 128 ? 2 : 4;           // per warp
+  static constexpr int kStages = (NB == 1 ? 16 : 24) * 1024 / (2 * kTile);  // per warp: 64 or 96 KB a CTA
   static constexpr int kOffV = kTile;                         // within a stage: K, V
   static constexpr int kStage = 2 * kTile;
   static constexpr int kOffScale = kWarps * kStages * kStage; // per stage: (ks, vs) of each group
@@ -235,10 +235,10 @@ __device__ __forceinline__ void deal_and_find(const Cache8Params& p, int runs, i
 
 // SPREAD: a cluster of CTAs per pair, whose workers take its tiles in turn and join their sums through
 // distributed shared memory; no workspace and no second kernel.
-template <typename T, typename Code, int DP, int NB, bool SPREAD>
-__global__ void __launch_bounds__(kThreads, (Layout<DP, NB>::kCtas))
+template <typename T, typename Code, int DP, int NB, int KEYS, bool SPREAD>
+__global__ void __launch_bounds__(kThreads, (Layout<DP, NB, KEYS>::kCtas))
     cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Cache8Params p) {
-  using L = Layout<DP, NB>;
+  using L = Layout<DP, NB, KEYS>;
   constexpr int kKeys = L::kKeys, kGroups = L::kGroups;
   constexpr int kSteps = DP / 16;  // contraction steps of K Q^T
   constexpr int kCols = DP / 16;   // 16-column blocks of V
@@ -710,8 +710,8 @@ __global__ void __launch_bounds__(kThreads, (Layout<DP, NB>::kCtas))
 }
 
 // Merges the parts of the pairs that several runs share.  A row is one warp's (W = 1) or a CTA's
-// eight warps' (W = 8), each taking every W-th part, eight at a time.
-template <typename OutT, int W>
+// eight warps' (W = 8), each taking every W-th part, kAhead at a time.
+template <typename OutT, int W, int kAhead>
 __global__ void __launch_bounds__(256) cache8_merge_kernel(const Cache8Params p) {
   __shared__ float4 s_o[8][32];
   __shared__ float2 s_ml[8];
@@ -725,11 +725,11 @@ __global__ void __launch_bounds__(256) cache8_merge_kernel(const Cache8Params p)
   if (parts.y <= 0 || parts.x < 0 || parts.x >= p.runs || parts.y > p.runs - parts.x) return;
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = W == 8 ? warp : 0; k0 < parts.y; k0 += 8 * W) {
-    float e[8];
-    float4 x[8];
+  for (int k0 = W == 8 ? warp : 0; k0 < parts.y; k0 += kAhead * W) {
+    float e[kAhead];
+    float4 x[kAhead];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
+    for (int u = 0; u < kAhead; ++u) {
       const int k = k0 + u * W;
       const bool in = k < parts.y;
       // the first run's part ends inside the pair, the others' begin there
@@ -739,13 +739,13 @@ __global__ void __launch_bounds__(256) cache8_merge_kernel(const Cache8Params p)
     }
     float top = m;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) top = fmaxf(top, e[u]);
+    for (int u = 0; u < kAhead; ++u) top = fmaxf(top, e[u]);
     const float a = m == top ? 1.f : ex2_approx(m - top);  // m = -inf: 0
     acc.x *= a; acc.y *= a; acc.z *= a; acc.w *= a;
     l *= a;
     m = top;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
+    for (int u = 0; u < kAhead; ++u) {
       // a NaN part stays; an empty one (no key that the row sees) has no weight
       const float b = e[u] == -INFINITY ? 0.f : ex2_approx(e[u] - top);
       acc.x += x[u].x * b;
@@ -796,10 +796,21 @@ __global__ void __launch_bounds__(256) cache8_none_kernel(const Cache8Params p) 
   if (first < static_cast<size_t>(p.B)) cache_len(p.cache_seqlens, static_cast<int>(first), p.Nk, p.status, true);
 }
 
-template <typename T, typename Code, int DP, int NB, bool SPREAD>
+// By the parts that a pair has on average: 228 of them (1 x 8 heads of 32k keys) a warp's share in two rounds
+// of loads, 28 (8 x 8 heads) in one, a few for one warp; 16 loads ahead for those of 64 x 8 heads, 3 each,
+// took 8 us more.
+template <typename OutT>
+cudaError_t launch_merge(const Cache8Params& p, cudaStream_t stream) {
+  const long long pairs = static_cast<long long>(p.B) * p.Hkv, rows = pairs * p.R;
+  if (p.runs < 8 * pairs) return launch_dependent(cache8_merge_kernel<OutT, 1, 8>, dim3(static_cast<unsigned>((rows + 7) / 8)), 256, stream, p);
+  if (p.runs < 64 * pairs) return launch_dependent(cache8_merge_kernel<OutT, 8, 4>, dim3(static_cast<unsigned>(rows)), 256, stream, p);
+  return launch_dependent(cache8_merge_kernel<OutT, 8, 16>, dim3(static_cast<unsigned>(rows)), 256, stream, p);
+}
+
+template <typename T, typename Code, int DP, int NB, int KEYS, bool SPREAD>
 cudaError_t run(const CUtensorMap& k, const CUtensorMap& v, const Cache8Params& p, cudaStream_t stream) {
-  using L = Layout<DP, NB>;
-  auto kern = cache8_kernel<T, Code, DP, NB, SPREAD>;
+  using L = Layout<DP, NB, KEYS>;
+  auto kern = cache8_kernel<T, Code, DP, NB, KEYS, SPREAD>;
   static std::atomic<unsigned long long> ready{0};  // devices on which the kernel is set up
   cudaError_t e = once_per_device(ready, [&] {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
@@ -822,20 +833,17 @@ cudaError_t run(const CUtensorMap& k, const CUtensorMap& v, const Cache8Params& 
   kern<<<p.ctas, kThreads, L::kBytes, stream>>>(k, v, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // launched while the first kernel runs (it takes its SMs' room as that ends), waits for it inside.
-  // Rows by the thousand have few parts each; few rows have many
-  const long long rows = static_cast<long long>(p.B) * p.Hkv * p.R;
-  if (rows >= 4096) {
-    const dim3 grid(static_cast<unsigned>((rows + 7) / 8));
-    return p.out_f32 ? launch_dependent(cache8_merge_kernel<float, 1>, grid, 256, stream, p) : launch_dependent(cache8_merge_kernel<T, 1>, grid, 256, stream, p);
-  }
-  const dim3 grid(static_cast<unsigned>(rows));
-  return p.out_f32 ? launch_dependent(cache8_merge_kernel<float, 8>, grid, 256, stream, p) : launch_dependent(cache8_merge_kernel<T, 8>, grid, 256, stream, p);
+  // launched while the first kernel runs (it takes its SMs' room as that ends), waits for it inside
+  return p.out_f32 ? launch_merge<float>(p, stream) : launch_merge<T>(p, stream);
 }
 
 template <typename T, typename Code, int DP, int NB>
 cudaError_t run_s(const CUtensorMap& k, const CUtensorMap& v, const Cache8Params& p, cudaStream_t stream) {
-  return p.cluster ? run<T, Code, DP, NB, true>(k, v, p, stream) : run<T, Code, DP, NB, false>(k, v, p, stream);
+  constexpr int kKeys = NB == 1 ? 32 : 48;
+  if (p.cluster) return run<T, Code, DP, NB, kKeys, true>(k, v, p, stream);
+  if constexpr (DP == 64)
+    if (p.tile_keys == 64) return run<T, Code, DP, NB, 64, false>(k, v, p, stream);
+  return run<T, Code, DP, NB, kKeys, false>(k, v, p, stream);
 }
 
 template <typename T, typename Code>

@@ -40,13 +40,44 @@ __device__ __forceinline__ void expand16(const uint4 w, float scale, uint4* dst)
   dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
 }
 
+// One key range: the rows of a 128-row block that sees no key have no work item; O = 0, LSE = -inf. Blocks first,
+// first + step, .. of one (batch, kv head).
+__device__ __forceinline__ void unseen_rows(const Cache8Params& p, int bh, int L, int first, int step) {
+  const int es = p.out_f32 ? 4 : 2;
+  for (int rb = first; rb < (p.R + 127) / 128; rb += step) {
+    if (kv_needed_keys(L, p.Nq, p.R, rb, p.causal != 0) > 0) continue;
+    const int rows = min(128, p.R - rb * 128);
+    const size_t row = static_cast<size_t>(bh) * p.R + rb * 128;
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.o) + row * p.d * es);
+    for (int i = threadIdx.x; i < rows * p.d * es / 16; i += 256) dst[i] = make_uint4(0, 0, 0, 0);
+    if (p.lse)
+      for (int i = threadIdx.x; i < rows; i += 256) p.lse[row + i] = -INFINITY;
+  }
+}
+
 // A CTA expands 128 tokens of one (batch, kv head): 16 codes of K and of V per thread and step.
 template <typename T, typename Code>
-__global__ void __launch_bounds__(256) expand_kernel(const Cache8Params p, T* k16, __half* v16, float* v_unit, int tiles) {
+__global__ void __launch_bounds__(256) expand_kernel(const Cache8Params p, T* k16, __half* v16, float* v_unit, int tiles, bool final_rows) {
   __shared__ float s_max[8];
   const int bh = blockIdx.x / tiles, j0 = (blockIdx.x % tiles) * 128;
   const int L = cache_len(p.cache_seqlens, bh / p.Hkv, p.Nk, nullptr, false);
+  if (final_rows) unseen_rows(p, bh, L, blockIdx.x % tiles, tiles);
   if (j0 >= L) return;
+  const int chunks = p.d / 16, n = min(128, p.Nk - j0) * chunks;
+  const size_t base = (static_cast<size_t>(bh) * p.Nk + j0) * p.d;
+  const uint4* k = reinterpret_cast<const uint4*>(p.k8 + base);
+  const uint4* v = reinterpret_cast<const uint4*>(p.v8 + base);
+  uint4* ko = reinterpret_cast<uint4*>(k16 + base);
+  uint4* vo = reinterpret_cast<uint4*>(v16 + base);
+  uint4 kw[4], vw[4];  // all of a thread's codes on their way at once (128 tokens, 8 chunks of 16: four each)
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int i = u * 256 + threadIdx.x;
+    if (i < n && j0 + i / chunks < L) {
+      kw[u] = k[i];
+      vw[u] = v[i];
+    }
+  }
   // the unit: the largest scale of the blocks that hold tokens (a NaN shows in its own block's values)
   const float* vs = p.v_scale + static_cast<size_t>(bh) * p.n_blocks;
   float unit = 0.f;
@@ -58,19 +89,15 @@ __global__ void __launch_bounds__(256) expand_kernel(const Cache8Params p, T* k1
 #pragma unroll
   for (int i = 0; i < 8; ++i) unit = fmaxf(unit, s_max[i]);
   if (j0 == 0 && threadIdx.x == 0) v_unit[bh] = unit;
-  const int chunks = p.d / 16, n = min(128, p.Nk - j0) * chunks;
-  const size_t base = (static_cast<size_t>(bh) * p.Nk + j0) * p.d;
-  const uint4* k = reinterpret_cast<const uint4*>(p.k8 + base);
-  const uint4* v = reinterpret_cast<const uint4*>(p.v8 + base);
-  uint4* ko = reinterpret_cast<uint4*>(k16 + base);
-  uint4* vo = reinterpret_cast<uint4*>(v16 + base);
-  for (int i = threadIdx.x; i < n; i += 256) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int i = u * 256 + threadIdx.x;
+    if (i >= n) break;
     const int j = j0 + i / chunks;
     if (j < L) {
       const float r = unit == 0.f ? 0.f : vs[j >> p.block_shift] / unit;
-      const uint4 a = k[i], b = v[i];
-      expand16<T, Code>(a, 1.f, ko + 2 * i);
-      expand16<__half, Code>(b, r, vo + 2 * i);
+      expand16<T, Code>(kw[u], 1.f, ko + 2 * i);
+      expand16<__half, Code>(vw[u], r, vo + 2 * i);
     } else {  // the tile's rest: a weight of zero times what lies there has to be zero
       const uint4 z = make_uint4(0, 0, 0, 0);
       ko[2 * i] = ko[2 * i + 1] = vo[2 * i] = vo[2 * i + 1] = z;
@@ -78,40 +105,24 @@ __global__ void __launch_bounds__(256) expand_kernel(const Cache8Params p, T* k1
   }
 }
 
-// One key range: rows of a 128-row block that sees no key have no work item; O = 0, LSE = -inf.
-__global__ void __launch_bounds__(256) unseen_kernel(const FwdParams p, int es, bool causal) {
-  const int bh = blockIdx.x / p.n_qtiles, rb = blockIdx.x % p.n_qtiles;
-  const int L = cache_len(p.cache_seqlens, bh / p.Hkv, p.Nk, nullptr, false);
-  if (kv_needed_keys(L, p.Nq, p.R, rb, causal) > 0) return;
-  const int rows = min(128, p.R - rb * 128);
-  const size_t row = static_cast<size_t>(bh) * p.R + rb * 128;
-  uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.o) + row * p.d * es);
-  for (int i = threadIdx.x; i < rows * p.d * es / 16; i += 256) dst[i] = make_uint4(0, 0, 0, 0);
-  if (p.lse)
-    for (int i = threadIdx.x; i < rows; i += 256) p.lse[row + i] = -INFINITY;
-}
-
 template <typename T>
-cudaError_t expand(const Cache8Params& p, void* k16, void* v16, float* v_unit, attn_cache_dtype_t cache, cudaStream_t stream) {
+cudaError_t expand(const Cache8Params& p, void* k16, void* v16, float* v_unit, bool final_rows, attn_cache_dtype_t cache,
+                   cudaStream_t stream) {
   const int tiles = (p.Nk + 127) / 128;
   const int grid = p.B * p.Hkv * tiles;
   if (cache == ATTN_CACHE_I8)
-    expand_kernel<T, CodeI8><<<grid, 256, 0, stream>>>(p, static_cast<T*>(k16), static_cast<__half*>(v16), v_unit, tiles);
+    expand_kernel<T, CodeI8><<<grid, 256, 0, stream>>>(p, static_cast<T*>(k16), static_cast<__half*>(v16), v_unit, tiles, final_rows);
   else
-    expand_kernel<T, CodeE4m3><<<grid, 256, 0, stream>>>(p, static_cast<T*>(k16), static_cast<__half*>(v16), v_unit, tiles);
+    expand_kernel<T, CodeE4m3><<<grid, 256, 0, stream>>>(p, static_cast<T*>(k16), static_cast<__half*>(v16), v_unit, tiles, final_rows);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_cache8_expand(const Cache8Params& p, void* k16, void* v16, float* v_unit, attn_dtype_t dtype,
+cudaError_t launch_cache8_expand(const Cache8Params& p, void* k16, void* v16, float* v_unit, bool final_rows, attn_dtype_t dtype,
                                  attn_cache_dtype_t cache, cudaStream_t stream) {
-  return dtype == ATTN_F16 ? expand<__half>(p, k16, v16, v_unit, cache, stream) : expand<__nv_bfloat16>(p, k16, v16, v_unit, cache, stream);
-}
-
-cudaError_t launch_kv8_unseen(const FwdParams& p, bool out16, bool causal, cudaStream_t stream) {
-  unseen_kernel<<<p.B * p.Hkv * p.n_qtiles, 256, 0, stream>>>(p, out16 ? 2 : 4, causal);
-  return cudaGetLastError();
+  return dtype == ATTN_F16 ? expand<__half>(p, k16, v16, v_unit, final_rows, cache, stream)
+                           : expand<__nv_bfloat16>(p, k16, v16, v_unit, final_rows, cache, stream);
 }
 
 }  // namespace attn

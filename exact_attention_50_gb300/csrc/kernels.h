@@ -181,22 +181,28 @@ struct Cache8Params {
   int2* parts;             // [B * Hkv]: the first run of a pair that several share and their number, else (., 0)
 };
 constexpr int kCache8Rows = 64;
-// For R rows: blocks of 8 rows per warp, the warps that share a run, and the keys of a tile and CTAs (of
-// four warps) per SM that go with the former.
+// For R rows: blocks of 8 rows per warp, the warps that share a run, the CTAs (of four warps) per SM that go
+// with the former, and the keys of a tile.  With d <= 64 and at least eight tiles a run for all of the
+// GPU's warps a tile has 64 keys: its fixed costs weigh more there (8 x 8 heads of 16k-32k keys, d = 64:
+// 43.6 us, with 32 keys 52.0 us; 4 x 32 heads of 300 to 4111 keys, 2.6 such tiles a run: 21.2 and 18.5 us).
 constexpr int cache8_row_blocks(int R) { return R <= 8 ? 1 : 2; }
 constexpr int cache8_run_warps(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : 4; }
-constexpr int cache8_keys(int row_blocks) { return row_blocks == 1 ? 32 : 48; }
 constexpr int cache8_ctas_per_sm(int row_blocks) { return row_blocks == 1 ? 3 : 2; }
+constexpr int cache8_keys(long long pairs, int R, int Nk, int d) {
+  const int nb = cache8_row_blocks(R), workers = 4 / cache8_run_warps(R) * cache8_ctas_per_sm(nb) * 152;
+  if (d <= 64 && pairs * ((static_cast<long long>(Nk) + 63) / 64) >= 8LL * workers) return 64;
+  return nb == 1 ? 32 : 48;
+}
 cudaError_t launch_cache8_fwd(const CUtensorMap& k, const CUtensorMap& v, const Cache8Params& p, attn_dtype_t dtype,
                               attn_cache_dtype_t cache, cudaStream_t stream);
 // Many rows: K's codes in dtype and V's values in fp16, in units of the largest scale of their head
 // (v_unit [B*Hkv]), [B*Hkv, Nk, d] each, for the tokens that the caches hold and zeros behind them up to a
-// tile's end; then the tcgen05 forward in kModeKv8 on those, and with
-// one key range the rows of which it computed nothing.
-cudaError_t launch_cache8_expand(const Cache8Params& p, void* k16, void* v16, float* v_unit, attn_dtype_t dtype,
+// tile's end; and, when the forward writes final rows (one key range), those of which it computes nothing.
+// Then the tcgen05 forward in kModeKv8 on that.
+cudaError_t launch_cache8_expand(const Cache8Params& p, void* k16, void* v16, float* v_unit, bool final_rows, attn_dtype_t dtype,
                                  attn_cache_dtype_t cache, cudaStream_t stream);
 cudaError_t launch_fwd_kv8(const FwdMaps& maps, const FwdParams& p, attn_dtype_t dtype, bool causal, cudaStream_t stream);
-cudaError_t launch_kv8_unseen(const FwdParams& p, bool out16, bool causal, cudaStream_t stream);
+
 cudaError_t launch_cache8_none(const Cache8Params& p, cudaStream_t stream);
 
 struct WeightParams {
