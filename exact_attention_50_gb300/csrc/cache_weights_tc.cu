@@ -410,7 +410,7 @@ cudaError_t run(const CUtensorMap& q, const CUtensorMap& k, const WeightParams& 
   });
   if (e != cudaSuccess) return e;
   const long long items = static_cast<long long>(p.B) * p.Hkv * ((p.Nk + 255) / 256);
-  const int grid = static_cast<int>(std::min<long long>(items * split, 152));
+  const int grid = static_cast<int>(SPLIT ? items * split : std::min<long long>(items, 152));
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = split;
@@ -432,7 +432,11 @@ cudaError_t launch_cache_weights_tc(const CUtensorMap& q, const CUtensorMap& k, 
   const bool few = p.R <= q_rows;
   const long long items = static_cast<long long>(p.B) * p.Hkv * ((p.Nk + 255) / 256);
   int split = 1;
-  while (!few && split < 8 && items * 2 * split <= 152 && 2 * split <= (p.R + q_rows - 1) / q_rows) split *= 2;
+  const int q_tiles = (p.R + q_rows - 1) / q_rows;
+  while (!few && split < 8 && items * 2 * split <= 152 && 2 * split <= q_tiles) split *= 2;
+  // the first keys of a causal prompt have twice the average's Q tiles: two CTAs for them, the light ones
+  // in a second wave (two prompts of 2048: 70 -> 59 us, one of 4096: 140 -> 94; without a mask 43 -> 52)
+  if (split == 1 && p.causal && items <= 152 && q_tiles >= 16) split = 2;
   auto pick = [&](auto bf16, auto dp) {
     constexpr bool kB = decltype(bf16)::value;
     constexpr int kD = decltype(dp)::value;
