@@ -183,6 +183,15 @@ def test_attend_prefill(dev, cache, Nq, Nk):
 def test_attend_many_short_sequences(dev):
     lens = [(37 * b) % 130 for b in range(120)]
     run_attend(dev, 120, 8, 4, 1, 130, 128, 64, "bf16", "i8", lens, True, seed=7)
+    run_attend(dev, 700, 2, 1, 1, 40, 64, 16, "f16", "e4m3", [(7 * b) % 41 for b in range(700)], True, seed=8)
+
+
+@pytest.mark.parametrize("Hq,Nq,block,dtype", [(8, 1, 64, "bf16"), (8, 3, 16, "f16"), (32, 4, 32, "bf16")])
+def test_attend_long_caches_of_64_columns(dev, Hq, Nq, block, dtype):
+    """Enough tiles for 64 keys each."""
+    lens = [30011, 1, 64, 29000, 65, 30011, 7]
+    run_attend(dev, 7, Hq, 8, Nq, 30011, 64, block, dtype, "i8", lens, True, seed=Nq)
+    run_attend(dev, 7, Hq, 8, Nq, 30011, 48, block, dtype, "e4m3", lens, False, seed=Nq)
 
 
 @pytest.mark.parametrize("cache,d", [("i8", 128), ("e4m3", 64)])
@@ -242,21 +251,22 @@ def test_attend_reports_bad_lengths(dev, Nq):
         assert bool(torch.isneginf(lse[1]).all()) and bool((o[1] == 0).all()) and bool((o[0] == 1).all())
 
 
-def test_attend_in_graphs_and_on_other_streams(dev):
+@pytest.mark.parametrize("Nq,Nk", [(1, 2000), (1, 30000), (100, 2000)])
+def test_attend_in_graphs_and_on_other_streams(dev, Nq, Nk):
     """Captured once and replayed with other lengths and other codes; two streams at a time, each
     call with its own workspace; a caller's workspace."""
-    B, Hq, Hkv, Nk, d = 3, 8, 2, 2000, 128
-    q = torch.randn(B, Hq, 1, d, device=dev).bfloat16()
+    B, Hq, Hkv, d = 3, 8, 2, 128
+    q = torch.randn(B, Hq, Nq, d, device=dev).bfloat16()
     k8, ks = P.quantise(rows(21, (B, Hkv, Nk, d), dev), 64, "i8")
     v8, vs = P.quantise(rows(22, (B, Hkv, Nk, d), dev), 64, "i8")
-    cl = torch.tensor([2000, 700, 1], dtype=torch.int32, device=dev)
-    ws = torch.empty(A.kvcache8_workspace_bytes(B, Hq, Hkv, 1, Nk, d), dtype=torch.uint8, device=dev)
+    cl = torch.tensor([Nk, 700, 1], dtype=torch.int32, device=dev)
+    ws = torch.empty(max(1, A.kvcache8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d)), dtype=torch.uint8, device=dev)
     A.fwd_kvcache8(q, k8, v8, ks, vs, cl, True, workspace=ws)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         o, lse = A.fwd_kvcache8(q, k8, v8, ks, vs, cl, True, workspace=ws)
-    for lens in ([2000, 700, 1], [5, 1999, 0], [64, 65, 1500]):
+    for lens in ([Nk, 700, 1], [5, Nk - 1, 0], [64, 65, 1500]):
         cl.copy_(torch.tensor(lens, dtype=torch.int32))
         v8.neg_()
         ws.fill_(255)  # what it holds does not matter

@@ -68,6 +68,8 @@ def test_weights_lengths(dev, dtype, Nk):
 def test_weights_scale_and_many_rows(dev):
     run_weights(dev, 2, 4, 4, 600, 520, 64, "bf16", [520, 400], True, seed=3, scale=0.4)
     run_weights(dev, 1, 32, 1, 129, 1111, 128, "f16", None, True, seed=4)
+    run_weights(dev, 4, 16, 4, 1200, 1200, 64, "bf16", [1200, 1100, 300, 0], True, seed=5)  # two CTAs per 256 keys
+    run_weights(dev, 20, 8, 8, 300, 700, 128, "bf16", [700 - 30 * b for b in range(20)], True, seed=6)  # several items a CTA
 
 
 def test_weights_sum_to_the_number_of_rows_after_the_forward(dev):
@@ -155,6 +157,44 @@ def test_evict_lengths(dev, Nk, keep, recent):
     got = A.kvcache_evict(k, v, w, keep, recent)
     status_ok()
     check_evict(k, v, w, keep, recent, None, got, tuple(torch.zeros_like(x) for x in got[:2]))
+
+
+@pytest.mark.parametrize("Nk", [3000, 40000, 300000])
+def test_evict_many_equal_weights(dev, Nk):
+    """More keys of one weight, or of nearly one, than any list holds."""
+    k, v = randn(4, (1, 2, Nk, 16), dev, torch.bfloat16), randn(5, (1, 2, Nk, 16), dev, torch.bfloat16)
+    w = torch.full((1, 2, Nk), 0.5, device=dev)
+    w[0, 1] += 1e-6 * torch.randint(0, 30, (Nk,), generator=torch.Generator(dev).manual_seed(1), device=dev)
+    w[0, 0, 100:120] = 2.0
+    got = A.kvcache_evict(k, v, w, Nk // 3, 10)
+    status_ok()
+    check_evict(k, v, w, Nk // 3, 10, None, got, tuple(torch.zeros_like(x) for x in got[:2]))
+
+
+def test_offsets_past_32_bits(dev):
+    """Caches of more than 2^32 bytes, the keys that matter in the last head's last rows."""
+    Hkv, Nk, d = 3, 2 ** 23, 128  # 2.1 GB of keys a head
+    k = torch.zeros(1, Hkv, Nk, d, dtype=torch.bfloat16, device=dev)
+    k[0, :, -2:] = randn(7, (Hkv, 2, d), dev, torch.bfloat16)
+    q = randn(8, (1, 6, 2, d), dev, torch.bfloat16)
+    lse = torch.full((1, 6, 2), 3.0, device=dev)
+    w = A.kvcache_weights(q, k, lse, None, False)
+    status_ok()
+    for h in range(Hkv):
+        s = q[0, 2 * h:2 * h + 2].double().reshape(4, d) @ k[0, h, -2:].double().T / d ** 0.5
+        want = torch.exp(s - 3.0).sum(0)
+        assert float((w[0, h, -2:].double() / want - 1).abs().max()) < 1e-5
+        assert float((w[0, h, :-2].double() / (4 * np.exp(-3.0)) - 1).abs().max()) < 1e-5
+    w.zero_()
+    w[0, :, 5], w[0, :, -3], w[0, :, -2] = 1.0, 2.0, 3.0
+    v = k.clone()
+    v[0, :, -3] = 7.0
+    ko, vo, wo, index, lens = A.kvcache_evict(k, v, w, 3, 1)
+    status_ok()
+    at = [5, Nk - 3, Nk - 2, Nk - 1]
+    assert index[0].tolist() == [at] * Hkv and lens.tolist() == [4]
+    for h in range(Hkv):
+        assert torch.equal(ko[0, h], k[0, h, at]) and torch.equal(vo[0, h], v[0, h, at])
 
 
 def test_evict_bad_lengths_empty_cache_and_refusals(dev):
