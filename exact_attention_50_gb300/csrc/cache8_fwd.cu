@@ -5,9 +5,9 @@
 // keys.  With code c and block scales ks, vs:
 //   s_j = scale ks_j (q . ck_j), masked;  l = sum_j exp(s_j - m);  o = sum_j exp(s_j - m) vs_j cv_j / l.
 //
-// Work: the caches are cut into tiles of 32 keys (48 for more than 8 rows, 64 for many of 64 columns), and all tiles of all
-// (batch, kv head) pairs, one after the other, are dealt in equal runs to the workers, whatever the
-// sequences' lengths.  A worker is one warp per block of rows, four warps a CTA, as many CTAs as
+// Work: the caches are cut into tiles of 32 keys (48 for more than 8 rows, 64 for long caches of 64
+// columns), and all tiles of all (batch, kv head) pairs, one after the other, are dealt in equal runs
+// to the workers, whatever the sequences' lengths.  A worker is one warp per block of rows, four warps a CTA, as many CTAs as
 // fit.  A run may begin and end inside a pair: such parts go to the workspace, normalised with
 // their log-sum-exp, and a second kernel merges them; a pair that lies within one run is
 // finished by its worker.  (Warps of a CTA that shared a run and joined their sums in shared memory

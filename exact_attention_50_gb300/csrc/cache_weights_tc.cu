@@ -29,10 +29,13 @@
 namespace attn {
 namespace {
 
-constexpr int kMaxStages = 12;  // of either ring
+constexpr int kMaxStages = 12;  // of the Q ring, and of both K rings together
+constexpr int kRing = kMaxStages / 2;
 constexpr int kNl = 4;          // stages of row terms; even: a stage is read by the groups of one buffer
 
-// Shared memory: the K ring (128-key tiles), the Q ring, then the fixed part.
+// Shared memory: a ring of 128-key tiles for each of an item's two, the Q ring, then the fixed part.  Every
+// ring's barriers are waited for in every turn by the same threads: an issuer that waited only for its
+// own tiles of a common K ring could be two turns off, where the parity says nothing.
 struct Smem {
   static constexpr int kNlOff = 0;                 // [kNl][128] float
   static constexpr int kLimOff = kNlOff + kNl * 512;   // [kNl][128] int
@@ -92,8 +95,8 @@ __global__ void __launch_bounds__(640, 1)
     return;
   }
   const int q_bytes = qn * DP * 2;
-  uint8_t* const sK = smem;
-  uint8_t* const sQ = smem + k_stages * kTileK;
+  uint8_t* const sK = smem;  // [key tile][stage]
+  uint8_t* const sQ = smem + 2 * k_stages * kTileK;
   uint8_t* const fixed = sQ + q_stages * q_bytes;
   float* const s_nl = reinterpret_cast<float*>(fixed + Smem::kNlOff);
   int* const s_lim = reinterpret_cast<int*>(fixed + Smem::kLimOff);
@@ -165,7 +168,7 @@ __global__ void __launch_bounds__(640, 1)
     if (lane == 0) {
       tma_prefetch_desc(&tmQ);
       tma_prefetch_desc(&tmK);
-      uint32_t nk = 0, nq = 0;  // tiles issued
+      uint32_t nk0 = 0, nk1 = 0, nq = 0;  // tiles issued
       bool ok = true;
       for (int k = 0; ok && k * G < n_items; ++k) {
         const int idx = snake<SPLIT>(k, split);
@@ -175,12 +178,13 @@ __global__ void __launch_bounds__(640, 1)
         int rb = first_tile(it);
         if (rb >= n_rb) continue;
         for (int h = 0; ok && h < 2 && it.key0 + 128 * h < it.L; ++h) {
-          const uint32_t st = nk % k_stages;
+          const uint32_t nk = h ? nk1 : nk0, st = h * kRing + nk % k_stages;
           if (nk >= static_cast<uint32_t>(k_stages) && !mbar_wait(k_empty + st, ((nk / k_stages) - 1) & 1, abort_flag, p.status)) { ok = false; break; }
           mbar_expect_tx(k_full + st, kTileK);
           for (int c = 0; c < kChunks; ++c)
-            tma_load_3d(sK + st * kTileK + c * 128 * 128, &tmK, k_full + st, c * 64, it.key0 + 128 * h, it.bh);
-          ++nk;
+            tma_load_3d(sK + (h * k_stages + nk % k_stages) * kTileK + c * 128 * 128, &tmK, k_full + st, c * 64, it.key0 + 128 * h, it.bh);
+          nk0 += 1 - h;
+          nk1 += h;
         }
         for (; ok && rb < n_rb; rb = next_tile(it, rb)) {
           const uint32_t st = nq % q_stages;
@@ -191,7 +195,10 @@ __global__ void __launch_bounds__(640, 1)
         }
       }
       if (!ok || abort_read(abort_flag)) {  // let the copies land before the shared memory goes away
-        for (uint32_t i = nk > static_cast<uint32_t>(k_stages) ? nk - k_stages : 0; i < nk; ++i) mbar_drain(k_full + i % k_stages, (i / k_stages) & 1);
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t nk = h ? nk1 : nk0;
+          for (uint32_t i = nk > static_cast<uint32_t>(k_stages) ? nk - k_stages : 0; i < nk; ++i) mbar_drain(k_full + h * kRing + i % k_stages, (i / k_stages) & 1);
+        }
         for (uint32_t i = nq > static_cast<uint32_t>(q_stages) ? nq - q_stages : 0; i < nq; ++i) mbar_drain(q_full + i % q_stages, (i / q_stages) & 1);
       }
     }
@@ -202,7 +209,7 @@ __global__ void __launch_bounds__(640, 1)
       const int h = warp - kSums - 1;
       const uint32_t id = idesc_f16(BF16, false, false, 128, qn);
       const uint64_t dK = smem_desc_sw128(smem_u32(sK), 16, 1024), dQ = smem_desc_sw128(smem_u32(sQ), 16, 1024);
-      uint32_t nk = 0, nq = 0, ns0 = 0, ns1 = 0;  // K and Q tiles passed; tiles put into either buffer
+      uint32_t nk = 0, nq = 0, ns0 = 0, ns1 = 0;  // this ring's K tiles and the Q tiles passed; tiles put into either buffer
       bool ok = true;
       for (int k = 0; ok && k * G < n_items; ++k) {
         const int idx = snake<SPLIT>(k, split);
@@ -212,8 +219,8 @@ __global__ void __launch_bounds__(640, 1)
         int rb = first_tile(it);
         if (rb >= n_rb) continue;
         const int halves = it.key0 + 128 < it.L ? 2 : 1;
-        const uint32_t ks = (nk + h) % k_stages;
-        if (h < halves && !mbar_wait(k_full + ks, ((nk + h) / k_stages) & 1, abort_flag, p.status)) { ok = false; break; }
+        const uint32_t ks = nk % k_stages;
+        if (h < halves && !mbar_wait(k_full + h * kRing + ks, (nk / k_stages) & 1, abort_flag, p.status)) { ok = false; break; }
         for (; rb < n_rb; rb = next_tile(it, rb), ++nq) {
           const uint32_t qs = nq % q_stages, b = nq & 1;
           if (!mbar_wait(q_full + qs, (nq / q_stages) & 1, abort_flag, p.status)) { ok = false; break; }
@@ -226,7 +233,7 @@ __global__ void __launch_bounds__(640, 1)
           ns0 += 1 - b;
           ns1 += b;
           tc_fence_after();
-          const uint64_t kx = dK + ((ks * kTileK) >> 4), qx = dQ + ((qs * q_bytes) >> 4);
+          const uint64_t kx = dK + (((h * k_stages + ks) * kTileK) >> 4), qx = dQ + ((qs * q_bytes) >> 4);
 #pragma unroll
           for (int s = 0; s < DP / 16; ++s)
             mma_ss(tmem + h * 256 + b * 128, kx + (((s >> 2) * 128 * 128 + (s & 3) * 32) >> 4),
@@ -235,8 +242,10 @@ __global__ void __launch_bounds__(640, 1)
           mma_commit(q_empty + qs);
         }
         if (!ok) break;
-        if (h < halves) mma_commit(k_empty + ks);
-        nk += halves;
+        if (h < halves) {
+          mma_commit(k_empty + h * kRing + ks);
+          ++nk;
+        }
       }
       if (!ok) {
         mma_commit(drain + h);  // every MMA issued completes before this arrives
@@ -398,11 +407,12 @@ __global__ void __launch_bounds__(640, 1)
 
 template <bool BF16, int DP, bool FEW, bool SPLIT>
 cudaError_t run(const CUtensorMap& q, const CUtensorMap& k, const WeightParams& p, int qn, int split, cudaStream_t stream) {
-  // 192 KB for the rings.  Few rows: K has most of it, Q four small stages.
-  constexpr int kTileK = 128 * DP * 2, kData = 192 * 1024;
+  // 208 KB for the rings: two Q stages (more gain nothing), the rest for K, six tiles of 128 columns with few
+  // rows and four with many
+  constexpr int kTileK = 128 * DP * 2, kData = 208 * 1024;
   const int q_bytes = qn * DP * 2;
-  const int q_stages = qn > 64 ? kData / 2 / kTileK : 4;
-  const int k_stages = std::min(kMaxStages, (kData - q_stages * q_bytes) / kTileK);
+  const int q_stages = 2;
+  const int k_stages = std::min(kRing, (kData - q_stages * q_bytes) / (2 * kTileK));
   auto kern = weights_tc_kernel<BF16, DP, FEW, SPLIT>;
   static std::atomic<unsigned long long> ready{0};
   cudaError_t e = once_per_device(ready, [&] {
@@ -418,7 +428,7 @@ cudaError_t run(const CUtensorMap& q, const CUtensorMap& k, const WeightParams& 
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(640);
-  cfg.dynamicSmemBytes = k_stages * kTileK + q_stages * q_bytes + Smem::kBytes;
+  cfg.dynamicSmemBytes = 2 * k_stages * kTileK + q_stages * q_bytes + Smem::kBytes;
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = split > 1 ? 1 : 0;

@@ -72,6 +72,21 @@ def test_weights_scale_and_many_rows(dev):
     run_weights(dev, 20, 8, 8, 300, 700, 128, "bf16", [700 - 30 * b for b in range(20)], True, seed=6)  # several items a CTA
 
 
+@pytest.mark.parametrize("Hq,Nq,d", [(8, 1, 128), (8, 30, 128), (4, 200, 64), (8, 1, 64)])
+def test_weights_long_caches(dev, Hq, Nq, d):
+    """Dozens of items per CTA, some of them with keys in their first half only: every ring turns
+    many times, and its readers at different speeds.  The same bits each time."""
+    lens = [200001, 130, 77000, 100, 256 * 300 + 128, 1, 199999]
+    run_weights(dev, 7, Hq, 4, Nq, 200001, d, "bf16", lens, True, seed=Nq)
+    q, k = randn(1, (7, Hq, Nq, d), dev, torch.bfloat16), randn(2, (7, 4, 200001, d), dev, torch.bfloat16)
+    lse = torch.full((7, Hq, Nq), 11.0, device=dev)
+    cl = torch.tensor(lens, dtype=torch.int32, device=dev)
+    want = A.kvcache_weights(q, k, lse, cl)
+    for _ in range(20):
+        assert torch.equal(A.kvcache_weights(q, k, lse, cl), want)
+    status_ok()
+
+
 def test_weights_sum_to_the_number_of_rows_after_the_forward(dev):
     """With the forward's own LSE: each row's weights add up to one, so the sum over the keys is the
     number of (head, query) rows that see any key."""
