@@ -223,40 +223,30 @@ def fwd_kvcache(q, k_cache, v_cache, cache_seqlens=None, causal: bool = False, s
     return o, lse
 
 
-def _cache_args(name: str, tensors, dtypes, names) -> int:
-    """Checks of the cache calls: contiguous tensors on one GPU, that of the first, called `name`; a
-    dtype or None for each.  Returns the GPU's index.  Optional tensors that are None are left out
-    by the caller."""
-    try:
-        dev = tensors[0].get_device()
-        ok = dev >= 0
-        for t, dtype in zip(tensors, dtypes):
-            if t.get_device() != dev or not t.is_contiguous() or (dtype is not None and t.dtype is not dtype):
-                ok = False
-                break
-        if ok:
-            return dev
-    except AttributeError:  # not a tensor
-        pass
-    for t, n, dtype in zip(tensors, names, dtypes):  # say what is wrong
-        _require(t, n, dtype)
-        if t.device != tensors[0].device:
-            raise ValueError(f"{n} must be on {name}'s device")
-    raise TypeError("tensors on a CUDA device are wanted")
+def _fit(dev: int, *tensors) -> bool:
+    """Contiguous tensors on GPU `dev`; None stands for an optional one that is not given."""
+    for t in tensors:
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            return False
+    return dev >= 0
 
 
-def _optional(tensors, dtypes, names, *more):
-    """The argument lists with the optional (tensor, dtype, name) that are there behind them."""
-    for t, dtype, n in more:
-        if t is not None:
-            tensors, dtypes, names = tensors + (t,), dtypes + (dtype,), names + (n,)
-    return tensors, dtypes, names
+def _explain(*named):
+    """Raises what is wrong with the arguments of a cache call: (tensor, name, dtype, optional) each,
+    contiguous tensors on the first one's GPU."""
+    for t, name, dtype, optional in named:
+        if t is None and optional:
+            continue
+        _require(t, name, dtype)
+        if t.device != named[0][0].device:
+            raise ValueError(f"{name} must be on {named[0][1]}'s device")
+    raise TypeError("the tensors' types do not fit together")
 
 
 def _on_device(dev: int, call, *args) -> int:
     """call(*args, stream) with `dev` as the current device, on its current stream."""
     stream = torch._C._cuda_getCurrentRawStream(dev)
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         return call(*args, stream)
     with torch.cuda.device(dev):
         return call(*args, stream)
@@ -271,7 +261,9 @@ def _lens_ptr(t, name: str, B: int):
 
 
 def _check_cache8(k8, v8, k_scale, v_scale, block: int):
-    if k8.dtype not in _DT8:
+    """Shapes of an 8-bit cache; returns them and the C code of its type."""
+    code = _DT8.get(k8.dtype)
+    if code is None:
         raise TypeError(f"unsupported cache dtype {k8.dtype}: int8 or float8_e4m3fn")
     if block not in (16, 32, 64, 128):
         raise ValueError("block must be 16, 32, 64 or 128")
@@ -279,9 +271,10 @@ def _check_cache8(k8, v8, k_scale, v_scale, block: int):
     if len(shape) != 4 or shape != v8.shape:
         raise ValueError("k8 and v8 must be [B,Hkv,Nk,d]")
     B, Hkv, Nk, d = shape
-    if k_scale.shape != (B, Hkv, -(-Nk // block)) or v_scale.shape != k_scale.shape:
+    scales = (B, Hkv, -(-Nk // block))
+    if k_scale.shape != scales or v_scale.shape != scales:
         raise ValueError("k_scale and v_scale must be [B,Hkv,ceil(Nk/block)]")
-    return B, Hkv, Nk, d
+    return B, Hkv, Nk, d, code
 
 
 def kvcache8_append(k8, v8, k_scale, v_scale, k_new, v_new, cache_seqlens=None, new_seqlens=None, block: int = 64):
@@ -290,21 +283,27 @@ def kvcache8_append(k8, v8, k_scale, v_scale, k_new, v_new, cache_seqlens=None, 
     go behind its first cache_seqlens[b] (int32 [B] on the device; None: an empty cache), the
     first new_seqlens[b] of them (None: Nn); the caller advances the lengths.  block: tokens per
     scale, 16, 32, 64 or 128."""
-    _require(k8, "k8")
-    _require(k_new, "k_new")
-    dev = _cache_args("k8", *_optional((k8, v8, k_scale, v_scale, k_new, v_new),
-                                       (None, k8.dtype, torch.float32, torch.float32, None, k_new.dtype),
-                                       ("k8", "v8", "k_scale", "v_scale", "k_new", "v_new"),
-                                       (cache_seqlens, torch.int32, "cache_seqlens"),
-                                       (new_seqlens, torch.int32, "new_seqlens")))
-    B, Hkv, Nk, d = _check_cache8(k8, v8, k_scale, v_scale, block)
+    f32, i32 = torch.float32, torch.int32
+    try:
+        dev = k8.get_device()
+        fit = (_fit(dev, k8, v8, k_scale, v_scale, k_new, v_new, cache_seqlens, new_seqlens) and v8.dtype is k8.dtype
+               and k_scale.dtype is f32 and v_scale.dtype is f32 and v_new.dtype is k_new.dtype
+               and (cache_seqlens is None or cache_seqlens.dtype is i32) and (new_seqlens is None or new_seqlens.dtype is i32))
+    except AttributeError:  # not a tensor
+        fit = False
+    if not fit:
+        _explain((k8, "k8", None, False), (v8, "v8", getattr(k8, "dtype", None), False), (k_scale, "k_scale", f32, False),
+                 (v_scale, "v_scale", f32, False), (k_new, "k_new", None, False),
+                 (v_new, "v_new", getattr(k_new, "dtype", None), False), (cache_seqlens, "cache_seqlens", i32, True),
+                 (new_seqlens, "new_seqlens", i32, True))
+    B, Hkv, Nk, d, code = _check_cache8(k8, v8, k_scale, v_scale, block)
     shape = k_new.shape
     if len(shape) != 4 or shape != v_new.shape or shape[0] != B or shape[1] != Hkv or shape[3] != d:
         raise ValueError("k_new and v_new must be [B,Hkv,Nn,d]")
     st = _on_device(dev, _lib.attn_kvcache8_append, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                     k_new.data_ptr(), v_new.data_ptr(), _lens_ptr(cache_seqlens, "cache_seqlens", B),
                     _lens_ptr(new_seqlens, "new_seqlens", B), B, Hkv, shape[2], Nk, d, block, _dtype_code(k_new),
-                    _DT8[k8.dtype])
+                    code)
     _lib._check(st, "attn_kvcache8_append")
 
 
@@ -320,12 +319,18 @@ def fwd_kvcache8(q, k8, v8, k_scale, v_scale, cache_seqlens=None, causal: bool =
     v_scale and block as kvcache8_append writes them; cache_seqlens int32 [B] on the device (None:
     Nk tokens each).  Calls that may run at the same time need a workspace each.  Returns
     (o [B,Hq,Nq,d], lse [B,Hq,Nq] or None)."""
-    _require(q, "q")
-    _require(k8, "k8")
-    dev = _cache_args("q", *_optional((q, k8, v8, k_scale, v_scale), (None, None, k8.dtype, torch.float32, torch.float32),
-                                      ("q", "k8", "v8", "k_scale", "v_scale"), (cache_seqlens, torch.int32, "cache_seqlens"),
-                                      (workspace, None, "workspace")))
-    B, Hkv, Nk, d = _check_cache8(k8, v8, k_scale, v_scale, block)
+    f32, i32 = torch.float32, torch.int32
+    try:
+        dev = q.get_device()
+        fit = (_fit(dev, q, k8, v8, k_scale, v_scale, cache_seqlens, workspace) and v8.dtype is k8.dtype
+               and k_scale.dtype is f32 and v_scale.dtype is f32 and (cache_seqlens is None or cache_seqlens.dtype is i32))
+    except AttributeError:  # not a tensor
+        fit = False
+    if not fit:
+        _explain((q, "q", None, False), (k8, "k8", None, False), (v8, "v8", getattr(k8, "dtype", None), False),
+                 (k_scale, "k_scale", f32, False), (v_scale, "v_scale", f32, False),
+                 (cache_seqlens, "cache_seqlens", i32, True), (workspace, "workspace", None, True))
+    B, Hkv, Nk, d, code = _check_cache8(k8, v8, k_scale, v_scale, block)
     shape = q.shape
     if len(shape) != 4 or shape[0] != B or shape[3] != d:
         raise ValueError("q must be [B,Hq,Nq,d], with the cache's batch and head_dim")
@@ -340,8 +345,7 @@ def fwd_kvcache8(q, k8, v8, k_scale, v_scale, cache_seqlens=None, causal: bool =
                     v_scale.data_ptr(), _lens_ptr(cache_seqlens, "cache_seqlens", B), o.data_ptr(),
                     lse.data_ptr() if with_lse else None, None if workspace is None else workspace.data_ptr(),
                     0 if workspace is None else workspace.nbytes, B, Hq, Hkv, Nq, Nk, d, block, causal,
-                    _scale_arg(scale), _dtype_code(q), _DT8[k8.dtype],
-                    _lib.ATTN_FLAG_OUT_F32 if out_f32 else 0)
+                    _scale_arg(scale), _dtype_code(q), code, _lib.ATTN_FLAG_OUT_F32 if out_f32 else 0)
     _lib._check(st, "attn_fwd_kvcache8")
     return o, lse
 
@@ -352,10 +356,17 @@ def kvcache_weights(q, k_cache, lse, cache_seqlens=None, causal: bool = False, s
     causal and scale as given to fwd_kvcache (or fwd), and lse [B,Hq,Nq] as it returned it.
     weights float32 [B,Hkv,Nk]: what earlier queries added up to (None: zeros).  out: where to
     write (may be weights).  Returns float32 [B,Hkv,Nk]."""
-    _require(q, "q")
-    dev = _cache_args("q", *_optional((q, k_cache, lse), (None, q.dtype, torch.float32), ("q", "k_cache", "lse"),
-                                      (cache_seqlens, torch.int32, "cache_seqlens"), (weights, torch.float32, "weights"),
-                                      (out, torch.float32, "out")))
+    f32, i32 = torch.float32, torch.int32
+    try:
+        dev = q.get_device()
+        fit = (_fit(dev, q, k_cache, lse, cache_seqlens, weights, out) and k_cache.dtype is q.dtype and lse.dtype is f32
+               and (cache_seqlens is None or cache_seqlens.dtype is i32) and (weights is None or weights.dtype is f32)
+               and (out is None or out.dtype is f32))
+    except AttributeError:  # not a tensor
+        fit = False
+    if not fit:
+        _explain((q, "q", None, False), (k_cache, "k_cache", getattr(q, "dtype", None), False), (lse, "lse", f32, False),
+                 (cache_seqlens, "cache_seqlens", i32, True), (weights, "weights", f32, True), (out, "out", f32, True))
     if q.dim() != 4 or k_cache.dim() != 4:
         raise ValueError("q must be [B,Hq,Nq,d] and k_cache [B,Hkv,Nk,d]")
     B, Hq, Nq, d = q.shape
@@ -396,10 +407,16 @@ def kvcache_evict(k_cache, v_cache, weights, keep: int, recent: int, cache_seqle
     if out is None:
         out = tuple(torch.zeros((B, Hkv, keep + recent, d), dtype=k_cache.dtype, device=device) for _ in range(2))
     k_out, v_out = out
-    dt = k_cache.dtype
-    dev = _cache_args("k_cache", *_optional((k_cache, v_cache, weights, k_out, v_out), (dt, dt, torch.float32, dt, dt),
-                                            ("k_cache", "v_cache", "weights", "k_out", "v_out"),
-                                            (cache_seqlens, torch.int32, "cache_seqlens")))
+    dt, f32, i32 = k_cache.dtype, torch.float32, torch.int32
+    try:
+        dev = k_cache.get_device()
+        fit = (_fit(dev, k_cache, v_cache, weights, k_out, v_out, cache_seqlens) and v_cache.dtype is dt and weights.dtype is f32
+               and k_out.dtype is dt and v_out.dtype is dt and (cache_seqlens is None or cache_seqlens.dtype is i32))
+    except AttributeError:  # not a tensor
+        fit = False
+    if not fit:
+        _explain((k_cache, "k_cache", None, False), (v_cache, "v_cache", dt, False), (weights, "weights", f32, False),
+                 (k_out, "k_out", dt, False), (v_out, "v_out", dt, False), (cache_seqlens, "cache_seqlens", i32, True))
     if v_cache.shape != k_cache.shape or weights.shape != (B, Hkv, Nk):
         raise ValueError("k_cache and v_cache must be [B,Hkv,Nk,d] and weights [B,Hkv,Nk]")
     if k_out.dim() != 4 or k_out.shape != v_out.shape or k_out.shape[:2] != (B, Hkv) or k_out.shape[3] != d:

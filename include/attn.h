@@ -234,7 +234,8 @@ attn_status_t attn_fwd_kvcache(const void* q, const void* k_cache, const void* v
  * computation, the decode phase), so its bytes bound the time; these calls hold them in 8 bits.
  *   k8, v8           [B, Hkv, Nk, d] codes of cache_dtype: int8 (codes -127 .. 127) or e4m3
  *   k_scale, v_scale [B, Hkv, ceil(Nk / block)] float32: one scale per head and block of `block`
- *                    consecutive tokens; token j stands for code * scale[j / block]
+ *                    consecutive tokens, not negative; token j stands for
+ *                    code * scale[j / block]
  *   block            16, 32, 64 or 128
  */
 typedef enum { ATTN_CACHE_I8 = 0, ATTN_CACHE_E4M3 = 1 } attn_cache_dtype_t;
@@ -252,7 +253,7 @@ typedef enum { ATTN_CACHE_I8 = 0, ATTN_CACHE_E4M3 = 1 } attn_cache_dtype_t;
  * nothing.  An infinity or NaN among a block's tokens makes its scale that and the block reads back
  * as infinities and NaN.  Blocks and tokens outside L .. L + n - 1 are left as they are, but for
  * that recoding; the scale of a block without tokens is never read.
- *   k_new, v_new   [B, Hkv, Nn, d] (dtype: float32, float16 or bfloat16)
+ *   k_new, v_new   [B, Hkv, Nn, d] (dtype: float32, float16 or bfloat16), Nn <= Nk
  *   cache_seqlens  DEVICE int32 [B], or NULL: empty caches (L = 0)
  *   new_seqlens    DEVICE int32 [B], 0 <= new_seqlens[b] <= Nn, or NULL: Nn each
  * A batch with a length out of its range, or L + n > Nk, is left untouched and
@@ -271,6 +272,8 @@ attn_status_t attn_kvcache8_append(void* k8, void* v8, float* k_scale, float* v_
  *   workspace  DEVICE, at least attn_fwd_kvcache8_workspace_bytes(...) bytes, 256-byte aligned
  *              (0 bytes for small problems: it may then be NULL); contents on entry are ignored,
  *              on exit undefined.  Calls that may run at the same time need one each.
+ * Tokens, codes and scales past a cache's length may hold anything; an infinity or NaN among the
+ * values within it can reach rows whose causal mask hides that token (0 * NaN).
  */
 size_t attn_fwd_kvcache8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d);
 attn_status_t attn_fwd_kvcache8(const void* q, const void* k8, const void* v8, const float* k_scale,
