@@ -289,7 +289,8 @@ attn_status_t attn_fwd_kvcache8(const void* q, const void* k8, const void* v8, c
  *                          of exp(scale * Q_gi . K_j - lse_gi)
  *   q, k_cache, cache_seqlens, causal, scale, dtype: as given to attn_fwd_kvcache (or, with
  *                Nq == Nk and no lengths, to attn_fwd)
- *   lse          its float32 LSE [B, Hq, Nq]; a row with LSE -inf (no key) adds nothing
+ *   lse          its float32 LSE [B, Hq, Nq]; a row with LSE -inf (no key, or a padded query)
+ *                adds nothing, whatever its q holds
  *   weights_in   [B, Hkv, Nk] float32, or NULL: zeros
  *   weights_out  [B, Hkv, Nk] float32; may be weights_in.  Keys past a cache's length get
  *                weights_in (0 when it is NULL)

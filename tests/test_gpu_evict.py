@@ -87,6 +87,29 @@ def test_weights_long_caches(dev, Hq, Nq, d):
     status_ok()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("Nq", [1, 9, 200, 600])
+def test_weights_of_rows_that_a_caller_leaves_out(dev, dtype, causal, Nq):
+    """Padded queries: an LSE of -inf, and q whatever was there.  Such rows add nothing, nor do the
+    rows that fill up a tile, against keys with infinities either."""
+    q, k = randn(1, (3, 4, Nq, 64), dev, DT[dtype]), randn(2, (3, 2, 400, 64), dev, DT[dtype])
+    cl = torch.tensor([400, 390, 0], dtype=torch.int32, device=dev)
+    lse = torch.full((3, 4, Nq), 12.0, device=dev)
+    lse[0, 1], lse[1, :, Nq // 2:] = float("-inf"), float("-inf")
+    want, err = P.weights(q, k, lse, cl.tolist(), causal, None)
+    q[0, 1], q[1, 2, Nq // 2:], q[1, 3, Nq // 2:] = float("nan"), float("inf"), float("-inf")
+    got = A.kvcache_weights(q, k, lse, cl, causal)
+    status_ok()
+    assert bool(((got.double() - want).abs() <= err).all())
+    # one component of a key infinite, all queries on its other side: a score of -inf, a weight of 0
+    q = randn(1, (3, 4, Nq, 64), dev, DT[dtype]).abs()
+    k[:, :, 7, 3] = float("-inf")
+    got = A.kvcache_weights(q, k, lse, cl, causal)
+    status_ok()
+    assert bool((got[:, :, 7] == 0).all()) and bool(got.isfinite().all())
+
+
 def test_weights_sum_to_the_number_of_rows_after_the_forward(dev):
     """With the forward's own LSE: each row's weights add up to one, so the sum over the keys is the
     number of (head, query) rows that see any key."""
