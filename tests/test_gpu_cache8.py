@@ -200,7 +200,10 @@ def test_attend_long_runs_behind_short_sequences(dev, cache, d, Hq, Nq):
     """Many tiles per CTA, long sequences next to sequences of one tile: a CTA's warps take very
     unequal numbers of them, and the ring turns many times."""
     lens = [9000, 1, 1, 40, 12321, 2, 3, 1, 1, 5, 8000]
-    run_attend(dev, len(lens), Hq, 8, Nq, 12321, d, 64, "bf16", cache, lens, True, seed=Nq)
+    q, k8, v8, ks, vs, cl, o = run_attend(dev, len(lens), Hq, 8, Nq, 12321, d, 64, "bf16", cache, lens, True, seed=Nq)
+    for _ in range(20):
+        assert torch.equal(A.fwd_kvcache8(q, k8, v8, ks, vs, cl, True, None, 64)[0], o)
+    status_ok()
 
 
 def test_attend_scales_of_very_different_size(dev):
