@@ -231,6 +231,13 @@ def _fit(dev: int, *tensors) -> bool:
     return dev >= 0
 
 
+def _check_sizes(*shapes):
+    """C takes sizes in 32 bits."""
+    for s in shapes:
+        if max(s) >= 2 ** 31:
+            raise ValueError("every size must be below 2**31")
+
+
 def _explain(*named):
     """Raises what is wrong with the arguments of a cache call: (tensor, name, dtype, optional) each,
     contiguous tensors on the first one's GPU."""
@@ -300,6 +307,7 @@ def kvcache8_append(k8, v8, k_scale, v_scale, k_new, v_new, cache_seqlens=None, 
     shape = k_new.shape
     if len(shape) != 4 or shape != v_new.shape or shape[0] != B or shape[1] != Hkv or shape[3] != d:
         raise ValueError("k_new and v_new must be [B,Hkv,Nn,d]")
+    _check_sizes(k8.shape, shape)
     st = _on_device(dev, _lib.attn_kvcache8_append, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                     k_new.data_ptr(), v_new.data_ptr(), _lens_ptr(cache_seqlens, "cache_seqlens", B),
                     _lens_ptr(new_seqlens, "new_seqlens", B), B, Hkv, shape[2], Nk, d, block, _dtype_code(k_new),
@@ -334,6 +342,7 @@ def fwd_kvcache8(q, k8, v8, k_scale, v_scale, cache_seqlens=None, causal: bool =
     shape = q.shape
     if len(shape) != 4 or shape[0] != B or shape[3] != d:
         raise ValueError("q must be [B,Hq,Nq,d], with the cache's batch and head_dim")
+    _check_sizes(shape, k8.shape)
     Hq, Nq = shape[1], shape[2]
     device = q.device
     o = torch.empty_like(q, dtype=torch.float32) if out_f32 else torch.empty_like(q)
@@ -373,6 +382,7 @@ def kvcache_weights(q, k_cache, lse, cache_seqlens=None, causal: bool = False, s
     Bk, Hkv, Nk, dk = k_cache.shape
     if Bk != B or dk != d:
         raise ValueError("q and the cache disagree on batch or head_dim")
+    _check_sizes(q.shape, k_cache.shape)
     if lse.shape != (B, Hq, Nq):
         raise ValueError("lse must be [B,Hq,Nq]")
     for t, n in ((weights, "weights"), (out, "out")):
@@ -421,6 +431,7 @@ def kvcache_evict(k_cache, v_cache, weights, keep: int, recent: int, cache_seqle
         raise ValueError("k_cache and v_cache must be [B,Hkv,Nk,d] and weights [B,Hkv,Nk]")
     if k_out.dim() != 4 or k_out.shape != v_out.shape or k_out.shape[:2] != (B, Hkv) or k_out.shape[3] != d:
         raise ValueError("k_out and v_out must be [B,Hkv,capacity,d]")
+    _check_sizes(k_cache.shape, k_out.shape)
     cap = k_out.shape[2]
     if cap < keep + recent:
         raise ValueError("the capacity of k_out and v_out must be at least keep + recent")

@@ -615,11 +615,15 @@ attn_status_t attn_fwd_kvcache(const void* q, const void* k_cache, const void* v
 
 namespace {
 
+// Tokens of a cache and rows of a (batch, kv head): their numbers, rounded up to a tile or a step of a
+// loop over them (8192 at most), stay within 32 bits.
+constexpr long long kMaxTokens = 0x7fff0000LL;
+
 // Sizes shared by the calls on [B, Hkv, Nk, d] caches; the grids and row counts are 32-bit.
 attn_status_t check_cache(int B, int Hkv, int Nk, int d) {
   if (B < 0 || Hkv <= 0 || Nk < 0 || d <= 0) return ATTN_ERR_INVALID_ARG;
   if (d % 16 != 0 || d > 128) return ATTN_ERR_UNSUPPORTED;
-  if (static_cast<long long>(B) * Hkv > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * Hkv > 0x7fffffffLL || Nk > kMaxTokens) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
 
@@ -764,6 +768,9 @@ attn_status_t attn_kvcache8_append(void* k8, void* v8, float* k_scale, float* v_
   // tokens L .. L + Nn - 1 touch the most blocks when L is the last token of one
   p.blocks_per_head = static_cast<int>(std::min<long long>((static_cast<long long>(Nn) + block - 2) / block + 1, p.n_blocks));
   if (static_cast<long long>(B) * Hkv * 2 * p.blocks_per_head > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  // one cache for both sides would be recoded by two CTAs
+  const size_t codes = static_cast<size_t>(B) * Hkv * Nk * d, scales = static_cast<size_t>(B) * Hkv * p.n_blocks * 4;
+  if (overlap(k8, codes, v8, codes) || overlap(k_scale, scales, v_scale, scales)) return ATTN_ERR_INVALID_ARG;
   if (!(p.status = status_word())) return ATTN_ERR_CUDA;
   return from_cuda(attn::launch_cache8_append(p, dtype, cache_dtype, static_cast<cudaStream_t>(stream)));
 }
@@ -795,10 +802,11 @@ attn_status_t attn_fwd_kvcache8(const void* q, const void* k8, const void* v8, c
   if (!all_aligned16({q, o}) || (Nk > 0 && (!k8 || !v8 || !k_scale || !v_scale)) || !aligned(k8, 16) || !aligned(v8, 16) ||
       !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(lse, 4) || !aligned(cache_seqlens, 4))
     return ATTN_ERR_INVALID_ARG;
+  const long long R = static_cast<long long>(Hq / Hkv) * Nq, bh = static_cast<long long>(B) * Hkv;
+  if (Nk > kMaxTokens || R > kMaxTokens || bh * R > 0x7fffffffLL || static_cast<long long>(B) * Hq > 0x7fffffffLL)
+    return ATTN_ERR_UNSUPPORTED;
   const size_t need = attn_fwd_kvcache8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d);
   if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return ATTN_ERR_INVALID_ARG;
-  const long long R = static_cast<long long>(Hq / Hkv) * Nq, bh = static_cast<long long>(B) * Hkv;
-  if (R > 0x7fffffffLL || bh * R > 0x7fffffffLL || static_cast<long long>(B) * Hq > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
   attn::Cache8Params p{};
   p.q = q;
   p.k8 = static_cast<const uint8_t*>(k8);
@@ -845,15 +853,19 @@ attn_status_t attn_kvcache_weights(const void* q, const void* k_cache, const flo
   if (!weights_out || !aligned(weights_out, 4) || !aligned(weights_in, 4) || !aligned(cache_seqlens, 4))
     return ATTN_ERR_INVALID_ARG;
   const long long R = static_cast<long long>(Hq / Hkv) * Nq, bh = static_cast<long long>(B) * Hkv;
+  if (Nk > kMaxTokens || R > kMaxTokens || bh * R > 0x7fffffffLL || static_cast<long long>(B) * Hq > 0x7fffffffLL)
+    return ATTN_ERR_UNSUPPORTED;
+  const size_t bytes = static_cast<size_t>(bh) * Nk * sizeof(float);
+  if ((weights_in && weights_in != weights_out && overlap(weights_out, bytes, weights_in, bytes)) ||
+      (lse && overlap(weights_out, bytes, lse, static_cast<size_t>(bh) * R * sizeof(float))))
+    return ATTN_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (Nq == 0) {  // no query adds anything
-    const size_t bytes = static_cast<size_t>(bh) * Nk * sizeof(float);
     if (!weights_in) return from_cuda(cudaMemsetAsync(weights_out, 0, bytes, s));
     return weights_in == weights_out ? ATTN_OK
                                      : from_cuda(cudaMemcpyAsync(weights_out, weights_in, bytes, cudaMemcpyDeviceToDevice, s));
   }
   if (!all_aligned16({q, k_cache}) || !lse || !aligned(lse, 4)) return ATTN_ERR_INVALID_ARG;
-  if (R > 0x7fffffffLL || bh * R > 0x7fffffffLL || static_cast<long long>(B) * Hq > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
   if (bh * ((static_cast<long long>(Nk) + 63) / 64) > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
   attn::WeightParams p{};
   p.q = q;
@@ -889,6 +901,7 @@ attn_status_t attn_kvcache_evict(const void* k_cache, const void* v_cache, const
   if (!dtype_ok(dtype) || keep < 0 || recent < 0) return ATTN_ERR_INVALID_ARG;
   const long long M = static_cast<long long>(keep) + recent;
   if (M < 1 || capacity < M) return ATTN_ERR_INVALID_ARG;
+  if (capacity > kMaxTokens) return ATTN_ERR_UNSUPPORTED;
   if (B == 0) return ATTN_OK;
   const long long bh = static_cast<long long>(B) * Hkv;
   if ((Nk > 0 && (!k_cache || !v_cache || !weights)) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(weights, 4) ||
@@ -902,6 +915,8 @@ attn_status_t attn_kvcache_evict(const void* k_cache, const void* v_cache, const
   for (const void* out : {static_cast<const void*>(k_out), static_cast<const void*>(v_out)})
     if (overlap(out, out_bytes, k_cache, in_bytes) || overlap(out, out_bytes, v_cache, in_bytes)) return ATTN_ERR_INVALID_ARG;
   if (overlap(k_out, out_bytes, v_out, out_bytes) || overlap(weights_out, wo_bytes, weights, w_bytes)) return ATTN_ERR_INVALID_ARG;
+  const size_t len_bytes = static_cast<size_t>(B) * 4;  // the other heads still read the lengths when the first writes its own
+  if (cache_seqlens && overlap(out_seqlens, len_bytes, cache_seqlens, len_bytes)) return ATTN_ERR_INVALID_ARG;
   attn::EvictParams p{};
   p.k = k_cache; p.v = v_cache; p.w = weights;
   p.cache_seqlens = cache_seqlens;

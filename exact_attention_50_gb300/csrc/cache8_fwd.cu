@@ -34,9 +34,10 @@
 // instruction.
 //
 // What it reaches (8 sequences of 16k to 32k keys, 32 over 8 heads, d = 128, int8): 76 us, 5.6 TB/s, 83% of
-// the copy rate; 73 us with one query row per head, so the conversions cost a little still; about 8 us
-// of it are the launches, the first tiles' latency and the merge.  With 16 rows (NB = 2) 87 us, with 32
-// (two warps per tile, the codes converted twice) 150 us, bound by instruction issue.
+// the copy rate: 71 us in this kernel, the rest the merge (5 us alone, partly hidden) and the launch; 75 us with
+// one query row per kv head.  With 16 rows (NB = 2) 86 us.  With 32 (two warps per tile, the codes converted
+// twice) 147 us: 247 registers leave two warps per scheduler, which issue in 45% of the cycles, waiting
+// mostly for results of fixed latency; ALU 41%, tensor pipe 33%, DRAM 38%, so no unit bounds it.
 //
 // Rounding: q in bf16 becomes fp16 after a multiplication by a power of two per row (largest
 // element in [2^14, 2^15)), exact but for elements below 2^-28 of that.  P is rounded to fp16

@@ -237,6 +237,8 @@ attn_status_t attn_fwd_kvcache(const void* q, const void* k_cache, const void* v
  *                    consecutive tokens, not negative; token j stands for
  *                    code * scale[j / block]
  *   block            16, 32, 64 or 128
+ * In this call and the ones below more than 2^31 - 2^16 tokens in a cache, or query rows of a kv
+ * head, are ATTN_ERR_UNSUPPORTED.
  */
 typedef enum { ATTN_CACHE_I8 = 0, ATTN_CACHE_E4M3 = 1 } attn_cache_dtype_t;
 
@@ -253,6 +255,7 @@ typedef enum { ATTN_CACHE_I8 = 0, ATTN_CACHE_E4M3 = 1 } attn_cache_dtype_t;
  * nothing.  An infinity or NaN among a block's tokens makes its scale that and the block reads back
  * as infinities and NaN.  Blocks and tokens outside L .. L + n - 1 are left as they are, but for
  * that recoding; the scale of a block without tokens is never read.
+ * k8 and v8, and k_scale and v_scale, must not overlap.
  *   k_new, v_new   [B, Hkv, Nn, d] (dtype: float32, float16 or bfloat16), Nn <= Nk
  *   cache_seqlens  DEVICE int32 [B], or NULL: empty caches (L = 0)
  *   new_seqlens    DEVICE int32 [B], 0 <= new_seqlens[b] <= Nn, or NULL: Nn each
@@ -292,7 +295,7 @@ attn_status_t attn_fwd_kvcache8(const void* q, const void* k8, const void* v8, c
  *   lse          its float32 LSE [B, Hq, Nq]; a row with LSE -inf (no key, or a padded query)
  *                adds nothing, whatever its q holds
  *   weights_in   [B, Hkv, Nk] float32, or NULL: zeros
- *   weights_out  [B, Hkv, Nk] float32; may be weights_in.  Keys past a cache's length get
+ *   weights_out  [B, Hkv, Nk] float32; may be weights_in, overlaps no other input.  Keys past a cache's length get
  *                weights_in (0 when it is NULL)
  * The sums are float32, in an order fixed by the sizes: results are bitwise reproducible.
  */
@@ -310,6 +313,7 @@ attn_status_t attn_kvcache_weights(const void* q, const void* k_cache, const flo
  *   k_out, v_out   [B, Hkv, capacity, d], capacity >= keep + recent; they must not overlap the
  *                  inputs.  Rows past the kept ones are left as they are
  *   weights_out    [B, Hkv, capacity] float32: the kept keys' weights, then zeros
+ *                  (weights_out and out_seqlens not over weights and cache_seqlens either)
  *   index          int32 [B, Hkv, keep + recent]: the kept keys' positions, then -1
  *   out_seqlens    int32 [B]: min(L, keep + recent)
  * keep, recent >= 0 and keep + recent >= 1.  A cache_seqlens entry outside [0, Nk] counts as 0

@@ -96,6 +96,50 @@ def test_evict_refusals(lib):
     assert f(keep=2 ** 31 - 1, recent=2 ** 31 - 1) == BAD  # their sum does not wrap
 
 
+def test_sizes_whose_tile_numbers_leave_32_bits_are_refused(lib):
+    """Lengths and row counts are rounded up to tiles and stepped over in 32 bits on the device."""
+    MB, big = 1 << 20, 0x7fff0001
+    assert _lib.attn_kvcache8_append(MB, 1 << 50, 1 << 51, 1 << 52, MB, MB, None, None, 1, 1, 1, big, 16, 64, _lib.ATTN_BF16, 0, None) == NO
+    for Nq in (1, 100):
+        assert _lib.attn_fwd_kvcache8(MB, MB, MB, MB, MB, None, MB, None, MB, 1 << 60, 1, 1, 1, Nq, big, 16, 64, 1, 0.0,
+                                      _lib.ATTN_BF16, 0, 0, None) == NO
+    assert _lib.attn_fwd_kvcache8(MB, MB, MB, MB, MB, None, MB, None, MB, 1 << 60, 1, 1, 1, big, 64, 16, 64, 1, 0.0,
+                                  _lib.ATTN_BF16, 0, 0, None) == NO
+    for dtype in (_lib.ATTN_BF16, _lib.ATTN_F32):
+        for Nq, Nk in ((1, big), (big, 64)):
+            assert _lib.attn_kvcache_weights(MB, MB, MB, None, None, 1 << 50, 1, 1, 1, Nq, Nk, 16, 1, 0.0, dtype, None) == NO
+    for Nk, cap, keep in ((big, 40, 24), (100, big, 24), (100, big, big - 1)):
+        assert _lib.attn_kvcache_evict(MB, 1 << 42, 1 << 44, None, 1 << 46, 1 << 48, 1 << 50, 1 << 52, 1 << 54, 1, 1, Nk, cap,
+                                       16, keep, 1, _lib.ATTN_BF16, None) == NO
+
+
+def test_outputs_that_overlap_what_is_read_are_refused(lib):
+    MB = 1 << 20
+
+    def append(**kw):
+        a = dict(k8=MB, v8=2 * MB, ks=3 * MB, vs=4 * MB)
+        a.update(kw)
+        return _lib.attn_kvcache8_append(a["k8"], a["v8"], a["ks"], a["vs"], 5 * MB, 6 * MB, None, None, 2, 2, 4, 100, 64, 64,
+                                         _lib.ATTN_BF16, _lib.ATTN_CACHE_I8, None)
+    for kw in (dict(v8=MB), dict(v8=MB + 25584), dict(vs=3 * MB), dict(vs=3 * MB + 28)):
+        assert append(**kw) == BAD, kw
+
+    def weights(out, w=4 * MB, Nq=3):
+        return _lib.attn_kvcache_weights(MB, 2 * MB, 3 * MB, None, w, out, 2, 4, 2, Nq, 100, 64, 1, 0.0, _lib.ATTN_BF16, None)
+    for Nq in (3, 0):
+        assert weights(4 * MB + 4, Nq=Nq) == BAD and weights(4 * MB - 1596, Nq=Nq) == BAD
+    assert weights(3 * MB) == BAD and weights(3 * MB - 4, None) == BAD
+    for lo in (9 * MB, 9 * MB + 4):  # the new lengths over the old ones, which other heads still read
+        assert _lib.attn_kvcache_evict(MB, 2 * MB, 3 * MB, 9 * MB, 4 * MB, 5 * MB, 6 * MB, 7 * MB, lo, 2, 2, 100, 40, 64, 24, 16,
+                                       _lib.ATTN_BF16, None) == BAD
+
+
+def test_the_python_layer_refuses_sizes_that_c_would_cut(lib):
+    A._check_sizes((1, 2, 2 ** 31 - 1), (4,))
+    with pytest.raises(ValueError, match="2\\*\\*31"):
+        A._check_sizes((1, 2), (1, 2 ** 31, 16))
+
+
 def test_python_layer_wants_cuda_tensors_of_the_right_kind():
     q = torch.zeros(1, 2, 1, 64, dtype=torch.bfloat16)
     k8 = torch.zeros(1, 1, 64, 64, dtype=torch.int8)
