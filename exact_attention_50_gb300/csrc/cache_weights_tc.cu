@@ -7,20 +7,24 @@
 // one (batch, kv head): two 128-key tiles that stay in shared memory while the rows' Q tiles
 // (of up to 128 rows, as even as R allows) stream past both, which halves Q's traffic out of L2,
 // the bound of a 128-key item (32 KB of Q per 128 x 128 x 128 product).  With few rows (decode)
-// every item has one Q tile and K streams from HBM; up to eight rows are summed over their eight columns
-// alone (8 x 8 heads of 16k-32k keys, 4 rows: 73 us, 6.1 TB/s; over the tile's 32 columns 77 us).  Items are numbered by key tile, those that
-// the most queries see first, and dealt to the CTAs in snake order.  When there are fewer items than
-// half the SMs, a cluster of CTAs takes each one's Q tiles in turn and adds its sums up in distributed
-// shared memory, in order (one 2048-token prompt, 32 over 8 heads: 45 us, 69 without).
+// every item has one Q tile and K streams from HBM; up to eight rows are summed over their eight
+// columns alone (8 x 8 heads of 16k-32k keys, 4 rows: 73 us, 6.1 TB/s; over the tile's 32 columns 77 us).
+// Items are numbered by key tile, those that the most queries see first, and dealt to the CTAs in snake
+// order.  When there are fewer items than half the SMs, a cluster of CTAs takes each one's Q tiles in
+// turn and adds its sums up in distributed shared memory, in order (one 2048-token prompt, 32 over 8
+// heads: 45 us, 69 without).
 //
 // 640 threads: sixteen warps that sum (tcgen05.ld, one paired FMA and two ex2 per pair of scores), four
 // for each key tile and each of its two S^T buffers of 128 columns, the buffers taken in turn;
 // then a warp for the TMA loads, one MMA issuer per key tile, on two sub-partitions (one thread
 // issues 16 of them in about 1700 cycles, more than they take), and one that prepares the rows'
-// -LSE log2(e) and last visible keys.  Measured on 2048-token prompts (B = 4, 32 over 8 heads,
-// d = 128): eight summing warps and one issuer 160 us without and 116 us with the causal mask, as
-// here 131 and 86; eight warps that take a whole tile into registers first 149 and 92; two groups
-// that halve every tile's columns 135 and 90; loads of 32 columns ahead of the sums 162 and 102.
+// -LSE log2(e) and last visible keys.  2048-token prompts (B = 4, 32 over 8 heads, d = 128) take 132 us
+// without and 78 us (880 TFLOP/s) with the causal mask, 86 with integer divisions in every role's walk
+// over the tiles.  Measured beside 131 and 86, with those: eight summing warps and one issuer 160 and
+// 116; eight warps that take a whole tile into registers first 149 and 92; two groups that halve every
+// tile's columns 135 and 90; loads of 32 columns ahead of the sums 162 and 102; tiles handed over in
+// parts of 64 columns, with twice the products to issue, 183 and 108.  Tiles of 256 rows, one buffer per
+// key tile, halved by the two groups: beside 132 and 78, 138 and 84.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -79,15 +83,20 @@ __device__ __forceinline__ Item item_of(const WeightParams& p, int idx) {
   return it;
 }
 
-// The first Q tile from rb on with a row that sees a key of the item (or a number past the last): under
-// the causal mask the rows of queries i >= key0 - (L - Nq) of each head.
-__device__ __forceinline__ int seen_tile(const WeightParams& p, const Item& it, int rb, int qn) {
-  const int least = it.key0 - (it.L - p.Nq);
-  if (!p.causal || least <= 0) return rb;
-  const int r0 = rb * qn;
-  if (r0 >= p.R) return rb;
-  const int head = r0 / p.Nq * p.Nq;
-  return r0 - head >= least ? rb : (head + least) / qn;
+// A Q tile, and the first row of the head that its first row belongs to (kept under the causal mask when a
+// head is longer than a tile).  Every role walks them, so without a division per tile.
+struct Tile {
+  int rb, head;
+};
+
+// From tile t on the first with a row that sees a key of the item (or one past the last): under the causal
+// mask the rows of queries i >= key0 - (L - Nq) of each head, of which a tile as long as a head has one.
+__device__ __forceinline__ void seek(const WeightParams& p, const Item& it, int qn, Tile& t) {
+  if (!p.causal || p.Nq <= qn) return;
+  const int r0 = t.rb * qn, least = it.key0 - (it.L - p.Nq);
+  if (r0 >= p.R) return;
+  if (r0 - t.head >= p.Nq) t.head += p.Nq;
+  if (r0 - t.head < least) t.rb = (t.head + least) / qn;
 }
 
 // FEW: one Q tile per item, so the sets of summing warps take the items in turn and join no sums.
@@ -160,17 +169,21 @@ __global__ void __launch_bounds__(640, 1)
   const int n_rb = (p.R + qn - 1) / qn;
   const int G = gridDim.x, rank = SPLIT ? blockIdx.x % split : 0;
   // this CTA's Q tiles of an item: those that see its keys, every split-th
-  auto next_tile = [&](const Item& it, int rb) {
-    rb = seen_tile(p, it, rb + 1, qn);
+  auto step = [&](const Item& it, Tile& t) {
+    ++t.rb;
+    seek(p, it, qn, t);
+  };
+  auto next_tile = [&](const Item& it, Tile& t) {
+    step(it, t);
     if constexpr (SPLIT)
-      for (int i = 1; i < split && rb < n_rb; ++i) rb = seen_tile(p, it, rb + 1, qn);
-    return rb;
+      for (int i = 1; i < split && t.rb < n_rb; ++i) step(it, t);
   };
   auto first_tile = [&](const Item& it) {
-    int rb = seen_tile(p, it, 0, qn);
+    Tile t{0, 0};
+    seek(p, it, qn, t);
     if constexpr (SPLIT)
-      for (int i = 0; i < rank && rb < n_rb; ++i) rb = seen_tile(p, it, rb + 1, qn);
-    return rb;
+      for (int i = 0; i < rank && t.rb < n_rb; ++i) step(it, t);
+    return t;
   };
 
   if (warp == kSums) {
@@ -185,8 +198,8 @@ __global__ void __launch_bounds__(640, 1)
         if (idx >= n_items) continue;
         const Item it = item_of(p, idx);
         if (it.key0 >= it.L) continue;
-        int rb = first_tile(it);
-        if (rb >= n_rb) continue;
+        Tile t = first_tile(it);
+        if (t.rb >= n_rb) continue;
         for (int h = 0; ok && h < 2 && it.key0 + 128 * h < it.L; ++h) {
           const uint32_t nk = h ? nk1 : nk0, st = h * kRing + nk % k_stages;
           if (nk >= static_cast<uint32_t>(k_stages) && !mbar_wait(k_empty + st, ((nk / k_stages) - 1) & 1, abort_flag, p.status)) { ok = false; break; }
@@ -196,11 +209,11 @@ __global__ void __launch_bounds__(640, 1)
           nk0 += 1 - h;
           nk1 += h;
         }
-        for (; ok && rb < n_rb; rb = next_tile(it, rb)) {
+        for (; ok && t.rb < n_rb; next_tile(it, t)) {
           const uint32_t st = nq % q_stages;
           if (nq >= static_cast<uint32_t>(q_stages) && !mbar_wait(q_empty + st, ((nq / q_stages) - 1) & 1, abort_flag, p.status)) { ok = false; break; }
           mbar_expect_tx(q_full + st, q_bytes);
-          for (int c = 0; c < kChunks; ++c) tma_load_3d(sQ + st * q_bytes + c * qn * 128, &tmQ, q_full + st, c * 64, rb * qn, it.bh);
+          for (int c = 0; c < kChunks; ++c) tma_load_3d(sQ + st * q_bytes + c * qn * 128, &tmQ, q_full + st, c * 64, t.rb * qn, it.bh);
           ++nq;
         }
       }
@@ -226,12 +239,12 @@ __global__ void __launch_bounds__(640, 1)
         if (idx >= n_items) continue;
         const Item it = item_of(p, idx);
         if (it.key0 >= it.L) continue;
-        int rb = first_tile(it);
-        if (rb >= n_rb) continue;
+        Tile t = first_tile(it);
+        if (t.rb >= n_rb) continue;
         const int halves = it.key0 + 128 < it.L ? 2 : 1;
         const uint32_t ks = nk % k_stages;
         if (h < halves && !mbar_wait(k_full + h * kRing + ks, (nk / k_stages) & 1, abort_flag, p.status)) { ok = false; break; }
-        for (; rb < n_rb; rb = next_tile(it, rb), ++nq) {
+        for (; t.rb < n_rb; next_tile(it, t), ++nq) {
           const uint32_t qs = nq % q_stages, b = nq & 1;
           if (!mbar_wait(q_full + qs, (nq / q_stages) & 1, abort_flag, p.status)) { ok = false; break; }
           if (h >= halves) {  // no keys of this tile: its share of the Q stage is done
@@ -273,23 +286,28 @@ __global__ void __launch_bounds__(640, 1)
       const Item it = item_of(p, idx);
       if (it.key0 >= it.L) continue;
       const float* lse = p.lse + static_cast<size_t>(it.bh) * p.R;
-      for (int rb = first_tile(it); rb < n_rb; rb = next_tile(it, rb), ++n) {
+      for (Tile t = first_tile(it); t.rb < n_rb; next_tile(it, t), ++n) {
         const uint32_t st = n % kNl;
+        auto query = [&](int r) {  // r % Nq
+          if (p.Nq <= qn) return r % p.Nq;
+          const int i = r - t.head;
+          return i >= p.Nq ? i - p.Nq : i;
+        };
         float nl[4];
         int lim[4], least = 0x7fffffff;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int c = u * 32 + lane, r = rb * qn + c;
+          const int c = u * 32 + lane, r = t.rb * qn + c;
           const bool in = c < qn && r < p.R;
           const float x = in ? lse[r] : -INFINITY;
           nl[u] = x == -INFINITY ? -INFINITY : -x * 1.4426950408889634f;  // a row without a key adds nothing
-          lim[u] = in ? (p.causal ? min(it.L - p.Nq + r % p.Nq, it.L - 1) : it.L - 1) : c < qn ? -1 : 0x7fffffff;
+          lim[u] = in ? (p.causal ? min(it.L - p.Nq + query(r), it.L - 1) : it.L - 1) : c < qn ? -1 : 0x7fffffff;
           least = min(least, lim[u]);
         }
         least = __reduce_min_sync(0xffffffffu, least);
         if (n >= kNl && !mbar_wait_warp(nl_empty + st, ((n / kNl) - 1) & 1, abort_flag, p.status)) { ok = false; break; }
         // a row without a key sees none, like those that fill up the tile: an infinity or NaN that its q
-        // makes stays out.  (With the LSE in the terms above, ahead of the wait, 109 us for 86.)
+        // makes stays out.  (Not above, ahead of the wait, where the LSE may not have come yet.)
         bool none = false;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -325,7 +343,7 @@ __global__ void __launch_bounds__(640, 1)
       const bool works = it.key0 + h * 128 < it.L;
       float sum = 0.f;
       if (it.key0 < it.L) {
-        for (int rb = first_tile(it); rb < n_rb; rb = next_tile(it, rb), ++n) {
+        for (Tile t = first_tile(it); t.rb < n_rb; next_tile(it, t), ++n) {
           const uint32_t b = n & 1, st = n % kNl;
           ++tiles;
           if (b != mine) continue;
