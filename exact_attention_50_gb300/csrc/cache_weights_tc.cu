@@ -8,11 +8,11 @@
 // (of up to 128 rows, as even as R allows) stream past both, which halves Q's traffic out of L2,
 // the bound of a 128-key item (32 KB of Q per 128 x 128 x 128 product).  With few rows (decode)
 // every item has one Q tile and K streams from HBM; up to eight rows are summed over their eight
-// columns alone (8 x 8 heads of 16k-32k keys, 4 rows: 73 us, 6.1 TB/s; over the tile's 32 columns 77 us).
+// columns alone (8 x 8 heads of 16k-32k keys, 4 rows: 71.5 us, 6.2 TB/s; 4 us more over the tile's 32 columns).
 // Items are numbered by key tile, those that the most queries see first, and dealt to the CTAs in snake
 // order.  When there are fewer items than half the SMs, a cluster of CTAs takes each one's Q tiles in
 // turn and adds its sums up in distributed shared memory, in order (one 2048-token prompt, 32 over 8
-// heads: 45 us, 69 without).
+// heads: 45 us, 72 without).
 //
 // 640 threads: sixteen warps that sum (tcgen05.ld, one paired FMA and two ex2 per pair of scores), four
 // for each key tile and each of its two S^T buffers of 128 columns, the buffers taken in turn;
@@ -62,6 +62,18 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
       : "memory");
 }
 
+// n / d for 0 <= n < 2^31: with m = ceil(2^(31 + s) / d), 2^s >= d, the product's error stays below 1 / d.
+// (Every role finds every item by two divisions.  With the compiler's the decode case took 73.7 us, with 64
+// columns 66 us; now 71.5 and 55.)
+struct Divisor {
+  uint32_t m, s;
+  explicit Divisor(uint32_t d) : s(0) {
+    while ((1ull << s) < d) ++s;
+    m = static_cast<uint32_t>(((1ull << (31 + s)) + d - 1) / d);
+  }
+  __device__ __forceinline__ int of(int n) const { return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(n)) * m >> 31 >> s); }
+};
+
 struct Item {
   int bh, key0, L;
 };
@@ -74,12 +86,15 @@ __device__ __forceinline__ int snake(int k, int split) {
   return k * G + ((k & 1) ? G - 1 - c : c);
 }
 
-__device__ __forceinline__ Item item_of(const WeightParams& p, int idx) {
-  const int bhs = p.B * p.Hkv;
+struct Heads {
+  Divisor all, kv, query;  // B Hkv, Hkv and Nq
+};
+__device__ __forceinline__ Item item_of(const WeightParams& p, const Heads& heads, int idx) {
+  const int tile = heads.all.of(idx);
   Item it;
-  it.bh = idx % bhs;
-  it.key0 = idx / bhs * 256;
-  it.L = cache_len(p.cache_seqlens, it.bh / p.Hkv, p.Nk, nullptr, false);
+  it.bh = idx - tile * (p.B * p.Hkv);
+  it.key0 = tile * 256;
+  it.L = cache_len(p.cache_seqlens, heads.kv.of(it.bh), p.Nk, nullptr, false);
   return it;
 }
 
@@ -105,7 +120,7 @@ __device__ __forceinline__ void seek(const WeightParams& p, const Item& it, int 
 template <bool BF16, int DP, bool FEW, bool SPLIT>
 __global__ void __launch_bounds__(640, 1)
     weights_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, const WeightParams p,
-                      int n_items, int qn, int k_stages, int q_stages, int split) {
+                      const Heads heads, int n_items, int qn, int k_stages, int q_stages, int split) {
   constexpr int kChunks = DP / 64;
   constexpr int kTileK = 128 * DP * 2;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -196,7 +211,7 @@ __global__ void __launch_bounds__(640, 1)
       for (int k = 0; ok && k * G < n_items; ++k) {
         const int idx = snake<SPLIT>(k, split);
         if (idx >= n_items) continue;
-        const Item it = item_of(p, idx);
+        const Item it = item_of(p, heads, idx);
         if (it.key0 >= it.L) continue;
         Tile t = first_tile(it);
         if (t.rb >= n_rb) continue;
@@ -237,7 +252,7 @@ __global__ void __launch_bounds__(640, 1)
       for (int k = 0; ok && k * G < n_items; ++k) {
         const int idx = snake<SPLIT>(k, split);
         if (idx >= n_items) continue;
-        const Item it = item_of(p, idx);
+        const Item it = item_of(p, heads, idx);
         if (it.key0 >= it.L) continue;
         Tile t = first_tile(it);
         if (t.rb >= n_rb) continue;
@@ -283,13 +298,13 @@ __global__ void __launch_bounds__(640, 1)
     for (int k = 0; ok && k * G < n_items; ++k) {
       const int idx = snake<SPLIT>(k, split);
       if (idx >= n_items) continue;
-      const Item it = item_of(p, idx);
+      const Item it = item_of(p, heads, idx);
       if (it.key0 >= it.L) continue;
       const float* lse = p.lse + static_cast<size_t>(it.bh) * p.R;
       for (Tile t = first_tile(it); t.rb < n_rb; next_tile(it, t), ++n) {
         const uint32_t st = n % kNl;
         auto query = [&](int r) {  // r % Nq
-          if (p.Nq <= qn) return r % p.Nq;
+          if (p.Nq <= qn) return r - heads.query.of(r) * p.Nq;
           const int i = r - t.head;
           return i >= p.Nq ? i - p.Nq : i;
         };
@@ -332,7 +347,7 @@ __global__ void __launch_bounds__(640, 1)
     for (int k = 0; ok && k * G < n_items; ++k) {
       const int idx = snake<SPLIT>(k, split);
       if (idx >= n_items) continue;
-      const Item it = item_of(p, idx);
+      const Item it = item_of(p, heads, idx);
       const int key = it.key0 + h * 128 + (threadIdx.x & 127);
       const size_t at = static_cast<size_t>(it.bh) * p.Nk + key;
       const bool writes = (n & 1) == mine;  // the set that has the item's first Q tile
@@ -435,7 +450,7 @@ __global__ void __launch_bounds__(640, 1)
   if constexpr (SPLIT) {  // the cluster's sums, rank by rank
     const auto cluster = cooperative_groups::this_cluster();
     cluster.sync();
-    const Item it = item_of(p, snake<SPLIT>(0, split));
+    const Item it = item_of(p, heads, snake<SPLIT>(0, split));
     const int key = it.key0 + threadIdx.x;
     if (rank == 0 && threadIdx.x < 256 && key < p.Nk) {
       const size_t at = static_cast<size_t>(it.bh) * p.Nk + key;
@@ -474,7 +489,7 @@ cudaError_t run(const CUtensorMap& q, const CUtensorMap& k, const WeightParams& 
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = split > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, q, k, p, static_cast<int>(items), qn, k_stages, q_stages, split);
+  return cudaLaunchKernelEx(&cfg, kern, q, k, p, Heads{Divisor(p.B * p.Hkv), Divisor(p.Hkv), Divisor(p.Nq)}, static_cast<int>(items), qn, k_stages, q_stages, split);
 }
 
 }  // namespace
@@ -487,7 +502,7 @@ cudaError_t launch_cache_weights_tc(const CUtensorMap& q, const CUtensorMap& k, 
   const int q_tiles = (p.R + q_rows - 1) / q_rows;
   while (!few && split < 8 && items * 2 * split <= 152 && 2 * split <= q_tiles) split *= 2;
   // the first keys of a causal prompt have twice the average's Q tiles: two CTAs for them, the light ones
-  // in a second wave (two prompts of 2048: 70 -> 59 us, one of 4096: 140 -> 94; without a mask 43 -> 52)
+  // in a second wave (two prompts of 2048: 74 -> 55 us, one of 4096: 140 -> 85; without a mask 68 -> 81 and 130 -> 147)
   if (split == 1 && p.causal && items <= 152 && q_tiles >= 16) split = 2;
   auto pick = [&](auto bf16, auto dp) {
     constexpr bool kB = decltype(bf16)::value;
