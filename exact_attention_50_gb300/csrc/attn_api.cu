@@ -635,7 +635,7 @@ bool dtype_ok(attn_dtype_t dt) { return dt == ATTN_F32 || dt == ATTN_F16 || dt =
 
 // The 8-bit codes [heads, Nk, d]: boxes of one tile's tokens, 64 or 128 columns, swizzled over a row's
 // 16-byte chunks; tokens past Nk and columns past d load as zeros.  L2 fetches of 128 bytes: 8 x 8 heads of
-// 16k-32k keys, d = 80 / 128 / 64: 77.3 / 74.5 / 42.6 us, with 256 bytes 95 / 76.4 / 43.6.
+// 16k-32k keys, d = 80: 77 us, with 256 bytes 91; the same for d = 64, 112 and 128.
 bool make_cache8_map(CUtensorMap* map, const void* base, int heads, int Nk, int d, int keys) {
   auto fn = encode_fn();
   if (!fn) return false;

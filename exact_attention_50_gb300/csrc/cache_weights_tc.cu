@@ -8,7 +8,7 @@
 // (of up to 128 rows, as even as R allows) stream past both, which halves Q's traffic out of L2,
 // the bound of a 128-key item (32 KB of Q per 128 x 128 x 128 product).  With few rows (decode)
 // every item has one Q tile and K streams from HBM; up to eight rows are summed over their eight
-// columns alone (8 x 8 heads of 16k-32k keys, 4 rows: 71.5 us, 6.2 TB/s; 4 us more over the tile's 32 columns).
+// columns alone (8 x 8 heads of 16k-32k keys, 4 rows: 72.7 us, 6.1 TB/s; 4 us more over the tile's 32 columns).
 // Items are numbered by key tile, those that the most queries see first, and dealt to the CTAs in snake
 // order.  When there are fewer items than half the SMs, a cluster of CTAs takes each one's Q tiles in
 // turn and adds its sums up in distributed shared memory, in order (one 2048-token prompt, 32 over 8
@@ -63,8 +63,8 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
 }
 
 // n / d for 0 <= n < 2^31: with m = ceil(2^(31 + s) / d), 2^s >= d, the product's error stays below 1 / d.
-// (Every role finds every item by two divisions.  With the compiler's the decode case took 73.7 us, with 64
-// columns 66 us; now 71.5 and 55.)
+// (Every role finds every item by two divisions.  With the compiler's the decode case took 73.9 us, with 64
+// columns 65.7, four windows of 48 queries 22.7 us; now 72.7, 54.9 and 21.6.)
 struct Divisor {
   uint32_t m, s;
   explicit Divisor(uint32_t d) : s(0) {
