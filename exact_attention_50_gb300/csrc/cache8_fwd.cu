@@ -33,7 +33,7 @@
 // subtracting 1152: there the offset would be far larger than the sums.  e4m3 by the conversion
 // instruction.
 //
-// What it reaches (8 sequences of 16k to 32k keys, 32 over 8 heads, d = 128, int8): 76 us, 5.6 TB/s, 83% of
+// What it reaches (8 sequences of 16k to 32k keys, 32 over 8 heads, d = 128, int8): 77 us, 5.5 TB/s, 81% of
 // the copy rate: 71 us in this kernel, the rest the merge (5 us alone, partly hidden) and the launch; 75 us with
 // one query row per kv head.  With 16 rows (NB = 2) 86 us.  With 32 (two warps per tile, the codes converted
 // twice) 147 us: 247 registers leave two warps per scheduler, which issue in 45% of the cycles, waiting
