@@ -186,6 +186,52 @@ def test_attend_many_short_sequences(dev):
     run_attend(dev, 700, 2, 1, 1, 40, 64, 16, "f16", "e4m3", [(7 * b) % 41 for b in range(700)], True, seed=8)
 
 
+@pytest.mark.parametrize("cache", ["i8", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv", [(17, 1), (33, 1), (64, 1), (71, 1), (128, 1), (142, 2)])
+def test_attend_many_heads_share_a_cache(dev, cache, Hq, Hkv):
+    """One query each: row blocks that two, four or all warps share, and the kernel of many rows."""
+    run_attend(dev, 3, Hq, Hkv, 1, 900, 64, 64, "bf16", cache, [900, 1, 333], True, seed=Hq)
+    run_attend(dev, 2, Hq, Hkv, 1, 9000, 112, 16, "f16", cache, [9000, 77], False, seed=Hq)
+
+
+def test_attend_and_append_with_thousands_of_sequences(dev):
+    B = 5000
+    lens = [(13 * b) % 34 for b in range(B)]
+    q, k8, v8, ks, vs, cl, _ = run_attend(dev, B, 2, 2, 1, 40, 16, 16, "bf16", "i8", lens, True, seed=3, poison=False)
+    x = rows(9, (B, 2, 3, 16), dev).bfloat16()
+    codes, scales = k8.clone(), ks.clone()
+    A.kvcache8_append(k8, v8, ks, vs, x, x, cl, block=16)
+    status_ok()
+    for b in (0, 1, 2, 33, 1234, 2500, 4097, B - 1):
+        for h in range(2):
+            c, s = codes[b, h].float().cpu().numpy(), scales[b, h].cpu().numpy()
+            P.append(c, s, x[b, h].float().cpu().numpy(), lens[b], 3, 16, "i8")
+            assert torch.equal(k8[b, h].float().cpu(), torch.from_numpy(c)) and torch.equal(ks[b, h].cpu(), torch.from_numpy(s))
+
+
+def test_attend_two_graphs_at_once(dev):
+    """Two captured calls, each with its own workspace, replayed on two streams at the same time."""
+    calls = []
+    for i, (Nq, Nk) in enumerate(((1, 20000), (20, 3000), (100, 2000))):
+        q = torch.randn(3, 8, Nq, 128, generator=torch.Generator(dev).manual_seed(i), device=dev).bfloat16()
+        k8, ks = P.quantise(rows(i + 1, (3, 2, Nk, 128), dev), 64, "i8")
+        v8, vs = P.quantise(rows(i + 2, (3, 2, Nk, 128), dev), 64, "i8")
+        want = A.fwd_kvcache8(q, k8, v8, ks, vs, None, True)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = A.fwd_kvcache8(q, k8, v8, ks, vs, None, True)
+        calls.append((g, got, want, torch.cuda.Stream(), (q, k8, v8, ks, vs)))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for g, got, _, s, _ in calls:
+            with torch.cuda.stream(s):
+                got[0].zero_()
+                g.replay()
+    status_ok()
+    for _, got, want, _, _ in calls:
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 @pytest.mark.parametrize("Hq,Nq,block,dtype", [(8, 1, 64, "bf16"), (8, 3, 16, "f16"), (32, 4, 32, "bf16")])
 def test_attend_long_caches_of_64_columns(dev, Hq, Nq, block, dtype):
     """Enough tiles for 64 keys each."""

@@ -87,6 +87,27 @@ def test_weights_long_caches(dev, Hq, Nq, d):
     status_ok()
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("Nq", [127, 128, 129, 257, 1000])
+def test_weights_walk_over_heads(dev, causal, Nq):
+    """Heads a little shorter, as long as and longer than a tile, caches shorter and longer than the
+    queries: which tiles see a key, for whole items and for those that several CTAs share."""
+    run_weights(dev, 20, 6, 2, Nq, 1100, 64, "bf16", [1100 - 53 * b for b in range(20)], causal, seed=Nq)
+    run_weights(dev, 2, 3, 1, Nq, 1100, 128, "f16", [1100, Nq // 2], causal, seed=Nq)
+
+
+def test_weights_and_evict_with_thousands_of_sequences(dev):
+    B = 5000
+    lens = [(13 * b) % 34 for b in range(B)]
+    run_weights(dev, B, 4, 2, 1, 33, 16, "bf16", lens, True, seed=4)
+    k, w = randn(1, (B, 2, 33, 16), dev, torch.bfloat16), randn(2, (B, 2, 33), dev, torch.float32)
+    got = A.kvcache_evict(k, k, w, 9, 4, torch.tensor(lens, dtype=torch.int32, device=dev))
+    status_ok()
+    some = [0, 1, 33, 1234, 2500, 4097, B - 1]
+    check_evict(k[some], k[some], w[some], 9, 4, [lens[b] for b in some], tuple(x[some] for x in got),
+                tuple(torch.zeros_like(x[some]) for x in got[:2]))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("Nq", [1, 9, 200, 600])
