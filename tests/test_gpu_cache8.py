@@ -180,6 +180,12 @@ def test_attend_prefill(dev, cache, Nq, Nk):
     run_attend(dev, 1, 4, 4, Nq, Nk, 64, 16, "f16", cache, None, False, seed=6)
 
 
+def test_attend_many_rows_on_long_caches(dev):
+    """More tokens than the expansion has CTAs for at once."""
+    run_attend(dev, 2, 142, 2, 1, 100001, 16, 16, "bf16", "i8", [100001, 80000], False, seed=1)
+    run_attend(dev, 3, 16, 4, 20, 40001, 64, 32, "f16", "e4m3", [40001, 1, 39000], True, seed=2)
+
+
 def test_attend_many_short_sequences(dev):
     lens = [(37 * b) % 130 for b in range(120)]
     run_attend(dev, 120, 8, 4, 1, 130, 128, 64, "bf16", "i8", lens, True, seed=7)
