@@ -672,9 +672,12 @@ Cache8Plan cache8_plan(int B, int Hkv, int R, int Nk, int d) {
           round256(static_cast<size_t>(pairs) * sizeof(int2))};
 }
 
-// Many rows: the key ranges, one as soon as the row blocks fill the GPU twice (a second pass over the
-// fp32 parts costs more than the last wave's idle SMs), and the workspace: the expanded K and V
-// and the units of V, then the ranges' parts.
+// Many rows: the key ranges, and the workspace: the expanded K and V and the units of V, then the ranges' parts.
+// With n ranges each of 152 CTAs takes every 152nd item, about 6 us for an item and 1 for each of its 128-key
+// tiles, and the combination 5 us and 0.55 a range, or what its parts' bytes take at a third of the copy rate:
+// the n of the least sum.  (Beside the rule of the 16-bit cache, about 8 items a CTA, with one range from 304
+// row blocks on: 1 x 4 heads, 128 rows, 32k keys 56 us for 100; 1 x 8, 2048 rows, 512 keys 17 for 42; 3 x 8,
+// 1280 rows, 4096 keys 89 for 147; 1 x 8, 2800 rows, 16k keys 214 for 224; 4 x 8, 2048 rows, 8192 keys 198.)
 struct Kv8Plan {
   KvSplit split;
   size_t cache_bytes, unit_bytes, o_bytes, lse_bytes;  // cache_bytes: K or V
@@ -682,7 +685,19 @@ struct Kv8Plan {
 Kv8Plan kv8_plan(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
   const long long R = static_cast<long long>(Hq / Hkv) * Nq, bh = static_cast<long long>(B) * Hkv;
   Kv8Plan plan{};
-  plan.split = kv_split(B, Hq, Hkv, Nq, Nk, bh * ((R + attn::kBM - 1) / attn::kBM) >= 2 * 152 ? 1 : 0);
+  const long long tiles = (static_cast<long long>(Nk) + attn::kBN - 1) / attn::kBN, blocks = bh * ((R + attn::kBM - 1) / attn::kBM);
+  double least = 0.;
+  for (long long n = 1; n <= std::min(tiles, 128LL); ++n) {
+    const long long each = (tiles + n - 1) / n, ranges = (tiles + each - 1) / each;
+    const double bytes = static_cast<double>(bh) * R * ranges * d * 8;  // written and read
+    const double us = static_cast<double>((blocks * ranges + 151) / 152) * (6. + static_cast<double>(each)) +
+                      (ranges > 1 ? 5. + std::max(0.55 * static_cast<double>(ranges), bytes / 2.3e6) : 0.);
+    if (n == 1 || us < least) {
+      least = us;
+      plan.split = {static_cast<int>(ranges), static_cast<int>(each)};
+    }
+  }
+  if (tiles <= 0) plan.split = {1, 1};
   plan.cache_bytes = round256(static_cast<size_t>(bh) * Nk * d * 2);
   plan.unit_bytes = round256(static_cast<size_t>(bh) * sizeof(float));
   if (plan.split.n_splits > 1) {
