@@ -672,7 +672,7 @@ Cache8Plan cache8_plan(int B, int Hkv, int R, int Nk, int d) {
           round256(static_cast<size_t>(pairs) * sizeof(int2))};
 }
 
-// Many rows: the key ranges, and the workspace: the expanded K and V and the units of V, then the ranges' parts.
+// Many rows: the key ranges, and the workspace: the expanded K and V, the units of V and its scales' logarithms, then the ranges' parts.
 // With n ranges each of 152 CTAs takes every 152nd item, about 6 us for an item and 1 for each of its 128-key
 // tiles, and the combination 5 us and 0.55 a range, or what its parts' bytes take at a third of the copy rate:
 // the n of the least sum.  (Beside the rule of the 16-bit cache, about 8 items a CTA, with one range from 304
@@ -680,7 +680,7 @@ Cache8Plan cache8_plan(int B, int Hkv, int R, int Nk, int d) {
 // 1280 rows, 4096 keys 89 for 147; 1 x 8, 2800 rows, 16k keys 214 for 224; 4 x 8, 2048 rows, 8192 keys 198.)
 struct Kv8Plan {
   KvSplit split;
-  size_t cache_bytes, unit_bytes, o_bytes, lse_bytes;  // cache_bytes: K or V
+  size_t cache_bytes, unit_bytes, log_bytes, o_bytes, lse_bytes;  // cache_bytes: K or V; log_bytes: for the smallest block
 };
 Kv8Plan kv8_plan(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
   const long long R = static_cast<long long>(Hq / Hkv) * Nq, bh = static_cast<long long>(B) * Hkv;
@@ -700,6 +700,7 @@ Kv8Plan kv8_plan(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
   if (tiles <= 0) plan.split = {1, 1};
   plan.cache_bytes = round256(static_cast<size_t>(bh) * Nk * d * 2);
   plan.unit_bytes = round256(static_cast<size_t>(bh) * sizeof(float));
+  plan.log_bytes = round256(static_cast<size_t>(bh) * ((static_cast<size_t>(Nk) + 15) / 16) * sizeof(float));
   if (plan.split.n_splits > 1) {
     plan.o_bytes = round256(static_cast<size_t>(plan.split.n_splits) * bh * R * d * sizeof(float));
     plan.lse_bytes = round256(static_cast<size_t>(plan.split.n_splits) * bh * R * sizeof(float));
@@ -719,7 +720,8 @@ attn_status_t fwd_kv8(const attn::Cache8Params& c, void* workspace, int Hq, attn
   void* const k16 = ws;
   void* const v16 = ws + plan.cache_bytes;
   float* const v_unit = reinterpret_cast<float*>(ws + 2 * plan.cache_bytes);
-  char* const parts = ws + 2 * plan.cache_bytes + plan.unit_bytes;
+  float* const v_log = reinterpret_cast<float*>(ws + 2 * plan.cache_bytes + plan.unit_bytes);
+  char* const parts = ws + 2 * plan.cache_bytes + plan.unit_bytes + plan.log_bytes;
   FwdParams p{};
   p.o = c.o;
   p.lse = c.lse;
@@ -737,6 +739,7 @@ attn_status_t fwd_kv8(const attn::Cache8Params& c, void* workspace, int Hq, attn
   p.out_f32 = c.out_f32;
   p.k_scale = c.k_scale;
   p.v_unit = v_unit;
+  p.v_log = v_log;
   p.n_blocks = c.n_blocks;
   p.block_shift = c.block_shift;
   FwdMaps maps;
@@ -748,7 +751,7 @@ attn_status_t fwd_kv8(const attn::Cache8Params& c, void* workspace, int Hq, attn
     maps.o = maps.q;
   else if (!make_dense_map(&maps.o, c.o, dtype, bh, c.R, c.d))
     return ATTN_ERR_CUDA;
-  if (attn::launch_cache8_expand(c, k16, v16, v_unit, p.n_splits == 1, dtype, cache_dtype, s) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (attn::launch_cache8_expand(c, k16, v16, v_unit, v_log, p.n_splits == 1, dtype, cache_dtype, s) != cudaSuccess) return ATTN_ERR_CUDA;
   const cudaError_t e = attn::launch_fwd_kv8(maps, p, dtype, c.causal != 0, s);
   if (e != cudaSuccess || p.n_splits == 1) return from_cuda(e);
   return from_cuda(attn::launch_kv_combine(p, dtype, c.causal != 0, s));
@@ -796,7 +799,7 @@ size_t attn_fwd_kvcache8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk,
   const size_t R = static_cast<size_t>(Hq / Hkv) * Nq;
   if (R > static_cast<size_t>(attn::kCache8Rows)) {
     const Kv8Plan plan = kv8_plan(B, Hq, Hkv, Nq, Nk, d);
-    return 2 * plan.cache_bytes + plan.unit_bytes + plan.o_bytes + plan.lse_bytes;
+    return 2 * plan.cache_bytes + plan.unit_bytes + plan.log_bytes + plan.o_bytes + plan.lse_bytes;
   }
   const Cache8Plan plan = cache8_plan(B, Hkv, static_cast<int>(R), Nk, d);
   return plan.o_bytes + plan.lse_bytes + plan.parts_bytes;

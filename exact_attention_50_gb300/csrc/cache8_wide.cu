@@ -4,10 +4,12 @@
 // With R rows per kv head the forward reads every key R / 128 times, so expanding inside it would
 // repeat the conversion as often, on the warps whose exponentials bound it; once costs 5 bytes of
 // traffic per code.  K is expanded to bare codes, exact in either 16-bit type, and its scales
-// multiply the scores in fp32.  V is expanded to code * scale / unit in fp16, the unit the largest
-// scale of the head, rounded once (half a step 2^-11; absolute 2^-25 units where a scale is below
-// 2^-14 of it), and P, at most 2^8, is fp16 as well: with both in bf16 the outputs' error was 1.5
-// times that of their own rounding (2^-8), with either type it is now that alone.
+// multiply the scores in fp32.  P, at most 2^8, and V are fp16 whatever the type.  For bf16 V is code * scale /
+// unit, the unit the largest scale of the head, rounded once (half a step 2^-11; absolute 2^-25 units where
+// a scale is below 2^-14 of it): the outputs' error is that of their own rounding (2^-8) then, with both in
+// bf16 it was 1.5 times that.  For fp16 it would be 1.6 times that of the outputs' rounding (2^-11), so there V
+// is bare codes, exact, and log2 of scale / unit goes into P's exponent: 1.3 times.  A scale below
+// 2^-24 of the unit counts as that.
 #include <algorithm>
 #include <type_traits>
 #include "cache8.cuh"
@@ -60,7 +62,8 @@ __device__ __forceinline__ void unseen_rows(const Cache8Params& p, int bh, int L
 // read more of than a quarter of its codes' traffic, while there are 16 CTAs per SM (4 heads of 2^20 tokens
 // in blocks of 16, 128 rows: 1066 us, with a CTA for each 128 tokens 1557; in blocks of 128: 960 and 956).
 template <typename T, typename Code>
-__global__ void __launch_bounds__(256) expand_kernel(const Cache8Params p, T* k16, __half* v16, float* v_unit, int per, bool final_rows) {
+__global__ void __launch_bounds__(256) expand_kernel(const Cache8Params p, T* k16, __half* v16, float* v_unit, float* v_log, int per, bool final_rows) {
+  constexpr bool kBare = std::is_same<T, __half>::value;
   __shared__ float s_max[8];
   const int bh = blockIdx.x / per, first = blockIdx.x % per;
   const int L = cache_len(p.cache_seqlens, bh / p.Hkv, p.Nk, nullptr, false);
@@ -99,13 +102,18 @@ __global__ void __launch_bounds__(256) expand_kernel(const Cache8Params p, T* k1
     const size_t base = (static_cast<size_t>(bh) * p.Nk + j0) * p.d;
     uint4* ko = reinterpret_cast<uint4*>(k16 + base);
     uint4* vo = reinterpret_cast<uint4*>(v16 + base);
+    const int block = (j0 >> p.block_shift) + threadIdx.x;  // of the blocks that hold tokens
+    if (kBare && block <= (min(j0 + 128, L) - 1) >> p.block_shift) {
+      const float r = unit == 0.f ? 0.f : vs[block] / unit;
+      v_log[static_cast<size_t>(bh) * p.n_blocks + block] = r < 0x1p-24f ? -24.f : log2f(r);  // NaN stays
+    }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int i = u * 256 + threadIdx.x;
       if (i >= n) break;
       const int j = j0 + i / chunks;
       if (j < L) {
-        const float r = unit == 0.f ? 0.f : vs[j >> p.block_shift] / unit;
+        const float r = kBare ? 1.f : unit == 0.f ? 0.f : vs[j >> p.block_shift] / unit;
         expand16<T, Code>(kw[u], 1.f, ko + 2 * i);
         expand16<__half, Code>(vw[u], r, vo + 2 * i);
       } else {  // the tile's rest: a weight of zero times what lies there has to be zero
@@ -120,25 +128,25 @@ __global__ void __launch_bounds__(256) expand_kernel(const Cache8Params p, T* k1
 }
 
 template <typename T>
-cudaError_t expand(const Cache8Params& p, void* k16, void* v16, float* v_unit, bool final_rows, attn_cache_dtype_t cache,
+cudaError_t expand(const Cache8Params& p, void* k16, void* v16, float* v_unit, float* v_log, bool final_rows, attn_cache_dtype_t cache,
                    cudaStream_t stream) {
   const long long heads = static_cast<long long>(p.B) * p.Hkv;
   const long long tiles = (p.Nk + 127) / 128, each = std::max(1, p.n_blocks / (40 * p.d));
   const int per = static_cast<int>(std::min(tiles, std::max((tiles + each - 1) / each, (16 * 152 + heads - 1) / heads)));
   const int grid = static_cast<int>(heads) * per;
   if (cache == ATTN_CACHE_I8)
-    expand_kernel<T, CodeI8><<<grid, 256, 0, stream>>>(p, static_cast<T*>(k16), static_cast<__half*>(v16), v_unit, per, final_rows);
+    expand_kernel<T, CodeI8><<<grid, 256, 0, stream>>>(p, static_cast<T*>(k16), static_cast<__half*>(v16), v_unit, v_log, per, final_rows);
   else
-    expand_kernel<T, CodeE4m3><<<grid, 256, 0, stream>>>(p, static_cast<T*>(k16), static_cast<__half*>(v16), v_unit, per, final_rows);
+    expand_kernel<T, CodeE4m3><<<grid, 256, 0, stream>>>(p, static_cast<T*>(k16), static_cast<__half*>(v16), v_unit, v_log, per, final_rows);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_cache8_expand(const Cache8Params& p, void* k16, void* v16, float* v_unit, bool final_rows, attn_dtype_t dtype,
+cudaError_t launch_cache8_expand(const Cache8Params& p, void* k16, void* v16, float* v_unit, float* v_log, bool final_rows, attn_dtype_t dtype,
                                  attn_cache_dtype_t cache, cudaStream_t stream) {
-  return dtype == ATTN_F16 ? expand<__half>(p, k16, v16, v_unit, final_rows, cache, stream)
-                           : expand<__nv_bfloat16>(p, k16, v16, v_unit, final_rows, cache, stream);
+  return dtype == ATTN_F16 ? expand<__half>(p, k16, v16, v_unit, v_log, final_rows, cache, stream)
+                           : expand<__nv_bfloat16>(p, k16, v16, v_unit, v_log, final_rows, cache, stream);
 }
 
 }  // namespace attn

@@ -32,10 +32,11 @@ struct FwdParams {
   int n_splits, tiles_per_split;
   float* o_part;           // [n_splits, B*Hkv*R, d]
   float* lse_part;         // [n_splits, B*Hkv*R] (natural log)
-  // KV cache in 8 bits (kModeKv8): the key codes' scales [B*Hkv, n_blocks], 2^block_shift keys each,
-  // and the unit of each head's values [B*Hkv]
+  // KV cache in 8 bits (kModeKv8): the key codes' scales [B*Hkv, n_blocks], 2^block_shift keys each, the
+  // unit of each head's values [B*Hkv], and (fp16) log2 of what their scales are of it [B*Hkv, n_blocks]
   const float* k_scale;
   const float* v_unit;
+  const float* v_log;
   int n_blocks, block_shift;
 };
 
@@ -195,11 +196,12 @@ constexpr int cache8_keys(long long pairs, int R, int Nk, int d) {
 }
 cudaError_t launch_cache8_fwd(const CUtensorMap& k, const CUtensorMap& v, const Cache8Params& p, attn_dtype_t dtype,
                               attn_cache_dtype_t cache, cudaStream_t stream);
-// Many rows: K's codes in dtype and V's values in fp16, in units of the largest scale of their head
-// (v_unit [B*Hkv]), [B*Hkv, Nk, d] each, for the tokens that the caches hold and zeros behind them up to a
+// Many rows: K's codes in dtype and V in fp16, [B*Hkv, Nk, d] each, the largest V scale of a head (v_unit
+// [B*Hkv]) and, for fp16, where V is bare codes, log2 of each one's part of it, at least -24 (v_log
+// [B*Hkv, n_blocks]); for bf16 V is in units of v_unit; for the tokens that the caches hold and zeros behind them up to a
 // tile's end; and, when the forward writes final rows (one key range), those of which it computes nothing.
 // Then the tcgen05 forward in kModeKv8 on that.
-cudaError_t launch_cache8_expand(const Cache8Params& p, void* k16, void* v16, float* v_unit, bool final_rows, attn_dtype_t dtype,
+cudaError_t launch_cache8_expand(const Cache8Params& p, void* k16, void* v16, float* v_unit, float* v_log, bool final_rows, attn_dtype_t dtype,
                                  attn_cache_dtype_t cache, cudaStream_t stream);
 cudaError_t launch_fwd_kv8(const FwdMaps& maps, const FwdParams& p, attn_dtype_t dtype, bool causal, cudaStream_t stream);
 

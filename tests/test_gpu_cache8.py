@@ -258,6 +258,44 @@ def test_attend_long_runs_behind_short_sequences(dev, cache, d, Hq, Nq):
     status_ok()
 
 
+@pytest.mark.parametrize("cache", ["i8", "e4m3"])
+@pytest.mark.parametrize("block", [16, 64])
+@pytest.mark.parametrize("dtype,Nq", [("f16", 100), ("bf16", 100), ("f16", 1), ("bf16", 5)])
+def test_attend_error_is_that_of_two_roundings_at_most(dev, cache, block, dtype, Nq):
+    """Root mean square: the outputs' rounding and that of P, independent and of one size in fp16 (where
+    codes add none): sqrt(2) times the former; in bf16 P's, and with many rows V's, are an eighth each.
+    A twentieth over that for the sample (102400 outputs at Nq = 100, at least 2048)."""
+    k8, ks = P.quantise(rows(1, (2, 2, 3000, 128), dev), block, cache)
+    v8, vs = P.quantise(rows(2, (2, 2, 3000, 128), dev), block, cache)
+    q = torch.randn(2, 8, Nq, 128, generator=torch.Generator(dev).manual_seed(3), device=dev).to(DT[dtype])
+    o, _ = A.fwd_kvcache8(q, k8, v8, ks, vs, None, True, None, block)
+    status_ok()
+    ro = P.attend(q, P.dequantise(k8, ks, block), P.dequantise(v8, vs, block), None, True, None)[0]
+    alone = (ro.to(q.dtype).double() - ro).norm()
+    assert float((o.double() - ro).norm() / alone) <= 1.05 * (2 ** 0.5 if dtype == "f16" else (1 + 2 / 64) ** 0.5)
+
+
+@pytest.mark.parametrize("block", [16, 128])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_attend_many_rows_scales_of_very_different_size(dev, block, dtype):
+    """Values' scales over 2^-20 .. 1, some of them and a key's 0."""
+    k8, ks = P.quantise(rows(1, (2, 2, 1500, 64), dev), block, "i8")
+    v8, vs = P.quantise(rows(2, (2, 2, 1500, 64), dev), block, "i8")
+    vs = vs * torch.exp2(-(torch.arange(vs.shape[2], device=dev) * 7 % 21).float())
+    vs[:, :, 3], vs[0, 0, 5], ks[:, :, 4] = 0, 0, 0
+    q = torch.randn(2, 8, 60, 64, generator=torch.Generator(dev).manual_seed(3), device=dev).to(DT[dtype])
+    cl = torch.tensor([1500, 1111], dtype=torch.int32, device=dev)
+    for causal in (True, False):
+        o32, lse = A.fwd_kvcache8(q, k8, v8, ks, vs, cl, causal, None, block, out_f32=True)
+        o, _ = A.fwd_kvcache8(q, k8, v8, ks, vs, cl, causal, None, block)
+        status_ok()
+        check_attend(o32, o, lse, q, k8, v8, ks, vs, block, [1500, 1111], causal)
+    none = torch.zeros_like(vs)
+    o, _ = A.fwd_kvcache8(q, k8, v8, ks, none, cl, True, None, block)
+    status_ok()
+    assert bool((o == 0).all())
+
+
 def test_attend_scales_of_very_different_size(dev):
     """Blocks whose value scales lie many powers of two apart, the weights concentrated on the
     small ones and on the large ones; a block of zeros; rows of large and of tiny queries."""
