@@ -139,3 +139,67 @@ def evict(k, v, w, L, keep, recent):
     # NaN above infinity: a second key
     best = np.lexsort((np.arange(len(old)), -key, ~np.isnan(old)))[:keep]
     return np.sort(np.concatenate((best, np.arange(L - recent, L))))
+
+
+def attend8(q, k8, v8, ks, vs, block, lens, causal, scale=None):
+    """Attention over an 8-bit cache in 64 bits, with the errors that it may have before its output is
+    rounded.  Returns o, lse, a bound [B,Hq,Nq,d] of each element's error, one [B,Hq,Nq] of the length of
+    a row's error vector where rounding errors of different keys are independent, and E of attend.
+
+    The kernels round P vs of a key to fp16 (u = 2^-11 of it; a term below 2^-14 of the unit, 2^-25 of the
+    unit), the unit at most the largest P vs among the keys that the row sees, and multiply by
+    the codes exactly.  A score's error E enters numerator and denominator, the exponential's is
+    2^-18.  For the length: (u + E)^2 per key in squares, and 2^-17 of sum P|V| for what the fp32 sums
+    and the exponential may have in common."""
+    B, Hq, Nq, d = q.shape
+    Hkv, Nk = k8.shape[1:3]
+    G = Hq // Hkv
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    new = lambda *s: torch.zeros(B, Hq, Nq, *s, dtype=torch.float64, device=q.device)
+    o, bound, length, E, lse = new(d), new(d), new(), new(), new() - math.inf
+    at = torch.arange(Nk, device=q.device) // block
+    u = 2.0 ** -11
+    for b in range(B):
+        L = Nk if lens is None else int(lens[b])
+        if L == 0:
+            continue
+        m = seen_keys(Nq, L, L, causal, q.device)
+        for h in range(Hq):
+            g = h // G
+            sv, code = vs[b, g].double()[at[:L]], v8[b, g, :L].float().double()
+            kk = k8[b, g, :L].float().double() * ks[b, g].double()[at[:L]][:, None]
+            vv, qq = code * sv[:, None], q[b, h].double()
+            s = (qq @ kk.T * scale).masked_fill(~m, -math.inf)
+            row = torch.logsumexp(s, -1)
+            p = torch.exp(s - torch.where(row == -math.inf, torch.zeros_like(row), row)[:, None])
+            e = (qq.abs() @ kk.abs().T * scale).amax(-1) * (d + 16) * 2.0 ** -24
+            t = p * sv
+            top = t.amax(-1, keepdim=True)
+            small = (t < 2.0 ** -14 * top).double()
+            pv = p @ vv.abs()
+            low = 2.0 ** -25 * top
+            o[b, h], lse[b, h], E[b, h] = p @ vv, row, e
+            bound[b, h] = pv * (u + 2 * e[:, None] + 2.0 ** -18) + low * (small @ code.abs())
+            squares = (u + e)[:, None] ** 2 * ((p * p) @ (vv * vv)) + low ** 2 * (small @ (code * code))
+            length[b, h] = (squares + (2.0 ** -17 * pv) ** 2).sum(-1).sqrt()
+    return o, lse, bound, length, E
+
+
+def check_attend8(o32, o, lse, q, k8, v8, ks, vs, block, lens, causal, scale=None):
+    """o32: the fp32 outputs, o: those in q's type (or None).  Every element, every row's length (where weights are
+    even, a tile of wrong values hides within the elements' bound on a long cache, not within this one), the LSE."""
+    ro, rl, bound, length, E = attend8(q, k8, v8, ks, vs, block, lens, causal, scale)
+    assert bool(torch.isfinite(o32).all())
+    err = (o32.double() - ro).abs()
+    assert bool((err <= bound).all()), float((err / bound.clamp(min=1e-300)).max())
+    got = err.norm(dim=-1)
+    assert bool((got <= length).all()), float((got / length.clamp(min=1e-300)).max())
+    if o is not None:
+        u = HALF[q.dtype]
+        tiny = 2.0 ** -25 if q.dtype == torch.float16 else 2.0 ** -134  # half the smallest step of the type
+        assert bool(((o.double() - ro).abs() <= bound + u * (ro.abs() + bound) + tiny).all())
+    empty = torch.isneginf(rl)
+    assert torch.equal(torch.isneginf(lse), empty)
+    assert bool((o32[empty] == 0).all())
+    off = (lse.double() - rl).abs().masked_fill(empty, 0)
+    assert bool((off <= E + 2.0 ** -18 + rl.abs().masked_fill(empty, 0) * 2.0 ** -22).all()), float(off.max())
