@@ -35,14 +35,16 @@
 //
 // What it reaches (8 sequences of 16k to 32k keys, 32 over 8 heads, d = 128, int8): 77 us, 5.5 TB/s, 81% of
 // the copy rate: 71 us in this kernel, the rest the merge (5 us alone, partly hidden) and the launch; 75 us with
-// one query row per kv head.  With 16 rows (NB = 2) 86 us.  With 32 (two warps per tile, the codes converted
-// twice) 147 us: 247 registers leave two warps per scheduler, which issue in 45% of the cycles, waiting
+// one query row per kv head.  With 16 rows (NB = 2) 84 us.  With 32 (two warps per tile, the codes converted
+// twice) 143 us: 251 registers leave two warps per scheduler, which issue in 45% of the cycles, waiting
 // mostly for results of fixed latency; ALU 41%, tensor pipe 33%, DRAM 38%, so no unit bounds it.
 //
 // Rounding: q in bf16 becomes fp16 after a multiplication by a power of two per row (largest
-// element in [2^14, 2^15)), exact but for elements below 2^-28 of that.  P is rounded to fp16
-// (half a step 2^-11) after its multiplication by vs / (the largest vs so far): a block whose
-// scale is below 2^-14 of that has absolute errors of 2^-25 times the largest value instead.
+// element in [2^14, 2^15)), exact but for elements below 2^-28 of that.  P vs is rounded to fp16 (half a
+// step 2^-11) in units near the largest P vs among the keys that the row sees, so an error
+// is relative to the row's own terms, whatever the scales of other blocks; a term below 2^-14 of the largest
+// has an absolute error of 2^-25 of that.  A block whose scale is below 2^-60 of the largest of a worker's
+// keys, and one below 2^-126, counts as values of zero.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -54,6 +56,7 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr float kLazy = 8.0f;   // log2 units by which a tile's maximum may exceed the running one
+constexpr int kSpread = 60;     // powers of two that value scales may lie apart
 
 // NB: blocks of 8 query rows per warp, 1 or 2.
 template <int DP, int NB, int KEYS>
@@ -415,7 +418,12 @@ __global__ void __launch_bounds__(kThreads, (Layout<DP, NB, KEYS>::kCtas))
       m[b][0] = m[b][1] = -INFINITY;
       l[b][0] = l[b][1] = 0.f;
     }
-    float vref = 0.f;  // the largest value scale so far: o is in units of it
+    // The value scales lie in the exponents: with w = log2(vs) and m the running maximum of s + w over the keys
+    // that a row sees,
+    //   o = sum 2^(s + w - m) cv,  l = sum 2^(s + w - m) 2^(c - w):  O = 2^c o / l,  LSE = m - c + log2(l).
+    // c, of the first tile's largest scale, only keeps l's terms within float's range.
+    int vexp = 0;
+    float vhigh = 0.f;  // 2^(c + kSpread); 0 before the first scale
     {
       for (int x = 0; x < part; ++x, ++n) {
         const uint32_t st = n % stages;
@@ -468,17 +476,45 @@ __global__ void __launch_bounds__(kThreads, (Layout<DP, NB, KEYS>::kCtas))
         }
         // ---- scale, mask, running maximum
         const int key0 = (w.j + x * stride) * kKeys;
-        const float v_old = vref;
+        float largest = 0.f;
 #pragma unroll
-        for (int i = 0; i < kGroups; ++i) vref = fmaxf(vref, vg[i]);
-        bool move = vref != v_old;
+        for (int i = 0; i < kGroups; ++i) largest = fmaxf(largest, vg[i]);
+        if (largest > vhigh) {  // the first scale, or one that leaves c far behind
+          const int e = min(max(static_cast<int>(__float_as_uint(largest) >> 23), 1), 254);
+          const float up = static_cast<float>(e - 127 - vexp), down = ex2_approx(-up);
+          vexp = e - 127;
+          vhigh = __uint_as_float(static_cast<uint32_t>(min(e + kSpread, 255)) << 23);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            m[b][0] += up;
+            m[b][1] += up;
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) {
+              o[i][b][0] *= down; o[i][b][1] *= down; o[i][b][2] *= down; o[i][b][3] *= down;
+            }
+          }
+        }
+        // per group: w, 2^(c - w), and what P is masked with: nothing of a scale of 0, or of one too small to
+        // count beside the largest
+        float wv[kGroups], lw[kGroups];
+        uint32_t counts[kGroups];
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+          const float least = static_cast<float>(vexp - kSpread), x = __log2f(vg[i]);
+          const bool none = __float_as_uint(vg[i]) < 0x00800000u || x < least;
+          wv[i] = none ? least : x;
+          lw[i] = ex2_approx(static_cast<float>(vexp) - wv[i]);
+          counts[i] = none ? 0u : 0xffffffffu;
+        }
+        bool move = false;
         float mx[NB][2];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
 #pragma unroll
           for (int i = 0; i < kGroups; ++i) {
             const float f0 = f[b][0] * kg[i], f1 = f[b][1] * kg[i];
-            s[i][b][0] *= f0; s[i][b][1] *= f1; s[i][b][2] *= f0; s[i][b][3] *= f1;
+            s[i][b][0] = fmaf(s[i][b][0], f0, wv[i]); s[i][b][1] = fmaf(s[i][b][1], f1, wv[i]);
+            s[i][b][2] = fmaf(s[i][b][2], f0, wv[i]); s[i][b][3] = fmaf(s[i][b][3], f1, wv[i]);
           }
           if (__any_sync(0xffffffffu, key0 + kKeys - 1 > min(last[b][0], last[b][1]))) {
 #pragma unroll
@@ -505,28 +541,23 @@ __global__ void __launch_bounds__(kThreads, (Layout<DP, NB, KEYS>::kCtas))
           for (int e = 0; e < 2; ++e) move |= mx[b][e] > m[b][e] + kLazy || (m[b][e] == -INFINITY && mx[b][e] != -INFINITY);
         }
         if (__any_sync(0xffffffffu, move)) {
-          const float back = v_old == vref ? 1.f : v_old / vref;
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            float c[2];
+            float a[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const float top = fmaxf(m[b][e], mx[b][e]);
-              const float a = m[b][e] == top ? 1.f : m[b][e] == -INFINITY ? 0.f : ex2_approx(m[b][e] - top);
+              a[e] = m[b][e] == top ? 1.f : m[b][e] == -INFINITY ? 0.f : ex2_approx(m[b][e] - top);
               m[b][e] = top;
-              l[b][e] *= a;
-              c[e] = a * back;
+              l[b][e] *= a[e];
             }
 #pragma unroll
             for (int i = 0; i < kCols; ++i) {
-              o[i][b][0] *= c[0]; o[i][b][1] *= c[1]; o[i][b][2] *= c[0]; o[i][b][3] *= c[1];
+              o[i][b][0] *= a[0]; o[i][b][1] *= a[1]; o[i][b][2] *= a[0]; o[i][b][3] *= a[1];
             }
           }
         }
-        float ratio[kGroups];
-#pragma unroll
-        for (int i = 0; i < kGroups; ++i) ratio[i] = vref == 0.f ? 0.f : vg[i] / vref;
-        // ---- P = exp2(S - m), its sum, and P vs / vref as fp16 B fragments
+        // ---- P = exp2(S + w - m), its sum, and fp16 B fragments
         uint32_t pb[kGroups][NB][2];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -535,10 +566,10 @@ __global__ void __launch_bounds__(kThreads, (Layout<DP, NB, KEYS>::kCtas))
           for (int i = 0; i < kGroups; ++i) {
             const float e0 = ex2_approx(s[i][b][0] - n0), e1 = ex2_approx(s[i][b][1] - n1);
             const float e2 = ex2_approx(s[i][b][2] - n0), e3 = ex2_approx(s[i][b][3] - n1);
-            l[b][0] += e0 + e2;
-            l[b][1] += e1 + e3;
-            pb[i][b][0] = transpose8x8(pack_half(e0 * ratio[i], e1 * ratio[i]));
-            pb[i][b][1] = transpose8x8(pack_half(e2 * ratio[i], e3 * ratio[i]));
+            l[b][0] = fmaf(e0 + e2, lw[i], l[b][0]);
+            l[b][1] = fmaf(e1 + e3, lw[i], l[b][1]);
+            pb[i][b][0] = transpose8x8(pack_half(e0, e1) & counts[i]);
+            pb[i][b][1] = transpose8x8(pack_half(e2, e3) & counts[i]);
           }
         }
         // a code behind the cache's end may be e4m3's NaN, which a weight of zero does not cancel
@@ -581,16 +612,23 @@ __global__ void __launch_bounds__(kThreads, (Layout<DP, NB, KEYS>::kCtas))
       }
     }
     if (!SPREAD && !ok) break;
-    // ---- this warp's part: sums over the eight lanes that share a row, o in units of one
+    // ---- this warp's part: sums over the eight lanes that share a row; the output, normalised before it is
+    // multiplied by 2^c, so that it overflows only where the values do; m and l in units of one
+    const float unit = __uint_as_float(static_cast<uint32_t>(vexp + 127) << 23);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
+      float il[2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], d);
+        m[b][e] -= static_cast<float>(vexp);
+        il[e] = l[b][e] == 0.f ? 0.f : 1.f / l[b][e];
+      }
 #pragma unroll
       for (int i = 0; i < kCols; ++i) {
-        o[i][b][0] *= vref; o[i][b][1] *= vref; o[i][b][2] *= vref; o[i][b][3] *= vref;
+        o[i][b][0] = o[i][b][0] * il[0] * unit; o[i][b][1] = o[i][b][1] * il[1] * unit;
+        o[i][b][2] = o[i][b][2] * il[0] * unit; o[i][b][3] = o[i][b][3] * il[1] * unit;
       }
     }
     if constexpr (SPREAD) {
@@ -633,8 +671,8 @@ __global__ void __launch_bounds__(kThreads, (Layout<DP, NB, KEYS>::kCtas))
         for (int k = 0; k < workers; ++k) {
           const float2 ml = all_ml[k * kRows + r];
           const float2 v = *reinterpret_cast<const float2*>(cluster.map_shared_rank(part_o + ((k % kWarps) * kRows + r) * DP + c, k / kWarps));
-          const float a = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top);
-          sum += ml.y * a;
+          const float a = ml.y * (ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top));
+          sum += a;
           x += v.x * a;
           y += v.y * a;
         }
@@ -665,7 +703,6 @@ __global__ void __launch_bounds__(kThreads, (Layout<DP, NB, KEYS>::kCtas))
         for (int e = 0; e < 2; ++e) {
           const int r = row0 + 8 * b + 2 * t + e;
           if (r >= p.R) continue;
-          const float il = l[b][e] == 0.f ? 0.f : 1.f / l[b][e];
           const float lse2 = l[b][e] == 0.f ? -INFINITY : m[b][e] + __log2f(l[b][e]);
           const size_t row = whole ? bh * p.R + r : slot * p.R + r;
           if (g == 0) {
@@ -674,12 +711,12 @@ __global__ void __launch_bounds__(kThreads, (Layout<DP, NB, KEYS>::kCtas))
           }
           // columns (DP / 8) g + i: element 2 (i % 2) + e of block i / 2
 #pragma unroll
-          for (int c = 0; c < DP / 8; c += 8) {
-            const int col = (DP / 8) * g + c;
+          for (int i = 0; i < DP / 8; i += 8) {
+            const int col = (DP / 8) * g + i;
             if (col >= p.d) continue;
             float y[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] = o[(c + k) / 2][b][2 * (k & 1) + e] * il;
+            for (int k = 0; k < 8; ++k) y[k] = o[(i + k) / 2][b][2 * (k & 1) + e];
             if (!whole || p.out_f32) {
               float4* dst = reinterpret_cast<float4*>((whole ? static_cast<float*>(p.o) : p.o_part) + row * p.d + col);
               dst[0] = make_float4(y[0], y[1], y[2], y[3]);
