@@ -3,15 +3,13 @@
 //
 // With R rows per kv head the forward reads every key R / 128 times, so expanding inside it would
 // repeat the conversion as often, on the warps whose exponentials bound it; once costs 5 bytes of
-// traffic per code.  K is expanded to bare codes, exact in either 16-bit type, and its scales
-// multiply the scores in fp32.  P, at most 2^8, and V are fp16 whatever the type.  For bf16 V is code * scale /
-// unit, the unit the largest scale of the head, rounded once (half a step 2^-11; absolute 2^-25 units where
-// a scale is below 2^-14 of it): the outputs' error is that of their own rounding (2^-8) then, with both in
-// bf16 it was 1.5 times that.  For fp16 it would be 1.6 times that of the outputs' rounding (2^-11), so there V
-// is bare codes, exact, and log2 of scale / unit goes into P's exponent: 1.3 times.  A scale below
-// 2^-24 of the unit counts as that.
+// traffic per code.  K and V are expanded to bare codes, exact in either 16-bit type; K's scales multiply
+// the scores in fp32, and log2 of V's, in units of the head's largest, goes into P's exponent.  So the one
+// rounding is that of P (fp16 whatever the type, half a step 2^-11), relative to the largest P vs of the
+// row's own keys: scale / unit in V (a chunk of 2048 queries took 817 to 859 us with that, now 829 to 832) would lose
+// the digits of rows that see small scales only.  A block whose scale is below 2^-60 of the head's largest, or below 2^-126,
+// counts as values of zero.
 #include <algorithm>
-#include <type_traits>
 #include "cache8.cuh"
 
 namespace attn {
@@ -27,7 +25,7 @@ __device__ __forceinline__ uint32_t pair(const __nv_bfloat16*, float a, float b)
 }
 
 template <typename T, typename Code>
-__device__ __forceinline__ void expand16(const uint4 w, float scale, uint4* dst) {
+__device__ __forceinline__ void expand16(const uint4 w, uint4* dst) {
   const T* tag = nullptr;
   const uint32_t in[4] = {w.x, w.y, w.z, w.w};
   uint32_t out[8];
@@ -35,8 +33,8 @@ __device__ __forceinline__ void expand16(const uint4 w, float scale, uint4* dst)
   for (int i = 0; i < 4; ++i) {
     float x[4];
     Code::decode4(in[i], x);
-    out[2 * i] = pair(tag, x[0] * scale, x[1] * scale);
-    out[2 * i + 1] = pair(tag, x[2] * scale, x[3] * scale);
+    out[2 * i] = pair(tag, x[0], x[1]);
+    out[2 * i + 1] = pair(tag, x[2], x[3]);
   }
   dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
   dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
@@ -63,7 +61,7 @@ __device__ __forceinline__ void unseen_rows(const Cache8Params& p, int bh, int L
 // in blocks of 16, 128 rows: 1066 us, with a CTA for each 128 tokens 1557; in blocks of 128: 960 and 956).
 template <typename T, typename Code>
 __global__ void __launch_bounds__(256) expand_kernel(const Cache8Params p, T* k16, __half* v16, float* v_unit, float* v_log, int per, bool final_rows) {
-  constexpr bool kBare = std::is_same<T, __half>::value;
+  constexpr float kSpread = 60.f;
   __shared__ float s_max[8];
   const int bh = blockIdx.x / per, first = blockIdx.x % per;
   const int L = cache_len(p.cache_seqlens, bh / p.Hkv, p.Nk, nullptr, false);
@@ -97,25 +95,23 @@ __global__ void __launch_bounds__(256) expand_kernel(const Cache8Params p, T* k1
 #pragma unroll
   for (int i = 0; i < 8; ++i) unit = fmaxf(unit, s_max[i]);
   if (first == 0 && threadIdx.x == 0) v_unit[bh] = unit;
+  const float least = fmaxf(unit * 0x1p-60f, 0x1p-126f);  // scales below it count as 0
   for (int tile = first;;) {
     const int j0 = tile * 128, n = min(128, p.Nk - j0) * chunks;
     const size_t base = (static_cast<size_t>(bh) * p.Nk + j0) * p.d;
     uint4* ko = reinterpret_cast<uint4*>(k16 + base);
     uint4* vo = reinterpret_cast<uint4*>(v16 + base);
     const int block = (j0 >> p.block_shift) + threadIdx.x;  // of the blocks that hold tokens
-    if (kBare && block <= (min(j0 + 128, L) - 1) >> p.block_shift) {
-      const float r = unit == 0.f ? 0.f : vs[block] / unit;
-      v_log[static_cast<size_t>(bh) * p.n_blocks + block] = r < 0x1p-24f ? -24.f : log2f(r);  // NaN stays
-    }
+    if (block <= (min(j0 + 128, L) - 1) >> p.block_shift)
+      v_log[static_cast<size_t>(bh) * p.n_blocks + block] = vs[block] < least ? -kSpread : log2f(vs[block] / unit);  // NaN stays
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int i = u * 256 + threadIdx.x;
       if (i >= n) break;
       const int j = j0 + i / chunks;
       if (j < L) {
-        const float r = kBare ? 1.f : unit == 0.f ? 0.f : vs[j >> p.block_shift] / unit;
-        expand16<T, Code>(kw[u], 1.f, ko + 2 * i);
-        expand16<__half, Code>(vw[u], r, vo + 2 * i);
+        expand16<T, Code>(kw[u], ko + 2 * i);
+        expand16<__half, Code>(vs[j >> p.block_shift] < least ? make_uint4(0, 0, 0, 0) : vw[u], vo + 2 * i);
       } else {  // the tile's rest: a weight of zero times what lies there has to be zero
         const uint4 z = make_uint4(0, 0, 0, 0);
         ko[2 * i] = ko[2 * i + 1] = vo[2 * i] = vo[2 * i + 1] = z;

@@ -8,11 +8,9 @@
 // In the KV-cache mode a row is query i = row % Nq of the G query heads of a kv head, its keys
 // are those of one range of the cache, masked past the cache length L and, when causal, past
 // L - Nq + i; it writes fp32 partials that a combine kernel merges.  The 8-bit cache mode is that
-// mode on bare key codes in 16 bits, with the codes' scales applied to the scores, on values in fp16 in a
-// unit of each kv head (so P is fp16 too).  For fp16 outputs the values are bare codes as well, and what a
-// block's scale is of the unit goes into P as an offset of the exponent, taken back in the row sum: one
-// rounding less, 848 us for 820 on a chunk of 2048 queries, which bf16 outputs need not pay.  With one
-// key range it writes final outputs.
+// mode on bare key and value codes in 16 bits (the values and P in fp16): the key codes' scales multiply the
+// scores; log2 of what a block's value scale is of a unit of the kv head goes into P as an offset of the
+// exponent, taken back in the row sum.  With one key range it writes final outputs.
 // The tiling follows the attention-operator article (m.xxqk.cn/news/636956) section 2.2: Q/K/V
 // tiles staged on chip, the max-subtracted softmax kept in registers and only O written back.
 // The online max/sum update follows the FlashAttention-T review, best practice 4; scale and
@@ -265,7 +263,6 @@ __global__ void __launch_bounds__(512, 1)
   // an 8-bit cache in one range: the items' outputs are final, written as a dense item's are
   const bool kv_final = KV8 && p.n_splits == 1;
   using PElem = std::conditional_t<KV8, Elem<__half>, Elem<T>>;  // of P and V
-  constexpr bool OFFSETS = KV8 && !Elem<T>::kBf16;                // the values' scales in P's exponents
   // 16-bit output of a dense item, or of a varlen item whose 128 rows all lie in its
   // sequence: the epilogue warps stage the item's O tile in the item's Q slot (free once its
   // last S has run) and their thread 0 writes it with tile stores, then frees the slot.
@@ -718,7 +715,7 @@ __global__ void __launch_bounds__(512, 1)
         const int b = t & 1;
         // 8-bit cache: the K operand holds the bare codes; their scales (one per 16 to 128 keys) are
         // fetched before the wait and multiply the scores.  Past the cache's end none is read.
-        // vl (fp16): log2 of what the values' scales are of their unit.
+        // vl: log2 of what the values' scales are of their unit, an offset of the exponents.
         float ks[4], vl[4];
         if constexpr (KV8) {
           const int k0 = (it.j0 + j) * kBN + grp * 64;
@@ -727,7 +724,7 @@ __global__ void __launch_bounds__(512, 1)
           for (int i = 0; i < 4; ++i) {
             const bool in = (i == 0 || p.block_shift < 6) && k0 + 16 * i < it.seq_len;
             ks[i] = in ? __ldg(p.k_scale + head + ((k0 + 16 * i) >> p.block_shift)) : 0.f;
-            vl[i] = OFFSETS && in ? __ldg(p.v_log + head + ((k0 + 16 * i) >> p.block_shift)) : 0.f;
+            vl[i] = in ? __ldg(p.v_log + head + ((k0 + 16 * i) >> p.block_shift)) : 0.f;
           }
         }
         if (!mbar_wait_warp(s_full + b, (t >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
@@ -749,15 +746,17 @@ __global__ void __launch_bounds__(512, 1)
         }
         float sl2 = p.scale_log2, offset = 0.f;  // offset: of every exponent of the tile
         if constexpr (KV8) {
-          if (OFFSETS && p.block_shift >= 6) vl[1] = vl[2] = vl[3] = vl[0];
-          if (p.block_shift >= 6 && ks[0] > 0.f) {  // one scale for the group's 64 keys
+          if (p.block_shift >= 6) {
+            ks[1] = ks[2] = ks[3] = ks[0];
+            vl[1] = vl[2] = vl[3] = vl[0];
+          }
+          if (p.block_shift >= 6 && sl2 * ks[0] > 0.f) {  // one scale for the group's 64 keys
             sl2 *= ks[0];
-            if (OFFSETS) offset = vl[0];
+            offset = vl[0];
           } else {
-            if (p.block_shift >= 6) ks[1] = ks[2] = ks[3] = ks[0];
-            const float per = OFFSETS ? 1.f / p.scale_log2 : 0.f;
 #pragma unroll
-            for (int c = 0; c < 64; ++c) s[c] = OFFSETS ? fmaf(s[c], ks[c / 16], vl[c / 16] * per) : s[c] * ks[c / 16];
+            for (int c = 0; c < 64; ++c) s[c] = fmaf(s[c], sl2 * ks[c / 16], vl[c / 16]);
+            sl2 = 1.f;
           }
         }
         // keys key0 + c with c > lim are masked (past the diagonal, or past the sequence)
@@ -780,7 +779,7 @@ __global__ void __launch_bounds__(512, 1)
         m0 = max3f(m0, s[60], s[61]);
         m1 = max3f(m1, s[62], s[63]);
         float mx2 = max3f(m0, m1, fmaxf(m2, m3)) * sl2;  // scale > 0: max commutes with it
-        if constexpr (OFFSETS) mx2 += offset;
+        if constexpr (KV8) mx2 += offset;
         float alpha = 1.f;
         bool resc = false;
         if (mx2 > m + kRescaleLog2 || (m == -INFINITY && mx2 != -INFINITY)) {
@@ -821,11 +820,11 @@ __global__ void __launch_bounds__(512, 1)
         // sum in 4 paired chains, and the 16-bit pair of P.  In tiles with no masked key the
         // pairs selected by kPolyPairs run on the FMA pipe, the rest on the special-function
         // unit; masked tiles use the latter only (exact zeros).
-        const float nm = OFFSETS ? offset - mb : -mb;
+        const float nm = KV8 ? offset - mb : -mb;
         const uint64_t scl = f2_pack(sl2, sl2), nmb = f2_pack(nm, nm);
         // the sum's chains: of every fourth pair, or of the 16 keys that share an offset
-        auto chain = [](int c) { return OFFSETS ? c / 16 : (c >> 1) & 3; };
-        auto opens = [](int c) { return OFFSETS ? c % 16 == 0 : c < 8; };
+        auto chain = [](int c) { return KV8 ? c / 16 : (c >> 1) & 3; };
+        auto opens = [](int c) { return KV8 ? c % 16 == 0 : c < 8; };
         uint64_t acc[4];
         // P over the first 32 of this group's S columns, in PH parts of 64 / PH keys: each part
         // is stored and handed to its PV issuer while the next part's exponentials run.  The S
@@ -874,7 +873,7 @@ __global__ void __launch_bounds__(512, 1)
           ok = false;
           break;
         }
-        if constexpr (OFFSETS) {  // without the offsets
+        if constexpr (KV8) {  // without the offsets
           float sum = 0.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {

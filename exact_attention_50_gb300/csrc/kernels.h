@@ -33,7 +33,7 @@ struct FwdParams {
   float* o_part;           // [n_splits, B*Hkv*R, d]
   float* lse_part;         // [n_splits, B*Hkv*R] (natural log)
   // KV cache in 8 bits (kModeKv8): the key codes' scales [B*Hkv, n_blocks], 2^block_shift keys each, the
-  // unit of each head's values [B*Hkv], and (fp16) log2 of what their scales are of it [B*Hkv, n_blocks]
+  // unit of each head's values [B*Hkv], and log2 of what their scales are of it [B*Hkv, n_blocks]
   const float* k_scale;
   const float* v_unit;
   const float* v_log;
@@ -196,9 +196,9 @@ constexpr int cache8_keys(long long pairs, int R, int Nk, int d) {
 }
 cudaError_t launch_cache8_fwd(const CUtensorMap& k, const CUtensorMap& v, const Cache8Params& p, attn_dtype_t dtype,
                               attn_cache_dtype_t cache, cudaStream_t stream);
-// Many rows: K's codes in dtype and V in fp16, [B*Hkv, Nk, d] each, the largest V scale of a head (v_unit
-// [B*Hkv]) and, for fp16, where V is bare codes, log2 of each one's part of it, at least -24 (v_log
-// [B*Hkv, n_blocks]); for bf16 V is in units of v_unit; for the tokens that the caches hold and zeros behind them up to a
+// Many rows: K's codes in dtype and V's in fp16, [B*Hkv, Nk, d] each, the largest V scale of a head (v_unit
+// [B*Hkv]) and log2 of each one's part of it, at least -60 (v_log [B*Hkv, n_blocks]; codes whose scale is below
+// that are expanded to zeros); for the tokens that the caches hold, and zeros behind them up to a
 // tile's end; and, when the forward writes final rows (one key range), those of which it computes nothing.
 // Then the tcgen05 forward in kModeKv8 on that.
 cudaError_t launch_cache8_expand(const Cache8Params& p, void* k16, void* v16, float* v_unit, float* v_log, bool final_rows, attn_dtype_t dtype,

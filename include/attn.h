@@ -275,9 +275,9 @@ attn_status_t attn_kvcache8_append(void* k8, void* v8, float* k_scale, float* v_
  *   workspace  DEVICE, at least attn_fwd_kvcache8_workspace_bytes(...) bytes, 256-byte aligned
  *              (0 bytes for small problems: it may then be NULL); contents on entry are ignored,
  *              on exit undefined.  Calls that may run at the same time need one each.
- * Rounding: with at most 64 query rows per kv head (Hq / Hkv * Nq) the weights times the value scales are
- * rounded to 16 bits (half a step 2^-11), relative to the largest among the keys that the row sees.  A block whose
- * value scale is below 2^-126, or below 2^-60 of the largest of its kv head, may count as values of zero.
+ * Rounding: codes are exact, scores and sums fp32; the weights times the value scales are rounded to fp16 (half a
+ * step 2^-11) in units near the largest among the keys that the row sees.  A block whose value scale is below
+ * 2^-126, or below 2^-60 of the largest of its kv head, may count as values of zero.
  * Tokens, codes and scales past a cache's length may hold anything; an infinity or NaN among the
  * values within it can reach rows whose causal mask hides that token (0 * NaN).
  */

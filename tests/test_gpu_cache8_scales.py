@@ -9,7 +9,7 @@ from tests import cache_plain as P
 
 pytestmark = pytest.mark.gpu
 DT = {"bf16": torch.bfloat16, "f16": torch.float16}
-ROWS = [(4, 30)]  # query heads over two kv heads, queries: 60 rows
+ROWS = [(4, 30), (4, 90)]  # query heads over two kv heads, queries: 60 and 180 rows
 
 
 @pytest.fixture(scope="module")
@@ -131,7 +131,7 @@ def test_scales_beyond_the_range_count_as_zero(dev, Hq, Nq, order):
 
 
 @pytest.mark.parametrize("scale", [1e-38, 1e-30, 50.0])
-@pytest.mark.parametrize("Nq", [1])
+@pytest.mark.parametrize("Nq", [1, 100])
 def test_scales_of_the_scores_at_the_ends_of_their_range(dev, scale, Nq):
     """Products of the scale and a key's that leave float's normal range: even weights, nothing masked that is seen."""
     for block in (16, 128):
