@@ -325,8 +325,9 @@ def fwd_kvcache8(q, k8, v8, k_scale, v_scale, cache_seqlens=None, causal: bool =
                  out_f32: bool = False, with_lse: bool = True, workspace=None):
     """fwd_kvcache over an 8-bit cache.  q [B,Hq,Nq,d] float16 or bfloat16; k8, v8, k_scale,
     v_scale and block as kvcache8_append writes them; cache_seqlens int32 [B] on the device (None:
-    Nk tokens each).  Calls that may run at the same time need a workspace each.  Returns
-    (o [B,Hq,Nq,d], lse [B,Hq,Nq] or None)."""
+    Nk tokens each).  Calls that may run at the same time need a workspace each; with more than 64
+    rows per kv head (Hq / Hkv * Nq) it takes up to 1 GB, or 4 * Nk * d bytes where a single kv head has
+    more.  Returns (o [B,Hq,Nq,d], lse [B,Hq,Nq] or None)."""
     f32, i32 = torch.float32, torch.int32
     try:
         dev = q.get_device()

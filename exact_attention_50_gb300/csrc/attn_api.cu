@@ -681,9 +681,9 @@ Cache8Plan cache8_plan(int B, int Hkv, int R, int Nk, int d) {
 struct Kv8Plan {
   KvSplit split;
   size_t cache_bytes, unit_bytes, log_bytes, o_bytes, lse_bytes;  // cache_bytes: K or V; log_bytes: for the smallest block
+  size_t bytes() const { return 2 * cache_bytes + unit_bytes + log_bytes + o_bytes + lse_bytes; }
 };
-Kv8Plan kv8_plan(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
-  const long long R = static_cast<long long>(Hq / Hkv) * Nq, bh = static_cast<long long>(B) * Hkv;
+Kv8Plan kv8_plan(long long bh, long long R, int Nk, int d) {
   Kv8Plan plan{};
   const long long tiles = (static_cast<long long>(Nk) + attn::kBN - 1) / attn::kBN, blocks = bh * ((R + attn::kBM - 1) / attn::kBM);
   double least = 0.;
@@ -708,14 +708,48 @@ Kv8Plan kv8_plan(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
   return plan;
 }
 
-// The forward over many rows and an 8-bit cache; p describes the call.
-attn_status_t fwd_kv8(const attn::Cache8Params& c, void* workspace, int Hq, attn_dtype_t dtype, attn_cache_dtype_t cache_dtype,
-                      cudaStream_t s) {
-  const Kv8Plan plan = kv8_plan(c.B, Hq, c.Hkv, c.Nq, c.Nk, c.d);
+// A call expands and attends to as many (batch, kv head) pairs at a time as kKv8Bytes hold in 16 bits, whole batches
+// where one fits, else kv heads of one batch; one pair at least.  The pairs that follow reuse the workspace,
+// ordered by the stream, so it does not grow with the batch.  Fewer pairs fill the GPU worse when each has few
+// rows (8 x 8 heads of 32k keys, d = 128, 1 GB: at once 128 rows 373 us, 2048 rows 1675 us; by 512 MB 396 and 1824, by 256 MB
+// 445 and 1757, by 64 MB 769 and 2449; 16 x 8 heads, 4096 rows, 2 GB: 6.66 ms, by 1 GB 6.12, by 512 MB 5.79).
+constexpr size_t kKv8Bytes = size_t{1} << 30;
+struct Kv8Work {
+  int batches, heads;  // at a time; the last time may have fewer of the one that is cut
+  Kv8Plan full, last;
+  size_t bytes;
+  bool fits;           // item numbers stay within 32 bits
+};
+Kv8Work kv8_work(int B, int G, int Hkv, int Nq, int Nk, int d) {
+  const long long R = static_cast<long long>(G) * Nq;
+  const size_t pair = std::max<size_t>(1, static_cast<size_t>(Nk) * d * 4);
+  const long long fit = std::max<long long>(1, static_cast<long long>(kKv8Bytes / pair));
+  const auto even = [](long long n, long long most) {  // n in equal parts of at most that
+    const long long parts = (n + most - 1) / most;
+    return static_cast<int>((n + parts - 1) / parts);
+  };
+  Kv8Work w{};
+  w.batches = fit >= Hkv ? even(B, fit / Hkv) : 1;
+  w.heads = fit >= Hkv ? Hkv : even(Hkv, fit);
+  const int rest = fit >= Hkv ? B % w.batches * Hkv : Hkv % w.heads;
+  const long long n_rb = (R + attn::kBM - 1) / attn::kBM;
+  const auto plan = [&](long long bh) {
+    const Kv8Plan p = kv8_plan(bh, R, Nk, d);
+    w.bytes = std::max(w.bytes, p.bytes());
+    w.fits &= n_rb * bh * p.split.n_splits <= 0x7fffffffLL && (static_cast<long long>(Nk) + 127) / 128 * bh <= 0x7fffffffLL;
+    return p;
+  };
+  w.fits = true;
+  w.full = plan(static_cast<long long>(w.batches) * w.heads);
+  w.last = rest ? plan(rest) : w.full;
+  return w;
+}
+
+// The forward over many rows and an 8-bit cache, for the pairs of one time; c describes them.
+attn_status_t fwd_kv8_pairs(const attn::Cache8Params& c, const Kv8Plan& plan, void* workspace, int Hq, attn_dtype_t dtype,
+                            attn_cache_dtype_t cache_dtype, cudaStream_t s) {
   const int bh = c.B * c.Hkv;
   const long long n_rb = (static_cast<long long>(c.R) + attn::kBM - 1) / attn::kBM;
-  if (n_rb * bh * plan.split.n_splits > 0x7fffffffLL || (static_cast<long long>(c.Nk) + 127) / 128 * bh > 0x7fffffffLL)
-    return ATTN_ERR_UNSUPPORTED;
   char* const ws = static_cast<char*>(workspace);
   void* const k16 = ws;
   void* const v16 = ws + plan.cache_bytes;
@@ -755,6 +789,29 @@ attn_status_t fwd_kv8(const attn::Cache8Params& c, void* workspace, int Hq, attn
   const cudaError_t e = attn::launch_fwd_kv8(maps, p, dtype, c.causal != 0, s);
   if (e != cudaSuccess || p.n_splits == 1) return from_cuda(e);
   return from_cuda(attn::launch_kv_combine(p, dtype, c.causal != 0, s));
+}
+
+attn_status_t fwd_kv8(const attn::Cache8Params& c, const Kv8Work& w, void* workspace, int G, attn_dtype_t dtype,
+                      attn_cache_dtype_t cache_dtype, cudaStream_t s) {
+  for (int b = 0; b < c.B; b += w.batches)
+    for (int h = 0; h < c.Hkv; h += w.heads) {
+      attn::Cache8Params p = c;
+      p.B = std::min(w.batches, c.B - b);
+      p.Hkv = std::min(w.heads, c.Hkv - h);
+      const size_t pair = static_cast<size_t>(b) * c.Hkv + h, row = pair * c.R;
+      p.q = static_cast<const char*>(c.q) + row * c.d * 2;
+      p.k8 += pair * c.Nk * c.d;
+      p.v8 += pair * c.Nk * c.d;
+      p.k_scale += pair * c.n_blocks;
+      p.v_scale += pair * c.n_blocks;
+      if (p.cache_seqlens) p.cache_seqlens += b;
+      p.o = static_cast<char*>(c.o) + row * c.d * (c.out_f32 ? 4 : 2);
+      if (p.lse) p.lse += row;
+      const bool full = p.B == w.batches && p.Hkv == w.heads;
+      const attn_status_t st = fwd_kv8_pairs(p, full ? w.full : w.last, workspace, G * p.Hkv, dtype, cache_dtype, s);
+      if (st != ATTN_OK) return st;
+    }
+  return ATTN_OK;
 }
 
 bool overlap(const void* a, size_t an, const void* b, size_t bn) {
@@ -797,10 +854,7 @@ attn_status_t attn_kvcache8_append(void* k8, void* v8, float* k_scale, float* v_
 size_t attn_fwd_kvcache8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Nq <= 0 || Nk < 0 || d <= 0) return 0;
   const size_t R = static_cast<size_t>(Hq / Hkv) * Nq;
-  if (R > static_cast<size_t>(attn::kCache8Rows)) {
-    const Kv8Plan plan = kv8_plan(B, Hq, Hkv, Nq, Nk, d);
-    return 2 * plan.cache_bytes + plan.unit_bytes + plan.log_bytes + plan.o_bytes + plan.lse_bytes;
-  }
+  if (R > static_cast<size_t>(attn::kCache8Rows)) return kv8_work(B, Hq / Hkv, Hkv, Nq, Nk, d).bytes;
   const Cache8Plan plan = cache8_plan(B, Hkv, static_cast<int>(R), Nk, d);
   return plan.o_bytes + plan.lse_bytes + plan.parts_bytes;
 }
@@ -824,7 +878,9 @@ attn_status_t attn_fwd_kvcache8(const void* q, const void* k8, const void* v8, c
   const long long R = static_cast<long long>(Hq / Hkv) * Nq, bh = static_cast<long long>(B) * Hkv;
   if (Nk > kMaxTokens || R > kMaxTokens || bh * R > 0x7fffffffLL || static_cast<long long>(B) * Hq > 0x7fffffffLL)
     return ATTN_ERR_UNSUPPORTED;
-  const size_t need = attn_fwd_kvcache8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d);
+  const bool many = R > attn::kCache8Rows;
+  const Kv8Work work = many ? kv8_work(B, Hq / Hkv, Hkv, Nq, Nk, d) : Kv8Work{};
+  const size_t need = many ? work.bytes : attn_fwd_kvcache8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d);
   if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return ATTN_ERR_INVALID_ARG;
   attn::Cache8Params p{};
   p.q = q;
@@ -845,7 +901,7 @@ attn_status_t attn_fwd_kvcache8(const void* q, const void* k8, const void* v8, c
   p.out_f32 = (flags & ATTN_FLAG_OUT_F32) ? 1 : 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (Nk == 0) return from_cuda(attn::launch_cache8_none(p, s));
-  if (R > attn::kCache8Rows) return fwd_kv8(p, workspace, Hq, dtype, cache_dtype, s);
+  if (many) return work.fits ? fwd_kv8(p, work, workspace, Hq / Hkv, dtype, cache_dtype, s) : ATTN_ERR_UNSUPPORTED;
   p.tile_keys = attn::cache8_keys(bh, p.R, Nk, d);
   // tiles are numbered in 32 bits (two terabytes of codes)
   if (bh * ((static_cast<long long>(Nk) + p.tile_keys - 1) / p.tile_keys) > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;

@@ -274,7 +274,9 @@ attn_status_t attn_kvcache8_append(void* k8, void* v8, float* k_scale, float* v_
  * (ATTN_F32: ATTN_ERR_UNSUPPORTED).  The split over key ranges is chosen from the sizes.
  *   workspace  DEVICE, at least attn_fwd_kvcache8_workspace_bytes(...) bytes, 256-byte aligned
  *              (0 bytes for small problems: it may then be NULL); contents on entry are ignored,
- *              on exit undefined.  Calls that may run at the same time need one each.
+ *              on exit undefined.  Calls that may run at the same time need one each.  With more than 64
+ *              query rows per kv head (Hq / Hkv * Nq) it holds keys and values in 16 bits, of as many kv
+ *              heads at a time as fit in 1 GB (4 * Nk * d bytes each; one at least), whatever their lengths.
  * Rounding: codes are exact, scores and sums fp32; the weights times the value scales are rounded to fp16 (half a
  * step 2^-11) in units near the largest among the keys that the row sees.  A block whose value scale is below
  * 2^-126, or below 2^-60 of the largest of its kv head, may count as values of zero.

@@ -1,8 +1,9 @@
 """The bounds that the GPU tests of the 8-bit attention use, tried on the CPU: outputs with the roundings that
-the kernels make pass, outputs of a cache with one tile's values wrong do not."""
+the kernels make pass, outputs of a cache with one tile's values wrong do not.  And the attention's workspace."""
 import pytest
 import torch
 
+from exact_attention_50_gb300 import _lib, build
 from tests import cache_plain as P
 
 DT = {"bf16": torch.bfloat16, "f16": torch.float16}
@@ -87,3 +88,17 @@ def test_scales_over_forty_powers_pass_with_one_rounding():
             rl = P.attend8(q, k8, v8, ks, vs, 16, None, causal)[1]
             good = rounded(q, k8, v8, ks, vs, 16, causal)
             P.check_attend8(good.float(), good.to(q.dtype), rl.float(), q, k8, v8, ks, vs, 16, None, causal)
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,Nq,Nk,d", [(8, 32, 8, 17, 32768, 128), (64, 32, 8, 32, 32768, 128), (500, 8, 8, 100, 9001, 80), (1, 32, 8, 64, 2 ** 20, 128),
+                                              (1, 1, 1, 65, 2 ** 23, 128), (3, 128, 128, 300, 70000, 64)])
+def test_workspace_of_many_rows_does_not_grow_with_the_batch(B, Hq, Hkv, Nq, Nk, d):
+    """The keys and values of one time in 16 bits (1 GB, or one kv head's), a float per 16 keys of those, and the parts
+    of at most 128 ranges of those rows."""
+    build.build()
+    _lib.load()
+    size = _lib.attn_fwd_kvcache8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d)
+    pair, rows = 4 * Nk * d, Hq // Hkv * Nq
+    held = max(2 ** 30, pair)
+    pairs = min(B * Hkv, max(1, 2 ** 30 // pair))
+    assert min(pairs * pair // 2, held) <= size <= held * (1 + 1 / (16 * d)) + pairs * 4 + 128 * pairs * rows * (d + 1) * 4 + 2048

@@ -174,6 +174,20 @@ def test_every_key_of_long_caches_counts_with_many_rows(dev):
     long_case(dev, 2, 71, 1, 1, 9000, 112, 16, "f16", "i8", [9000, 77], False, 3)
 
 
+@pytest.mark.parametrize("B,Hkv,Nk,d,dtype", [(9, 4, 120000, 64, "bf16"), (2, 5, 700001, 112, "f16")])
+def test_many_rows_by_groups_of_batches_and_of_heads(dev, B, Hkv, Nk, d, dtype):
+    """More keys than are held in 16 bits at a time: five batches and then four, three heads and then two; a batch
+    in the last group with a bad length."""
+    lens = [Nk, 1000, 0, Nk - 77, 5, 65536, 70001, 80, Nk - 1][:B]
+    long_case(dev, B, 2 * Hkv, Hkv, 40, Nk, d, 64, dtype, "i8", lens, True, 1)
+    q, k8 = randn(1, (B, 2 * Hkv, 40, d), dev).to(DT[dtype]), torch.ones(B, Hkv, Nk, d, dtype=torch.int8, device=dev)
+    s = torch.ones(B, Hkv, -(-Nk // 64), device=dev)
+    o, lse = A.fwd_kvcache8(q, k8, k8, s, s, torch.tensor([40] * (B - 1) + [Nk + 1], dtype=torch.int32, device=dev))
+    torch.cuda.synchronize()
+    assert A.get_device_status() == _lib.ATTN_ERR_DEVICE_INPUT and A.get_device_status() == _lib.ATTN_OK
+    assert bool((o[:-1] == 1).all()) and bool((o[-1] == 0).all()) and bool(torch.isneginf(lse[-1]).all())
+
+
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("dtype,cache,d,block", [("bf16", "i8", 128, 64), ("f16", "e4m3", 64, 32), ("f16", "i8", 80, 16), ("bf16", "e4m3", 112, 128)])
 @pytest.mark.parametrize("Hq,Hkv,Nq", [(8, 2, 1), (8, 1, 2), (6, 2, 5), (16, 2, 5), (4, 1, 13), (4, 1, 37), (8, 2, 130)])
