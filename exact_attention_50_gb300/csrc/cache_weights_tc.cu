@@ -372,25 +372,25 @@ __global__ void __launch_bounds__(640, 1)
             const bool mask = s_min[st] < it.key0 + h * 128 + 127;  // some row of the tile sees not all these keys
             uint64_t acc0 = 0, acc1 = 0;  // pairs of zeros
             auto add = [&](auto& r, int c0) {
-              constexpr int kN = sizeof(r) / 4;
-              if (mask) {
+              auto sums = [&](auto masked) {
 #pragma unroll
-                for (int c = 0; c < kN; c += 4) {  // a score of -inf adds nothing
-                  const int4 l4 = *reinterpret_cast<const int4*>(lim + c0 + c);
-                  if (key > l4.x) r[c] = 0xff800000u;
-                  if (key > l4.y) r[c + 1] = 0xff800000u;
-                  if (key > l4.z) r[c + 2] = 0xff800000u;
-                  if (key > l4.w) r[c + 3] = 0xff800000u;
+                for (int c = 0; c < static_cast<int>(sizeof(r) / 4); c += 4) {
+                  const float4 t4 = *reinterpret_cast<const float4*>(nl + c0 + c);
+                  float2 x = f2_unpack(f2_fma(f2_pack(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), scl, f2_pack(t4.x, t4.y)));
+                  float2 y = f2_unpack(f2_fma(f2_pack(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])), scl, f2_pack(t4.z, t4.w)));
+                  if constexpr (decltype(masked)::value) {  // whatever its score and LSE, a row that does not see the key adds nothing
+                    const int4 l4 = *reinterpret_cast<const int4*>(lim + c0 + c);
+                    if (key > l4.x) x.x = -INFINITY;
+                    if (key > l4.y) x.y = -INFINITY;
+                    if (key > l4.z) y.x = -INFINITY;
+                    if (key > l4.w) y.y = -INFINITY;
+                  }
+                  acc0 = f2_add(acc0, f2_pack(ex2_approx(x.x), ex2_approx(x.y)));
+                  acc1 = f2_add(acc1, f2_pack(ex2_approx(y.x), ex2_approx(y.y)));
                 }
-              }
-#pragma unroll
-              for (int c = 0; c < kN; c += 4) {
-                const float4 t4 = *reinterpret_cast<const float4*>(nl + c0 + c);
-                const float2 x = f2_unpack(f2_fma(f2_pack(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), scl, f2_pack(t4.x, t4.y)));
-                const float2 y = f2_unpack(f2_fma(f2_pack(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])), scl, f2_pack(t4.z, t4.w)));
-                acc0 = f2_add(acc0, f2_pack(ex2_approx(x.x), ex2_approx(x.y)));
-                acc1 = f2_add(acc1, f2_pack(ex2_approx(y.x), ex2_approx(y.y)));
-              }
+              };
+              if (mask) sums(std::true_type{});
+              else sums(std::false_type{});
             };
             if (FEW && p.R <= 8) {  // a decode's rows: nothing to do for the tile's other columns
               uint32_t r[8];

@@ -44,3 +44,25 @@ def test_evict_hands_weights_on_as_they_are(dev, Nk):
             at = torch.from_numpy(P.evict(None, None, w[0, h].cpu().numpy(), Nk, keep, recent)).to(dev)
             assert torch.equal(index[0, h].long(), at)
             assert torch.equal(wo.view(torch.int32)[0, h], bits[0, h, at])
+
+
+# ------------------------------------------------------------------------------------ weights
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("Nq", [1, 3, 30, 200, 600])
+def test_a_row_whose_lse_is_nan_reaches_the_keys_that_it_sees_alone(dev, dtype, Nq):
+    """As for a query of NaN: the keys behind its causal limit keep the other rows' weights."""
+    q, k = randn(1, (2, 4, Nq, 64), dev, DT[dtype]), randn(2, (2, 2, 700, 64), dev, DT[dtype])
+    cl = torch.tensor([700, 650], dtype=torch.int32, device=dev)
+    lse = torch.full((2, 4, Nq), 12.0, device=dev)
+    i = Nq // 3
+    without = lse.clone()
+    without[0, 1, i] = without[1, 2, i] = float("-inf")
+    want, err = P.weights(q, k, without, cl.tolist(), True, None)
+    lse[0, 1, i] = float("nan")
+    q[1, 2, i] = float("nan")
+    got = A.kvcache_weights(q, k, lse, cl, True)
+    status_ok()
+    seen = torch.zeros(2, 2, 700, dtype=torch.bool, device=dev)
+    seen[0, 0, :700 - Nq + i + 1], seen[1, 1, :650 - Nq + i + 1] = True, True
+    assert torch.equal(got.isnan(), seen)
+    assert bool(((got.double() - want).abs() <= err)[~seen].all())
