@@ -66,9 +66,15 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const FwdParams p) {
     const int nv = min(p.n_splits, (need_tiles + p.tiles_per_split - 1) / p.tiles_per_split);
     // the largest range LSE: lanes over the ranges, then a warp reduction
     float mx = -INFINITY;
-    for (int s = lane; s < nv; s += 32) mx = fmaxf(mx, p.lse_part[s * rows + r]);
+    bool nan = false;  // in a range's LSE: it makes the row's, and with it every weight, NaN
+    for (int s = lane; s < nv; s += 32) {
+      const float x = p.lse_part[s * rows + r];
+      mx = fmaxf(mx, x);
+      nan |= x != x;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (__any_sync(0xffffffffu, nan)) mx = __int_as_float(0x7fffffff);
     // weighted sum of the range outputs, eight ranges' loads in flight at a time
     float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f, wsum = 0.f;
     if (mx != -INFINITY) {
@@ -95,7 +101,7 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const FwdParams p) {
     }
     const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
     if (col_ok) store4<OutT>(static_cast<OutT*>(p.o) + r * p.d + lane * 4, a0 * inv, a1 * inv, a2 * inv, a3 * inv);
-    if (lane == 0 && p.lse) p.lse[r] = wsum > 0.f ? mx + logf(wsum) : -INFINITY;
+    if (lane == 0 && p.lse) p.lse[r] = wsum == 0.f ? -INFINITY : mx + logf(wsum);
   }
 }
 

@@ -338,13 +338,13 @@ __global__ void __launch_bounds__(128) fwd_f32_kv_kernel(const float* __restrict
     const int qrow = row0 + warp * 8 + r;
     if (qrow >= Nq) continue;
     const size_t orow = static_cast<size_t>(split) * rows + (static_cast<size_t>(b) * p.Hq + h) * Nq + qrow;
-    const float inv_l = l[r] > 0.f ? 1.f / l[r] : 0.f;
+    const float inv_l = l[r] == 0.f ? 0.f : 1.f / l[r];  // 0: the row sees no key of the range
 #pragma unroll
     for (int i = 0; i < kColsPerLane; ++i) {
       const int c = lane + 32 * i;
       if (c < d) p.o_part[orow * d + c] = acc[r][i] * inv_l;
     }
-    if (lane == 0) p.lse_part[orow] = l[r] > 0.f ? (m[r] + log2f(l[r])) / kLog2e : -INFINITY;
+    if (lane == 0) p.lse_part[orow] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) / kLog2e;
   }
 }
 

@@ -66,3 +66,42 @@ def test_a_row_whose_lse_is_nan_reaches_the_keys_that_it_sees_alone(dev, dtype, 
     seen[0, 0, :700 - Nq + i + 1], seen[1, 1, :650 - Nq + i + 1] = True, True
     assert torch.equal(got.isnan(), seen)
     assert bool(((got.double() - want).abs() <= err)[~seen].all())
+
+
+# --------------------------------------------------------------------------------- key ranges
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("splits", [1, 2, 5])
+def test_nan_in_some_or_all_ranges_of_a_cache(dev, dtype, splits):
+    """A query of NaN, and a key that some rows see: NaN in O and LSE of those rows, not an empty row's 0 and -inf."""
+    q = randn(1, (2, 4, 6, 64), dev, DT[dtype])
+    k, v = (randn(i, (2, 2, 900, 64), dev, DT[dtype]) for i in (2, 3))
+    cl = torch.tensor([900, 3], dtype=torch.int32, device=dev)
+    want, wl = A.fwd_kvcache(q, k, v, cl, True, num_splits=splits)
+    q[0, 1, 2] = float("nan")
+    k[0, 1, 897] = float("nan")  # seen by the queries from 3 on, of heads 2 and 3
+    o, lse = A.fwd_kvcache(q, k, v, cl, True, num_splits=splits)
+    status_ok()
+    bad = torch.zeros(2, 4, 6, dtype=torch.bool, device=dev)
+    bad[0, 1, 2] = bad[0, 2:, 3:] = True
+    assert torch.equal(lse.isnan(), bad) and torch.equal(o.isnan().all(-1), bad) and torch.equal(o.isnan().any(-1), bad)
+    assert torch.equal(lse[~bad], wl[~bad]) and torch.equal(o[~bad], want[~bad])
+    assert bool(torch.isneginf(lse[1, :, :3]).all()) and bool((o[1, :, :3] == 0).all())
+
+
+@pytest.mark.parametrize("Nq", [1, 12, 100])
+@pytest.mark.parametrize("Nk", [200, 30000])
+def test_nan_scores_over_an_8_bit_cache(dev, Nq, Nk):
+    """A query of NaN (every row of its tile keeps its own scores) and a key scale of NaN: O and LSE of the rows
+    that see it are NaN, with one key range and with several."""
+    q = randn(1, (2, 4, Nq, 64), dev, torch.bfloat16)
+    k8, ks = P.quantise(randn(2, (2, 2, Nk, 64), dev), 16, "i8")
+    v8, vs = P.quantise(randn(3, (2, 2, Nk, 64), dev), 16, "i8")
+    want, wl = A.fwd_kvcache8(q, k8, v8, ks, vs, None, True, block=16)
+    q[0, 1, Nq // 2] = float("nan")
+    ks[1, 0, 0] = float("nan")
+    o, lse = A.fwd_kvcache8(q, k8, v8, ks, vs, None, True, block=16)
+    status_ok()
+    bad = torch.zeros(2, 4, Nq, dtype=torch.bool, device=dev)
+    bad[0, 1, Nq // 2] = bad[1, :2] = True
+    assert torch.equal(lse.isnan(), bad) and torch.equal(o.isnan().all(-1), bad) and torch.equal(o.isnan().any(-1), bad)
+    assert torch.equal(lse[~bad], wl[~bad]) and torch.equal(o[~bad], want[~bad])
