@@ -424,6 +424,7 @@ __global__ void __launch_bounds__(kThreads, (Layout<DP, NB, KEYS>::kCtas))
     // c, of the first tile's largest scale, only keeps l's terms within float's range.
     int vexp = 0;
     float vhigh = 0.f;  // 2^(c + kSpread); 0 before the first scale
+    bool finite = true; // the value scales; one that is not leaves the LSE alone
     {
       for (int x = 0; x < part; ++x, ++n) {
         const uint32_t st = n % stages;
@@ -478,7 +479,13 @@ __global__ void __launch_bounds__(kThreads, (Layout<DP, NB, KEYS>::kCtas))
         const int key0 = (w.j + x * stride) * kKeys;
         float largest = 0.f;
 #pragma unroll
-        for (int i = 0; i < kGroups; ++i) largest = fmaxf(largest, vg[i]);
+        for (int i = 0; i < kGroups; ++i) {
+          if (!(vg[i] < INFINITY)) {
+            finite = false;
+            vg[i] = 0.f;
+          }
+          largest = fmaxf(largest, vg[i]);
+        }
         if (largest > vhigh) {  // the first scale, or one that leaves c far behind
           const int e = min(max(static_cast<int>(__float_as_uint(largest) >> 23), 1), 254);
           const float up = static_cast<float>(e - 127 - vexp), down = ex2_approx(-up);
@@ -614,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, (Layout<DP, NB, KEYS>::kCtas))
     if (!SPREAD && !ok) break;
     // ---- this warp's part: sums over the eight lanes that share a row; the output, normalised before it is
     // multiplied by 2^c, so that it overflows only where the values do; m and l in units of one
-    const float unit = __uint_as_float(static_cast<uint32_t>(vexp + 127) << 23);
+    const float unit = finite ? __uint_as_float(static_cast<uint32_t>(vexp + 127) << 23) : __int_as_float(0x7fffffff);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       float il[2];

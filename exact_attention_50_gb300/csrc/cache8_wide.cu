@@ -84,10 +84,11 @@ __global__ void __launch_bounds__(256) expand_kernel(const Cache8Params p, T* k1
     }
   };
   load(first);
-  // the unit: the largest scale of the blocks that hold tokens (a NaN shows in its own block's values)
+  // the unit: the largest scale of the blocks that hold tokens; one that is infinite or NaN shows in its block's values
   const float* vs = p.v_scale + static_cast<size_t>(bh) * p.n_blocks;
   float unit = 0.f;
-  for (int i = threadIdx.x; i <= (L - 1) >> p.block_shift; i += 256) unit = fmaxf(unit, vs[i]);
+  for (int i = threadIdx.x; i <= (L - 1) >> p.block_shift; i += 256)
+    if (vs[i] < INFINITY) unit = fmaxf(unit, vs[i]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) unit = fmaxf(unit, __shfl_xor_sync(0xffffffffu, unit, o));
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = unit;
@@ -103,7 +104,8 @@ __global__ void __launch_bounds__(256) expand_kernel(const Cache8Params p, T* k1
     uint4* vo = reinterpret_cast<uint4*>(v16 + base);
     const int block = (j0 >> p.block_shift) + threadIdx.x;  // of the blocks that hold tokens
     if (block <= (min(j0 + 128, L) - 1) >> p.block_shift)
-      v_log[static_cast<size_t>(bh) * p.n_blocks + block] = vs[block] < least ? -kSpread : log2f(vs[block] / unit);  // NaN stays
+      v_log[static_cast<size_t>(bh) * p.n_blocks + block] =
+          vs[block] < least ? -kSpread : vs[block] < INFINITY ? log2f(vs[block] / unit) : 0.f;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int i = u * 256 + threadIdx.x;
@@ -111,7 +113,9 @@ __global__ void __launch_bounds__(256) expand_kernel(const Cache8Params p, T* k1
       const int j = j0 + i / chunks;
       if (j < L) {
         expand16<T, Code>(kw[u], ko + 2 * i);
-        expand16<__half, Code>(vs[j >> p.block_shift] < least ? make_uint4(0, 0, 0, 0) : vw[u], vo + 2 * i);
+        const float s = vs[j >> p.block_shift];
+        expand16<__half, Code>(s < least ? make_uint4(0, 0, 0, 0) : vw[u], vo + 2 * i);
+        if (!(s < INFINITY)) vo[2 * i] = vo[2 * i + 1] = make_uint4(0x7e007e00u, 0x7e007e00u, 0x7e007e00u, 0x7e007e00u);  // NaN
       } else {  // the tile's rest: a weight of zero times what lies there has to be zero
         const uint4 z = make_uint4(0, 0, 0, 0);
         ko[2 * i] = ko[2 * i + 1] = vo[2 * i] = vo[2 * i + 1] = z;

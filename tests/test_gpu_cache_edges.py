@@ -105,3 +105,23 @@ def test_nan_scores_over_an_8_bit_cache(dev, Nq, Nk):
     bad[0, 1, Nq // 2] = bad[1, :2] = True
     assert torch.equal(lse.isnan(), bad) and torch.equal(o.isnan().all(-1), bad) and torch.equal(o.isnan().any(-1), bad)
     assert torch.equal(lse[~bad], wl[~bad]) and torch.equal(o[~bad], want[~bad])
+
+
+@pytest.mark.parametrize("Nq", [1, 12, 100])
+@pytest.mark.parametrize("Nk", [200, 30000])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("what", ["nan", "inf"])
+def test_value_scales_that_are_not_finite_leave_the_lse(dev, Nq, Nk, dtype, what):
+    """O of the rows that see such a block is not finite; the LSE is that of the keys, and other heads are as they were."""
+    q = randn(1, (2, 4, Nq, 64), dev, DT[dtype])
+    k8, ks = P.quantise(randn(2, (2, 2, Nk, 64), dev), 16, "i8")
+    v8, vs = P.quantise(randn(3, (2, 2, Nk, 64), dev), 16, "i8")
+    want, wl = A.fwd_kvcache8(q, k8, v8, ks, vs, None, False, block=16)
+    for block in (0, 5, -1):
+        bad = vs.clone()
+        bad[1, 0, block] = float(what)
+        o, lse = A.fwd_kvcache8(q, k8, v8, ks, bad, None, False, block=16)
+        status_ok()
+        assert bool((lse - wl).abs().max() <= 2.0 ** -18 * wl.abs().max())
+        assert not bool(o[1, :2].isfinite().all(-1).any())
+        assert torch.equal(o[0], want[0]) and torch.equal(o[1, 2:], want[1, 2:])
