@@ -814,9 +814,24 @@ attn_status_t fwd_kv8(const attn::Cache8Params& c, const Kv8Work& w, void* works
   return ATTN_OK;
 }
 
-bool overlap(const void* a, size_t an, const void* b, size_t bn) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + bn && y < x + an;
+struct Span {
+  const void* p;  // null: not given
+  size_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && a.bytes > 0 && b.bytes > 0 && x < y + b.bytes && y < x + a.bytes;
+}
+// Does an output overlap an input or another output?  Other CTAs may still read the one or write the other; positions
+// read back from an overwritten index would be addresses out of range.
+bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span* a = outs.begin(); a != outs.end(); ++a) {
+    for (const Span* b = a + 1; b != outs.end(); ++b)
+      if (overlap(*a, *b)) return true;
+    for (const Span& b : ins)
+      if (overlap(*a, b)) return true;
+  }
+  return false;
 }
 
 }  // namespace
@@ -844,9 +859,12 @@ attn_status_t attn_kvcache8_append(void* k8, void* v8, float* k_scale, float* v_
   // tokens L .. L + Nn - 1 touch the most blocks when L is the last token of one
   p.blocks_per_head = static_cast<int>(std::min<long long>((static_cast<long long>(Nn) + block - 2) / block + 1, p.n_blocks));
   if (static_cast<long long>(B) * Hkv * 2 * p.blocks_per_head > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
-  // one cache for both sides would be recoded by two CTAs
+  // (one cache for both sides would be recoded by two CTAs)
   const size_t codes = static_cast<size_t>(B) * Hkv * Nk * d, scales = static_cast<size_t>(B) * Hkv * p.n_blocks * 4;
-  if (overlap(k8, codes, v8, codes) || overlap(k_scale, scales, v_scale, scales)) return ATTN_ERR_INVALID_ARG;
+  const size_t fresh = static_cast<size_t>(B) * Hkv * Nn * d * (dtype == ATTN_F32 ? 4 : 2), len_bytes = static_cast<size_t>(B) * 4;
+  if (clash({{k8, codes}, {v8, codes}, {k_scale, scales}, {v_scale, scales}},
+            {{k_new, fresh}, {v_new, fresh}, {cache_seqlens, len_bytes}, {new_seqlens, len_bytes}}))
+    return ATTN_ERR_INVALID_ARG;
   if (!(p.status = status_word())) return ATTN_ERR_CUDA;
   return from_cuda(attn::launch_cache8_append(p, dtype, cache_dtype, static_cast<cudaStream_t>(stream)));
 }
@@ -931,8 +949,9 @@ attn_status_t attn_kvcache_weights(const void* q, const void* k_cache, const flo
   if (Nk > kMaxTokens || R > kMaxTokens || bh * R > 0x7fffffffLL || static_cast<long long>(B) * Hq > 0x7fffffffLL)
     return ATTN_ERR_UNSUPPORTED;
   const size_t bytes = static_cast<size_t>(bh) * Nk * sizeof(float);
-  if ((weights_in && weights_in != weights_out && overlap(weights_out, bytes, weights_in, bytes)) ||
-      (lse && overlap(weights_out, bytes, lse, static_cast<size_t>(bh) * R * sizeof(float))))
+  const size_t es = dtype == ATTN_F32 ? 4 : 2, rows = static_cast<size_t>(bh) * R;
+  if (clash({{weights_out, bytes}}, {{weights_in == weights_out ? nullptr : weights_in, bytes}, {lse, rows * sizeof(float)}, {q, rows * d * es},
+                                     {k_cache, static_cast<size_t>(bh) * Nk * d * es}, {cache_seqlens, static_cast<size_t>(B) * 4}}))
     return ATTN_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (Nq == 0) {  // no query adds anything
@@ -987,11 +1006,10 @@ attn_status_t attn_kvcache_evict(const void* k_cache, const void* v_cache, const
   if (bh * ((M * static_cast<long long>(row / 16) + 1023) / 1024) > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;  // the copy's grid
   const size_t in_bytes = static_cast<size_t>(bh) * Nk * row, out_bytes = static_cast<size_t>(bh) * capacity * row;
   const size_t w_bytes = static_cast<size_t>(bh) * Nk * 4, wo_bytes = static_cast<size_t>(bh) * capacity * 4;
-  for (const void* out : {static_cast<const void*>(k_out), static_cast<const void*>(v_out)})
-    if (overlap(out, out_bytes, k_cache, in_bytes) || overlap(out, out_bytes, v_cache, in_bytes)) return ATTN_ERR_INVALID_ARG;
-  if (overlap(k_out, out_bytes, v_out, out_bytes) || overlap(weights_out, wo_bytes, weights, w_bytes)) return ATTN_ERR_INVALID_ARG;
-  const size_t len_bytes = static_cast<size_t>(B) * 4;  // the other heads still read the lengths when the first writes its own
-  if (cache_seqlens && overlap(out_seqlens, len_bytes, cache_seqlens, len_bytes)) return ATTN_ERR_INVALID_ARG;
+  const size_t len_bytes = static_cast<size_t>(B) * 4;  // (the other heads still read the lengths when the first writes its own)
+  if (clash({{k_out, out_bytes}, {v_out, out_bytes}, {weights_out, wo_bytes}, {index, static_cast<size_t>(bh) * M * 4}, {out_seqlens, len_bytes}},
+            {{k_cache, in_bytes}, {v_cache, in_bytes}, {weights, w_bytes}, {cache_seqlens, len_bytes}}))
+    return ATTN_ERR_INVALID_ARG;
   attn::EvictParams p{};
   p.k = k_cache; p.v = v_cache; p.w = weights;
   p.cache_seqlens = cache_seqlens;

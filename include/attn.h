@@ -255,7 +255,7 @@ typedef enum { ATTN_CACHE_I8 = 0, ATTN_CACHE_E4M3 = 1 } attn_cache_dtype_t;
  * nothing.  An infinity or NaN among a block's tokens makes its scale that and the block reads back
  * as infinities and NaN.  Blocks and tokens outside L .. L + n - 1 are left as they are, but for
  * that recoding; the scale of a block without tokens is never read.
- * k8 and v8, and k_scale and v_scale, must not overlap.
+ * k8, v8, k_scale and v_scale must not overlap one another or the other arguments.
  *   k_new, v_new   [B, Hkv, Nn, d] (dtype: float32, float16 or bfloat16), Nn <= Nk
  *   cache_seqlens  DEVICE int32 [B], or NULL: empty caches (L = 0)
  *   new_seqlens    DEVICE int32 [B], 0 <= new_seqlens[b] <= Nn, or NULL: Nn each
@@ -315,12 +315,12 @@ attn_status_t attn_kvcache_weights(const void* q, const void* k_cache, const flo
  * copied, in the order of their positions, to the front of another cache.
  *   k_cache, v_cache, weights   [B, Hkv, Nk, d] (dtype), [B, Hkv, Nk] float32
  *   cache_seqlens  DEVICE int32 [B], or NULL: Nk keys for every batch
- *   k_out, v_out   [B, Hkv, capacity, d], capacity >= keep + recent; they must not overlap the
- *                  inputs.  Rows past the kept ones are left as they are
+ *   k_out, v_out   [B, Hkv, capacity, d], capacity >= keep + recent.  Rows past the kept ones are
+ *                  left as they are
  *   weights_out    [B, Hkv, capacity] float32: the kept keys' weights, then zeros
- *                  (weights_out and out_seqlens not over weights and cache_seqlens either)
  *   index          int32 [B, Hkv, keep + recent]: the kept keys' positions, then -1
  *   out_seqlens    int32 [B]: min(L, keep + recent)
+ * No output overlaps an input or another output.
  * keep, recent >= 0 and keep + recent >= 1.  A cache_seqlens entry outside [0, Nk] counts as 0
  * and attn_get_device_status() returns ATTN_ERR_DEVICE_INPUT.
  */
