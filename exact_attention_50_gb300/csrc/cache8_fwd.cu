@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, (Layout<DP, NB, KEYS>::kCtas))
           const T* tag = nullptr;
           *reinterpret_cast<uint32_t*>(static_cast<T*>(p.o) + row * p.d + c) = pack2(tag, x * il, y * il);
         }
-        if (c == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
+        if (c == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : add_log2(top, sum) * 0.69314718055994531f;
       }
       cluster.sync();  // the others may still read this CTA's parts
       return;
@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, (Layout<DP, NB, KEYS>::kCtas))
         for (int e = 0; e < 2; ++e) {
           const int r = row0 + 8 * b + 2 * t + e;
           if (r >= p.R) continue;
-          const float lse2 = l[b][e] == 0.f ? -INFINITY : m[b][e] + __log2f(l[b][e]);
+          const float lse2 = l[b][e] == 0.f ? -INFINITY : add_log2(m[b][e], l[b][e]);
           const size_t row = whole ? bh * p.R + r : slot * p.R + r;
           if (g == 0) {
             if (!whole) p.lse_part[row] = lse2;

@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(512, 1)
         if (warp == 12) ok = __all_sync(0xffffffffu, ok);  // the warp leaves the loop together
       }
       if (valid && ((KV && !kv_final) || p.lse)) {
-        const float lse = (mr + __log2f(l_all)) * 0.69314718055994531f;
+        const float lse = (KV8 && l_all > 0.f ? add_log2(mr, l_all) : mr + __log2f(l_all)) * 0.69314718055994531f;
         if constexpr (KV)
           (kv_final ? p.lse : p.lse_part)[kv_row] = lse;
         else if constexpr (VARLEN)

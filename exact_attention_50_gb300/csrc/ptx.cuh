@@ -24,6 +24,13 @@ __device__ __forceinline__ unsigned long long globaltimer() {
   return t;
 }
 
+// m + log2(l) for an l > 0 far from one (a row sum whose exponents carry offsets): l's exponent is added to m,
+// where the two cancel, so that the approximate logarithm keeps its error of 2^-22 near one.
+__device__ __forceinline__ float add_log2(float m, float l) {
+  const int k = static_cast<int>(__float_as_uint(l) >> 23) - 127;
+  return (m + static_cast<float>(k)) + __log2f(l * __uint_as_float(static_cast<uint32_t>(127 - k) << 23));
+}
+
 // Records the first error raised on the device since the last status read.
 __device__ __forceinline__ void raise_status(unsigned* status, unsigned code) {
   if (status) atomicCAS(status, 0u, code);

@@ -94,6 +94,18 @@ def test_rows_that_see_a_scale_of_zero_only(dev, Hq, Nq, dtype, block):
 
 
 @pytest.mark.parametrize("Hq,Nq", [(4, 1), (4, 30), (4, 90)])
+@pytest.mark.parametrize("Nk", [90, 700, 9000])
+def test_the_lse_does_not_depend_on_the_values(dev, Hq, Nq, Nk):
+    """Scales of zero, and one large scale at the front of small ones: a row sum 2^60 or 2^50 times its usual
+    size, and an LSE as exact as ever: small queries, so E is next to nothing."""
+    for seed in range(5):
+        k8, ks, v8, vs = cache_of(dev, (3, 2, Nk, 64), 16, "i8", seed)
+        vs[0], vs[1, :, 1:] = 0, vs[1, :, 1:] * 2.0 ** -50
+        q = (1e-3 * randn(seed + 9, (3, Hq, Nq, 64), dev)).half()
+        check(q, k8, v8, ks, vs, 16, [Nk, Nk, Nk - 13], True)
+
+
+@pytest.mark.parametrize("Hq,Nq", [(4, 1), (4, 30), (4, 90)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("power", [-100, 100])
 def test_heads_of_very_small_and_very_large_values(dev, Hq, Nq, dtype, power):
