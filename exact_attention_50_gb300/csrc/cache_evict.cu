@@ -35,8 +35,8 @@ __device__ __forceinline__ float weight_of(uint32_t u, const float* w) {
   return __uint_as_float((u & 0x80000000u) ? u ^ 0x80000000u : ~u);
 }
 
-// Exclusive prefix sum over the CTA of two counts packed in 16-bit halves (each at most 1024).
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* s_warp, uint32_t& total) {
+// Exclusive prefix sum over the CTA; total: the whole sum.  (Also of two counts in 16-bit halves, at most 1024 each.)
+__device__ __forceinline__ uint32_t scan_all(uint32_t v, uint32_t* s_warp, uint32_t& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t x = v;
 #pragma unroll
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
       }
     }
     uint32_t total;
-    const uint32_t r = block_scan((take ? 1u : 0u) | (eq ? 0x10000u : 0u), s_warp, total);
+    const uint32_t r = scan_all((take ? 1u : 0u) | (eq ? 0x10000u : 0u), s_warp, total);
     // equals before this key in the whole sequence; of them, the first `want` are kept
     const uint32_t eq_before = equal + (r >> 16);
     if (eq && eq_before < want) take = true;
@@ -151,35 +151,6 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
   }
   for (int i = left + tid; i < p.M; i += kThreads) index[i] = -1;
   for (int i = left + tid; i < p.cap; i += kThreads) w_out[i] = 0.f;
-}
-
-// Exclusive prefix sum over the CTA; total: the whole sum.
-__device__ __forceinline__ uint32_t scan_all(uint32_t v, uint32_t* s_warp, uint32_t& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) s_warp[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    const uint32_t w = s_warp[lane];
-    uint32_t y = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t z = __shfl_up_sync(0xffffffffu, y, o);
-      if (lane >= o) y += z;
-    }
-    s_warp[lane] = y - w;
-    if (lane == 31) s_warp[32] = y;
-  }
-  __syncthreads();
-  const uint32_t r = s_warp[warp] + x - v;
-  total = s_warp[32];
-  __syncthreads();
-  return r;
 }
 
 // A cluster of C CTAs per (batch, kv head), up to C * E * 1024 keys: CTA r has keys [r E 1024, (r + 1) E
