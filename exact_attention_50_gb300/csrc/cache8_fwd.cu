@@ -29,15 +29,16 @@
 // that of an operand by an 8 x 8 transposition between the lanes (movmatrix).
 //
 // Conversion: K's int8 codes as fp16 subnormals, (code + 128) 2^-24, exact, two instructions a pair;
-// the sum starts at -128 2^-24 sum(q).  V's by placing code + 128 in the mantissa of 1024 + u and
+// the sum starts at -128 2^-24 sum(q), so it rounds at the size of 255 sum|q| instead of sum|q code|: scores
+// are off by about 2e-7 (rms, q.k of size one), 2e-6 with one column of K far above the others.  V's by placing code + 128 in the mantissa of 1024 + u and
 // subtracting 1152: there the offset would be far larger than the sums.  e4m3 by the conversion
 // instruction.
 //
 // What it reaches (8 sequences of 16k to 32k keys, 32 over 8 heads, d = 128, int8): 77 us, 5.5 TB/s, 81% of
 // the copy rate: 71 us in this kernel, the rest the merge (5 us alone, partly hidden) and the launch; 75 us with
-// one query row per kv head.  With 16 rows (NB = 2) 84 us.  With 32 (two warps per tile, the codes converted
-// twice) 143 us: 251 registers leave two warps per scheduler, which issue in 45% of the cycles, waiting
-// mostly for results of fixed latency; ALU 41%, tensor pipe 33%, DRAM 38%, so no unit bounds it.
+// one query row per kv head.  With 16 rows (NB = 2) 85 us.  With 32 (two warps per tile, the codes converted
+// twice) 145 us: 253 registers leave two warps per scheduler, which issue in 45% of the cycles, waiting
+// mostly for results of fixed latency; ALU 45%, tensor pipe 34%, DRAM 38%, so no unit bounds it.  With 64 264 us.
 //
 // Rounding: q in bf16 becomes fp16 after a multiplication by a power of two per row (largest
 // element in [2^14, 2^15)), exact but for elements below 2^-28 of that.  P vs is rounded to fp16 (half a

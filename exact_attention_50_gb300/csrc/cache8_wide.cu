@@ -6,7 +6,7 @@
 // traffic per code.  K and V are expanded to bare codes, exact in either 16-bit type; K's scales multiply
 // the scores in fp32, and log2 of V's, in units of the head's largest, goes into P's exponent.  So the one
 // rounding is that of P (fp16 whatever the type, half a step 2^-11), relative to the largest P vs of the
-// row's own keys: scale / unit in V (a chunk of 2048 queries took 817 to 859 us with that, now 829 to 832) would lose
+// row's own keys: scale / unit in V (a chunk of 2048 queries took 817 to 859 us with that, now 820 to 832) would lose
 // the digits of rows that see small scales only.  A block whose scale is below 2^-60 of the head's largest, or below 2^-126,
 // counts as values of zero.
 #include <algorithm>

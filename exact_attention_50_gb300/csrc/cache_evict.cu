@@ -12,7 +12,8 @@
 // a walk with a scan per 1024 keys.  gather: all SMs copy the rows, 16 bytes per thread and step; it
 // is launched while select runs and waits for it inside.
 // 8 x 8 heads, 16k-32k keys to 4096: select 44 us with the second form, 19 us with the first; gather 39
-// us for 268 MB (6.9 TB/s, what a copy reaches).
+// us for 268 MB (6.9 TB/s, what a copy reaches).  Both kernels, 65536 keys each: 69 us; where the second form
+// begins, with one key more, 135 us, 131072 keys 227, 262144 keys 403; 8 heads of 262144 keys 38 us, of one more 328.
 #include <cooperative_groups.h>
 #include "cache8.cuh"
 

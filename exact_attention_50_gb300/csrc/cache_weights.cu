@@ -6,7 +6,9 @@
 // CUDA-core kernel: a CTA of 256 threads owns 64 keys of one (batch, kv head), staged transposed
 // ([d][64 + 4], fp32) in shared memory, and walks the rows in tiles of 64; a thread forms a 4 x 4
 // block of scores and keeps four keys' sums in registers, reduced over the 16 threads of a row at
-// the end.  No atomics: the order of the sum is fixed.
+// the end.  No atomics: the order of the sum is fixed.  8 x 8 heads of 16k-32k keys, 4 rows: 1160 us for 128 of
+// bytes (60 of the 64 rows of its tile are padding, and the staging's stores meet four to a bank); 4 x 8
+// heads of 4k-8k keys, 192 rows: 391 us, 26 TFLOP/s.
 #include <algorithm>
 #include "cache8.cuh"
 

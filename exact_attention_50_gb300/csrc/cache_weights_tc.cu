@@ -18,8 +18,8 @@
 // for each key tile and each of its two S^T buffers of 128 columns, the buffers taken in turn;
 // then a warp for the TMA loads, one MMA issuer per key tile, on two sub-partitions (one thread
 // issues 16 of them in about 1700 cycles, more than they take), and one that prepares the rows'
-// -LSE log2(e) and last visible keys.  2048-token prompts (B = 4, 32 over 8 heads, d = 128) take 132 us
-// without and 78 us (880 TFLOP/s) with the causal mask, 86 with integer divisions in every role's walk
+// -LSE log2(e) and last visible keys.  2048-token prompts (B = 4, 32 over 8 heads, d = 128) take 130 us
+// without and 77 us (889 TFLOP/s) with the causal mask, 86 with integer divisions in every role's walk
 // over the tiles.  Measured beside 131 and 86, with those: eight summing warps and one issuer 160 and
 // 116; eight warps that take a whole tile into registers first 149 and 92; two groups that halve every
 // tile's columns 135 and 90; loads of 32 columns ahead of the sums 162 and 102; tiles handed over in
