@@ -82,6 +82,31 @@ def load() -> ctypes.CDLL:
         lib.attn_kvcache_weights.restype = i
         lib.attn_kvcache_evict.argtypes = [vp] * 9 + [i] * 8 + [vp]
         lib.attn_kvcache_evict.restype = i
+        ll, sz = ctypes.c_int64, ctypes.c_size_t
+        lib.attn_fwd_varlen_gqa_workspace_bytes.argtypes = [i] * 5
+        lib.attn_fwd_varlen_gqa_workspace_bytes.restype = sz
+        lib.attn_fwd_varlen_gqa.argtypes = [vp] * 4 + [i] * 3 + [vp] * 3 + [sz] + [i] * 3 + [ll] * 3 + [i, f, i, u, vp]
+        lib.attn_fwd_varlen_gqa.restype = i
+        lib.attn_bwd_varlen_gqa_workspace_bytes.argtypes = [i] * 6
+        lib.attn_bwd_varlen_gqa_workspace_bytes.restype = sz
+        lib.attn_bwd_varlen_gqa.argtypes = [vp] * 7 + [i] * 3 + [vp] * 4 + [sz] + [i] * 3 + [ll] * 3 + [i, f, i, u, vp]
+        lib.attn_bwd_varlen_gqa.restype = i
+        lib.attn_fwd_kvpages_workspace_bytes.argtypes = [i] * 9
+        lib.attn_fwd_kvpages_workspace_bytes.restype = sz
+        lib.attn_fwd_kvpages.argtypes = [vp] * 8 + [sz] + [i] * 10 + [f, i, u, vp]
+        lib.attn_fwd_kvpages.restype = i
+        lib.attn_kvpages_append.argtypes = [vp] * 7 + [i] * 7 + [ll, ll, i, vp]
+        lib.attn_kvpages_append.restype = i
+        lib.attn_kvpages_free.argtypes = [vp] * 7 + [i] * 4 + [vp]
+        lib.attn_kvpages_free.restype = i
+        lib.attn_kvpages_fork.argtypes = [vp] * 9 + [i] * 5 + [vp]
+        lib.attn_kvpages_fork.restype = i
+        lib.attn_kvpages_reserve.argtypes = [vp] * 6 + [i] * 4 + [vp]
+        lib.attn_kvpages_reserve.restype = i
+        lib.attn_kvpages_compact.argtypes = [vp] * 6 + [i] * 3 + [vp]
+        lib.attn_kvpages_compact.restype = i
+        lib.attn_kvpages_copy.argtypes = [vp] * 3 + [i] * 6 + [vp]
+        lib.attn_kvpages_copy.restype = i
         lib.attn_get_device_status.argtypes = [vp]
         lib.attn_get_device_status.restype = i
         lib.attn_status_string.argtypes = [i]
@@ -151,6 +176,66 @@ def attn_kvcache_evict(k_cache, v_cache, weights, cache_seqlens, k_out, v_out, w
                        Nk, capacity, d, keep, recent, dtype, stream) -> int:
     return load().attn_kvcache_evict(k_cache, v_cache, weights, cache_seqlens, k_out, v_out, weights_out, index,
                                      out_seqlens, B, Hkv, Nk, capacity, d, keep, recent, dtype, stream)
+
+
+def attn_fwd_varlen_gqa_workspace_bytes(nseq, total_tokens, max_seqlen, Hq, Hkv) -> int:
+    return load().attn_fwd_varlen_gqa_workspace_bytes(nseq, total_tokens, max_seqlen, Hq, Hkv)
+
+
+def attn_fwd_varlen_gqa(q, k, v, cu_seqlens, nseq, total_tokens, max_seqlen, out, lse, workspace, workspace_bytes, Hq, Hkv, d, q_stride,
+                        k_stride, v_stride, causal, scale, dtype, flags, stream) -> int:
+    return load().attn_fwd_varlen_gqa(q, k, v, cu_seqlens, nseq, total_tokens, max_seqlen, out, lse, workspace, workspace_bytes, Hq, Hkv, d,
+                                      q_stride, k_stride, v_stride, int(causal), float(scale), dtype, flags, stream)
+
+
+def attn_bwd_varlen_gqa_workspace_bytes(nseq, total_tokens, max_seqlen, Hq, Hkv, d) -> int:
+    return load().attn_bwd_varlen_gqa_workspace_bytes(nseq, total_tokens, max_seqlen, Hq, Hkv, d)
+
+
+def attn_bwd_varlen_gqa(q, k, v, out, dout, lse, cu_seqlens, nseq, total_tokens, max_seqlen, dq, dk, dv, workspace, workspace_bytes, Hq, Hkv,
+                        d, q_stride, k_stride, v_stride, causal, scale, dtype, flags, stream) -> int:
+    return load().attn_bwd_varlen_gqa(q, k, v, out, dout, lse, cu_seqlens, nseq, total_tokens, max_seqlen, dq, dk, dv, workspace,
+                                      workspace_bytes, Hq, Hkv, d, q_stride, k_stride, v_stride, int(causal), float(scale), dtype, flags,
+                                      stream)
+
+
+def attn_fwd_kvpages_workspace_bytes(B, Hq, Hkv, Nq, max_pages, page, max_seqlen, d, dtype) -> int:
+    return load().attn_fwd_kvpages_workspace_bytes(B, Hq, Hkv, Nq, max_pages, page, max_seqlen, d, dtype)
+
+
+def attn_fwd_kvpages(q, k_pages, v_pages, page_table, cache_seqlens, o, lse, workspace, workspace_bytes, B, Hq, Hkv, Nq, max_pages, pages,
+                     page, max_seqlen, d, causal, scale, dtype, flags, stream) -> int:
+    return load().attn_fwd_kvpages(q, k_pages, v_pages, page_table, cache_seqlens, o, lse, workspace, workspace_bytes, B, Hq, Hkv, Nq,
+                                   max_pages, pages, page, max_seqlen, d, int(causal), float(scale), dtype, flags, stream)
+
+
+def attn_kvpages_append(k_pages, v_pages, page_table, k_new, v_new, cu_seqlens, cache_seqlens, B, total_tokens, Hkv, max_pages, pages, page, d,
+                        k_stride, v_stride, dtype, stream) -> int:
+    return load().attn_kvpages_append(k_pages, v_pages, page_table, k_new, v_new, cu_seqlens, cache_seqlens, B, total_tokens, Hkv, max_pages,
+                                      pages, page, d, k_stride, v_stride, dtype, stream)
+
+
+def attn_kvpages_free(page_table, cache_seqlens, refs, keep_seqlens, table_out, seqlens_out, refs_out, B, max_pages, pages, page, stream) -> int:
+    return load().attn_kvpages_free(page_table, cache_seqlens, refs, keep_seqlens, table_out, seqlens_out, refs_out, B, max_pages, pages, page,
+                                    stream)
+
+
+def attn_kvpages_fork(page_table, cache_seqlens, refs, src, dst, table_out, seqlens_out, refs_out, copies, n, B, max_pages, pages, page,
+                      stream) -> int:
+    return load().attn_kvpages_fork(page_table, cache_seqlens, refs, src, dst, table_out, seqlens_out, refs_out, copies, n, B, max_pages, pages,
+                                    page, stream)
+
+
+def attn_kvpages_reserve(page_table, cache_seqlens, refs, new_seqlens, table_out, refs_out, B, max_pages, pages, page, stream) -> int:
+    return load().attn_kvpages_reserve(page_table, cache_seqlens, refs, new_seqlens, table_out, refs_out, B, max_pages, pages, page, stream)
+
+
+def attn_kvpages_compact(page_table, refs, table_out, refs_out, copies, used, B, max_pages, pages, stream) -> int:
+    return load().attn_kvpages_compact(page_table, refs, table_out, refs_out, copies, used, B, max_pages, pages, stream)
+
+
+def attn_kvpages_copy(k_pages, v_pages, copies, n, Hkv, pages, page, d, dtype, stream) -> int:
+    return load().attn_kvpages_copy(k_pages, v_pages, copies, n, Hkv, pages, page, d, dtype, stream)
 
 
 def attn_bwd_cross_workspace_bytes(B, Hq, Nq, Nk, d, dtype, flags) -> int:

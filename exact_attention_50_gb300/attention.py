@@ -12,6 +12,11 @@ every step of the computation runs in libattn_gb300.so's kernels.
 - ``kvcache8_append``, ``fwd_kvcache8``: a KV cache held in 8 bits with a scale per block of
   tokens and head, and attention over it; ``kvcache_weights``, ``kvcache_evict``: the attention
   weight that each cached key has received, and eviction by it.
+- ``fwd_varlen_gqa``, ``bwd_varlen_gqa``, ``flash_attn_varlen_gqa_func``: packed sequences with fewer kv
+  heads than query heads, from tensors of their own or parts of one projection's output.
+- ``kvpages_append``, ``fwd_kvpages``: a KV cache in pages, and attention over it; ``kvpages_free``,
+  ``kvpages_fork``, ``kvpages_reserve``, ``kvpages_compact``, ``kvpages_copy``: its page tables and reference
+  counts, and the copies of pages that they ask for.
 """
 from __future__ import annotations
 
@@ -446,6 +451,342 @@ def kvcache_evict(k_cache, v_cache, weights, keep: int, recent: int, cache_seqle
     return k_out, v_out, w_out, index, lens
 
 
+# ------------------------------------------------------------- packed sequences with grouped heads
+def _token_strides(dev: int, *tensors):
+    """The distances from token to token of [T,H,d] tensors on GPU `dev` whose rows of one token lie one behind the other,
+    or None."""
+    strides = []
+    for t in tensors:
+        if t.get_device() != dev or dev < 0 or t.dim() != 3:
+            return None
+        T, H, d = t.shape
+        a, b, c = t.stride()
+        if T * H * d == 0 or t.is_contiguous():
+            a = H * d
+        elif (c != 1 and d > 1) or (b != d and H > 1):
+            return None
+        elif T == 1:
+            a = H * d
+        strides.append(a)
+    return strides
+
+
+def _explain_packed(q, k, v, cu_seqlens, *more):
+    """Raises what is wrong with the tensors of a packed call; more: contiguous tensors (tensor, name, dtype, optional)."""
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dim() != 3:
+            raise ValueError(f"{name} must be [total_tokens, heads, head_dim]")
+        if t.dtype != q.dtype:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {q.dtype}")
+        if t.device != q.device:
+            raise ValueError(f"{name} must be on q's device")
+        if _token_strides(t.get_device(), t) is None:
+            raise ValueError(f"{name}'s heads and columns must lie one behind the other (any stride from token to token)")
+    for t, name, dtype, optional in ((cu_seqlens, "cu_seqlens", torch.int32, False),) + more:
+        if t is None and optional:
+            continue
+        _require(t, name, dtype)
+        if t.device != q.device:
+            raise ValueError(f"{name} must be on q's device")
+    raise TypeError("the tensors' types do not fit together")
+
+
+def _packed_sizes(q, k, v, cu_seqlens, max_seqlen):
+    T, Hq, d = q.shape
+    Tk, Hkv, dk = k.shape
+    if v.shape != k.shape or Tk != T or dk != d:
+        raise ValueError("q must be [total_tokens,Hq,d] and k, v [total_tokens,Hkv,d]")
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+        raise ValueError("cu_seqlens must be 1-D with batch_size + 1 entries")
+    if Hq < 1 or Hkv < 1 or Hq % Hkv:
+        raise ValueError("the query heads must be a multiple of the kv heads")
+    max_seqlen = int(max_seqlen)
+    if max_seqlen < 0:
+        raise ValueError("max_seqlen must not be negative")
+    _check_sizes(q.shape, cu_seqlens.shape, (max_seqlen,))
+    return T, Hq, Hkv, d, cu_seqlens.shape[0] - 1, max_seqlen
+
+
+@functools.lru_cache(maxsize=1024)
+def _varlen_gqa_workspace_bytes(nseq, T, max_seqlen, Hq, Hkv):
+    return _lib.attn_fwd_varlen_gqa_workspace_bytes(nseq, T, max_seqlen, Hq, Hkv)
+
+
+def fwd_varlen_gqa(q, k, v, cu_seqlens, max_seqlen: int, causal: bool, scale=None, out_f32: bool = False, with_lse: bool = True,
+                   workspace=None):
+    """Packed forward with grouped heads.  q [T,Hq,d], k and v [T,Hkv,d] with any stride from token to token that is a
+    multiple of 16 bytes (parts of one projection's output, for example); cu_seqlens int32 [nseq+1] on the device.
+    Tokens may lie behind the last sequence: their rows become O = 0, LSE = -inf.  Calls that may run at the same time
+    need a workspace each.  Returns (out [T,Hq,d], lse [Hq,T] or None)."""
+    f32, i32 = torch.float32, torch.int32
+    try:
+        dev = q.get_device()
+        strides = _token_strides(dev, q, k, v)
+        fit = strides is not None and _fit(dev, cu_seqlens, workspace) and k.dtype is q.dtype and v.dtype is q.dtype and cu_seqlens.dtype is i32
+    except AttributeError:  # not a tensor
+        fit = False
+    if not fit:
+        _explain_packed(q, k, v, cu_seqlens, (workspace, "workspace", None, True))
+    T, Hq, Hkv, d, nseq, max_seqlen = _packed_sizes(q, k, v, cu_seqlens, max_seqlen)
+    dtype, device = _dtype_code(q), q.device
+    out = torch.empty((T, Hq, d), dtype=f32 if out_f32 else q.dtype, device=device)
+    lse = torch.empty((Hq, T), dtype=f32, device=device) if with_lse else None
+    if workspace is None:
+        workspace = torch.empty(max(1, _varlen_gqa_workspace_bytes(nseq, T, max_seqlen, Hq, Hkv)), dtype=torch.uint8, device=device)
+    st = _on_device(dev, _lib.attn_fwd_varlen_gqa, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), nseq, T, max_seqlen,
+                    out.data_ptr(), lse.data_ptr() if with_lse else None, workspace.data_ptr(), workspace.nbytes, Hq, Hkv, d, *strides, causal,
+                    _scale_arg(scale), dtype, _lib.ATTN_FLAG_OUT_F32 if out_f32 else 0)
+    _lib._check(st, "attn_fwd_varlen_gqa")
+    return out, lse
+
+
+def bwd_varlen_gqa(q, k, v, out, lse, dout, cu_seqlens, max_seqlen: int, causal: bool, scale=None, out_f32: bool = False, workspace=None,
+                   deterministic: bool = False):
+    """Packed backward with grouped heads: q, k, v, cu_seqlens, max_seqlen, causal and scale as given to fwd_varlen_gqa, out
+    and lse as it returned them, dout [T,Hq,d].  Returns (dq [T,Hq,d], dk, dv [T,Hkv,d]); zeros for tokens behind the
+    last sequence."""
+    f32, i32 = torch.float32, torch.int32
+    try:
+        dev = q.get_device()
+        strides = _token_strides(dev, q, k, v)
+        fit = (strides is not None and _fit(dev, cu_seqlens, out, lse, dout, workspace) and k.dtype is q.dtype and v.dtype is q.dtype
+               and out.dtype is q.dtype and dout.dtype is q.dtype and lse.dtype is f32 and cu_seqlens.dtype is i32)
+    except AttributeError:  # not a tensor
+        fit = False
+    if not fit:
+        dt = getattr(q, "dtype", None)
+        _explain_packed(q, k, v, cu_seqlens, (out, "out", dt, False), (lse, "lse", f32, False), (dout, "dout", dt, False),
+                        (workspace, "workspace", None, True))
+    T, Hq, Hkv, d, nseq, max_seqlen = _packed_sizes(q, k, v, cu_seqlens, max_seqlen)
+    if out.shape != q.shape or dout.shape != q.shape or lse.shape != (Hq, T):
+        raise ValueError("out and dout must be shaped like q, lse [Hq,T]")
+    dtype, device = _dtype_code(q), q.device
+    odt = f32 if out_f32 else q.dtype
+    dq = torch.empty((T, Hq, d), dtype=odt, device=device)
+    dk, dv = (torch.empty((T, Hkv, d), dtype=odt, device=device) for _ in range(2))
+    if workspace is None:
+        need = _lib.attn_bwd_varlen_gqa_workspace_bytes(nseq, T, max_seqlen, Hq, Hkv, d)
+        workspace = torch.empty(max(1, need), dtype=torch.uint8, device=device)
+    st = _on_device(dev, _lib.attn_bwd_varlen_gqa, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(), lse.data_ptr(),
+                    cu_seqlens.data_ptr(), nseq, T, max_seqlen, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
+                    workspace.nbytes, Hq, Hkv, d, *strides, causal, _scale_arg(scale), dtype, _bwd_flags(out_f32, deterministic))
+    _lib._check(st, "attn_bwd_varlen_gqa")
+    return dq, dk, dv
+
+
+# ------------------------------------------------------------------------- KV caches in pages
+def _check_pools(k_pages, v_pages):
+    """Shapes of a pool of pages: (pages, Hkv, page, d)."""
+    shape = k_pages.shape
+    if len(shape) != 4 or shape != v_pages.shape:
+        raise ValueError("k_pages and v_pages must be [pages,Hkv,page,d]")
+    _check_sizes(shape)
+    return shape
+
+
+def _check_table(page_table):
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B,max_pages]")
+    _check_sizes(page_table.shape)
+    return page_table.shape
+
+
+@functools.lru_cache(maxsize=1024)
+def kvpages_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, max_pages: int, page: int, d: int, dtype=torch.bfloat16, max_seqlen=None) -> int:
+    """Bytes of the device workspace fwd_kvpages needs for these sizes."""
+    return _lib.attn_fwd_kvpages_workspace_bytes(B, Hq, Hkv, Nq, max_pages, page, max_seqlen or 0, d, _DT[dtype])
+
+
+def fwd_kvpages(q, k_pages, v_pages, page_table, cache_seqlens, causal: bool = False, scale=None, max_seqlen=None, out_f32: bool = False,
+                with_lse: bool = True, workspace=None):
+    """fwd_kvcache over a cache in pages.  q [B,Hq,Nq,d]; k_pages, v_pages [pages,Hkv,page,d], page 16, 32, 64 or 128;
+    page_table int32 [B,max_pages]: the numbers of each sequence's pages; cache_seqlens int32 [B], both on the device.
+    max_seqlen: an upper bound on the lengths, by which the work is planned (None: max_pages * page).  Calls that may
+    run at the same time need a workspace each.  Returns (o [B,Hq,Nq,d], lse [B,Hq,Nq] or None)."""
+    i32 = torch.int32
+    try:
+        dev = q.get_device()
+        fit = (_fit(dev, q, k_pages, v_pages, page_table, cache_seqlens, workspace) and k_pages.dtype is q.dtype and v_pages.dtype is q.dtype
+               and page_table.dtype is i32 and cache_seqlens is not None and cache_seqlens.dtype is i32)
+    except AttributeError:  # not a tensor
+        fit = False
+    if not fit:
+        dt = getattr(q, "dtype", None)
+        _explain((q, "q", None, False), (k_pages, "k_pages", dt, False), (v_pages, "v_pages", dt, False), (page_table, "page_table", i32, False),
+                 (cache_seqlens, "cache_seqlens", i32, False), (workspace, "workspace", None, True))
+    P, Hkv, page, d = _check_pools(k_pages, v_pages)
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != d:
+        raise ValueError("q must be [B,Hq,Nq,d], with the pages' head_dim")
+    B, Hq, Nq = shape[0], shape[1], shape[2]
+    tb, M = _check_table(page_table)
+    if tb != B:
+        raise ValueError("page_table must be [B,max_pages], with q's batch")
+    _check_sizes(shape)
+    if max_seqlen is None:
+        max_seqlen = 0
+    elif not 1 <= max_seqlen < 2 ** 31:
+        raise ValueError("max_seqlen must be positive (None: max_pages * page)")
+    device = q.device
+    o = torch.empty_like(q, dtype=torch.float32) if out_f32 else torch.empty_like(q)
+    lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=device) if with_lse else None
+    code = _dtype_code(q)
+    if workspace is None:
+        need = kvpages_workspace_bytes(B, Hq, Hkv, Nq, M, page, d, q.dtype, max_seqlen)
+        workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    st = _on_device(dev, _lib.attn_fwd_kvpages, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+                    _lens_ptr(cache_seqlens, "cache_seqlens", B), o.data_ptr(), lse.data_ptr() if with_lse else None,
+                    None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes, B, Hq, Hkv, Nq, M, P,
+                    page, max_seqlen, d, causal, _scale_arg(scale), code, _lib.ATTN_FLAG_OUT_F32 if out_f32 else 0)
+    _lib._check(st, "attn_fwd_kvpages")
+    return o, lse
+
+
+def kvpages_append(k_pages, v_pages, page_table, k_new, v_new, cu_seqlens, cache_seqlens=None):
+    """Writes packed tokens into the pages that the table gives them, in place.  k_new, v_new [T,Hkv,d] with any stride from
+    token to token that is a multiple of 16 bytes; cu_seqlens int32 [B+1]: sequence b's tokens; they go behind its first
+    cache_seqlens[b] (int32 [B]; None: empty sequences).  The caller advances the lengths."""
+    i32 = torch.int32
+    try:
+        dev = k_pages.get_device()
+        strides = _token_strides(dev, k_new, v_new)
+        fit = (strides is not None and _fit(dev, k_pages, v_pages, page_table, cu_seqlens, cache_seqlens) and v_pages.dtype is k_pages.dtype
+               and k_new.dtype is k_pages.dtype and v_new.dtype is k_pages.dtype and page_table.dtype is i32 and cu_seqlens.dtype is i32
+               and (cache_seqlens is None or cache_seqlens.dtype is i32))
+    except AttributeError:  # not a tensor
+        fit = False
+    if not fit:
+        dt = getattr(k_pages, "dtype", None)
+        for t, name in ((k_new, "k_new"), (v_new, "v_new")):
+            if isinstance(t, torch.Tensor) and t.is_cuda and _token_strides(t.get_device(), t) is None:
+                raise ValueError(f"{name} must be [total_tokens,Hkv,d], heads and columns one behind the other")
+        _explain((k_pages, "k_pages", None, False), (v_pages, "v_pages", dt, False), (page_table, "page_table", i32, False),
+                 *((t.contiguous() if isinstance(t, torch.Tensor) else t, name, dt, False) for t, name in ((k_new, "k_new"), (v_new, "v_new"))),
+                 (cu_seqlens, "cu_seqlens", i32, False), (cache_seqlens, "cache_seqlens", i32, True))
+    P, Hkv, page, d = _check_pools(k_pages, v_pages)
+    B, M = _check_table(page_table)
+    T = k_new.shape[0]
+    if k_new.shape != (T, Hkv, d) or v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must be [total_tokens,Hkv,d], with the pages' heads and head_dim")
+    if cu_seqlens.shape != (B + 1,):
+        raise ValueError("cu_seqlens must be int32 [B+1]")
+    _check_sizes(k_new.shape)
+    st = _on_device(dev, _lib.attn_kvpages_append, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), k_new.data_ptr(),
+                    v_new.data_ptr(), cu_seqlens.data_ptr(), _lens_ptr(cache_seqlens, "cache_seqlens", B), B, T, Hkv, M, P, page, d, *strides,
+                    _dtype_code(k_new))
+    _lib._check(st, "attn_kvpages_append")
+
+
+def _books(named, page: int, out, like):
+    """Checks the int32 arrays of a call on the books (named: (tensor, name)) and the outputs: `out`, or new ones shaped like
+    `like`.  Returns (device, B, max_pages, pages, outputs)."""
+    i32 = torch.int32
+    try:
+        dev = named[0][0].get_device()
+        fit = _fit(dev, *(t for t, _ in named)) and all(t.dtype is i32 for t, _ in named)
+    except AttributeError:  # not a tensor
+        fit = False
+    if not fit:
+        _explain(*((t, n, i32, False) for t, n in named))
+    if page not in (16, 32, 64, 128):
+        raise ValueError("page must be 16, 32, 64 or 128")
+    B, M = _check_table(named[0][0])
+    refs = dict((n, t) for t, n in named)["refs"]
+    if refs.dim() != 1:
+        raise ValueError("refs must be int32 [pages]")
+    _check_sizes(refs.shape)
+    for t, n in named:
+        if n not in ("page_table", "refs", "src", "dst") and t.shape != (B,):
+            raise ValueError(f"{n} must be int32 [B]")
+    if out is None:
+        out = tuple(torch.empty_like(t) for t in like)
+    else:
+        out = tuple(out)
+        if len(out) != len(like):
+            raise ValueError(f"out must hold {len(like)} tensors")
+        for t, x in zip(out, like):
+            _require(t, "out", i32)
+            if t.shape != x.shape or t.device != x.device:
+                raise ValueError("out must be shaped like the arrays that it follows, on their device")
+    return dev, B, M, refs.shape[0], out
+
+
+def kvpages_free(page_table, cache_seqlens, refs, keep_seqlens, page: int, out=None):
+    """Cuts each sequence to its first keep_seqlens[b] tokens (0 ends it) and gives back the pages behind them.  page_table
+    int32 [B,max_pages], cache_seqlens and keep_seqlens int32 [B], refs int32 [pages].  out: (page_table, cache_seqlens,
+    refs) to write to, which may be the inputs (None: new ones).  Returns those three."""
+    dev, B, M, P, o = _books(((page_table, "page_table"), (cache_seqlens, "cache_seqlens"), (refs, "refs"), (keep_seqlens, "keep_seqlens")),
+                             page, out, (page_table, cache_seqlens, refs))
+    st = _on_device(dev, _lib.attn_kvpages_free, page_table.data_ptr(), cache_seqlens.data_ptr(), refs.data_ptr(), keep_seqlens.data_ptr(),
+                    o[0].data_ptr(), o[1].data_ptr(), o[2].data_ptr(), B, M, P, page)
+    _lib._check(st, "attn_kvpages_free")
+    return o
+
+
+def kvpages_fork(page_table, cache_seqlens, refs, src, dst, page: int, out=None):
+    """Makes the empty rows dst[i] copies of the rows src[i] (int32 [n]): full pages are shared, a partly filled last page is
+    replaced by a free one.  out: (page_table, cache_seqlens, refs) as for kvpages_free.  Returns (page_table, cache_seqlens,
+    refs, copies int32 [n,2]); copies goes to kvpages_copy for each pair of pools."""
+    dev, B, M, P, o = _books(((page_table, "page_table"), (cache_seqlens, "cache_seqlens"), (refs, "refs"), (src, "src"), (dst, "dst")), page,
+                             out, (page_table, cache_seqlens, refs))
+    if src.dim() != 1 or src.shape != dst.shape:
+        raise ValueError("src and dst must be int32 [n]")
+    n = src.shape[0]
+    copies = torch.empty((n, 2), dtype=torch.int32, device=src.device)
+    st = _on_device(dev, _lib.attn_kvpages_fork, page_table.data_ptr(), cache_seqlens.data_ptr(), refs.data_ptr(), src.data_ptr(), dst.data_ptr(),
+                    o[0].data_ptr(), o[1].data_ptr(), o[2].data_ptr(), copies.data_ptr(), n, B, M, P, page)
+    _lib._check(st, "attn_kvpages_fork")
+    return o + (copies,)
+
+
+def kvpages_reserve(page_table, cache_seqlens, refs, new_seqlens, page: int, out=None):
+    """Appends free pages to each row until it has room for new_seqlens[b] tokens behind its first cache_seqlens[b].  out:
+    (page_table, refs) to write to, which may be the inputs (None: new ones).  Returns those two."""
+    dev, B, M, P, o = _books(((page_table, "page_table"), (cache_seqlens, "cache_seqlens"), (refs, "refs"), (new_seqlens, "new_seqlens")), page,
+                             out, (page_table, refs))
+    st = _on_device(dev, _lib.attn_kvpages_reserve, page_table.data_ptr(), cache_seqlens.data_ptr(), refs.data_ptr(), new_seqlens.data_ptr(),
+                    o[0].data_ptr(), o[1].data_ptr(), B, M, P, page)
+    _lib._check(st, "attn_kvpages_reserve")
+    return o
+
+
+def kvpages_compact(page_table, refs, out=None):
+    """Moves the used pages to the front of the pool: with U in use, those from U on go to the free places before it.  out:
+    (page_table, refs) to write to, which may be the inputs (None: new ones).  Returns (page_table, refs, copies int32
+    [pages // 2, 2], used int32 [1]: U); copies goes to kvpages_copy for each pair of pools."""
+    dev, B, M, P, o = _books(((page_table, "page_table"), (refs, "refs")), 16, out, (page_table, refs))
+    copies = torch.empty((P // 2, 2), dtype=torch.int32, device=refs.device)
+    used = torch.empty((1,), dtype=torch.int32, device=refs.device)
+    st = _on_device(dev, _lib.attn_kvpages_compact, page_table.data_ptr(), refs.data_ptr(), o[0].data_ptr(), o[1].data_ptr(), copies.data_ptr(),
+                    used.data_ptr(), B, M, P)
+    _lib._check(st, "attn_kvpages_compact")
+    return o + (copies, used)
+
+
+def kvpages_copy(k_pages, v_pages, copies):
+    """Copies pages of keys and of values within their pools, in place: copies int32 [n,2], (from, to), as kvpages_fork and
+    kvpages_compact return it; (-1, -1) is passed over."""
+    i32 = torch.int32
+    try:
+        dev = k_pages.get_device()
+        fit = _fit(dev, k_pages, v_pages, copies) and v_pages.dtype is k_pages.dtype and copies.dtype is i32
+    except AttributeError:  # not a tensor
+        fit = False
+    if not fit:
+        _explain((k_pages, "k_pages", None, False), (v_pages, "v_pages", getattr(k_pages, "dtype", None), False), (copies, "copies", i32, False))
+    P, Hkv, page, d = _check_pools(k_pages, v_pages)
+    if copies.dim() != 2 or copies.shape[1] != 2:
+        raise ValueError("copies must be int32 [n,2]")
+    _check_sizes(copies.shape)
+    st = _on_device(dev, _lib.attn_kvpages_copy, k_pages.data_ptr(), v_pages.data_ptr(), copies.data_ptr(), copies.shape[0], Hkv, P, page, d,
+                    _dtype_code(k_pages))
+    _lib._check(st, "attn_kvpages_copy")
+
+
 class _AttnFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, causal, scale, deterministic):
@@ -514,3 +855,25 @@ def flash_attn_varlen_qkvpacked_func(qkv, cu_seqlens, max_seqlen, dropout_p=0.0,
         raise ValueError("Token count mismatch")
     return _VarlenFn.apply(qkv, cu_seqlens.to(torch.int32), int(max_seqlen), bool(causal), softmax_scale,
                            bool(deterministic))
+
+
+class _VarlenGqaFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, cu_seqlens, max_seqlen, causal, scale, deterministic):
+        out, lse = fwd_varlen_gqa(q, k, v, cu_seqlens, max_seqlen, causal, scale)
+        ctx.save_for_backward(q, k, v, out, lse, cu_seqlens)
+        ctx.max_seqlen, ctx.causal, ctx.scale, ctx.deterministic = max_seqlen, causal, scale, deterministic
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        q, k, v, out, lse, cu_seqlens = ctx.saved_tensors
+        dq, dk, dv = bwd_varlen_gqa(q, k, v, out, lse, dout.contiguous(), cu_seqlens, ctx.max_seqlen, ctx.causal, ctx.scale,
+                                    deterministic=ctx.deterministic)
+        return dq, dk, dv, None, None, None, None, None
+
+
+def flash_attn_varlen_gqa_func(q, k, v, cu_seqlens, max_seqlen, softmax_scale=None, causal=False, deterministic=False):
+    """Differentiable fwd_varlen_gqa: q [T,Hq,d], k and v [T,Hkv,d], cu_seqlens int32 [batch+1] -> [T,Hq,d].  deterministic
+    makes the backward's dq bitwise reproducible (slower)."""
+    return _VarlenGqaFn.apply(q, k, v, cu_seqlens, int(max_seqlen), bool(causal), softmax_scale, bool(deterministic))

@@ -273,6 +273,7 @@ attn_status_t attn_fwd_varlen(const void* qkv, const int32_t* cu_seqlens, int ns
   const size_t plane = static_cast<size_t>(H) * d;
   if (f32) {
     const float* base = static_cast<const float*>(qkv);
+    p.tok_q = p.tok_k = p.tok_v = 3LL * H * d;
     return from_cuda(attn::launch_fwd_f32(base, base + plane, base + 2 * plane, p, causal != 0, attn::kModeVarlen, s));
   }
   FwdMaps maps;
@@ -316,7 +317,7 @@ attn_status_t bwd_setup(BwdParams* p, void* workspace, size_t workspace_bytes, i
   p->B = B; p->Hq = Hq; p->Hkv = Hkv; p->N = N; p->Nk = N; p->d = d; p->G = Hq / Hkv;
   p->n_ktiles = (N + attn::kBN - 1) / attn::kBN;
   const BwdParams::Rows dense{d, static_cast<long long>(N) * d};
-  p->lay_q = p->lay_kv = p->lay_o = p->lay_dq = p->lay_dkv = dense;
+  p->lay_q = p->lay_k = p->lay_v = p->lay_o = p->lay_dq = p->lay_dkv = dense;
   p->cu_seqlens = nullptr;
   p->scale = resolve_scale(scale, d);
   p->scale_log2 = p->scale * kLog2e;
@@ -438,7 +439,7 @@ attn_status_t attn_bwd_cross(const void* q, const void* k, const void* v, const 
   if (st != ATTN_OK) return st;
   p.Nk = Nk;
   p.n_ktiles = (Nk + attn::kBN - 1) / attn::kBN;
-  p.lay_kv = p.lay_dkv = BwdParams::Rows{d, static_cast<long long>(Nk) * d};
+  p.lay_k = p.lay_v = p.lay_dkv = BwdParams::Rows{d, static_cast<long long>(Nk) * d};
   p.q = q; p.k = k; p.v = v; p.o = o; p.dout = dout; p.lse = lse;
   p.dq = dq; p.dk = dk; p.dv = dv;
   if (!(p.status = status_word())) return ATTN_ERR_CUDA;
@@ -478,7 +479,7 @@ attn_status_t attn_bwd_varlen(const void* qkv, const void* out, const void* dout
   if (st != ATTN_OK) return st;
   const long long hd = static_cast<long long>(H) * d;
   const BwdParams::Rows packed{3 * hd, d}, rows{hd, d};
-  p.lay_q = p.lay_kv = p.lay_dq = p.lay_dkv = packed;
+  p.lay_q = p.lay_k = p.lay_v = p.lay_dq = p.lay_dkv = packed;
   p.lay_o = rows;
   p.cu_seqlens = cu_seqlens;
   p.nseq = nseq;
@@ -1022,6 +1023,544 @@ attn_status_t attn_kvcache_evict(const void* k_cache, const void* v_cache, const
   p.B = B; p.Hkv = Hkv; p.Nk = Nk; p.cap = capacity; p.keep = keep; p.recent = recent; p.M = static_cast<int>(M);
   p.row_bytes = static_cast<int>(row);
   return from_cuda(attn::launch_cache_evict(p, static_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------- packed sequences with grouped heads
+namespace {
+
+// A work item holds `heads` neighbouring query heads of a kv head for tile_tokens tokens: the divisor of the group
+// (16 at most) that needs the fewest 128-row tiles for sequences of the average length, the larger one of equals.
+// Short sequences want many heads; long ones only that tokens * heads fill the 128 rows (12 heads: 10 tokens, 120).
+struct PackedTile {
+  int heads, tokens;
+};
+PackedTile packed_tile(int G, int total_tokens, int nseq) {
+  const long long mean = std::max(1, total_tokens / std::max(1, nseq));
+  PackedTile best{1, 128};
+  long long least = G * ((mean + 127) / 128);
+  for (int h = 2; h <= std::min(G, 16); ++h) {
+    if (G % h != 0) continue;
+    const long long tokens = 128 / h, tiles = G / h * ((mean + tokens - 1) / tokens);
+    if (tiles <= least) {
+      least = tiles;
+      best = {h, static_cast<int>(tokens)};
+    }
+  }
+  return best;
+}
+
+// {d, heads, tokens} over [T, H, d] with a token stride: boxes of a work item's tokens and heads.
+bool make_packed_rows_map(CUtensorMap* map, const void* base, attn_dtype_t dt, int T, int H, int d, long long stride, const PackedTile& t) {
+  const uint64_t dims[3] = {static_cast<uint64_t>(d), static_cast<uint64_t>(H), static_cast<uint64_t>(T)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(d) * 2, static_cast<uint64_t>(stride) * 2};
+  const uint32_t box[3] = {64, static_cast<uint32_t>(t.heads), static_cast<uint32_t>(t.tokens)};
+  return make_map(map, base, dt, 3, dims, strides, box);
+}
+
+// The fp32 dQ accumulator, [T, H, d], with boxes of 32 columns by a query tile's heads and tokens.
+bool make_packed_acc_map(CUtensorMap* map, const float* base, int T, int H, int d, const PackedTile& t) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const uint64_t dims[3] = {static_cast<uint64_t>(d), static_cast<uint64_t>(H), static_cast<uint64_t>(T)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(d) * 4, static_cast<uint64_t>(H) * d * 4};
+  const uint32_t box[3] = {32, static_cast<uint32_t>(t.heads), static_cast<uint32_t>(t.tokens)};
+  const uint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr size_t kListHead = 256;  // bytes before the tiles: their count and the last token
+size_t packed_list_bytes(int T, int nseq, int max_seqlen, int tile) {
+  return kListHead + round256(static_cast<size_t>(attn::packed_bound(T, nseq, max_seqlen, tile)) * sizeof(int4));
+}
+
+// Checks that the forward and the backward share.  *run is left false when there is nothing to do.
+attn_status_t check_packed(const void* cu_seqlens, int nseq, int total_tokens, int max_seqlen, int Hq, int Hkv, int d, int64_t q_stride,
+                           int64_t k_stride, int64_t v_stride, float scale, attn_dtype_t dtype, bool* run) {
+  *run = false;
+  const attn_status_t st = check_common(d, scale, dtype);
+  if (st != ATTN_OK) return st;
+  if (nseq < 0 || total_tokens < 0 || max_seqlen < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+  const int vec = dtype == ATTN_F32 ? 4 : 8;  // elements of 16 bytes
+  if (q_stride < static_cast<int64_t>(Hq) * d || k_stride < static_cast<int64_t>(Hkv) * d || v_stride < static_cast<int64_t>(Hkv) * d ||
+      q_stride % vec != 0 || k_stride % vec != 0 || v_stride % vec != 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (total_tokens == 0) return ATTN_OK;
+  if (nseq == 0 || !cu_seqlens || !aligned(cu_seqlens, 4) || max_seqlen == 0) return ATTN_ERR_INVALID_ARG;
+  // tensor maps take byte strides below 2^40; items, tiles and rows of the statistics are numbered in 32 bits
+  if (std::max(q_stride, std::max(k_stride, v_stride)) >= (int64_t{1} << 36) || nseq > 65535 || (max_seqlen + 31LL) / 32 > 65535 ||
+      static_cast<long long>(total_tokens) * Hq > 0x7fffffffLL || total_tokens > 0x7fff0000)
+    return ATTN_ERR_UNSUPPORTED;
+  if (attn::packed_bound(total_tokens, nseq, max_seqlen, 8) * Hq > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;  // tiles of 8 tokens at least
+  *run = true;
+  return ATTN_OK;
+}
+
+}  // namespace
+
+size_t attn_fwd_varlen_gqa_workspace_bytes(int nseq, int total_tokens, int max_seqlen, int Hq, int Hkv) {
+  if (nseq <= 0 || total_tokens <= 0 || max_seqlen <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
+  return packed_list_bytes(total_tokens, nseq, max_seqlen, packed_tile(Hq / Hkv, total_tokens, nseq).tokens);
+}
+
+attn_status_t attn_fwd_varlen_gqa(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int nseq, int total_tokens,
+                                  int max_seqlen, void* out, float* lse, void* workspace, size_t workspace_bytes, int Hq, int Hkv, int d,
+                                  int64_t q_stride, int64_t k_stride, int64_t v_stride, int causal, float scale, attn_dtype_t dtype,
+                                  unsigned flags, void* stream) {
+  bool run;
+  const attn_status_t st = check_packed(cu_seqlens, nseq, total_tokens, max_seqlen, Hq, Hkv, d, q_stride, k_stride, v_stride, scale, dtype, &run);
+  if (st != ATTN_OK) return st;
+  if (flags & ~ATTN_FLAG_OUT_F32) return ATTN_ERR_INVALID_ARG;
+  if (!run) return ATTN_OK;
+  if (!all_aligned16({q, k, v, out}) || !aligned(lse, 4)) return ATTN_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < attn_fwd_varlen_gqa_workspace_bytes(nseq, total_tokens, max_seqlen, Hq, Hkv))
+    return ATTN_ERR_INVALID_ARG;
+  const size_t T = static_cast<size_t>(total_tokens), es = dtype == ATTN_F32 ? 4 : 2;
+  const size_t eo = dtype == ATTN_F32 || (flags & ATTN_FLAG_OUT_F32) ? 4 : 2;
+  const auto span = [&](int64_t stride, int H) { return ((T - 1) * static_cast<size_t>(stride) + static_cast<size_t>(H) * d) * es; };
+  if (clash({{out, T * Hq * d * eo}, {lse, T * Hq * sizeof(float)}, {workspace, workspace_bytes}},
+            {{q, span(q_stride, Hq)}, {k, span(k_stride, Hkv)}, {v, span(v_stride, Hkv)}, {cu_seqlens, (static_cast<size_t>(nseq) + 1) * 4}}))
+    return ATTN_ERR_INVALID_ARG;
+  FwdParams p{};
+  p.o = out;
+  p.lse = lse;
+  p.cu_seqlens = cu_seqlens;
+  p.status = status_word();
+  p.wait_ns = wait_limit_ns();
+  if (!p.status) return ATTN_ERR_CUDA;
+  p.B = 1; p.Hq = Hq; p.Hkv = Hkv; p.N = 0; p.d = d; p.G = Hq / Hkv;
+  p.nseq = nseq; p.total_tokens = total_tokens; p.max_seqlen = max_seqlen;
+  p.scale = resolve_scale(scale, d);
+  p.scale_log2 = p.scale * kLog2e;
+  p.out_f32 = (flags & ATTN_FLAG_OUT_F32) ? 1 : 0;
+  p.tok_q = q_stride; p.tok_k = k_stride; p.tok_v = v_stride;
+  const PackedTile t = packed_tile(p.G, total_tokens, nseq);
+  p.heads = t.heads;
+  p.tile_tokens = t.tokens;
+  p.open_end = 1;
+  int* const head = static_cast<int*>(workspace);
+  int4* const tiles = reinterpret_cast<int4*>(static_cast<char*>(workspace) + kListHead);
+  p.head = head;
+  p.tiles = tiles;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (attn::launch_packed_tiles(cu_seqlens, nseq, total_tokens, max_seqlen, t.tokens, causal != 0, false, head, tiles, p.status, s) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  if (dtype == ATTN_F32) {  // rows of sequences from the grid, rows behind the last one by a kernel of its own
+    void* const x[3] = {out, nullptr, nullptr};
+    const int bytes[3] = {Hq * d * 4, 0, 0};
+    if (attn::launch_fwd_f32(q, k, v, p, causal != 0, attn::kModePacked, s) != cudaSuccess) return ATTN_ERR_CUDA;
+    return from_cuda(attn::launch_packed_tail(x, bytes, lse, Hq, total_tokens, head + 1, s));
+  }
+  FwdMaps maps;
+  if (!make_packed_rows_map(&maps.q, q, dtype, total_tokens, Hq, d, q_stride, t) ||
+      !make_rows_map(&maps.k, k, dtype, total_tokens, Hkv, d, k_stride, d) || !make_rows_map(&maps.v, v, dtype, total_tokens, Hkv, d, v_stride, d))
+    return ATTN_ERR_CUDA;
+  if (p.out_f32)
+    maps.o = maps.q;  // unused: fp32 rows are stored by the threads
+  else if (!make_packed_rows_map(&maps.o, out, dtype, total_tokens, Hq, d, static_cast<long long>(Hq) * d, t))
+    return ATTN_ERR_CUDA;
+  return from_cuda(attn::launch_fwd_packed(maps, p, dtype, causal != 0, s));
+}
+
+size_t attn_bwd_varlen_gqa_workspace_bytes(int nseq, int total_tokens, int max_seqlen, int Hq, int Hkv, int d) {
+  if (nseq <= 0 || total_tokens <= 0 || max_seqlen <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || d <= 0) return 0;
+  return attn_bwd_workspace_bytes(1, Hq, total_tokens, d) + packed_list_bytes(total_tokens, nseq, max_seqlen, attn::kBN);
+}
+
+attn_status_t attn_bwd_varlen_gqa(const void* q, const void* k, const void* v, const void* out, const void* dout, const float* lse,
+                                  const int32_t* cu_seqlens, int nseq, int total_tokens, int max_seqlen, void* dq, void* dk, void* dv,
+                                  void* workspace, size_t workspace_bytes, int Hq, int Hkv, int d, int64_t q_stride, int64_t k_stride,
+                                  int64_t v_stride, int causal, float scale, attn_dtype_t dtype, unsigned flags, void* stream) {
+  bool run;
+  attn_status_t st = check_packed(cu_seqlens, nseq, total_tokens, max_seqlen, Hq, Hkv, d, q_stride, k_stride, v_stride, scale, dtype, &run);
+  if (st != ATTN_OK) return st;
+  if (flags & ~(ATTN_FLAG_OUT_F32 | ATTN_FLAG_DETERMINISTIC)) return ATTN_ERR_INVALID_ARG;
+  if (!run) return ATTN_OK;
+  if (!all_aligned16({q, k, v, out, dout, dq, dk, dv}) || !lse || !aligned(lse, 4)) return ATTN_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < attn_bwd_varlen_gqa_workspace_bytes(nseq, total_tokens, max_seqlen, Hq, Hkv, d))
+    return ATTN_ERR_INVALID_ARG;
+  const size_t T = static_cast<size_t>(total_tokens), es = dtype == ATTN_F32 ? 4 : 2;
+  const size_t eo = dtype == ATTN_F32 || (flags & ATTN_FLAG_OUT_F32) ? 4 : 2;
+  const auto span = [&](int64_t stride, int H) { return ((T - 1) * static_cast<size_t>(stride) + static_cast<size_t>(H) * d) * es; };
+  const size_t rows_q = T * Hq * d, rows_k = T * Hkv * d;
+  if (clash({{dq, rows_q * eo}, {dk, rows_k * eo}, {dv, rows_k * eo}, {workspace, workspace_bytes}},
+            {{q, span(q_stride, Hq)}, {k, span(k_stride, Hkv)}, {v, span(v_stride, Hkv)}, {out, rows_q * es}, {dout, rows_q * es},
+             {lse, T * Hq * sizeof(float)}, {cu_seqlens, (static_cast<size_t>(nseq) + 1) * 4}}))
+    return ATTN_ERR_INVALID_ARG;
+  BwdParams p{};
+  st = bwd_setup(&p, workspace, workspace_bytes, 1, Hq, Hkv, total_tokens, d, scale, dtype, flags, max_seqlen);
+  if (st != ATTN_OK) return st;
+  const BwdParams::Rows rq{static_cast<long long>(Hq) * d, d}, rk{static_cast<long long>(Hkv) * d, d};
+  p.lay_q = {q_stride, d};
+  p.lay_o = rq;
+  p.lay_dq = rq;
+  p.lay_dkv = rk;
+  p.cu_seqlens = cu_seqlens;
+  p.nseq = nseq;
+  p.max_seqlen = max_seqlen;
+  p.open_end = 1;
+  p.q = q; p.k = k; p.v = v; p.o = out; p.dout = dout; p.lse = lse;
+  p.dq = dq; p.dk = dk; p.dv = dv;
+  if (!(p.status = status_word())) return ATTN_ERR_CUDA;
+  char* const list = static_cast<char*>(workspace) + attn_bwd_workspace_bytes(1, Hq, total_tokens, d);
+  int* const head = reinterpret_cast<int*>(list);
+  int4* const tiles = reinterpret_cast<int4*>(list + kListHead);
+  p.head = head;
+  p.tiles = tiles;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (attn::launch_packed_tiles(cu_seqlens, nseq, total_tokens, max_seqlen, attn::kBN, causal != 0, true, head, tiles, p.status, s) != cudaSuccess ||
+      attn::launch_bwd_preprocess(p, dtype, dtype != ATTN_F32, s) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  if (dtype == ATTN_F32) {
+    p.lay_k = {k_stride, d};
+    p.lay_v = {v_stride, d};
+    void* const x[3] = {dq, dk, dv};
+    const int bytes[3] = {Hq * d * 4, Hkv * d * 4, Hkv * d * 4};
+    if (attn::launch_bwd_f32(p, causal != 0, s) != cudaSuccess) return ATTN_ERR_CUDA;
+    return from_cuda(attn::launch_packed_tail(x, bytes, nullptr, 0, total_tokens, head + 1, s));
+  }
+  const PackedTile t = packed_tile(p.G, total_tokens, nseq);
+  p.heads = t.heads;
+  p.tile_tokens = t.tokens;
+  BwdMaps maps;
+  if (!make_packed_rows_map(&maps.q, q, dtype, total_tokens, Hq, d, q_stride, t) ||
+      !make_packed_rows_map(&maps.dout, dout, dtype, total_tokens, Hq, d, static_cast<long long>(Hq) * d, t) ||
+      !make_rows_map(&maps.k, k, dtype, total_tokens, Hkv, d, k_stride, d) || !make_rows_map(&maps.v, v, dtype, total_tokens, Hkv, d, v_stride, d) ||
+      !make_packed_acc_map(&maps.dq_acc, p.dq_acc, total_tokens, Hq, d, t))
+    return ATTN_ERR_CUDA;
+  if (attn::launch_bwd_packed(maps, p, dtype, causal != 0, s) != cudaSuccess) return ATTN_ERR_CUDA;
+  // the accumulator is in the order of dq
+  p.lay_dq = {d, static_cast<long long>(total_tokens) * d};
+  return from_cuda(attn::launch_bwd_postprocess(p, dtype, s));
+}
+
+// ---------------------------------------------------------------- KV caches in pages
+namespace {
+
+bool page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+int page_shift_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
+
+// {d, page, P * Hkv} over a pool [P, Hkv, page, d]: boxes of `rows` keys.
+bool make_pages_map(CUtensorMap* map, const void* base, attn_dtype_t dt, long long heads, int page, int d, int rows) {
+  const uint64_t dims[3] = {static_cast<uint64_t>(d), static_cast<uint64_t>(page), static_cast<uint64_t>(heads)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(d) * 2, static_cast<uint64_t>(page) * d * 2};
+  const uint32_t box[3] = {64, static_cast<uint32_t>(rows), 1};
+  return make_map(map, base, dt, 3, dims, strides, box);
+}
+
+// The few-rows kernel's launch, as for the 8-bit cache (cache8_plan).
+Cache8Plan paged_plan(int B, int Hkv, int R, int Nk, int d) {
+  const long long pairs = static_cast<long long>(B) * Hkv;
+  const int nb = R <= 8 ? 1 : 2, keys = attn::paged_tile_keys(d);
+  const long long tiles = (static_cast<long long>(Nk) + keys - 1) / keys;
+  const long long room = attn::paged_ctas_per_sm(nb) * 152LL;
+  int cluster = 1;
+  while (cluster < 8 && pairs * 2 * cluster <= room && tiles > 4 * cluster) cluster *= 2;
+  if (pairs * cluster <= room && tiles <= 4 * 4LL * cluster) return {static_cast<int>(pairs) * cluster, cluster, 0, 0, 0};
+  const long long ctas = std::max(1LL, std::min((pairs * tiles + 3) / 4, room));
+  const size_t rows = 2 * static_cast<size_t>(ctas) * 4 * R;
+  return {static_cast<int>(ctas), 0, round256(rows * d * sizeof(float)), round256(rows * sizeof(float)),
+          round256(static_cast<size_t>(pairs) * sizeof(int2))};
+}
+
+// Many rows: the key ranges of the least estimated time (kv8_plan's rule, without its expansion).
+struct PagedRanges {
+  KvSplit split;
+  size_t o_bytes, lse_bytes;
+};
+PagedRanges paged_ranges(long long bh, long long R, int Nk, int d, bool f32, int Hq, int Hkv, int Nq, int B) {
+  PagedRanges r{};
+  r.split = f32 ? kv_split(B, Hq, Hkv, Nq, Nk, 0) : kv8_plan(bh, R, Nk, d).split;
+  if (f32 || r.split.n_splits > 1) {
+    r.o_bytes = round256(static_cast<size_t>(r.split.n_splits) * bh * R * d * sizeof(float));
+    r.lse_bytes = round256(static_cast<size_t>(r.split.n_splits) * bh * R * sizeof(float));
+  }
+  return r;
+}
+
+// The tokens that a sequence may hold.
+int most_tokens(int M, int page, int max_seqlen) {
+  const long long room = static_cast<long long>(M) * page;
+  return static_cast<int>(max_seqlen > 0 ? std::min<long long>(max_seqlen, room) : room);
+}
+
+// Sizes that the calls on pools and tables share.
+attn_status_t check_pool(int B, int Hkv, int M, int P, int page, int d) {
+  if (B < 0 || Hkv <= 0 || M < 0 || P < 0 || d <= 0 || !page_ok(page)) return ATTN_ERR_INVALID_ARG;
+  if (d % 16 != 0 || d > 128) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * Hkv > 0x7fffffffLL || static_cast<long long>(P) * Hkv >= 0x7fffffffLL ||
+      static_cast<long long>(M) * page > kMaxTokens || static_cast<long long>(B) * M > 0x7fffffffLL ||
+      static_cast<long long>(Hkv) * page * d * 4 / 16 > 0x7fffffffLL)
+    return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+}  // namespace
+
+size_t attn_fwd_kvpages_workspace_bytes(int B, int Hq, int Hkv, int Nq, int max_pages, int page, int max_seqlen, int d, attn_dtype_t dtype) {
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Nq <= 0 || max_pages < 0 || !page_ok(page) || max_seqlen < 0 || d <= 0 ||
+      static_cast<long long>(max_pages) * page > kMaxTokens)
+    return 0;
+  const int Nk = most_tokens(max_pages, page, max_seqlen);
+  const long long R = static_cast<long long>(Hq / Hkv) * Nq, bh = static_cast<long long>(B) * Hkv;
+  if (Nk == 0 || R > kMaxTokens) return 0;
+  if (dtype != ATTN_F32 && R <= attn::kPagedRows) {
+    const Cache8Plan plan = paged_plan(B, Hkv, static_cast<int>(R), Nk, d);
+    return plan.o_bytes + plan.lse_bytes + plan.parts_bytes;
+  }
+  const PagedRanges r = paged_ranges(bh, R, Nk, d, dtype == ATTN_F32, Hq, Hkv, Nq, B);
+  return r.o_bytes + r.lse_bytes;
+}
+
+attn_status_t attn_fwd_kvpages(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table, const int32_t* cache_seqlens,
+                               void* o, float* lse, void* workspace, size_t workspace_bytes, int B, int Hq, int Hkv, int Nq, int max_pages,
+                               int pages, int page, int max_seqlen, int d, int causal, float scale, attn_dtype_t dtype, unsigned flags,
+                               void* stream) {
+  attn_status_t st = check_common(d, scale, dtype);
+  if (st != ATTN_OK) return st;
+  if (B < 0 || Nq < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || max_seqlen < 0) return ATTN_ERR_INVALID_ARG;
+  st = check_pool(B, Hkv, max_pages, pages, page, d);
+  if (st != ATTN_OK) return st;
+  if (flags & ~ATTN_FLAG_OUT_F32) return ATTN_ERR_INVALID_ARG;
+  if (B == 0 || Nq == 0) return ATTN_OK;
+  // a pool or a table without pages is never read: its pointers may be null
+  const int Nk = pages > 0 ? most_tokens(max_pages, page, max_seqlen) : 0;
+  if (!all_aligned16({q, o}) || !cache_seqlens || !aligned(cache_seqlens, 4) || !aligned(lse, 4) ||
+      (Nk > 0 && (!all_aligned16({k_pages, v_pages}) || !page_table || !aligned(page_table, 4))))
+    return ATTN_ERR_INVALID_ARG;
+  const int G = Hq / Hkv;
+  const long long R = static_cast<long long>(G) * Nq, bh = static_cast<long long>(B) * Hkv;
+  if (R > kMaxTokens || bh * R > 0x7fffffffLL || static_cast<long long>(B) * Hq > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  const bool f32 = dtype == ATTN_F32;
+  const size_t need = Nk > 0 ? attn_fwd_kvpages_workspace_bytes(B, Hq, Hkv, Nq, max_pages, page, max_seqlen, d, dtype) : 0;
+  if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return ATTN_ERR_INVALID_ARG;
+  const size_t es = f32 ? 4 : 2, eo = f32 || (flags & ATTN_FLAG_OUT_F32) ? 4 : 2, rows = static_cast<size_t>(bh) * R;
+  const size_t pool = static_cast<size_t>(pages) * Hkv * page * d * es;
+  if (clash({{o, rows * d * eo}, {lse, rows * sizeof(float)}, {need ? workspace : nullptr, need}},
+            {{q, rows * d * es}, {k_pages, pool}, {v_pages, pool}, {page_table, static_cast<size_t>(B) * max_pages * 4},
+             {cache_seqlens, static_cast<size_t>(B) * 4}}))
+    return ATTN_ERR_INVALID_ARG;
+  unsigned* const status = status_word();
+  if (!status) return ATTN_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int shift = page_shift_of(page);
+  if (Nk == 0 || (!f32 && R <= attn::kPagedRows)) {
+    attn::PagedParams p{};
+    p.q = q;
+    p.table = page_table;
+    p.cache_seqlens = cache_seqlens;
+    p.o = o;
+    p.lse = lse;
+    p.status = status;
+    p.wait_ns = wait_limit_ns();
+    p.B = B; p.Hkv = Hkv; p.Nq = Nq; p.Nk = Nk; p.R = static_cast<int>(R); p.d = d;
+    p.causal = causal != 0;
+    p.M = max_pages; p.P = pages; p.page_shift = shift;
+    p.scale_log2 = resolve_scale(scale, d) * kLog2e;
+    p.out_f32 = eo == 4 ? 1 : 0;
+    if (Nk == 0) return from_cuda(attn::launch_paged_none(p, s));
+    p.tile_keys = attn::paged_tile_keys(d);
+    p.box_shift = std::min(shift, p.tile_keys == 32 ? 5 : 4);
+    if (bh * ((static_cast<long long>(Nk) + p.tile_keys - 1) / p.tile_keys) > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+    const Cache8Plan plan = paged_plan(B, Hkv, p.R, Nk, d);
+    char* const ws = static_cast<char*>(workspace);
+    p.ctas = plan.ctas;
+    p.cluster = plan.cluster;
+    p.runs = plan.ctas * 4;
+    p.o_part = reinterpret_cast<float*>(ws);
+    p.lse_part = reinterpret_cast<float*>(ws + plan.o_bytes);
+    p.parts = reinterpret_cast<int2*>(ws + plan.o_bytes + plan.lse_bytes);
+    CUtensorMap mk, mv;
+    const long long heads = static_cast<long long>(pages) * Hkv;
+    if (!make_pages_map(&mk, k_pages, dtype, heads, page, d, 1 << p.box_shift) || !make_pages_map(&mv, v_pages, dtype, heads, page, d, 1 << p.box_shift))
+      return ATTN_ERR_CUDA;
+    return from_cuda(attn::launch_paged_fwd(mk, mv, p, dtype, s));
+  }
+  const PagedRanges ranges = paged_ranges(bh, R, Nk, d, f32, Hq, Hkv, Nq, B);
+  const long long n_rb = (R + attn::kBM - 1) / attn::kBM;
+  if (f32 ? (Nq + 31) / 32 > 65535 : n_rb * bh * ranges.split.n_splits > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  FwdParams p{};
+  p.o = o;
+  p.lse = lse;
+  p.status = status;
+  p.wait_ns = wait_limit_ns();
+  p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.N = Nk; p.d = d; p.G = G;
+  p.Nq = Nq; p.Nk = Nk; p.R = static_cast<int>(R);
+  p.cache_seqlens = cache_seqlens;
+  p.n_splits = ranges.split.n_splits;
+  p.tiles_per_split = ranges.split.tiles_per_split;
+  p.o_part = static_cast<float*>(workspace);
+  p.lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + ranges.o_bytes);
+  p.n_qtiles = static_cast<int>(n_rb);
+  p.scale = resolve_scale(scale, d);
+  p.scale_log2 = p.scale * kLog2e;
+  p.out_f32 = (flags & ATTN_FLAG_OUT_F32) ? 1 : 0;
+  p.table = page_table;
+  p.M = max_pages; p.P = pages; p.page_shift = shift;
+  cudaError_t e;
+  if (f32) {
+    e = attn::launch_fwd_f32(q, k_pages, v_pages, p, causal != 0, attn::kModePaged, s);
+  } else {
+    FwdMaps maps;
+    const long long heads = static_cast<long long>(pages) * Hkv;
+    if (!make_dense_map(&maps.q, q, dtype, static_cast<int>(bh), p.R, d) || !make_pages_map(&maps.k, k_pages, dtype, heads, page, d, page) ||
+        !make_pages_map(&maps.v, v_pages, dtype, heads, page, d, page))
+      return ATTN_ERR_CUDA;
+    maps.o = maps.q;
+    if (p.n_splits == 1 && !p.out_f32 && !make_dense_map(&maps.o, o, dtype, static_cast<int>(bh), p.R, d)) return ATTN_ERR_CUDA;
+    e = attn::launch_fwd_paged(maps, p, dtype, causal != 0, s);
+    if (p.n_splits == 1) return from_cuda(e);
+  }
+  if (e != cudaSuccess) return ATTN_ERR_CUDA;
+  return from_cuda(attn::launch_kv_combine(p, dtype, causal != 0, s));
+}
+
+attn_status_t attn_kvpages_append(void* k_pages, void* v_pages, const int32_t* page_table, const void* k_new, const void* v_new,
+                                  const int32_t* cu_seqlens, const int32_t* cache_seqlens, int B, int total_tokens, int Hkv, int max_pages,
+                                  int pages, int page, int d, int64_t k_stride, int64_t v_stride, attn_dtype_t dtype, void* stream) {
+  const attn_status_t st = check_pool(B, Hkv, max_pages, pages, page, d);
+  if (st != ATTN_OK) return st;
+  if (!dtype_ok(dtype) || total_tokens < 0) return ATTN_ERR_INVALID_ARG;
+  const int vec = dtype == ATTN_F32 ? 4 : 8;
+  if (k_stride < static_cast<int64_t>(Hkv) * d || v_stride < static_cast<int64_t>(Hkv) * d || k_stride % vec != 0 || v_stride % vec != 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (total_tokens == 0) return ATTN_OK;
+  if (B == 0 || max_pages == 0 || pages == 0) return ATTN_ERR_INVALID_ARG;  // tokens without a place
+  if (total_tokens > kMaxTokens) return ATTN_ERR_UNSUPPORTED;
+  if (!all_aligned16({k_pages, v_pages, k_new, v_new}) || !page_table || !aligned(page_table, 4) || !cu_seqlens || !aligned(cu_seqlens, 4) ||
+      !aligned(cache_seqlens, 4))
+    return ATTN_ERR_INVALID_ARG;
+  const size_t es = dtype == ATTN_F32 ? 4 : 2, pool = static_cast<size_t>(pages) * Hkv * page * d * es;
+  const auto span = [&](int64_t stride) { return ((static_cast<size_t>(total_tokens) - 1) * stride + static_cast<size_t>(Hkv) * d) * es; };
+  if (clash({{k_pages, pool}, {v_pages, pool}}, {{k_new, span(k_stride)}, {v_new, span(v_stride)}, {page_table, static_cast<size_t>(B) * max_pages * 4},
+                                                 {cu_seqlens, (static_cast<size_t>(B) + 1) * 4}, {cache_seqlens, static_cast<size_t>(B) * 4}}))
+    return ATTN_ERR_INVALID_ARG;
+  attn::PagesAppendParams p{};
+  p.k = static_cast<uint4*>(k_pages);
+  p.v = static_cast<uint4*>(v_pages);
+  p.k_new = static_cast<const uint4*>(k_new);
+  p.v_new = static_cast<const uint4*>(v_new);
+  p.k_stride = static_cast<size_t>(k_stride / vec);
+  p.v_stride = static_cast<size_t>(v_stride / vec);
+  p.table = page_table;
+  p.cu = cu_seqlens;
+  p.lens = cache_seqlens;
+  if (!(p.status = status_word())) return ATTN_ERR_CUDA;
+  p.T = total_tokens; p.B = B; p.M = max_pages; p.P = pages; p.Hkv = Hkv; p.page = page; p.row_vecs = d / vec;
+  return from_cuda(attn::launch_pages_append(p, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+struct Books {
+  const int32_t *table, *lens, *refs;
+  int32_t *table_out, *lens_out, *refs_out;  // lens_out: null where the call leaves the lengths
+};
+
+// Arguments that the calls on the books share.  Each output is its input itself, or lies apart from everything else.
+attn_status_t check_books(attn::PagesParams* p, const Books& b, int B, int M, int P, int page, std::initializer_list<Span> more_outs,
+                          std::initializer_list<Span> more_ins) {
+  if (B < 0 || M < 0 || P < 0 || !page_ok(page)) return ATTN_ERR_INVALID_ARG;
+  if (B > attn::kMaxTableRows || static_cast<long long>(B) * M > 0x7fffffffLL || static_cast<long long>(M) * page > kMaxTokens || P > kMaxTokens)
+    return ATTN_ERR_UNSUPPORTED;
+  const size_t t = static_cast<size_t>(B) * M * 4, l = static_cast<size_t>(B) * 4, r = static_cast<size_t>(P) * 4;
+  for (const void* x : {static_cast<const void*>(b.table), static_cast<const void*>(b.lens), static_cast<const void*>(b.refs),
+                        static_cast<const void*>(b.table_out), static_cast<const void*>(b.lens_out), static_cast<const void*>(b.refs_out)})
+    if (!aligned(x, 4)) return ATTN_ERR_INVALID_ARG;
+  if ((t > 0 && (!b.table || !b.table_out)) || (r > 0 && (!b.refs || !b.refs_out))) return ATTN_ERR_INVALID_ARG;
+  Span outs[8] = {{b.table_out, t}, {b.lens_out, l}, {b.refs_out, r}};
+  Span ins[8] = {{b.table, t}, {b.lens, l}, {b.refs, r}};
+  int n_outs = 3, n_ins = 3;
+  for (const Span& x : more_outs) outs[n_outs++] = x;
+  for (const Span& x : more_ins) ins[n_ins++] = x;
+  for (int i = 0; i < n_outs; ++i) {
+    for (int j = i + 1; j < n_outs; ++j)
+      if (overlap(outs[i], outs[j])) return ATTN_ERR_INVALID_ARG;
+    for (int j = 0; j < n_ins; ++j)
+      if (overlap(outs[i], ins[j]) && !(i == j && i < 3 && outs[i].p == ins[j].p)) return ATTN_ERR_INVALID_ARG;
+  }
+  p->table = b.table; p->lens = b.lens; p->refs = b.refs;
+  p->table_out = b.table_out; p->lens_out = b.lens_out; p->refs_out = b.refs_out;
+  p->B = B; p->M = M; p->P = P; p->page = page;
+  p->status = status_word();
+  return ATTN_OK;
+}
+
+}  // namespace
+
+attn_status_t attn_kvpages_free(const int32_t* page_table, const int32_t* cache_seqlens, const int32_t* refs, const int32_t* keep_seqlens,
+                                int32_t* table_out, int32_t* seqlens_out, int32_t* refs_out, int B, int max_pages, int pages, int page,
+                                void* stream) {
+  attn::PagesParams p{};
+  const attn_status_t st = check_books(&p, {page_table, cache_seqlens, refs, table_out, seqlens_out, refs_out}, B, max_pages, pages, page, {},
+                                       {{keep_seqlens, static_cast<size_t>(std::max(B, 0)) * 4}});
+  if (st != ATTN_OK) return st;
+  if (B > 0 && (!cache_seqlens || !seqlens_out || !keep_seqlens || !aligned(keep_seqlens, 4))) return ATTN_ERR_INVALID_ARG;
+  if (B == 0 && pages == 0) return ATTN_OK;
+  if (!p.status) return ATTN_ERR_CUDA;
+  p.arg = keep_seqlens;
+  return from_cuda(attn::launch_pages_free(p, static_cast<cudaStream_t>(stream)));
+}
+
+attn_status_t attn_kvpages_fork(const int32_t* page_table, const int32_t* cache_seqlens, const int32_t* refs, const int32_t* src,
+                                const int32_t* dst, int32_t* table_out, int32_t* seqlens_out, int32_t* refs_out, int32_t* copies, int n, int B,
+                                int max_pages, int pages, int page, void* stream) {
+  if (n < 0) return ATTN_ERR_INVALID_ARG;
+  if (n > attn::kMaxTableRows) return ATTN_ERR_UNSUPPORTED;
+  attn::PagesParams p{};
+  const size_t list = static_cast<size_t>(n) * 4;
+  const attn_status_t st = check_books(&p, {page_table, cache_seqlens, refs, table_out, seqlens_out, refs_out}, B, max_pages, pages, page,
+                                       {{copies, 2 * list}}, {{src, list}, {dst, list}});
+  if (st != ATTN_OK) return st;
+  if (B > 0 && (!cache_seqlens || !seqlens_out)) return ATTN_ERR_INVALID_ARG;
+  if (n > 0 && (!src || !dst || !copies || !aligned(src, 4) || !aligned(dst, 4) || !aligned(copies, 8))) return ATTN_ERR_INVALID_ARG;
+  if (B == 0 && pages == 0 && n == 0) return ATTN_OK;
+  if (!p.status) return ATTN_ERR_CUDA;
+  p.src = src; p.dst = dst; p.copies = copies;
+  p.n = n;
+  return from_cuda(attn::launch_pages_fork(p, static_cast<cudaStream_t>(stream)));
+}
+
+attn_status_t attn_kvpages_reserve(const int32_t* page_table, const int32_t* cache_seqlens, const int32_t* refs, const int32_t* new_seqlens,
+                                   int32_t* table_out, int32_t* refs_out, int B, int max_pages, int pages, int page, void* stream) {
+  attn::PagesParams p{};
+  const attn_status_t st = check_books(&p, {page_table, cache_seqlens, refs, table_out, nullptr, refs_out}, B, max_pages, pages, page, {},
+                                       {{new_seqlens, static_cast<size_t>(std::max(B, 0)) * 4}});
+  if (st != ATTN_OK) return st;
+  if (B > 0 && (!cache_seqlens || !new_seqlens || !aligned(new_seqlens, 4))) return ATTN_ERR_INVALID_ARG;
+  if (B == 0 && pages == 0) return ATTN_OK;
+  if (!p.status) return ATTN_ERR_CUDA;
+  p.arg = new_seqlens;
+  return from_cuda(attn::launch_pages_reserve(p, static_cast<cudaStream_t>(stream)));
+}
+
+attn_status_t attn_kvpages_compact(const int32_t* page_table, const int32_t* refs, int32_t* table_out, int32_t* refs_out, int32_t* copies,
+                                   int32_t* used, int B, int max_pages, int pages, void* stream) {
+  attn::PagesParams p{};
+  const attn_status_t st = check_books(&p, {page_table, nullptr, refs, table_out, nullptr, refs_out}, B, max_pages, pages, 16,
+                                       {{copies, static_cast<size_t>(std::max(pages, 0) / 2) * 8}, {used, 4}}, {});
+  if (st != ATTN_OK) return st;
+  if (!used || !aligned(used, 4) || (pages > 1 && (!copies || !aligned(copies, 8)))) return ATTN_ERR_INVALID_ARG;
+  if (!p.status) return ATTN_ERR_CUDA;
+  p.copies = copies;
+  p.used = used;
+  return from_cuda(attn::launch_pages_compact(p, static_cast<cudaStream_t>(stream)));
+}
+
+attn_status_t attn_kvpages_copy(void* k_pages, void* v_pages, const int32_t* copies, int n, int Hkv, int pages, int page, int d,
+                                attn_dtype_t dtype, void* stream) {
+  const attn_status_t st = check_pool(0, Hkv, 0, pages, page, d);
+  if (st != ATTN_OK) return st;
+  if (!dtype_ok(dtype) || n < 0) return ATTN_ERR_INVALID_ARG;
+  if (n == 0) return ATTN_OK;
+  if (!copies || !aligned(copies, 8) || (pages > 0 && !all_aligned16({k_pages, v_pages}))) return ATTN_ERR_INVALID_ARG;
+  const size_t bytes = static_cast<size_t>(Hkv) * page * d * (dtype == ATTN_F32 ? 4 : 2), pool = bytes * pages;
+  if (clash({{k_pages, pool}, {v_pages, pool}}, {{copies, static_cast<size_t>(n) * 8}})) return ATTN_ERR_INVALID_ARG;
+  unsigned* const status = status_word();
+  if (!status) return ATTN_ERR_CUDA;
+  return from_cuda(attn::launch_pages_copy(k_pages, v_pages, copies, n, pages, bytes, status, static_cast<cudaStream_t>(stream)));
 }
 
 attn_status_t attn_get_device_status(void* stream) {

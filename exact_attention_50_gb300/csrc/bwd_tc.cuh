@@ -98,7 +98,11 @@ __device__ __forceinline__ void split_pack<__half>(float a, float b, uint32_t& h
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
-template <typename T, int DP, bool CAUSAL>
+// PACKED: packed sequences with grouped heads.  The CTA's key tile comes from the list of tiles (launch_packed_tiles),
+// and a query tile is p.tile_tokens tokens by p.heads neighbouring query heads, row = token * heads + head, so short
+// sequences fill it.  What lies in the tiles behind the sequence's end is another sequence's, or anything: P and dS are
+// zero there by selection, not by multiplication, and the operands that they meet are set to zero in shared memory.
+template <typename T, int DP, bool CAUSAL, bool PACKED = false>
 __global__ void __launch_bounds__(512, 1)
     bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
@@ -158,10 +162,27 @@ __global__ void __launch_bounds__(512, 1)
   // heaviest tile left, which keeps the causal tail short.
   // Dense: x = batch * kv head.  Varlen: x = sequence * head; the sequence is the diagonal block
   // [seq_start, seq_start + seq_len) of a B = 1, N = total_tokens problem (G = 1).
-  const int kt = blockIdx.y;
+  int kt = blockIdx.y;
   // kv head (row block), its first query head; the sequence's start, its query and key counts
   int hkv, hq0, seq_start = 0, seq_len = p.N, kv_len = p.Nk;
-  if (p.cu_seqlens) {
+  if constexpr (PACKED) {
+    // rows behind the last sequence: dK = dV = 0
+    const int vecs = p.Hkv * p.d * (p.out_f32 ? 4 : 2) / 16;
+    for (int tok = p.head[1] + static_cast<int>(blockIdx.x); tok < p.N; tok += static_cast<int>(gridDim.x))
+      for (int i = threadIdx.x; i < vecs; i += L::kThreads) {
+        static_cast<uint4*>(p.dk)[static_cast<size_t>(tok) * vecs + i] = make_uint4(0, 0, 0, 0);
+        static_cast<uint4*>(p.dv)[static_cast<size_t>(tok) * vecs + i] = make_uint4(0, 0, 0, 0);
+      }
+    const int e = blockIdx.x / p.Hkv;
+    if (e >= p.head[0]) return;  // the whole CTA, before any barrier or allocation
+    const int4 tile = p.tiles[e];
+    if (tile.y == 0) return;
+    seq_start = tile.x;
+    seq_len = kv_len = tile.y;
+    kt = tile.z;
+    hkv = blockIdx.x % p.Hkv;
+    hq0 = hkv * p.G;
+  } else if (p.cu_seqlens) {
     const int s = blockIdx.x / p.Hkv, hh = blockIdx.x % p.Hkv;
     const int c0 = p.cu_seqlens[s], c1 = p.cu_seqlens[s + 1];
     const bool bad = c0 < 0 || c1 < c0 || c1 > p.N || c1 - c0 > p.max_seqlen || (s == 0 && c0 != 0) ||
@@ -181,15 +202,17 @@ __global__ void __launch_bounds__(512, 1)
     hq0 = b * p.Hq + g * p.G;
   }
   const int N = p.N;
-  const int n_q = (seq_len + kBM - 1) / kBM;
+  const int qtok = PACKED ? p.tile_tokens : kBM;  // tokens and heads of a query tile
+  const int qheads = PACKED ? p.heads : 1;
+  const int n_q = (seq_len + qtok - 1) / qtok;
   if (kt * kBN >= kv_len) return;  // a key tile past this sequence's end (varlen): the whole CTA
   // causal: query i sees key j iff j <= i + off (off = 0 for self-attention; cross-attention
   // aligns the queries with the last keys), so the first query tile that sees key tile kt is
   // the one holding query kt * 128 - off; every key tile is seen by the last query
   const int off = kv_len - seq_len;
-  const int qt0 = CAUSAL ? max(0, (kt * kBN - off) >= 0 ? (kt * kBN - off) / kBM : 0) : 0;
+  const int qt0 = CAUSAL ? max(0, (kt * kBN - off) >= 0 ? (kt * kBN - off) / qtok : 0) : 0;
   const int per_head = n_q - qt0;
-  const int n_it = p.G * per_head;
+  const int n_it = p.G / qheads * per_head;
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
@@ -219,6 +242,15 @@ __global__ void __launch_bounds__(512, 1)
     wait_limit_set(abort_flag, p.wait_ns);
     mbar_init_fence();
   }
+  if constexpr (PACKED) {  // rows that no query tile fills
+    const int r0 = qtok * qheads;
+    if (r0 < kBM) {
+      const int vecs = (kBM - r0) * 8;
+      for (int i = threadIdx.x; i < 2 * QS * kChunks * vecs; i += L::kThreads)  // the Q tiles, then the dO tiles
+        *reinterpret_cast<uint4*>(sQ + i / vecs * L::kChunkBytes + r0 * 128 + i % vecs * 16) = make_uint4(0, 0, 0, 0);
+      fence_async_smem();
+    }
+  }
   if (warp == 12) tmem_alloc(tmem_slot, L::kTmemCols);
   tc_fence_before();
   __syncthreads();
@@ -240,21 +272,22 @@ __global__ void __launch_bounds__(512, 1)
       }
       int nq_issued = 0, ndo_issued = 0;
       for (int it = 0; it < n_it; ++it) {
-        const int hq = hq0 + it / per_head, qt = qt0 + it % per_head;
+        const int hq = hq0 + it / per_head * qheads, qt = qt0 + it % per_head;
         const int st = it % QS;
         const uint32_t ph = ((it / QS) - 1) & 1;
+        const uint32_t q_bytes = PACKED ? kChunks * qtok * qheads * 128 : L::kTileBytes;
         // dO first: its slot frees earlier (after dV)
         if (it >= QS && !mbar_wait(do_empty + st, ph, abort_flag, p.status)) break;
-        mbar_expect_tx(do_full + st, L::kTileBytes);
+        mbar_expect_tx(do_full + st, q_bytes);
         for (int c = 0; c < kChunks; ++c)
           tma_load_3d(sdO + st * L::kTileBytes + c * L::kChunkBytes, &tmdO, do_full + st, c * 64,
-                      seq_start + qt * kBM, hq);
+                      PACKED ? hq : seq_start + qt * qtok, PACKED ? seq_start + qt * qtok : hq);
         ndo_issued = it + 1;
         if (it >= QS && !mbar_wait(q_empty + st, ph, abort_flag, p.status)) break;
-        mbar_expect_tx(q_full + st, L::kTileBytes);
+        mbar_expect_tx(q_full + st, q_bytes);
         for (int c = 0; c < kChunks; ++c)
           tma_load_3d(sQ + st * L::kTileBytes + c * L::kChunkBytes, &tmQ, q_full + st, c * 64,
-                      seq_start + qt * kBM, hq);
+                      PACKED ? hq : seq_start + qt * qtok, PACKED ? seq_start + qt * qtok : hq);
         nq_issued = it + 1;
       }
       if (abort_read(abort_flag)) {
@@ -404,7 +437,11 @@ __global__ void __launch_bounds__(512, 1)
     // past the accumulator are skipped by the map.
     for (int it = 0; it < n_it; ++it) {
       const int qt = qt0 + it % per_head;
-      const int row0 = static_cast<int>(static_cast<size_t>(hq0 + it / per_head) * N + seq_start) + qt * kBM;
+      const int hq = hq0 + it / per_head * qheads, tok0 = seq_start + qt * qtok;
+      // the tile's first row in the accumulator, and the place of its turn counter
+      const int row0 = PACKED ? 0 : static_cast<int>(static_cast<size_t>(hq0 + it / per_head) * N + seq_start) + qt * kBM;
+      const size_t turn = PACKED ? static_cast<size_t>(tok0) * p.Hq + hq : static_cast<size_t>(row0);
+      const bool drop = PACKED && (t >= qtok * qheads || qt * qtok + t / qheads >= seq_len);  // not a row of this sequence
       if (!mbar_wait_warp(dq_full, it & 1, abort_flag, p.status)) { ok = false; break; }
       if (it >= 1 && !mbar_wait_warp(stage_free, (it - 1) & 1, abort_flag, p.status)) { ok = false; break; }
       tc_fence_after();
@@ -424,6 +461,10 @@ __global__ void __launch_bounds__(512, 1)
           tc_fence_before();
           mbar_arrive_warp(dq_free);  // the dQ columns may be overwritten once everything is loaded
         }
+        if constexpr (PACKED) {
+#pragma unroll
+          for (int g = 0; g < 32; ++g) r[g] = drop ? 0u : r[g];
+        }
         uint8_t* row = (c < L::kOwnStageChunks ? sStage + c * 16384 : sdSl + (c - L::kOwnStageChunks) * 16384) + t * 128;
 #pragma unroll
         for (int g = 0; g < 8; ++g)
@@ -440,7 +481,7 @@ __global__ void __launch_bounds__(512, 1)
         // deterministic: key tile kt adds into this dQ tile after key tiles 0 .. kt-1 (the
         // tiles of the same sequence that also reach it, launched before this CTA)
         if (ok && p.deterministic) {
-          if (wait_turn(p.dq_turn + row0, kt, abort_flag, p.status))
+          if (wait_turn(p.dq_turn + turn, kt, abort_flag, p.status))
             fence_async_global();  // the reductions below come after the turn was seen
           else
             ok = false;
@@ -448,11 +489,21 @@ __global__ void __launch_bounds__(512, 1)
         if (ok) {
           if (L::kLoStageChunks > 0) {
             for (int c = L::kOwnStageChunks; c < DP / 32; ++c)
-              if (c * 32 < p.d) tma_reduce_add_2d(&tmAcc, sdSl + (c - L::kOwnStageChunks) * 16384, c * 32, row0);
+              if (c * 32 < p.d) {
+                if constexpr (PACKED)
+                  tma_reduce_add_3d(&tmAcc, sdSl + (c - L::kOwnStageChunks) * 16384, c * 32, hq, tok0);
+                else
+                  tma_reduce_add_2d(&tmAcc, sdSl + (c - L::kOwnStageChunks) * 16384, c * 32, row0);
+              }
             bulk_commit();
           }
           for (int c = 0; c < L::kOwnStageChunks; ++c)
-            if (c * 32 < p.d) tma_reduce_add_2d(&tmAcc, sStage + c * 16384, c * 32, row0);
+            if (c * 32 < p.d) {
+              if constexpr (PACKED)
+                tma_reduce_add_3d(&tmAcc, sStage + c * 16384, c * 32, hq, tok0);
+              else
+                tma_reduce_add_2d(&tmAcc, sStage + c * 16384, c * 32, row0);
+            }
           bulk_commit();
           if (L::kLoStageChunks > 0) {
             bulk_wait_read<1>();     // every group but the last: the dS lo chunks
@@ -463,7 +514,7 @@ __global__ void __launch_bounds__(512, 1)
           if (p.deterministic) {
             bulk_wait_all();       // the reductions have been performed ...
             fence_async_global();  // ... before the turn passes to key tile kt + 1
-            red_release_gpu_add(p.dq_turn + row0, 1);
+            red_release_gpu_add(p.dq_turn + turn, 1);
           }
         }
       }
@@ -531,9 +582,10 @@ __global__ void __launch_bounds__(512, 1)
     auto load_rows = [&](int it) {
       if (threadIdx.x < 128 && it < n_it) {
         const int qt = qt0 + it % per_head;
-        const size_t row_base = static_cast<size_t>(hq0 + it / per_head) * N + seq_start;
-        const int q = qt * kBM + threadIdx.x;
-        row_next = q < seq_len;
+        const int lane_head = PACKED ? static_cast<int>(threadIdx.x) % qheads : 0;
+        const size_t row_base = static_cast<size_t>(hq0 + it / per_head * qheads + lane_head) * N + seq_start;
+        const int q = qt * qtok + static_cast<int>(threadIdx.x) / qheads;
+        row_next = q < seq_len && (!PACKED || static_cast<int>(threadIdx.x) < qtok * qheads);
         const size_t r = row_base + (row_next ? q : seq_len - 1);
         lse_next = p.lse[r];
         d_next = p.delta[r];
@@ -554,6 +606,34 @@ __global__ void __launch_bounds__(512, 1)
       // ---- phase 1: P^T = exp2(S^T * scale * log2e - LSE * log2e), hi/lo back into TMEM
       if (!mbar_wait_warp(s_full, it & 1, abort_flag, p.status)) break;
       tc_fence_after();
+      // columns c < lim are masked: queries q < key - off under the causal mask (only tiles on the diagonal have any; a
+      // query row that sees no key at all has every column masked), and all 64 of a key past the sequence; the selects
+      // run only where a thread has such columns.  Packed: and columns c >= hi, rows behind the sequence's end
+      const int lim = !key_ok ? 64 : (CAUSAL ? (key - off - qt * qtok) * qheads - half * 64 : -1);
+      const int rows_held = PACKED ? min(qtok, seq_len - qt * qtok) * qheads : kBM;
+      const int hi = rows_held - half * 64;
+      if constexpr (PACKED) {
+        // S^T has been computed, so Q has landed and, behind the end, may go; dO when it has landed, too (dP^T may
+        // still read it: its columns there are not used).  K's rows behind the end, once.
+        const int st = it % QS;
+        if (rows_held < qtok * qheads) {
+          if (!mbar_wait_warp(do_full + st, (it / QS) & 1, abort_flag, p.status)) break;
+          const int vecs = (qtok * qheads - rows_held) * 8;
+          for (int i = threadIdx.x; i < kChunks * vecs; i += kEw) {
+            const int at = st * L::kTileBytes + i / vecs * L::kChunkBytes + rows_held * 128 + i % vecs * 16;
+            *reinterpret_cast<uint4*>(sQ + at) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(sdO + at) = make_uint4(0, 0, 0, 0);
+          }
+          fence_async_smem();
+        }
+        const int keys = kv_len - kt * kBN;
+        if (it == 0 && keys < kBN) {
+          const int vecs = (kBN - keys) * 8;
+          for (int i = threadIdx.x; i < kChunks * vecs; i += kEw)
+            *reinterpret_cast<uint4*>(sK + i / vecs * L::kChunkBytes + keys * 128 + i % vecs * 16) = make_uint4(0, 0, 0, 0);
+          fence_async_smem();
+        }
+      }
       float pv[64];
       {
         uint32_t r0[32], r1[32];
@@ -568,11 +648,6 @@ __global__ void __launch_bounds__(512, 1)
         // first half of the dV MMAs runs while the second part is computed.
         const float4* nl4 = reinterpret_cast<const float4*>(lse_buf + half * 64);
         const uint64_t scl = f2_pack(sl2, sl2);
-        // queries q < key - off are masked under causal (only tiles on the diagonal have any; a
-        // query row that sees no key at all has every column masked), and keys past the
-        // sequence give P = 0: the selects run only where a thread has such columns
-        // columns c < lim are masked (a key past the sequence: all 64)
-        const int lim = !key_ok ? 64 : (CAUSAL ? key - off - qt * kBM - half * 64 : -1);
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           uint32_t(&r)[32] = cc == 0 ? r0 : r1;
@@ -592,6 +667,12 @@ __global__ void __launch_bounds__(512, 1)
           if (lim > 32 * cc) {
 #pragma unroll
             for (int i = 32 * cc; i < 32 * cc + 32; ++i) pv[i] = i < lim ? 0.f : pv[i];
+          }
+          if constexpr (PACKED) {
+            if (hi < 32 * cc + 32) {
+#pragma unroll
+              for (int i = 32 * cc; i < 32 * cc + 32; ++i) pv[i] = i >= hi ? 0.f : pv[i];
+            }
           }
           uint32_t ph[16], pl[16];
 #pragma unroll
@@ -631,6 +712,12 @@ __global__ void __launch_bounds__(512, 1)
           pv[i + 1] *= __uint_as_float(r[4 * j4 + 1]) + nd.y;
           pv[i + 2] *= __uint_as_float(r[4 * j4 + 2]) + nd.z;
           pv[i + 3] *= __uint_as_float(r[4 * j4 + 3]) + nd.w;
+        }
+        if constexpr (PACKED) {  // 0 times what is behind the end
+          if (lim > 32 * h || hi < 32 * h + 32) {
+#pragma unroll
+            for (int i = 32 * h; i < 32 * h + 32; ++i) pv[i] = i < lim || i >= hi ? 0.f : pv[i];
+          }
         }
         uint4 lo[4];
 #pragma unroll
@@ -673,10 +760,10 @@ __global__ void __launch_bounds__(512, 1)
   }
 }
 
-template <typename T, int DP, bool CAUSAL>
+template <typename T, int DP, bool CAUSAL, bool PACKED = false>
 cudaError_t launch_bwd_tc_t(const BwdMaps& maps, const BwdParams& p, cudaStream_t stream) {
   using L = BwdLayout<DP>;
-  auto kern = bwd_tc_kernel<T, DP, CAUSAL>;
+  auto kern = bwd_tc_kernel<T, DP, CAUSAL, PACKED>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemAlloc);
   if (e != cudaSuccess) return e;
   // The in-kernel register split assumes the launch allocation; never launch otherwise.
@@ -684,9 +771,22 @@ cudaError_t launch_bwd_tc_t(const BwdMaps& maps, const BwdParams& p, cudaStream_
   e = cudaFuncGetAttributes(&fa, kern);
   if (e != cudaSuccess) return e;
   if (fa.numRegs != static_cast<int>(L::kLaunchRegs)) return cudaErrorInvalidConfiguration;
+  if constexpr (PACKED) {  // the number of tiles is on the device: a CTA for each that there may be
+    const long long most = packed_bound(p.N, p.nseq, p.max_seqlen, kBN) * p.Hkv;
+    if (most > 0x7fffffffLL) return cudaErrorInvalidValue;
+    kern<<<static_cast<unsigned>(most), L::kThreads, L::kSmemAlloc, stream>>>(maps.q, maps.k, maps.v, maps.dout, maps.dq_acc, p);
+    return cudaGetLastError();
+  }
   const dim3 grid(p.cu_seqlens ? p.nseq * p.Hkv : p.B * p.Hkv, p.n_ktiles);
   kern<<<grid, L::kThreads, L::kSmemAlloc, stream>>>(maps.q, maps.k, maps.v, maps.dout, maps.dq_acc, p);
   return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_bwd_packed_dtype(const BwdMaps& maps, const BwdParams& p, bool causal, cudaStream_t stream) {
+  if (p.d <= 64)
+    return causal ? launch_bwd_tc_t<T, 64, true, true>(maps, p, stream) : launch_bwd_tc_t<T, 64, false, true>(maps, p, stream);
+  return causal ? launch_bwd_tc_t<T, 128, true, true>(maps, p, stream) : launch_bwd_tc_t<T, 128, false, true>(maps, p, stream);
 }
 
 template <typename T>

@@ -1,0 +1,8 @@
+// fwd_packed_bf16.cu -- bf16 instantiations of the tcgen05 forward over packed sequences with grouped heads.
+#include "fwd_tc.cuh"
+
+namespace attn {
+cudaError_t launch_fwd_packed_bf16(const FwdMaps& maps, const FwdParams& p, bool causal, cudaStream_t stream) {
+  return launch_fwd_mode<__nv_bfloat16, kModePacked>(maps, p, causal, stream);
+}
+}  // namespace attn

@@ -48,6 +48,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <type_traits>
+#include "cache8.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -138,7 +139,19 @@ __device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int idx) {
   FwdItem it;
   it.j0 = 0;
   it.split = 0;
-  if constexpr (MODE == kModeKv || MODE == kModeKv8) {
+  if constexpr (MODE == kModePacked) {
+    const int groups = p.Hq / p.heads;
+    const int4 tile = p.tiles[idx / groups];
+    it.b = 0;
+    it.h = idx % groups;  // the item's head group: query heads [h heads, h heads + heads)
+    it.seq_start = tile.x;
+    it.seq_len = tile.y;
+    it.qt = tile.z;
+    it.valid = tile.y > 0;
+    it.n_kv = ((CAUSAL ? min(tile.y, (tile.z + 1) * p.tile_tokens) : tile.y) + kBN - 1) / kBN;
+    return it;
+  }
+  if constexpr (MODE == kModeKv || MODE == kModeKv8 || MODE == kModePaged) {
     // later row blocks first (under the causal mask they see the most keys), then the key
     // range (first ranges first: they are full, the last ones short or empty), then (batch,
     // kv head).  A CTA takes one item per round of gridDim.x items, so it gets a mix of
@@ -259,9 +272,12 @@ __global__ void __launch_bounds__(512, 1)
                   const FwdParams p, int n_items) {
   constexpr bool VARLEN = MODE == kModeVarlen;
   constexpr bool KV8 = MODE == kModeKv8;
-  constexpr bool KV = MODE == kModeKv || KV8;
-  // an 8-bit cache in one range: the items' outputs are final, written as a dense item's are
-  const bool kv_final = KV8 && p.n_splits == 1;
+  constexpr bool PAGED = MODE == kModePaged, PACKED = MODE == kModePacked;
+  constexpr bool KV = MODE == kModeKv || KV8 || PAGED;
+  // an 8-bit cache, or one in pages, in one range: the items' outputs are final, written as a dense item's are
+  const bool kv_final = (KV8 || PAGED) && p.n_splits == 1;
+  // what lies behind the last key in a tile is another sequence's, or anything: its values are set to zero
+  constexpr bool CLEAN = PAGED || PACKED;
   using PElem = std::conditional_t<KV8, Elem<__half>, Elem<T>>;  // of P and V
   // 16-bit output of a dense item, or of a varlen item whose 128 rows all lie in its
   // sequence: the epilogue warps stage the item's O tile in the item's Q slot (free once its
@@ -269,8 +285,9 @@ __global__ void __launch_bounds__(512, 1)
   // Otherwise (a varlen tile that ends past its sequence must not write into the next one; fp32
   // output or KV-cache partials) the epilogue warps store their rows themselves and the last S
   // frees the Q slot.  Every role decides per item with the same function.
-  const bool tile_out = (MODE == kModeDense || MODE == kModeVarlen || kv_final) && !p.out_f32;
+  const bool tile_out = (MODE == kModeDense || MODE == kModeVarlen || PACKED || kv_final) && !p.out_f32;
   auto tile_item = [&](const FwdItem& it) -> bool {
+    if (PACKED) return tile_out && (it.qt + 1) * p.tile_tokens <= it.seq_len;
     return tile_out && (MODE != kModeVarlen || (it.qt + 1) * kBM <= it.seq_len);
   };
   using L = FwdLayout<DP, MODE>;
@@ -354,6 +371,10 @@ __global__ void __launch_bounds__(512, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if constexpr (PACKED) {
+    dependency_wait();  // the list of tiles
+    n_items = p.head[0] * (p.Hq / p.heads);
+  }
 
   if (warp >= 8 && warp < 12) {
     regs_dec<L::kRegsIo>();
@@ -374,15 +395,32 @@ __global__ void __launch_bounds__(512, 1)
         bool q_cur = false;   // the Q of ck's item has been issued
         bool ok = true;
         unsigned long long t_idle = 0;
+        // the keys or values of key tile j of an item, a box for each of its pages; rows behind the last page keep
+        // what they hold.  A page number outside the pool loads as zeros.
+        [[maybe_unused]] auto load_pages = [&](uint8_t* tile, const CUtensorMap* map, uint64_t* bar, const FwdItem& it, int j) {
+          const int page = 1 << p.page_shift, key0 = (it.j0 + j) * kBN;
+          const int n = (min(kBN, it.seq_len - key0) + page - 1) >> p.page_shift;
+          const int32_t* ids = p.table + static_cast<size_t>(it.b) * p.M + (key0 >> p.page_shift);
+          mbar_expect_tx(bar, static_cast<uint32_t>(n) * kChunks * page * 128);
+          for (int i = 0; i < n; ++i) {
+            const int id = ids[i];
+            const bool in = id >= 0 && id < p.P;
+            if (!in) raise_status(p.status, ATTN_ERR_DEVICE_INPUT);
+            const int z = in ? id * p.Hkv + it.h : p.P * p.Hkv;
+            for (int c = 0; c < kChunks; ++c) tma_load_3d(tile + c * L::kChunkBytes + i * page * 128, map, bar, c * 64, 0, z);
+          }
+        };
         while (!ck.done || !cv.done) {
           bool progress = false;
           const uint32_t qs = nq % SQ;
           if (!ck.done && !q_cur && (nq < static_cast<uint32_t>(SQ) || mbar_test(q_empty + qs, ((nq / SQ) - 1) & 1))) {
             const FwdItem& it = ck.it;
-            mbar_expect_tx(q_full + qs, L::kTileBytes);
+            mbar_expect_tx(q_full + qs, PACKED ? kChunks * p.tile_tokens * p.heads * 128 : L::kTileBytes);
             for (int c = 0; c < kChunks; ++c) {
               uint8_t* dst = sQ + qs * L::kTileBytes + c * L::kChunkBytes;
-              if constexpr (VARLEN)
+              if constexpr (PACKED)
+                tma_load_3d(dst, &tmQ, q_full + qs, c * 64, it.h * p.heads, it.seq_start + it.qt * p.tile_tokens);
+              else if constexpr (VARLEN)
                 tma_load_4d(dst, &tmQ, q_full + qs, c * 64, it.h, 0, it.seq_start + it.qt * kBM);
               else if constexpr (KV)
                 tma_load_3d(dst, &tmQ, q_full + qs, c * 64, it.qt * kBM, it.b * p.Hkv + it.h);
@@ -397,15 +435,21 @@ __global__ void __launch_bounds__(512, 1)
             const uint32_t st = ck.t % SK;
             if (ck.t < static_cast<uint32_t>(SK) || mbar_test(k_empty + st, ((ck.t / SK) - 1) & 1)) {
               const FwdItem& it = ck.it;
+              if constexpr (PAGED) {
+                load_pages(sK + st * L::kTileBytes, &tmK, k_full + st, it, ck.j);
+              } else {
               mbar_expect_tx(k_full + st, L::kTileBytes);
               for (int c = 0; c < kChunks; ++c) {
                 uint8_t* dst = sK + st * L::kTileBytes + c * L::kChunkBytes;
-                if constexpr (VARLEN)
+                if constexpr (PACKED)
+                  tma_load_3d(dst, &tmK, k_full + st, c * 64, it.seq_start + ck.j * kBN, it.h * p.heads / p.G);
+                else if constexpr (VARLEN)
                   tma_load_4d(dst, &tmK, k_full + st, c * 64, it.h, 1, it.seq_start + ck.j * kBN);
                 else if constexpr (KV)
                   tma_load_3d(dst, &tmK, k_full + st, c * 64, (it.j0 + ck.j) * kBN, it.b * p.Hkv + it.h);
                 else
                   tma_load_3d(dst, &tmK, k_full + st, c * 64, ck.j * kBN, it.b * p.Hkv + it.h / p.G);
+              }
               }
               ck.advance(p, n_items);
               if (ck.j == 0) q_cur = false;  // the next K belongs to a new item: its Q comes first
@@ -416,15 +460,21 @@ __global__ void __launch_bounds__(512, 1)
             const uint32_t st = cv.t % SV;
             if (cv.t < static_cast<uint32_t>(SV) || mbar_test(v_empty + st, ((cv.t / SV) - 1) & 1)) {
               const FwdItem& it = cv.it;
+              if constexpr (PAGED) {
+                load_pages(sV + st * L::kTileBytes, &tmV, v_full + st, it, cv.j);
+              } else {
               mbar_expect_tx(v_full + st, L::kTileBytes);
               for (int c = 0; c < kChunks; ++c) {
                 uint8_t* dst = sV + st * L::kTileBytes + c * L::kChunkBytes;
-                if constexpr (VARLEN)
+                if constexpr (PACKED)
+                  tma_load_3d(dst, &tmV, v_full + st, c * 64, it.seq_start + cv.j * kBN, it.h * p.heads / p.G);
+                else if constexpr (VARLEN)
                   tma_load_4d(dst, &tmV, v_full + st, c * 64, it.h, 2, it.seq_start + cv.j * kBN);
                 else if constexpr (KV)
                   tma_load_3d(dst, &tmV, v_full + st, c * 64, (it.j0 + cv.j) * kBN, it.b * p.Hkv + it.h);
                 else
                   tma_load_3d(dst, &tmV, v_full + st, c * 64, cv.j * kBN, it.b * p.Hkv + it.h / p.G);
+              }
               }
               cv.advance(p, n_items);
               progress = true;
@@ -565,7 +615,8 @@ __global__ void __launch_bounds__(512, 1)
       if (idx >= n_items) continue;
       const FwdItem it = fwd_item<CAUSAL, MODE>(p, idx);
       if (!it.valid) continue;
-      const int q_row = it.qt * kBM + row;
+      // relative to the sequence (KV cache: to the R rows); packed: the row's token
+      const int q_row = PACKED ? it.qt * p.tile_tokens + row / p.heads : it.qt * kBM + row;
       kv += it.n_kv;
       if (!mbar_wait_warp(stats_ready, ic & 1, abort_flag, p.status)) { ok = false; break; }
       const float2 s0 = sStats[row], s1 = sStats[128 + row];
@@ -580,12 +631,13 @@ __global__ void __launch_bounds__(512, 1)
       const uint32_t t_last = kv - 1;
       if (!mbar_wait_warp(pv_done + (t_last & 1), (t_last >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
       tc_fence_after();
-      const bool valid = q_row < (KV ? p.R : it.seq_len);
+      const bool valid = q_row < (KV ? p.R : it.seq_len) && (!PACKED || row < p.tile_tokens * p.heads);
+      const int q_head = PACKED ? it.h * p.heads + row % p.heads : it.h;
       size_t row_off;
       // a KV cache range writes its partial output in fp32 to its slice of the split buffer
       const size_t kv_row = KV ? (static_cast<size_t>(it.split) * p.B * p.Hkv + static_cast<size_t>(it.b) * p.Hkv + it.h) * p.R + q_row : 0;
-      if constexpr (VARLEN)
-        row_off = (static_cast<size_t>(it.seq_start + q_row) * p.Hq + it.h) * p.d;
+      if constexpr (VARLEN || PACKED)
+        row_off = (static_cast<size_t>(it.seq_start + q_row) * p.Hq + q_head) * p.d;
       else if constexpr (KV)
         row_off = kv_row * p.d;
       else
@@ -663,7 +715,9 @@ __global__ void __launch_bounds__(512, 1)
           } else {
             for (int c = 0; c < kChunks; ++c) {
               const uint8_t* src = sQ + qs * L::kTileBytes + c * L::kChunkBytes;
-              if constexpr (VARLEN)  // map {d, T, H} over the [T, H, d] output
+              if constexpr (PACKED)  // map {d, H, T} over the [T, H, d] output
+                tma_store_3d(&tmO, src, c * 64, it.h * p.heads, it.seq_start + it.qt * p.tile_tokens);
+              else if constexpr (VARLEN)  // map {d, T, H} over the [T, H, d] output
                 tma_store_3d(&tmO, src, c * 64, it.seq_start + it.qt * kBM, it.h);
               else
                 tma_store_3d(&tmO, src, c * 64, it.qt * kBM, it.b * (KV ? p.Hkv : p.Hq) + it.h);
@@ -679,14 +733,37 @@ __global__ void __launch_bounds__(512, 1)
         const float lse = (KV8 && l_all > 0.f ? add_log2(mr, l_all) : mr + __log2f(l_all)) * 0.69314718055994531f;
         if constexpr (KV)
           (kv_final ? p.lse : p.lse_part)[kv_row] = lse;
-        else if constexpr (VARLEN)
-          p.lse[static_cast<size_t>(it.h) * p.total_tokens + it.seq_start + q_row] = lse;
+        else if constexpr (VARLEN || PACKED)
+          p.lse[static_cast<size_t>(q_head) * p.total_tokens + it.seq_start + q_row] = lse;
         else
           p.lse[(static_cast<size_t>(it.b) * p.Hq + it.h) * p.N + q_row] = lse;
       }
       ++ic;
     }
     if (storer) bulk_wait_all();  // the tile stores are complete before the CTA ends
+    if constexpr (PACKED) {  // rows behind the last sequence: O = 0, LSE = -inf
+      const int vecs = p.Hq * p.d * (p.out_f32 ? 4 : 2) / 16;
+      for (int tok = p.head[1] + static_cast<int>(blockIdx.x); tok < p.total_tokens; tok += static_cast<int>(gridDim.x)) {
+        uint4* const dst = static_cast<uint4*>(p.o) + static_cast<size_t>(tok) * vecs;
+        for (int i = row; i < vecs; i += 128) dst[i] = make_uint4(0, 0, 0, 0);
+        if (p.lse)
+          for (int h = row; h < p.Hq; h += 128) p.lse[static_cast<size_t>(h) * p.total_tokens + tok] = -INFINITY;
+      }
+    }
+    if constexpr (PAGED) {  // blocks of rows that see no key: O = 0, LSE = -inf
+      for (int k = 0; kv_final && k * static_cast<int>(gridDim.x) < n_items; ++k) {
+        const int idx = cta_item<MODE>(k);
+        if (idx >= n_items) continue;
+        const FwdItem it = fwd_item<CAUSAL, MODE>(p, idx);
+        if (it.valid) continue;
+        const int r0 = it.qt * kBM, rows = min(kBM, p.R - r0);
+        const size_t first = (static_cast<size_t>(it.b) * p.Hkv + it.h) * p.R + r0;
+        const int vecs = p.d * (p.out_f32 ? 4 : 2) / 16;
+        uint4* const dst = static_cast<uint4*>(p.o) + first * vecs;
+        for (int i = row; i < rows * vecs; i += 128) dst[i] = make_uint4(0, 0, 0, 0);
+        if (p.lse && row < rows) p.lse[first + row] = -INFINITY;
+      }
+    }
   } else {
     regs_inc<L::kRegsSmx>();
     // ================================================================ softmax groups
@@ -701,7 +778,8 @@ __global__ void __launch_bounds__(512, 1)
       if (idx >= n_items) continue;
       const FwdItem it = fwd_item<CAUSAL, MODE>(p, idx);
       if (!it.valid) continue;
-      const int q_row = it.qt * kBM + row;  // relative to the sequence (KV cache: to the R rows)
+      // relative to the sequence (KV cache: to the R rows); packed: the row's token
+      const int q_row = PACKED ? it.qt * p.tile_tokens + row / p.heads : it.qt * kBM + row;
       // the last key this row sees: the diagonal under the causal mask, the sequence's end;
       // for a KV cache row (query q_row % Nq) the same, aligned to the cache's last Nq keys
       int last_key;
@@ -821,6 +899,20 @@ __global__ void __launch_bounds__(512, 1)
         // pairs selected by kPolyPairs run on the FMA pipe, the rest on the special-function
         // unit; masked tiles use the latter only (exact zeros).
         const float nm = KV8 ? offset - mb : -mb;
+        if constexpr (CLEAN) {
+          // The values of this group's keys behind the last one become zeros: there P = 0, but 0 * NaN is NaN.  The
+          // tile must have landed; the PV issuers read it after this group's p_full.
+          const int held = it.seq_len - key0;  // warp-uniform
+          if (held < 64) {
+            if (!mbar_wait_warp(v_full + t % SV, (t / SV) & 1, abort_flag, p.status)) { ok = false; break; }
+            const int r0 = max(held, 0);
+            uint8_t* const vt = sV + (t % SV) * L::kTileBytes + (grp * 64 + r0) * 128;
+            const int vecs = (64 - r0) * 8;
+            for (int i = row; i < vecs * kChunks; i += 128)
+              *reinterpret_cast<uint4*>(vt + i / vecs * L::kChunkBytes + i % vecs * 16) = make_uint4(0, 0, 0, 0);
+            fence_async_smem();
+          }
+        }
         const uint64_t scl = f2_pack(sl2, sl2), nmb = f2_pack(nm, nm);
         // the sum's chains: of every fourth pair, or of the 16 keys that share an offset
         auto chain = [](int c) { return KV8 ? c / 16 : (c >> 1) & 3; };
@@ -927,8 +1019,22 @@ cudaError_t launch_fwd_tc_t(const FwdMaps& maps, const FwdParams& p, cudaStream_
   e = cudaFuncGetAttributes(&fa, kern);
   if (e != cudaSuccess) return e;
   if (fa.numRegs != static_cast<int>(L::kLaunchRegs)) return cudaErrorInvalidConfiguration;
+  if constexpr (MODE == kModePacked) {  // the number of items is on the device: `tiles` is its bound
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    const long long most = packed_bound(p.total_tokens, p.nseq, p.max_seqlen, p.tile_tokens) * (p.Hq / p.heads);
+    cfg.gridDim = dim3(static_cast<unsigned>(most < sm_count() ? most : sm_count()));
+    cfg.blockDim = dim3(L::kThreads);
+    cfg.dynamicSmemBytes = L::kSmemAlloc;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, maps.q, maps.k, maps.v, maps.o, p, 0);
+  }
   const long heads = MODE == kModeVarlen ? static_cast<long>(p.Hq) * p.nseq
-                     : (MODE == kModeKv || MODE == kModeKv8) ? static_cast<long>(p.B) * p.Hkv * p.n_splits
+                     : (MODE == kModeKv || MODE == kModeKv8 || MODE == kModePaged) ? static_cast<long>(p.B) * p.Hkv * p.n_splits
                                          : static_cast<long>(p.B) * p.Hq;
   const long items = heads * p.n_qtiles;
   if (items > 0x7fffffffL) return cudaErrorInvalidValue;
@@ -964,6 +1070,13 @@ cudaError_t launch_fwd_kv8_dtype(const FwdMaps& maps, const FwdParams& p, bool c
   if (p.d <= 64)
     return causal ? launch_fwd_tc_t<T, 64, true, kModeKv8>(maps, p, stream) : launch_fwd_tc_t<T, 64, false, kModeKv8>(maps, p, stream);
   return causal ? launch_fwd_tc_t<T, 128, true, kModeKv8>(maps, p, stream) : launch_fwd_tc_t<T, 128, false, kModeKv8>(maps, p, stream);
+}
+
+// fwd_paged_*.cu, fwd_packed_*.cu: one of the modes of its own
+template <typename T, int MODE>
+cudaError_t launch_fwd_mode(const FwdMaps& maps, const FwdParams& p, bool causal, cudaStream_t stream) {
+  if (p.d <= 64) return causal ? launch_fwd_tc_t<T, 64, true, MODE>(maps, p, stream) : launch_fwd_tc_t<T, 64, false, MODE>(maps, p, stream);
+  return causal ? launch_fwd_tc_t<T, 128, true, MODE>(maps, p, stream) : launch_fwd_tc_t<T, 128, false, MODE>(maps, p, stream);
 }
 
 }  // namespace attn

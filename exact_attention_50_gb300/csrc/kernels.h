@@ -38,6 +38,18 @@ struct FwdParams {
   const float* v_unit;
   const float* v_log;
   int n_blocks, block_shift;
+  // KV cache in pages (kModePaged): page numbers [B, M], pages of 1 << page_shift keys, P of them
+  const int32_t* table;
+  int M, P, page_shift;
+  // Packed sequences with grouped heads (kModePacked): a work item is `tile_tokens` tokens by `heads` neighbouring
+  // query heads of one kv head, row = token * heads + head; tiles (start, length, number, -) and their count, head[0],
+  // as launch_packed_tiles leaves them, tokens end at head[1]
+  const int4* tiles;
+  const int* head;
+  int heads, tile_tokens;
+  // fp32 varlen and packed forward: element strides from token to token; may tokens lie behind the last sequence
+  long long tok_q, tok_k, tok_v;
+  int open_end;
 };
 
 // KV cache: the number of leading keys that some row of 128-row block rb of a (batch, kv head)
@@ -62,7 +74,7 @@ struct FwdMaps {
 };
 
 // Work-item layouts of the forward kernels.
-constexpr int kModeDense = 0, kModeVarlen = 1, kModeKv = 2, kModeKv8 = 3;
+constexpr int kModeDense = 0, kModeVarlen = 1, kModeKv = 2, kModeKv8 = 3, kModePaged = 4, kModePacked = 5;
 
 cudaError_t launch_fwd_tc(const FwdMaps& maps, const FwdParams& p, attn_dtype_t dtype, bool causal, int mode,
                           cudaStream_t stream);
@@ -124,11 +136,17 @@ struct BwdParams {
   struct Rows {
     long long row, head;
   };
-  Rows lay_q, lay_kv, lay_o, lay_dq, lay_dkv;  // q; k and v; o and dout; dq; dk and dv
+  Rows lay_q, lay_k, lay_v, lay_o, lay_dq, lay_dkv;  // q; k; v; o and dout; dq; dk and dv
   // Varlen: the sequences are the diagonal blocks of a B = 1, N = total_tokens problem; the
   // fp32 row statistics (LSE, D) and the dQ accumulator are [H, T] ([H, T, d]).
   const int32_t* cu_seqlens;  // null for dense
   int nseq, max_seqlen;
+  int open_end;            // varlen: tokens may lie behind the last sequence
+  // Packed sequences with grouped heads: as in FwdParams, a query tile is tile_tokens tokens by `heads` query heads;
+  // the dQ accumulator is [T, Hq, d]
+  const int4* tiles;
+  const int* head;
+  int heads, tile_tokens;
 };
 
 // Tensor maps for the tcgen05 backward: 3-D {d, rows, heads} with the layout's row / head
@@ -143,6 +161,17 @@ cudaError_t launch_bwd_postprocess(const BwdParams& p, attn_dtype_t dtype, cudaS
 cudaError_t launch_bwd_tc(const BwdMaps& maps, const BwdParams& p, attn_dtype_t dtype, bool causal,
                           cudaStream_t stream);  // varlen when p.cu_seqlens is set
 cudaError_t launch_bwd_f32(const BwdParams& p, bool causal, cudaStream_t stream);
+
+// ---------------------------------------------------------------- packed sequences with grouped heads
+// The tiles of `tile` tokens that cu holds, heaviest first: at most packed_bound of them.
+long long packed_bound(int T, int nseq, int max_seqlen, int tile);
+cudaError_t launch_packed_tiles(const int32_t* cu, int nseq, int T, int max_seqlen, int tile, bool causal, bool backward, int* head, int4* tiles,
+                                unsigned* status, cudaStream_t stream);
+// Rows [*end, T) of up to three tensors become zeros, and -inf in lse [H, T] (nullable).
+cudaError_t launch_packed_tail(void* const x[3], const int row_bytes[3], float* lse, int H, int T, const int32_t* end, cudaStream_t stream);
+cudaError_t launch_fwd_packed(const FwdMaps& maps, const FwdParams& p, attn_dtype_t dtype, bool causal, cudaStream_t stream);
+cudaError_t launch_bwd_packed(const BwdMaps& maps, const BwdParams& p, attn_dtype_t dtype, bool causal, cudaStream_t stream);
+cudaError_t launch_fwd_paged(const FwdMaps& maps, const FwdParams& p, attn_dtype_t dtype, bool causal, cudaStream_t stream);
 
 // ---------------------------------------------------------------- KV caches in 8 bits, eviction
 struct AppendParams {
@@ -240,5 +269,69 @@ struct EvictParams {
   int row_bytes;           // d * sizeof(dtype), a multiple of 16
 };
 cudaError_t launch_cache_evict(const EvictParams& p, cudaStream_t stream);
+
+// ---------------------------------------------------------------- KV caches in pages
+// The books: tables [B, M] of page numbers, lengths [B], reference counts [P]; outputs may be the inputs.
+struct PagesParams {
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* refs;
+  int32_t* table_out;
+  int32_t* lens_out;       // free, fork
+  int32_t* refs_out;
+  const int32_t* arg;      // [B]: free: the tokens to keep; reserve: the new tokens
+  const int32_t* src;      // fork: [n] rows
+  const int32_t* dst;
+  int32_t* copies;         // fork: [n, 2]; compact: [P / 2, 2]: (from, to) or (-1, -1)
+  int32_t* used;           // compact: [1]
+  unsigned* status;
+  int B, M, P, n, page;
+};
+cudaError_t launch_pages_free(const PagesParams& p, cudaStream_t stream);
+cudaError_t launch_pages_fork(const PagesParams& p, cudaStream_t stream);
+cudaError_t launch_pages_reserve(const PagesParams& p, cudaStream_t stream);
+cudaError_t launch_pages_compact(const PagesParams& p, cudaStream_t stream);
+cudaError_t launch_pages_copy(void* k, void* v, const int32_t* copies, int n, int P, size_t page_bytes, unsigned* status, cudaStream_t stream);
+constexpr int kMaxTableRows = 65536;
+
+// Attention of few rows (R <= kPagedRows) over a cache in pages: rows r = g * Nq + i of a (batch, kv head) as in FwdParams.
+struct PagedParams {
+  const void* q;           // [B*Hkv, R, d]
+  const int32_t* table;    // [B, M]
+  const int32_t* cache_seqlens;
+  void* o;                 // [B*Hkv, R, d]
+  float* lse;              // [B*Hkv, R]; nullable
+  unsigned* status;
+  unsigned long long wait_ns;
+  int B, Hkv, Nq, Nk, R, d, causal, M, P, page_shift;  // Nk: the most tokens of a sequence
+  int box_shift;           // log2 of the keys of a TMA box: a page's, at most a tile's
+  float scale_log2;
+  int out_f32;
+  // as in Cache8Params
+  int ctas, runs, tile_keys, cluster;
+  float* o_part;
+  float* lse_part;
+  int2* parts;
+};
+constexpr int kPagedRows = 16;
+constexpr int paged_tile_keys(int d) { return d <= 64 ? 32 : 16; }
+constexpr int paged_ctas_per_sm(int row_blocks) { return row_blocks == 1 ? 3 : 2; }
+// maps {d, page, P*Hkv} with boxes of {64, 1 << box_shift}
+cudaError_t launch_paged_fwd(const CUtensorMap& k, const CUtensorMap& v, const PagedParams& p, attn_dtype_t dtype, cudaStream_t stream);
+cudaError_t launch_paged_none(const PagedParams& p, cudaStream_t stream);
+
+struct PagesAppendParams {
+  uint4* k;                // [P, Hkv, page, row_vecs]
+  uint4* v;
+  const uint4* k_new;      // token t at t * k_stride (16-byte vectors)
+  const uint4* v_new;
+  size_t k_stride, v_stride;
+  const int32_t* table;    // [B, M]
+  const int32_t* cu;       // [B + 1]
+  const int32_t* lens;     // [B]; nullable: 0 each
+  unsigned* status;
+  int T, B, M, P, Hkv, page, row_vecs;
+};
+cudaError_t launch_pages_append(const PagesAppendParams& p, cudaStream_t stream);
 
 }  // namespace attn

@@ -1,0 +1,493 @@
+// paged_fwd.cu -- attention of few query rows (decode, drafts) over a 16-bit KV cache in pages: HBM-bound, each
+// key and value is read once.
+//
+// A row r is query i = r % Nq of head g = r / Nq of a kv head's group, R = G Nq rows share its keys:
+//   s_j = scale q . k_j, masked;  l = sum_j exp(s_j - m);  o = sum_j exp(s_j - m) v_j / l.
+//
+// Work: tiles of 16 keys (32 for 64 columns; 8 kB of K and V) of all (batch, kv head) pairs, dealt in equal runs to
+// the workers, one warp each (kv_runs.cuh); small problems take a cluster of CTAs per pair, whose workers join their
+// sums through distributed shared memory.  A worker keeps its own ring of tiles full with TMA boxes of at most a
+// page's rows, swizzled; the page numbers of the next tile are read while the present one is computed.
+//
+// Behind a cache's end a page may hold anything, NaN included, which a weight of zero does not cancel.  So the last
+// box of a cache is placed to end with the cache's last key: its first rows are earlier keys of the page, or lie in
+// front of it and load as zeros.  Boxes behind it, and those of a page number outside the pool, lie outside the map
+// and load as zeros.
+//
+// mma.sync.m16n8k16, keys (or columns of V) as the 16 rows and query rows as the 8 columns: S^T = K Q^T,
+// O^T = V^T P^T.  A tcgen05 product has at least 64 rows, of which the few queries of a decode fill 4; here they
+// fill half.  P goes through the product in two 16-bit halves, round16(p) and round16(p - that): the rounding of P
+// leaves nothing beside that of the outputs, and the tensor pipe has the time.
+#include <cooperative_groups.h>
+#include "kv_runs.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr float kLazy = 8.0f;  // log2 units by which a tile's maximum may exceed the running one
+
+// NB: blocks of 8 query rows per warp, 1 or 2.
+template <int DP, int NB>
+struct Layout {
+  static constexpr int kKeys = paged_tile_keys(DP);
+  static constexpr int kGroups = kKeys / 16;
+  static constexpr int kCtas = paged_ctas_per_sm(NB);
+  static constexpr int kChunk = kKeys * 128;                  // 64 columns of a tile
+  static constexpr int kTile = kKeys * DP * 2;                // bytes of K or V
+  static constexpr int kStage = 2 * kTile;
+  static constexpr int kStages = NB == 1 ? 2 : 3;             // per warp: 64 or 96 kB a CTA
+  static constexpr int kOffBar = kWarps * kStages * kStage;
+  static constexpr int kOffMisc = kOffBar + kWarps * kStages * 8;  // pad, abort flag, wait limit
+  static constexpr int kBytes = kOffMisc + 16;
+  static_assert((kBytes + 1024) * kCtas <= 228 * 1024, "shared memory of an SM");
+  static_assert(kOffBar % 8 == 0 && kOffMisc % 16 == 0, "alignment");
+};
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+__device__ __forceinline__ float2 unpack(const __half*, uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+__device__ __forceinline__ float2 unpack(const __nv_bfloat16*, uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+
+// SPREAD: a cluster of CTAs per pair, whose workers take its tiles in turn; no workspace and no second kernel.
+template <typename T, int DP, int NB, bool SPREAD>
+__global__ void __launch_bounds__(kThreads, (Layout<DP, NB>::kCtas))
+    paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
+  using L = Layout<DP, NB>;
+  constexpr int kKeys = L::kKeys, kGroups = L::kGroups;
+  constexpr int kSteps = DP / 16;  // contraction steps of K Q^T, and 16-column blocks of V
+  constexpr uint32_t kStages = L::kStages;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {  // the swizzle needs aligned tiles
+    if (threadIdx.x == 0) raise_status(p.status, ATTN_ERR_CUDA);
+    return;
+  }
+  const T* const tag = nullptr;
+  const uint32_t abort_flag = smem_u32(smem + L::kOffMisc + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* const ring = smem + warp * kStages * L::kStage;
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + L::kOffBar) + warp * kStages;
+  if (threadIdx.x == 0) {
+    uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+    for (int i = 0; i < kWarps * L::kStages; ++i) mbar_init(bars + i, 1);
+    abort_set(abort_flag, 0);
+    wait_limit_set(abort_flag, p.wait_ns);
+    mbar_init_fence();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  __syncthreads();
+  if (!SPREAD) dependents_launch();
+  const int run = blockIdx.x * kWarps + warp;
+  const int stride = SPREAD ? p.cluster * kWarps : 1;  // from a worker's tile of a pair to its next
+  Deal deal{};
+  Walk w;
+  if constexpr (SPREAD) {
+    const int bh = blockIdx.x / p.cluster;
+    w.b = bh / p.Hkv;
+    w.h = bh % p.Hkv;
+    w.j = run % stride;
+    const int len = cache_len(p.cache_seqlens, w.b, p.Nk, p.status, w.h == 0 && w.j == 0 && lane == 0);
+    w.nt = (len + kKeys - 1) / kKeys;
+    w.t = w.j;
+    w.end = w.nt;
+  } else {
+    deal_and_find(p, p.runs, run, deal, w);
+  }
+
+  // ---- the copies of the run's next tile, into the stage of its number.  A tile is kKeys / box boxes of p.box
+  // rows (a power of two, at most a page's), one lane's each.
+  const int boxes = kKeys >> p.box_shift;
+  Walk ahead = w;
+  uint32_t issued = 0;
+  bool ok = true;
+  int page = 0;  // this lane's box of the next tile: its page's number
+  auto look_up = [&]() {
+    if (ahead.t < ahead.end && lane < boxes) {
+      const int key = ahead.j * kKeys + (lane << p.box_shift);
+      const int slot = key >> p.page_shift;
+      page = slot < p.M ? p.table[static_cast<size_t>(ahead.b) * p.M + slot] : -1;
+    }
+  };
+  look_up();
+  auto issue = [&]() {
+    if (ahead.t >= ahead.end) return;
+    const uint32_t st = issued % kStages;
+    if (lane == 0) mbar_expect_tx(full + st, L::kStage);
+    __syncwarp();
+    if (lane < boxes) {
+      const int len = cache_len(p.cache_seqlens, ahead.b, p.Nk, nullptr, false);
+      const int key = ahead.j * kKeys + (lane << p.box_shift);
+      int z = p.P * p.Hkv, row = 0;  // outside the pool: zeros
+      if (key < len) {
+        const int here = min(len - key, 1 << p.box_shift);
+        row = (key & ((1 << p.page_shift) - 1)) + here - (1 << p.box_shift);
+        if (page >= 0 && page < p.P) z = page * p.Hkv + ahead.h;
+        else raise_status(p.status, ATTN_ERR_DEVICE_INPUT);
+      }
+      uint8_t* const dst = ring + st * L::kStage + (lane << p.box_shift) * 128;
+#pragma unroll
+      for (int c = 0; c < DP / 64; ++c) tma_load_3d(dst + c * L::kChunk, &tmK, full + st, c * 64, row, z);
+#pragma unroll
+      for (int c = 0; c < DP / 64; ++c) tma_load_3d(dst + L::kTile + c * L::kChunk, &tmV, full + st, c * 64, row, z);
+    }
+    __syncwarp();
+    ++issued;
+    if (SPREAD) {
+      ahead.t = ahead.j += stride;
+    } else if (ahead.j + 1 < ahead.nt) {
+      ++ahead.t;
+      ++ahead.j;
+    } else {
+      ahead.next(p);  // the pair's last tile: its part is this one
+    }
+    look_up();
+  };
+  for (uint32_t i = 0; i < kStages; ++i) issue();
+
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t tiles = smem_u32(ring);
+  // ldmatrix: this lane's row address within a 16 x 16 block, as K's (non-transposed) and as V's
+  const int mat = lane >> 3, mrow = lane & 7;
+  const uint32_t k_row = ((mat & 1) * 8 + mrow) * 128, v_row = ((mat >> 1) * 8 + mrow) * 128;
+  const int k_gran = mat >> 1, v_gran = mat & 1;
+  uint32_t n = 0;  // tiles of the run passed
+  for (; SPREAD || (ok && w.t < w.end); w.next(p)) {
+    const int len = cache_len(p.cache_seqlens, w.b, p.Nk, nullptr, false);
+    const size_t bh = static_cast<size_t>(w.b) * p.Hkv + w.h;
+    const int part = SPREAD ? (max(w.nt - w.j, 0) + stride - 1) / stride : w.part();
+    // ---- Q as B fragments: step s holds columns 16 s + 2 t (+ 1, + 8, + 9) of row 8 b + g
+    uint32_t qb[NB][kSteps][2];
+    int last[NB][2];  // the last key that this thread's rows 8 b + 2 t + e see
+    {
+      const T* q = static_cast<const T*>(p.q) + bh * p.R * p.d;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int r = 8 * b + g;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int c = 16 * s + 8 * e + 2 * t;
+            qb[b][s][e] = r < p.R && c < p.d ? *reinterpret_cast<const uint32_t*>(q + static_cast<size_t>(r) * p.d + c) : 0u;
+          }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = (8 * b + 2 * t + e) % p.Nq;
+          last[b][e] = p.causal ? min(len - p.Nq + i, len - 1) : len - 1;
+        }
+      }
+    }
+    float o[kSteps][NB][4];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) o[i][b][0] = o[i][b][1] = o[i][b][2] = o[i][b][3] = 0.f;
+    float m[NB][2], l[NB][2];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      m[b][0] = m[b][1] = -INFINITY;
+      l[b][0] = l[b][1] = 0.f;
+    }
+    for (int x = 0; x < part; ++x, ++n) {
+      const uint32_t st = n % kStages;
+      if (!ok || !mbar_wait_warp(full + st, (n / kStages) & 1, abort_flag, p.status)) { ok = false; break; }
+      const uint32_t kt = tiles + st * L::kStage, vt = kt + L::kTile;
+      const int j = w.j + x * stride, key0 = j * kKeys;
+      // ---- S^T = K Q^T: blocks of 16 keys
+      float s[kGroups][NB][4];
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) s[i][b][0] = s[i][b][1] = s[i][b][2] = s[i][b][3] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks)
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+          uint32_t a[4];
+          ldsm4(kt + (ks >> 2) * L::kChunk + i * 2048 + k_row + (((2 * (ks & 3) + k_gran) ^ mrow) << 4), a);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) mma16816<T>(s[i][b], a, qb[b][ks][0], qb[b][ks][1]);
+        }
+      // ---- scale, mask, running maximum
+      // In the cache's last tile a box may be placed `shift` rows early (see the head): slots [s0, s0 + shift) hold
+      // keys that the ones before have, or none, and the slots behind hold key slot - shift.
+      int s0 = kKeys, shift = 0;
+      if (j == w.nt - 1) {
+        const int held = len - key0;  // 1 .. kKeys
+        s0 = (held - 1) >> p.box_shift << p.box_shift;
+        shift = (1 << p.box_shift) - (held - s0);
+      }
+      bool move = false;
+      float mx[NB][2];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[i][b][e] *= p.scale_log2;
+        if (shift || __any_sync(0xffffffffu, key0 + kKeys - 1 > min(last[b][0], last[b][1]))) {
+#pragma unroll
+          for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int slot = i * 16 + e * 8 + g;
+              int key = slot;
+              if (slot >= s0) key = slot < s0 + shift ? 0x40000000 : slot - shift;
+              key += key0;
+              if (key > last[b][0]) s[i][b][2 * e] = -INFINITY;
+              if (key > last[b][1]) s[i][b][2 * e + 1] = -INFINITY;
+            }
+        }
+        mx[b][0] = mx[b][1] = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+          mx[b][0] = max3f(mx[b][0], s[i][b][0], s[i][b][2]);
+          mx[b][1] = max3f(mx[b][1], s[i][b][1], s[i][b][3]);
+        }
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+          mx[b][0] = fmaxf(mx[b][0], __shfl_xor_sync(0xffffffffu, mx[b][0], d));
+          mx[b][1] = fmaxf(mx[b][1], __shfl_xor_sync(0xffffffffu, mx[b][1], d));
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) move |= mx[b][e] > m[b][e] + kLazy || (m[b][e] == -INFINITY && mx[b][e] != -INFINITY);
+      }
+      if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          float a[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float top = fmaxf(m[b][e], mx[b][e]);
+            a[e] = m[b][e] == top ? 1.f : m[b][e] == -INFINITY ? 0.f : ex2_approx(m[b][e] - top);
+            m[b][e] = top;
+            l[b][e] *= a[e];
+          }
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
+            o[i][b][0] *= a[0]; o[i][b][1] *= a[1]; o[i][b][2] *= a[0]; o[i][b][3] *= a[1];
+          }
+        }
+      }
+      // ---- P = exp2(S - m), its sum, and B fragments of its two halves
+      uint32_t ph[kGroups][NB][2], pl[kGroups][NB][2];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const float n0 = m[b][0] == -INFINITY ? 0.f : m[b][0], n1 = m[b][1] == -INFINITY ? 0.f : m[b][1];
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float e0 = ex2_approx(s[i][b][2 * e] - n0), e1 = ex2_approx(s[i][b][2 * e + 1] - n1);
+            l[b][0] += e0;
+            l[b][1] += e1;
+            const uint32_t hi = pack2(tag, e0, e1);
+            const float2 back = unpack(tag, hi);
+            ph[i][b][e] = transpose8x8(hi);
+            pl[i][b][e] = transpose8x8(pack2(tag, e0 - back.x, e1 - back.y));
+          }
+      }
+      // ---- O^T += V^T P^T: blocks of 16 columns and 16 keys
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+        for (int c = 0; c < kSteps; ++c) {
+          uint32_t a[4];
+          ldsm4t(vt + (c >> 2) * L::kChunk + i * 2048 + v_row + (((2 * (c & 3) + v_gran) ^ mrow) << 4), a);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            mma16816<T>(o[c][b], a, ph[i][b][0], ph[i][b][1]);
+            mma16816<T>(o[c][b], a, pl[i][b][0], pl[i][b][1]);
+          }
+        }
+      __syncwarp();  // every lane has read the tile: the next one into its stage
+      issue();
+    }
+    if (!SPREAD && !ok) break;
+    // ---- this warp's part: sums over the eight lanes that share a row, the output normalised
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      float il[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], d);
+        il[e] = l[b][e] == 0.f ? 0.f : 1.f / l[b][e];
+      }
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        o[i][b][0] *= il[0]; o[i][b][1] *= il[1]; o[i][b][2] *= il[0]; o[i][b][3] *= il[1];
+      }
+    }
+    // thread (g, t): column 16 i + 8 c + g of row 8 b + 2 t + e is o[i][b][2 c + e]
+    if constexpr (SPREAD) {
+      // ---- the workers' parts in their CTAs' shared memory (the ring, read to its end), then every thread of the
+      // cluster sums some outputs over them
+      const auto cluster = cooperative_groups::this_cluster();
+      const int rank = blockIdx.x % p.cluster, workers = min(stride, w.nt);  // those with a tile
+      constexpr int kRows = 8 * NB;
+      float* const part_o = reinterpret_cast<float*>(smem);                               // [kWarps][kRows][DP]
+      float2* const part_ml = reinterpret_cast<float2*>(smem + kWarps * kRows * DP * 4);  // [kWarps][kRows]
+      float2* const all_ml = part_ml + kWarps * kRows;                                    // [workers][kRows]
+      static_assert(kWarps * kRows * DP * 4 + 9 * kWarps * kRows * 8 <= L::kOffBar, "the parts lie in the ring");
+      if (!ok || abort_read(abort_flag))  // let the copies land before their stages are written
+        for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i) mbar_drain(full + i % kStages, (i / kStages) & 1);
+      __syncthreads();
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * b + 2 * t + e;
+          if (g == 0) part_ml[warp * kRows + r] = make_float2(m[b][e], l[b][e]);
+          float* const dst = part_o + (warp * kRows + r) * DP + g;
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
+            dst[16 * i] = o[i][b][e];
+            dst[16 * i + 8] = o[i][b][2 + e];
+          }
+        }
+      cluster.sync();
+      for (int i = threadIdx.x; i < workers * kRows; i += kThreads) {
+        const int k = i / kRows;
+        all_ml[i] = *cluster.map_shared_rank(part_ml + (k % kWarps) * kRows + i % kRows, k / kWarps);
+      }
+      __syncthreads();
+      const int half = p.d / 2;
+      for (int i = rank * kThreads + threadIdx.x; i < p.R * half; i += p.cluster * kThreads) {
+        const int r = i / half, c = i % half * 2;
+        float top = -INFINITY;
+        for (int k = 0; k < workers; ++k) top = fmaxf(top, all_ml[k * kRows + r].x);
+        float sum = 0.f, x = 0.f, y = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < workers; ++k) {
+          const float2 ml = all_ml[k * kRows + r];
+          const float2 v = *reinterpret_cast<const float2*>(cluster.map_shared_rank(part_o + ((k % kWarps) * kRows + r) * DP + c, k / kWarps));
+          const float a = ml.y * (ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top));
+          sum += a;
+          x += v.x * a;
+          y += v.y * a;
+        }
+        const float il = sum == 0.f ? 0.f : 1.f / sum;
+        const size_t row = bh * p.R + r;
+        if (p.out_f32)
+          *reinterpret_cast<float2*>(static_cast<float*>(p.o) + row * p.d + c) = make_float2(x * il, y * il);
+        else
+          *reinterpret_cast<uint32_t*>(static_cast<T*>(p.o) + row * p.d + c) = pack2(tag, x * il, y * il);
+        if (c == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
+      }
+      cluster.sync();  // the others may still read this CTA's parts
+      return;
+    }
+    // ---- the pair's output, or this run's part of it
+    {
+      const bool whole = part == w.nt;
+      // a run's first part may begin inside a pair (slot 0), another one ends inside it (slot 1)
+      const size_t slot = static_cast<size_t>(run) * 2 + (w.j > 0 ? 0 : 1);
+      // for the merge: the pair's first run and its number of runs
+      if (w.j == 0 && lane == 0) p.parts[bh] = make_int2(run, whole ? 0 : deal.holder(w.t + w.nt - 1) - run + 1);
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * b + 2 * t + e;
+          if (r >= p.R) continue;
+          const float lse2 = l[b][e] == 0.f ? -INFINITY : m[b][e] + __log2f(l[b][e]);
+          const size_t row = whole ? bh * p.R + r : slot * p.R + r;
+          if (g == 0) {
+            if (!whole) p.lse_part[row] = lse2;
+            else if (p.lse) p.lse[row] = lse2 * 0.69314718055994531f;
+          }
+#pragma unroll
+          for (int i = 0; i < 2 * kSteps; ++i) {
+            const int col = 8 * i + g;
+            const float y = o[i >> 1][b][2 * (i & 1) + e];
+            if (col >= p.d) continue;
+            if (!whole) p.o_part[row * p.d + col] = y;
+            else if (p.out_f32) static_cast<float*>(p.o)[row * p.d + col] = y;
+            else static_cast<T*>(p.o)[row * p.d + col] = static_cast<T>(y);
+          }
+        }
+    }
+  }
+  if (!ok || abort_read(abort_flag))  // let the copies land before the shared memory goes away
+    for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i) mbar_drain(full + i % kStages, (i / kStages) & 1);
+  // ---- batches without a key: O = 0, LSE = -inf, nothing to merge; dealt to the CTAs
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (cache_len(p.cache_seqlens, b, p.Nk, p.status, threadIdx.x == 0) > 0) continue;
+    const size_t rows = static_cast<size_t>(p.Hkv) * p.R;
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.o) + b * rows * p.d * (p.out_f32 ? 4 : 2));
+    const size_t n16 = rows * p.d * (p.out_f32 ? 4 : 2) / 16;
+    for (size_t i = threadIdx.x; i < n16; i += kThreads) dst[i] = make_uint4(0, 0, 0, 0);
+    if (p.lse)
+      for (size_t i = threadIdx.x; i < rows; i += kThreads) p.lse[b * rows + i] = -INFINITY;
+    for (int i = threadIdx.x; i < p.Hkv; i += kThreads) p.parts[static_cast<size_t>(b) * p.Hkv + i] = make_int2(0, 0);
+  }
+}
+
+template <typename T, int DP, int NB, bool SPREAD>
+cudaError_t run(const CUtensorMap& k, const CUtensorMap& v, const PagedParams& p, cudaStream_t stream) {
+  using L = Layout<DP, NB>;
+  auto kern = paged_kernel<T, DP, NB, SPREAD>;
+  static std::atomic<unsigned long long> ready{0};  // devices on which the kernel is set up
+  cudaError_t e = once_per_device(ready, [&] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  });
+  if (e != cudaSuccess) return e;
+  if (SPREAD) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = p.cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(p.ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = L::kBytes;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, k, v, p);
+  }
+  kern<<<p.ctas, kThreads, L::kBytes, stream>>>(k, v, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return p.out_f32 ? launch_merge<float>(p, stream) : launch_merge<T>(p, stream);
+}
+
+template <typename T>
+cudaError_t run_t(const CUtensorMap& k, const CUtensorMap& v, const PagedParams& p, cudaStream_t stream) {
+  const bool few = p.R <= 8, spread = p.cluster != 0;
+  if (p.d <= 64) {
+    if (few) return spread ? run<T, 64, 1, true>(k, v, p, stream) : run<T, 64, 1, false>(k, v, p, stream);
+    return spread ? run<T, 64, 2, true>(k, v, p, stream) : run<T, 64, 2, false>(k, v, p, stream);
+  }
+  if (few) return spread ? run<T, 128, 1, true>(k, v, p, stream) : run<T, 128, 1, false>(k, v, p, stream);
+  return spread ? run<T, 128, 2, true>(k, v, p, stream) : run<T, 128, 2, false>(k, v, p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_none(const PagedParams& p, cudaStream_t stream) { return launch_none(p, stream); }
+
+cudaError_t launch_paged_fwd(const CUtensorMap& k, const CUtensorMap& v, const PagedParams& p, attn_dtype_t dtype, cudaStream_t stream) {
+  return dtype == ATTN_F16 ? run_t<__half>(k, v, p, stream) : run_t<__nv_bfloat16>(k, v, p, stream);
+}
+
+}  // namespace attn

@@ -1,0 +1,539 @@
+// pages.cu -- the books of a KV cache in pages, and the copies that they ask for.
+//
+// A table row holds a sequence's page numbers in order, then negative entries; refs[p] counts the rows that
+// hold page p (0: free).  Each call reads one state (table, lengths, counts) and writes another, which may
+// be the same arrays, in one launch of a single cluster: its CTAs agree through their shared memory and
+// cluster barriers, so nothing is left to a second launch and no workspace is needed.
+//   free     rows cut to ceil(keep / page) pages
+//   fork     a row shares another's full pages; its last, partly filled page is to be copied to a free one
+//   reserve  free pages appended to rows
+//   compact  the k-th used page behind the first U takes the k-th free place among them (U: pages in use)
+// Free pages are taken in ascending order, so the outcome is a function of the state alone.
+//
+// The r-th free page: every thread counts the free pages of its own segment of refs, one scan over the
+// cluster's threads gives each segment's first rank, and who wants page r finds the segment by bisection and
+// walks it.  Integer work on a few kB: what bounds it is the chain of barriers and L2 reads, not bytes.
+#include <cooperative_groups.h>
+#include <algorithm>
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace attn {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 1024;
+constexpr int kMaxCluster = 8;
+
+// Exclusive sum over the CTA's threads; total gets the sum of all.  s_warp: 33 ints of shared memory.
+__device__ __forceinline__ int block_scan(int x, int* s_warp, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int y = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int z = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) y += z;
+  }
+  __syncthreads();  // s_warp may still be read from the scan before
+  if (lane == 31) s_warp[warp] = y;
+  __syncthreads();
+  if (warp == 0) {
+    const int w = s_warp[lane];
+    int v = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += z;
+    }
+    s_warp[lane] = v - w;
+    if (lane == 31) s_warp[32] = v;
+  }
+  __syncthreads();
+  total = s_warp[32];
+  return s_warp[warp] + y - x;
+}
+
+// What the CTAs of the cluster keep in shared memory.
+struct Shared {
+  int warp[33];
+  int mine;             // this CTA's part of the sum that is being joined
+  int mine2;
+  int first[kThreads];  // the number of counted pages before each of this CTA's threads' segments, within the CTA
+};
+
+struct Team {  // the cluster
+  cg::cluster_group cl;
+  int n, rank, tid, threads;
+  __device__ __forceinline__ Team() : cl(cg::this_cluster()) {
+    n = static_cast<int>(cl.num_blocks());
+    rank = static_cast<int>(cl.block_rank());
+    tid = rank * kThreads + static_cast<int>(threadIdx.x);
+    threads = n * kThreads;
+  }
+  // every thread: this CTA's value x (uniform) -> the sum of the CTAs before this one; total: of all
+  __device__ __forceinline__ int before(int* slot, int x, int& total) {
+    if (threadIdx.x == 0) *slot = x;
+    cl.sync();
+    int b = 0;
+    total = 0;
+    for (int i = 0; i < n; ++i) {
+      const int y = *cl.map_shared_rank(slot, i);
+      if (i < rank) b += y;
+      total += y;
+    }
+    return b;
+  }
+};
+
+// The pages counted by `which` (free or used), as ranks: see the head of the file.
+struct Ranks {
+  int seg;              // pages of a thread's segment
+  int total;            // counted pages
+  int base[kMaxCluster];
+  template <typename F>
+  __device__ __forceinline__ void count(Team& t, Shared& s, int P, F which) {
+    seg = (P + t.threads - 1) / t.threads;
+    const long long lo = static_cast<long long>(t.tid) * seg, hi = min(static_cast<long long>(P), lo + seg);
+    int c = 0;
+    for (long long i = lo; i < hi; ++i) c += which(static_cast<int>(i)) ? 1 : 0;
+    int all;
+    s.first[threadIdx.x] = block_scan(c, s.warp, all);
+    (void)t.before(&s.mine, all, total);
+    for (int i = 0, b = 0; i < kMaxCluster; ++i) {
+      base[i] = b;
+      if (i < t.n) b += *t.cl.map_shared_rank(&s.mine, i);
+    }
+  }
+  // the counted page of rank r, 0 <= r < total
+  template <typename F>
+  __device__ __forceinline__ int select(Team& t, Shared& s, int P, int r, F which) const {
+    int c = 0;
+    while (c + 1 < t.n && base[c + 1] <= r) ++c;
+    const int* first = t.cl.map_shared_rank(s.first, c);
+    int left = r - base[c], lo = 0, hi = kThreads - 1;  // the last thread with first <= left
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first[mid] <= left) lo = mid; else hi = mid - 1;
+    }
+    left -= first[lo];
+    long long i = (static_cast<long long>(c) * kThreads + lo) * seg;
+    for (; i < P; ++i)
+      if (which(static_cast<int>(i)) && left-- == 0) break;
+    return static_cast<int>(i);
+  }
+  // the counted pages before page i
+  template <typename F>
+  __device__ __forceinline__ int rank(Team& t, Shared& s, int i, F which) const {
+    const int g = i / seg, c = g / kThreads;
+    int r = base[c] + *t.cl.map_shared_rank(s.first + g % kThreads, c);
+    for (int j = g * seg; j < i; ++j) r += which(j) ? 1 : 0;
+    return r;
+  }
+};
+
+__device__ __forceinline__ void copy_ints(const Team& t, const int32_t* in, int32_t* out, long long n) {
+  if (in == out) return;
+  for (long long i = t.tid; i < n; i += t.threads) out[i] = in[i];
+}
+
+__device__ __forceinline__ long long pages_of(long long tokens, int page) { return (tokens + page - 1) / page; }
+
+// -------------------------------------------------------------------------------------- free
+__global__ void __launch_bounds__(kThreads) pages_free_kernel(const PagesParams p) {
+  Team t;
+  copy_ints(t, p.refs, p.refs_out, p.P);
+  t.cl.sync();
+  const int lane = threadIdx.x & 31;
+  for (int b = t.tid >> 5; b < p.B; b += t.threads >> 5) {
+    const int L = p.lens[b], keep = p.arg[b];
+    const bool bad = L < 0 || keep < 0;
+    const int kept = bad ? L : min(L, keep);
+    if (bad && lane == 0) raise_status(p.status, ATTN_ERR_DEVICE_INPUT);
+    const long long stay = bad ? p.M : pages_of(kept, p.page);
+    __syncwarp();
+    for (int i = lane; i < p.M; i += 32) {
+      const size_t at = static_cast<size_t>(b) * p.M + i;
+      int e = p.table[at];
+      if (i >= stay && e >= 0) {
+        if (e < p.P) atomicSub(p.refs_out + e, 1);
+        else raise_status(p.status, ATTN_ERR_DEVICE_INPUT);
+        e = -1;
+      }
+      p.table_out[at] = e;
+    }
+    if (lane == 0) p.lens_out[b] = kept;
+  }
+}
+
+// -------------------------------------------------------------------------------------- fork
+// Pairs are dealt to the CTAs in contiguous parts, a thread each.  Of several pairs with one dst the first
+// counts: the dst rows' first pairs stand in a table spread over the CTAs' shared memory.
+__global__ void __launch_bounds__(kThreads) pages_fork_kernel(const PagesParams p) {
+  extern __shared__ int dyn[];
+  __shared__ Shared s;
+  Team t;
+  const int rows = (p.B + t.n - 1) / t.n, part = (p.n + t.n - 1) / t.n;
+  int* const owner = dyn;             // [rows]: of dst rows rank, rank + n, ...
+  int* const fresh = owner + rows;    // [part]: the copy's page; -1: none; -2: the pair is refused
+  int* const len = fresh + part;      // [part]
+  for (int i = threadIdx.x; i < rows; i += kThreads) owner[i] = 0x7fffffff;
+  copy_ints(t, p.table, p.table_out, static_cast<long long>(p.B) * p.M);
+  copy_ints(t, p.lens, p.lens_out, p.B);
+  copy_ints(t, p.refs, p.refs_out, p.P);
+  t.cl.sync();
+  const int k0 = min(p.n, t.rank * part), k1 = min(p.n, k0 + part);
+  for (int k = k0 + threadIdx.x; k < k1; k += kThreads) {
+    const int dst = p.dst[k];
+    if (dst >= 0 && dst < p.B) atomicMin(t.cl.map_shared_rank(owner + dst / t.n, dst % t.n), k);
+  }
+  const int32_t* const refs = p.refs;  // counted before any of them changes
+  const auto is_free = [refs](int i) { return refs[i] <= 0; };
+  Ranks ranks;
+  ranks.count(t, s, p.P, is_free);  // (its barrier: the owners are complete)
+  int done = 0;  // tails of this CTA's pairs so far
+  int want = 0;
+  // pass 0 counts this CTA's tails, pass 1 gives them their pages
+  for (int pass = 0; pass < 2; ++pass) {
+    int base = 0;
+    if (pass == 1) base = t.before(&s.mine2, done, want);
+    done = 0;
+    for (int q0 = k0; q0 < k1; q0 += kThreads) {
+      const int k = q0 + static_cast<int>(threadIdx.x);
+      bool ok = false, tail = false;
+      int L = 0;
+      if (k < k1) {
+        const int src = p.src[k], dst = p.dst[k];
+        ok = src >= 0 && src < p.B && dst >= 0 && dst < p.B;
+        if (ok) {
+          L = p.lens[src];
+          ok = *t.cl.map_shared_rank(owner + dst / t.n, dst % t.n) == k && p.lens[dst] == 0 && L >= 0 && pages_of(L, p.page) <= p.M;
+          if (ok && p.M > 0) ok = p.table[static_cast<size_t>(dst) * p.M] < 0;
+          if (ok && L > 0) {
+            const int e = p.table[static_cast<size_t>(src) * p.M + (L - 1) / p.page];
+            ok = e >= 0 && e < p.P;
+          }
+        }
+        tail = ok && L % p.page != 0;
+      }
+      int all;
+      const int r = block_scan(tail ? 1 : 0, s.warp, all);
+      if (pass == 1 && k < k1) {
+        const int at = base + done + r;
+        int f = ok ? -1 : -2;
+        if (tail) f = at < ranks.total ? ranks.select(t, s, p.P, at, is_free) : -2;
+        fresh[k - k0] = f;
+        len[k - k0] = L;
+        if (f == -2) raise_status(p.status, ATTN_ERR_DEVICE_INPUT);
+      }
+      done += all;
+    }
+  }
+  t.cl.sync();  // every page has been chosen and every length read: the state may change
+  const int lane = threadIdx.x & 31;
+  for (int k = k0 + (threadIdx.x >> 5); k < k1; k += kThreads / 32) {
+    const int f = fresh[k - k0], L = len[k - k0];
+    if (f == -2) {
+      if (lane < 2) p.copies[2 * static_cast<size_t>(k) + lane] = -1;
+      continue;
+    }
+    const size_t src = static_cast<size_t>(p.src[k]) * p.M, dst = static_cast<size_t>(p.dst[k]) * p.M;
+    const int full = L / p.page;
+    for (int i = lane; i < p.M; i += 32) {
+      int e = -1;
+      if (i < full) {
+        e = p.table[src + i];
+        if (e >= 0 && e < p.P) atomicAdd(p.refs_out + e, 1);
+        else raise_status(p.status, ATTN_ERR_DEVICE_INPUT);
+      } else if (i == full && f >= 0) {
+        e = f;
+      }
+      p.table_out[dst + i] = e;
+    }
+    if (lane == 0) {
+      p.lens_out[p.dst[k]] = L;
+      if (f >= 0) p.refs_out[f] = 1;
+      p.copies[2 * static_cast<size_t>(k)] = f >= 0 ? p.table[src + full] : -1;
+      p.copies[2 * static_cast<size_t>(k) + 1] = f;
+    }
+  }
+  t.cl.sync();  // (the others may still read this CTA's shared memory)
+}
+
+// -------------------------------------------------------------------------------------- reserve
+__global__ void __launch_bounds__(kThreads) pages_reserve_kernel(const PagesParams p) {
+  extern __shared__ int dyn[];
+  __shared__ Shared s;
+  Team t;
+  const int part = (p.B + t.n - 1) / t.n;
+  int* const have = dyn;          // [part]: pages that a row holds
+  int* const need = have + part;  // [part]
+  int* const first = need + part; // [part]: the rank of its first new page; -1: refused
+  const int b0 = min(p.B, t.rank * part), b1 = min(p.B, b0 + part);
+  const int lane = threadIdx.x & 31;
+  for (int b = b0 + (threadIdx.x >> 5); b < b1; b += kThreads / 32) {
+    const size_t row = static_cast<size_t>(b) * p.M;
+    int h = p.M;  // the first negative entry
+    for (int i0 = 0; i0 < p.M; i0 += 32) {
+      const unsigned none = __ballot_sync(0xffffffffu, i0 + lane < p.M && p.table[row + min(i0 + lane, p.M - 1)] < 0);
+      if (none) {
+        h = i0 + __ffs(none) - 1;
+        break;
+      }
+    }
+    if (lane == 0) {
+      const int L = p.lens[b], n = p.arg[b];
+      const long long want = pages_of(static_cast<long long>(L) + n, p.page);
+      const bool bad = L < 0 || n < 0 || want > p.M;
+      if (bad) raise_status(p.status, ATTN_ERR_DEVICE_INPUT);
+      have[b - b0] = h;
+      need[b - b0] = bad ? 0 : max(0, static_cast<int>(want) - h);
+    }
+  }
+  copy_ints(t, p.table, p.table_out, static_cast<long long>(p.B) * p.M);
+  copy_ints(t, p.refs, p.refs_out, p.P);
+  const int32_t* const refs = p.refs;
+  const auto is_free = [refs](int i) { return refs[i] <= 0; };
+  Ranks ranks;
+  ranks.count(t, s, p.P, is_free);  // (its barriers: have and need are complete, and so are the copies)
+  int mine = 0;
+  for (int q0 = 0; q0 < part; q0 += kThreads) {
+    const int i = q0 + static_cast<int>(threadIdx.x);
+    int all;
+    const int x = i < b1 - b0 ? need[i] : 0;
+    const int r = block_scan(x, s.warp, all);
+    if (i < b1 - b0) first[i] = mine + r;
+    mine += all;
+  }
+  int want;
+  const int base = t.before(&s.mine2, mine, want);
+  __syncthreads();
+  // a row is served when its pages and those of the rows before it are there
+  for (int b = b0 + (threadIdx.x >> 5); b < b1; b += kThreads / 32) {
+    const int n = need[b - b0], r0 = base + first[b - b0];
+    if (n == 0) continue;
+    if (r0 < 0 || r0 > ranks.total - n) {
+      if (lane == 0) raise_status(p.status, ATTN_ERR_DEVICE_INPUT);
+      __syncwarp();
+      if (lane == 0) need[b - b0] = 0;
+      continue;
+    }
+    for (int i = lane; i < n; i += 32)
+      p.table_out[static_cast<size_t>(b) * p.M + have[b - b0] + i] = ranks.select(t, s, p.P, r0 + i, is_free);
+  }
+  t.cl.sync();  // every page has been chosen: the counts may change
+  for (int b = b0 + (threadIdx.x >> 5); b < b1; b += kThreads / 32) {
+    const int n = need[b - b0];
+    for (int i = lane; i < n; i += 32) p.refs_out[p.table_out[static_cast<size_t>(b) * p.M + have[b - b0] + i]] = 1;
+  }
+}
+
+// -------------------------------------------------------------------------------------- compact
+__global__ void __launch_bounds__(kThreads) pages_compact_kernel(const PagesParams p) {
+  __shared__ Shared s;
+  Team t;
+  const int32_t* const refs = p.refs;
+  const auto is_used = [refs](int i) { return refs[i] > 0; };
+  Ranks ranks;
+  ranks.count(t, s, p.P, is_used);
+  const int U = ranks.total;
+  const int in_front = U < p.P ? ranks.rank(t, s, U, is_used) : U;  // used pages among the first U
+  const int moves = U - in_front;
+  for (int k = moves + t.tid; k < p.P / 2; k += t.threads) p.copies[2 * static_cast<size_t>(k)] = p.copies[2 * static_cast<size_t>(k) + 1] = -1;
+  {
+    const long long lo = static_cast<long long>(t.tid) * ranks.seg, hi = min(static_cast<long long>(p.P), lo + ranks.seg);
+    int u = 0;  // used pages before page i
+    if (lo < hi) u = ranks.base[t.rank] + s.first[threadIdx.x];
+    for (long long i = lo; i < hi; ++i) {
+      const bool used = is_used(static_cast<int>(i));
+      if (i < U && !used) p.copies[2 * static_cast<size_t>(i - u) + 1] = static_cast<int>(i);
+      if (i >= U && used) p.copies[2 * static_cast<size_t>(u - in_front)] = static_cast<int>(i);
+      u += used ? 1 : 0;
+    }
+  }
+  if (t.tid == 0) p.used[0] = U;
+  t.cl.sync();  // the moves are known
+  for (long long i = t.tid; i < static_cast<long long>(p.B) * p.M; i += t.threads) {
+    int e = p.table[i];
+    if (e >= p.P) {
+      raise_status(p.status, ATTN_ERR_DEVICE_INPUT);
+    } else if (e >= U) {
+      if (is_used(e)) e = p.copies[2 * static_cast<size_t>(ranks.rank(t, s, e, is_used) - in_front) + 1];
+      else raise_status(p.status, ATTN_ERR_DEVICE_INPUT);  // a page that is counted as free
+    }
+    p.table_out[i] = e;
+  }
+  t.cl.sync();  // the counts have been read: the first U may change, then the others
+  if (p.refs_out != p.refs)
+    for (int i = t.tid; i < U; i += t.threads)
+      if (is_used(i)) p.refs_out[i] = refs[i];
+  for (int k = t.tid; k < moves; k += t.threads) p.refs_out[p.copies[2 * static_cast<size_t>(k) + 1]] = refs[p.copies[2 * static_cast<size_t>(k)]];
+  t.cl.sync();
+  for (int i = U + t.tid; i < p.P; i += t.threads) p.refs_out[i] = 0;
+}
+
+// -------------------------------------------------------------------------------------- copies of pages
+// Items of 32 kB of K or V of a listed pair, 128 bytes a thread, all in flight before the first is written.
+// The entries of four items are read at once: lists end in entries without a copy, and one read after the
+// other would cost an L2 latency each.
+constexpr int kCopyThreads = 256, kCopyVecs = 8, kCopyAhead = 4;
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(uint4* __restrict__ k, uint4* __restrict__ v, const int2* __restrict__ copies,
+                                                                  int n, int P, int vecs, int chunks, unsigned* status) {
+  const long long items = static_cast<long long>(n) * 2 * chunks;
+  for (long long i0 = blockIdx.x; i0 < items; i0 += static_cast<long long>(gridDim.x) * kCopyAhead) {
+    int2 pair[kCopyAhead];
+#pragma unroll
+    for (int u = 0; u < kCopyAhead; ++u) {
+      const long long i = i0 + static_cast<long long>(u) * gridDim.x;
+      pair[u] = i < items ? copies[i / (2 * chunks)] : make_int2(-1, -1);
+    }
+#pragma unroll
+    for (int u = 0; u < kCopyAhead; ++u) {
+      const long long i = i0 + static_cast<long long>(u) * gridDim.x;
+      const int src = pair[u].x, dst = pair[u].y;
+      if (src < 0 && dst < 0) continue;
+      const int part = static_cast<int>(i % (2 * chunks));
+      if (src < 0 || dst < 0 || src >= P || dst >= P) {
+        if (threadIdx.x == 0 && part == 0) raise_status(status, ATTN_ERR_DEVICE_INPUT);
+        continue;
+      }
+      if (src == dst) continue;
+      uint4* const pool = part < chunks ? k : v;
+      const int c = part % chunks;
+      const uint4* from = pool + static_cast<size_t>(src) * vecs;
+      uint4* to = pool + static_cast<size_t>(dst) * vecs;
+      const int first = c * kCopyThreads * kCopyVecs + static_cast<int>(threadIdx.x);
+      uint4 x[kCopyVecs];
+#pragma unroll
+      for (int j = 0; j < kCopyVecs; ++j)
+        if (first + j * kCopyThreads < vecs) x[j] = from[first + j * kCopyThreads];
+#pragma unroll
+      for (int j = 0; j < kCopyVecs; ++j)
+        if (first + j * kCopyThreads < vecs) to[first + j * kCopyThreads] = x[j];
+    }
+  }
+}
+
+// -------------------------------------------------------------------------------------- append
+// A warp per token: the sequence that holds it (the last b with cu[b] <= token, 32 entries of cu at a time),
+// its place, then its keys and values, 16 bytes a lane.  The first 8 loads of a lane, a whole token of 8 heads
+// of 128 columns, start before the place is known.
+constexpr int kAppendThreads = 128, kAppendVecs = 4;
+__global__ void __launch_bounds__(kAppendThreads) pages_append_kernel(const PagesAppendParams p) {
+  const int lane = threadIdx.x & 31;
+  const int row = p.row_vecs, all = p.Hkv * row;  // 16-byte vectors of a head's row, of a token
+  const int warps = gridDim.x * (kAppendThreads / 32);
+  const int end = p.cu[p.B];
+  if (end < 0 || end > p.T || p.cu[0] != 0) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) raise_status(p.status, ATTN_ERR_DEVICE_INPUT);
+    return;
+  }
+  for (int t = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5); t < end; t += warps) {
+    const uint4* const kn = p.k_new + static_cast<size_t>(t) * p.k_stride;
+    const uint4* const vn = p.v_new + static_cast<size_t>(t) * p.v_stride;
+    uint4 x[kAppendVecs], y[kAppendVecs];
+#pragma unroll
+    for (int j = 0; j < kAppendVecs; ++j)
+      if (lane + 32 * j < all) {
+        x[j] = kn[lane + 32 * j];
+        y[j] = vn[lane + 32 * j];
+      }
+    // the last b with cu[b] <= t, among [lo, lo + span)
+    int lo = 0;
+    for (long long span = p.B; span > 1;) {
+      const int step = static_cast<int>((span + 31) / 32);
+      const long long at = lo + static_cast<long long>(lane) * step;
+      const unsigned below = __ballot_sync(0xffffffffu, static_cast<long long>(lane) * step < span && p.cu[min(at, static_cast<long long>(p.B))] <= t);
+      const int last = below ? 31 - __clz(below) : 0;
+      span = min(static_cast<long long>(step), span - static_cast<long long>(last) * step);
+      lo += last * step;
+    }
+    const int c0 = p.cu[lo], c1 = p.cu[lo + 1];
+    const int L = p.lens ? p.lens[lo] : 0;
+    const long long pos = static_cast<long long>(L) + (t - c0);
+    // (cu out of order: a token that no sequence holds is left out)
+    bool ok = c0 >= 0 && t >= c0 && t < c1 && L >= 0 && static_cast<long long>(L) + (c1 - c0) <= static_cast<long long>(p.M) * p.page;
+    int id = -1;
+    if (ok) id = p.table[static_cast<size_t>(lo) * p.M + pos / p.page];
+    ok = ok && id >= 0 && id < p.P;
+    if (!ok) {
+      if (lane == 0) raise_status(p.status, ATTN_ERR_DEVICE_INPUT);
+      continue;
+    }
+    // head h's row of this token: [id, h, pos % page]
+    const size_t base = (static_cast<size_t>(id) * p.Hkv * p.page + pos % p.page) * row;
+    const size_t head = static_cast<size_t>(p.page) * row;
+#pragma unroll
+    for (int j = 0; j < kAppendVecs; ++j) {
+      const int i = lane + 32 * j;
+      if (i < all) {
+        const size_t at = base + i / row * head + i % row;
+        p.k[at] = x[j];
+        p.v[at] = y[j];
+      }
+    }
+    for (int i = lane + 32 * kAppendVecs; i < all; i += 32) {
+      const size_t at = base + i / row * head + i % row;
+      p.k[at] = kn[i];
+      p.v[at] = vn[i];
+    }
+  }
+}
+
+// One cluster: a CTA for each 8k ints that a call looks at, up to 8.
+template <typename K>
+cudaError_t launch_books(K kern, const PagesParams& p, long long ints, size_t smem_of(const PagesParams&, int), cudaStream_t stream) {
+  int n = 1;
+  while (n < kMaxCluster && ints > 8192LL * n) n *= 2;
+  size_t smem = smem_of(p, n);
+  while (n < kMaxCluster && smem > 32 * 1024) smem = smem_of(p, n *= 2);
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = n;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(n);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+size_t no_smem(const PagesParams&, int) { return 0; }
+size_t fork_smem(const PagesParams& p, int n) { return 4 * (static_cast<size_t>((p.B + n - 1) / n) + 2 * static_cast<size_t>((p.n + n - 1) / n)); }
+size_t reserve_smem(const PagesParams& p, int n) { return 12 * static_cast<size_t>((p.B + n - 1) / n); }
+
+}  // namespace
+
+cudaError_t launch_pages_free(const PagesParams& p, cudaStream_t s) {
+  return launch_books(pages_free_kernel, p, static_cast<long long>(p.B) * p.M + p.P, no_smem, s);
+}
+cudaError_t launch_pages_fork(const PagesParams& p, cudaStream_t s) {
+  return launch_books(pages_fork_kernel, p, static_cast<long long>(p.B) * p.M + p.P, fork_smem, s);
+}
+cudaError_t launch_pages_reserve(const PagesParams& p, cudaStream_t s) {
+  return launch_books(pages_reserve_kernel, p, static_cast<long long>(p.B) * p.M + p.P, reserve_smem, s);
+}
+cudaError_t launch_pages_compact(const PagesParams& p, cudaStream_t s) {
+  return launch_books(pages_compact_kernel, p, static_cast<long long>(p.B) * p.M + p.P, no_smem, s);
+}
+cudaError_t launch_pages_copy(void* k, void* v, const int32_t* copies, int n, int P, size_t page_bytes, unsigned* status, cudaStream_t s) {
+  const int vecs = static_cast<int>(page_bytes / 16), chunks = (vecs + kCopyThreads * kCopyVecs - 1) / (kCopyThreads * kCopyVecs);
+  const long long items = static_cast<long long>(n) * 2 * chunks;
+  const int grid = static_cast<int>(std::min(items, 152LL * 6));
+  pages_copy_kernel<<<grid, kCopyThreads, 0, s>>>(static_cast<uint4*>(k), static_cast<uint4*>(v), reinterpret_cast<const int2*>(copies), n, P, vecs,
+                                                  chunks, status);
+  return cudaGetLastError();
+}
+cudaError_t launch_pages_append(const PagesAppendParams& p, cudaStream_t s) {
+  const long long ctas = (static_cast<long long>(p.T) + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
+  pages_append_kernel<<<static_cast<int>(std::min(ctas, 152LL * 64)), kAppendThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace attn

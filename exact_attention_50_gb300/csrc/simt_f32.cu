@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(256) fwd_f32_kernel(const float* __restrict__ 
     const int s = blockIdx.z;
     const int c0 = p.cu_seqlens[s], c1 = p.cu_seqlens[s + 1];
     const bool bad = c0 < 0 || c1 < c0 || c1 > p.total_tokens || c1 - c0 > p.max_seqlen ||
-                     (s == 0 && c0 != 0) || (s == p.nseq - 1 && c1 != p.total_tokens);
+                     (s == 0 && c0 != 0) || (s == p.nseq - 1 && c1 != p.total_tokens && !p.open_end);
     if (bad) {
       if (threadIdx.x == 0) raise_status(p.status, ATTN_ERR_DEVICE_INPUT);
       return;
@@ -93,15 +93,17 @@ __global__ void __launch_bounds__(256) fwd_f32_kernel(const float* __restrict__ 
     seq_len = p.N;
   }
   const int d = p.d, g = h / p.G, d4 = d / 4;
-  RowAddr qa, ka;
+  RowAddr qa, ka, va;
   if constexpr (VARLEN) {
-    // q, k and v already point at planes 0, 1 and 2 of the packed [T,3,H,d] tensor
-    const size_t tok = 3ull * p.Hq * d;
-    qa = {static_cast<size_t>(seq_start) * tok + static_cast<size_t>(h) * d, tok};
-    ka = qa;
+    // q, k and v already point at planes 0, 1 and 2 of the packed [T,3,H,d] tensor, or are tensors of their own
+    const size_t tq = static_cast<size_t>(p.tok_q), tk = static_cast<size_t>(p.tok_k), tv = static_cast<size_t>(p.tok_v);
+    qa = {static_cast<size_t>(seq_start) * tq + static_cast<size_t>(h) * d, tq};
+    ka = {static_cast<size_t>(seq_start) * tk + static_cast<size_t>(g) * d, tk};
+    va = {static_cast<size_t>(seq_start) * tv + static_cast<size_t>(g) * d, tv};
   } else {
     qa = {(static_cast<size_t>(b) * p.Hq + h) * p.N * d, static_cast<size_t>(d)};
     ka = {(static_cast<size_t>(b) * p.Hkv + g) * p.N * d, static_cast<size_t>(d)};
+    va = ka;
   }
   const int row0 = qt * kBM32;
   // Q^T: column c of row r at sQt[c][r]; a warp stores 32 consecutive rows of one column group
@@ -139,7 +141,7 @@ __global__ void __launch_bounds__(256) fwd_f32_kernel(const float* __restrict__ 
     for (int idx = t; idx < kBN32 * (DMAX / 4); idx += 256) {
       const int r = idx / (DMAX / 4), c4 = idx % (DMAX / 4);
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (key0 + r < seq_len && c4 < d4) x = *reinterpret_cast<const float4*>(v + ka.base + (key0 + r) * ka.stride + 4 * c4);
+      if (key0 + r < seq_len && c4 < d4) x = *reinterpret_cast<const float4*>(v + va.base + (key0 + r) * va.stride + 4 * c4);
       *reinterpret_cast<float4*>(sV + r * SV + 4 * c4) = x;
     }
     __syncthreads();
@@ -253,8 +255,9 @@ __global__ void __launch_bounds__(256) fwd_f32_kernel(const float* __restrict__ 
 // absent) and, when causal, only j <= L - Nq + i.  Range s covers the keys
 // [s * tiles_per_split * 128, (s + 1) * tiles_per_split * 128); every range writes its
 // normalised partial output and LSE (O = 0, LSE = -inf for a row that sees none of its keys),
-// which the split combine merges.
-template <bool CAUSAL>
+// which the split combine merges.  PAGED: key j lies in the pool, row j % page of page table[b][j / page]; a page number
+// outside the pool reads as zeros.
+template <bool CAUSAL, bool PAGED>
 __global__ void __launch_bounds__(128) fwd_f32_kv_kernel(const float* __restrict__ q, const float* __restrict__ k,
                                                          const float* __restrict__ v, const FwdParams p) {
   extern __shared__ float smem_f[];
@@ -297,9 +300,18 @@ __global__ void __launch_bounds__(128) fwd_f32_kv_kernel(const float* __restrict
     __syncthreads();
     for (int idx = threadIdx.x; idx < kTile * d; idx += blockDim.x) {
       const int r = idx / d, c = idx % d;
-      const bool in = key0 + r < k_end;
-      sK[r * dp1 + c] = in ? k[kbase + static_cast<size_t>(key0 + r) * d + c] : 0.f;
-      sV[r * d + c] = in ? v[kbase + static_cast<size_t>(key0 + r) * d + c] : 0.f;
+      bool in = key0 + r < k_end;
+      size_t at = kbase + static_cast<size_t>(key0 + r) * d + c;
+      if constexpr (PAGED) {
+        if (in) {
+          const int id = p.table[static_cast<size_t>(b) * p.M + ((key0 + r) >> p.page_shift)];
+          in = id >= 0 && id < p.P;
+          if (!in) raise_status(p.status, ATTN_ERR_DEVICE_INPUT);
+          at = (((static_cast<size_t>(id) * p.Hkv + g) << p.page_shift) + ((key0 + r) & ((1 << p.page_shift) - 1))) * d + c;
+        }
+      }
+      sK[r * dp1 + c] = in ? k[at] : 0.f;
+      sV[r * d + c] = in ? v[at] : 0.f;
     }
     __syncthreads();
     const int key = key0 + lane;
@@ -360,7 +372,7 @@ __device__ __forceinline__ BwdBlock bwd_block(const BwdParams& p, int x) {
     const int s = x / p.Hkv, hh = x % p.Hkv;
     const int c0 = p.cu_seqlens[s], c1 = p.cu_seqlens[s + 1];
     if (c0 < 0 || c1 < c0 || c1 > p.N || c1 - c0 > p.max_seqlen || (s == 0 && c0 != 0) ||
-        (s == p.nseq - 1 && c1 != p.N)) {
+        (s == p.nseq - 1 && c1 != p.N && !p.open_end)) {
       if (threadIdx.x == 0 && blockIdx.y == 0 && hh == 0) raise_status(p.status, ATTN_ERR_DEVICE_INPUT);
       r.ok = false;
       return r;
@@ -403,8 +415,8 @@ __global__ void __launch_bounds__(128) bwd_dq_f32_kernel(const BwdParams p) {
   const size_t qbase = static_cast<size_t>(hq) * p.N + s0;  // row statistics of this head
   const float* qh = q + hq * p.lay_q.head + s0 * p.lay_q.row;
   const float* doh = dout + hq * p.lay_o.head + s0 * p.lay_o.row;
-  const float* kh = k + bb.hkv * p.lay_kv.head + s0 * p.lay_kv.row;
-  const float* vh = v + bb.hkv * p.lay_kv.head + s0 * p.lay_kv.row;
+  const float* kh = k + bb.hkv * p.lay_k.head + s0 * p.lay_k.row;
+  const float* vh = v + bb.hkv * p.lay_v.head + s0 * p.lay_v.row;
   for (int idx = threadIdx.x; idx < kRows * d; idx += blockDim.x) {
     const int r = idx / d, c = idx % d;
     const bool in = row0 + r < N;
@@ -426,8 +438,8 @@ __global__ void __launch_bounds__(128) bwd_dq_f32_kernel(const BwdParams p) {
     for (int idx = threadIdx.x; idx < kTile * d; idx += blockDim.x) {
       const int r = idx / d, c = idx % d;
       const bool in = key0 + r < Nk;
-      sK[r * dp1 + c] = in ? kh[(key0 + r) * p.lay_kv.row + c] : 0.f;
-      sV[r * dp1 + c] = in ? vh[(key0 + r) * p.lay_kv.row + c] : 0.f;
+      sK[r * dp1 + c] = in ? kh[(key0 + r) * p.lay_k.row + c] : 0.f;
+      sV[r * dp1 + c] = in ? vh[(key0 + r) * p.lay_v.row + c] : 0.f;
     }
     __syncthreads();
     const int key = key0 + lane;
@@ -486,13 +498,13 @@ __global__ void __launch_bounds__(128) bwd_dkdv_f32_kernel(const BwdParams p) {
   const int d = p.d, N = bb.L, Nk = bb.Lk, off = Nk - N, s0 = bb.seq_start;
   const int key0 = blockIdx.y * kRows;
   if (key0 >= Nk) return;  // past this sequence's end (varlen)
-  const float* kh = k + bb.hkv * p.lay_kv.head + s0 * p.lay_kv.row;
-  const float* vh = v + bb.hkv * p.lay_kv.head + s0 * p.lay_kv.row;
+  const float* kh = k + bb.hkv * p.lay_k.head + s0 * p.lay_k.row;
+  const float* vh = v + bb.hkv * p.lay_v.head + s0 * p.lay_v.row;
   for (int idx = threadIdx.x; idx < kRows * d; idx += blockDim.x) {
     const int r = idx / d, c = idx % d;
     const bool in = key0 + r < Nk;
-    sK[r * d + c] = in ? kh[(key0 + r) * p.lay_kv.row + c] : 0.f;
-    sV[r * d + c] = in ? vh[(key0 + r) * p.lay_kv.row + c] : 0.f;
+    sK[r * d + c] = in ? kh[(key0 + r) * p.lay_k.row + c] : 0.f;
+    sV[r * d + c] = in ? vh[(key0 + r) * p.lay_v.row + c] : 0.f;
   }
   float dk[8][kColsPerLane], dv[8][kColsPerLane];
 #pragma unroll
@@ -584,7 +596,11 @@ cudaError_t launch_fwd_f32(const void* q, const void* k, const void* v, const Fw
   };
   if (mode == kModeKv) {
     const dim3 grid(p.B * p.Hq, (p.Nq + kRows - 1) / kRows, p.n_splits);
-    return causal ? run(fwd_f32_kv_kernel<true>, grid) : run(fwd_f32_kv_kernel<false>, grid);
+    return causal ? run(fwd_f32_kv_kernel<true, false>, grid) : run(fwd_f32_kv_kernel<false, false>, grid);
+  }
+  if (mode == kModePaged) {
+    const dim3 grid(p.B * p.Hq, (p.Nq + kRows - 1) / kRows, p.n_splits);
+    return causal ? run(fwd_f32_kv_kernel<true, true>, grid) : run(fwd_f32_kv_kernel<false, true>, grid);
   }
   // dense and varlen: the register-tiled kernel, 64 query rows per CTA
   auto run_tiled = [&](auto kern, dim3 grid, size_t bytes) -> cudaError_t {
@@ -593,7 +609,7 @@ cudaError_t launch_fwd_f32(const void* q, const void* k, const void* v, const Fw
     kern<<<grid, 256, bytes, stream>>>(qf, kf, vf, p);
     return cudaGetLastError();
   };
-  const bool varlen = mode == kModeVarlen;
+  const bool varlen = mode == kModeVarlen || mode == kModePacked;
   const dim3 grid = varlen ? dim3(p.Hq, (p.max_seqlen + kBM32 - 1) / kBM32, p.nseq)
                            : dim3(p.B * p.Hq, (p.N + kBM32 - 1) / kBM32, 1);
   if (p.d <= 64) {

@@ -58,8 +58,9 @@ typedef enum {
   ATTN_ERR_CUDA = 3,         /* a CUDA runtime/driver call failed (launch, tensor map, ...) */
   ATTN_ERR_TIMEOUT = 4,      /* device: a pipeline wait exceeded its time limit; CTA stopped */
   ATTN_ERR_DEVICE_INPUT = 5  /* device: cu_seqlens not non-decreasing from 0, a sequence
-                                longer than max_seqlen, a cache length outside [0, Nk], or
-                                tokens appended past the end of a cache */
+                                longer than max_seqlen, a cache length outside [0, Nk],
+                                tokens appended past the end of a cache, a page number
+                                outside the pool, or pages that there are not */
 } attn_status_t;
 
 #define ATTN_FLAG_OUT_F32 1u
@@ -328,6 +329,127 @@ attn_status_t attn_kvcache_evict(const void* k_cache, const void* v_cache, const
                                  const int32_t* cache_seqlens, void* k_out, void* v_out, float* weights_out,
                                  int32_t* index, int32_t* out_seqlens, int B, int Hkv, int Nk, int capacity, int d,
                                  int keep, int recent, attn_dtype_t dtype, void* stream);
+
+/*
+ * Attention of packed sequences with grouped heads: attn_fwd_varlen for query and kv heads of different number and for
+ * q, k and v of their own, each with its distance from token to token, so they may be parts of one projection's
+ * output.  O, LSE, masks and sequences are those of attn_fwd_varlen.
+ *   q          token t's head h at q + t * q_stride + h * d elements; k, v likewise.  Strides are multiples of 16 bytes
+ *              (q_stride >= Hq * d, k_stride and v_stride >= Hkv * d)
+ *   cu_seqlens DEVICE int32 [nseq + 1], not decreasing from 0, cu_seqlens[nseq] <= total_tokens: tokens may lie behind
+ *              the last sequence; their rows get O = 0 and LSE = -inf, and gradients of zero, whatever they hold
+ *   max_seqlen an upper bound on every sequence length
+ *   out        [total_tokens, Hq, d] (dtype, or float32 with ATTN_FLAG_OUT_F32); lse [Hq, total_tokens] float32, nullable
+ *   workspace  DEVICE, 256-byte aligned, at least the bytes below (a list of the tiles that the sequences fill); contents
+ *              on entry are ignored, on exit undefined.  Calls that may run at the same time need one each
+ * A sequence never reads another's tokens as anything but numbers that count for nothing: NaN there stays there.
+ * Sequences that break the rules on cu_seqlens or max_seqlen are skipped (their rows are left as they are) and
+ * attn_get_device_status() returns ATTN_ERR_DEVICE_INPUT; when cu_seqlens decreases, so may all others be.
+ * More than 65535 sequences, or 2^31 rows (total_tokens * Hq), are ATTN_ERR_UNSUPPORTED.  No output overlaps an input or
+ * another output.
+ */
+size_t attn_fwd_varlen_gqa_workspace_bytes(int nseq, int total_tokens, int max_seqlen, int Hq, int Hkv);
+attn_status_t attn_fwd_varlen_gqa(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int nseq, int total_tokens,
+                                  int max_seqlen, void* out, float* lse, void* workspace, size_t workspace_bytes, int Hq, int Hkv, int d,
+                                  int64_t q_stride, int64_t k_stride, int64_t v_stride, int causal, float scale, attn_dtype_t dtype,
+                                  unsigned flags, void* stream);
+
+/*
+ * Its backward: dq [total_tokens, Hq, d], dk and dv [total_tokens, Hkv, d] (dtype, or float32 with ATTN_FLAG_OUT_F32),
+ * by the formulas of attn_bwd; a kv head's dk and dv sum over the query heads of its group.
+ *   out, dout  [total_tokens, Hq, d] (dtype); lse [Hq, total_tokens], as the forward wrote them
+ * The other arguments are the forward's; ATTN_FLAG_DETERMINISTIC as for attn_bwd.
+ */
+size_t attn_bwd_varlen_gqa_workspace_bytes(int nseq, int total_tokens, int max_seqlen, int Hq, int Hkv, int d);
+attn_status_t attn_bwd_varlen_gqa(const void* q, const void* k, const void* v, const void* out, const void* dout, const float* lse,
+                                  const int32_t* cu_seqlens, int nseq, int total_tokens, int max_seqlen, void* dq, void* dk, void* dv,
+                                  void* workspace, size_t workspace_bytes, int Hq, int Hkv, int d, int64_t q_stride, int64_t k_stride,
+                                  int64_t v_stride, int causal, float scale, attn_dtype_t dtype, unsigned flags, void* stream);
+
+/*
+ * A KV cache in pages.  The pools of keys and of values are [pages, Hkv, page, d], page = 16, 32, 64 or 128 tokens; row b
+ * of the table [B, max_pages] holds the page numbers of sequence b in order, then negative numbers: its token j is
+ * row j % page of page table[b][j / page], and row, page and sequence are the same for all kv heads (and, in a model,
+ * for the pools of all layers).  refs [pages] counts the rows that hold a page; 0 is free.  In the calls below more than
+ * 2^31 - 2^16 tokens in a sequence, 2^31 - 1 pages * Hkv or table entries, or (free, fork, reserve, compact) 65536 rows
+ * or pairs are ATTN_ERR_UNSUPPORTED.
+ *
+ * attn_fwd_kvcache over such a cache.  Shapes of q, o and lse, masks, rows without keys, flags and argument rules are those
+ * of attn_fwd_kvcache; all three types.  The split over key ranges is chosen from the sizes.
+ *   page_table     DEVICE int32 [B, max_pages]; cache_seqlens DEVICE int32 [B]
+ *   max_seqlen     an upper bound on every cache length, by which the work is planned; 0: max_pages * page
+ *   workspace      DEVICE, at least attn_fwd_kvpages_workspace_bytes(...) bytes, 256-byte aligned (0 bytes for small
+ *                  problems: it may then be NULL); contents on entry are ignored, on exit undefined.  Calls that may run
+ *                  at the same time need one each
+ * Rows of a page behind a cache's end, and pages of others, may hold anything.  An infinity or NaN among the values
+ * within a cache can reach rows whose causal mask hides that token (0 * NaN).  A length outside [0, max_seqlen] counts
+ * as an empty cache, a page number outside [0, pages) as a page of zeros, and attn_get_device_status() returns
+ * ATTN_ERR_DEVICE_INPUT.
+ */
+size_t attn_fwd_kvpages_workspace_bytes(int B, int Hq, int Hkv, int Nq, int max_pages, int page, int max_seqlen, int d, attn_dtype_t dtype);
+attn_status_t attn_fwd_kvpages(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table, const int32_t* cache_seqlens,
+                               void* o, float* lse, void* workspace, size_t workspace_bytes, int B, int Hq, int Hkv, int Nq, int max_pages,
+                               int pages, int page, int max_seqlen, int d, int causal, float scale, attn_dtype_t dtype, unsigned flags,
+                               void* stream);
+
+/*
+ * Writes new tokens into the pages that the table gives them, in place: token i of sequence b goes to position
+ * cache_seqlens[b] + i.  The lengths themselves are not changed.
+ *   k_new, v_new   token t's head h at k_new + t * k_stride + h * d elements (strides as in attn_fwd_varlen_gqa)
+ *   cu_seqlens     DEVICE int32 [B + 1], not decreasing from 0: sequence b's tokens are cu_seqlens[b] .. cu_seqlens[b + 1] - 1;
+ *                  tokens from cu_seqlens[B] on are left out
+ *   cache_seqlens  DEVICE int32 [B], or NULL: empty sequences
+ * Tokens without a place (past max_pages * page, or a page number outside [0, pages)) are left out and
+ * attn_get_device_status() returns ATTN_ERR_DEVICE_INPUT.  A page that two sequences write into at the same place
+ * keeps either.  The pools overlap no other argument.
+ */
+attn_status_t attn_kvpages_append(void* k_pages, void* v_pages, const int32_t* page_table, const void* k_new, const void* v_new,
+                                  const int32_t* cu_seqlens, const int32_t* cache_seqlens, int B, int total_tokens, int Hkv, int max_pages,
+                                  int pages, int page, int d, int64_t k_stride, int64_t v_stride, attn_dtype_t dtype, void* stream);
+
+/*
+ * The books.  Each call reads one state and writes the next one to table_out, seqlens_out and refs_out; each of these is
+ * the array that it follows, or overlaps nothing else.  Free pages are taken in ascending order, so the outcome depends
+ * on the state alone.  What a call refuses it leaves as it was, and attn_get_device_status() returns ATTN_ERR_DEVICE_INPUT.
+ *
+ * free: cuts each sequence to its first keep_seqlens[b] tokens (all when it has no more; 0 ends it).  The pages behind
+ * the ones that these need lose a reference, and their entries become -1.  Refused: a negative length or number, for its row.
+ */
+attn_status_t attn_kvpages_free(const int32_t* page_table, const int32_t* cache_seqlens, const int32_t* refs, const int32_t* keep_seqlens,
+                                int32_t* table_out, int32_t* seqlens_out, int32_t* refs_out, int B, int max_pages, int pages, int page,
+                                void* stream);
+/*
+ * fork: row dst[i], which must be empty (length 0, first entry negative), becomes a copy of row src[i].  The full pages
+ * are shared (a reference each); a last page that is partly filled is replaced by a free one, and copies[i] says which
+ * page to copy where, for attn_kvpages_copy in each layer, or (-1, -1).  Sources are as they were before the call.
+ * Refused, pair by pair: numbers out of range; a dst that is not empty, or stands in the list before; a source without its
+ * last page; a page that is not there, free pages going to the pairs in order.
+ *   src, dst       DEVICE int32 [n]; copies DEVICE int32 [n, 2], 8-byte aligned
+ */
+attn_status_t attn_kvpages_fork(const int32_t* page_table, const int32_t* cache_seqlens, const int32_t* refs, const int32_t* src,
+                                const int32_t* dst, int32_t* table_out, int32_t* seqlens_out, int32_t* refs_out, int32_t* copies, int n, int B,
+                                int max_pages, int pages, int page, void* stream);
+/*
+ * reserve: appends free pages to each row until it has room for new_seqlens[b] tokens behind its cache_seqlens[b]; rows
+ * that have the room keep what they hold.  Refused: a negative length or number and more than max_pages, for its row; and a row
+ * for which, with the rows before it, there are not enough free pages.
+ */
+attn_status_t attn_kvpages_reserve(const int32_t* page_table, const int32_t* cache_seqlens, const int32_t* refs, const int32_t* new_seqlens,
+                                   int32_t* table_out, int32_t* refs_out, int B, int max_pages, int pages, int page, void* stream);
+/*
+ * compact: with U pages in use, moves those from U on to the free places before it, in ascending order, so that they
+ * occupy [0, U): table entries and counts follow, copies [pages / 2, 2] says which page to copy where, then (-1, -1), and
+ * used [1] is U.  An entry that counts as free, or lies outside the pool, keeps its number, with the status above.
+ */
+attn_status_t attn_kvpages_compact(const int32_t* page_table, const int32_t* refs, int32_t* table_out, int32_t* refs_out, int32_t* copies,
+                                   int32_t* used, int B, int max_pages, int pages, void* stream);
+/*
+ * copy: copies whole pages of the keys and of the values, copies[i] = (from, to), as fork and compact list them; pairs of
+ * two negative numbers are passed over, and pairs out of range too, with the status above.  The pairs are carried out in
+ * no order: a page that is the target of two, or of one and the source of another, may end up with a mixture.
+ */
+attn_status_t attn_kvpages_copy(void* k_pages, void* v_pages, const int32_t* copies, int n, int Hkv, int pages, int page, int d,
+                                attn_dtype_t dtype, void* stream);
 
 /*
  * attn_bwd_noalloc -- the backward (same arguments, layouts and results as attn_bwd) for callers
