@@ -681,46 +681,56 @@ def kvpages_append(k_pages, v_pages, page_table, k_new, v_new, cu_seqlens, cache
     _lib._check(st, "attn_kvpages_append")
 
 
-def _books(named, page: int, out, like):
-    """Checks the int32 arrays of a call on the books (named: (tensor, name)) and the outputs: `out`, or new ones shaped like
-    `like`.  Returns (device, B, max_pages, pages, outputs)."""
+def _books(dev, page, tensors, names, out, like):
+    """Checks the int32 arrays of a call on the books, the table first and refs second, then `names` for the others; and the
+    outputs: `out`, or new ones shaped like `like`.  Returns (B, max_pages, pages, outputs)."""
     i32 = torch.int32
-    try:
-        dev = named[0][0].get_device()
-        fit = _fit(dev, *(t for t, _ in named)) and all(t.dtype is i32 for t, _ in named)
-    except AttributeError:  # not a tensor
-        fit = False
-    if not fit:
-        _explain(*((t, n, i32, False) for t, n in named))
+    for t in tensors:
+        if not isinstance(t, torch.Tensor) or t.dtype is not i32 or t.get_device() != dev or dev < 0 or not t.is_contiguous():
+            _explain(*((x, n, i32, False) for x, n in zip(tensors, ("page_table", "refs") + names)))
     if page not in (16, 32, 64, 128):
         raise ValueError("page must be 16, 32, 64 or 128")
-    B, M = _check_table(named[0][0])
-    refs = dict((n, t) for t, n in named)["refs"]
-    if refs.dim() != 1:
+    shape = tensors[0].shape
+    if len(shape) != 2:
+        raise ValueError("page_table must be [B,max_pages]")
+    B, M = shape
+    refs = tensors[1].shape
+    if len(refs) != 1:
         raise ValueError("refs must be int32 [pages]")
-    _check_sizes(refs.shape)
-    for t, n in named:
-        if n not in ("page_table", "refs", "src", "dst") and t.shape != (B,):
-            raise ValueError(f"{n} must be int32 [B]")
+    if B >= 2 ** 31 or M >= 2 ** 31 or refs[0] >= 2 ** 31:
+        raise ValueError("every size must be below 2**31")
     if out is None:
-        out = tuple(torch.empty_like(t) for t in like)
-    else:
-        out = tuple(out)
-        if len(out) != len(like):
-            raise ValueError(f"out must hold {len(like)} tensors")
-        for t, x in zip(out, like):
-            _require(t, "out", i32)
-            if t.shape != x.shape or t.device != x.device:
-                raise ValueError("out must be shaped like the arrays that it follows, on their device")
-    return dev, B, M, refs.shape[0], out
+        return B, M, refs[0], tuple([torch.empty_like(t) for t in like])
+    out = tuple(out)
+    if len(out) != len(like):
+        raise ValueError(f"out must hold {len(like)} tensors")
+    for t, x in zip(out, like):
+        _require(t, "out", i32)
+        if t.shape != x.shape or t.device != x.device:
+            raise ValueError("out must be shaped like the arrays that it follows, on their device")
+    return B, M, refs[0], out
+
+
+def _of_rows(B, *named):
+    for t, n in named:
+        if t.shape != (B,):
+            raise ValueError(f"{n} must be int32 [B]")
+
+
+def _device_of(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    return t.get_device()
 
 
 def kvpages_free(page_table, cache_seqlens, refs, keep_seqlens, page: int, out=None):
     """Cuts each sequence to its first keep_seqlens[b] tokens (0 ends it) and gives back the pages behind them.  page_table
     int32 [B,max_pages], cache_seqlens and keep_seqlens int32 [B], refs int32 [pages].  out: (page_table, cache_seqlens,
     refs) to write to, which may be the inputs (None: new ones).  Returns those three."""
-    dev, B, M, P, o = _books(((page_table, "page_table"), (cache_seqlens, "cache_seqlens"), (refs, "refs"), (keep_seqlens, "keep_seqlens")),
-                             page, out, (page_table, cache_seqlens, refs))
+    dev = _device_of(page_table, "page_table")
+    B, M, P, o = _books(dev, page, (page_table, refs, cache_seqlens, keep_seqlens), ("cache_seqlens", "keep_seqlens"), out,
+                        (page_table, cache_seqlens, refs))
+    _of_rows(B, (cache_seqlens, "cache_seqlens"), (keep_seqlens, "keep_seqlens"))
     st = _on_device(dev, _lib.attn_kvpages_free, page_table.data_ptr(), cache_seqlens.data_ptr(), refs.data_ptr(), keep_seqlens.data_ptr(),
                     o[0].data_ptr(), o[1].data_ptr(), o[2].data_ptr(), B, M, P, page)
     _lib._check(st, "attn_kvpages_free")
@@ -731,8 +741,10 @@ def kvpages_fork(page_table, cache_seqlens, refs, src, dst, page: int, out=None)
     """Makes the empty rows dst[i] copies of the rows src[i] (int32 [n]): full pages are shared, a partly filled last page is
     replaced by a free one.  out: (page_table, cache_seqlens, refs) as for kvpages_free.  Returns (page_table, cache_seqlens,
     refs, copies int32 [n,2]); copies goes to kvpages_copy for each pair of pools."""
-    dev, B, M, P, o = _books(((page_table, "page_table"), (cache_seqlens, "cache_seqlens"), (refs, "refs"), (src, "src"), (dst, "dst")), page,
-                             out, (page_table, cache_seqlens, refs))
+    dev = _device_of(page_table, "page_table")
+    B, M, P, o = _books(dev, page, (page_table, refs, cache_seqlens, src, dst), ("cache_seqlens", "src", "dst"), out,
+                        (page_table, cache_seqlens, refs))
+    _of_rows(B, (cache_seqlens, "cache_seqlens"))
     if src.dim() != 1 or src.shape != dst.shape:
         raise ValueError("src and dst must be int32 [n]")
     n = src.shape[0]
@@ -746,8 +758,9 @@ def kvpages_fork(page_table, cache_seqlens, refs, src, dst, page: int, out=None)
 def kvpages_reserve(page_table, cache_seqlens, refs, new_seqlens, page: int, out=None):
     """Appends free pages to each row until it has room for new_seqlens[b] tokens behind its first cache_seqlens[b].  out:
     (page_table, refs) to write to, which may be the inputs (None: new ones).  Returns those two."""
-    dev, B, M, P, o = _books(((page_table, "page_table"), (cache_seqlens, "cache_seqlens"), (refs, "refs"), (new_seqlens, "new_seqlens")), page,
-                             out, (page_table, refs))
+    dev = _device_of(page_table, "page_table")
+    B, M, P, o = _books(dev, page, (page_table, refs, cache_seqlens, new_seqlens), ("cache_seqlens", "new_seqlens"), out, (page_table, refs))
+    _of_rows(B, (cache_seqlens, "cache_seqlens"), (new_seqlens, "new_seqlens"))
     st = _on_device(dev, _lib.attn_kvpages_reserve, page_table.data_ptr(), cache_seqlens.data_ptr(), refs.data_ptr(), new_seqlens.data_ptr(),
                     o[0].data_ptr(), o[1].data_ptr(), B, M, P, page)
     _lib._check(st, "attn_kvpages_reserve")
@@ -758,7 +771,8 @@ def kvpages_compact(page_table, refs, out=None):
     """Moves the used pages to the front of the pool: with U in use, those from U on go to the free places before it.  out:
     (page_table, refs) to write to, which may be the inputs (None: new ones).  Returns (page_table, refs, copies int32
     [pages // 2, 2], used int32 [1]: U); copies goes to kvpages_copy for each pair of pools."""
-    dev, B, M, P, o = _books(((page_table, "page_table"), (refs, "refs")), 16, out, (page_table, refs))
+    dev = _device_of(page_table, "page_table")
+    B, M, P, o = _books(dev, 16, (page_table, refs), (), out, (page_table, refs))
     copies = torch.empty((P // 2, 2), dtype=torch.int32, device=refs.device)
     used = torch.empty((1,), dtype=torch.int32, device=refs.device)
     st = _on_device(dev, _lib.attn_kvpages_compact, page_table.data_ptr(), refs.data_ptr(), o[0].data_ptr(), o[1].data_ptr(), copies.data_ptr(),

@@ -58,7 +58,8 @@ struct BwdLayout {
   // kv_full, q_full[QS], q_empty[QS], do_full[QS], do_empty[QS], s_full, dp_full, p_full[2],
   // dv_done, ds_full[2], dsl_free, stage_free, dq_full, dq_free, dkdv_done, rows_ready,
   // stage_full, drain, drain2
-  static constexpr int kNumBars = 1 + 4 * kQStages + 16;
+  // and for packed sequences part_full[QS], kv_clean
+  static constexpr int kNumBars = 1 + 4 * kQStages + 16 + kQStages + 1;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;  // tmem base, abort flag, wait limit (u64)
   static constexpr int kBytes = kOffMisc + 16;
   static constexpr int kSmemAlloc = kBytes;  // the dynamic shared memory starts 1024-byte aligned
@@ -100,8 +101,9 @@ __device__ __forceinline__ void split_pack<__half>(float a, float b, uint32_t& h
 
 // PACKED: packed sequences with grouped heads.  The CTA's key tile comes from the list of tiles (launch_packed_tiles),
 // and a query tile is p.tile_tokens tokens by p.heads neighbouring query heads, row = token * heads + head, so short
-// sequences fill it.  What lies in the tiles behind the sequence's end is another sequence's, or anything: P and dS are
-// zero there by selection, not by multiplication, and the operands that they meet are set to zero in shared memory.
+// sequences fill it.  What lies in the tiles behind the sequence's end is another sequence's, or anything: warp 15 sets
+// those rows to zero in shared memory before an MMA reads them.  (Zeros by selection in the elementwise warps instead,
+// with Q and dO cleaned behind their products: 4 x 2048 tokens, 32 over 8 heads, 472 us for 404.)
 template <typename T, int DP, bool CAUSAL, bool PACKED = false>
 __global__ void __launch_bounds__(512, 1)
     bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -153,6 +155,10 @@ __global__ void __launch_bounds__(512, 1)
   uint64_t* stage_full = rows_ready + 1;  // the read-out warps have staged the dQ tile
   uint64_t* drain = stage_full + 1;   // abort path of issuer 13
   uint64_t* drain2 = drain + 1;        // abort path of issuer 14
+  // packed: Q and dO tiles that end behind the sequence have landed in stage st, for the cleaning warp, which arrives on
+  // q_full and do_full in the copies' place; and: K and V are clean
+  uint64_t* part_full = drain2 + 1;
+  uint64_t* kv_clean = part_full + QS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   const uint32_t abort_flag = smem_u32(smem + L::kOffMisc + 4);  // CTA abort flag (shared)
 
@@ -221,7 +227,9 @@ __global__ void __launch_bounds__(512, 1)
       mbar_init(q_empty + i, 1);
       mbar_init(do_full + i, 1);
       mbar_init(do_empty + i, 1);
+      if (PACKED) mbar_init(part_full + i, 1);
     }
+    if (PACKED) mbar_init(kv_clean, 1);
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
     mbar_init(p_full, kEw / 32);  // one arrival per warp
@@ -276,17 +284,21 @@ __global__ void __launch_bounds__(512, 1)
         const int st = it % QS;
         const uint32_t ph = ((it / QS) - 1) & 1;
         const uint32_t q_bytes = PACKED ? kChunks * qtok * qheads * 128 : L::kTileBytes;
+        // a packed tile that ends behind the sequence goes through the cleaning warp
+        const bool part = PACKED && (qt + 1) * qtok > seq_len;
+        uint64_t* const q_bar = part ? part_full + st : q_full + st;
+        uint64_t* const do_bar = part ? part_full + st : do_full + st;
         // dO first: its slot frees earlier (after dV)
         if (it >= QS && !mbar_wait(do_empty + st, ph, abort_flag, p.status)) break;
-        mbar_expect_tx(do_full + st, q_bytes);
+        mbar_expect_tx(do_bar, part ? 2 * q_bytes : q_bytes);
         for (int c = 0; c < kChunks; ++c)
-          tma_load_3d(sdO + st * L::kTileBytes + c * L::kChunkBytes, &tmdO, do_full + st, c * 64,
+          tma_load_3d(sdO + st * L::kTileBytes + c * L::kChunkBytes, &tmdO, do_bar, c * 64,
                       PACKED ? hq : seq_start + qt * qtok, PACKED ? seq_start + qt * qtok : hq);
         ndo_issued = it + 1;
         if (it >= QS && !mbar_wait(q_empty + st, ph, abort_flag, p.status)) break;
-        mbar_expect_tx(q_full + st, q_bytes);
+        if (!part) mbar_expect_tx(q_bar, q_bytes);
         for (int c = 0; c < kChunks; ++c)
-          tma_load_3d(sQ + st * L::kTileBytes + c * L::kChunkBytes, &tmQ, q_full + st, c * 64,
+          tma_load_3d(sQ + st * L::kTileBytes + c * L::kChunkBytes, &tmQ, q_bar, c * 64,
                       PACKED ? hq : seq_start + qt * qtok, PACKED ? seq_start + qt * qtok : hq);
         nq_issued = it + 1;
       }
@@ -295,6 +307,7 @@ __global__ void __launch_bounds__(512, 1)
         for (int it = max(0, nq_issued - QS); it < nq_issued; ++it) mbar_drain(q_full + it % QS, (it / QS) & 1);
         for (int it = max(0, ndo_issued - QS); it < ndo_issued; ++it)
           mbar_drain(do_full + it % QS, (it / QS) & 1);
+        // (copies that the cleaning warp did not hand on: each of these waits 0.2 s at most, time enough for them to land)
       }
     } else if ((warp == 13 || warp == 14) && lane == 0) {
       // ============================================================== MMA issuers
@@ -320,6 +333,7 @@ __global__ void __launch_bounds__(512, 1)
       const uint64_t dSl_mn = smem_desc_sw128(smem_u32(sdSl), L::kChunkBytes, 1024);
       constexpr uint32_t kStage16 = L::kTileBytes >> 4;
       bool ok = mbar_wait(kv_full, 0, abort_flag, p.status);
+      if (PACKED && ok && (kt + 1) * kBN > kv_len) ok = mbar_wait(kv_clean, 0, abort_flag, p.status);
       for (int it = 0; ok && it < n_it; ++it) {
         const int st = it % QS;
         const uint32_t ph = (it / QS) & 1;
@@ -419,6 +433,52 @@ __global__ void __launch_bounds__(512, 1)
         mbar_drain(dr, 0);
       }
     }
+    if (PACKED && warp == 15) {
+      // ============================================================== cleaning warp
+      // Zeros into the rows behind the sequence's end, before an MMA reads them: what lies there is another
+      // sequence's, or anything, and 0 * NaN is NaN.  With Q = dO = 0 there P = exp2(0 - inf) = 0 and dS = 0.  The copies of
+      // such a tile complete on a barrier of this warp's own, and it hands the tile on.  (As a reader of every tile it
+      // slowed them all: 4 x 2048 tokens, 452 us for 405.)
+      auto wipe = [&](uint8_t* tile, int first, int rows) {
+        const int vecs = (rows - first) * 8;
+        for (int i = lane; i < kChunks * vecs; i += 32)
+          *reinterpret_cast<uint4*>(tile + i / vecs * L::kChunkBytes + first * 128 + i % vecs * 16) = make_uint4(0, 0, 0, 0);
+      };
+      bool ok = true;
+      const int keys = kv_len - kt * kBN;
+      if (keys < kBN) {
+        ok = mbar_wait_warp(kv_full, 0, abort_flag, p.status);
+        if (ok) {
+          wipe(sK, keys, kBN);
+          wipe(sV, keys, kBN);
+          fence_async_smem();
+          mbar_arrive_warp(kv_clean);
+        }
+      }
+      // the last query tile of each pass over the sequence, if it ends behind it
+      const int held = (seq_len - (n_q - 1) * qtok) * qheads;
+      uint32_t turns = 0;  // bit st: the parity of part_full[st]
+      for (int it = per_head - 1; ok && held < qtok * qheads && it < n_it; it += per_head) {
+        const int st = it % QS;
+        // This wait may last as long as the CTA runs, so it has no limit of its own: the other roles' waits have one, and
+        // where one runs out it raises the abort flag.
+        while (!mbar_try_wait(smem_u32(part_full + st), (turns >> st) & 1)) {
+          __nanosleep(200);
+          if (abort_read(abort_flag)) {
+            ok = false;
+            break;
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        turns ^= 1u << st;
+        wipe(sQ + st * L::kTileBytes, held, qtok * qheads);
+        wipe(sdO + st * L::kTileBytes, held, qtok * qheads);
+        fence_async_smem();
+        mbar_arrive_warp(do_full + st);
+        mbar_arrive_warp(q_full + st);
+      }
+    }
     __syncwarp();
   } else if (warp >= 8) {
     regs_dec<L::kRegsDq>();
@@ -441,7 +501,6 @@ __global__ void __launch_bounds__(512, 1)
       // the tile's first row in the accumulator, and the place of its turn counter
       const int row0 = PACKED ? 0 : static_cast<int>(static_cast<size_t>(hq0 + it / per_head) * N + seq_start) + qt * kBM;
       const size_t turn = PACKED ? static_cast<size_t>(tok0) * p.Hq + hq : static_cast<size_t>(row0);
-      const bool drop = PACKED && (t >= qtok * qheads || qt * qtok + t / qheads >= seq_len);  // not a row of this sequence
       if (!mbar_wait_warp(dq_full, it & 1, abort_flag, p.status)) { ok = false; break; }
       if (it >= 1 && !mbar_wait_warp(stage_free, (it - 1) & 1, abort_flag, p.status)) { ok = false; break; }
       tc_fence_after();
@@ -461,10 +520,6 @@ __global__ void __launch_bounds__(512, 1)
           tc_fence_before();
           mbar_arrive_warp(dq_free);  // the dQ columns may be overwritten once everything is loaded
         }
-        if constexpr (PACKED) {
-#pragma unroll
-          for (int g = 0; g < 32; ++g) r[g] = drop ? 0u : r[g];
-        }
         uint8_t* row = (c < L::kOwnStageChunks ? sStage + c * 16384 : sdSl + (c - L::kOwnStageChunks) * 16384) + t * 128;
 #pragma unroll
         for (int g = 0; g < 8; ++g)
@@ -472,6 +527,15 @@ __global__ void __launch_bounds__(512, 1)
         if (c + 1 < DP / 32) {
           tmem_ld_wait();
           tmem_reg_fence(nx);
+        }
+      }
+      if (PACKED && (qt + 1) * qtok > seq_len && qt * qtok + t / qheads >= seq_len) {
+        // not a row of this sequence: zeros, but for NaN among the sequence's own keys, which must not reach another's
+#pragma unroll 1
+        for (int c = 0; c < DP / 32; ++c) {
+          uint8_t* row = (c < L::kOwnStageChunks ? sStage + c * 16384 : sdSl + (c - L::kOwnStageChunks) * 16384) + t * 128;
+#pragma unroll 1
+          for (int g = 0; g < 8; ++g) *reinterpret_cast<uint4*>(row + (g << 4)) = make_uint4(0, 0, 0, 0);
         }
       }
       fence_async_smem();
@@ -579,16 +643,22 @@ __global__ void __launch_bounds__(512, 1)
     // Rows past the sequence read its last row and are replaced there.
     float lse_next = 0.f, d_next = 0.f;
     bool row_next = false;
+    // packed: the row's head and token in a query tile, its LSE [H, T] and its D [T, H]
+    const int my_tok = PACKED ? static_cast<int>(threadIdx.x) / qheads : static_cast<int>(threadIdx.x);
+    const int my_head = PACKED ? static_cast<int>(threadIdx.x) - my_tok * qheads : 0;
     auto load_rows = [&](int it) {
       if (threadIdx.x < 128 && it < n_it) {
         const int qt = qt0 + it % per_head;
-        const int lane_head = PACKED ? static_cast<int>(threadIdx.x) % qheads : 0;
-        const size_t row_base = static_cast<size_t>(hq0 + it / per_head * qheads + lane_head) * N + seq_start;
-        const int q = qt * qtok + static_cast<int>(threadIdx.x) / qheads;
-        row_next = q < seq_len && (!PACKED || static_cast<int>(threadIdx.x) < qtok * qheads);
+        const int head = hq0 + it / per_head * qheads + my_head;
+        const size_t row_base = static_cast<size_t>(head) * N + seq_start;
+        const int q = qt * qtok + my_tok;
+        row_next = q < seq_len && (!PACKED || my_tok < qtok);
         const size_t r = row_base + (row_next ? q : seq_len - 1);
         lse_next = p.lse[r];
-        d_next = p.delta[r];
+        if constexpr (PACKED)
+          d_next = p.delta[static_cast<size_t>(seq_start + (row_next ? q : seq_len - 1)) * p.Hq + head];
+        else
+          d_next = p.delta[r];
       }
     };
     load_rows(0);
@@ -606,34 +676,6 @@ __global__ void __launch_bounds__(512, 1)
       // ---- phase 1: P^T = exp2(S^T * scale * log2e - LSE * log2e), hi/lo back into TMEM
       if (!mbar_wait_warp(s_full, it & 1, abort_flag, p.status)) break;
       tc_fence_after();
-      // columns c < lim are masked: queries q < key - off under the causal mask (only tiles on the diagonal have any; a
-      // query row that sees no key at all has every column masked), and all 64 of a key past the sequence; the selects
-      // run only where a thread has such columns.  Packed: and columns c >= hi, rows behind the sequence's end
-      const int lim = !key_ok ? 64 : (CAUSAL ? (key - off - qt * qtok) * qheads - half * 64 : -1);
-      const int rows_held = PACKED ? min(qtok, seq_len - qt * qtok) * qheads : kBM;
-      const int hi = rows_held - half * 64;
-      if constexpr (PACKED) {
-        // S^T has been computed, so Q has landed and, behind the end, may go; dO when it has landed, too (dP^T may
-        // still read it: its columns there are not used).  K's rows behind the end, once.
-        const int st = it % QS;
-        if (rows_held < qtok * qheads) {
-          if (!mbar_wait_warp(do_full + st, (it / QS) & 1, abort_flag, p.status)) break;
-          const int vecs = (qtok * qheads - rows_held) * 8;
-          for (int i = threadIdx.x; i < kChunks * vecs; i += kEw) {
-            const int at = st * L::kTileBytes + i / vecs * L::kChunkBytes + rows_held * 128 + i % vecs * 16;
-            *reinterpret_cast<uint4*>(sQ + at) = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(sdO + at) = make_uint4(0, 0, 0, 0);
-          }
-          fence_async_smem();
-        }
-        const int keys = kv_len - kt * kBN;
-        if (it == 0 && keys < kBN) {
-          const int vecs = (kBN - keys) * 8;
-          for (int i = threadIdx.x; i < kChunks * vecs; i += kEw)
-            *reinterpret_cast<uint4*>(sK + i / vecs * L::kChunkBytes + keys * 128 + i % vecs * 16) = make_uint4(0, 0, 0, 0);
-          fence_async_smem();
-        }
-      }
       float pv[64];
       {
         uint32_t r0[32], r1[32];
@@ -648,6 +690,11 @@ __global__ void __launch_bounds__(512, 1)
         // first half of the dV MMAs runs while the second part is computed.
         const float4* nl4 = reinterpret_cast<const float4*>(lse_buf + half * 64);
         const uint64_t scl = f2_pack(sl2, sl2);
+        // queries q < key - off are masked under causal (only tiles on the diagonal have any; a
+        // query row that sees no key at all has every column masked), and keys past the
+        // sequence give P = 0: the selects run only where a thread has such columns
+        // columns c < lim are masked (a key past the sequence: all 64)
+        const int lim = !key_ok ? 64 : (CAUSAL ? (key - off - qt * qtok) * qheads - half * 64 : -1);
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           uint32_t(&r)[32] = cc == 0 ? r0 : r1;
@@ -667,12 +714,6 @@ __global__ void __launch_bounds__(512, 1)
           if (lim > 32 * cc) {
 #pragma unroll
             for (int i = 32 * cc; i < 32 * cc + 32; ++i) pv[i] = i < lim ? 0.f : pv[i];
-          }
-          if constexpr (PACKED) {
-            if (hi < 32 * cc + 32) {
-#pragma unroll
-              for (int i = 32 * cc; i < 32 * cc + 32; ++i) pv[i] = i >= hi ? 0.f : pv[i];
-            }
           }
           uint32_t ph[16], pl[16];
 #pragma unroll
@@ -712,12 +753,6 @@ __global__ void __launch_bounds__(512, 1)
           pv[i + 1] *= __uint_as_float(r[4 * j4 + 1]) + nd.y;
           pv[i + 2] *= __uint_as_float(r[4 * j4 + 2]) + nd.z;
           pv[i + 3] *= __uint_as_float(r[4 * j4 + 3]) + nd.w;
-        }
-        if constexpr (PACKED) {  // 0 times what is behind the end
-          if (lim > 32 * h || hi < 32 * h + 32) {
-#pragma unroll
-            for (int i = 32 * h; i < 32 * h + 32; ++i) pv[i] = i < lim || i >= hi ? 0.f : pv[i];
-          }
         }
         uint4 lo[4];
 #pragma unroll
@@ -764,13 +799,17 @@ template <typename T, int DP, bool CAUSAL, bool PACKED = false>
 cudaError_t launch_bwd_tc_t(const BwdMaps& maps, const BwdParams& p, cudaStream_t stream) {
   using L = BwdLayout<DP>;
   auto kern = bwd_tc_kernel<T, DP, CAUSAL, PACKED>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemAlloc);
+  static std::atomic<unsigned long long> ready{0};  // devices on which the kernel is set up
+  const cudaError_t e = once_per_device(ready, [&] {
+    const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemAlloc);
+    if (r != cudaSuccess) return r;
+    // The in-kernel register split assumes the launch allocation; never launch otherwise.
+    cudaFuncAttributes fa;
+    const cudaError_t a = cudaFuncGetAttributes(&fa, kern);
+    if (a != cudaSuccess) return a;
+    return fa.numRegs == static_cast<int>(L::kLaunchRegs) ? cudaSuccess : cudaErrorInvalidConfiguration;
+  });
   if (e != cudaSuccess) return e;
-  // The in-kernel register split assumes the launch allocation; never launch otherwise.
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, kern);
-  if (e != cudaSuccess) return e;
-  if (fa.numRegs != static_cast<int>(L::kLaunchRegs)) return cudaErrorInvalidConfiguration;
   if constexpr (PACKED) {  // the number of tiles is on the device: a CTA for each that there may be
     const long long most = packed_bound(p.N, p.nseq, p.max_seqlen, kBN) * p.Hkv;
     if (most > 0x7fffffffLL) return cudaErrorInvalidValue;

@@ -901,7 +901,8 @@ __global__ void __launch_bounds__(512, 1)
         const float nm = KV8 ? offset - mb : -mb;
         if constexpr (CLEAN) {
           // The values of this group's keys behind the last one become zeros: there P = 0, but 0 * NaN is NaN.  The
-          // tile must have landed; the PV issuers read it after this group's p_full.
+          // tile must have landed; the PV issuers read it after this group's p_full.  (Between the exponentials and
+          // the hand-over of P, where the wait would cost less, it slowed every tile: 144 us for 123 on 4 x 2048 tokens.)
           const int held = it.seq_len - key0;  // warp-uniform
           if (held < 64) {
             if (!mbar_wait_warp(v_full + t % SV, (t / SV) & 1, abort_flag, p.status)) { ok = false; break; }
@@ -1012,13 +1013,17 @@ template <typename T, int DP, bool CAUSAL, int MODE>
 cudaError_t launch_fwd_tc_t(const FwdMaps& maps, const FwdParams& p, cudaStream_t stream) {
   using L = FwdLayout<DP, MODE>;
   auto kern = fwd_tc_kernel<T, DP, CAUSAL, MODE>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemAlloc);
+  static std::atomic<unsigned long long> ready{0};  // devices on which the kernel is set up
+  const cudaError_t e = once_per_device(ready, [&] {
+    const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemAlloc);
+    if (r != cudaSuccess) return r;
+    // The in-kernel register split assumes the launch allocation; never launch otherwise.
+    cudaFuncAttributes fa;
+    const cudaError_t a = cudaFuncGetAttributes(&fa, kern);
+    if (a != cudaSuccess) return a;
+    return fa.numRegs == static_cast<int>(L::kLaunchRegs) ? cudaSuccess : cudaErrorInvalidConfiguration;
+  });
   if (e != cudaSuccess) return e;
-  // The in-kernel register split assumes the launch allocation; never launch otherwise.
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, kern);
-  if (e != cudaSuccess) return e;
-  if (fa.numRegs != static_cast<int>(L::kLaunchRegs)) return cudaErrorInvalidConfiguration;
   if constexpr (MODE == kModePacked) {  // the number of items is on the device: `tiles` is its bound
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

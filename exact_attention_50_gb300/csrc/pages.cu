@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const PagesParams 
   Team t;
   const int rows = (p.B + t.n - 1) / t.n, part = (p.n + t.n - 1) / t.n;
   int* const owner = dyn;             // [rows]: of dst rows rank, rank + n, ...
-  int* const fresh = owner + rows;    // [part]: the copy's page; -1: none; -2: the pair is refused
+  int* const fresh = owner + rows;    // [part]: the copy's page; -1: none; -2: the pair is refused; -3: still to be chosen
   int* const len = fresh + part;      // [part]
   for (int i = threadIdx.x; i < rows; i += kThreads) owner[i] = 0x7fffffff;
   copy_ints(t, p.table, p.table_out, static_cast<long long>(p.B) * p.M);
@@ -191,43 +191,38 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const PagesParams 
   const auto is_free = [refs](int i) { return refs[i] <= 0; };
   Ranks ranks;
   ranks.count(t, s, p.P, is_free);  // (its barrier: the owners are complete)
-  int done = 0;  // tails of this CTA's pairs so far
-  int want = 0;
-  // pass 0 counts this CTA's tails, pass 1 gives them their pages
-  for (int pass = 0; pass < 2; ++pass) {
-    int base = 0;
-    if (pass == 1) base = t.before(&s.mine2, done, want);
-    done = 0;
-    for (int q0 = k0; q0 < k1; q0 += kThreads) {
-      const int k = q0 + static_cast<int>(threadIdx.x);
-      bool ok = false, tail = false;
+  int tails = 0;  // of this CTA's pairs
+  for (int q0 = k0; q0 < k1; q0 += kThreads) {
+    const int k = q0 + static_cast<int>(threadIdx.x);
+    bool ok = false, tail = false;
+    if (k < k1) {
+      const int src = p.src[k], dst = p.dst[k];
       int L = 0;
-      if (k < k1) {
-        const int src = p.src[k], dst = p.dst[k];
-        ok = src >= 0 && src < p.B && dst >= 0 && dst < p.B;
-        if (ok) {
-          L = p.lens[src];
-          ok = *t.cl.map_shared_rank(owner + dst / t.n, dst % t.n) == k && p.lens[dst] == 0 && L >= 0 && pages_of(L, p.page) <= p.M;
-          if (ok && p.M > 0) ok = p.table[static_cast<size_t>(dst) * p.M] < 0;
-          if (ok && L > 0) {
-            const int e = p.table[static_cast<size_t>(src) * p.M + (L - 1) / p.page];
-            ok = e >= 0 && e < p.P;
-          }
-        }
-        tail = ok && L % p.page != 0;
+      ok = src >= 0 && src < p.B && dst >= 0 && dst < p.B;
+      if (ok) {
+        L = p.lens[src];
+        const int held = p.lens[dst], e = p.M > 0 ? p.table[static_cast<size_t>(dst) * p.M] : -1;
+        ok = *t.cl.map_shared_rank(owner + dst / t.n, dst % t.n) == k && held == 0 && e < 0 && L >= 0 && pages_of(L, p.page) <= p.M;
       }
-      int all;
-      const int r = block_scan(tail ? 1 : 0, s.warp, all);
-      if (pass == 1 && k < k1) {
-        const int at = base + done + r;
-        int f = ok ? -1 : -2;
-        if (tail) f = at < ranks.total ? ranks.select(t, s, p.P, at, is_free) : -2;
-        fresh[k - k0] = f;
-        len[k - k0] = L;
-        if (f == -2) raise_status(p.status, ATTN_ERR_DEVICE_INPUT);
+      if (ok && L > 0) {
+        const int e = p.table[static_cast<size_t>(src) * p.M + (L - 1) / p.page];
+        ok = e >= 0 && e < p.P;
       }
-      done += all;
+      tail = ok && L % p.page != 0;
+      fresh[k - k0] = !ok ? -2 : tail ? -3 : -1;
+      len[k - k0] = L;
     }
+    tails += __syncthreads_count(tail);
+  }
+  int want, done = 0;
+  const int base = t.before(&s.mine2, tails, want);
+  for (int q0 = k0; q0 < k1; q0 += kThreads) {
+    const int k = q0 + static_cast<int>(threadIdx.x);
+    int f = k < k1 ? fresh[k - k0] : 0, all;
+    const int at = base + done + block_scan(f == -3 ? 1 : 0, s.warp, all);
+    if (f == -3) fresh[k - k0] = f = at < ranks.total ? ranks.select(t, s, p.P, at, is_free) : -2;
+    if (f == -2) raise_status(p.status, ATTN_ERR_DEVICE_INPUT);
+    done += all;
   }
   t.cl.sync();  // every page has been chosen and every length read: the state may change
   const int lane = threadIdx.x & 31;
@@ -273,12 +268,16 @@ __global__ void __launch_bounds__(kThreads) pages_reserve_kernel(const PagesPara
   const int lane = threadIdx.x & 31;
   for (int b = b0 + (threadIdx.x >> 5); b < b1; b += kThreads / 32) {
     const size_t row = static_cast<size_t>(b) * p.M;
-    int h = p.M;  // the first negative entry
-    for (int i0 = 0; i0 < p.M; i0 += 32) {
-      const unsigned none = __ballot_sync(0xffffffffu, i0 + lane < p.M && p.table[row + min(i0 + lane, p.M - 1)] < 0);
-      if (none) {
-        h = i0 + __ffs(none) - 1;
-        break;
+    int h = p.M;  // the first negative entry; the row is copied on the way, 128 entries in flight
+    for (int i0 = 0; i0 < p.M; i0 += 128) {
+      int e[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) e[u] = i0 + 32 * u + lane < p.M ? p.table[row + i0 + 32 * u + lane] : 0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const unsigned none = __ballot_sync(0xffffffffu, e[u] < 0);
+        if (none && h == p.M) h = i0 + 32 * u + __ffs(none) - 1;
+        if (i0 + 32 * u + lane < p.M && p.table != p.table_out) p.table_out[row + i0 + 32 * u + lane] = e[u];
       }
     }
     if (lane == 0) {
@@ -290,7 +289,6 @@ __global__ void __launch_bounds__(kThreads) pages_reserve_kernel(const PagesPara
       need[b - b0] = bad ? 0 : max(0, static_cast<int>(want) - h);
     }
   }
-  copy_ints(t, p.table, p.table_out, static_cast<long long>(p.B) * p.M);
   copy_ints(t, p.refs, p.refs_out, p.P);
   const int32_t* const refs = p.refs;
   const auto is_free = [refs](int i) { return refs[i] <= 0; };
@@ -487,6 +485,14 @@ cudaError_t launch_books(K kern, const PagesParams& p, long long ints, size_t sm
   while (n < kMaxCluster && ints > 8192LL * n) n *= 2;
   size_t smem = smem_of(p, n);
   while (n < kMaxCluster && smem > 32 * 1024) smem = smem_of(p, n *= 2);
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  if (n == 1) {  // a cluster of one
+    kern<<<1, kThreads, smem, stream>>>(p);
+    return cudaGetLastError();
+  }
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = n;
@@ -498,10 +504,6 @@ cudaError_t launch_books(K kern, const PagesParams& p, long long ints, size_t sm
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 size_t no_smem(const PagesParams&, int) { return 0; }
