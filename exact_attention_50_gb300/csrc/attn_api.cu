@@ -1138,6 +1138,7 @@ attn_status_t attn_fwd_varlen_gqa(const void* q, const void* k, const void* v, c
   const PackedTile t = packed_tile(p.G, total_tokens, nseq);
   p.heads = t.heads;
   p.tile_tokens = t.tokens;
+  p.groups_per_kv = p.G / t.heads;
   p.open_end = 1;
   int* const head = static_cast<int*>(workspace);
   int4* const tiles = reinterpret_cast<int4*>(static_cast<char*>(workspace) + kListHead);

@@ -141,9 +141,10 @@ __device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int idx) {
   it.split = 0;
   if constexpr (MODE == kModePacked) {
     const int groups = p.Hq / p.heads;
-    const int4 tile = p.tiles[idx / groups];
-    it.b = 0;
-    it.h = idx % groups;  // the item's head group: query heads [h heads, h heads + heads)
+    const int entry = idx / groups;
+    const int4 tile = p.tiles[entry];
+    it.h = idx - entry * groups;  // the item's head group: query heads [h heads, h heads + heads)
+    it.b = it.h / p.groups_per_kv;  // its kv head
     it.seq_start = tile.x;
     it.seq_len = tile.y;
     it.qt = tile.z;
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(512, 1)
               for (int c = 0; c < kChunks; ++c) {
                 uint8_t* dst = sK + st * L::kTileBytes + c * L::kChunkBytes;
                 if constexpr (PACKED)
-                  tma_load_3d(dst, &tmK, k_full + st, c * 64, it.seq_start + ck.j * kBN, it.h * p.heads / p.G);
+                  tma_load_3d(dst, &tmK, k_full + st, c * 64, it.seq_start + ck.j * kBN, it.b);
                 else if constexpr (VARLEN)
                   tma_load_4d(dst, &tmK, k_full + st, c * 64, it.h, 1, it.seq_start + ck.j * kBN);
                 else if constexpr (KV)
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(512, 1)
               for (int c = 0; c < kChunks; ++c) {
                 uint8_t* dst = sV + st * L::kTileBytes + c * L::kChunkBytes;
                 if constexpr (PACKED)
-                  tma_load_3d(dst, &tmV, v_full + st, c * 64, it.seq_start + cv.j * kBN, it.h * p.heads / p.G);
+                  tma_load_3d(dst, &tmV, v_full + st, c * 64, it.seq_start + cv.j * kBN, it.b);
                 else if constexpr (VARLEN)
                   tma_load_4d(dst, &tmV, v_full + st, c * 64, it.h, 2, it.seq_start + cv.j * kBN);
                 else if constexpr (KV)
@@ -608,7 +609,9 @@ __global__ void __launch_bounds__(512, 1)
     const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const bool storer = row == 0 && tile_out;  // issues the tile stores of staged items
     if (storer) tma_prefetch_desc(&tmO);
-    uint32_t kv = 0, ic = 0, nt[2] = {0, 0};  // nt: per Q slot, items stored by tiles (o_staged phases)
+    uint32_t kv = 0, ic = 0, nt = 0;  // nt: bit per Q slot, the parity of the items stored by tiles (o_staged phases)
+    // packed: this row's token and head in a tile
+    const int tile_tok = PACKED ? row / p.heads : row, tile_head = PACKED ? row - tile_tok * p.heads : 0;
     bool ok = true;
     for (int k = 0; ok && k * static_cast<int>(gridDim.x) < n_items; ++k) {
       const int idx = cta_item<MODE>(k);
@@ -616,7 +619,7 @@ __global__ void __launch_bounds__(512, 1)
       const FwdItem it = fwd_item<CAUSAL, MODE>(p, idx);
       if (!it.valid) continue;
       // relative to the sequence (KV cache: to the R rows); packed: the row's token
-      const int q_row = PACKED ? it.qt * p.tile_tokens + row / p.heads : it.qt * kBM + row;
+      const int q_row = PACKED ? it.qt * p.tile_tokens + tile_tok : it.qt * kBM + row;
       kv += it.n_kv;
       if (!mbar_wait_warp(stats_ready, ic & 1, abort_flag, p.status)) { ok = false; break; }
       const float2 s0 = sStats[row], s1 = sStats[128 + row];
@@ -631,8 +634,8 @@ __global__ void __launch_bounds__(512, 1)
       const uint32_t t_last = kv - 1;
       if (!mbar_wait_warp(pv_done + (t_last & 1), (t_last >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
       tc_fence_after();
-      const bool valid = q_row < (KV ? p.R : it.seq_len) && (!PACKED || row < p.tile_tokens * p.heads);
-      const int q_head = PACKED ? it.h * p.heads + row % p.heads : it.h;
+      const bool valid = q_row < (KV ? p.R : it.seq_len) && (!PACKED || tile_tok < p.tile_tokens);
+      const int q_head = PACKED ? it.h * p.heads + tile_head : it.h;
       size_t row_off;
       // a KV cache range writes its partial output in fp32 to its slice of the split buffer
       const size_t kv_row = KV ? (static_cast<size_t>(it.split) * p.B * p.Hkv + static_cast<size_t>(it.b) * p.Hkv + it.h) * p.R + q_row : 0;
@@ -710,7 +713,9 @@ __global__ void __launch_bounds__(512, 1)
         // for the Q of the item after next
         const uint32_t qs = ic % SQ;
         if (storer) {
-          if (!mbar_wait(o_staged + qs, nt[qs]++ & 1, abort_flag, p.status)) {
+          const uint32_t turn = (nt >> qs) & 1;
+          nt ^= 1u << qs;
+          if (!mbar_wait(o_staged + qs, turn, abort_flag, p.status)) {
             ok = false;
           } else {
             for (int c = 0; c < kChunks; ++c) {
@@ -771,6 +776,7 @@ __global__ void __launch_bounds__(512, 1)
     const int row = threadIdx.x & 127;        // TMEM lane
     const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t tOg = tl + L::kColO + grp * DP;  // this group's accumulator O_g
+    const int tile_tok = PACKED ? row / p.heads : row;  // packed: this row's token in a tile
     uint32_t kv = 0, ic = 0;
     bool ok = true;
     for (int k = 0; ok && k * static_cast<int>(gridDim.x) < n_items; ++k) {
@@ -779,7 +785,7 @@ __global__ void __launch_bounds__(512, 1)
       const FwdItem it = fwd_item<CAUSAL, MODE>(p, idx);
       if (!it.valid) continue;
       // relative to the sequence (KV cache: to the R rows); packed: the row's token
-      const int q_row = PACKED ? it.qt * p.tile_tokens + row / p.heads : it.qt * kBM + row;
+      const int q_row = PACKED ? it.qt * p.tile_tokens + tile_tok : it.qt * kBM + row;
       // the last key this row sees: the diagonal under the causal mask, the sequence's end;
       // for a KV cache row (query q_row % Nq) the same, aligned to the cache's last Nq keys
       int last_key;

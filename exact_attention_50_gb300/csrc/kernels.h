@@ -46,7 +46,7 @@ struct FwdParams {
   // as launch_packed_tiles leaves them, tokens end at head[1]
   const int4* tiles;
   const int* head;
-  int heads, tile_tokens;
+  int heads, tile_tokens, groups_per_kv;  // groups_per_kv: G / heads
   // fp32 varlen and packed forward: element strides from token to token; may tokens lie behind the last sequence
   long long tok_q, tok_k, tok_v;
   int open_end;
