@@ -452,23 +452,15 @@ def kvcache_evict(k_cache, v_cache, weights, keep: int, recent: int, cache_seqle
 
 
 # ------------------------------------------------------------- packed sequences with grouped heads
-def _token_strides(dev: int, *tensors):
-    """The distances from token to token of [T,H,d] tensors on GPU `dev` whose rows of one token lie one behind the other,
-    or None."""
-    strides = []
-    for t in tensors:
-        if t.get_device() != dev or dev < 0 or t.dim() != 3:
-            return None
-        T, H, d = t.shape
-        a, b, c = t.stride()
-        if T * H * d == 0 or t.is_contiguous():
-            a = H * d
-        elif (c != 1 and d > 1) or (b != d and H > 1):
-            return None
-        elif T == 1:
-            a = H * d
-        strides.append(a)
-    return strides
+def _token_stride(t) -> int:
+    """The distance from token to token of a [T,H,d] tensor whose rows of one token lie one behind the other, or -1."""
+    T, H, d = t.shape
+    if t.is_contiguous():
+        return H * d
+    a, b, c = t.stride()
+    if (c != 1 and d > 1) or (b != d and H > 1):
+        return -1
+    return H * d if T == 1 else a
 
 
 def _explain_packed(q, k, v, cu_seqlens, *more):
@@ -484,7 +476,7 @@ def _explain_packed(q, k, v, cu_seqlens, *more):
             raise TypeError(f"{name} has dtype {t.dtype}, expected {q.dtype}")
         if t.device != q.device:
             raise ValueError(f"{name} must be on q's device")
-        if _token_strides(t.get_device(), t) is None:
+        if _token_stride(t) < 0:
             raise ValueError(f"{name}'s heads and columns must lie one behind the other (any stride from token to token)")
     for t, name, dtype, optional in ((cu_seqlens, "cu_seqlens", torch.int32, False),) + more:
         if t is None and optional:
@@ -497,18 +489,20 @@ def _explain_packed(q, k, v, cu_seqlens, *more):
 
 def _packed_sizes(q, k, v, cu_seqlens, max_seqlen):
     T, Hq, d = q.shape
-    Tk, Hkv, dk = k.shape
-    if v.shape != k.shape or Tk != T or dk != d:
+    shape, n = k.shape, cu_seqlens.shape
+    Hkv = shape[1]
+    if v.shape != shape or shape != (T, Hkv, d):
         raise ValueError("q must be [total_tokens,Hq,d] and k, v [total_tokens,Hkv,d]")
-    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+    if len(n) != 1 or n[0] < 2:
         raise ValueError("cu_seqlens must be 1-D with batch_size + 1 entries")
     if Hq < 1 or Hkv < 1 or Hq % Hkv:
         raise ValueError("the query heads must be a multiple of the kv heads")
     max_seqlen = int(max_seqlen)
     if max_seqlen < 0:
         raise ValueError("max_seqlen must not be negative")
-    _check_sizes(q.shape, cu_seqlens.shape, (max_seqlen,))
-    return T, Hq, Hkv, d, cu_seqlens.shape[0] - 1, max_seqlen
+    if T >= 2 ** 31 or Hq >= 2 ** 31 or d >= 2 ** 31 or n[0] > 2 ** 31 or max_seqlen >= 2 ** 31:
+        raise ValueError("every size must be below 2**31")
+    return T, Hq, Hkv, d, n[0] - 1, max_seqlen
 
 
 @functools.lru_cache(maxsize=1024)
@@ -524,21 +518,22 @@ def fwd_varlen_gqa(q, k, v, cu_seqlens, max_seqlen: int, causal: bool, scale=Non
     need a workspace each.  Returns (out [T,Hq,d], lse [Hq,T] or None)."""
     f32, i32 = torch.float32, torch.int32
     try:
-        dev = q.get_device()
-        strides = _token_strides(dev, q, k, v)
-        fit = strides is not None and _fit(dev, cu_seqlens, workspace) and k.dtype is q.dtype and v.dtype is q.dtype and cu_seqlens.dtype is i32
-    except AttributeError:  # not a tensor
+        dev, dt = q.get_device(), q.dtype
+        qs, ks, vs = _token_stride(q), _token_stride(k), _token_stride(v)
+        fit = (dev == k.get_device() == v.get_device() and _fit(dev, cu_seqlens, workspace) and qs >= 0 and ks >= 0 and vs >= 0
+               and k.dtype is dt and v.dtype is dt and cu_seqlens.dtype is i32)
+    except (AttributeError, ValueError):  # not a tensor, not of three dimensions
         fit = False
     if not fit:
         _explain_packed(q, k, v, cu_seqlens, (workspace, "workspace", None, True))
     T, Hq, Hkv, d, nseq, max_seqlen = _packed_sizes(q, k, v, cu_seqlens, max_seqlen)
     dtype, device = _dtype_code(q), q.device
-    out = torch.empty((T, Hq, d), dtype=f32 if out_f32 else q.dtype, device=device)
+    out = torch.empty((T, Hq, d), dtype=f32 if out_f32 else dt, device=device)
     lse = torch.empty((Hq, T), dtype=f32, device=device) if with_lse else None
     if workspace is None:
         workspace = torch.empty(max(1, _varlen_gqa_workspace_bytes(nseq, T, max_seqlen, Hq, Hkv)), dtype=torch.uint8, device=device)
     st = _on_device(dev, _lib.attn_fwd_varlen_gqa, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), nseq, T, max_seqlen,
-                    out.data_ptr(), lse.data_ptr() if with_lse else None, workspace.data_ptr(), workspace.nbytes, Hq, Hkv, d, *strides, causal,
+                    out.data_ptr(), lse.data_ptr() if with_lse else None, workspace.data_ptr(), workspace.nbytes, Hq, Hkv, d, qs, ks, vs, causal,
                     _scale_arg(scale), dtype, _lib.ATTN_FLAG_OUT_F32 if out_f32 else 0)
     _lib._check(st, "attn_fwd_varlen_gqa")
     return out, lse
@@ -551,11 +546,11 @@ def bwd_varlen_gqa(q, k, v, out, lse, dout, cu_seqlens, max_seqlen: int, causal:
     last sequence."""
     f32, i32 = torch.float32, torch.int32
     try:
-        dev = q.get_device()
-        strides = _token_strides(dev, q, k, v)
-        fit = (strides is not None and _fit(dev, cu_seqlens, out, lse, dout, workspace) and k.dtype is q.dtype and v.dtype is q.dtype
-               and out.dtype is q.dtype and dout.dtype is q.dtype and lse.dtype is f32 and cu_seqlens.dtype is i32)
-    except AttributeError:  # not a tensor
+        dev, dt = q.get_device(), q.dtype
+        qs, ks, vs = _token_stride(q), _token_stride(k), _token_stride(v)
+        fit = (dev == k.get_device() == v.get_device() and _fit(dev, cu_seqlens, out, lse, dout, workspace) and qs >= 0 and ks >= 0 and vs >= 0
+               and k.dtype is dt and v.dtype is dt and out.dtype is dt and dout.dtype is dt and lse.dtype is f32 and cu_seqlens.dtype is i32)
+    except (AttributeError, ValueError):  # not a tensor, not of three dimensions
         fit = False
     if not fit:
         dt = getattr(q, "dtype", None)
@@ -573,7 +568,7 @@ def bwd_varlen_gqa(q, k, v, out, lse, dout, cu_seqlens, max_seqlen: int, causal:
         workspace = torch.empty(max(1, need), dtype=torch.uint8, device=device)
     st = _on_device(dev, _lib.attn_bwd_varlen_gqa, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(), lse.data_ptr(),
                     cu_seqlens.data_ptr(), nseq, T, max_seqlen, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
-                    workspace.nbytes, Hq, Hkv, d, *strides, causal, _scale_arg(scale), dtype, _bwd_flags(out_f32, deterministic))
+                    workspace.nbytes, Hq, Hkv, d, qs, ks, vs, causal, _scale_arg(scale), dtype, _bwd_flags(out_f32, deterministic))
     _lib._check(st, "attn_bwd_varlen_gqa")
     return dq, dk, dv
 
@@ -609,9 +604,9 @@ def fwd_kvpages(q, k_pages, v_pages, page_table, cache_seqlens, causal: bool = F
     run at the same time need a workspace each.  Returns (o [B,Hq,Nq,d], lse [B,Hq,Nq] or None)."""
     i32 = torch.int32
     try:
-        dev = q.get_device()
-        fit = (_fit(dev, q, k_pages, v_pages, page_table, cache_seqlens, workspace) and k_pages.dtype is q.dtype and v_pages.dtype is q.dtype
-               and page_table.dtype is i32 and cache_seqlens is not None and cache_seqlens.dtype is i32)
+        dev, dt = q.get_device(), q.dtype
+        fit = (_fit(dev, q, k_pages, v_pages, page_table, cache_seqlens, workspace) and k_pages.dtype is dt and v_pages.dtype is dt
+               and page_table.dtype is i32 and cache_seqlens.dtype is i32)
     except AttributeError:  # not a tensor
         fit = False
     if not fit:
@@ -619,14 +614,14 @@ def fwd_kvpages(q, k_pages, v_pages, page_table, cache_seqlens, causal: bool = F
         _explain((q, "q", None, False), (k_pages, "k_pages", dt, False), (v_pages, "v_pages", dt, False), (page_table, "page_table", i32, False),
                  (cache_seqlens, "cache_seqlens", i32, False), (workspace, "workspace", None, True))
     P, Hkv, page, d = _check_pools(k_pages, v_pages)
-    shape = q.shape
+    shape, table = q.shape, page_table.shape
     if len(shape) != 4 or shape[3] != d:
         raise ValueError("q must be [B,Hq,Nq,d], with the pages' head_dim")
-    B, Hq, Nq = shape[0], shape[1], shape[2]
-    tb, M = _check_table(page_table)
-    if tb != B:
+    B, Hq, Nq, _ = shape
+    if len(table) != 2 or table[0] != B:
         raise ValueError("page_table must be [B,max_pages], with q's batch")
-    _check_sizes(shape)
+    M = table[1]
+    _check_sizes(shape, table)
     if max_seqlen is None:
         max_seqlen = 0
     elif not 1 <= max_seqlen < 2 ** 31:
@@ -636,7 +631,7 @@ def fwd_kvpages(q, k_pages, v_pages, page_table, cache_seqlens, causal: bool = F
     lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=device) if with_lse else None
     code = _dtype_code(q)
     if workspace is None:
-        need = kvpages_workspace_bytes(B, Hq, Hkv, Nq, M, page, d, q.dtype, max_seqlen)
+        need = kvpages_workspace_bytes(B, Hq, Hkv, Nq, M, page, d, dt, max_seqlen)
         workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
     st = _on_device(dev, _lib.attn_fwd_kvpages, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
                     _lens_ptr(cache_seqlens, "cache_seqlens", B), o.data_ptr(), lse.data_ptr() if with_lse else None,
@@ -652,17 +647,17 @@ def kvpages_append(k_pages, v_pages, page_table, k_new, v_new, cu_seqlens, cache
     cache_seqlens[b] (int32 [B]; None: empty sequences).  The caller advances the lengths."""
     i32 = torch.int32
     try:
-        dev = k_pages.get_device()
-        strides = _token_strides(dev, k_new, v_new)
-        fit = (strides is not None and _fit(dev, k_pages, v_pages, page_table, cu_seqlens, cache_seqlens) and v_pages.dtype is k_pages.dtype
-               and k_new.dtype is k_pages.dtype and v_new.dtype is k_pages.dtype and page_table.dtype is i32 and cu_seqlens.dtype is i32
+        dev, dt = k_pages.get_device(), k_pages.dtype
+        ks, vs = _token_stride(k_new), _token_stride(v_new)
+        fit = (dev == k_new.get_device() == v_new.get_device() and _fit(dev, k_pages, v_pages, page_table, cu_seqlens, cache_seqlens) and ks >= 0
+               and vs >= 0 and v_pages.dtype is dt and k_new.dtype is dt and v_new.dtype is dt and page_table.dtype is i32 and cu_seqlens.dtype is i32
                and (cache_seqlens is None or cache_seqlens.dtype is i32))
-    except AttributeError:  # not a tensor
+    except (AttributeError, ValueError):  # not a tensor, not of three dimensions
         fit = False
     if not fit:
         dt = getattr(k_pages, "dtype", None)
         for t, name in ((k_new, "k_new"), (v_new, "v_new")):
-            if isinstance(t, torch.Tensor) and t.is_cuda and _token_strides(t.get_device(), t) is None:
+            if isinstance(t, torch.Tensor) and t.is_cuda and (t.dim() != 3 or _token_stride(t) < 0):
                 raise ValueError(f"{name} must be [total_tokens,Hkv,d], heads and columns one behind the other")
         _explain((k_pages, "k_pages", None, False), (v_pages, "v_pages", dt, False), (page_table, "page_table", i32, False),
                  *((t.contiguous() if isinstance(t, torch.Tensor) else t, name, dt, False) for t, name in ((k_new, "k_new"), (v_new, "v_new"))),
@@ -676,39 +671,42 @@ def kvpages_append(k_pages, v_pages, page_table, k_new, v_new, cu_seqlens, cache
         raise ValueError("cu_seqlens must be int32 [B+1]")
     _check_sizes(k_new.shape)
     st = _on_device(dev, _lib.attn_kvpages_append, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), k_new.data_ptr(),
-                    v_new.data_ptr(), cu_seqlens.data_ptr(), _lens_ptr(cache_seqlens, "cache_seqlens", B), B, T, Hkv, M, P, page, d, *strides,
+                    v_new.data_ptr(), cu_seqlens.data_ptr(), _lens_ptr(cache_seqlens, "cache_seqlens", B), B, T, Hkv, M, P, page, d, ks, vs,
                     _dtype_code(k_new))
     _lib._check(st, "attn_kvpages_append")
 
 
-def _books(dev, page, tensors, names, out, like):
-    """Checks the int32 arrays of a call on the books, the table first and refs second, then `names` for the others; and the
-    outputs: `out`, or new ones shaped like `like`.  Returns (B, max_pages, pages, outputs)."""
+def _books(page_table, refs, others, names, page, out, like):
+    """Checks the int32 arrays of a call on the books (names: those of the others) and the outputs: `out`, or new ones shaped
+    like `like`.  Returns (device, B, max_pages, pages, outputs)."""
     i32 = torch.int32
-    for t in tensors:
-        if not isinstance(t, torch.Tensor) or t.dtype is not i32 or t.get_device() != dev or dev < 0 or not t.is_contiguous():
-            _explain(*((x, n, i32, False) for x, n in zip(tensors, ("page_table", "refs") + names)))
+    try:
+        dev = page_table.get_device()
+        fit = page_table.dtype is i32 and refs.dtype is i32 and _fit(dev, page_table, refs, *others)
+        for t in others:
+            fit = fit and t.dtype is i32
+    except AttributeError:  # not a tensor
+        fit = False
+    if not fit:
+        _explain((page_table, "page_table", i32, False), (refs, "refs", i32, False), *((t, n, i32, False) for t, n in zip(others, names)))
+    shape, pages = page_table.shape, refs.shape
+    if len(shape) != 2 or len(pages) != 1:
+        raise ValueError("page_table must be [B,max_pages] and refs [pages]")
     if page not in (16, 32, 64, 128):
         raise ValueError("page must be 16, 32, 64 or 128")
-    shape = tensors[0].shape
-    if len(shape) != 2:
-        raise ValueError("page_table must be [B,max_pages]")
-    B, M = shape
-    refs = tensors[1].shape
-    if len(refs) != 1:
-        raise ValueError("refs must be int32 [pages]")
-    if B >= 2 ** 31 or M >= 2 ** 31 or refs[0] >= 2 ** 31:
-        raise ValueError("every size must be below 2**31")
+    _check_sizes(shape, pages)
     if out is None:
-        return B, M, refs[0], tuple([torch.empty_like(t) for t in like])
-    out = tuple(out)
-    if len(out) != len(like):
-        raise ValueError(f"out must hold {len(like)} tensors")
-    for t, x in zip(out, like):
-        _require(t, "out", i32)
-        if t.shape != x.shape or t.device != x.device:
-            raise ValueError("out must be shaped like the arrays that it follows, on their device")
-    return B, M, refs[0], out
+        out = tuple([torch.empty_like(t) for t in like])
+    else:
+        out = tuple(out)
+        if len(out) != len(like):
+            raise ValueError(f"out must hold {len(like)} tensors")
+        for t, x in zip(out, like):
+            if t is not x:
+                _require(t, "out", i32)
+                if t.shape != x.shape or t.device != x.device:
+                    raise ValueError("out must be shaped like the arrays that it follows, on their device")
+    return dev, shape[0], shape[1], pages[0], out
 
 
 def _of_rows(B, *named):
@@ -717,19 +715,12 @@ def _of_rows(B, *named):
             raise ValueError(f"{n} must be int32 [B]")
 
 
-def _device_of(t, name: str) -> int:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor")
-    return t.get_device()
-
-
 def kvpages_free(page_table, cache_seqlens, refs, keep_seqlens, page: int, out=None):
     """Cuts each sequence to its first keep_seqlens[b] tokens (0 ends it) and gives back the pages behind them.  page_table
     int32 [B,max_pages], cache_seqlens and keep_seqlens int32 [B], refs int32 [pages].  out: (page_table, cache_seqlens,
     refs) to write to, which may be the inputs (None: new ones).  Returns those three."""
-    dev = _device_of(page_table, "page_table")
-    B, M, P, o = _books(dev, page, (page_table, refs, cache_seqlens, keep_seqlens), ("cache_seqlens", "keep_seqlens"), out,
-                        (page_table, cache_seqlens, refs))
+    dev, B, M, P, o = _books(page_table, refs, (cache_seqlens, keep_seqlens), ("cache_seqlens", "keep_seqlens"), page, out,
+                             (page_table, cache_seqlens, refs))
     _of_rows(B, (cache_seqlens, "cache_seqlens"), (keep_seqlens, "keep_seqlens"))
     st = _on_device(dev, _lib.attn_kvpages_free, page_table.data_ptr(), cache_seqlens.data_ptr(), refs.data_ptr(), keep_seqlens.data_ptr(),
                     o[0].data_ptr(), o[1].data_ptr(), o[2].data_ptr(), B, M, P, page)
@@ -741,13 +732,13 @@ def kvpages_fork(page_table, cache_seqlens, refs, src, dst, page: int, out=None)
     """Makes the empty rows dst[i] copies of the rows src[i] (int32 [n]): full pages are shared, a partly filled last page is
     replaced by a free one.  out: (page_table, cache_seqlens, refs) as for kvpages_free.  Returns (page_table, cache_seqlens,
     refs, copies int32 [n,2]); copies goes to kvpages_copy for each pair of pools."""
-    dev = _device_of(page_table, "page_table")
-    B, M, P, o = _books(dev, page, (page_table, refs, cache_seqlens, src, dst), ("cache_seqlens", "src", "dst"), out,
-                        (page_table, cache_seqlens, refs))
+    dev, B, M, P, o = _books(page_table, refs, (cache_seqlens, src, dst), ("cache_seqlens", "src", "dst"), page, out,
+                             (page_table, cache_seqlens, refs))
     _of_rows(B, (cache_seqlens, "cache_seqlens"))
-    if src.dim() != 1 or src.shape != dst.shape:
+    shape = src.shape
+    if len(shape) != 1 or shape != dst.shape:
         raise ValueError("src and dst must be int32 [n]")
-    n = src.shape[0]
+    n = shape[0]
     copies = torch.empty((n, 2), dtype=torch.int32, device=src.device)
     st = _on_device(dev, _lib.attn_kvpages_fork, page_table.data_ptr(), cache_seqlens.data_ptr(), refs.data_ptr(), src.data_ptr(), dst.data_ptr(),
                     o[0].data_ptr(), o[1].data_ptr(), o[2].data_ptr(), copies.data_ptr(), n, B, M, P, page)
@@ -758,8 +749,7 @@ def kvpages_fork(page_table, cache_seqlens, refs, src, dst, page: int, out=None)
 def kvpages_reserve(page_table, cache_seqlens, refs, new_seqlens, page: int, out=None):
     """Appends free pages to each row until it has room for new_seqlens[b] tokens behind its first cache_seqlens[b].  out:
     (page_table, refs) to write to, which may be the inputs (None: new ones).  Returns those two."""
-    dev = _device_of(page_table, "page_table")
-    B, M, P, o = _books(dev, page, (page_table, refs, cache_seqlens, new_seqlens), ("cache_seqlens", "new_seqlens"), out, (page_table, refs))
+    dev, B, M, P, o = _books(page_table, refs, (cache_seqlens, new_seqlens), ("cache_seqlens", "new_seqlens"), page, out, (page_table, refs))
     _of_rows(B, (cache_seqlens, "cache_seqlens"), (new_seqlens, "new_seqlens"))
     st = _on_device(dev, _lib.attn_kvpages_reserve, page_table.data_ptr(), cache_seqlens.data_ptr(), refs.data_ptr(), new_seqlens.data_ptr(),
                     o[0].data_ptr(), o[1].data_ptr(), B, M, P, page)
@@ -771,8 +761,7 @@ def kvpages_compact(page_table, refs, out=None):
     """Moves the used pages to the front of the pool: with U in use, those from U on go to the free places before it.  out:
     (page_table, refs) to write to, which may be the inputs (None: new ones).  Returns (page_table, refs, copies int32
     [pages // 2, 2], used int32 [1]: U); copies goes to kvpages_copy for each pair of pools."""
-    dev = _device_of(page_table, "page_table")
-    B, M, P, o = _books(dev, 16, (page_table, refs), (), out, (page_table, refs))
+    dev, B, M, P, o = _books(page_table, refs, (), (), 16, out, (page_table, refs))
     copies = torch.empty((P // 2, 2), dtype=torch.int32, device=refs.device)
     used = torch.empty((1,), dtype=torch.int32, device=refs.device)
     st = _on_device(dev, _lib.attn_kvpages_compact, page_table.data_ptr(), refs.data_ptr(), o[0].data_ptr(), o[1].data_ptr(), copies.data_ptr(),
