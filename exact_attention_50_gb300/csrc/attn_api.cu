@@ -1205,6 +1205,13 @@ attn_status_t attn_bwd_varlen_gqa(const void* q, const void* k, const void* v, c
   p.q = q; p.k = k; p.v = v; p.o = out; p.dout = dout; p.lse = lse;
   p.dq = dq; p.dk = dk; p.dv = dv;
   if (!(p.status = status_word())) return ATTN_ERR_CUDA;
+  // The key tiles' order.  By levels the CTAs' work comes out even (3 x 1500 tokens, 32 over 8 heads, d = 128, 70 MB of dQ: 189
+  // us, one sequence after the other 243), but all sequences are worked on at once, and a dQ accumulator that does not
+  // fit the L2 goes through HBM again at each addition.  Past that one sequence after the other is faster: 16 x 64 to
+  // 2048 tokens, 290 MB, 727 us for 777; 40 x 2000, 1250 MB, 3986 for 5211; 20 x 1000, 312 MB, 654 for 775; 64 x 10 to
+  // 300, 156 MB, 179 for 187; 4 x 2048, 128 MB, 416 for 423; 2 x 8192, 256 MB, 2931 for 2910.  (Passes over the list
+  // for one or two kv heads: 631 on the third, 755 on the first, 4195 on the second.)
+  const bool by_level = causal != 0 && static_cast<size_t>(total_tokens) * Hq * d * sizeof(float) < size_t{128} << 20;
   char* const list = static_cast<char*>(workspace) + attn_bwd_workspace_bytes(1, Hq, total_tokens, d);
   int* const head = reinterpret_cast<int*>(list);
   int4* const tiles = reinterpret_cast<int4*>(list + kListHead);
@@ -1215,7 +1222,7 @@ attn_status_t attn_bwd_varlen_gqa(const void* q, const void* k, const void* v, c
   // one sweep (16.5k tokens of 32 heads: 118 us in the order of the LSE).
   const BwdParams::Rows sweep{d, static_cast<long long>(total_tokens) * d};
   if (dtype != ATTN_F32) p.lay_o = p.lay_dq = sweep;
-  if (attn::launch_packed_tiles(cu_seqlens, nseq, total_tokens, max_seqlen, attn::kBN, causal != 0, true, head, tiles, p.status, s) != cudaSuccess ||
+  if (attn::launch_packed_tiles(cu_seqlens, nseq, total_tokens, max_seqlen, attn::kBN, by_level, true, head, tiles, p.status, s) != cudaSuccess ||
       attn::launch_bwd_preprocess(p, dtype, dtype != ATTN_F32, s) != cudaSuccess)
     return ATTN_ERR_CUDA;
   if (dtype == ATTN_F32) {

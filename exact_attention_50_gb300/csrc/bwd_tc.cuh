@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(512, 1)
     seq_start = tile.x;
     seq_len = kv_len = tile.y;
     kt = tile.z;
-    hkv = blockIdx.x % p.Hkv;
+    hkv = blockIdx.x - e * p.Hkv;
     hq0 = hkv * p.G;
   } else if (p.cu_seqlens) {
     const int s = blockIdx.x / p.Hkv, hh = blockIdx.x % p.Hkv;

@@ -163,9 +163,10 @@ cudaError_t launch_bwd_tc(const BwdMaps& maps, const BwdParams& p, attn_dtype_t 
 cudaError_t launch_bwd_f32(const BwdParams& p, bool causal, cudaStream_t stream);
 
 // ---------------------------------------------------------------- packed sequences with grouped heads
-// The tiles of `tile` tokens that cu holds, heaviest first: at most packed_bound of them.
+// The tiles of `tile` tokens that cu holds, at most packed_bound of them: by levels, all sequences' heaviest tiles first
+// (backward: a tile's level falls with its number), or one sequence after the other, the longest first.
 long long packed_bound(int T, int nseq, int max_seqlen, int tile);
-cudaError_t launch_packed_tiles(const int32_t* cu, int nseq, int T, int max_seqlen, int tile, bool causal, bool backward, int* head, int4* tiles,
+cudaError_t launch_packed_tiles(const int32_t* cu, int nseq, int T, int max_seqlen, int tile, bool by_level, bool backward, int* head, int4* tiles,
                                 unsigned* status, cudaStream_t stream);
 // Rows [*end, T) of up to three tensors become zeros, and -inf in lse [H, T] (nullable).
 cudaError_t launch_packed_tail(void* const x[3], const int row_bytes[3], float* lse, int H, int T, const int32_t* end, cudaStream_t stream);

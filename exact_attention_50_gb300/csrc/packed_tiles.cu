@@ -29,7 +29,7 @@ constexpr int kLevels = 2048, kThreads = 1024;
 
 struct ListParams {
   const int32_t* cu;
-  int nseq, T, max_seqlen, tile, shift, levels, causal, backward, bound;
+  int nseq, T, max_seqlen, tile, shift, levels, by_level, backward, bound;
   int* head;
   int4* out;
   unsigned* status;
@@ -119,10 +119,10 @@ __global__ void __launch_bounds__(kThreads) packed_tiles_kernel(const ListParams
     if (!fits) raise_status(p.status, ATTN_ERR_DEVICE_INPUT);
   }
   if (!fits) return;
-  const bool turn = p.causal && p.backward;  // under the mask key tiles come in ascending order as the levels fall
+  const bool turn = p.by_level && p.backward;  // key tiles in ascending order as the levels fall
   const auto put = [&](int c0, int len, int n, int r, int held, int at) {  // tile `at` of the r-th sequence of n levels, `held` tiles
     const int l = at >> p.shift, in = at & (sub - 1);
-    const int place = p.causal ? M[l + 1] - (l + 1) * A[l + 1] + A[n] + r : M[n] + r * n + l;
+    const int place = p.by_level ? M[l + 1] - (l + 1) * A[l + 1] + A[n] + r : M[n] + r * n + l;
     const int no = turn ? n * sub - 1 - at : at;
     p.out[static_cast<long long>(place) * sub + (turn ? sub - 1 - in : in)] = make_int4(c0, no < held ? len : 0, no, 0);
   };
@@ -178,14 +178,14 @@ long long packed_bound(int T, int nseq, int max_seqlen, int tile) {
   return T / tile + (static_cast<long long>(nseq) << packed_shift(max_seqlen, tile));
 }
 
-cudaError_t launch_packed_tiles(const int32_t* cu, int nseq, int T, int max_seqlen, int tile, bool causal, bool backward, int* head, int4* tiles,
+cudaError_t launch_packed_tiles(const int32_t* cu, int nseq, int T, int max_seqlen, int tile, bool by_level, bool backward, int* head, int4* tiles,
                                 unsigned* status, cudaStream_t stream) {
   ListParams p{};
   p.cu = cu;
   p.nseq = nseq; p.T = T; p.max_seqlen = max_seqlen; p.tile = tile;
   p.shift = packed_shift(max_seqlen, tile);
   p.levels = static_cast<int>(((static_cast<long long>(max_seqlen) + tile - 1) / tile + (1LL << p.shift) - 1) >> p.shift);
-  p.causal = causal; p.backward = backward;
+  p.by_level = by_level; p.backward = backward;
   p.bound = static_cast<int>(packed_bound(T, nseq, max_seqlen, tile));
   p.head = head;
   p.out = tiles;
