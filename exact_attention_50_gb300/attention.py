@@ -879,4 +879,4 @@ class _VarlenGqaFn(torch.autograd.Function):
 def flash_attn_varlen_gqa_func(q, k, v, cu_seqlens, max_seqlen, softmax_scale=None, causal=False, deterministic=False):
     """Differentiable fwd_varlen_gqa: q [T,Hq,d], k and v [T,Hkv,d], cu_seqlens int32 [batch+1] -> [T,Hq,d].  deterministic
     makes the backward's dq bitwise reproducible (slower)."""
-    return _VarlenGqaFn.apply(q, k, v, cu_seqlens, int(max_seqlen), bool(causal), softmax_scale, bool(deterministic))
+    return _VarlenGqaFn.apply(q, k, v, cu_seqlens.to(torch.int32), int(max_seqlen), bool(causal), softmax_scale, bool(deterministic))

@@ -1275,14 +1275,19 @@ Cache8Plan paged_plan(int B, int Hkv, int R, int Nk, int d) {
           round256(static_cast<size_t>(pairs) * sizeof(int2))};
 }
 
-// Many rows: the key ranges of the least estimated time (kv8_plan's rule, without its expansion).
+// The key ranges of the tcgen05 kernel.  One row block (R <= 128) is bound by HBM and gets three items per SM, so that caches
+// of different lengths come out even; more are planned by estimated time (kv8_plan's rule).  8 x 8 heads of 16k to 32k
+// keys, 32 rows, pages of 64, kernel and combination, d = 64 / 128: with 8, 6, 4, 3, 2 items per SM 112 / 158, 116 / 160, 107 / 151,
+// 98 / 142, 102 / 142 us; by the second rule 115 / 157.
 struct PagedRanges {
   KvSplit split;
   size_t o_bytes, lse_bytes;
 };
 PagedRanges paged_ranges(long long bh, long long R, int Nk, int d, bool f32, int Hq, int Hkv, int Nq, int B) {
   PagedRanges r{};
-  r.split = f32 ? kv_split(B, Hq, Hkv, Nq, Nk, 0) : kv8_plan(bh, R, Nk, d).split;
+  r.split = f32            ? kv_split(B, Hq, Hkv, Nq, Nk, 0)
+            : R <= attn::kBM ? kv_split(B, Hq, Hkv, Nq, Nk, static_cast<int>((3 * 152 + bh - 1) / bh))
+                             : kv8_plan(bh, R, Nk, d).split;
   if (f32 || r.split.n_splits > 1) {
     r.o_bytes = round256(static_cast<size_t>(r.split.n_splits) * bh * R * d * sizeof(float));
     r.lse_bytes = round256(static_cast<size_t>(r.split.n_splits) * bh * R * sizeof(float));

@@ -385,7 +385,11 @@ __global__ void __launch_bounds__(512, 1)
       // item's Q) and V.  Neither waits behind the other, so K tiles run ahead into their
       // deeper ring while V waits for its PV to free a slot.  Every barrier tested here cannot
       // complete its next phase before this thread issues another copy, so no phase is skipped.
-      if (lane == 0) {
+      // Pages: the whole warp, every decision lane 0's, a lane for each box of a tile, and 32 page numbers of a
+      // stream at a time.  (One thread that read the numbers and issued the
+      // boxes in turn bounded the kernel: 8 x 8 heads, 32 rows, 16k to 32k keys, d = 64, pages
+      // of 16 / 64 / 128: 281 / 131 / 106 us, now 127 / 91 / 86.)
+      if (lane == 0 || PAGED) {
         tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
@@ -396,28 +400,44 @@ __global__ void __launch_bounds__(512, 1)
         bool q_cur = false;   // the Q of ck's item has been issued
         bool ok = true;
         unsigned long long t_idle = 0;
-        // the keys or values of key tile j of an item, a box for each of its pages; rows behind the last page keep
+        auto passed = [&](uint64_t* bar, uint32_t parity) -> bool {
+          const bool r = mbar_test(bar, parity);
+          return PAGED ? __shfl_sync(0xffffffffu, r, 0) : r;
+        };
+        // a stream's page numbers: this lane's of 32 neighbouring entries of the table row of batch b, from entry `first`
+        // on.  (The 32 behind them, read ahead, were worth nothing.)
+        struct Pages {
+          int number, b, first;
+        };
+        [[maybe_unused]] Pages pages_k{-1, -1, 0}, pages_v{-1, -1, 0};
+        // the keys or values of a key tile, a box for each of its pages and 64 columns; rows behind the last page keep
         // what they hold.  A page number outside the pool loads as zeros.
-        [[maybe_unused]] auto load_pages = [&](uint8_t* tile, const CUtensorMap* map, uint64_t* bar, const FwdItem& it, int j) {
-          const int page = 1 << p.page_shift, key0 = (it.j0 + j) * kBN;
-          const int n = (min(kBN, it.seq_len - key0) + page - 1) >> p.page_shift;
-          const int32_t* ids = p.table + static_cast<size_t>(it.b) * p.M + (key0 >> p.page_shift);
-          mbar_expect_tx(bar, static_cast<uint32_t>(n) * kChunks * page * 128);
-          for (int i = 0; i < n; ++i) {
-            const int id = ids[i];
+        [[maybe_unused]] auto load_pages = [&](uint8_t* tile, const CUtensorMap* map, uint64_t* bar, const TileCursor<CAUSAL, MODE>& c, Pages& g) {
+          const int page = 1 << p.page_shift, key0 = (c.it.j0 + c.j) * kBN;
+          const int n = (min(kBN, c.it.seq_len - key0) + page - 1) >> p.page_shift, entry = key0 >> p.page_shift;
+          if (g.b != c.it.b || entry < g.first || entry + n > g.first + 32) {
+            g.b = c.it.b;
+            g.first = entry;
+            g.number = entry + lane < p.M ? p.table[static_cast<size_t>(g.b) * p.M + entry + lane] : -1;
+          }
+          if (lane == 0) mbar_expect_tx(bar, static_cast<uint32_t>(n) * kChunks * page * 128);
+          const int box = lane / kChunks;
+          const int id = __shfl_sync(0xffffffffu, g.number, (entry - g.first + box) & 31);  // (and lane 0's arrival before the copies)
+          if (box < n) {
             const bool in = id >= 0 && id < p.P;
             if (!in) raise_status(p.status, ATTN_ERR_DEVICE_INPUT);
-            const int z = in ? id * p.Hkv + it.h : p.P * p.Hkv;
-            for (int c = 0; c < kChunks; ++c) tma_load_3d(tile + c * L::kChunkBytes + i * page * 128, map, bar, c * 64, 0, z);
+            const int col = lane % kChunks;
+            tma_load_3d(tile + col * L::kChunkBytes + box * page * 128, map, bar, col * 64, 0, in ? id * p.Hkv + c.it.h : p.P * p.Hkv);
           }
+          __syncwarp();
         };
         while (!ck.done || !cv.done) {
           bool progress = false;
           const uint32_t qs = nq % SQ;
-          if (!ck.done && !q_cur && (nq < static_cast<uint32_t>(SQ) || mbar_test(q_empty + qs, ((nq / SQ) - 1) & 1))) {
+          if (!ck.done && !q_cur && (nq < static_cast<uint32_t>(SQ) || passed(q_empty + qs, ((nq / SQ) - 1) & 1))) {
             const FwdItem& it = ck.it;
-            mbar_expect_tx(q_full + qs, PACKED ? kChunks * p.tile_tokens * p.heads * 128 : L::kTileBytes);
-            for (int c = 0; c < kChunks; ++c) {
+            if (!PAGED || lane == 0) mbar_expect_tx(q_full + qs, PACKED ? kChunks * p.tile_tokens * p.heads * 128 : L::kTileBytes);
+            for (int c = 0; c < kChunks && (!PAGED || lane == 0); ++c) {
               uint8_t* dst = sQ + qs * L::kTileBytes + c * L::kChunkBytes;
               if constexpr (PACKED)
                 tma_load_3d(dst, &tmQ, q_full + qs, c * 64, it.h * p.heads, it.seq_start + it.qt * p.tile_tokens);
@@ -434,10 +454,10 @@ __global__ void __launch_bounds__(512, 1)
           }
           if (!ck.done && q_cur) {
             const uint32_t st = ck.t % SK;
-            if (ck.t < static_cast<uint32_t>(SK) || mbar_test(k_empty + st, ((ck.t / SK) - 1) & 1)) {
+            if (ck.t < static_cast<uint32_t>(SK) || passed(k_empty + st, ((ck.t / SK) - 1) & 1)) {
               const FwdItem& it = ck.it;
               if constexpr (PAGED) {
-                load_pages(sK + st * L::kTileBytes, &tmK, k_full + st, it, ck.j);
+                load_pages(sK + st * L::kTileBytes, &tmK, k_full + st, ck, pages_k);
               } else {
               mbar_expect_tx(k_full + st, L::kTileBytes);
               for (int c = 0; c < kChunks; ++c) {
@@ -459,10 +479,10 @@ __global__ void __launch_bounds__(512, 1)
           }
           if (!cv.done) {
             const uint32_t st = cv.t % SV;
-            if (cv.t < static_cast<uint32_t>(SV) || mbar_test(v_empty + st, ((cv.t / SV) - 1) & 1)) {
+            if (cv.t < static_cast<uint32_t>(SV) || passed(v_empty + st, ((cv.t / SV) - 1) & 1)) {
               const FwdItem& it = cv.it;
               if constexpr (PAGED) {
-                load_pages(sV + st * L::kTileBytes, &tmV, v_full + st, it, cv.j);
+                load_pages(sV + st * L::kTileBytes, &tmV, v_full + st, cv, pages_v);
               } else {
               mbar_expect_tx(v_full + st, L::kTileBytes);
               for (int c = 0; c < kChunks; ++c) {
@@ -486,10 +506,13 @@ __global__ void __launch_bounds__(512, 1)
           } else {
             const unsigned long long now = globaltimer();
             if (t_idle == 0) t_idle = now;
-            if (abort_read(abort_flag)) { ok = false; break; }
-            if (now - t_idle > wait_limit(abort_flag)) {
+            int stop = abort_read(abort_flag) ? 1 : now - t_idle > wait_limit(abort_flag) ? 2 : 0;
+            if constexpr (PAGED) stop = __shfl_sync(0xffffffffu, stop, 0);
+            if (stop == 2) {
               raise_status(p.status, ATTN_ERR_TIMEOUT);
               abort_set(abort_flag, 1);
+            }
+            if (stop) {
               ok = false;
               break;
             }

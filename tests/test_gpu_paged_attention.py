@@ -92,7 +92,8 @@ def test_against_64_bits(dev, dtype, Hq, Hkv, Nq, d, page, causal):
 @pytest.mark.parametrize("dtype,Hq,Hkv,Nq,d,page,lens", [
     ("bf16", 8, 2, 1, 128, 64, [4001, 12000, 1, 0, 9000]), ("f16", 8, 8, 1, 64, 16, [3000, 8191]), ("bf16", 4, 1, 4, 128, 128, [20001]),
     ("f16", 32, 8, 1, 128, 32, [1001]), ("bf16", 32, 8, 2, 80, 16, [5000, 300]), ("bf16", 8, 1, 128, 128, 64, [6000, 200]),
-    ("f32", 4, 4, 1, 64, 64, [2500, 1])])
+    ("f32", 4, 4, 1, 64, 64, [2500, 1]), ("f16", 8, 1, 3, 64, 16, [7000, 33, 513, 0, 2049]), ("bf16", 8, 2, 20, 128, 32, [4100, 1, 1300]),
+    ("bf16", 16, 2, 30, 80, 16, [1537, 2600])])
 def test_long_caches(dev, dtype, Hq, Hkv, Nq, d, page, lens):
     """Runs that end inside a cache, clusters, key ranges that are joined."""
     q, k, v, table, n, rows = make(dev, dtype, Hq, Hkv, Nq, lens, page, d, seed=3)
