@@ -1142,11 +1142,15 @@ attn_status_t attn_fwd_varlen_gqa(const void* q, const void* k, const void* v, c
   p.open_end = 1;
   int* const head = static_cast<int*>(workspace);
   int4* const tiles = reinterpret_cast<int4*>(static_cast<char*>(workspace) + kListHead);
-  p.head = head;
-  p.tiles = tiles;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (attn::launch_packed_tiles(cu_seqlens, nseq, total_tokens, max_seqlen, t.tokens, causal != 0, false, head, tiles, p.status, s) != cudaSuccess)
-    return ATTN_ERR_CUDA;
+  // one sequence needs no list while the kernel keeps a CTA's items in shared memory (201 tokens: 9 us for 11)
+  const long long items = attn::packed_bound(total_tokens, nseq, max_seqlen, t.tokens) * (Hq / t.heads);
+  if (nseq > 1 || dtype == ATTN_F32 || items > attn::kPackedListed * 128LL) {
+    p.head = head;
+    p.tiles = tiles;
+    if (attn::launch_packed_tiles(cu_seqlens, nseq, total_tokens, max_seqlen, t.tokens, causal != 0, false, head, tiles, p.status, s) != cudaSuccess)
+      return ATTN_ERR_CUDA;
+  }
   if (dtype == ATTN_F32) {  // rows of sequences from the grid, rows behind the last one by a kernel of its own
     void* const x[3] = {out, nullptr, nullptr};
     const int bytes[3] = {Hq * d * 4, 0, 0};
@@ -1215,16 +1219,18 @@ attn_status_t attn_bwd_varlen_gqa(const void* q, const void* k, const void* v, c
   char* const list = static_cast<char*>(workspace) + attn_bwd_workspace_bytes(1, Hq, total_tokens, d);
   int* const head = reinterpret_cast<int*>(list);
   int4* const tiles = reinterpret_cast<int4*>(list + kListHead);
-  p.head = head;
-  p.tiles = tiles;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // The 16-bit path keeps D and the dQ accumulator in the order of O, [T, Hq] rows, so that both are read and written in
   // one sweep (16.5k tokens of 32 heads: 118 us in the order of the LSE).
   const BwdParams::Rows sweep{d, static_cast<long long>(total_tokens) * d};
   if (dtype != ATTN_F32) p.lay_o = p.lay_dq = sweep;
-  if (attn::launch_packed_tiles(cu_seqlens, nseq, total_tokens, max_seqlen, attn::kBN, by_level, true, head, tiles, p.status, s) != cudaSuccess ||
-      attn::launch_bwd_preprocess(p, dtype, dtype != ATTN_F32, s) != cudaSuccess)
-    return ATTN_ERR_CUDA;
+  if (nseq > 1 || dtype == ATTN_F32) {
+    p.head = head;
+    p.tiles = tiles;
+    if (attn::launch_packed_tiles(cu_seqlens, nseq, total_tokens, max_seqlen, attn::kBN, by_level, true, head, tiles, p.status, s) != cudaSuccess)
+      return ATTN_ERR_CUDA;
+  }
+  if (attn::launch_bwd_preprocess(p, dtype, dtype != ATTN_F32, s) != cudaSuccess) return ATTN_ERR_CUDA;
   if (dtype == ATTN_F32) {
     p.lay_k = {k_stride, d};
     p.lay_v = {v_stride, d};

@@ -174,14 +174,22 @@ __global__ void __launch_bounds__(512, 1)
   if constexpr (PACKED) {
     // rows behind the last sequence: dK = dV = 0
     const int vecs = p.Hkv * p.d * (p.out_f32 ? 4 : 2) / 16;
-    for (int tok = p.head[1] + static_cast<int>(blockIdx.x); tok < p.N; tok += static_cast<int>(gridDim.x))
+    const int last = p.tiles ? p.head[1] : p.cu_seqlens[1];
+    for (int tok = last < 0 || last > p.N ? p.N : last + static_cast<int>(blockIdx.x); tok < p.N; tok += static_cast<int>(gridDim.x))
       for (int i = threadIdx.x; i < vecs; i += L::kThreads) {
         static_cast<uint4*>(p.dk)[static_cast<size_t>(tok) * vecs + i] = make_uint4(0, 0, 0, 0);
         static_cast<uint4*>(p.dv)[static_cast<size_t>(tok) * vecs + i] = make_uint4(0, 0, 0, 0);
       }
     const int e = blockIdx.x / p.Hkv;
-    if (e >= p.head[0]) return;  // the whole CTA, before any barrier or allocation
-    const int4 tile = p.tiles[e];
+    int4 tile;
+    if (p.tiles) {
+      if (e >= p.head[0]) return;  // the whole CTA, before any barrier or allocation
+      tile = p.tiles[e];
+    } else {  // one sequence
+      const int len = packed_single(p.cu_seqlens, p.N, p.max_seqlen);
+      if (len == 0 && blockIdx.x == 0 && threadIdx.x == 0 && (p.cu_seqlens[0] != 0 || p.cu_seqlens[1] != 0)) raise_status(p.status, ATTN_ERR_DEVICE_INPUT);
+      tile = make_int4(0, e * kBN < len ? len : 0, e, 0);
+    }
     if (tile.y == 0) return;
     seq_start = tile.x;
     seq_len = kv_len = tile.y;

@@ -108,7 +108,12 @@ struct FwdLayout {
   static constexpr int kNumBars = 4 + 2 * kStagesK + 2 * kStagesV + 2 + 8 + 2 + 1 + 1 + 2 + 2 + 2;
   // tmem base (u32), abort flag (int), wait limit (u64, ns)
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
-  static constexpr int kBytes = kOffMisc + 16;
+  // packed: the CTA's first items, as many as there is room for, so that no role waits an L2 latency between its items
+  // (60 sequences of 100 to 500 tokens, 32 over 8 heads, d = 64: 92 us for 99)
+  static constexpr int kListed = MODE != kModePacked ? 0 : DP == 128 ? kPackedListed : 256;
+  static constexpr int kOffList = (kOffMisc + 16 + 15) / 16 * 16;
+  static constexpr int kBytes = kOffList + 16 * kListed;
+  static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
   static constexpr int kSmemAlloc = kBytes;  // the dynamic shared memory starts 1024-byte aligned
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColO = 256;  // O_0; O_1 at kColO + DP
@@ -133,17 +138,24 @@ struct FwdItem {
   bool valid;
 };
 
+// Packed: item idx as the list has it (start, length, tile) and its head group.
+__device__ __forceinline__ int4 packed_item(const FwdParams& p, int idx) {
+  const int groups = p.Hq / p.heads, entry = idx / groups;
+  int4 t = p.tiles[entry];
+  t.w = idx - entry * groups;
+  return t;
+}
+
+// The CTA's k-th item, number idx.  Packed: the first `listed` are in shared memory (`list`).
 template <bool CAUSAL, int MODE>
-__device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int idx) {
+__device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int idx, int k, const int4* list, int listed) {
   constexpr bool VARLEN = MODE == kModeVarlen;
   FwdItem it;
   it.j0 = 0;
   it.split = 0;
   if constexpr (MODE == kModePacked) {
-    const int groups = p.Hq / p.heads;
-    const int entry = idx / groups;
-    const int4 tile = p.tiles[entry];
-    it.h = idx - entry * groups;  // the item's head group: query heads [h heads, h heads + heads)
+    const int4 tile = k < listed ? list[k] : packed_item(p, idx);
+    it.h = tile.w;  // the item's head group: query heads [h heads, h heads + heads)
     it.b = it.h / p.groups_per_kv;  // its kv head
     it.seq_start = tile.x;
     it.seq_len = tile.y;
@@ -238,17 +250,21 @@ struct TileCursor {
   uint32_t t;   // key tiles passed so far: ring position and barrier phases, across items
   uint32_t ic;  // items passed so far
   FwdItem it;
+  const int4* list;  // packed: the items in shared memory, and their number
+  int listed;
   bool done;
   __device__ __forceinline__ void seek(const FwdParams& p, int n_items) {
     for (; k * static_cast<int>(gridDim.x) < n_items; ++k) {
       const int idx = cta_item<MODE>(k);
       if (idx >= n_items) continue;
-      it = fwd_item<CAUSAL, MODE>(p, idx);
+      it = fwd_item<CAUSAL, MODE>(p, idx, k, list, listed);
       if (it.valid) return;
     }
     done = true;
   }
-  __device__ __forceinline__ void start(const FwdParams& p, int n_items) {
+  __device__ __forceinline__ void start(const FwdParams& p, int n_items, const int4* items, int n) {
+    list = items;
+    listed = n;
     k = 0;
     j = 0;
     t = 0;
@@ -372,9 +388,29 @@ __global__ void __launch_bounds__(512, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  int tokens_end = 0;  // packed: the end of the last sequence
+  [[maybe_unused]] const int4* const list = reinterpret_cast<const int4*>(smem + L::kOffList);
   if constexpr (PACKED) {
-    dependency_wait();  // the list of tiles
-    n_items = p.head[0] * (p.Hq / p.heads);
+    const int groups = p.Hq / p.heads;
+    int len = 0;  // without a list: the one sequence's
+    if (p.tiles) {
+      dependency_wait();  // the list of tiles
+      n_items = p.head[0] * groups;
+      tokens_end = p.head[1];
+    } else {
+      len = packed_single(p.cu_seqlens, p.total_tokens, p.max_seqlen);
+      const int end = p.cu_seqlens[1];
+      if (len == 0 && blockIdx.x == 0 && threadIdx.x == 0 && (p.cu_seqlens[0] != 0 || end != 0)) raise_status(p.status, ATTN_ERR_DEVICE_INPUT);
+      n_items = (len + p.tile_tokens - 1) / p.tile_tokens * groups;
+      tokens_end = end >= 0 && end <= p.total_tokens ? end : p.total_tokens;
+    }
+    for (int k = threadIdx.x; k < L::kListed; k += L::kThreads) {
+      const int idx = cta_item<MODE>(k);
+      int4 t = make_int4(0, 0, 0, 0);
+      if (idx < n_items) t = p.tiles ? packed_item(p, idx) : make_int4(0, len, n_items / groups - 1 - idx / groups, idx % groups);  // the last tile first
+      reinterpret_cast<int4*>(smem + L::kOffList)[k] = t;
+    }
+    __syncthreads();
   }
 
   if (warp >= 8 && warp < 12) {
@@ -394,8 +430,8 @@ __global__ void __launch_bounds__(512, 1)
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
         TileCursor<CAUSAL, MODE> ck, cv;
-        ck.start(p, n_items);
-        cv.start(p, n_items);
+        ck.start(p, n_items, list, L::kListed);
+        cv.start(p, n_items, list, L::kListed);
         uint32_t nq = 0;      // Q tiles issued (one per item, slot item % 2)
         bool q_cur = false;   // the Q of ck's item has been issued
         bool ok = true;
@@ -551,7 +587,7 @@ __global__ void __launch_bounds__(512, 1)
         for (int k = 0; ok && k * static_cast<int>(gridDim.x) < n_items; ++k) {
           const int idx = cta_item<MODE>(k);
           if (idx >= n_items) continue;
-          const FwdItem it = fwd_item<CAUSAL, MODE>(p, idx);
+          const FwdItem it = fwd_item<CAUSAL, MODE>(p, idx, k, list, L::kListed);
           if (!it.valid) continue;
           const int n = it.n_kv;
           const uint32_t qs = ic % SQ;
@@ -639,7 +675,7 @@ __global__ void __launch_bounds__(512, 1)
     for (int k = 0; ok && k * static_cast<int>(gridDim.x) < n_items; ++k) {
       const int idx = cta_item<MODE>(k);
       if (idx >= n_items) continue;
-      const FwdItem it = fwd_item<CAUSAL, MODE>(p, idx);
+      const FwdItem it = fwd_item<CAUSAL, MODE>(p, idx, k, list, L::kListed);
       if (!it.valid) continue;
       // relative to the sequence (KV cache: to the R rows); packed: the row's token
       const int q_row = PACKED ? it.qt * p.tile_tokens + tile_tok : it.qt * kBM + row;
@@ -771,7 +807,7 @@ __global__ void __launch_bounds__(512, 1)
     if (storer) bulk_wait_all();  // the tile stores are complete before the CTA ends
     if constexpr (PACKED) {  // rows behind the last sequence: O = 0, LSE = -inf
       const int vecs = p.Hq * p.d * (p.out_f32 ? 4 : 2) / 16;
-      for (int tok = p.head[1] + static_cast<int>(blockIdx.x); tok < p.total_tokens; tok += static_cast<int>(gridDim.x)) {
+      for (int tok = tokens_end + static_cast<int>(blockIdx.x); tok < p.total_tokens; tok += static_cast<int>(gridDim.x)) {
         uint4* const dst = static_cast<uint4*>(p.o) + static_cast<size_t>(tok) * vecs;
         for (int i = row; i < vecs; i += 128) dst[i] = make_uint4(0, 0, 0, 0);
         if (p.lse)
@@ -782,7 +818,7 @@ __global__ void __launch_bounds__(512, 1)
       for (int k = 0; kv_final && k * static_cast<int>(gridDim.x) < n_items; ++k) {
         const int idx = cta_item<MODE>(k);
         if (idx >= n_items) continue;
-        const FwdItem it = fwd_item<CAUSAL, MODE>(p, idx);
+        const FwdItem it = fwd_item<CAUSAL, MODE>(p, idx, k, list, L::kListed);
         if (it.valid) continue;
         const int r0 = it.qt * kBM, rows = min(kBM, p.R - r0);
         const size_t first = (static_cast<size_t>(it.b) * p.Hkv + it.h) * p.R + r0;
@@ -805,7 +841,7 @@ __global__ void __launch_bounds__(512, 1)
     for (int k = 0; ok && k * static_cast<int>(gridDim.x) < n_items; ++k) {
       const int idx = cta_item<MODE>(k);
       if (idx >= n_items) continue;
-      const FwdItem it = fwd_item<CAUSAL, MODE>(p, idx);
+      const FwdItem it = fwd_item<CAUSAL, MODE>(p, idx, k, list, L::kListed);
       if (!it.valid) continue;
       // relative to the sequence (KV cache: to the R rows); packed: the row's token
       const int q_row = PACKED ? it.qt * p.tile_tokens + tile_tok : it.qt * kBM + row;
@@ -1064,7 +1100,7 @@ cudaError_t launch_fwd_tc_t(const FwdMaps& maps, const FwdParams& p, cudaStream_
     cfg.dynamicSmemBytes = L::kSmemAlloc;
     cfg.stream = stream;
     cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = p.tiles ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kern, maps.q, maps.k, maps.v, maps.o, p, 0);
   }
   const long heads = MODE == kModeVarlen ? static_cast<long>(p.Hq) * p.nseq

@@ -10,6 +10,14 @@ namespace attn {
 constexpr int kBM = 128;  // query rows per tile (one TMEM lane per row)
 constexpr int kBN = 128;  // keys per tile
 
+constexpr int kPackedListed = 32;  // items of a CTA that the packed forward keeps in shared memory, at least
+
+// The length of the one sequence of cu [2], or 0 where it breaks the rules.
+__device__ __forceinline__ int packed_single(const int32_t* cu, int tokens, int max_seqlen) {
+  const int c0 = cu[0], c1 = cu[1];
+  return c0 != 0 || c1 < 0 || c1 > tokens || c1 > max_seqlen ? 0 : c1;
+}
+
 // Everything a forward launch needs besides the tensor maps.
 struct FwdParams {
   void* o;                 // [B,Hq,N,d] or varlen [T,H,d]
@@ -43,7 +51,8 @@ struct FwdParams {
   int M, P, page_shift;
   // Packed sequences with grouped heads (kModePacked): a work item is `tile_tokens` tokens by `heads` neighbouring
   // query heads of one kv head, row = token * heads + head; tiles (start, length, number, -) and their count, head[0],
-  // as launch_packed_tiles leaves them, tokens end at head[1]
+  // as launch_packed_tiles leaves them, tokens end at head[1]; null for one sequence of at most
+  // kPackedListed items a CTA
   const int4* tiles;
   const int* head;
   int heads, tile_tokens, groups_per_kv;  // groups_per_kv: G / heads

@@ -170,6 +170,29 @@ def test_bad_cu_seqlens(dev):
     assert torch.equal(o[100:], good[0][100:])
 
 
+def test_one_sequence(dev):
+    """The path without a list: lengths below the bound, tokens behind the end, an empty and a broken sequence."""
+    for L, T, bound in ((300, 300, 300), (129, 140, 500), (1, 9, 1), (16, 16, 16), (1000, 1003, 1001)):
+        q, k, v, dout, cu = make(dev, "bf16", 8, 2, 64, [L], seed=L, behind=T - L)
+        for causal in (True, False):
+            o, lse = A.fwd_varlen_gqa(q, k, v, cu, bound, causal)
+            check_fwd(o, lse, q, k, v, [L], causal, False)
+            for det in (False, True):
+                check_bwd(A.bwd_varlen_gqa(q, k, v, o, lse, dout, cu, bound, causal, deterministic=det), q, k, v, dout, [L], causal, False)
+            status()
+    for bad in ([1, 100], [0, 1004], [0, -1], [0, 1002]):
+        c = torch.tensor(bad, dtype=torch.int32, device=dev)
+        A.fwd_varlen_gqa(q, k, v, c, 1001, True)
+        status(True)
+        A.bwd_varlen_gqa(q, k, v, o, lse, dout, c, 1001, True)
+        status(True)
+    none = torch.zeros(2, dtype=torch.int32, device=dev)
+    o, lse = A.fwd_varlen_gqa(q, k, v, none, 1001, True)
+    assert (o == 0).all() and (lse == -INF).all()
+    assert all((x == 0).all() for x in A.bwd_varlen_gqa(q, k, v, o, lse, dout.nan_to_num(), none, 1001, True))
+    status()
+
+
 def test_deterministic_gradients(dev):
     q, k, v, dout, cu = make(dev, "bf16", 8, 2, 128, [900, 77, 400], seed=4)
     o, lse = A.fwd_varlen_gqa(q, k, v, cu, 900, True)
