@@ -172,24 +172,32 @@ __global__ void __launch_bounds__(512, 1)
   // kv head (row block), its first query head; the sequence's start, its query and key counts
   int hkv, hq0, seq_start = 0, seq_len = p.N, kv_len = p.Nk;
   if constexpr (PACKED) {
-    // rows behind the last sequence: dK = dV = 0
-    const int vecs = p.Hkv * p.d * (p.out_f32 ? 4 : 2) / 16;
-    const int last = p.tiles ? p.head[1] : p.cu_seqlens[1];
-    for (int tok = last < 0 || last > p.N ? p.N : last + static_cast<int>(blockIdx.x); tok < p.N; tok += static_cast<int>(gridDim.x))
-      for (int i = threadIdx.x; i < vecs; i += L::kThreads) {
-        static_cast<uint4*>(p.dk)[static_cast<size_t>(tok) * vecs + i] = make_uint4(0, 0, 0, 0);
-        static_cast<uint4*>(p.dv)[static_cast<size_t>(tok) * vecs + i] = make_uint4(0, 0, 0, 0);
-      }
+    // the list's head and this CTA's entry together (there is room for it, whatever the count)
     const int e = blockIdx.x / p.Hkv;
+    int count, last;
     int4 tile;
     if (p.tiles) {
-      if (e >= p.head[0]) return;  // the whole CTA, before any barrier or allocation
+      const int2 head = *reinterpret_cast<const int2*>(p.head);
       tile = p.tiles[e];
+      count = head.x;
+      last = head.y;
     } else {  // one sequence
-      const int len = packed_single(p.cu_seqlens, p.N, p.max_seqlen);
-      if (len == 0 && blockIdx.x == 0 && threadIdx.x == 0 && (p.cu_seqlens[0] != 0 || p.cu_seqlens[1] != 0)) raise_status(p.status, ATTN_ERR_DEVICE_INPUT);
-      tile = make_int4(0, e * kBN < len ? len : 0, e, 0);
+      const int len = packed_single(p.cu_seqlens, p.N, p.max_seqlen), end = p.cu_seqlens[1];
+      if (len == 0 && blockIdx.x == 0 && threadIdx.x == 0 && (p.cu_seqlens[0] != 0 || end != 0)) raise_status(p.status, ATTN_ERR_DEVICE_INPUT);
+      tile = make_int4(0, len, e, 0);
+      count = (len + kBN - 1) / kBN;
+      last = end >= 0 && end <= p.N ? end : p.N;
     }
+    // rows behind the last sequence: dK = dV = 0
+    if (last < p.N) {
+      const int vecs = p.Hkv * p.d * (p.out_f32 ? 4 : 2) / 16;
+      for (int tok = last + static_cast<int>(blockIdx.x); tok < p.N; tok += static_cast<int>(gridDim.x))
+        for (int i = threadIdx.x; i < vecs; i += L::kThreads) {
+          static_cast<uint4*>(p.dk)[static_cast<size_t>(tok) * vecs + i] = make_uint4(0, 0, 0, 0);
+          static_cast<uint4*>(p.dv)[static_cast<size_t>(tok) * vecs + i] = make_uint4(0, 0, 0, 0);
+        }
+    }
+    if (e >= count) return;  // the whole CTA, before any barrier or allocation
     if (tile.y == 0) return;
     seq_start = tile.x;
     seq_len = kv_len = tile.y;
@@ -593,7 +601,6 @@ __global__ void __launch_bounds__(512, 1)
       __syncwarp();
       if (!__all_sync(0xffffffffu, ok)) break;
     }
-    if (warp == 8 && lane == 0) bulk_wait_all();  // the reductions complete before the CTA ends
     // ---- epilogue: dK (scaled) and dV rows of this key tile
     if (ok && mbar_wait_warp(dkdv_done, 0, abort_flag, p.status)) {
       tc_fence_after();
@@ -636,6 +643,7 @@ __global__ void __launch_bounds__(512, 1)
         }
       }
     }
+    if (warp == 8 && lane == 0) bulk_wait_all();  // the reductions complete before the CTA ends
   } else {
     regs_inc<L::kRegsEw>();
     // ================================================================ elementwise warps 0-7
