@@ -293,6 +293,10 @@ __global__ void __launch_bounds__(512, 1)
   constexpr bool KV = MODE == kModeKv || KV8 || PAGED;
   // an 8-bit cache, or one in pages, in one range: the items' outputs are final, written as a dense item's are
   const bool kv_final = (KV8 || PAGED) && p.n_splits == 1;
+  // Tiles without a masked key have a path of their own for the exponentials only when some of them run on the FMA pipe:
+  // otherwise it is the same code twice, and the instruction cache feels it (16 prompts of 64 to 2048 tokens 215 us with
+  // both, 204 with one; dense 4 x 2048 115 and 111; pages alone are 1% faster with both).
+  constexpr bool kFastPath = kPolyPairs != 0u || PAGED;
   // what lies behind the last key in a tile is another sequence's, or anything: its values are set to zero
   constexpr bool CLEAN = PAGED || PACKED;
   using PElem = std::conditional_t<KV8, Elem<__half>, Elem<T>>;  // of P and V
@@ -991,7 +995,7 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
         for (int h = 0; h < PH; ++h) {
           uint32_t pk[PK / 2];
-          if (lim >= 63) {
+          if (kFastPath && lim >= 63) {
 #pragma unroll
             for (int c = PK * h; c < PK * h + PK; c += 2) {
               const uint64_t x = f2_fma(f2_pack(s[c], s[c + 1]), scl, nmb);
