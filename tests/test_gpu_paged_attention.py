@@ -274,3 +274,33 @@ def test_the_whole_path(dev):
             want, _, p, size = P.attend(qh, kh, vh, 0, True)
             bound, _ = P.attend_bounds(vh, p, size, want, d, P.HALF[torch.bfloat16], P.HALF[torch.bfloat16])
             assert ((got[h * G:(h + 1) * G].double() - want).abs() <= bound).all()
+
+
+def test_refusals(dev):
+    q, k, v, table, n, _ = make(dev, "bf16", 4, 2, 1, [20, 9], 16, 64)
+    for bad in (lambda: A.fwd_kvpages(q[:1], k, v, table, n), lambda: A.fwd_kvpages(q, k, v[:-1], table, n), lambda: A.fwd_kvpages(q, k, v, table[0], n),
+                lambda: A.fwd_kvpages(q, k, v, table, n[:1]), lambda: A.fwd_kvpages(q[..., :32], k, v, table, n), lambda: A.fwd_kvpages(q[:, :3], k, v, table, n),
+                lambda: A.fwd_kvpages(q, k[:, :, :8], v[:, :, :8], table, n), lambda: A.fwd_kvpages(q, k[:, :, :8].contiguous(), v[:, :, :8].contiguous(), table, n),
+                lambda: A.fwd_kvpages(q, k, v, table, n, max_seqlen=0), lambda: A.fwd_kvpages(q, k, v, table, n, scale=0.0),
+                lambda: A.kvpages_append(k, v, table, q[:, :2, 0], q[:, :1, 0], torch.tensor([0, 1, 2], dtype=torch.int32, device=dev)),
+                lambda: A.kvpages_append(k, v, table, k[0], v[0], torch.tensor([0, 1], dtype=torch.int32, device=dev)),
+                lambda: A.kvpages_copy(k, k, torch.zeros(1, 2, dtype=torch.int32, device=dev)),
+                lambda: A.kvpages_copy(k, v, torch.zeros(2, dtype=torch.int32, device=dev))):
+        with pytest.raises((ValueError, _lib.AttnError)):
+            bad()
+    for bad in (lambda: A.fwd_kvpages(q, k.half(), v.half(), table, n), lambda: A.fwd_kvpages(q, k, v, table.long(), n),
+                lambda: A.fwd_kvpages(q, k, v, table, n.long()), lambda: A.fwd_kvpages(q, k, v, table, None), lambda: A.kvpages_copy(k, v, table.long())):
+        with pytest.raises(TypeError):
+            bad()
+    refs, row = torch.zeros(9, dtype=torch.int32, device=dev), torch.zeros(2, dtype=torch.int32, device=dev)
+    for bad in (lambda: A.kvpages_free(table, n, refs, row[:1], 16), lambda: A.kvpages_free(table, n, refs, row, 17), lambda: A.kvpages_free(n, n, refs, row, 16),
+                lambda: A.kvpages_fork(table, n, refs, row, row[:1], 16), lambda: A.kvpages_reserve(table, n, refs[None], row, 16),
+                lambda: A.kvpages_free(table, n, refs, row, 16, out=(table, n)), lambda: A.kvpages_free(table, n, refs, row, 16, out=(table, refs, n)),
+                lambda: A.kvpages_reserve(table, n, refs, row, 16, out=(table, refs[:4]))):
+        with pytest.raises((ValueError, _lib.AttnError)):
+            bad()
+    with pytest.raises(_lib.AttnError):  # an output that lies over an input which it does not follow
+        A.kvpages_free(table, n, refs, row, 16, out=(table, row, refs))
+    with pytest.raises(TypeError):
+        A.kvpages_reserve(table, n, refs.long(), row, 16)
+    status()

@@ -305,3 +305,71 @@ def test_long_sequences_over_many_levels(dev):
             torch.zeros(1, 17000, dtype=torch.bool, device=dev), -INF), -1) for i in range(0, 17000, 500)], 1)
         assert (lse[:, :17000].double() - e).abs().max() <= P.sum_error(17000) + P.sum_error(16) * 30 + 2.0 ** -18
         check_fwd(o[17000:], lse[:, 17000:], q[17000:], k[17000:], v[17000:], lens[1:], causal, False)
+
+
+def test_empty_sequences_and_tokens_behind_them(dev):
+    for lens, behind in (([0, 0, 0], 5), ([0], 3), ([0, 7, 0], 0), ([0, 0, 1], 130)):
+        q, k, v, dout, cu = make(dev, "bf16", 4, 2, 64, lens, seed=10, behind=behind)
+        for bound in (max(max(lens), 1), 3000):
+            o, lse = A.fwd_varlen_gqa(q, k, v, cu, bound, True)
+            check_fwd(o, lse, q, k, v, lens, True, False)
+            check_bwd(A.bwd_varlen_gqa(q, k, v, o, lse, dout, cu, bound, True), q, k, v, dout, lens, True, False)
+            status()
+    q = torch.empty(0, 4, 64, device=dev, dtype=torch.float16)
+    k = torch.empty(0, 2, 64, device=dev, dtype=torch.float16)
+    o, lse = A.fwd_varlen_gqa(q, k, k, torch.zeros(3, dtype=torch.int32, device=dev), 8, True)
+    assert o.shape == (0, 4, 64) and lse.shape == (4, 0)
+    assert [x.shape[0] for x in A.bwd_varlen_gqa(q, k, k, o, lse, o, torch.zeros(3, dtype=torch.int32, device=dev), 8, True)] == [0, 0, 0]
+    status()
+
+
+def test_elements_past_32_bits(dev):
+    """1350 sequences of 100 tokens with 128 query heads: 2.2e9 elements of q, and the last sequences' rows."""
+    n, L, Hq, Hkv, d = 1350, 100, 128, 2, 128
+    T = n * L
+    q, dout = (torch.zeros(T, Hq, d, device=dev, dtype=torch.bfloat16) for _ in range(2))
+    k, v = (torch.zeros(T, Hkv, d, device=dev, dtype=torch.bfloat16) for _ in range(2))
+    assert q.numel() > 2 ** 31
+    g = torch.Generator(dev).manual_seed(11)
+    picks = [0, 7, n // 2, n - 2, n - 1]
+    for i in picks:
+        for x in (q, k, v, dout):
+            x[i * L:(i + 1) * L] = torch.randn(L, x.shape[1], d, generator=g, device=dev).to(x.dtype)
+    cu = torch.arange(0, T + 1, L, device=dev, dtype=torch.int32)
+    o, lse = A.fwd_varlen_gqa(q, k, v, cu, L, True)
+    got = A.bwd_varlen_gqa(q, k, v, o, lse, dout, cu, L, True)
+    status()
+    for i in picks:
+        t = slice(i * L, (i + 1) * L)
+        check_fwd(o[t], lse[:, t], q[t], k[t], v[t], [L], True, False)
+        check_bwd([x[t] for x in got], q[t], k[t], v[t], dout[t], [L], True, False)
+    t = slice(3 * L, 4 * L)
+    assert (o[t] == 0).all() and all((x[t] == 0).all() for x in got)
+
+
+def test_refusals(dev):
+    """What the library refuses comes back as an error before anything runs; shapes and types in the Python layer."""
+    q, k, v, dout, cu = make(dev, "bf16", 4, 2, 64, [20, 9], seed=12, fused=False)
+    for bad in (lambda: A.fwd_varlen_gqa(q.transpose(0, 1), k, v, cu, 20, True), lambda: A.fwd_varlen_gqa(q[..., :32], k, v, cu, 20, True),
+                lambda: A.fwd_varlen_gqa(q, k[:-1], v[:-1], cu, 20, True), lambda: A.fwd_varlen_gqa(q, k, v[:, :1], cu, 20, True),
+                lambda: A.fwd_varlen_gqa(q, k, v, cu[:1], 20, True), lambda: A.fwd_varlen_gqa(q, k, v, cu[None], 20, True),
+                lambda: A.fwd_varlen_gqa(q, k, v, cu, -1, True), lambda: A.fwd_varlen_gqa(q[:, :3], k, v, cu, 20, True),
+                lambda: A.fwd_varlen_gqa(q, k, v, cu, 2 ** 31, True), lambda: A.fwd_varlen_gqa(q, k, v, cu, 20, True, scale=-1.0),
+                lambda: A.fwd_varlen_gqa(q, k.expand(29, 2, 64).transpose(1, 2), v, cu, 20, True)):
+        with pytest.raises((ValueError, TypeError, _lib.AttnError)):
+            bad()
+    for bad in (lambda: A.fwd_varlen_gqa(q, k.half(), v, cu, 20, True), lambda: A.fwd_varlen_gqa(q, k, v, cu.long(), 20, True),
+                lambda: A.fwd_varlen_gqa(q.double(), k.double(), v.double(), cu, 20, True), lambda: A.fwd_varlen_gqa([q], k, v, cu, 20, True)):
+        with pytest.raises(TypeError):
+            bad()
+    with pytest.raises(_lib.AttnError):  # a workspace that is too small
+        A.fwd_varlen_gqa(q, k, v, cu, 20, True, workspace=torch.empty(64, dtype=torch.uint8, device=dev))
+    x = torch.zeros(29, 4 * 64 + 4, device=dev, dtype=torch.bfloat16)
+    with pytest.raises(_lib.AttnError):  # tokens 8 bytes off the 16 that a copy needs
+        A.fwd_varlen_gqa(x[:, :256].view(29, 4, 64), k, v, cu, 20, True)
+    o, lse = A.fwd_varlen_gqa(q, k, v, cu, 20, True)
+    for bad in (lambda: A.bwd_varlen_gqa(q, k, v, o[:-1], lse, dout, cu, 20, True), lambda: A.bwd_varlen_gqa(q, k, v, o, lse.t(), dout, cu, 20, True),
+                lambda: A.bwd_varlen_gqa(q, k, v, o, lse, dout[:, :2], cu, 20, True)):
+        with pytest.raises(ValueError):
+            bad()
+    status()
