@@ -718,7 +718,8 @@ def _of_rows(B, *named):
 def kvpages_free(page_table, cache_seqlens, refs, keep_seqlens, page: int, out=None):
     """Cuts each sequence to its first keep_seqlens[b] tokens (0 ends it) and gives back the pages behind them.  page_table
     int32 [B,max_pages], cache_seqlens and keep_seqlens int32 [B], refs int32 [pages].  out: (page_table, cache_seqlens,
-    refs) to write to, which may be the inputs (None: new ones).  Returns those three."""
+    refs) to write to, which may be the inputs (None: new ones).  Returns those three.  A row that is cut inside a page
+    which others share must be forked to an empty row before tokens are appended: they would be written into theirs."""
     dev, B, M, P, o = _books(page_table, refs, (cache_seqlens, keep_seqlens), ("cache_seqlens", "keep_seqlens"), page, out,
                              (page_table, cache_seqlens, refs))
     _of_rows(B, (cache_seqlens, "cache_seqlens"), (keep_seqlens, "keep_seqlens"))

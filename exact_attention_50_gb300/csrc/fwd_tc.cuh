@@ -1099,6 +1099,7 @@ cudaError_t launch_fwd_tc_t(const FwdMaps& maps, const FwdParams& p, cudaStream_
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     const long long most = packed_bound(p.total_tokens, p.nseq, p.max_seqlen, p.tile_tokens) * (p.Hq / p.heads);
+    if (!p.tiles && most > static_cast<long long>(L::kListed) * sm_count()) return cudaErrorInvalidValue;  // items that nothing lists
     cfg.gridDim = dim3(static_cast<unsigned>(most < sm_count() ? most : sm_count()));
     cfg.blockDim = dim3(L::kThreads);
     cfg.dynamicSmemBytes = L::kSmemAlloc;

@@ -353,12 +353,10 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const PagesPara
   t.cl.sync();  // the moves are known
   for (long long i = t.tid; i < static_cast<long long>(p.B) * p.M; i += t.threads) {
     int e = p.table[i];
-    if (e >= p.P) {
+    if (e >= p.P || (e >= 0 && !is_used(e)))  // outside the pool, or counted as free
       raise_status(p.status, ATTN_ERR_DEVICE_INPUT);
-    } else if (e >= U) {
-      if (is_used(e)) e = p.copies[2 * static_cast<size_t>(ranks.rank(t, s, e, is_used) - in_front) + 1];
-      else raise_status(p.status, ATTN_ERR_DEVICE_INPUT);  // a page that is counted as free
-    }
+    else if (e >= U)
+      e = p.copies[2 * static_cast<size_t>(ranks.rank(t, s, e, is_used) - in_front) + 1];
     p.table_out[i] = e;
   }
   t.cl.sync();  // the counts have been read: the first U may change, then the others

@@ -414,6 +414,8 @@ attn_status_t attn_kvpages_append(void* k_pages, void* v_pages, const int32_t* p
  *
  * free: cuts each sequence to its first keep_seqlens[b] tokens (all when it has no more; 0 ends it).  The pages behind
  * the ones that these need lose a reference, and their entries become -1.  Refused: a negative length or number, for its row.
+ * A row that is cut inside a page that others share goes on sharing it: what is appended to it there is written into
+ * theirs too.  Fork such a row to an empty one, which gets that page for itself, and append to the fork.
  */
 attn_status_t attn_kvpages_free(const int32_t* page_table, const int32_t* cache_seqlens, const int32_t* refs, const int32_t* keep_seqlens,
                                 int32_t* table_out, int32_t* seqlens_out, int32_t* refs_out, int B, int max_pages, int pages, int page,
@@ -423,7 +425,8 @@ attn_status_t attn_kvpages_free(const int32_t* page_table, const int32_t* cache_
  * are shared (a reference each); a last page that is partly filled is replaced by a free one, and copies[i] says which
  * page to copy where, for attn_kvpages_copy in each layer, or (-1, -1).  Sources are as they were before the call.
  * Refused, pair by pair: numbers out of range; a dst that is not empty, or stands in the list before; a source without its
- * last page; a page that is not there, free pages going to the pairs in order.
+ * last page; a page that is not there, free pages going to the pairs in order.  An entry among a source's full pages that
+ * is no page of the pool becomes -1, with the status.
  *   src, dst       DEVICE int32 [n]; copies DEVICE int32 [n, 2], 8-byte aligned
  */
 attn_status_t attn_kvpages_fork(const int32_t* page_table, const int32_t* cache_seqlens, const int32_t* refs, const int32_t* src,

@@ -163,7 +163,7 @@ def compact(table, refs):
         for i, x in enumerate(row):
             if x in to:
                 row[i] = to[x]
-            elif x >= U:
+            elif x >= U or (x >= 0 and refs[x] <= 0):
                 bad = True
     out = [r if r > 0 else 0 for r in refs[:U]] + [0] * (len(refs) - U)
     for a, b in moves:

@@ -150,6 +150,37 @@ def test_compact(dev, B, M, pages, page, in_place):
         assert got[2].tolist() == want[2] and got[3].tolist() == [want[3]]
 
 
+def test_compact_entry_that_counts_as_free(dev):
+    """A stale entry keeps its number and raises the status, before the used pages' end as behind it."""
+    for entry in (1, 3, 6):  # U = 4: free places 1 and 3 are filled from 5 and 7, page 6 is free and stays so
+        table, refs = [[0, 2, 5], [5, 7, entry]], [1, 0, 1, 0, 0, 2, 0, 1]
+        want = P.compact(table, refs)
+        assert want[4] and want[0][1] == [1, 3, entry]
+        got = A.kvpages_compact(ints(table, dev), ints(refs, dev))
+        status(True)
+        assert got[0].tolist() == want[0] and got[1].tolist() == want[1] and got[2].tolist() == want[2] and got[3].tolist() == [4]
+
+
+def test_cut_inside_a_shared_page(dev):
+    """A row cut inside a page that another shares gets it for itself by a fork: what is appended leaves the other as it was."""
+    page, d, Hkv = 16, 64, 2
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn(9, Hkv, page, d, generator=g).to(dev, torch.bfloat16) for _ in range(2))
+    table, lens, refs = ints([[4, 7, 2], [4, 7, -1], [-1, -1, -1]], dev), ints([40, 32, 0], dev), ints([0, 0, 1, 0, 2, 0, 0, 2, 0], dev)
+    before = k[[4, 7, 2]].clone(), v[[4, 7, 2]].clone()
+    table, lens, refs = A.kvpages_free(table, lens, refs, ints([99, 21, 0], dev), page)
+    assert lens.tolist() == [40, 21, 0] and refs.tolist() == [0, 0, 1, 0, 2, 0, 0, 2, 0]
+    table, lens, refs, copies = A.kvpages_fork(table, lens, refs, ints([1], dev), ints([2], dev), page)
+    A.kvpages_copy(k, v, copies)
+    table, lens, refs = A.kvpages_free(table, lens, refs, ints([99, 0, 99], dev), page)
+    assert table.tolist() == [[4, 7, 2], [-1, -1, -1], [4, 0, -1]] and refs.tolist() == [1, 0, 1, 0, 2, 0, 0, 1, 0]
+    x = torch.randn(5, Hkv, d, generator=g).to(dev, torch.bfloat16)
+    A.kvpages_append(k, v, table, x, -x, ints([0, 0, 0, 5], dev), lens)
+    status(False)
+    assert torch.equal(k[[4, 7, 2]], before[0]) and torch.equal(v[[4, 7, 2]], before[1])
+    assert torch.equal(k[0, :, :5], before[0][1][:, :5]) and torch.equal(k[0, :, 5:10], x.transpose(0, 1)) and torch.equal(v[0, :, 5:10], -x.transpose(0, 1))
+
+
 def test_books_of_every_row(dev):
     """65536 rows: the largest table."""
     B, page = 65536, 16
