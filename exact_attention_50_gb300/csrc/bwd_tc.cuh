@@ -99,18 +99,6 @@ __device__ __forceinline__ void split_pack<__half>(float a, float b, uint32_t& h
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
-// Packed sequences: tokens from a sequence's start whose D is summed over the keys, a warp's lanes (without the causal mask:
-// if the sequence has no more).  The preprocess takes D from O as it was stored, rounded to 16 bits.  A row that sees many keys has
-// an O much smaller than the values, and that rounding does not show.  A row of a few keys has not, and its
-// dP_ij - D_i is a small difference: with one key it is zero, but |dO| |v| 2^-9 of noise came out.
-// Error of dq against 64 bits, relative by the 2-norm, in 1e-4, with D from O everywhere / exact up to 16 / 32 / 64 keys / of
-// rounding dq alone: bf16, causal, 10 to 30 tokens 22.3 / 16.9 / 16.6 / 16.6 / 16.6, 40 to 120 tokens 20.1 / 17.3 / 16.9 / 16.7 /
-// 16.6, 64 to 1500 tokens 18.6 / 17.1 / 16.9 / 16.8 / 16.6; 1 to 9 tokens come out to the rounding.  The largest
-// single error of the third, of the larger of the value and the root mean square: 0.049 / 0.016 / 0.014 / 0.014.
-// It costs 4 x 2048 tokens 6 us of 416, 200 sequences of 9 to 150 tokens (d = 64) 6 of 87, 512 of 32 tokens 14 of 499.  (Behind
-// the loads of dP, with the loop's registers full, 20 of the first; a kernel of its own before this one 135 of the third.)
-constexpr int kFew = 32;
-
 // PACKED: packed sequences with grouped heads.  The CTA's key tile comes from the list of tiles (launch_packed_tiles),
 // and a query tile is p.tile_tokens tokens by p.heads neighbouring query heads, row = token * heads + head, so short
 // sequences fill it.  What lies in the tiles behind the sequence's end is another sequence's, or anything: warp 15 sets
@@ -690,7 +678,6 @@ __global__ void __launch_bounds__(512, 1)
       }
     };
     load_rows(0);
-    const int few = PACKED && (CAUSAL || seq_len <= kFew) ? kFew : 0;
     for (int it = 0; it < n_it; ++it) {
       const int qt = qt0 + it % per_head;
       float* lse_buf = sLse + (it & 1) * 128;
@@ -759,33 +746,6 @@ __global__ void __launch_bounds__(512, 1)
       // the dS hi area is free; the dS lo area waits for the reductions of the dQ chunks staged in it.
       if (!mbar_wait_warp(dp_full, it & 1, abort_flag, p.status)) break;
       tc_fence_after();
-      if (PACKED && kt == 0 && quad == 0 && qt * qtok < few) {
-        // Rows whose keys are all this warp's (the first 32 of the sequence): D = sum over the lanes of P dP, exactly, in
-        // place of dO . O with O rounded (see kFew).  By way of this warp's rows of the dS area, 32 columns at a time.  The
-        // other warps may read either D: their keys are masked for these rows, P = 0.
-        uint8_t* const own = sdSh + half * L::kChunkBytes + quad * 4096;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t r[32];
-          tmem_ld32(tl + L::kColdP + half * 64 + 32 * h, r);
-          tmem_ld_wait();
-          tmem_reg_fence(r);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4*>(own + lane * 128 + ((i ^ (lane & 7)) << 4)) =
-                make_float4(pv[32 * h + 4 * i] * __uint_as_float(r[4 * i]), pv[32 * h + 4 * i + 1] * __uint_as_float(r[4 * i + 1]),
-                            pv[32 * h + 4 * i + 2] * __uint_as_float(r[4 * i + 2]), pv[32 * h + 4 * i + 3] * __uint_as_float(r[4 * i + 3]));
-          __syncwarp();
-          float sum = 0.f;
-#pragma unroll 1
-          for (int j = 0; j < 32; j += 8)
-#pragma unroll
-            for (int u = 0; u < 8; ++u) sum += *reinterpret_cast<const float*>(own + (j + u) * 128 + (((lane >> 2) ^ u) << 4) + (lane & 3) * 4);
-          const int col = half * 64 + 32 * h + lane;
-          if (qt * qtok + col / qheads < few) d_buf[col] = -sum;
-          __syncwarp();
-        }
-      }
       uint32_t r0[32], r1[32];
       tmem_ld32(tl + L::kColdP + half * 64, r0);
       tmem_ld32(tl + L::kColdP + half * 64 + 32, r1);
