@@ -1230,8 +1230,8 @@ attn_status_t attn_bwd_varlen_gqa(const void* q, const void* k, const void* v, c
     if (attn::launch_packed_tiles(cu_seqlens, nseq, total_tokens, max_seqlen, attn::kBN, by_level, true, head, tiles, p.status, s) != cudaSuccess)
       return ATTN_ERR_CUDA;
   }
-  if (attn::launch_bwd_preprocess(p, dtype, dtype != ATTN_F32, s) != cudaSuccess) return ATTN_ERR_CUDA;
   if (dtype == ATTN_F32) {
+    if (attn::launch_bwd_preprocess(p, dtype, false, s) != cudaSuccess) return ATTN_ERR_CUDA;
     p.lay_k = {k_stride, d};
     p.lay_v = {v_stride, d};
     void* const x[3] = {dq, dk, dv};
@@ -1248,6 +1248,7 @@ attn_status_t attn_bwd_varlen_gqa(const void* q, const void* k, const void* v, c
       !make_rows_map(&maps.k, k, dtype, total_tokens, Hkv, d, k_stride, d) || !make_rows_map(&maps.v, v, dtype, total_tokens, Hkv, d, v_stride, d) ||
       !make_packed_acc_map(&maps.dq_acc, p.dq_acc, total_tokens, Hq, d, t))
     return ATTN_ERR_CUDA;
+  if (attn::launch_packed_delta(maps, p, dtype, causal != 0, s) != cudaSuccess) return ATTN_ERR_CUDA;
   if (attn::launch_bwd_packed(maps, p, dtype, causal != 0, s) != cudaSuccess) return ATTN_ERR_CUDA;
   return from_cuda(attn::launch_bwd_postprocess(p, dtype, s));
 }

@@ -7,7 +7,6 @@
 // Both are HBM-bound streams with 16-byte accesses.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include "cache8.cuh"
 #include "kernels.h"
 
 namespace attn {
@@ -74,7 +73,6 @@ __global__ void __launch_bounds__(256) preprocess_kernel(const T* __restrict__ o
       }
     }
   }
-  dependency_wait();  // packed sequences: the kernel behind this one needs the list of tiles too
 }
 
 template <typename T>
@@ -163,30 +161,27 @@ bool contiguous(const BwdParams::Rows& lay, const BwdParams& p) {
   return lay.row == p.d && lay.head == static_cast<long long>(p.N) * p.d;
 }
 
-template <typename T, bool CONTIG, int GS>
-cudaError_t preprocess_launch(const BwdParams& p, float* acc, long rows, int grid, cudaStream_t stream) {
+template <typename T, bool CONTIG>
+void preprocess_g(const BwdParams& p, float* acc, long rows, int grid, cudaStream_t stream) {
   const T* o = static_cast<const T*>(p.o);
   const T* g = static_cast<const T*>(p.dout);
-  // Packed sequences: beside the one CTA that makes the list of tiles (200 sequences, forward and backward: 163.4 us, now 161.4).
-  if (p.tiles) return launch_dependent(preprocess_kernel<T, CONTIG, GS>, dim3(grid), 256, stream, o, g, p.delta, acc, p.dq_turn, rows, p.N, p.lay_o, p.d);
-  preprocess_kernel<T, CONTIG, GS><<<grid, 256, 0, stream>>>(o, g, p.delta, acc, p.dq_turn, rows, p.N, p.lay_o, p.d);
-  return cudaGetLastError();
-}
-
-template <typename T, bool CONTIG>
-cudaError_t preprocess_g(const BwdParams& p, float* acc, long rows, int grid, cudaStream_t stream) {
   const int lanes = p.d / (16 / static_cast<int>(sizeof(T)));  // 16-byte vectors per row: 2 .. 32
-  if (lanes <= 4) return preprocess_launch<T, CONTIG, 4>(p, acc, rows, grid, stream);
-  if (lanes <= 8) return preprocess_launch<T, CONTIG, 8>(p, acc, rows, grid, stream);
-  // 16-bit rows of d <= 128 take at most 16 vectors
-  if (sizeof(T) == 2 || lanes <= 16) return preprocess_launch<T, CONTIG, 16>(p, acc, rows, grid, stream);
-  return preprocess_launch<T, CONTIG, sizeof(T) == 4 ? 32 : 16>(p, acc, rows, grid, stream);
+  if (lanes <= 4)
+    preprocess_kernel<T, CONTIG, 4><<<grid, 256, 0, stream>>>(o, g, p.delta, acc, p.dq_turn, rows, p.N, p.lay_o, p.d);
+  else if (lanes <= 8)
+    preprocess_kernel<T, CONTIG, 8><<<grid, 256, 0, stream>>>(o, g, p.delta, acc, p.dq_turn, rows, p.N, p.lay_o, p.d);
+  else if (sizeof(T) == 2 || lanes <= 16)  // 16-bit rows of d <= 128 take at most 16 vectors
+    preprocess_kernel<T, CONTIG, 16><<<grid, 256, 0, stream>>>(o, g, p.delta, acc, p.dq_turn, rows, p.N, p.lay_o, p.d);
+  else if constexpr (sizeof(T) == 4)
+    preprocess_kernel<T, CONTIG, 32><<<grid, 256, 0, stream>>>(o, g, p.delta, acc, p.dq_turn, rows, p.N, p.lay_o, p.d);
 }
 
 template <typename T>
-cudaError_t preprocess_t(const BwdParams& p, float* acc, long rows, int grid, cudaStream_t stream) {
-  if (contiguous(p.lay_o, p)) return preprocess_g<T, true>(p, acc, rows, grid, stream);
-  return preprocess_g<T, false>(p, acc, rows, grid, stream);
+void preprocess_t(const BwdParams& p, float* acc, long rows, int grid, cudaStream_t stream) {
+  if (contiguous(p.lay_o, p))
+    preprocess_g<T, true>(p, acc, rows, grid, stream);
+  else
+    preprocess_g<T, false>(p, acc, rows, grid, stream);
 }
 
 template <typename OutT>
@@ -206,10 +201,11 @@ cudaError_t launch_bwd_preprocess(const BwdParams& p, attn_dtype_t dtype, bool z
   const int grid = grid_for(rows, 64);
   float* acc = zero_acc ? p.dq_acc : nullptr;
   switch (dtype) {
-    case ATTN_F32: return preprocess_t<float>(p, acc, rows, grid, stream);
-    case ATTN_F16: return preprocess_t<__half>(p, acc, rows, grid, stream);
-    default: return preprocess_t<__nv_bfloat16>(p, acc, rows, grid, stream);
+    case ATTN_F32: preprocess_t<float>(p, acc, rows, grid, stream); break;
+    case ATTN_F16: preprocess_t<__half>(p, acc, rows, grid, stream); break;
+    default: preprocess_t<__nv_bfloat16>(p, acc, rows, grid, stream); break;
   }
+  return cudaGetLastError();
 }
 
 cudaError_t launch_bwd_postprocess(const BwdParams& p, attn_dtype_t dtype, cudaStream_t stream) {

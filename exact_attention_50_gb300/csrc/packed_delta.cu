@@ -1,0 +1,312 @@
+// packed_delta.cu -- what the backward of packed sequences needs beforehand: the row terms D, and zeros in the dQ accumulator.
+//
+//   dS_ij = P_ij (dP_ij - D_i),   dP_ij = dO_i . v_j,   D_i = sum_j P_ij dP_ij  ( = dO_i . O_i ).
+// dO . O with O as it was stored, rounded to 16 bits, costs one sweep of memory, and is right to |dO| |O| 2^-9.  Where a row's
+// weight lies on a few keys, O is as large as the values and dP - D is a small difference: the row's gradient came
+// out off by that times its keys.  (16 x 64 to 2048 tokens with channels of different size, bf16: the largest error of
+// dq was 0.54 of its root mean square; 1 to 9 tokens, fp16: 6.2e-4 by the 2-norm, of which 2.1e-4 is dq's own
+// rounding.)  O from the same products to more bits would not do, because P was rounded in them.  So D is summed over
+// the keys in fp32, with the P of the main kernel.
+//
+// A CTA per key tile of the list and kv head, as in the main kernel, here for the 128 tokens as queries: query tiles of
+// tile_tokens tokens by `heads` heads, all keys they see.  Warp 8 loads (Q and dO, two tiles; K and V through one ring), warp 9
+// issues S = Q K^T and dP = dO V^T into two stages of TMEM, a thread of warps 0-7 has 64 columns of a row and adds up
+// exp2(S scale log2e - LSE log2e) dP; nothing is written back and nothing rescaled.  Warps 10 and 11 write the zeros meanwhile.
+// 4 x 2048 tokens, 32 over 8 heads, d = 128: 150 us, 137 GFLOP at 0.9 PFLOP/s, where the sweep and its zeros took 40; errors against 64
+// bits are those of rounding the results (dq, dk, dv 16.6e-4 in bf16, 2.07e-4 in fp16, at all lengths).
+#include "bwd_tc.cuh"
+
+namespace attn {
+namespace {
+
+template <int DP>
+struct DeltaLayout {
+  static constexpr int kChunks = DP / 64;
+  static constexpr int kChunkBytes = 128 * 128;
+  static constexpr int kTileBytes = kChunks * kChunkBytes;
+  static constexpr int kRing = DP == 128 ? 3 : 6;          // tiles of K, V, K, V, ...
+  static constexpr int kOffQ = 0;                           // two slots of Q and dO
+  static constexpr int kOffRing = kOffQ + 4 * kTileBytes;
+  static constexpr int kOffSum = kOffRing + kRing * kTileBytes;  // [4][128] sums of the second halves
+  static constexpr int kOffBar = kOffSum + 4 * 128 * 4;
+  static constexpr int kNumBars = 2 + 2 + 2 * kRing + 2 + 2 + 4 + 1;
+  static constexpr int kOffMisc = kOffBar + 8 * kNumBars;  // tmem base, abort flag, wait limit (u64)
+  static constexpr int kBytes = kOffMisc + 16;
+  static_assert(kBytes <= 227 * 1024 && kOffMisc % 8 == 0, "shared memory of a CTA");
+  static constexpr int kThreads = 384;
+  static constexpr uint32_t kTmemCols = 512, kColS = 0, kColdP = 256;  // two stages of 128 columns each
+};
+
+template <typename T, int DP, bool CAUSAL>
+__global__ void __launch_bounds__(384, 1)
+    packed_delta_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                        const __grid_constant__ CUtensorMap tmdO, const BwdParams p) {
+  using L = DeltaLayout<DP>;
+  constexpr int kChunks = L::kChunks, R = L::kRing;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (p.tiles) dependency_wait();  // the list of tiles
+  const int e = blockIdx.x / p.Hkv, hkv = blockIdx.x - e * p.Hkv;
+  int count, last;
+  int4 tile;
+  if (p.tiles) {
+    count = p.head[0];
+    last = p.head[1];
+    tile = p.tiles[e];
+  } else {  // one sequence; the main kernel reports it where it breaks the rules
+    const int len = packed_single(p.cu_seqlens, p.N, p.max_seqlen), end = p.cu_seqlens[1];
+    tile = make_int4(0, len, e, 0);
+    count = (len + kBN - 1) / kBN;
+    last = end >= 0 && end <= p.N ? end : p.N;
+  }
+  // rows behind the last sequence: dQ = 0
+  for (int tok = last + static_cast<int>(blockIdx.x); tok < p.N; tok += static_cast<int>(gridDim.x))
+    for (int i = threadIdx.x; i < p.Hq * p.d / 4; i += L::kThreads)
+      reinterpret_cast<float4*>(p.dq_acc + static_cast<size_t>(tok) * p.Hq * p.d)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (e >= count || tile.y == 0) return;  // the whole CTA
+  if (smem_u32(smem) & 1023u) {           // the swizzle needs aligned tiles
+    if (threadIdx.x == 0) raise_status(p.status, ATTN_ERR_CUDA);
+    return;
+  }
+  const int start = tile.x, len = tile.y, tok0 = tile.z * kBN, tok1 = min(len, tok0 + kBN);  // the tokens that are its queries
+  const int qtok = p.tile_tokens, qheads = p.heads;
+  const int per_head = (tok1 - tok0 + qtok - 1) / qtok, n_q = p.G / qheads * per_head;  // query tiles
+  const int n_kv = CAUSAL ? tile.z + 1 : (len + kBN - 1) / kBN;
+  uint8_t* const ring = smem + L::kOffRing;
+  uint64_t* const q_full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  uint64_t* const q_empty = q_full + 2;
+  uint64_t* const r_full = q_empty + 2;
+  uint64_t* const r_empty = r_full + R;
+  uint64_t* const s_full = r_empty + R;
+  uint64_t* const s_empty = s_full + 2;
+  uint64_t* const sum_full = s_empty + 2;
+  uint64_t* const drain = sum_full + 4;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
+  const uint32_t abort_flag = smem_u32(smem + L::kOffMisc + 4);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + i, 1);
+      mbar_init(q_empty + i, 1);
+      mbar_init(s_full + i, 1);
+      mbar_init(s_empty + i, 8);  // one arrival per warp
+    }
+    for (int i = 0; i < R; ++i) {
+      mbar_init(r_full + i, 1);
+      mbar_init(r_empty + i, 1);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(sum_full + i, 4);
+    mbar_init(drain, 1);
+    abort_set(abort_flag, 0);
+    wait_limit_set(abort_flag, p.wait_ns);
+    mbar_init_fence();
+  }
+  if (warp == 8) tmem_alloc(tmem_slot, L::kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 8) {
+    // ================================================================ TMA producer
+    if (lane == 0) {
+      int nq = 0;       // query tiles loaded
+      uint32_t nr = 0;  // tiles of the ring loaded
+      const auto load_q = [&]() -> bool {
+        const int t = nq, s = t & 1, hq = hkv * p.G + t / per_head * qheads, tok = start + tok0 + t % per_head * qtok;
+        if (t >= 2 && !mbar_wait(q_empty + s, ((t >> 1) - 1) & 1, abort_flag, p.status)) return false;
+        mbar_expect_tx(q_full + s, 2 * kChunks * qtok * qheads * 128);
+        uint8_t* const dst = smem + L::kOffQ + s * 2 * L::kTileBytes;
+        for (int c = 0; c < kChunks; ++c) {
+          tma_load_3d(dst + c * L::kChunkBytes, &tmQ, q_full + s, c * 64, hq, tok);
+          tma_load_3d(dst + L::kTileBytes + c * L::kChunkBytes, &tmdO, q_full + s, c * 64, hq, tok);
+        }
+        ++nq;
+        return true;
+      };
+      const auto load_r = [&](const CUtensorMap* map, int j) -> bool {
+        const uint32_t s = nr % R;
+        if (nr >= static_cast<uint32_t>(R) && !mbar_wait(r_empty + s, ((nr / R) - 1) & 1, abort_flag, p.status)) return false;
+        mbar_expect_tx(r_full + s, L::kTileBytes);
+        for (int c = 0; c < kChunks; ++c) tma_load_3d(ring + s * L::kTileBytes + c * L::kChunkBytes, map, r_full + s, c * 64, start + j * kBN, hkv);
+        ++nr;
+        return true;
+      };
+      bool ok = load_q();
+      for (int t = 0; ok && t < n_q; ++t)
+        for (int j = 0; ok && j < n_kv; ++j) {
+          ok = load_r(&tmK, j) && load_r(&tmV, j);
+          if (ok && j == 0 && nq < n_q) ok = load_q();  // the next one, as soon as there is room
+        }
+      if (abort_read(abort_flag)) {  // let the copies land before the shared memory goes away
+        for (int t = max(0, nq - 2); t < nq; ++t) mbar_drain(q_full + (t & 1), (t >> 1) & 1);
+        for (uint32_t i = nr > static_cast<uint32_t>(R) ? nr - R : 0; i < nr; ++i) mbar_drain(r_full + i % R, (i / R) & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ================================================================ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t id = idesc_f16(Elem<T>::kBf16, false, false, 128, 128);
+      const uint64_t dq = smem_desc_sw128(smem_u32(smem + L::kOffQ), 16, 1024), dr = smem_desc_sw128(smem_u32(ring), 16, 1024);
+      constexpr uint32_t kTile16 = L::kTileBytes >> 4;
+      uint32_t n = 0, u = 0;  // key tiles, tiles of the ring passed
+      bool ok = true;
+      const auto product = [&](uint32_t col, uint64_t a0) -> bool {
+        const uint32_t s = u % R;
+        if (!mbar_wait(r_full + s, (u / R) & 1, abort_flag, p.status)) return false;
+        tc_fence_after();
+        const uint64_t a = opaque(a0), b = opaque(dr + s * kTile16);
+#pragma unroll
+        for (int ks = 0; ks < DP / 16; ++ks) {
+          const uint32_t off = ((ks >> 2) * L::kChunkBytes + (ks & 3) * 32) >> 4;
+          mma_ss(tmem + col, a + off, b + off, id, ks > 0 ? 1u : 0u);
+        }
+        mma_commit(r_empty + s);
+        ++u;
+        return true;
+      };
+      for (int t = 0; ok && t < n_q; ++t) {
+        const uint64_t q = dq + (t & 1) * 2 * kTile16;
+        ok = mbar_wait(q_full + (t & 1), (t >> 1) & 1, abort_flag, p.status);
+        for (int j = 0; ok && j < n_kv; ++j, ++n) {
+          const uint32_t b = n & 1;
+          if (n >= 2 && !mbar_wait(s_empty + b, ((n >> 1) - 1) & 1, abort_flag, p.status)) { ok = false; break; }
+          tc_fence_after();
+          ok = product(L::kColS + b * 128, q) && product(L::kColdP + b * 128, q + kTile16);
+          if (ok) mma_commit(s_full + b);
+        }
+        if (ok) mma_commit(q_empty + (t & 1));
+      }
+      if (!ok) {
+        mma_commit(drain);
+        mbar_drain(drain, 0);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 10) {
+    // ================================================================ zeros for these tokens' rows of dQ
+    const int first = threadIdx.x - 320, vecs = p.G * p.d / 4;
+    for (int tok = tok0; tok < tok1; ++tok) {
+      const size_t row = static_cast<size_t>(start + tok) * p.Hq + hkv * p.G;
+      float4* const dst = reinterpret_cast<float4*>(p.dq_acc + row * p.d);
+      for (int i = first; i < vecs; i += 64) dst[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p.deterministic)
+        for (int i = first; i < p.G; i += 64) p.dq_turn[row + i] = 0;
+    }
+  } else {
+    // ================================================================ rows
+    const int quad = warp & 3, half = warp >> 2, r = quad * 32 + lane;
+    const int my_tok = r / qheads, my_head = r - my_tok * qheads;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 64;
+    float* const s_sum = reinterpret_cast<float*>(smem + L::kOffSum);
+    const uint64_t scl = f2_pack(p.scale_log2, p.scale_log2);
+    uint32_t n = 0;
+    bool ok = true;
+    for (int t = 0; ok && t < n_q; ++t) {
+      const int q = tok0 + t % per_head * qtok + my_tok, head = hkv * p.G + t / per_head * qheads + my_head;
+      const bool valid = my_tok < qtok && q < tok1;
+      const float nl = valid ? -(p.lse[static_cast<size_t>(head) * p.N + start + q] * 1.4426950408889634f) : -INFINITY;
+      const int seen = CAUSAL ? min(q + 1, len) : len;
+      const uint64_t nlb = f2_pack(nl, nl);
+      float sum = 0.f;
+      uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
+      for (int j = 0; j < n_kv; ++j, ++n) {
+        const uint32_t b = n & 1;
+        if (!mbar_wait_warp(s_full + b, (n >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t s0[32], s1[32], d0[32], d1[32];
+        tmem_ld32(tl + L::kColS + b * 128, s0);
+        tmem_ld32(tl + L::kColdP + b * 128, d0);
+        tmem_ld32(tl + L::kColS + b * 128 + 32, s1);
+        tmem_ld32(tl + L::kColdP + b * 128 + 32, d1);
+        tmem_ld_wait();
+        tmem_reg_fence(s0);
+        tmem_reg_fence(d0);
+        tmem_reg_fence(s1);
+        tmem_reg_fence(d1);
+        tc_fence_before();
+        mbar_arrive_warp(s_empty + b);
+        const int vis = seen - j * kBN - half * 64;  // this row sees columns [0, vis)
+        if (__all_sync(0xffffffffu, vis >= 64)) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t(&s)[32] = h ? s1 : s0;
+            uint32_t(&d)[32] = h ? d1 : d0;
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float2 x = f2_unpack(f2_fma(f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), scl, nlb));
+              const float2 y = f2_unpack(f2_fma(f2_pack(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), scl, nlb));
+              acc0 = f2_fma(f2_pack(ex2_approx(x.x), ex2_approx(x.y)), f2_pack(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), acc0);
+              acc1 = f2_fma(f2_pack(ex2_approx(y.x), ex2_approx(y.y)), f2_pack(__uint_as_float(d[i + 2]), __uint_as_float(d[i + 3])), acc1);
+            }
+          }
+        } else if (__any_sync(0xffffffffu, vis > 0)) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t(&s)[32] = h ? s1 : s0;
+            uint32_t(&d)[32] = h ? d1 : d0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float x = ex2_approx(fmaf(__uint_as_float(s[i]), p.scale_log2, nl)) * __uint_as_float(d[i]);
+              sum += 32 * h + i < vis ? x : 0.f;
+            }
+          }
+        }
+      }
+      if (!ok) break;
+      const float2 a0 = f2_unpack(acc0), a1 = f2_unpack(acc1);
+      sum += (a0.x + a0.y) + (a1.x + a1.y);
+      // The second half's sums through one of four buffers: a warp is at most two key tiles behind another, so the buffer
+      // of four tiles ago has been read.
+      if (half == 1) {
+        s_sum[(t & 3) * 128 + r] = sum;
+        mbar_arrive_warp(sum_full + (t & 3));
+      } else {
+        if (!mbar_wait_warp(sum_full + (t & 3), (t >> 2) & 1, abort_flag, p.status)) { ok = false; break; }
+        if (valid) p.delta[static_cast<size_t>(start + q) * p.Hq + head] = sum + s_sum[(t & 3) * 128 + r];
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kTmemCols);
+  }
+}
+
+template <typename T, int DP, bool CAUSAL>
+cudaError_t run(const BwdMaps& maps, const BwdParams& p, cudaStream_t stream) {
+  using L = DeltaLayout<DP>;
+  auto kern = packed_delta_kernel<T, DP, CAUSAL>;
+  static std::atomic<unsigned long long> ready{0};  // devices on which the kernel is set up
+  const cudaError_t e = once_per_device(ready, [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes); });
+  if (e != cudaSuccess) return e;
+  const long long most = packed_bound(p.N, p.nseq, p.max_seqlen, kBN) * p.Hkv;
+  if (most > 0x7fffffffLL) return cudaErrorInvalidValue;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(most));
+  cfg.blockDim = dim3(L::kThreads);
+  cfg.dynamicSmemBytes = L::kBytes;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = p.tiles ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, maps.q, maps.k, maps.v, maps.dout, p);
+}
+
+template <typename T>
+cudaError_t run_t(const BwdMaps& maps, const BwdParams& p, bool causal, cudaStream_t stream) {
+  if (p.d <= 64) return causal ? run<T, 64, true>(maps, p, stream) : run<T, 64, false>(maps, p, stream);
+  return causal ? run<T, 128, true>(maps, p, stream) : run<T, 128, false>(maps, p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_packed_delta(const BwdMaps& maps, const BwdParams& p, attn_dtype_t dtype, bool causal, cudaStream_t stream) {
+  return dtype == ATTN_F16 ? run_t<__half>(maps, p, causal, stream) : run_t<__nv_bfloat16>(maps, p, causal, stream);
+}
+
+}  // namespace attn

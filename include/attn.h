@@ -357,6 +357,7 @@ attn_status_t attn_fwd_varlen_gqa(const void* q, const void* k, const void* v, c
 /*
  * Its backward: dq [total_tokens, Hq, d], dk and dv [total_tokens, Hkv, d] (dtype, or float32 with ATTN_FLAG_OUT_F32),
  * by the formulas of attn_bwd; a kv head's dk and dv sum over the query heads of its group.
+ * In 16 bits D is summed over the keys in float32, not taken from out, whose rounding a row with few keys would feel.
  *   out, dout  [total_tokens, Hq, d] (dtype); lse [Hq, total_tokens], as the forward wrote them
  * The other arguments are the forward's; ATTN_FLAG_DETERMINISTIC as for attn_bwd.
  */

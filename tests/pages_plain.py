@@ -51,9 +51,9 @@ def spread(x, dim):
     return torch.minimum(x.abs().sum(dim), 6 * x.square().sum(dim).sqrt())
 
 
-def grads(q, k, v, dout, first, causal, half_in, half_out, rho, scale=None):
+def grads(q, k, v, dout, first, causal, half_in, half_out, rho, scale=None, few=0):
     """One kv head in 64 bits: (dq, dk, dv) and their bounds.  The kernels take D = dO . O with O as the forward gave it, its P
-    and itself rounded (half_in each), hold P and dS with an error of rho, relative, and round the results (half_out)."""
+    and itself rounded (half_in each; the first `few` queries: D summed over the keys), hold P and dS with an error of rho, relative, and round the results (half_out)."""
     G, Nq, d = q.shape
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     o, _, p, size = attend(q, k, v, first, causal, scale)
@@ -66,7 +66,10 @@ def grads(q, k, v, dout, first, causal, half_in, half_out, rho, scale=None):
     e_dp = (dout.abs() @ v.abs().t()) * sum_error(d)
     # D's error, one number for a row: the roundings of O's columns, of the weights behind them, and the sums
     other = (p * 2 * e_p) @ v.abs() + 2 * sum_error(n) * (p @ v.abs()) + n * 2.0 ** -24 * v.abs().amax(0) + sum_error(d) * o.abs()
-    e_d = (spread(half_in * dout * o, -1) + spread(half_in * p * dp, -1) + (dout.abs() * other).sum(-1))[..., None]
+    rounded = spread(half_in * dout * o, -1) + spread(half_in * p * dp, -1)
+    if few:  # these rows' D is a sum over their keys
+        rounded[:, :few] = ((p * e_dp + sum_error(n) * (p * dp).abs()).sum(-1))[:, :few]
+    e_d = (rounded + (dout.abs() * other).sum(-1))[..., None]
     e_ds = ds.abs() * (e_p + rho) + p * e_dp  # per (query, key), beside D's
     tiny = 2.0 ** -24 * (1 + ds.abs().amax())  # fp16 parts of dS below its normal numbers
     b_dv = torch.einsum("gij,gid->jd", p * (e_p + rho + rows), dout.abs()) + half_out * dv.abs() * 1.01 + G * Nq * 2.0 ** -24 * dout.abs().amax((0, 1))

@@ -65,7 +65,7 @@ def check_fwd(o, lse, q, k, v, lens, causal, out_f32, scale=None):
     assert (o[at:] == 0).all() and (lse[:, at:] == -INF).all()
 
 
-def check_bwd(got, q, k, v, dout, lens, causal, out_f32, scale=None):
+def check_bwd(got, q, k, v, dout, lens, causal, out_f32, scale=None, few=None):
     Hq, Hkv, dt = q.shape[1], k.shape[1], q.dtype
     G, at = Hq // Hkv, 0
     half = 2.0 ** -24 if out_f32 or dt == torch.float32 else P.HALF[dt]
@@ -79,7 +79,7 @@ def check_bwd(got, q, k, v, dout, lens, causal, out_f32, scale=None):
             if L == 0:
                 continue
             x, kh, vh, do = q[t, g].double().transpose(0, 1), k[t, h].double(), v[t, h].double(), dout[t, g].double().transpose(0, 1)
-            want, bounds = P.grads(x, kh, vh, do, 0, causal, P.HALF[dt], half, rho, scale)
+            want, bounds = P.grads(x, kh, vh, do, 0, causal, P.HALF[dt], half, rho, scale, few(L) if few else 0)
             for name, y, w, b in zip(("dq", "dk", "dv"), (dq[t, g].transpose(0, 1), dk[t, h], dv[t, h]), want, bounds):
                 assert ((y - w).abs() <= b).all(), (name, L, h, float(((y - w).abs() - b).max()))
     assert all((x[at:] == 0).all() for x in (dq, dk, dv))
@@ -191,6 +191,23 @@ def test_one_sequence(dev):
     assert (o == 0).all() and (lse == -INF).all()
     assert all((x == 0).all() for x in A.bwd_varlen_gqa(q, k, v, o, lse, dout.nan_to_num(), none, 1001, True))
     status()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype,Hq,Hkv,d", [("bf16", 8, 2, 128), ("f16", 4, 4, 64), ("bf16", 5, 1, 80), ("f16", 71, 1, 16), ("f16", 32, 2, 112)])
+def test_gradients_without_the_rounding_of_o(dev, dtype, Hq, Hkv, d, causal):
+    """D is a sum over the keys: where a row sees one key its gradients are zero but for fp32's errors, and not what
+    rounding O leaves."""
+    for lens in ([1] * 20 + [2, 3, 1, 5, 8], [32, 33, 1, 31, 64, 300], [40], [129, 700]):
+        q, k, v, dout, cu = make(dev, dtype, Hq, Hkv, d, lens, seed=d, behind=3)
+        o, lse = A.fwd_varlen_gqa(q, k, v, cu, max(lens), causal)
+        got = A.bwd_varlen_gqa(q, k, v, o, lse, dout, cu, max(lens), causal, out_f32=True)
+        status()
+        check_bwd(got, q, k, v, dout, lens, causal, True, few=lambda L: L)
+        if lens[0] == 1:  # dS = P (dP - D), dP of two summations, P from an LSE of fp32
+            size = dout[:20].double().norm(dim=-1) * v[:20].double().norm(dim=-1).repeat_interleave(Hq // Hkv, 1)
+            bound = size[..., None] * 2.0 ** -16 * k[:20].double().abs().repeat_interleave(Hq // Hkv, 1) / d ** 0.5
+            assert (got[0][:20].double().abs() <= bound + 2.0 ** -20).all()
 
 
 def test_deterministic_gradients(dev):
