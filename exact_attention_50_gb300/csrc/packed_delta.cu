@@ -9,10 +9,11 @@
 // the keys in fp32, with the P of the main kernel.
 //
 // A CTA per key tile of the list and kv head, as in the main kernel, here for the 128 tokens as queries: query tiles of
-// tile_tokens tokens by `heads` heads, all keys they see.  Warp 8 loads (Q and dO, two tiles; K and V through one ring), warp 9
+// tile_tokens tokens by `heads` heads, two at a time, so that a key tile serves two; all keys they see.  Warp 8 loads (Q and dO
+// of the two; K and V through one ring), warp 9
 // issues S = Q K^T and dP = dO V^T into two stages of TMEM, a thread of warps 0-7 has 64 columns of a row and adds up
-// exp2(S scale log2e - LSE log2e) dP; nothing is written back and nothing rescaled.  Warps 10 and 11 write the zeros meanwhile.
-// 4 x 2048 tokens, 32 over 8 heads, d = 128: 150 us, 137 GFLOP at 0.9 PFLOP/s, where the sweep and its zeros took 40; errors against 64
+// exp2(S scale log2e - LSE log2e) dP; nothing is written back and nothing rescaled.  Warp 10 writes the zeros meanwhile.
+// 4 x 2048 tokens, 32 over 8 heads, d = 128: 136 us (150 with the list in its order and a query tile at a time), 137 GFLOP at 1.0 PFLOP/s, where the sweep and its zeros took 40; errors against 64
 // bits are those of rounding the results (dq, dk, dv 16.6e-4 in bf16, 2.07e-4 in fp16, at all lengths).
 #include "bwd_tc.cuh"
 
@@ -33,12 +34,12 @@ struct DeltaLayout {
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;  // tmem base, abort flag, wait limit (u64)
   static constexpr int kBytes = kOffMisc + 16;
   static_assert(kBytes <= 227 * 1024 && kOffMisc % 8 == 0, "shared memory of a CTA");
-  static constexpr int kThreads = 384;
+  static constexpr int kThreads = 352;
   static constexpr uint32_t kTmemCols = 512, kColS = 0, kColdP = 256;  // two stages of 128 columns each
 };
 
 template <typename T, int DP, bool CAUSAL>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(352, 1)
     packed_delta_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         const __grid_constant__ CUtensorMap tmdO, const BwdParams p) {
   using L = DeltaLayout<DP>;
@@ -68,10 +69,13 @@ __global__ void __launch_bounds__(384, 1)
     if (threadIdx.x == 0) raise_status(p.status, ATTN_ERR_CUDA);
     return;
   }
-  const int start = tile.x, len = tile.y, tok0 = tile.z * kBN, tok1 = min(len, tok0 + kBN);  // the tokens that are its queries
+  const int start = tile.x, len = tile.y;
+  // the list's order has a sequence's first tiles, the ones of most work as keys, first: as queries they have the least
+  const int no = CAUSAL ? (len + kBN - 1) / kBN - 1 - tile.z : tile.z;
+  const int tok0 = no * kBN, tok1 = min(len, tok0 + kBN);  // the tokens that are its queries
   const int qtok = p.tile_tokens, qheads = p.heads;
   const int per_head = (tok1 - tok0 + qtok - 1) / qtok, n_q = p.G / qheads * per_head;  // query tiles
-  const int n_kv = CAUSAL ? tile.z + 1 : (len + kBN - 1) / kBN;
+  const int n_kv = CAUSAL ? no + 1 : (len + kBN - 1) / kBN;
   uint8_t* const ring = smem + L::kOffRing;
   uint64_t* const q_full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
   uint64_t* const q_empty = q_full + 2;
@@ -131,12 +135,11 @@ __global__ void __launch_bounds__(384, 1)
         ++nr;
         return true;
       };
-      bool ok = load_q();
-      for (int t = 0; ok && t < n_q; ++t)
-        for (int j = 0; ok && j < n_kv; ++j) {
-          ok = load_r(&tmK, j) && load_r(&tmV, j);
-          if (ok && j == 0 && nq < n_q) ok = load_q();  // the next one, as soon as there is room
-        }
+      bool ok = true;
+      for (int t0 = 0; ok && t0 < n_q; t0 += 2) {
+        ok = load_q() && (nq >= n_q || load_q());
+        for (int j = 0; ok && j < n_kv; ++j) ok = load_r(&tmK, j) && load_r(&tmV, j);
+      }
       if (abort_read(abort_flag)) {  // let the copies land before the shared memory goes away
         for (int t = max(0, nq - 2); t < nq; ++t) mbar_drain(q_full + (t & 1), (t >> 1) & 1);
         for (uint32_t i = nr > static_cast<uint32_t>(R) ? nr - R : 0; i < nr; ++i) mbar_drain(r_full + i % R, (i / R) & 1);
@@ -149,34 +152,40 @@ __global__ void __launch_bounds__(384, 1)
       constexpr uint32_t id = idesc_f16(Elem<T>::kBf16, false, false, 128, 128);
       const uint64_t dq = smem_desc_sw128(smem_u32(smem + L::kOffQ), 16, 1024), dr = smem_desc_sw128(smem_u32(ring), 16, 1024);
       constexpr uint32_t kTile16 = L::kTileBytes >> 4;
-      uint32_t n = 0, u = 0;  // key tiles, tiles of the ring passed
+      uint32_t n = 0, u = 0;  // products, tiles of the ring passed
       bool ok = true;
-      const auto product = [&](uint32_t col, uint64_t a0) -> bool {
-        const uint32_t s = u % R;
-        if (!mbar_wait(r_full + s, (u / R) & 1, abort_flag, p.status)) return false;
-        tc_fence_after();
+      const auto product = [&](uint32_t col, uint64_t a0, uint32_t s) {
         const uint64_t a = opaque(a0), b = opaque(dr + s * kTile16);
 #pragma unroll
         for (int ks = 0; ks < DP / 16; ++ks) {
           const uint32_t off = ((ks >> 2) * L::kChunkBytes + (ks & 3) * 32) >> 4;
           mma_ss(tmem + col, a + off, b + off, id, ks > 0 ? 1u : 0u);
         }
-        mma_commit(r_empty + s);
-        ++u;
-        return true;
       };
-      for (int t = 0; ok && t < n_q; ++t) {
-        const uint64_t q = dq + (t & 1) * 2 * kTile16;
-        ok = mbar_wait(q_full + (t & 1), (t >> 1) & 1, abort_flag, p.status);
-        for (int j = 0; ok && j < n_kv; ++j, ++n) {
-          const uint32_t b = n & 1;
-          if (n >= 2 && !mbar_wait(s_empty + b, ((n >> 1) - 1) & 1, abort_flag, p.status)) { ok = false; break; }
-          tc_fence_after();
-          ok = product(L::kColS + b * 128, q) && product(L::kColdP + b * 128, q + kTile16);
-          if (ok) mma_commit(s_full + b);
+      for (int t0 = 0; ok && t0 < n_q; t0 += 2)
+        for (int j = 0; ok && j < n_kv; ++j, u += 2) {
+          const uint32_t sk = u % R, sv = (u + 1) % R;
+          for (int w = 0; w < 2 && t0 + w < n_q; ++w, ++n) {
+            const uint32_t b = n & 1;
+            if (j == 0 && !mbar_wait(q_full + w, (t0 >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
+            if (w == 0 && !mbar_wait(r_full + sk, (u / R) & 1, abort_flag, p.status)) { ok = false; break; }
+            if (n >= 2 && !mbar_wait(s_empty + b, ((n >> 1) - 1) & 1, abort_flag, p.status)) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t q = dq + w * 2 * kTile16;
+            product(L::kColS + b * 128, q, sk);
+            if (w == 0) {
+              if (!mbar_wait(r_full + sv, ((u + 1) / R) & 1, abort_flag, p.status)) { ok = false; break; }
+              tc_fence_after();
+            }
+            product(L::kColdP + b * 128, q + kTile16, sv);
+            mma_commit(s_full + b);
+            if (j == n_kv - 1) mma_commit(q_empty + w);
+          }
+          if (ok) {
+            mma_commit(r_empty + sk);
+            mma_commit(r_empty + sv);
+          }
         }
-        if (ok) mma_commit(q_empty + (t & 1));
-      }
       if (!ok) {
         mma_commit(drain);
         mbar_drain(drain, 0);
@@ -185,13 +194,13 @@ __global__ void __launch_bounds__(384, 1)
     __syncwarp();
   } else if (warp >= 10) {
     // ================================================================ zeros for these tokens' rows of dQ
-    const int first = threadIdx.x - 320, vecs = p.G * p.d / 4;
+    const int first = lane, vecs = p.G * p.d / 4;
     for (int tok = tok0; tok < tok1; ++tok) {
       const size_t row = static_cast<size_t>(start + tok) * p.Hq + hkv * p.G;
       float4* const dst = reinterpret_cast<float4*>(p.dq_acc + row * p.d);
-      for (int i = first; i < vecs; i += 64) dst[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = first; i < vecs; i += 32) dst[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (p.deterministic)
-        for (int i = first; i < p.G; i += 64) p.dq_turn[row + i] = 0;
+        for (int i = first; i < p.G; i += 32) p.dq_turn[row + i] = 0;
     }
   } else {
     // ================================================================ rows
@@ -202,68 +211,89 @@ __global__ void __launch_bounds__(384, 1)
     const uint64_t scl = f2_pack(p.scale_log2, p.scale_log2);
     uint32_t n = 0;
     bool ok = true;
-    for (int t = 0; ok && t < n_q; ++t) {
-      const int q = tok0 + t % per_head * qtok + my_tok, head = hkv * p.G + t / per_head * qheads + my_head;
-      const bool valid = my_tok < qtok && q < tok1;
-      const float nl = valid ? -(p.lse[static_cast<size_t>(head) * p.N + start + q] * 1.4426950408889634f) : -INFINITY;
-      const int seen = CAUSAL ? min(q + 1, len) : len;
-      const uint64_t nlb = f2_pack(nl, nl);
-      float sum = 0.f;
-      uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
-      for (int j = 0; j < n_kv; ++j, ++n) {
-        const uint32_t b = n & 1;
-        if (!mbar_wait_warp(s_full + b, (n >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
-        tc_fence_after();
-        uint32_t s0[32], s1[32], d0[32], d1[32];
-        tmem_ld32(tl + L::kColS + b * 128, s0);
-        tmem_ld32(tl + L::kColdP + b * 128, d0);
-        tmem_ld32(tl + L::kColS + b * 128 + 32, s1);
-        tmem_ld32(tl + L::kColdP + b * 128 + 32, d1);
-        tmem_ld_wait();
-        tmem_reg_fence(s0);
-        tmem_reg_fence(d0);
-        tmem_reg_fence(s1);
-        tmem_reg_fence(d1);
-        tc_fence_before();
-        mbar_arrive_warp(s_empty + b);
-        const int vis = seen - j * kBN - half * 64;  // this row sees columns [0, vis)
-        if (__all_sync(0xffffffffu, vis >= 64)) {
+    const auto token = [&](int t) { return tok0 + t % per_head * qtok + my_tok; };
+    const auto head_of = [&](int t) { return hkv * p.G + t / per_head * qheads + my_head; };
+    for (int t0 = 0; ok && t0 < n_q; t0 += 2) {
+      float nl[2], sum[2];
+      int seen[2];
+      uint64_t acc[2];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t(&s)[32] = h ? s1 : s0;
-            uint32_t(&d)[32] = h ? d1 : d0;
+      for (int w = 0; w < 2; ++w) {
+        const int q = token(t0 + w);
+        const bool valid = t0 + w < n_q && my_tok < qtok && q < tok1;
+        nl[w] = valid ? -(p.lse[static_cast<size_t>(head_of(t0 + w)) * p.N + start + q] * 1.4426950408889634f) : -INFINITY;
+        seen[w] = CAUSAL ? min(q + 1, len) : len;
+        sum[w] = 0.f;
+        acc[w] = f2_pack(0.f, 0.f);
+      }
+      for (int j = 0; ok && j < n_kv; ++j) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float2 x = f2_unpack(f2_fma(f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), scl, nlb));
-              const float2 y = f2_unpack(f2_fma(f2_pack(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), scl, nlb));
-              acc0 = f2_fma(f2_pack(ex2_approx(x.x), ex2_approx(x.y)), f2_pack(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), acc0);
-              acc1 = f2_fma(f2_pack(ex2_approx(y.x), ex2_approx(y.y)), f2_pack(__uint_as_float(d[i + 2]), __uint_as_float(d[i + 3])), acc1);
+        for (int w = 0; w < 2; ++w) {
+          if (t0 + w >= n_q) break;
+          const uint32_t b = n & 1;
+          if (!mbar_wait_warp(s_full + b, (n >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
+          ++n;
+          tc_fence_after();
+          uint32_t s0[32], s1[32], d0[32], d1[32];
+          tmem_ld32(tl + L::kColS + b * 128, s0);
+          tmem_ld32(tl + L::kColdP + b * 128, d0);
+          tmem_ld32(tl + L::kColS + b * 128 + 32, s1);
+          tmem_ld32(tl + L::kColdP + b * 128 + 32, d1);
+          tmem_ld_wait();
+          tmem_reg_fence(s0);
+          tmem_reg_fence(d0);
+          tmem_reg_fence(s1);
+          tmem_reg_fence(d1);
+          tc_fence_before();
+          mbar_arrive_warp(s_empty + b);
+          const int vis = seen[w] - j * kBN - half * 64;  // this row sees columns [0, vis)
+          if (__all_sync(0xffffffffu, vis >= 64)) {
+            const uint64_t nlb = f2_pack(nl[w], nl[w]);
+            uint64_t other = f2_pack(0.f, 0.f);  // a second chain of sums
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t(&s)[32] = h ? s1 : s0;
+              uint32_t(&d)[32] = h ? d1 : d0;
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const float2 x = f2_unpack(f2_fma(f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), scl, nlb));
+                const float2 y = f2_unpack(f2_fma(f2_pack(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), scl, nlb));
+                acc[w] = f2_fma(f2_pack(ex2_approx(x.x), ex2_approx(x.y)), f2_pack(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), acc[w]);
+                other = f2_fma(f2_pack(ex2_approx(y.x), ex2_approx(y.y)), f2_pack(__uint_as_float(d[i + 2]), __uint_as_float(d[i + 3])), other);
+              }
             }
-          }
-        } else if (__any_sync(0xffffffffu, vis > 0)) {
+            acc[w] = f2_add(acc[w], other);
+          } else if (__any_sync(0xffffffffu, vis > 0)) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t(&s)[32] = h ? s1 : s0;
-            uint32_t(&d)[32] = h ? d1 : d0;
+            for (int h = 0; h < 2; ++h) {
+              uint32_t(&s)[32] = h ? s1 : s0;
+              uint32_t(&d)[32] = h ? d1 : d0;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float x = ex2_approx(fmaf(__uint_as_float(s[i]), p.scale_log2, nl)) * __uint_as_float(d[i]);
-              sum += 32 * h + i < vis ? x : 0.f;
+              for (int i = 0; i < 32; ++i) {
+                const float x = ex2_approx(fmaf(__uint_as_float(s[i]), p.scale_log2, nl[w])) * __uint_as_float(d[i]);
+                sum[w] += 32 * h + i < vis ? x : 0.f;
+              }
             }
           }
         }
       }
       if (!ok) break;
-      const float2 a0 = f2_unpack(acc0), a1 = f2_unpack(acc1);
-      sum += (a0.x + a0.y) + (a1.x + a1.y);
-      // The second half's sums through one of four buffers: a warp is at most two key tiles behind another, so the buffer
-      // of four tiles ago has been read.
-      if (half == 1) {
-        s_sum[(t & 3) * 128 + r] = sum;
-        mbar_arrive_warp(sum_full + (t & 3));
-      } else {
-        if (!mbar_wait_warp(sum_full + (t & 3), (t >> 2) & 1, abort_flag, p.status)) { ok = false; break; }
-        if (valid) p.delta[static_cast<size_t>(start + q) * p.Hq + head] = sum + s_sum[(t & 3) * 128 + r];
+      // The second halves' sums, through one of two pairs of buffers: a warp is at most two products behind another, and a
+      // pair of tiles has two at least, so the buffers of the pair before the last have been read.
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const int t = t0 + w;
+        if (t >= n_q) break;
+        const float2 a = f2_unpack(acc[w]);
+        const float all = sum[w] + (a.x + a.y);
+        if (half == 1) {
+          s_sum[(t & 3) * 128 + r] = all;
+          mbar_arrive_warp(sum_full + (t & 3));
+        } else {
+          if (!mbar_wait_warp(sum_full + (t & 3), (t >> 2) & 1, abort_flag, p.status)) { ok = false; break; }
+          const int q = token(t);
+          if (my_tok < qtok && q < tok1) p.delta[static_cast<size_t>(start + q) * p.Hq + head_of(t)] = all + s_sum[(t & 3) * 128 + r];
+        }
       }
     }
   }
