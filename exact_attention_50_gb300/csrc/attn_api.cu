@@ -1220,8 +1220,8 @@ attn_status_t attn_bwd_varlen_gqa(const void* q, const void* k, const void* v, c
   int* const head = reinterpret_cast<int*>(list);
   int4* const tiles = reinterpret_cast<int4*>(list + kListHead);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // The 16-bit path keeps D and the dQ accumulator in the order of O, [T, Hq] rows, so that both are read and written in
-  // one sweep (16.5k tokens of 32 heads: 118 us in the order of the LSE).
+  // The 16-bit path keeps D and the dQ accumulator in the order of O, [T, Hq] rows: a token's heads lie together, and dQ is
+  // rounded in one sweep.
   const BwdParams::Rows sweep{d, static_cast<long long>(total_tokens) * d};
   if (dtype != ATTN_F32) p.lay_o = p.lay_dq = sweep;
   if (nseq > 1 || dtype == ATTN_F32) {
