@@ -543,7 +543,7 @@ def bwd_varlen_gqa(q, k, v, out, lse, dout, cu_seqlens, max_seqlen: int, causal:
                    deterministic: bool = False):
     """Packed backward with grouped heads: q, k, v, cu_seqlens, max_seqlen, causal and scale as given to fwd_varlen_gqa, out
     and lse as it returned them, dout [T,Hq,d].  Returns (dq [T,Hq,d], dk, dv [T,Hkv,d]); zeros for tokens behind the
-    last sequence."""
+    last sequence.  In 16 bits the row terms are summed over the keys, so that the rounding of out is not in them."""
     f32, i32 = torch.float32, torch.int32
     try:
         dev, dt = q.get_device(), q.dtype
